@@ -296,10 +296,11 @@ def _plain_append(s):
     if c["q8"]:
         x = k - s["k_mean"][:, :d]
         top = x.abs().amax(-1, keepdim=True)
-        k = torch.where(top > 0, torch.round(x * (127.0 / top)), 0.0)
+        most = torch.full_like(top, 127.0)     # divided as tensors: one rounding each
+        k = torch.where(top > 0, torch.round(x * (most / top)), 0.0)
         inv = torch.where(s["v_scale"] > 0, 1.0 / s["v_scale"], 0.0)[:, :d]
         v = (v * inv).clamp(-448, 448)
-        s["k_scale"].transpose(1, 2)[page, slot] = (top / 127.0).squeeze(-1)
+        s["k_scale"].transpose(1, 2)[page, slot] = (top / most).squeeze(-1)
         out["k_scale"] = s["k_scale"]
     at = (lambda x: x) if c["layout"] == "NHD" else (lambda x: x.transpose(1, 2))
     at(s["k"])[page, slot] = k.to(s["k"].dtype)
