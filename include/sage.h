@@ -401,6 +401,119 @@ SAGE_API sage_status sage_kv_stats_noalloc(const void* k, const void* v, int dty
  * counterpart. */
 SAGE_API sage_status sage_kv_stats_noalloc_status(sage_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Serving: rotary positions, a paged key/value cache, and attention of new
+ * tokens over it (the pages describe whole-sequence attention only; these
+ * calls are additions of this library).  16-bit results keep the inputs'
+ * type here, since the projection that follows reads 16 bits.
+ * ------------------------------------------------------------------------ */
+
+/* Rotary positions of q (T,Hq,D) and k (T,Hkv,D): channel pair i < R/2 of
+ * every head turns by the angle pos[t] * inv_freq[i] and is multiplied by
+ * mscale; channels R..D-1 are copied.  A pair is (i, i + R/2), or with
+ * `interleaved` (2i, 2i + 1).
+ *   q_strides, k_strides, qo_strides, ko_strides: host int64[2], {token, head}
+ *       in elements, positive, channel stride 1; NULL: dense.
+ *   q_out may be q itself with the same strides (in place), and likewise
+ *       k_out; any other overlap of inputs and outputs is not supported.
+ *   k may be NULL (Hkv = 0): q alone is turned.
+ *   pos: device int64 (pos_bits 64) or int32 (32), any value; the angle is
+ *       reduced exactly in 64-bit fixed point, so far positions lose nothing.
+ *   inv_freq: device double[R/2]; R even, 2..D; D 1..128.
+ *   inverse: turns by the negative angle (the transpose up to mscale^2): the
+ *       gradient of the forward call, with the same mscale. */
+SAGE_API sage_status sage_rope(const void* q, const void* k, void* q_out, void* k_out, int dtype,
+                               int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
+                               const int64_t* q_strides, const int64_t* k_strides,
+                               const int64_t* qo_strides, const int64_t* ko_strides,
+                               const void* pos, int pos_bits, const double* inv_freq, int64_t R,
+                               int interleaved, float mscale, int inverse,
+                               sage_stream_t stream);
+
+/* A paged key/value cache.  Page p, slot t, kv head h holds D channels of K
+ * and V at p*page_stride + t*token_stride + h*head_stride elements of k and
+ * of v (both tensors share the strides, which cover (pages, slots, heads, D)
+ * and (pages, heads, slots, D) layouts and views into larger tensors).
+ *   kind SAGE_F16 / SAGE_BF16: K and V in that type.
+ *   kind SAGE_Q8: K as int8 codes of k - k_mean (the smoothing of
+ *     sage_quant_prologue with a fixed mean: it adds one number to all logits
+ *     of a row, which the softmax drops) with one scale per token and head,
+ *     max|k - k_mean|/127, in k_scale [num_pages][Hkv][page_size]; V as e4m3
+ *     codes of v / v_scale, saturating.  k_mean and v_scale are fp32
+ *     [Hkv][Dp] (Dp = 64 if D <= 64 else 128), as sage_kv_stats_noalloc
+ *     writes them for one sequence; they stay fixed while the cache is used.
+ * page_size: a multiple of 16, up to 65536; D: a multiple of 8, 8..128; k and
+ * v 16-byte aligned, strides multiples of 8 elements. */
+enum { SAGE_Q8 = 2 };
+typedef struct {
+  void* k;
+  void* v;
+  float* k_scale;        /* SAGE_Q8 only, else NULL */
+  const float* k_mean;   /* SAGE_Q8 only, else NULL */
+  const float* v_scale;  /* SAGE_Q8 only, else NULL */
+  int64_t num_pages, page_size, Hkv, D;
+  int64_t page_stride, token_stride, head_stride;
+  int32_t kind;
+} sage_paged_cache;
+
+/* A batch of new tokens.  Sequence s holds the packed rows cu_q[s] ..
+ * cu_q[s+1]-1; kv_lens[s] is its cached length with these tokens, so row i
+ * of n has position kv_lens[s] - n + i; position j lives in page
+ * block_table[s*table_stride + j/page_size], slot j % page_size.  All three
+ * arrays are device int32; rows of q behind cu_q[nseq] are left as they are.
+ * max_q and max_kv bound the new tokens and the length of every sequence
+ * (max_kv <= table_width*page_size).  A sequence whose entries break these
+ * bounds is skipped (its rows are left as they are) and a page index outside
+ * the cache is never followed (nothing is written there, zeros are read);
+ * both are recorded in the workspace's status word.  Table entries of pages
+ * that hold no visible key of any new token are never read. */
+typedef struct {
+  const int32_t* cu_q;
+  const int32_t* kv_lens;
+  const int32_t* block_table;
+  int64_t nseq, total_q, table_stride, table_width;
+  int32_t max_q, max_kv;
+} sage_paged_batch;
+
+/* Workspace of the two paged calls: a fixed size for every problem, 256-byte
+ * aligned.  Its contents need no preparation, except that the status word at
+ * its start is cleared by the caller (16 zero bytes, once); the kernels only
+ * set bits of it and sage_device_status reads it.  Calls that may overlap on
+ * the GPU need workspaces of their own. */
+SAGE_API size_t sage_workspace_bytes_paged(void);
+
+/* Writes the new tokens' K and V (T rows of (T,Hkv,D), T = total_q) into the
+ * cache.  With inv_freq, k is turned by sage_rope's rotation at each token's
+ * position first, in 32 bits, and q (if not NULL) is turned into q_out.
+ * Tokens at negative positions (more new tokens than the cached length) are
+ * skipped.  Positions of one call live in distinct slots: a page that two
+ * sequences share is only read.
+ *   k_strides, v_strides, q_strides, qo_strides: as in sage_rope.
+ *   dtype: the type of k, v and q; a 16-bit cache holds the same type. */
+SAGE_API sage_status sage_kv_append(const sage_paged_cache* cache, const sage_paged_batch* batch,
+                                    const void* k, const void* v, const void* q, void* q_out,
+                                    int dtype, int64_t Hq, const int64_t* k_strides,
+                                    const int64_t* v_strides, const int64_t* q_strides,
+                                    const int64_t* qo_strides, const double* inv_freq, int64_t R,
+                                    int interleaved, float mscale, void* ws, size_t ws_bytes,
+                                    sage_stream_t stream);
+
+/* Attention of the new tokens (q (T,Hq,D)) over the cache, causal: the row
+ * at position p sees the keys j <= p of its sequence, and with window > 0 of
+ * those only j > p - window and j < sinks.  Logits, softmax and sums in fp32,
+ * P rounded to 16 bits for the tensor cores.  out: dense (T,Hq,D) of q's
+ * type; lse: NULL or fp32 (T,Hq), the natural logarithm of the row's sum of
+ * exponentials (of the smoothed logits with SAGE_Q8: all of a row's logits
+ * lack sm_scale * q . k_mean).  A row without visible keys gives zeros and
+ * -inf.  Keys and values that no row sees may hold anything; visible ones
+ * are finite.
+ *   q_strides: host int64[2], {token, head} in elements, or NULL: dense. */
+SAGE_API sage_status sage_attn_paged(const sage_paged_cache* cache, const sage_paged_batch* batch,
+                                     const void* q, void* out, float* lse, int dtype, int64_t Hq,
+                                     const int64_t* q_strides, int64_t window, int64_t sinks,
+                                     float sm_scale, void* ws, size_t ws_bytes,
+                                     sage_stream_t stream);
+
 /* Reason of the last failure on this thread ("" if none). */
 SAGE_API const char* sage_last_error(void);
 

@@ -16,6 +16,7 @@
 
 #include "sage.h"
 #include "sage_geom.h"
+#include "sage_host.h"
 #include "sage_kernels.h"
 
 using namespace sage;
@@ -201,6 +202,35 @@ using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, voi
 EncodeFn encode_fn();
 
 }  // namespace
+
+sage_status sage::refuse(sage_status st, const char* fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof(buf), fmt, ap);
+  va_end(ap);
+  return fail(st, "%s", buf);
+}
+sage_status sage::succeeded() { return ok(); }
+sage_status sage::cuda_refused(cudaError_t e, const char* what) { return cuda_fail(e, what); }
+uint64_t sage::device_wait_ns() { return wait_timeout_ns(); }
+
+sage_status sage::require_device(int* sms) {
+  static std::atomic<int> known[64] = {};     // SM count of a checked device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  int n = dev >= 0 && dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
+  if (n == 0) {
+    const sage_status s = check_device();
+    if (s != SAGE_OK) return s;
+    e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceGetAttribute");
+    if (dev >= 0 && dev < 64) known[dev].store(n, std::memory_order_relaxed);
+  }
+  *sms = n;
+  return SAGE_OK;
+}
 
 bool sage::encode_tiled(CUtensorMap* map, CUtensorMapDataType dt, uint32_t rank, void* base,
                         const uint64_t* dims, const uint64_t* strides_bytes,
@@ -1138,6 +1168,8 @@ sage_status status_of_word(uint32_t word) {
     return fail(SAGE_ERR_DEVICE_TIMEOUT, "a device-side wait ran out (status 0x%x)", word);
   if (word & kStatusBadSeqlens)
     return fail(SAGE_ERR_INVALID_ARG, "cu_seqlens inconsistent with totals/maxima");
+  if (word & kStatusBadPage)
+    return fail(SAGE_ERR_INVALID_ARG, "a block table entry lies outside the cache's pages");
   if (word & kStatusBadItem)
     return fail(SAGE_ERR_UNSUPPORTED, "internal error: a prologue work item fell outside "
                 "the call's plan and was skipped");

@@ -1,0 +1,751 @@
+// Attention of few new tokens per sequence over the paged cache (decoding,
+// checking drafted tokens): bound by reading the cache once.
+//
+//   x_jr = c q_r . K_j  (base 2, fp32),  m_r = max_j x_jr,
+//   O_r  = sum_j 2^(x_jr - m_r) V_j,  l_r = sum_j 2^(x_jr - m_r),  out = O / l
+//
+// The rows of one (sequence, kv head) are its new tokens times the query heads
+// of the group, so a key is loaded once for all of them.  The products run
+// transposed, S^T = K Q^T and O^T = V^T P^T, on m16n8k16 tensor instructions:
+// 16 keys (or channels) by 8 rows, which wastes nothing at a group of 8 or a
+// few tokens of 2 or 4.  A contraction's order is free, so each lane takes the
+// operands as whole 16-byte vectors of the cache: 4 lanes cover 64 bytes of a
+// key for S^T, 8 lanes 128 bytes of a value row for O^T, and the fragments are
+// put together by byte permutes.  K and V therefore go from memory straight to
+// registers, with no shared memory and no barrier in the loop; the next
+// block's loads are in flight during the present block's arithmetic.  S^T's
+// accumulators become P^T's operands by an 8x8 register transpose.
+//
+// Work is cut into units of 4 warps x 16 keys (32 of the 8-bit cache) and
+// dealt evenly to a fixed grid: every CTA derives its own contiguous range
+// from the lengths (a scan over the sequences), so ragged batches balance and
+// no length comes to the host.  A (sequence, head) that spans CTAs leaves fp32
+// parts (max, sum, O) in the workspace, two per CTA at most; a second kernel
+// joins them in the order of their ranges, so results do not depend on timing.
+//
+// P is rounded to the 16-bit type of the tensor instruction (relative 2^-9 in
+// bf16, 2^-12 in fp16, the size of the output's own rounding); the sum l takes
+// it unrounded.  The 8-bit cache's codes are exact in fp16: K codes |n| <= 127,
+// e4m3 values <= 448; bf16 queries are scaled per row by a power of two first.
+
+#include <atomic>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "sage_device.cuh"
+#include "sage_kernels.h"
+#include "sage_paged.h"
+
+namespace sage {
+namespace {
+
+constexpr int kThreads = 128, kWarps = 4;
+constexpr int kMaxCtas = 152 * 8;
+constexpr unsigned kAll = 0xFFFFFFFFu;
+
+// One part of a split item (in the workspace).
+struct PartHead {
+  int32_t used, seq, head, tile, last, pad[3];
+};
+constexpr int kMaxRows = 16;
+constexpr size_t kPartBytes = sizeof(PartHead) + kMaxRows * 8 + kMaxRows * 128 * 4;
+
+__device__ __forceinline__ uint8_t* part_at(uint8_t* parts, int cta, int which) {
+  return parts + (static_cast<size_t>(cta) * 2 + which) * kPartBytes;
+}
+
+// What a sequence's rows can see, in blocks of 16 keys: `sink` blocks from key
+// 0, then the blocks from `from` on, `count` in all.
+struct Span {
+  int sink, from, count;
+};
+__device__ __forceinline__ Span span_of(int p_lo, int p_hi, int window, int sinks) {
+  Span r{0, 0, 0};
+  if (p_hi < 0) return r;
+  int lo = 0;
+  if (window > 0 && p_lo - window + 1 > 0) lo = p_lo - window + 1;
+  r.from = lo / 16;
+  if (lo > 0) {
+    const int s = min(sinks, lo);
+    r.sink = min((s + 15) / 16, r.from);
+  }
+  r.count = r.sink + p_hi / 16 + 1 - r.from;
+  return r;
+}
+
+struct Units {
+  int per, tiles;            // units of one item; row tiles of one kv head
+  int64_t total;
+};
+template <int kRows, int kUnitBlocks>
+__device__ __forceinline__ Units units_of(const PagedAttnParams& p, int s, int* start, int* n,
+                                          int* len) {
+  Units u{0, 0, 0};
+  if (!paged_seq(p.c, s, start, n, len)) return u;
+  const int64_t rows = static_cast<int64_t>(*n) * p.group;
+  if (rows < p.min_rows || rows > p.max_rows || rows == 0) return u;
+  const Span sp = span_of(*len - *n, *len - 1, p.window, p.sinks);
+  u.per = max(1, (sp.count + kUnitBlocks - 1) / kUnitBlocks);
+  u.tiles = static_cast<int>((rows + kRows - 1) / kRows);
+  u.total = static_cast<int64_t>(u.per) * u.tiles * p.c.Hkv;
+  return u;
+}
+
+template <bool kBF16>
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                    uint32_t a3, uint32_t b0, uint32_t b1) {
+  if constexpr (kBF16)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, "
+                 "{%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, "
+                 "{%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+
+template <bool kBF16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  if constexpr (kBF16) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&b);
+  } else {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+}
+
+// Four int8 codes of a word as two fp16 pairs, exactly: the byte n + 128 under
+// 0x64 is the fp16 number 1024 + n + 128.
+__device__ __forceinline__ void int8_to_half(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  w ^= 0x80808080u;
+  lo = __byte_perm(w, 0x64646464u, 0x4140);
+  hi = __byte_perm(w, 0x64646464u, 0x4342);
+  const __half2 bias = __floats2half2_rn(1152.0f, 1152.0f);
+  __half2 a = __hsub2(*reinterpret_cast<__half2*>(&lo), bias);
+  __half2 b = __hsub2(*reinterpret_cast<__half2*>(&hi), bias);
+  lo = *reinterpret_cast<uint32_t*>(&a);
+  hi = *reinterpret_cast<uint32_t*>(&b);
+}
+
+__device__ __forceinline__ uint32_t e4m3x2_to_half2(uint32_t two) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(two)));
+  return r;
+}
+
+__device__ __forceinline__ void ld16(uint32_t* w, const uint8_t* p) {
+  asm volatile("ld.global.L1::no_allocate.L2::128B.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "l"(p));
+}
+__device__ __forceinline__ void ld8(uint32_t* w, const uint8_t* p) {
+  asm volatile("ld.global.L1::no_allocate.L2::128B.v2.u32 {%0,%1}, [%2];"
+               : "=r"(w[0]), "=r"(w[1]) : "l"(p));
+}
+// 16 channels of 8 bits at channel ch of a D-channel row: rows of the cache
+// start on 8 bytes at least, on 16 when D % 16 == 0 (wide).
+__device__ __forceinline__ void ld16_q8(uint32_t* w, const uint8_t* row, int ch, int D, bool wide) {
+  if (wide) {
+    if (ch < D) ld16(w, row + ch);
+  } else {
+    if (ch < D) ld8(w, row + ch);
+    if (ch + 8 < D) ld8(w + 2, row + ch + 8);
+  }
+}
+
+template <int kKind, bool kQBF16, int kDp, int kNr>
+__global__ void __launch_bounds__(kThreads)
+paged_few_kernel(const PagedAttnParams p) {
+  constexpr bool kQ8 = kKind == kKindQ8;
+  constexpr bool kMmaBF16 = kKind == kKindBF16;
+  constexpr int kRows = 8 * kNr;
+  constexpr int kKb = kQ8 ? 2 : 1;                        // 16-key blocks of a warp's step
+  constexpr int kUnitBlocks = kWarps * kKb;
+  constexpr int kKw = kQ8 ? kDp / 16 : kDp / 8;           // words of a key per lane
+  constexpr int kVw = kQ8 ? kDp / 32 : kDp / 16;          // words of a value per lane
+  constexpr int kSteps = kDp / 16;                        // k-steps of S^T
+  constexpr int kMt = kDp / 16;                           // 16-channel tiles of O^T
+  constexpr int kPitch = kDp + 4;
+  __shared__ int64_t scan_s[kWarps];
+  __shared__ int64_t off_s;
+  __shared__ int seq_s;
+  __shared__ float m_s[kWarps][kRows], l_s[kWarps][kRows];
+  __shared__ __align__(16) float acc_s[kWarps][kRows * kPitch];
+
+  const PagedGeo& c = p.c;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int g = lane >> 2, t = lane & 3;
+  const int cta = blockIdx.x, ctas = gridDim.x;
+  asm volatile("griddepcontrol.launch_dependents;");
+
+  // ---- this CTA's range of units
+  const int per_thread = (c.nseq + kThreads - 1) / kThreads;
+  const int s_begin = min(c.nseq, tid * per_thread), s_end = min(c.nseq, s_begin + per_thread);
+  int64_t mine = 0;
+  for (int s = s_begin; s < s_end; ++s) {
+    int a, n, len;
+    mine += units_of<kRows, kUnitBlocks>(p, s, &a, &n, &len).total;
+  }
+  int64_t incl = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {
+    const int64_t o = __shfl_up_sync(kAll, incl, d);
+    if (lane >= d) incl += o;
+  }
+  if (lane == 31) scan_s[warp] = incl;
+  __syncthreads();
+  int64_t total = 0, before = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) before += scan_s[w];
+    total += scan_s[w];
+  }
+  const int64_t end = before + incl, begin = end - mine;
+  // no CTA between two parts of an item is left without a unit: the join walks
+  // from CTA to CTA
+  const int64_t busy = min(total, static_cast<int64_t>(ctas));
+  const int64_t u0 = cta < busy ? total * cta / busy : 0;
+  const int64_t u1 = cta < busy ? total * (cta + 1) / busy : 0;
+  bool used[2] = {false, false};
+  if (u0 < u1) {
+    if (begin <= u0 && u0 < end) {                        // one thread
+      int64_t off = u0 - begin;
+      int s = s_begin;
+      for (; s < s_end; ++s) {
+        int a, n, len;
+        const int64_t w = units_of<kRows, kUnitBlocks>(p, s, &a, &n, &len).total;
+        if (off < w) break;
+        off -= w;
+      }
+      seq_s = s;
+      off_s = off;
+    }
+    __syncthreads();
+    int s = seq_s;
+    int64_t off = off_s;
+    const bool wide = !kQ8 || c.D % 16 == 0;
+
+    for (int64_t cur = u0; cur < u1 && s < c.nseq;) {
+      int start, n, len;
+      const Units un = units_of<kRows, kUnitBlocks>(p, s, &start, &n, &len);
+      if (off >= un.total) {                              // an empty sequence
+        off = 0;
+        ++s;
+        continue;
+      }
+      const int64_t item = off / un.per;
+      const int first_unit = static_cast<int>(off - item * un.per);
+      const int count = static_cast<int>(min(static_cast<int64_t>(un.per - first_unit), u1 - cur));
+      const int kvh = static_cast<int>(item / un.tiles), tile = static_cast<int>(item % un.tiles);
+      const int rows = n * p.group;
+      const int row0 = tile * kRows;
+      const int p_lo = len - n + row0 / p.group;
+      const int p_hi = len - n + (min(row0 + kRows, rows) - 1) / p.group;
+      const Span sp = span_of(len - n, len - 1, p.window, p.sinks);
+      const int sinks = p.window > 0 ? p.sinks : 0;
+      const int lo = p.window > 0 ? max(0, p_lo - p.window + 1) : 0;        // first key of row0
+      const int lo_hi = p.window > 0 ? max(0, p_hi - p.window + 1) : 0;     // of the last row
+
+      // ---- the rows' queries, as the B operand of S^T
+      uint32_t qw[kNr][kDp / 8];
+      float rs[kNr][2];                                   // logit scale of rows 2t, 2t + 1
+      int rpos[kNr][2];
+#pragma unroll
+      for (int nr = 0; nr < kNr; ++nr) {
+        const int r = row0 + 8 * nr + g;
+        const bool has = r < rows;
+        const uint16_t* qrow = p.q + (static_cast<int64_t>(start) + r / p.group) * p.q_tok +
+                               (static_cast<int64_t>(kvh) * p.group + r % p.group) * p.q_head;
+#pragma unroll
+        for (int i = 0; i < kDp / 32; ++i) {
+          const int ch = kQ8 ? 64 * (i / 2) + 16 * t + 8 * (i % 2) : 32 * i + 8 * t;
+          uint32_t* w = &qw[nr][4 * i];
+          w[0] = w[1] = w[2] = w[3] = 0;
+          if (has && ch < c.D) {
+            if (p.q_vec) {
+              const uint4 v = *reinterpret_cast<const uint4*>(qrow + ch);
+              w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+            } else {
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                w[e / 2] |= static_cast<uint32_t>(qrow[ch + e]) << (16 * (e & 1));
+            }
+          }
+        }
+        float row_scale = p.scale_log2;
+        if constexpr (kQ8 && kQBF16) {
+          // bf16 queries into fp16's range: times 2^-e, e the exponent of the largest
+          float top = 0.0f;
+#pragma unroll
+          for (int i = 0; i < kDp / 8; ++i) {
+            top = fmaxf(top, fabsf(__uint_as_float(qw[nr][i] << 16)));
+            top = fmaxf(top, fabsf(__uint_as_float(qw[nr][i] & 0xFFFF0000u)));
+          }
+          top = fmaxf(top, __shfl_xor_sync(kAll, top, 1));
+          top = fmaxf(top, __shfl_xor_sync(kAll, top, 2));
+          const int e = top > 0.0f ? ilogbf(top) : 0;
+#pragma unroll
+          for (int i = 0; i < kDp / 8; ++i)
+            qw[nr][i] = pack2<false>(ldexpf(__uint_as_float(qw[nr][i] << 16), -e),
+                                     ldexpf(__uint_as_float(qw[nr][i] & 0xFFFF0000u), -e));
+          row_scale = ldexpf(row_scale, e);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          rs[nr][i] = __shfl_sync(kAll, row_scale, (2 * t + i) * 4);
+          const int rr = row0 + 8 * nr + 2 * t + i;
+          rpos[nr][i] = rr < rows ? len - n + rr / p.group : -1;
+        }
+      }
+
+      float o[kMt][kNr][4], m[kNr][2], l[kNr][2];
+#pragma unroll
+      for (int nr = 0; nr < kNr; ++nr) {
+        m[nr][0] = m[nr][1] = -INFINITY;
+        l[nr][0] = l[nr][1] = 0.0f;
+#pragma unroll
+        for (int j = 0; j < kMt; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[j][nr][e] = 0.0f;
+      }
+
+      uint32_t kw[kKb][2][kKw], vw[kKb][4][kVw];
+      float ks[kKb][2];
+      int key0[kKb], page[kKb];
+      // a step's blocks and their pages; key0 = -1: past the last block
+      auto locate = [&](int unit, int (&k0)[kKb], int (&pg)[kKb]) {
+#pragma unroll
+        for (int b = 0; b < kKb; ++b) {
+          const int vb = (unit * kWarps + warp) * kKb + b;
+          const int blk = vb < sp.sink ? vb : vb - sp.sink + sp.from;
+          k0[b] = vb < sp.count ? 16 * blk : -1;
+          pg[b] = -1;
+          if (k0[b] >= 0 && k0[b] <= p_hi && (k0[b] + 15 >= lo || k0[b] < sinks))
+            pg[b] = paged_page(c, s, k0[b] / c.page_size);
+          else
+            k0[b] = -1;
+        }
+      };
+      auto seen = [&](int j) { return j <= p_hi && (j >= lo || j < sinks); };
+      auto load_k = [&](const int (&k0)[kKb], const int (&pg)[kKb]) {
+#pragma unroll
+        for (int b = 0; b < kKb; ++b) {
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const int j = k0[b] + g + 8 * y;
+#pragma unroll
+            for (int i = 0; i < kKw; ++i) kw[b][y][i] = 0;
+            if (kQ8) ks[b][y] = 0.0f;
+            if (pg[b] >= 0 && seen(j)) {
+              const int slot = k0[b] % c.page_size + g + 8 * y;
+              const int64_t at = pg[b] * c.page_stride + slot * c.token_stride +
+                                 kvh * c.head_stride;
+              if constexpr (kQ8) {
+#pragma unroll
+                for (int i = 0; i < kDp / 64; ++i)
+                  ld16_q8(&kw[b][y][4 * i], c.k + at, 64 * i + 16 * t, c.D, wide);
+                ks[b][y] = c.k_scale[(static_cast<int64_t>(pg[b]) * c.Hkv + kvh) * c.page_size +
+                                     slot];
+              } else {
+#pragma unroll
+                for (int i = 0; i < kDp / 32; ++i)
+                  if (32 * i + 8 * t < c.D)
+                    ld16(&kw[b][y][4 * i], c.k + 2 * (at + 32 * i + 8 * t));
+              }
+            }
+          }
+        }
+      };
+      auto load_v = [&](const int (&k0)[kKb], const int (&pg)[kKb]) {
+#pragma unroll
+        for (int b = 0; b < kKb; ++b) {
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const int in = 2 * t + (y & 1) + 8 * (y >> 1);
+#pragma unroll
+            for (int i = 0; i < kVw; ++i) vw[b][y][i] = 0;
+            if (pg[b] >= 0 && seen(k0[b] + in)) {
+              const int64_t at = pg[b] * c.page_stride +
+                                 (k0[b] % c.page_size + in) * c.token_stride +
+                                 kvh * c.head_stride;
+              if constexpr (kQ8 && kDp == 128) {
+                ld16_q8(vw[b][y], c.v + at, 16 * g, c.D, wide);
+              } else if constexpr (kQ8) {
+                if (8 * g < c.D) ld8(vw[b][y], c.v + at + 8 * g);
+              } else {
+#pragma unroll
+                for (int i = 0; i < kDp / 64; ++i)
+                  if (64 * i + 8 * g < c.D)
+                    ld16(&vw[b][y][4 * i], c.v + 2 * (at + 64 * i + 8 * g));
+              }
+            }
+          }
+        }
+      };
+
+      locate(first_unit, key0, page);
+      load_k(key0, page);
+      load_v(key0, page);
+      for (int u = first_unit; u < first_unit + count; ++u) {
+        int nkey0[kKb], npage[kKb];
+        const bool more = u + 1 < first_unit + count;
+        if (more) locate(u + 1, nkey0, npage);
+        // ---- S^T
+        float x[kKb][kNr][4];
+        bool any = false;
+#pragma unroll
+        for (int b = 0; b < kKb; ++b) {
+          any |= key0[b] >= 0;
+#pragma unroll
+          for (int nr = 0; nr < kNr; ++nr) x[b][nr][0] = x[b][nr][1] = x[b][nr][2] = x[b][nr][3] = 0.0f;
+#pragma unroll
+          for (int i = 0; i < kSteps; ++i) {
+            uint32_t a0, a1, a2, a3;
+            if constexpr (kQ8) {
+              int8_to_half(kw[b][0][i], a0, a2);
+              int8_to_half(kw[b][1][i], a1, a3);
+            } else {
+              a0 = kw[b][0][2 * i]; a2 = kw[b][0][2 * i + 1];
+              a1 = kw[b][1][2 * i]; a3 = kw[b][1][2 * i + 1];
+            }
+#pragma unroll
+            for (int nr = 0; nr < kNr; ++nr)
+              mma<kMmaBF16>(x[b][nr], a0, a1, a2, a3, qw[nr][2 * i], qw[nr][2 * i + 1]);
+          }
+        }
+        float sc[kKb][2];
+        if constexpr (kQ8) {
+#pragma unroll
+          for (int b = 0; b < kKb; ++b) {
+            sc[b][0] = ks[b][0];
+            sc[b][1] = ks[b][1];
+          }
+        }
+        if (more) load_k(nkey0, npage);
+        if (any) {
+          // ---- logits, masks, running maximum and sum
+          float mx[kNr][2];
+#pragma unroll
+          for (int nr = 0; nr < kNr; ++nr) mx[nr][0] = mx[nr][1] = -INFINITY;
+#pragma unroll
+          for (int b = 0; b < kKb; ++b) {
+            const bool full = key0[b] >= 0 && key0[b] + 15 <= p_lo &&
+                              (key0[b] >= lo_hi || key0[b] + 15 < sinks);
+#pragma unroll
+            for (int nr = 0; nr < kNr; ++nr)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                float v = x[b][nr][e] * rs[nr][e & 1];
+                if constexpr (kQ8) v *= sc[b][e >> 1];
+                if (!full) {
+                  const int j = key0[b] + g + 8 * (e >> 1);
+                  const int pos = rpos[nr][e & 1];
+                  const bool see = key0[b] >= 0 && j <= pos &&
+                                   (p.window <= 0 || j > pos - p.window || j < sinks);
+                  v = see ? v : -INFINITY;
+                }
+                x[b][nr][e] = v;
+                mx[nr][e & 1] = fmaxf(mx[nr][e & 1], v);
+              }
+          }
+          float alpha[kNr][2];
+          bool grew = false;
+#pragma unroll
+          for (int nr = 0; nr < kNr; ++nr)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              float v = mx[nr][i];
+              v = fmaxf(v, __shfl_xor_sync(kAll, v, 4));
+              v = fmaxf(v, __shfl_xor_sync(kAll, v, 8));
+              v = fmaxf(v, __shfl_xor_sync(kAll, v, 16));
+              v = fmaxf(v, m[nr][i]);
+              const float safe = v == -INFINITY ? 0.0f : v;
+              alpha[nr][i] = fast_exp2(m[nr][i] - safe);
+              grew |= v > m[nr][i];
+              m[nr][i] = v;
+              mx[nr][i] = safe;
+              l[nr][i] *= alpha[nr][i];
+            }
+          if (__any_sync(kAll, grew)) {
+#pragma unroll
+            for (int j = 0; j < kMt; ++j)
+#pragma unroll
+              for (int nr = 0; nr < kNr; ++nr)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[j][nr][e] *= alpha[nr][e & 1];
+          }
+          // ---- P^T and O^T
+#pragma unroll
+          for (int b = 0; b < kKb; ++b) {
+            uint32_t pb[kNr][2];
+#pragma unroll
+            for (int nr = 0; nr < kNr; ++nr) {
+              float e4[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                e4[e] = fast_exp2(x[b][nr][e] - mx[nr][e & 1]);
+                l[nr][e & 1] += e4[e];
+              }
+              pb[nr][0] = transpose8x8(pack2<kMmaBF16>(e4[0], e4[1]));
+              pb[nr][1] = transpose8x8(pack2<kMmaBF16>(e4[2], e4[3]));
+            }
+#pragma unroll
+            for (int j = 0; j < kMt; ++j) {
+              uint32_t a[4];
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {               // a0, a1: keys 2t, 2t+1; a2, a3: +8
+                const int y = 2 * (q >> 1), hi = q & 1;
+                if constexpr (kQ8) {
+                  const int word = (kDp == 128 ? 2 : 1) * hi + j / 4;
+                  const uint32_t two = __byte_perm(vw[b][y][word], vw[b][y + 1][word],
+                                                   (j & 3) == 0 ? 0x40 : (j & 3) == 1 ? 0x51
+                                                   : (j & 3) == 2 ? 0x62 : 0x73);
+                  a[q] = e4m3x2_to_half2(two);
+                } else {
+                  const int word = (kDp == 128 ? 4 : 2) * hi + j / 2;
+                  a[q] = __byte_perm(vw[b][y][word], vw[b][y + 1][word],
+                                     (j & 1) ? 0x7632 : 0x5410);
+                }
+              }
+#pragma unroll
+              for (int nr = 0; nr < kNr; ++nr)
+                mma<kMmaBF16>(o[j][nr], a[0], a[1], a[2], a[3], pb[nr][0], pb[nr][1]);
+            }
+          }
+        }
+        if (more) {
+          load_v(nkey0, npage);
+#pragma unroll
+          for (int b = 0; b < kKb; ++b) {
+            key0[b] = nkey0[b];
+            page[b] = npage[b];
+          }
+        }
+      }
+
+      // ---- join the warps
+#pragma unroll
+      for (int nr = 0; nr < kNr; ++nr)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float v = l[nr][i];
+          v += __shfl_xor_sync(kAll, v, 4);
+          v += __shfl_xor_sync(kAll, v, 8);
+          v += __shfl_xor_sync(kAll, v, 16);
+          if (g == 0) {
+            m_s[warp][8 * nr + 2 * t + i] = m[nr][i];
+            l_s[warp][8 * nr + 2 * t + i] = v;
+          }
+        }
+#pragma unroll
+      for (int j = 0; j < kMt; ++j)
+#pragma unroll
+        for (int nr = 0; nr < kNr; ++nr)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int hi = e >> 1;
+            const int ch = kQ8 && kDp == 128 ? 16 * g + 8 * hi + j
+                           : kDp == 128 ? 64 * hi + 8 * g + j : 8 * g + 4 * hi + j;
+            acc_s[warp][(8 * nr + 2 * t + (e & 1)) * kPitch + ch] = o[j][nr][e];
+          }
+      __syncthreads();
+      const bool whole = first_unit == 0 && count == un.per;
+      const int which = first_unit == 0 ? 1 : 0;
+      uint8_t* part = part_at(p.parts, cta, which);
+      float* part_m = reinterpret_cast<float*>(part + sizeof(PartHead));
+      float* part_l = part_m + kMaxRows;
+      float* part_o = part_l + kMaxRows;
+      if (!whole) {
+        used[which] = true;
+        if (tid == 0) {
+          PartHead h{};
+          h.used = 1;
+          h.seq = s;
+          h.head = kvh;
+          h.tile = tile;
+          h.last = first_unit + count == un.per;
+          *reinterpret_cast<PartHead*>(part) = h;
+        }
+      }
+      for (int i = tid; i < kRows * (kDp / 4); i += kThreads) {
+        const int r = i / (kDp / 4), ch = 4 * (i % (kDp / 4));
+        float top = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, m_s[w][r]);
+        const float safe = top == -INFINITY ? 0.0f : top;
+        float sum = 0.0f;
+        float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float f = fast_exp2(m_s[w][r] - safe);
+          sum += f * l_s[w][r];
+          const float4 v = *reinterpret_cast<const float4*>(&acc_s[w][r * kPitch + ch]);
+          a.x += f * v.x; a.y += f * v.y; a.z += f * v.z; a.w += f * v.w;
+        }
+        if (!whole) {
+          *reinterpret_cast<float4*>(part_o + r * kDp + ch) = a;
+          if (ch == 0) {
+            part_m[r] = top;
+            part_l[r] = sum;
+          }
+          continue;
+        }
+        const int rr = row0 + r;
+        if (rr >= rows || ch >= c.D) continue;
+        const int64_t tok = static_cast<int64_t>(start) + rr / p.group;
+        const int h = kvh * p.group + rr % p.group;
+        const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+        a.x *= inv; a.y *= inv; a.z *= inv; a.w *= inv;
+        if constexpr (kQ8) {
+          const float4 sv = *reinterpret_cast<const float4*>(c.v_scale + kvh * kDp + ch);
+          a.x *= sv.x; a.y *= sv.y; a.z *= sv.z; a.w *= sv.w;
+        }
+        *reinterpret_cast<uint2*>(p.out + (tok * p.Hq + h) * c.D + ch) =
+            make_uint2(pack2<kQBF16>(a.x, a.y), pack2<kQBF16>(a.z, a.w));
+        if (p.lse != nullptr && ch == 0)
+          p.lse[tok * p.Hq + h] = sum > 0.0f ? (top + log2f(sum)) * 0.69314718055994530942f
+                                             : -INFINITY;
+      }
+      __syncthreads();
+      cur += count;
+      off += count;
+    }
+  }
+  if (tid < 2 && !used[tid])
+    reinterpret_cast<PartHead*>(part_at(p.parts, cta, tid))->used = 0;
+}
+
+// Joins the parts of one row of the item that begins in CTA blockIdx.x and
+// ends in a later one: weights 2^(m_i - max), summed in the parts' order.
+template <bool kQBF16, int kDp, int kRows>
+__global__ void __launch_bounds__(128)
+paged_join_kernel(const PagedAttnParams p, int ctas) {
+  __shared__ float w_s[kMaxCtas];
+  __shared__ float red_s[4];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int c0 = blockIdx.x, r = blockIdx.y, tid = threadIdx.x;
+  const PartHead h = *reinterpret_cast<const PartHead*>(part_at(p.parts, c0, 1));
+  if (!h.used) return;
+  int start, n, len;
+  if (!paged_seq(p.c, h.seq, &start, &n, &len)) return;
+  const int rr = h.tile * kRows + r;
+  if (rr >= n * p.group) return;
+  // the parts: CTA c0's second, then the first ones of the CTAs behind it up to the last
+  int parts = 1;
+  while (c0 + parts < ctas) {
+    const PartHead* q = reinterpret_cast<const PartHead*>(part_at(p.parts, c0 + parts, 0));
+    if (!q->used) break;
+    ++parts;
+    if (q->last) break;
+  }
+  float top = -INFINITY;
+  for (int i = tid; i < parts; i += 128) {
+    const float v = reinterpret_cast<const float*>(part_at(p.parts, c0 + i, i == 0) +
+                                                   sizeof(PartHead))[r];
+    w_s[i] = v;
+    top = fmaxf(top, v);
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d /= 2) top = fmaxf(top, __shfl_xor_sync(kAll, top, d));
+  if ((tid & 31) == 0) red_s[tid >> 5] = top;
+  __syncthreads();
+  top = fmaxf(fmaxf(red_s[0], red_s[1]), fmaxf(red_s[2], red_s[3]));
+  const float safe = top == -INFINITY ? 0.0f : top;
+  float sum = 0.0f, acc = 0.0f;
+  const int ch = tid;
+#pragma unroll 4
+  for (int i = 0; i < parts; ++i) {
+    const float* f = reinterpret_cast<const float*>(part_at(p.parts, c0 + i, i == 0) +
+                                                    sizeof(PartHead));
+    const float w = fast_exp2(w_s[i] - safe);
+    sum += w * f[kMaxRows + r];
+    if (ch < kDp) acc += w * f[2 * kMaxRows + r * kDp + ch];
+  }
+  const int64_t tok = static_cast<int64_t>(start) + rr / p.group;
+  const int hq = h.head * p.group + rr % p.group;
+  if (ch < p.c.D) {
+    float v = sum > 0.0f ? acc / sum : 0.0f;
+    if (p.c.kind == kKindQ8) v *= p.c.v_scale[h.head * kDp + ch];
+    uint16_t bits;
+    if constexpr (kQBF16) {
+      const __nv_bfloat16 b = __float2bfloat16_rn(v);
+      bits = *reinterpret_cast<const uint16_t*>(&b);
+    } else {
+      const __half b = __float2half_rn(v);
+      bits = *reinterpret_cast<const uint16_t*>(&b);
+    }
+    p.out[(tok * p.Hq + hq) * p.c.D + ch] = bits;
+  }
+  if (p.lse != nullptr && ch == 0)
+    p.lse[tok * p.Hq + hq] = sum > 0.0f ? (top + log2f(sum)) * 0.69314718055994530942f
+                                        : -INFINITY;
+}
+
+template <int kKind, bool kQBF16, int kDp, int kNr>
+cudaError_t launch_few(const PagedAttnParams& p, int sms, cudaStream_t st) {
+  auto* kern = paged_few_kernel<kKind, kQBF16, kDp, kNr>;
+  static std::atomic<int> resident{0};       // CTAs of one SM (every GB300 is alike)
+  int per = resident.load(std::memory_order_relaxed);
+  if (per == 0) {
+    const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kern, kThreads, 0);
+    if (e != cudaSuccess) return e;
+    per = per < 1 ? 1 : per > 8 ? 8 : per;
+    resident.store(per, std::memory_order_relaxed);
+  }
+  // at most one CTA per unit of the longest lengths the call declares
+  constexpr int kUnitKeys = 16 * kWarps * (kKind == kKindQ8 ? 2 : 1);
+  const int64_t max_units = (static_cast<int64_t>(p.c.max_kv) + kUnitKeys - 1) / kUnitKeys + 1;
+  const int64_t tiles = (static_cast<int64_t>(p.c.max_q) * p.group + 8 * kNr - 1) / (8 * kNr);
+  const int64_t items = tiles * p.c.Hkv * p.c.nseq;
+  int ctas = sms * per < kMaxCtas ? sms * per : kMaxCtas;
+  if (items * max_units < ctas) ctas = static_cast<int>(items * max_units);
+  kern<<<ctas, kThreads, 0, st>>>(p);
+  note_launch();
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas), 8 * kNr);
+  cfg.blockDim = dim3(128);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, paged_join_kernel<kQBF16, kDp, 8 * kNr>, p, ctas);
+  note_launch();
+  return e;
+}
+
+template <int kKind, bool kQBF16>
+cudaError_t launch_kind(const PagedAttnParams& p, int sms, cudaStream_t st) {
+  // 8 rows at a time when a token's group fits and few tokens come: fewer
+  // registers, more loads in flight
+  const bool one = static_cast<int64_t>(p.c.max_q) * p.group <= 8;
+  if (p.c.Dp == 64)
+    return one ? launch_few<kKind, kQBF16, 64, 1>(p, sms, st)
+               : launch_few<kKind, kQBF16, 64, 2>(p, sms, st);
+  return one ? launch_few<kKind, kQBF16, 128, 1>(p, sms, st)
+             : launch_few<kKind, kQBF16, 128, 2>(p, sms, st);
+}
+
+}  // namespace
+
+size_t paged_few_bytes() { return 2 * static_cast<size_t>(kMaxCtas) * kPartBytes; }
+
+cudaError_t launch_paged_few(const PagedAttnParams& p, bool bf16, int sms, cudaStream_t st) {
+  if (p.c.kind == kKindQ8)
+    return bf16 ? launch_kind<kKindQ8, true>(p, sms, st) : launch_kind<kKindQ8, false>(p, sms, st);
+  return bf16 ? launch_kind<kKindBF16, true>(p, sms, st)
+              : launch_kind<kKindF16, false>(p, sms, st);
+}
+
+}  // namespace sage

@@ -1,0 +1,354 @@
+// Rotary positions and the paged cache's writer: one kernel over (token, head)
+// rows.
+//
+//   rotation   y1 = g (x1 cos a - x2 sin a),  y2 = g (x2 cos a + x1 sin a),
+//              a = pos * inv_freq[i] for channel pair i, in fp32
+//   16-bit     the row rounded once to the cache's type
+//   Q8         x = k - mean;  s = max|x| / 127;  code = rint(x * (127 / max|x|))
+//              V code = e4m3(v * (1 / v_scale)), saturating
+//              (each one IEEE fp32 operation, as in the quantisation prologue)
+//
+// The angle of a far position needs more bits than fp32 has: pos * inv_freq is
+// formed in turns as a 64-bit fixed-point fraction, F = frac(inv_freq / 2 pi)
+// * 2^64, whose product with the position modulo 2^64 is exact, so one double
+// multiplication per frequency (2^-53 relative) is the only rounding before
+// the fraction is cut to fp32.
+//
+// The work is bound by memory: each row is read once and written once.  A row
+// belongs to 8 or 16 lanes of 8 channels (one 16-byte vector each); the half
+// layout's partner channels come from another lane by a shuffle.  A group of
+// lanes keeps its head for all tokens of the CTA, so the per-channel means and
+// scales are loaded once.  cos and sin of the CTA's tokens are computed once
+// into shared memory and serve every head.
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "sage_device.cuh"
+#include "sage_kernels.h"
+#include "sage_paged.h"
+
+namespace sage {
+namespace {
+
+constexpr int kRowThreads = 256;
+constexpr int kMaxToks = 8;          // tokens of one CTA
+constexpr unsigned kAll = 0xFFFFFFFFu;
+
+template <bool kBF16>
+__device__ __forceinline__ void unpack8(const uint4& r, float (&x)[8]) {
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (kBF16) {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    } else {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      x[2 * i] = f.x;
+      x[2 * i + 1] = f.y;
+    }
+  }
+}
+
+template <bool kBF16>
+__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (kBF16) {
+      const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&b);
+    } else {
+      const __half2 h = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Channels c0..c0+7 of a row (zeros from D on), element by element.
+__device__ __forceinline__ uint4 load8_slow(const uint16_t* row, int c0, int D) {
+  uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if (c0 + e < D) w[e / 2] |= static_cast<uint32_t>(row[c0 + e]) << (16 * (e & 1));
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// The half layout's partners of channels c0..c0+7, element by element.
+__device__ __forceinline__ uint4 load8_partner(const uint16_t* row, int c0, int R) {
+  const int half = R / 2;
+  uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const int c = c0 + e;
+    if (c < R)
+      w[e / 2] |= static_cast<uint32_t>(row[c < half ? c + half : c - half]) << (16 * (e & 1));
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__device__ __forceinline__ void store8(uint16_t* row, int c0, int D, bool vec, const uint4& v) {
+  if (vec) {
+    *reinterpret_cast<uint4*>(row + c0) = v;
+    return;
+  }
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if (c0 + e < D) row[c0 + e] = static_cast<uint16_t>(w[e / 2] >> (16 * (e & 1)));
+}
+
+// The sequence that holds row `tok`: the last s with cu_q[s] <= tok, by a
+// warp's 32-way search (each round trip to memory cuts the range by 32).
+__device__ __forceinline__ int find_seq(const PagedGeo& c, int64_t tok, int lane) {
+  int lo = 0, hi = c.nseq;
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32;
+    const int i = lo + lane * step;
+    const unsigned b = __ballot_sync(kAll, i < hi && c.cu_q[i] <= tok);
+    const int n = __popc(b);
+    if (n == 0) break;
+    lo += (n - 1) * step;
+    hi = min(hi, lo + step);
+  }
+  return lo;
+}
+
+// kMode: 0 rope, 1 append 16-bit, 2 append Q8.  kLanes: lanes of a row.
+// kShfl: the half layout's partner vector is another lane's whole vector.
+template <int kMode, bool kBF16, int kLanes, bool kShfl>
+__global__ void __launch_bounds__(kRowThreads)
+rows_kernel(const RowsParams p) {
+  __shared__ float2 cs[kMaxToks * 64];
+  __shared__ int64_t pos_s[kMaxToks];
+  __shared__ int page_s[kMaxToks];          // -1: nothing is written for this token
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * p.toks;
+  const int nt = static_cast<int>(min(static_cast<int64_t>(p.toks), p.T - t0));
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int half = p.R / 2;
+  const PagedGeo& c = p.c;
+
+  if constexpr (kMode == 0) {
+    if (threadIdx.x < nt) {
+      pos_s[threadIdx.x] = p.pos64 ? static_cast<const int64_t*>(p.pos)[t0 + threadIdx.x]
+                                   : static_cast<const int32_t*>(p.pos)[t0 + threadIdx.x];
+      page_s[threadIdx.x] = 0;
+    }
+  } else {
+    for (int i = warp; i < nt; i += kRowThreads / 32) {
+      const int64_t tok = t0 + i;
+      const int s = find_seq(c, tok, lane);
+      if (lane == 0) {
+        int start = 0, n = 0, len = 0, page = -1;
+        int64_t pos = -1;
+        if (paged_seq(c, s, &start, &n, &len) && tok >= start && tok < start + n) {
+          pos = static_cast<int64_t>(len) - n + (tok - start);
+          if (pos >= 0) page = paged_page(c, s, static_cast<int>(pos / c.page_size));
+        }
+        pos_s[i] = pos;
+        page_s[i] = pos < 0 ? -2 : page;    // -2: no such token; -1: no such page
+      }
+    }
+  }
+  __syncthreads();
+  if (p.inv_freq != nullptr) {
+    for (int i = threadIdx.x; i < nt * half; i += kRowThreads) {
+      const int t = i / half, f = i - t * half;
+      const double turns = p.inv_freq[f] * 0.15915494309189533577;   // 1 / (2 pi)
+      const uint64_t frac = __double2ull_rn((turns - floor(turns)) * 18446744073709551616.0);
+      const uint64_t a = frac * static_cast<uint64_t>(pos_s[t]) + (1ull << 31);
+      float sn, cn;
+      sincospif(static_cast<float>(static_cast<int32_t>(a >> 32)) * 4.656612873077392578125e-10f,
+                &sn, &cn);                                           // 2^-31
+      cs[t * 64 + f] = make_float2(cn * p.mscale, sn * p.mscale * p.sign);
+    }
+  }
+  __syncthreads();
+
+  const int nq = p.Hq;
+  const int rows = nq + p.Hkv * (kMode == 0 ? 1 : 2);
+  const int sub = threadIdx.x % kLanes;
+  const int c0 = 8 * sub;
+  const bool live = c0 < p.D;
+  const int groups = kRowThreads / kLanes;
+  // partner lane of the half layout
+  int mate = sub;
+  if (kShfl && c0 < p.R) mate = c0 < half ? sub + half / 8 : sub - half / 8;
+  const int rstep = groups * gridDim.y;
+  const int rend = (rows + rstep - 1) / rstep * rstep;   // whole warps stay in the loop
+  for (int r = blockIdx.y * groups + threadIdx.x / kLanes; r < rend; r += rstep) {
+    const bool has = r < rows && live;
+    const int what = r < nq ? 0 : (r < nq + p.Hkv ? 1 : 2);          // q, k, v
+    const int h = what == 0 ? r : (what == 1 ? r - nq : r - nq - p.Hkv);
+    const uint16_t* src = what == 0 ? p.q + h * p.q_head
+                          : what == 1 ? p.k + h * p.k_head : p.v + h * p.v_head;
+    const int64_t tok_stride = what == 0 ? p.q_tok : what == 1 ? p.k_tok : p.v_tok;
+    const bool turn = p.inv_freq != nullptr && what != 2;
+    float chan[8];                          // Q8: k mean, or 1 / v scale
+    if constexpr (kMode == 2) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) chan[e] = 0.0f;
+      if (has && what != 0) {
+        const float* src4 = (what == 1 ? c.k_mean : c.v_scale) + h * c.Dp + c0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          chan[e] = src4[e];
+          if (what == 2) chan[e] = chan[e] > 0.0f ? __fdiv_rn(1.0f, chan[e]) : 0.0f;
+        }
+      }
+    }
+    constexpr int kUnroll = kShfl ? 4 : 1;
+    for (int tb = 0; tb < nt; tb += kUnroll) {
+      uint4 raw[kUnroll], rawp[kUnroll];
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        raw[u] = make_uint4(0, 0, 0, 0);
+        if (has && tb + u < nt) {
+          const uint16_t* row = src + (t0 + tb + u) * tok_stride;
+          raw[u] = p.vec ? *reinterpret_cast<const uint4*>(row + c0) : load8_slow(row, c0, p.D);
+          if constexpr (!kShfl)
+            rawp[u] = turn && !p.interleaved ? load8_partner(row, c0, p.R) : raw[u];
+        }
+      }
+      __syncwarp();                         // in place: every lane has read its row
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        const int t = tb + u;
+        if (t >= nt) break;                 // the same for every lane
+        if constexpr (kShfl) {
+          rawp[u].x = __shfl_sync(kAll, raw[u].x, mate, kLanes);
+          rawp[u].y = __shfl_sync(kAll, raw[u].y, mate, kLanes);
+          rawp[u].z = __shfl_sync(kAll, raw[u].z, mate, kLanes);
+          rawp[u].w = __shfl_sync(kAll, raw[u].w, mate, kLanes);
+        }
+        float x[8];
+        unpack8<kBF16>(raw[u], x);
+        if (turn && c0 < p.R) {
+          if (p.interleaved) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (c0 + 2 * i < p.R) {
+                const float2 a = cs[t * 64 + c0 / 2 + i];
+                const float x1 = x[2 * i], x2 = x[2 * i + 1];
+                x[2 * i] = x1 * a.x - x2 * a.y;
+                x[2 * i + 1] = x2 * a.x + x1 * a.y;
+              }
+          } else {
+            float y[8];
+            unpack8<kBF16>(rawp[u], y);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const int ch = c0 + e;
+              if (ch < p.R) {
+                const bool low = ch < half;
+                const float2 a = cs[t * 64 + (low ? ch : ch - half)];
+                x[e] = low ? x[e] * a.x - y[e] * a.y : x[e] * a.x + y[e] * a.y;
+              }
+            }
+          }
+        }
+        if constexpr (kMode == 0) {
+          if (has) {
+            uint16_t* dst = what == 0 ? p.q_out + (t0 + t) * p.qo_tok + h * p.qo_head
+                                      : p.k_out + (t0 + t) * p.ko_tok + h * p.ko_head;
+            store8(dst, c0, p.D, p.vec, pack8<kBF16>(x));
+          }
+        } else {
+          if (what == 0) {
+            if (has && page_s[t] != -2)
+              store8(p.q_out + (t0 + t) * p.qo_tok + h * p.qo_head, c0, p.D, p.vec,
+                     pack8<kBF16>(x));
+          }
+          const int page = page_s[t];
+          const int slot = static_cast<int>(pos_s[t] % c.page_size);
+          const int64_t at = page * c.page_stride + slot * c.token_stride + h * c.head_stride + c0;
+          const bool put = has && what != 0 && page >= 0;
+          if constexpr (kMode == 1) {
+            if (put) {
+              uint16_t* base = reinterpret_cast<uint16_t*>(what == 1 ? c.k : c.v);
+              *reinterpret_cast<uint4*>(base + at) = turn ? pack8<kBF16>(x) : raw[u];
+            }
+          } else {
+            float top = 0.0f;
+            if (what == 1) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                x[e] = __fsub_rn(x[e], chan[e]);
+                top = fmaxf(top, fabsf(x[e]));
+              }
+            }
+            // lanes of one row share `what`; the shuffles run in every lane
+#pragma unroll
+            for (int d = kLanes / 2; d > 0; d /= 2)
+              top = fmaxf(top, __shfl_xor_sync(kAll, top, d, kLanes));
+            if (put && what == 1) {
+              const float inv = top > 0.0f ? __fdiv_rn(127.0f, top) : 0.0f;
+              uint32_t w[2] = {0, 0};
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                w[e / 4] |= (static_cast<uint32_t>(__float2int_rn(__fmul_rn(x[e], inv))) & 0xFFu)
+                            << (8 * (e & 3));
+              *reinterpret_cast<uint2*>(c.k + at) = make_uint2(w[0], w[1]);
+              if (sub == 0)
+                c.k_scale[(static_cast<int64_t>(page) * c.Hkv + h) * c.page_size + slot] =
+                    __fdiv_rn(top, 127.0f);
+            } else if (put) {
+              uint32_t w[2];
+#pragma unroll
+              for (int i = 0; i < 2; ++i)
+                w[i] = pack_e4m3x2(__fmul_rn(x[4 * i], chan[4 * i]),
+                                   __fmul_rn(x[4 * i + 1], chan[4 * i + 1])) |
+                       pack_e4m3x2(__fmul_rn(x[4 * i + 2], chan[4 * i + 2]),
+                                   __fmul_rn(x[4 * i + 3], chan[4 * i + 3])) << 16;
+              *reinterpret_cast<uint2*>(c.v + at) = make_uint2(w[0], w[1]);
+            }
+          }
+        }
+      }
+      __syncwarp();
+    }
+  }
+}
+
+template <int kMode, bool kBF16, int kLanes>
+cudaError_t launch_lanes(const RowsParams& p, bool shfl, dim3 grid, cudaStream_t st) {
+  if (shfl) rows_kernel<kMode, kBF16, kLanes, true><<<grid, kRowThreads, 0, st>>>(p);
+  else rows_kernel<kMode, kBF16, kLanes, false><<<grid, kRowThreads, 0, st>>>(p);
+  note_launch();
+  return cudaGetLastError();
+}
+
+template <int kMode>
+cudaError_t launch_mode(const RowsParams& p0, bool bf16, int sms, cudaStream_t st) {
+  RowsParams p = p0;
+  const int lanes = p.D <= 64 ? 8 : 16;
+  const int rows = p.Hq + p.Hkv * (kMode == 0 ? 1 : 2);
+  const int groups = kRowThreads / lanes;
+  // Few tokens: one per CTA, and its heads over several CTAs, so that every SM
+  // has work; many: kMaxToks, which serve the means, scales and angles.
+  p.toks = 1;
+  while (p.toks < kMaxToks && p.T / (2 * p.toks) >= 4 * sms) p.toks *= 2;
+  const int64_t ctas = (p.T + p.toks - 1) / p.toks;
+  int64_t y = (rows + groups - 1) / groups;
+  if (ctas * y > 2 * sms) y = 2 * sms / ctas > 1 ? 2 * sms / ctas : 1;
+  if (ctas > 0x7FFFFFFF) return cudaErrorInvalidValue;
+  const dim3 grid(static_cast<unsigned>(ctas), static_cast<unsigned>(y));
+  const bool shfl = p.vec && (p.inv_freq == nullptr || p.interleaved || p.R % 16 == 0);
+  if (lanes == 8)
+    return bf16 ? launch_lanes<kMode, true, 8>(p, shfl, grid, st)
+                : launch_lanes<kMode, false, 8>(p, shfl, grid, st);
+  return bf16 ? launch_lanes<kMode, true, 16>(p, shfl, grid, st)
+              : launch_lanes<kMode, false, 16>(p, shfl, grid, st);
+}
+
+}  // namespace
+
+cudaError_t launch_rows(const RowsParams& p, int mode, bool bf16, int sms, cudaStream_t st) {
+  if (mode == 0) return launch_mode<0>(p, bf16, sms, st);
+  if (mode == 1) return launch_mode<1>(p, bf16, sms, st);
+  return launch_mode<2>(p, bf16, sms, st);
+}
+
+}  // namespace sage

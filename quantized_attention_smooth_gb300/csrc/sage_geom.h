@@ -17,6 +17,7 @@ namespace sage {
 constexpr uint32_t kStatusTimeout = 1u;      // a bounded wait ran out
 constexpr uint32_t kStatusBadSeqlens = 2u;   // cu_seqlens inconsistent
 constexpr uint32_t kStatusBadItem = 4u;      // a work item decoded outside the call's plan
+constexpr uint32_t kStatusBadPage = 8u;      // a block table entry outside the cache
 
 struct SegGeo {
   int64_t nseg, Hq, Hkv, Lq, Lk, D, Dp;

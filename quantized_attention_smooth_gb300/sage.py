@@ -12,7 +12,7 @@ import os
 
 from . import _build
 
-F16, BF16 = 0, 1
+F16, BF16, Q8 = 0, 1, 2
 HND, NHD = 0, 1
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_WORKSPACE, ERR_CUDA, ERR_DEVICE_TIMEOUT = range(6)
 STATUS_NAMES = ["OK", "INVALID_ARG", "UNSUPPORTED", "WORKSPACE", "CUDA", "DEVICE_TIMEOUT"]
@@ -30,6 +30,7 @@ EXPORTS = (
     "sage_debug_pv_accum", "sage_debug_set_fault_launches", "sage_kv_stats_noalloc_status",
     "sage_debug_tc_rate", "sage_workspace_bytes_varlen_host", "sage_attn_fwd_varlen_host",
     "sage_debug_set_host_fail_chunk",
+    "sage_rope", "sage_workspace_bytes_paged", "sage_kv_append", "sage_attn_paged",
 )
 
 
@@ -56,6 +57,26 @@ class Quantized(ctypes.Structure):
         ("s_q", ctypes.c_void_p), ("s_k", ctypes.c_void_p), ("s_v", ctypes.c_void_p),
         ("k_mean", ctypes.c_void_p), ("stats", ctypes.c_void_p),
         ("status", ctypes.c_void_p), ("v_fp16", ctypes.c_int32),
+    ]
+
+
+class _CacheC(ctypes.Structure):
+    """Mirror of sage_paged_cache."""
+    _fields_ = [
+        ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+        ("k_mean", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+        ("num_pages", ctypes.c_int64), ("page_size", ctypes.c_int64), ("Hkv", ctypes.c_int64),
+        ("D", ctypes.c_int64), ("page_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
+        ("head_stride", ctypes.c_int64), ("kind", ctypes.c_int32),
+    ]
+
+
+class _BatchC(ctypes.Structure):
+    """Mirror of sage_paged_batch."""
+    _fields_ = [
+        ("cu_q", ctypes.c_void_p), ("kv_lens", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
+        ("nseq", ctypes.c_int64), ("total_q", ctypes.c_int64), ("table_stride", ctypes.c_int64),
+        ("table_width", ctypes.c_int64), ("max_q", ctypes.c_int32), ("max_kv", ctypes.c_int32),
     ]
 
 
@@ -106,6 +127,10 @@ def _load():
         "sage_last_error": ([], ctypes.c_char_p),
         "sage_kv_stats_noalloc": ([P, P, I, I, I64, I64, I64, I64, P, P, P], I),
         "sage_launch_count": ([], ctypes.c_uint64),
+        "sage_rope": ([P, P, P, P, I, I64, I64, I64, I64, P, P, P, P, P, I, P, I64, I, F, I, P], I),
+        "sage_workspace_bytes_paged": ([], SZ),
+        "sage_kv_append": ([P, P, P, P, P, P, I, I64, P, P, P, P, P, I64, I, F, P, SZ, P], I),
+        "sage_attn_paged": ([P, P, P, P, P, I, I64, P, I64, I64, F, P, SZ, P], I),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -410,6 +435,302 @@ def sageattn_qk_int8_pv_fp16(q, k, v, tensor_layout="HND", is_causal=False, sm_s
     import torch
     out = torch.empty(q.shape, dtype=torch.float32, device=q.device)
     return attn_fwd_pv16(q, k, v, out, tensor_layout, is_causal, sm_scale)
+
+
+# ------------------------------------------------------------------ serving
+def rope_freqs(rotary_dim, base=10000.0, scaling=None, factor=1.0, original_len=4096, low=1.0,
+               high=32.0, device="cuda"):
+    """(inv_freq, mscale) for `rope` and `kv_append`: inv_freq float64
+    [rotary_dim / 2] on `device`, base ** (-2 i / rotary_dim), scaled for
+    lengths beyond `original_len`:
+      None        unscaled
+      "linear"    every frequency divided by `factor` (positions interpolated)
+      "ntk"       base times factor ** (R / (R - 2)): the longest wavelength is
+                  stretched by `factor`, the shortest kept
+      "by_parts"  frequencies that turn fewer than `low` times in original_len
+                  divided by `factor`, those above `high` kept, a linear ramp
+                  between
+      "yarn"      by_parts, and mscale = 0.1 ln(factor) + 1 on cos and sin"""
+    import math
+    import torch
+    r = int(rotary_dim)
+    if r < 2 or r % 2:
+        raise ValueError(f"rope_freqs: rotary_dim must be even and positive, got {rotary_dim}")
+    if not factor >= 1.0:
+        raise ValueError(f"rope_freqs: factor must be at least 1, got {factor}")
+    if scaling == "ntk":
+        if r == 2:
+            raise ValueError("rope_freqs: ntk scaling needs rotary_dim > 2")
+        base = base * factor ** (r / (r - 2))
+    f = float(base) ** (-torch.arange(r // 2, dtype=torch.float64) * 2 / r)
+    mscale = 1.0
+    if scaling == "linear":
+        f = f / factor
+    elif scaling in ("by_parts", "yarn"):
+        keep = ((original_len * f / (2 * math.pi) - low) / (high - low)).clamp(0, 1)
+        f = f * (keep + (1 - keep) / factor)
+        if scaling == "yarn":
+            mscale = 0.1 * math.log(factor) + 1.0
+    elif scaling not in (None, "ntk"):
+        raise ValueError(f"rope_freqs: unknown scaling {scaling!r}")
+    return f.to(device), mscale
+
+
+def _rows3(where, name, t, like=None):
+    """A (T, H, D) view the serving calls read or write: fp16/bf16 on the
+    current CUDA device, channel stride 1."""
+    if t.dim() != 3 or t.stride(2) != 1 and t.shape[2] > 1:
+        raise ValueError(f"{where}: {name} must be (T, H, D) with contiguous channels, got shape "
+                         f"{tuple(t.shape)}, strides {t.stride()}")
+    _on_device(where, name, t)
+    if like is not None and t.dtype != like.dtype:
+        raise TypeError(f"{where}: {name} is {t.dtype}, not {like.dtype}")
+
+
+def _on_device(where, name, t):
+    import torch
+    if not t.is_cuda:
+        raise ValueError(f"{where}: {name} is not on a CUDA device")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{where}: {name} is on {t.device}, the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+
+
+def _row_strides(t):
+    """None for a dense (T, H, D) tensor, else its {token, head} strides."""
+    if t is None or t.is_contiguous():
+        return None
+    return (ctypes.c_int64 * 2)(t.stride(0), t.stride(1))
+
+
+def _empty_on(stream, make):
+    """Allocates under `stream`, so that the memory is not reused while that
+    stream still works on it."""
+    if stream is None:
+        return make()
+    import torch
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream)
+    with torch.cuda.stream(stream):
+        return make()
+
+
+def _freqs(where, inv_freq):
+    import torch
+    if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+        raise ValueError(f"{where}: inv_freq must be a contiguous 1-D float64 tensor")
+    _on_device(where, "inv_freq", inv_freq)
+
+
+def _out_like(where, name, out, t):
+    if tuple(out.shape) != tuple(t.shape):
+        raise ValueError(f"{where}: {name} has shape {tuple(out.shape)}, not {tuple(t.shape)}")
+    _rows3(where, name, out, t)
+
+
+def rope(q, k, positions, inv_freq, interleaved=False, mscale=1.0, inverse=False, q_out=None,
+         k_out=None, stream=None):
+    """Rotary positions of q (T, Hq, D) and k (T, Hkv, D), fp16/bf16 views with
+    contiguous channels; k may be None.  positions: int64 or int32 (T,);
+    inv_freq: float64 (R/2,), R <= D (see rope_freqs).  Pairs are (i, i + R/2),
+    or (2i, 2i + 1) with `interleaved`.  q_out=q (k_out=k) turns in place.
+    `inverse` turns back; applied to the outputs' gradients with the same
+    mscale it gives the inputs' gradients.  Returns (q_out, k_out)."""
+    import torch
+    _rows3("rope", "q", q)
+    T, Hq, D = q.shape
+    Hkv = 0
+    if k is not None:
+        _rows3("rope", "k", k, q)
+        Hkv = k.shape[1]
+        if k.shape[0] != T or k.shape[2] != D:
+            raise ValueError(f"rope: k has shape {tuple(k.shape)}, q {tuple(q.shape)}")
+    if positions.dtype not in (torch.int64, torch.int32) or tuple(positions.shape) != (T,) or \
+            not positions.is_contiguous():
+        raise ValueError("rope: positions must be a contiguous int64 or int32 tensor of T entries")
+    _on_device("rope", "positions", positions)
+    _freqs("rope", inv_freq)
+    if q_out is None:
+        q_out = _empty_on(stream, lambda: torch.empty((T, Hq, D), dtype=q.dtype, device=q.device))
+    else:
+        _out_like("rope", "q_out", q_out, q)
+    if k is None:
+        k_out = None
+    elif k_out is None:
+        k_out = _empty_on(stream, lambda: torch.empty((T, Hkv, D), dtype=q.dtype, device=q.device))
+    else:
+        _out_like("rope", "k_out", k_out, k)
+    rc = _lib.sage_rope(_ptr(q), _ptr(k), _ptr(q_out), _ptr(k_out), _dtype_code(q), T, Hq, Hkv, D,
+                        _row_strides(q), _row_strides(k), _row_strides(q_out), _row_strides(k_out),
+                        _ptr(positions), 64 if positions.dtype == torch.int64 else 32,
+                        _ptr(inv_freq), 2 * inv_freq.numel(), int(bool(interleaved)),
+                        float(mscale), int(bool(inverse)), _stream(stream))
+    _check(rc, "sage_rope")
+    return q_out, k_out
+
+
+class PagedCache:
+    """A paged key/value cache over the caller's tensors (kept alive by it).
+    k, v: (pages, slots, Hkv, D) ("NHD") or (pages, Hkv, slots, D) ("HND"),
+    sharing their strides, channels contiguous.  fp16/bf16 tensors hold K and V
+    as they are; an int8 k with a float8_e4m3fn v holds them quantised, with
+    k_scale float32 (pages, Hkv, slots) and the fixed k_mean and v_scale
+    float32 (Hkv, Dp), Dp = 64 if D <= 64 else 128 (kv_stats_noalloc writes
+    them from a sample of keys and values)."""
+
+    def __init__(self, k, v, layout="NHD", k_scale=None, k_mean=None, v_scale=None):
+        import torch
+        lay = _layout_code(layout)
+        if k.dim() != 4 or tuple(v.shape) != tuple(k.shape):
+            raise ValueError(f"PagedCache: k {tuple(k.shape)} and v {tuple(v.shape)} must be 4-D "
+                             "tensors of one shape")
+        q8 = k.dtype == torch.int8
+        if q8 and v.dtype != torch.float8_e4m3fn or not q8 and (
+                k.dtype not in (torch.float16, torch.bfloat16) or v.dtype != k.dtype):
+            raise TypeError(f"PagedCache: k {k.dtype} and v {v.dtype} must be both float16, both "
+                            "bfloat16, or int8 and float8_e4m3fn")
+        self.kind = Q8 if q8 else _dtype_code(k)
+        pages, self.D = k.shape[0], k.shape[3]
+        slots, self.Hkv = (k.shape[2], k.shape[1]) if lay == HND else (k.shape[1], k.shape[2])
+        st, page_dims = k.stride(), (2, 1) if lay == HND else (1, 2)
+        for name, t in (("k", k), ("v", v)):
+            _on_device("PagedCache", name, t)
+            if any(n > 1 and a != b for n, a, b in zip(k.shape, t.stride(), st)):
+                raise ValueError(f"PagedCache: k and v must share their strides ({k.stride()} and "
+                                 f"{v.stride()})")
+        if st[3] != 1 and self.D > 1:
+            raise ValueError("PagedCache: the channels must be contiguous")
+        scales = (("k_scale", k_scale, (pages, self.Hkv, slots)),
+                  ("k_mean", k_mean, (self.Hkv, 64 if self.D <= 64 else 128)),
+                  ("v_scale", v_scale, (self.Hkv, 64 if self.D <= 64 else 128)))
+        for name, t, shape in scales:
+            if not q8:
+                if t is not None:
+                    raise ValueError(f"PagedCache: {name} belongs to a quantised cache only")
+                continue
+            if t is None or t.dtype != torch.float32 or tuple(t.shape) != shape or \
+                    not t.is_contiguous():
+                raise ValueError(f"PagedCache: {name} must be a contiguous float32 tensor of shape "
+                                 f"{shape}")
+            _on_device("PagedCache", name, t)
+        self.k, self.v, self.k_scale, self.k_mean, self.v_scale = k, v, k_scale, k_mean, v_scale
+        ptr = lambda t: 0 if t is None else t.data_ptr()
+        self._c = _CacheC(ptr(k), ptr(v), ptr(k_scale), ptr(k_mean), ptr(v_scale), pages, slots,
+                          self.Hkv, self.D, st[0], st[page_dims[0]], st[page_dims[1]], self.kind)
+
+
+class PagedBatch:
+    """A batch of new tokens: int32 CUDA tensors cu_q (n + 1 offsets of the
+    packed rows), kv_lens (n cached lengths, the new tokens included) and
+    block_table (n, width) of page indices; max_q and max_kv bound the new
+    tokens and the length of every sequence."""
+
+    def __init__(self, cu_q, kv_lens, block_table, max_q, max_kv):
+        import torch
+        for name, t in (("cu_q", cu_q), ("kv_lens", kv_lens), ("block_table", block_table)):
+            _on_device("PagedBatch", name, t)
+            if t.dtype != torch.int32:
+                raise TypeError(f"PagedBatch: {name} must be int32, got {t.dtype}")
+        n = kv_lens.numel()
+        if cu_q.dim() != 1 or cu_q.numel() != n + 1 or kv_lens.dim() != 1 or \
+                not cu_q.is_contiguous() or not kv_lens.is_contiguous():
+            raise ValueError("PagedBatch: cu_q and kv_lens must be contiguous, of n + 1 and n "
+                             "entries")
+        if block_table.dim() != 2 or block_table.shape[0] != n or \
+                block_table.shape[1] > 1 and block_table.stride(1) != 1:
+            raise ValueError(f"PagedBatch: block_table must be (n, width) with contiguous rows, "
+                             f"got {tuple(block_table.shape)}")
+        self.cu_q, self.kv_lens, self.block_table = cu_q, kv_lens, block_table
+        self.nseq, self.max_q, self.max_kv = n, int(max_q), int(max_kv)
+        self._c = _BatchC(cu_q.data_ptr(), kv_lens.data_ptr(), block_table.data_ptr(), n, 0,
+                          block_table.stride(0), block_table.shape[1], self.max_q, self.max_kv)
+
+    def _rows(self, total_q):
+        c = _BatchC.from_buffer_copy(self._c)       # calls of several threads share the batch
+        c.total_q = total_q
+        return ctypes.byref(c)
+
+
+def workspace_bytes_paged() -> int:
+    return int(_lib.sage_workspace_bytes_paged())
+
+
+def alloc_workspace_paged(device="cuda", stream=None):
+    """A workspace of kv_append and attn_paged, its status word cleared.  One
+    serves any number of calls in stream order."""
+    def make():
+        ws = alloc_workspace(workspace_bytes_paged(), device)
+        ws[:256].zero_()
+        return ws
+    return _empty_on(stream, make)
+
+
+def kv_append(cache, batch, k, v, q=None, q_out=None, inv_freq=None, interleaved=False, mscale=1.0,
+              ws=None, stream=None):
+    """Writes the batch's new k and v (T, Hkv, D) into the cache.  With
+    inv_freq, k is turned at each token's position first, and q (T, Hq, D), if
+    given, into q_out (returned)."""
+    import torch
+    _rows3("kv_append", "k", k)
+    _rows3("kv_append", "v", v, k)
+    T = k.shape[0]
+    if k.shape[1] != cache.Hkv or k.shape[2] != cache.D or v.shape != k.shape:
+        raise ValueError(f"kv_append: k {tuple(k.shape)} and v {tuple(v.shape)} do not fit a cache "
+                         f"of {cache.Hkv} heads of {cache.D} channels")
+    Hq = 0
+    if q is not None:
+        _rows3("kv_append", "q", q, k)
+        Hq = q.shape[1]
+        if q.shape[0] != T or q.shape[2] != cache.D:
+            raise ValueError(f"kv_append: q has shape {tuple(q.shape)}, k {tuple(k.shape)}")
+        if q_out is None:
+            q_out = _empty_on(stream, lambda: torch.empty((T, Hq, cache.D), dtype=q.dtype,
+                                                          device=q.device))
+        else:
+            _out_like("kv_append", "q_out", q_out, q)
+    if inv_freq is not None:
+        _freqs("kv_append", inv_freq)
+    if ws is None:
+        ws = alloc_workspace_paged(k.device, stream)
+    rc = _lib.sage_kv_append(
+        ctypes.byref(cache._c), batch._rows(T), _ptr(k), _ptr(v), _ptr(q),
+        _ptr(q_out if q is not None else None), _dtype_code(k), Hq, _row_strides(k),
+        _row_strides(v), _row_strides(q), _row_strides(q_out if q is not None else None),
+        _ptr(inv_freq), 0 if inv_freq is None else 2 * inv_freq.numel(), int(bool(interleaved)),
+        float(mscale), _ptr(ws), ws.numel(), _stream(stream))
+    _check(rc, "sage_kv_append")
+    return q_out if q is not None else None
+
+
+def attn_paged(cache, batch, q, out=None, window=0, sinks=0, sm_scale=None, lse=None, ws=None,
+               stream=None):
+    """Attention of the batch's new tokens, q (T, Hq, D), over the cache:
+    causal, with window > 0 only the last `window` keys and the first `sinks`
+    ones.  Returns out (T, Hq, D) of q's type; lse, if given, is a float32
+    (T, Hq) tensor that receives the log-sum-exp of every row."""
+    import torch
+    _rows3("attn_paged", "q", q)
+    T, Hq, D = q.shape
+    if D != cache.D:
+        raise ValueError(f"attn_paged: q has {D} channels, the cache {cache.D}")
+    if out is None:
+        out = _empty_on(stream, lambda: torch.empty((T, Hq, D), dtype=q.dtype, device=q.device))
+    else:
+        _out_like("attn_paged", "out", out, q)
+        if not out.is_contiguous():
+            raise ValueError("attn_paged: out must be contiguous")
+    if lse is not None:
+        if lse.dtype != torch.float32 or tuple(lse.shape) != (T, Hq) or not lse.is_contiguous():
+            raise ValueError("attn_paged: lse must be a contiguous float32 (T, Hq) tensor")
+        _on_device("attn_paged", "lse", lse)
+    if ws is None:
+        ws = alloc_workspace_paged(q.device, stream)
+    rc = _lib.sage_attn_paged(ctypes.byref(cache._c), batch._rows(T), _ptr(q), _ptr(out),
+                              _ptr(lse), _dtype_code(q), Hq, _row_strides(q), int(window),
+                              int(sinks), float(sm_scale or 0.0), _ptr(ws), ws.numel(),
+                              _stream(stream))
+    _check(rc, "sage_attn_paged")
+    return out
 
 
 def debug_qk_int32(qt: Quantized, seg, hq, qtile, ktile, out=None, stream=None):
