@@ -16,6 +16,11 @@ bool on(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 
 
 constexpr int64_t kMaxStride = int64_t(1) << 39;
 constexpr size_t kStatusBytes = 256;
+// Rows (new tokens times the group) up to which a sequence is served by the
+// kernel for few rows.
+constexpr int kFewRows = 16;
+
+size_t few_bytes() { return (paged_few_bytes() + 255) / 256 * 256; }
 
 // {token, head} strides of a (T, H, D) tensor; NULL: dense.  A dimension of
 // one entry has no stride worth checking.
@@ -146,7 +151,7 @@ sage_status paged_geo(const sage_paged_cache* cache, const sage_paged_batch* b, 
 extern "C" {
 
 size_t sage_workspace_bytes_paged(void) {
-  return (kStatusBytes + paged_few_bytes() + 255) / 256 * 256;
+  return kStatusBytes + few_bytes() + paged_many_bytes();
 }
 
 sage_status sage_rope(const void* q, const void* k, void* q_out, void* k_out, int dtype, int64_t T,
@@ -308,12 +313,23 @@ sage_status sage_attn_paged(const sage_paged_cache* cache, const sage_paged_batc
   p.scale_log2 = (sm_scale > 0.0f ? sm_scale : 1.0f / sqrtf(static_cast<float>(D))) *
                  1.44269504088896340736f;
   p.q_vec = vec_rows(q, p.q_tok, p.q_head);
-  p.min_rows = 0;
-  p.max_rows = INT_MAX;
-  p.parts = static_cast<uint8_t*>(ws) + kStatusBytes;
   p.timeout_ns = device_wait_ns();
-  const cudaError_t e = launch_paged_few(p, dtype == SAGE_BF16, sms,
-                                         reinterpret_cast<cudaStream_t>(stream));
+  uint8_t* parts = static_cast<uint8_t*>(ws) + kStatusBytes;
+  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const bool bf16 = dtype == SAGE_BF16;
+  const int64_t most = static_cast<int64_t>(batch->max_q) * p.group;
+  const bool many = most > kFewRows && paged_many_serves(p.c);
+  cudaError_t e = cudaSuccess;
+  p.min_rows = 0;
+  p.max_rows = many ? kFewRows : INT_MAX;
+  p.parts = parts;
+  e = launch_paged_few(p, bf16, sms, st);
+  if (e == cudaSuccess && many) {
+    p.min_rows = kFewRows + 1;
+    p.max_rows = INT_MAX;
+    p.parts = parts + few_bytes();
+    e = launch_paged_many(p, bf16, sms, st);
+  }
   return e == cudaSuccess ? succeeded() : cuda_refused(e, "paged attention launch");
 }
 

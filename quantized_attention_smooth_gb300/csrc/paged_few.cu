@@ -29,12 +29,8 @@
 // e4m3 values <= 448; bf16 queries are scaled per row by a power of two first.
 
 #include <atomic>
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-
-#include "sage_device.cuh"
 #include "sage_kernels.h"
-#include "sage_paged.h"
+#include "sage_paged_device.cuh"
 
 namespace sage {
 namespace {
@@ -54,25 +50,6 @@ __device__ __forceinline__ uint8_t* part_at(uint8_t* parts, int cta, int which) 
   return parts + (static_cast<size_t>(cta) * 2 + which) * kPartBytes;
 }
 
-// What a sequence's rows can see, in blocks of 16 keys: `sink` blocks from key
-// 0, then the blocks from `from` on, `count` in all.
-struct Span {
-  int sink, from, count;
-};
-__device__ __forceinline__ Span span_of(int p_lo, int p_hi, int window, int sinks) {
-  Span r{0, 0, 0};
-  if (p_hi < 0) return r;
-  int lo = 0;
-  if (window > 0 && p_lo - window + 1 > 0) lo = p_lo - window + 1;
-  r.from = lo / 16;
-  if (lo > 0) {
-    const int s = min(sinks, lo);
-    r.sink = min((s + 15) / 16, r.from);
-  }
-  r.count = r.sink + p_hi / 16 + 1 - r.from;
-  return r;
-}
-
 struct Units {
   int per, tiles;            // units of one item; row tiles of one kv head
   int64_t total;
@@ -84,7 +61,7 @@ __device__ __forceinline__ Units units_of(const PagedAttnParams& p, int s, int* 
   if (!paged_seq(p.c, s, start, n, len)) return u;
   const int64_t rows = static_cast<int64_t>(*n) * p.group;
   if (rows < p.min_rows || rows > p.max_rows || rows == 0) return u;
-  const Span sp = span_of(*len - *n, *len - 1, p.window, p.sinks);
+  const Span sp = span_of<16>(*len - *n, *len - 1, p.window, p.sinks);
   u.per = max(1, (sp.count + kUnitBlocks - 1) / kUnitBlocks);
   u.tiles = static_cast<int>((rows + kRows - 1) / kRows);
   u.total = static_cast<int64_t>(u.per) * u.tiles * p.c.Hkv;
@@ -110,55 +87,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
   uint32_t d;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
-}
-
-template <bool kBF16>
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  if constexpr (kBF16) {
-    const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&b);
-  } else {
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&h);
-  }
-}
-
-// Four int8 codes of a word as two fp16 pairs, exactly: the byte n + 128 under
-// 0x64 is the fp16 number 1024 + n + 128.
-__device__ __forceinline__ void int8_to_half(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  w ^= 0x80808080u;
-  lo = __byte_perm(w, 0x64646464u, 0x4140);
-  hi = __byte_perm(w, 0x64646464u, 0x4342);
-  const __half2 bias = __floats2half2_rn(1152.0f, 1152.0f);
-  __half2 a = __hsub2(*reinterpret_cast<__half2*>(&lo), bias);
-  __half2 b = __hsub2(*reinterpret_cast<__half2*>(&hi), bias);
-  lo = *reinterpret_cast<uint32_t*>(&a);
-  hi = *reinterpret_cast<uint32_t*>(&b);
-}
-
-__device__ __forceinline__ uint32_t e4m3x2_to_half2(uint32_t two) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(two)));
-  return r;
-}
-
-__device__ __forceinline__ void ld16(uint32_t* w, const uint8_t* p) {
-  asm volatile("ld.global.L1::no_allocate.L2::128B.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "l"(p));
-}
-__device__ __forceinline__ void ld8(uint32_t* w, const uint8_t* p) {
-  asm volatile("ld.global.L1::no_allocate.L2::128B.v2.u32 {%0,%1}, [%2];"
-               : "=r"(w[0]), "=r"(w[1]) : "l"(p));
-}
-// 16 channels of 8 bits at channel ch of a D-channel row: rows of the cache
-// start on 8 bytes at least, on 16 when D % 16 == 0 (wide).
-__device__ __forceinline__ void ld16_q8(uint32_t* w, const uint8_t* row, int ch, int D, bool wide) {
-  if (wide) {
-    if (ch < D) ld16(w, row + ch);
-  } else {
-    if (ch < D) ld8(w, row + ch);
-    if (ch + 8 < D) ld8(w + 2, row + ch + 8);
-  }
 }
 
 template <int kKind, bool kQBF16, int kDp, int kNr>
@@ -249,7 +177,7 @@ paged_few_kernel(const PagedAttnParams p) {
       const int row0 = tile * kRows;
       const int p_lo = len - n + row0 / p.group;
       const int p_hi = len - n + (min(row0 + kRows, rows) - 1) / p.group;
-      const Span sp = span_of(len - n, len - 1, p.window, p.sinks);
+      const Span sp = span_of<16>(len - n, len - 1, p.window, p.sinks);
       const int sinks = p.window > 0 ? p.sinks : 0;
       const int lo = p.window > 0 ? max(0, p_lo - p.window + 1) : 0;        // first key of row0
       const int lo_hi = p.window > 0 ? max(0, p_hi - p.window + 1) : 0;     // of the last row

@@ -1,0 +1,967 @@
+// Attention of many new tokens per sequence (a prompt's chunks) over the paged
+// cache on the tensor cores (tcgen05): bound by the products.
+//
+//   S = Q K^T (128 rows x 128 keys, fp32);  x = S c;  P = 2^(x - m_ref);
+//   O += P V;  l += sum P;  out = O / l
+//
+// The rows of one (sequence, kv head) are its new tokens times the query heads
+// of the group, token by token, so that heads which share keys share a tile.
+// A CTA works on a pair of 128-row tiles that share every K and V tile:
+//   warps 0-3, 4-7  softmax of tile 0 and 1: thread = row = TMEM lane
+//   warp 8          issues the MMAs (one thread)
+//   warp 9          copies K and V tiles from the pages (16-bit cache): one
+//                   tensor copy per page and 64 channels, each by its own lane
+//   warps 12-15     8-bit cache only: read K and V codes, widen them to fp16
+//                   (exactly) and store them where the copies would put them
+// TMEM (512 columns): S0 | S1 | O0 | O1, and P_t in the first half of S_t, as
+// the A operand of O_t += P_t V: shared memory then carries Q, K and V alone.
+// (With P in shared memory as well, the operands' reads and writes of a key
+// step come to 3000 cycles of its bandwidth against 2048 of the tensor pipe.)
+// K is the B operand with channels contiguous, V the B operand with its rows
+// contiguous (MN-major), so both tiles are used as they lie in the pages.
+//
+// Order of the MMAs:  QK_0(0) QK_1(0) | PV_0(j) QK_0(j+1) PV_1(j) QK_1(j+1) ...
+// While one tile's softmax runs, the other tile's products do.  QK_t(j+1)
+// overwrites P_t(j) behind PV_t(j) that reads it: one thread issues both, and
+// the pipe executes them in that order.  A commit covers everything issued
+// before it, so S_t(j+1) ready also means that PV_t(j) is done, and a softmax
+// warp may rescale O_t itself, with nobody else at it.  It does so only when
+// the row's maximum has grown by more than 2^8 since m_ref was taken (any m_ref
+// gives the same result; P then stays below 2^8 and keeps its relative
+// precision), which after the first tiles is hardly ever.
+//
+// Work is cut into units of (pair of tiles, kv head, 128 keys), dealt evenly to
+// one CTA per SM as one contiguous range each, derived from the lengths on the
+// device; pairs that span CTAs leave fp32 parts (m, l, O) in the workspace for a
+// second kernel, which joins them in order.  Key tiles that no row sees (before
+// the window, behind the sinks) are never visited.  Values of keys that no row
+// of the pair sees are zeroed in shared memory (0 times NaN would be NaN).
+
+#include <atomic>
+
+#include "sage_kernels.h"
+#include "sage_paged_device.cuh"
+
+namespace sage {
+namespace {
+
+constexpr int kPairRows = 256, kTileRows = 128, kKeys = 128;
+constexpr int kMaxManyCtas = 152;
+constexpr uint32_t kTmemCols = 512;
+constexpr unsigned kAll = 0xFFFFFFFFu;
+constexpr float kLazy = 8.0f;             // log2 of the growth that rescales O
+
+struct ManyHead {
+  int32_t used, seq, head, pair, last, pad[59];
+};
+constexpr size_t kManyPartBytes = sizeof(ManyHead) + 2 * kPairRows * 4 + kPairRows * 128 * 4;
+static_assert(sizeof(ManyHead) == 256, "parts stay 256-byte aligned");
+
+__device__ __forceinline__ uint8_t* many_part(uint8_t* parts, int cta, int which) {
+  return parts + (static_cast<size_t>(cta) * 2 + which) * kManyPartBytes;
+}
+
+template <int kKind, int kDp>
+struct Many {
+  static constexpr bool kQ8 = kKind == kKindQ8;
+  static constexpr int kThreads = kQ8 ? 512 : 384;
+  static constexpr int kPanel = kTileRows * 128;               // 128 rows x 64 channels
+  static constexpr int kTileBytes = kDp / 64 * kPanel;         // Q, K or V tile of 16 bits
+  static constexpr int kStages = kQ8 ? (kDp == 128 ? 4 : 8) : (kDp == 128 ? 5 : 10);
+  static constexpr int kScaleRing = 8;                         // key scales of 8 tiles
+  static constexpr int kRingOff = 2 * kTileBytes;
+  static constexpr int kScaleOff = kRingOff + kStages * kTileBytes;
+  static constexpr int kBarOff = kScaleOff + (kQ8 ? kScaleRing * kKeys * 4 : 0);
+  // full[stages], empty[stages], q_ready[2], s_full[2], p_ready[2], o_full[2], drain
+  static constexpr int kNumBars = 2 * kStages + 9;
+  static constexpr int kMiscOff = (kBarOff + kNumBars * 8 + 15) / 16 * 16;
+  static constexpr int kBytes = kMiscOff + 256;
+  static constexpr int kAlloc = kBytes + 1024;
+  static_assert(kAlloc <= 227 * 1024, "shared memory of one CTA");
+};
+
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};"
+      :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+
+// D (+)= A[tmem] B[smem]: A is 128 rows of 16-bit pairs, one pair a column.
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t b_hi,
+                                       uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .b64 bd;\n\t.reg .pred p;\n\t"
+      "mov.b64 bd, {%2, %3};\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], bd, %4, p;\n}"
+      :: "r"(d), "r"(a), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, int x, int y, int z,
+                                            int w, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];"
+      :: "r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w),
+         "r"(smem_u32(bar))
+      : "memory");
+}
+
+// The part of a (sequence, kv head, pair) that a CTA works on.
+struct Item {
+  int s, head, pair;
+  int start, n, len, rows;
+  int p_lo, p_hi;            // positions of the pair's first and last row
+  int lo;                    // first key of the window of the first row
+  int first, count, per;     // key tiles: from, how many, of how many
+  Span span;
+  __device__ __forceinline__ int key0(int i) const {     // first key of the i-th tile
+    const int v = first + i;
+    return kKeys * (v < span.sink ? v : v - span.sink + span.from);
+  }
+};
+
+__device__ __forceinline__ bool served(const PagedAttnParams& p, int s, int* start, int* n,
+                                       int* len, int* rows) {
+  if (!paged_seq(p.c, s, start, n, len)) return false;
+  *rows = *n * p.group;
+  return *rows > 0 && *rows >= p.min_rows && *rows <= p.max_rows;
+}
+
+__device__ __forceinline__ Span pair_span(const PagedAttnParams& p, int base, int rows, int pair,
+                                          int* p_lo, int* p_hi) {
+  *p_lo = base + pair * kPairRows / p.group;
+  *p_hi = base + (min((pair + 1) * kPairRows, rows) - 1) / p.group;
+  Span r = span_of<kKeys>(*p_lo, *p_hi, p.window, p.sinks);
+  r.count = max(1, r.count);             // a pair that sees nothing still writes its zeros
+  return r;
+}
+
+// Walks a CTA's range of units, item by item; every role walks on its own.
+struct Walk {
+  int s, pair, head, unit;
+  int64_t left;
+  __device__ __forceinline__ bool next(const PagedAttnParams& p, Item* it) {
+    while (left > 0 && s < p.c.nseq) {
+      if (!served(p, s, &it->start, &it->n, &it->len, &it->rows) ||
+          pair * kPairRows >= it->rows) {
+        ++s;
+        pair = head = unit = 0;
+        continue;
+      }
+      it->span = pair_span(p, it->len - it->n, it->rows, pair, &it->p_lo, &it->p_hi);
+      it->s = s;
+      it->head = head;
+      it->pair = pair;
+      it->per = it->span.count;
+      it->first = unit;
+      it->count = static_cast<int>(min(static_cast<int64_t>(it->per - unit), left));
+      it->lo = p.window > 0 ? max(0, it->p_lo - p.window + 1) : 0;
+      left -= it->count;
+      unit = 0;
+      if (++head == p.c.Hkv) {
+        head = 0;
+        ++pair;
+      }
+      return true;
+    }
+    return false;
+  }
+};
+
+// Inclusive sum over the block's threads; ends with a barrier.
+template <int kThreads>
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* warp_sums, int64_t* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {
+    const int64_t o = __shfl_up_sync(kAll, v, d);
+    if (lane >= d) v += o;
+  }
+  if (lane == 31) warp_sums[warp] = v;
+  __syncthreads();
+  int64_t all = 0, before = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    const int64_t x = warp_sums[w];
+    if (w < warp) before += x;
+    all += x;
+  }
+  __syncthreads();
+  *total = all;
+  return v + before;
+}
+
+__device__ __forceinline__ uint32_t below(int x) {       // the x lowest bits
+  return x <= 0 ? 0u : x >= 32 ? 0xFFFFFFFFu : (1u << x) - 1u;
+}
+
+template <int kKind, bool kQBF16, int kDp>
+__global__ void __launch_bounds__(kKind == kKindQ8 ? 512 : 384, 1)
+paged_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                  const PagedAttnParams p) {
+  using L = Many<kKind, kDp>;
+  constexpr bool kQ8 = L::kQ8;
+  constexpr bool kMmaBF16 = kKind == kKindBF16;
+  constexpr int kStages = L::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = align1024(smem_raw);
+  const PagedGeo& c = p.c;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int cta = blockIdx.x, ctas = gridDim.x;
+  asm volatile("griddepcontrol.launch_dependents;");
+
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
+  uint64_t* empty = full + kStages;
+  uint64_t* q_ready = empty + kStages;
+  uint64_t* s_full = q_ready + 2;
+  uint64_t* p_ready = s_full + 2;
+  uint64_t* o_full = p_ready + 2;
+  uint64_t* drain = o_full + 2;
+  int* scan_s = reinterpret_cast<int*>(smem);     // the plan's; the queries come there later
+  int64_t* sums_s = reinterpret_cast<int64_t*>(smem + L::kMiscOff);        // 16
+  Walk* walk_s = reinterpret_cast<Walk*>(smem + L::kMiscOff + 128);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMiscOff + 192);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMiscOff + 196);
+
+  if (tid == 0) {
+    *abort_flag = 0;
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&full[i], kQ8 ? 128 : 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&q_ready[t], kTileRows);
+      mbar_init(&s_full[t], 1);
+      mbar_init(&p_ready[t], kTileRows);
+      mbar_init(&o_full[t], 1);
+    }
+    mbar_init(drain, 1);
+    mbar_fence_init();
+  }
+  if (warp == 8) tmem_alloc(tmem_slot, kTmemCols);
+
+  // ---- this CTA's range of units: pairs per sequence, then tiles per pair
+  Walk walk{0, 0, 0, 0, 0};
+  bool used[2] = {false, false};
+  {
+    constexpr int T = L::kThreads;
+    const int spt = (c.nseq + T - 1) / T;
+    const int sb = min(c.nseq, tid * spt), se = min(c.nseq, sb + spt);
+    int64_t pairs = 0, all_pairs = 0, all = 0;
+    for (int s = sb; s < se; ++s) {
+      int a, n, len, rows;
+      if (served(p, s, &a, &n, &len, &rows)) pairs += (rows + kPairRows - 1) / kPairRows;
+    }
+    const int64_t pair_end = block_scan<T>(pairs, sums_s, &all_pairs);
+    scan_s[tid] = static_cast<int>(pair_end);
+    __syncthreads();
+    const int64_t ppt = (all_pairs + T - 1) / T;
+    const int64_t pb = min(all_pairs, tid * ppt), pe = min(all_pairs, pb + ppt);
+    // the pair pb: its thread's chunk of sequences by bisection, then a walk
+    int s0 = 0, p0 = 0;
+    if (pb < pe) {
+      int lo = 0, hi = T - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi) / 2;
+        if (scan_s[mid] > pb) hi = mid;
+        else lo = mid + 1;
+      }
+      int64_t rest = pb - (lo > 0 ? scan_s[lo - 1] : 0);
+      for (s0 = lo * spt; s0 < c.nseq; ++s0) {
+        int a, n, len, rows;
+        if (!served(p, s0, &a, &n, &len, &rows)) continue;
+        const int np = (rows + kPairRows - 1) / kPairRows;
+        if (rest < np) break;
+        rest -= np;
+      }
+      p0 = static_cast<int>(rest);
+    }
+    // visits this thread's pairs; f(s, pair, tiles) returns true to stop
+    auto visit = [&](auto f) {
+      int s = s0, pair = p0;
+      for (int64_t i = pb; i < pe; ++s, pair = 0) {
+        int a, n, len, rows;
+        if (s >= c.nseq) return;
+        if (!served(p, s, &a, &n, &len, &rows)) continue;
+        for (; i < pe && pair * kPairRows < rows; ++i, ++pair) {
+          int plo, phi;
+          if (f(s, pair, pair_span(p, len - n, rows, pair, &plo, &phi).count)) return;
+        }
+      }
+    };
+    int64_t mine = 0;
+    visit([&](int, int, int tiles) { mine += tiles; return false; });
+    mine *= c.Hkv;
+    const int64_t end = block_scan<T>(mine, sums_s, &all), begin = end - mine;
+    const int64_t busy = min(all, static_cast<int64_t>(ctas));
+    const int64_t u0 = cta < busy ? all * cta / busy : 0;
+    const int64_t u1 = cta < busy ? all * (cta + 1) / busy : 0;
+    if (u0 < u1 && begin <= u0 && u0 < end) {             // one thread
+      int64_t off = u0 - begin;
+      visit([&](int s, int pair, int tiles) {
+        const int64_t w = static_cast<int64_t>(tiles) * c.Hkv;
+        if (off >= w) {
+          off -= w;
+          return false;
+        }
+        *walk_s = Walk{s, pair, static_cast<int>(off / tiles), static_cast<int>(off % tiles),
+                       u1 - u0};
+        return true;
+      });
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (u0 < u1) walk = *walk_s;
+  }
+  const uint32_t tbase = *tmem_slot;
+  const int wg = warp >> 2;
+  Item it;
+
+  if (wg == 2) {
+    if constexpr (kQ8) regs_decrease<72>();
+    else regs_decrease<80>();
+    if (warp == 9 && !kQ8) {
+      // ================================================== copies of K and V
+      const int rows_box = min(c.page_size, kKeys), boxes = kKeys / rows_box;
+      int64_t seq = 0;                          // copies issued: K and V tiles alternate
+      bool ok = true;
+      while (ok && walk.next(p, &it)) {
+        const int sinks = p.window > 0 ? p.sinks : 0;
+        for (int i = 0; ok && i < it.count; ++i) {
+          const int key0 = it.key0(i);
+          // lane b finds the page of box b
+          int page = static_cast<int>(c.num_pages), slot = 0;
+          if (lane < boxes) {
+            const int k = key0 + lane * rows_box;
+            if (k <= it.p_hi && (k + rows_box - 1 >= it.lo || k < sinks)) {
+              const int pg = paged_page(c, it.s, k / c.page_size);
+              if (pg >= 0) page = pg;           // else the copy lies outside and reads zeros
+              slot = k % c.page_size;
+            }
+          }
+#pragma unroll
+          for (int kv = 0; kv < 2; ++kv, ++seq) {
+            const int st = static_cast<int>(seq % kStages);
+            if (seq >= kStages)
+              ok = __all_sync(kAll, mbar_wait(&empty[st], (seq / kStages - 1) & 1, abort_flag,
+                                              c.status, p.timeout_ns));
+            if (!ok) break;
+            if (lane == 0) mbar_expect_tx(&full[st], L::kTileBytes);
+            __syncwarp();
+            if (lane < boxes) {
+              uint8_t* dst = smem + L::kRingOff + st * L::kTileBytes + lane * rows_box * 128;
+#pragma unroll
+              for (int a = 0; a < kDp / 64; ++a)
+                tma_load_4d(dst + a * L::kPanel, kv == 0 ? &tm_k : &tm_v, 64 * a, slot, it.head,
+                            page, &full[st]);
+            }
+          }
+        }
+      }
+      // no copy may still be in flight when the CTA exits
+      for (int64_t i = seq > kStages ? seq - kStages : 0; i < seq; ++i)
+        mbar_wait(&full[i % kStages], (i / kStages) & 1, nullptr, c.status, p.timeout_ns);
+    } else if (warp == 8) {
+      // ================================================== MMAs
+      constexpr uint32_t kFmt = kMmaBF16 ? 1u : 0u;
+      constexpr uint32_t kIdQk = make_idesc(kFmt, kFmt, kTileRows, kKeys);
+      constexpr uint32_t kIdPv = make_idesc(kFmt, kFmt, kTileRows, kDp) | (1u << 16);
+      const uint32_t q_lo = sdesc_sw128_lo(smem_u32(smem));
+      const uint32_t ring_lo = sdesc_sw128_lo(smem_u32(smem + L::kRingOff));
+      // V: rows of 64 channels contiguous (MN-major), the next 64 channels a panel
+      // further (leading offset), the next 8 keys 1024 bytes further (stride offset)
+      const uint32_t v_lo = ((smem_u32(smem + L::kRingOff) & 0x3FFFFu) >> 4) |
+                            (static_cast<uint32_t>(L::kPanel >> 4) << 16);
+      auto qk = [&](int t, int st) {
+#pragma unroll
+        for (int k = 0; k < kDp / 16; ++k) {
+          const uint32_t off = ((k / 4) * L::kPanel + (k % 4) * 32) >> 4;
+          mma_f16_ss_lo(tbase + t * 128, q_lo + ((t * L::kTileBytes) >> 4) + off,
+                        ring_lo + ((st * L::kTileBytes) >> 4) + off, kIdQk, k > 0 ? 1u : 0u);
+        }
+      };
+      auto pv = [&](int t, int st, bool add) {
+#pragma unroll
+        for (int k = 0; k < kKeys / 16; ++k)
+          mma_ts(tbase + 256 + t * kDp, tbase + t * 128 + 8 * k,
+                 v_lo + ((st * L::kTileBytes + k * 2048) >> 4), kSdescSw128Hi, kIdPv,
+                 add || k > 0 ? 1u : 0u);
+      };
+      int64_t seq = 0;                          // tiles taken from the ring
+      uint32_t items[2] = {0, 0}, steps[2] = {0, 0};
+      bool ok = true, issued = false;
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        return __all_sync(kAll, mbar_wait(bar, parity & 1, abort_flag, c.status, p.timeout_ns));
+      };
+      while (ok && walk.next(p, &it)) {
+        const bool two = it.pair * kPairRows + kTileRows < it.rows;
+        const int sinks = p.window > 0 ? p.sinks : 0;
+        for (int t = 0; ok && t < (two ? 2 : 1); ++t) ok = wait(&q_ready[t], items[t]++);
+        const int k0 = static_cast<int>(seq % kStages);
+        ok = ok && wait(&full[k0], static_cast<uint32_t>(seq / kStages));
+        if (!ok) break;
+        ++seq;
+        tc_fence_after();
+        if (lane == 0) {
+          qk(0, k0);
+          tc_commit(&s_full[0]);
+          if (two) {
+            qk(1, k0);
+            tc_commit(&s_full[1]);
+          }
+          tc_commit(&empty[k0]);
+        }
+        __syncwarp();
+        issued = true;
+        for (int i = 0; ok && i < it.count; ++i) {
+          const bool more = i + 1 < it.count;
+          const int sv = static_cast<int>(seq % kStages);
+          ok = wait(&full[sv], static_cast<uint32_t>(seq / kStages));
+          if (!ok) break;
+          ++seq;
+          if constexpr (!kQ8) {
+            const int key0 = it.key0(i);
+            if (!(key0 + kKeys - 1 <= it.p_hi && (key0 >= it.lo || key0 + kKeys - 1 < sinks))) {
+              // values of keys that no row of the pair sees
+              for (int r = lane; r < kKeys; r += 32) {
+                const int key = key0 + r;
+                if (key <= it.p_hi && (key >= it.lo || key < sinks)) continue;
+                uint4* row = reinterpret_cast<uint4*>(smem + L::kRingOff + sv * L::kTileBytes +
+                                                      r * 128);
+#pragma unroll
+                for (int a = 0; a < kDp / 64; ++a)
+#pragma unroll
+                  for (int q = 0; q < 8; ++q) row[a * (L::kPanel / 16) + q] = make_uint4(0, 0, 0, 0);
+              }
+              fence_proxy_async_smem();
+              __syncwarp();
+            }
+          }
+          int sk = 0;
+          for (int t = 0; ok && t < (two ? 2 : 1); ++t) {
+            ok = wait(&p_ready[t], steps[t]++);
+            if (!ok) break;
+            tc_fence_after();
+            if (lane == 0) pv(t, sv, i > 0);
+            const bool last_tile = t == (two ? 1 : 0);
+            if (lane == 0 && last_tile) tc_commit(&empty[sv]);
+            __syncwarp();
+            if (more) {
+              if (t == 0) {
+                sk = static_cast<int>(seq % kStages);
+                ok = wait(&full[sk], static_cast<uint32_t>(seq / kStages));
+                if (!ok) break;
+                ++seq;
+                tc_fence_after();
+              }
+              if (lane == 0) {
+                qk(t, sk);
+                tc_commit(&s_full[t]);
+                if (last_tile) tc_commit(&empty[sk]);
+              }
+            } else if (lane == 0) {
+              tc_commit(&o_full[t]);
+            }
+            __syncwarp();
+          }
+        }
+      }
+      if (issued) {                             // every MMA ends before TMEM is released
+        if (lane == 0) tc_commit(drain);
+        __syncwarp();
+        mbar_wait(drain, 0, nullptr, c.status, p.timeout_ns);
+      }
+    }
+  } else if (wg == 3) {
+    // ==================================================== 8-bit cache: widen
+    if constexpr (kQ8) {
+      regs_decrease<88>();
+      constexpr int kRowLanes = kDp / 16;       // 16-byte vectors of a row
+      constexpr int kIter = kKeys * kRowLanes / 128;
+      const int r0 = (tid - 384) / kRowLanes, ch = (tid - 384) % kRowLanes * 16;
+      const bool wide = c.D % 16 == 0;
+      float* scales = reinterpret_cast<float*>(smem + L::kScaleOff);
+      uint32_t w[kIter][4];
+      float ks[kIter];
+      const int sinks = p.window > 0 ? p.sinks : 0;
+      // loads K (kv = 0) or V of the item's i-th tile
+      auto load = [&](const Item& x, int i, int kv) {
+        const int key0 = x.key0(i);
+#pragma unroll
+        for (int j = 0; j < kIter; ++j) {
+          const int key = key0 + r0 + j * (128 / kRowLanes);
+          w[j][0] = w[j][1] = w[j][2] = w[j][3] = 0;
+          ks[j] = 0.0f;
+          if (key <= x.p_hi && (key >= x.lo || key < sinks)) {
+            const int page = paged_page(c, x.s, key / c.page_size);
+            if (page >= 0) {
+              const int slot = key % c.page_size;
+              ld16_q8(w[j], (kv == 0 ? c.k : c.v) + page * c.page_stride + slot * c.token_stride +
+                                x.head * c.head_stride, ch, c.D, wide);
+              if (kv == 0 && ch == 0)
+                ks[j] = c.k_scale[(static_cast<int64_t>(page) * c.Hkv + x.head) * c.page_size +
+                                  slot];
+            }
+          }
+        }
+      };
+      int64_t seq = 0;
+      bool ok = true;
+      bool have = walk.next(p, &it);
+      if (have) load(it, 0, 0);
+      while (ok && have) {
+        Item nx = it;
+        bool have_next = true;
+        for (int i = 0; ok && i < it.count; ++i) {
+#pragma unroll
+          for (int kv = 0; kv < 2; ++kv, ++seq) {
+            const int st = static_cast<int>(seq % kStages);
+            if (seq >= kStages)
+              ok = mbar_wait(&empty[st], (seq / kStages - 1) & 1, abort_flag, c.status,
+                             p.timeout_ns);
+            ok = __all_sync(kAll, ok);
+            if (!ok) break;
+            uint8_t* tile = smem + L::kRingOff + st * L::kTileBytes + (ch / 64) * L::kPanel;
+#pragma unroll
+            for (int j = 0; j < kIter; ++j) {
+              const int r = r0 + j * (128 / kRowLanes);
+              uint32_t h[8];
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                if (kv == 0) {
+                  int8_to_half(w[j][q], h[2 * q], h[2 * q + 1]);
+                } else {
+                  h[2 * q] = e4m3x2_to_half2(w[j][q]);
+                  h[2 * q + 1] = e4m3x2_to_half2(w[j][q] >> 16);
+                }
+              }
+              const int q0 = (ch % 64) / 8;
+              uint4* row = reinterpret_cast<uint4*>(tile + r * 128);
+              row[q0 ^ (r & 7)] = make_uint4(h[0], h[1], h[2], h[3]);
+              row[(q0 + 1) ^ (r & 7)] = make_uint4(h[4], h[5], h[6], h[7]);
+              if (kv == 0 && ch == 0) scales[(seq / 2) % L::kScaleRing * kKeys + r] = ks[j];
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(&full[st]);
+            // the next tile's loads run while the barriers turn
+            if (kv == 0) load(it, i, 1);
+            else if (i + 1 < it.count) load(it, i + 1, 0);
+            else if ((have_next = walk.next(p, &nx))) load(nx, 0, 0);
+          }
+        }
+        it = nx;
+        have = have_next;
+      }
+    }
+  } else {
+    // ==================================================== softmax of tile wg
+    if constexpr (kQ8) regs_increase<176>();
+    else regs_increase<208>();
+    const int t = wg, r = tid - t * kTileRows;
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t ts = tbase + lane_off + t * 128, to = tbase + lane_off + 256 + t * kDp;
+    uint32_t items = 0, steps = 0;
+    int64_t tiles_seen = 0;                     // of the pair: the scale ring's index
+    bool ok = true;
+    while (ok && walk.next(p, &it)) {
+      const int row0 = it.pair * kPairRows + t * kTileRows;
+      if (row0 >= it.rows) {
+        tiles_seen += it.count;
+        continue;
+      }
+      const int base = it.len - it.n;
+      const int rr = row0 + r;
+      const bool has = rr < it.rows;
+      const int tok = rr / p.group, hq = it.head * p.group + rr % p.group;
+      const int pos = has ? base + tok : -1;
+      const int t_lo = base + row0 / p.group;
+      const int t_hi = base + (min(row0 + kTileRows, it.rows) - 1) / p.group;
+      const int sinks = p.window > 0 ? p.sinks : 0;
+      float sc = p.scale_log2;
+      {
+        // ---- this row's query into shared memory, swizzled as a copy would
+        const uint16_t* q = p.q + (static_cast<int64_t>(it.start) + tok) * p.q_tok +
+                            static_cast<int64_t>(hq) * p.q_head;
+        uint8_t* dst = smem + t * L::kTileBytes + r * 128;
+        auto vec = [&](int i) {
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (has && 8 * i < c.D) {
+            if (p.q_vec) {
+              v = *reinterpret_cast<const uint4*>(q + 8 * i);
+            } else {
+              uint32_t x[4] = {0, 0, 0, 0};
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                x[e / 2] |= static_cast<uint32_t>(q[8 * i + e]) << (16 * (e & 1));
+              v = make_uint4(x[0], x[1], x[2], x[3]);
+            }
+          }
+          return v;
+        };
+        uint4 v[kDp / 8];
+#pragma unroll
+        for (int i = 0; i < kDp / 8; ++i) v[i] = vec(i);
+        if constexpr (kQ8 && kQBF16) {
+          // bf16 queries into fp16's range: times 2^-e, e the exponent of the largest
+          float top = 0.0f;
+#pragma unroll
+          for (int i = 0; i < kDp / 8; ++i) {
+            const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              top = fmaxf(top, fabsf(__uint_as_float(x[e] << 16)));
+              top = fmaxf(top, fabsf(__uint_as_float(x[e] & 0xFFFF0000u)));
+            }
+          }
+          const int ex = top > 0.0f ? ilogbf(top) : 0;
+          auto half = [&](uint32_t x) {
+            return pack2<false>(ldexpf(__uint_as_float(x << 16), -ex),
+                                ldexpf(__uint_as_float(x & 0xFFFF0000u), -ex));
+          };
+#pragma unroll
+          for (int i = 0; i < kDp / 8; ++i)
+            v[i] = make_uint4(half(v[i].x), half(v[i].y), half(v[i].z), half(v[i].w));
+          sc = ldexpf(sc, ex);
+        }
+#pragma unroll
+        for (int i = 0; i < kDp / 8; ++i)
+          *reinterpret_cast<uint4*>(dst + (i / 8) * L::kPanel + (((i % 8) ^ (r & 7)) << 4)) = v[i];
+        fence_proxy_async_smem();
+        tc_fence_before();                      // the previous item's O has been read
+        mbar_arrive(&q_ready[t]);
+      }
+      float ref = -INFINITY, l = 0.0f;
+      for (int i = 0; i < it.count; ++i) {
+        ok = __all_sync(kAll, mbar_wait(&s_full[t], steps++ & 1, abort_flag, c.status,
+                                        p.timeout_ns));
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t sr[4][32];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) tmem_ld32(ts + 32 * q, sr[q]);
+        tmem_ld_wait();
+#pragma unroll
+        for (int q = 0; q < 4; ++q) reg_fence(sr[q]);
+        if constexpr (kQ8) {
+          const float4* ks = reinterpret_cast<const float4*>(
+              smem + L::kScaleOff + (tiles_seen % L::kScaleRing) * kKeys * 4);
+#pragma unroll
+          for (int q = 0; q < 32; ++q) {
+            const float4 k4 = ks[q];
+            uint32_t* x = &sr[q / 8][(q % 8) * 4];
+            const float2 a = __fmul2_rn(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])),
+                                        make_float2(k4.x, k4.y));
+            const float2 b = __fmul2_rn(make_float2(__uint_as_float(x[2]), __uint_as_float(x[3])),
+                                        make_float2(k4.z, k4.w));
+            x[0] = __float_as_uint(a.x);
+            x[1] = __float_as_uint(a.y);
+            x[2] = __float_as_uint(b.x);
+            x[3] = __float_as_uint(b.y);
+          }
+        }
+        ++tiles_seen;
+        const int key0 = it.key0(i);
+        if (!(key0 + kKeys - 1 <= t_lo &&
+              (p.window <= 0 || key0 >= t_hi - p.window + 1 || key0 + kKeys - 1 < sinks))) {
+          const int hi = pos + 1 - key0;                            // keys below: not later
+          const int lo = p.window > 0 ? pos - p.window + 1 - key0 : 0;   // keys below: too early
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const uint32_t early = below(lo - 32 * q) & ~below(sinks - key0 - 32 * q);
+            const uint32_t see = below(hi - 32 * q) & ~early;
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!((see >> e) & 1u)) sr[q][e] = 0xFF800000u;       // -inf
+          }
+        }
+        float mx[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          mx[q] = __uint_as_float(sr[q][0]);
+#pragma unroll
+          for (int e = 1; e < 32; ++e) mx[q] = fmaxf(mx[q], __uint_as_float(sr[q][e]));
+        }
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
+        const bool grew = top > ref + kLazy || (ref == -INFINITY && top > -INFINITY);
+        if (__any_sync(kAll, grew)) {
+          const float next = grew ? top : ref;
+          const float alpha = grew ? fast_exp2(ref - next) : 1.0f;  // 0 from -inf
+          if (i > 0) {
+#pragma unroll
+            for (int q = 0; q < kDp / 16; ++q) {
+              uint32_t o[16];
+              tmem_ld16(to + 16 * q, o);
+              tmem_ld_wait();
+              reg_fence(o);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+              tmem_st16(to + 16 * q, o);
+            }
+          }
+          l *= alpha;
+          ref = next;
+        }
+        const float safe = ref == -INFINITY ? 0.0f : ref;
+        const float2 sc2 = make_float2(sc, sc), nm2 = make_float2(-safe, -safe);
+        float2 a01 = make_float2(0.0f, 0.0f), a23 = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t w[32];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const uint32_t* x = &sr[2 * h + e / 8][(e % 8) * 4];
+            const float2 d01 = __ffma2_rn(
+                make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])), sc2, nm2);
+            const float2 d23 = __ffma2_rn(
+                make_float2(__uint_as_float(x[2]), __uint_as_float(x[3])), sc2, nm2);
+            const float2 p01 = make_float2(fast_exp2(d01.x), fast_exp2(d01.y));
+            const float2 p23 = make_float2(fast_exp2(d23.x), fast_exp2(d23.y));
+            w[2 * e] = pack2<kMmaBF16>(p01.x, p01.y);
+            w[2 * e + 1] = pack2<kMmaBF16>(p23.x, p23.y);
+            a01 = __fadd2_rn(a01, p01);
+            a23 = __fadd2_rn(a23, p23);
+          }
+          tmem_st32(ts + 32 * h, w);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(&p_ready[t]);
+        l += (a01.x + a01.y) + (a23.x + a23.y);
+      }
+      if (!ok) break;
+      // ---- out = O / l, or a part
+      ok = __all_sync(kAll, mbar_wait(&o_full[t], items++ & 1, abort_flag, c.status,
+                                      p.timeout_ns));
+      if (!ok) break;
+      tc_fence_after();
+      const bool whole = it.first == 0 && it.count == it.per;
+      if (whole) {
+        const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+        const int64_t orow = (static_cast<int64_t>(it.start) + tok) * p.Hq + hq;
+        const float* sv = c.v_scale + it.head * kDp;
+#pragma unroll
+        for (int q = 0; q < kDp / 32; ++q) {
+          uint32_t o[32];
+          tmem_ld32(to + 32 * q, o);
+          tmem_ld_wait();
+          reg_fence(o);
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            const int ch = 32 * q + 8 * v;
+            if (has && ch < c.D) {
+              uint32_t w[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                float a = __uint_as_float(o[8 * v + 2 * e]) * inv;
+                float b = __uint_as_float(o[8 * v + 2 * e + 1]) * inv;
+                if constexpr (kQ8) {
+                  a *= sv[ch + 2 * e];
+                  b *= sv[ch + 2 * e + 1];
+                }
+                w[e] = pack2<kQBF16>(a, b);
+              }
+              *reinterpret_cast<uint4*>(p.out + orow * c.D + ch) =
+                  make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+        }
+        if (has && p.lse != nullptr)
+          p.lse[orow] = l > 0.0f ? (ref + log2f(l)) * 0.69314718055994530942f : -INFINITY;
+      } else {
+        const int which = it.first == 0 ? 1 : 0;
+        uint8_t* part = many_part(p.parts, cta, which);
+        used[which] = true;
+        if (t == 0 && r == 0) {
+          ManyHead* h = reinterpret_cast<ManyHead*>(part);
+          h->used = 1;
+          h->seq = it.s;
+          h->head = it.head;
+          h->pair = it.pair;
+          h->last = it.first + it.count == it.per;
+        }
+        const int row = t * kTileRows + r;
+        float* ml = reinterpret_cast<float*>(part + sizeof(ManyHead));
+        ml[row] = ref;
+        ml[kPairRows + row] = l;
+        float4* po = reinterpret_cast<float4*>(ml + 2 * kPairRows);
+#pragma unroll
+        for (int q = 0; q < kDp / 32; ++q) {
+          uint32_t o[32];
+          tmem_ld32(to + 32 * q, o);
+          tmem_ld_wait();
+          reg_fence(o);
+#pragma unroll
+          for (int v = 0; v < 8; ++v)
+            po[(8 * q + v) * kPairRows + row] =
+                make_float4(__uint_as_float(o[4 * v]), __uint_as_float(o[4 * v + 1]),
+                            __uint_as_float(o[4 * v + 2]), __uint_as_float(o[4 * v + 3]));
+        }
+      }
+    }
+    if (tid == 0) {
+#pragma unroll
+      for (int w = 0; w < 2; ++w)
+        if (!used[w]) reinterpret_cast<ManyHead*>(many_part(p.parts, cta, w))->used = 0;
+    }
+  }
+
+  // ---- teardown: all roles have drained; release tensor memory
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tbase, kTmemCols);
+  }
+}
+
+// Joins 32 rows of the pair that begins in CTA blockIdx.x and ends in a later
+// one: weights 2^(m_i - max), summed in the parts' order.
+template <bool kQBF16, int kDp>
+__global__ void __launch_bounds__(256)
+paged_many_join_kernel(const PagedAttnParams p, int ctas) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int c0 = blockIdx.x;
+  const int row = blockIdx.y * 32 + (threadIdx.x & 31), grp = threadIdx.x >> 5;
+  const ManyHead* h = reinterpret_cast<const ManyHead*>(many_part(p.parts, c0, 1));
+  if (!h->used) return;
+  int start, n, len;
+  if (!paged_seq(p.c, h->seq, &start, &n, &len)) return;
+  const int rows = n * p.group, rr = h->pair * kPairRows + row;
+  if (rr >= rows) return;
+  int parts = 1;
+  while (c0 + parts < ctas) {
+    const ManyHead* q = reinterpret_cast<const ManyHead*>(many_part(p.parts, c0 + parts, 0));
+    if (!q->used) break;
+    ++parts;
+    if (q->last) break;
+  }
+  auto ml = [&](int i) {
+    return reinterpret_cast<const float*>(many_part(p.parts, c0 + i, i == 0) + sizeof(ManyHead));
+  };
+  float top = -INFINITY;
+  for (int i = 0; i < parts; ++i) top = fmaxf(top, ml(i)[row]);
+  const float safe = top == -INFINITY ? 0.0f : top;
+  constexpr int kVec = kDp / 32;                 // float4s of a thread
+  float sum = 0.0f;
+  float4 acc[kVec];
+#pragma unroll
+  for (int v = 0; v < kVec; ++v) acc[v] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  for (int i = 0; i < parts; ++i) {
+    const float* f = ml(i);
+    const float w = fast_exp2(f[row] - safe);
+    sum += w * f[kPairRows + row];
+    const float4* po = reinterpret_cast<const float4*>(f + 2 * kPairRows);
+#pragma unroll
+    for (int v = 0; v < kVec; ++v) {
+      const float4 o = po[(grp + 8 * v) * kPairRows + row];
+      acc[v].x += w * o.x; acc[v].y += w * o.y; acc[v].z += w * o.z; acc[v].w += w * o.w;
+    }
+  }
+  const int64_t tok = static_cast<int64_t>(start) + rr / p.group;
+  const int hq = h->head * p.group + rr % p.group;
+  const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+#pragma unroll
+  for (int v = 0; v < kVec; ++v) {
+    const int ch = 4 * (grp + 8 * v);
+    if (ch >= p.c.D) continue;
+    float4 a = acc[v];
+    a.x *= inv; a.y *= inv; a.z *= inv; a.w *= inv;
+    if (p.c.kind == kKindQ8) {
+      const float4 s = *reinterpret_cast<const float4*>(p.c.v_scale + h->head * kDp + ch);
+      a.x *= s.x; a.y *= s.y; a.z *= s.z; a.w *= s.w;
+    }
+    *reinterpret_cast<uint2*>(p.out + (tok * p.Hq + hq) * p.c.D + ch) =
+        make_uint2(pack2<kQBF16>(a.x, a.y), pack2<kQBF16>(a.z, a.w));
+  }
+  if (p.lse != nullptr && grp == 0)
+    p.lse[tok * p.Hq + hq] = sum > 0.0f ? (top + log2f(sum)) * 0.69314718055994530942f
+                                        : -INFINITY;
+}
+
+template <int kKind, bool kQBF16, int kDp>
+cudaError_t launch_many(const PagedAttnParams& p, int sms, cudaStream_t st) {
+  using L = Many<kKind, kDp>;
+  auto* kern = paged_many_kernel<kKind, kQBF16, kDp>;
+  static std::atomic<bool> configured[64] = {};   // a kernel attribute, per device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!configured[dev].load(std::memory_order_relaxed)) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
+    if (e != cudaSuccess) return e;
+    configured[dev].store(true, std::memory_order_relaxed);
+  }
+  CUtensorMap mk{}, mv{};
+  if constexpr (kKind != kKindQ8) {
+    const PagedGeo& c = p.c;
+    const uint64_t dims[4] = {static_cast<uint64_t>(c.D), static_cast<uint64_t>(c.page_size),
+                              static_cast<uint64_t>(c.Hkv), static_cast<uint64_t>(c.num_pages)};
+    const uint64_t strides[3] = {static_cast<uint64_t>(c.token_stride) * 2,
+                                 static_cast<uint64_t>(c.head_stride) * 2,
+                                 static_cast<uint64_t>(c.page_stride) * 2};
+    const uint32_t box[4] = {64, static_cast<uint32_t>(c.page_size < kKeys ? c.page_size : kKeys),
+                             1, 1};
+    if (!encode_tiled(&mk, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, c.k, dims, strides, box,
+                      CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !encode_tiled(&mv, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, c.v, dims, strides, box,
+                      CU_TENSOR_MAP_SWIZZLE_128B))
+      return cudaErrorInvalidValue;
+  }
+  // one CTA per SM, and no more than the units of the lengths the call declares
+  const int64_t pairs = (static_cast<int64_t>(p.c.max_q) * p.group + kPairRows - 1) / kPairRows;
+  const int64_t most = pairs * p.c.nseq * p.c.Hkv *
+                       ((static_cast<int64_t>(p.c.max_kv) + kKeys - 1) / kKeys + 1);
+  int ctas = sms < kMaxManyCtas ? sms : kMaxManyCtas;
+  if (most < ctas) ctas = static_cast<int>(most);
+  kern<<<ctas, L::kThreads, L::kAlloc, st>>>(mk, mv, p);
+  note_launch();
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas), kPairRows / 32);
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, paged_many_join_kernel<kQBF16, kDp>, p, ctas);
+  note_launch();
+  return e;
+}
+
+template <int kKind, bool kQBF16>
+cudaError_t launch_many_dim(const PagedAttnParams& p, int sms, cudaStream_t st) {
+  return p.c.Dp == 64 ? launch_many<kKind, kQBF16, 64>(p, sms, st)
+                      : launch_many<kKind, kQBF16, 128>(p, sms, st);
+}
+
+}  // namespace
+
+size_t paged_many_bytes() { return 2 * static_cast<size_t>(kMaxManyCtas) * kManyPartBytes; }
+
+// 16-bit pages are copied as boxes of whole pages or 128 slots, by tensor maps
+// whose strides are below 2^40 bytes; the 8-bit cache is read element-wise.
+bool paged_many_serves(const PagedGeo& c) {
+  if (c.kind == kKindQ8) return true;
+  if (c.page_size < kKeys ? kKeys % c.page_size != 0 : c.page_size % kKeys != 0) return false;
+  return c.page_stride < (int64_t(1) << 39) && c.token_stride < (int64_t(1) << 39) &&
+         c.head_stride < (int64_t(1) << 39);
+}
+
+cudaError_t launch_paged_many(const PagedAttnParams& p, bool bf16, int sms, cudaStream_t st) {
+  if (p.c.kind == kKindQ8)
+    return bf16 ? launch_many_dim<kKindQ8, true>(p, sms, st)
+                : launch_many_dim<kKindQ8, false>(p, sms, st);
+  return bf16 ? launch_many_dim<kKindBF16, true>(p, sms, st)
+              : launch_many_dim<kKindF16, false>(p, sms, st);
+}
+
+}  // namespace sage

@@ -68,6 +68,9 @@ struct PagedAttnParams {
 
 cudaError_t launch_paged_few(const PagedAttnParams& p, bool bf16, int sms, cudaStream_t st);
 size_t paged_few_bytes();
+cudaError_t launch_paged_many(const PagedAttnParams& p, bool bf16, int sms, cudaStream_t st);
+size_t paged_many_bytes();
+bool paged_many_serves(const PagedGeo& c);
 
 #ifdef __CUDACC__
 // A sequence's first row, new tokens and cached length; false (and the status
