@@ -49,6 +49,9 @@ constexpr int kPairRows = 256, kTileRows = 128, kKeys = 128;
 constexpr int kMaxManyCtas = 152;
 constexpr uint32_t kTmemCols = 512;
 constexpr unsigned kAll = 0xFFFFFFFFu;
+// Units that an item costs besides its key tiles: filling and draining the
+// pipeline takes about as long as this many tiles.
+constexpr int kItemUnits = 2;
 constexpr float kLazy = 8.0f;             // log2 of the growth that rescales O
 
 struct ManyHead {
@@ -116,6 +119,7 @@ struct Item {
   int p_lo, p_hi;            // positions of the pair's first and last row
   int lo;                    // first key of the window of the first row
   int first, count, per;     // key tiles: from, how many, of how many
+  int64_t before;            // key tiles of the CTA's earlier items
   Span span;
   __device__ __forceinline__ int key0(int i) const {     // first key of the i-th tile
     const int v = first + i;
@@ -139,10 +143,12 @@ __device__ __forceinline__ Span pair_span(const PagedAttnParams& p, int base, in
   return r;
 }
 
-// Walks a CTA's range of units, item by item; every role walks on its own.
+// Walks a CTA's range of units, item by item; every role walks on its own.  An
+// item takes kItemUnits + tiles units, the first ones without a tile; a CTA
+// whose range ends among those leaves the item to the next one.
 struct Walk {
   int s, pair, head, unit;
-  int64_t left;
+  int64_t left, tiles;
   __device__ __forceinline__ bool next(const PagedAttnParams& p, Item* it) {
     while (left > 0 && s < p.c.nseq) {
       if (!served(p, s, &it->start, &it->n, &it->len, &it->rows) ||
@@ -156,16 +162,21 @@ struct Walk {
       it->head = head;
       it->pair = pair;
       it->per = it->span.count;
-      it->first = unit;
-      it->count = static_cast<int>(min(static_cast<int64_t>(it->per - unit), left));
+      it->first = max(0, unit - kItemUnits);
+      const int64_t upto = unit + left - kItemUnits;      // tiles before the range's end
+      it->count = static_cast<int>(min(static_cast<int64_t>(it->per), upto)) - it->first;
       it->lo = p.window > 0 ? max(0, it->p_lo - p.window + 1) : 0;
-      left -= it->count;
+      it->before = tiles;
+      left -= it->per + kItemUnits - unit;
       unit = 0;
       if (++head == p.c.Hkv) {
         head = 0;
         ++pair;
       }
-      return true;
+      if (it->count > 0) {
+        tiles += it->count;
+        return true;
+      }
     }
     return false;
   }
@@ -244,7 +255,7 @@ paged_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
   if (warp == 8) tmem_alloc(tmem_slot, kTmemCols);
 
   // ---- this CTA's range of units: pairs per sequence, then tiles per pair
-  Walk walk{0, 0, 0, 0, 0};
+  Walk walk{0, 0, 0, 0, 0, 0};
   bool used[2] = {false, false};
   {
     constexpr int T = L::kThreads;
@@ -293,7 +304,7 @@ paged_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
       }
     };
     int64_t mine = 0;
-    visit([&](int, int, int tiles) { mine += tiles; return false; });
+    visit([&](int, int, int tiles) { mine += tiles + kItemUnits; return false; });
     mine *= c.Hkv;
     const int64_t end = block_scan<T>(mine, sums_s, &all), begin = end - mine;
     const int64_t busy = min(all, static_cast<int64_t>(ctas));
@@ -302,13 +313,13 @@ paged_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     if (u0 < u1 && begin <= u0 && u0 < end) {             // one thread
       int64_t off = u0 - begin;
       visit([&](int s, int pair, int tiles) {
-        const int64_t w = static_cast<int64_t>(tiles) * c.Hkv;
+        const int64_t per = tiles + kItemUnits, w = per * c.Hkv;
         if (off >= w) {
           off -= w;
           return false;
         }
-        *walk_s = Walk{s, pair, static_cast<int>(off / tiles), static_cast<int>(off % tiles),
-                       u1 - u0};
+        *walk_s = Walk{s, pair, static_cast<int>(off / per), static_cast<int>(off % per),
+                       u1 - u0, 0};
         return true;
       });
     }
@@ -565,26 +576,21 @@ paged_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t ts = tbase + lane_off + t * 128, to = tbase + lane_off + 256 + t * kDp;
     uint32_t items = 0, steps = 0;
-    int64_t tiles_seen = 0;                     // of the pair: the scale ring's index
     bool ok = true;
-    while (ok && walk.next(p, &it)) {
-      const int row0 = it.pair * kPairRows + t * kTileRows;
-      if (row0 >= it.rows) {
-        tiles_seen += it.count;
-        continue;
-      }
-      const int base = it.len - it.n;
-      const int rr = row0 + r;
-      const bool has = rr < it.rows;
-      const int tok = rr / p.group, hq = it.head * p.group + rr % p.group;
-      const int pos = has ? base + tok : -1;
-      const int t_lo = base + row0 / p.group;
-      const int t_hi = base + (min(row0 + kTileRows, it.rows) - 1) / p.group;
-      const int sinks = p.window > 0 ? p.sinks : 0;
-      float sc = p.scale_log2;
-      {
-        // ---- this row's query into shared memory, swizzled as a copy would
-        const uint16_t* q = p.q + (static_cast<int64_t>(it.start) + tok) * p.q_tok +
+    // the next item that has rows in this tile
+    auto advance = [&](Item* x) {
+      while (walk.next(p, x))
+        if (x->pair * kPairRows + t * kTileRows < x->rows) return true;
+      return false;
+    };
+    // This row's query into shared memory, swizzled as a copy would; returns the
+    // factor from S to base-2 logits.
+    auto load_q = [&](const Item& x) {
+        const int rr = x.pair * kPairRows + t * kTileRows + r;
+        const bool has = rr < x.rows;
+        const int tok = rr / p.group, hq = x.head * p.group + rr % p.group;
+        float sc = p.scale_log2;
+        const uint16_t* q = p.q + (static_cast<int64_t>(x.start) + tok) * p.q_tok +
                             static_cast<int64_t>(hq) * p.q_head;
         uint8_t* dst = smem + t * L::kTileBytes + r * 128;
         auto vec = [&](int i) {
@@ -593,11 +599,11 @@ paged_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             if (p.q_vec) {
               v = *reinterpret_cast<const uint4*>(q + 8 * i);
             } else {
-              uint32_t x[4] = {0, 0, 0, 0};
+              uint32_t u[4] = {0, 0, 0, 0};
 #pragma unroll
               for (int e = 0; e < 8; ++e)
-                x[e / 2] |= static_cast<uint32_t>(q[8 * i + e]) << (16 * (e & 1));
-              v = make_uint4(x[0], x[1], x[2], x[3]);
+                u[e / 2] |= static_cast<uint32_t>(q[8 * i + e]) << (16 * (e & 1));
+              v = make_uint4(u[0], u[1], u[2], u[3]);
             }
           }
           return v;
@@ -610,17 +616,17 @@ paged_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
           float top = 0.0f;
 #pragma unroll
           for (int i = 0; i < kDp / 8; ++i) {
-            const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+            const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              top = fmaxf(top, fabsf(__uint_as_float(x[e] << 16)));
-              top = fmaxf(top, fabsf(__uint_as_float(x[e] & 0xFFFF0000u)));
+              top = fmaxf(top, fabsf(__uint_as_float(u[e] << 16)));
+              top = fmaxf(top, fabsf(__uint_as_float(u[e] & 0xFFFF0000u)));
             }
           }
           const int ex = top > 0.0f ? ilogbf(top) : 0;
-          auto half = [&](uint32_t x) {
-            return pack2<false>(ldexpf(__uint_as_float(x << 16), -ex),
-                                ldexpf(__uint_as_float(x & 0xFFFF0000u), -ex));
+          auto half = [&](uint32_t u) {
+            return pack2<false>(ldexpf(__uint_as_float(u << 16), -ex),
+                                ldexpf(__uint_as_float(u & 0xFFFF0000u), -ex));
           };
 #pragma unroll
           for (int i = 0; i < kDp / 8; ++i)
@@ -631,9 +637,21 @@ paged_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         for (int i = 0; i < kDp / 8; ++i)
           *reinterpret_cast<uint4*>(dst + (i / 8) * L::kPanel + (((i % 8) ^ (r & 7)) << 4)) = v[i];
         fence_proxy_async_smem();
-        tc_fence_before();                      // the previous item's O has been read
         mbar_arrive(&q_ready[t]);
-      }
+        return sc;
+    };
+    bool have = advance(&it);
+    float sc = have ? load_q(it) : 0.0f;
+    while (ok && have) {
+      const int row0 = it.pair * kPairRows + t * kTileRows;
+      const int base = it.len - it.n;
+      const int rr = row0 + r;
+      const bool has = rr < it.rows;
+      const int tok = rr / p.group, hq = it.head * p.group + rr % p.group;
+      const int pos = has ? base + tok : -1;
+      const int t_lo = base + row0 / p.group;
+      const int t_hi = base + (min(row0 + kTileRows, it.rows) - 1) / p.group;
+      const int sinks = p.window > 0 ? p.sinks : 0;
       float ref = -INFINITY, l = 0.0f;
       for (int i = 0; i < it.count; ++i) {
         ok = __all_sync(kAll, mbar_wait(&s_full[t], steps++ & 1, abort_flag, c.status,
@@ -648,7 +666,7 @@ paged_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         for (int q = 0; q < 4; ++q) reg_fence(sr[q]);
         if constexpr (kQ8) {
           const float4* ks = reinterpret_cast<const float4*>(
-              smem + L::kScaleOff + (tiles_seen % L::kScaleRing) * kKeys * 4);
+              smem + L::kScaleOff + ((it.before + i) % L::kScaleRing) * kKeys * 4);
 #pragma unroll
           for (int q = 0; q < 32; ++q) {
             const float4 k4 = ks[q];
@@ -663,7 +681,6 @@ paged_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             x[3] = __float_as_uint(b.y);
           }
         }
-        ++tiles_seen;
         const int key0 = it.key0(i);
         if (!(key0 + kKeys - 1 <= t_lo &&
               (p.window <= 0 || key0 >= t_hi - p.window + 1 || key0 + kKeys - 1 < sinks))) {
@@ -733,6 +750,13 @@ paged_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         l += (a01.x + a01.y) + (a23.x + a23.y);
       }
       if (!ok) break;
+      // The next item's queries go out before this one's results: every QK^T of
+      // this tile has been read, so its first one can run meanwhile.  (It
+      // overwrites S_t behind the last PV that reads P_t; O_t is only
+      // overwritten once this thread has delivered the next P.)
+      Item nx = it;
+      const bool have_next = advance(&nx);
+      const float next_sc = have_next ? load_q(nx) : 0.0f;
       // ---- out = O / l, or a part
       ok = __all_sync(kAll, mbar_wait(&o_full[t], items++ & 1, abort_flag, c.status,
                                       p.timeout_ns));
@@ -801,6 +825,10 @@ paged_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                             __uint_as_float(o[4 * v + 2]), __uint_as_float(o[4 * v + 3]));
         }
       }
+      tc_fence_before();                        // O_t has been read
+      it = nx;
+      have = have_next;
+      sc = next_sc;
     }
     if (tid == 0) {
 #pragma unroll

@@ -172,7 +172,7 @@ def test_bad_page_is_reported_and_never_followed(sage, q_len):
 @pytest.mark.parametrize("what", ["kv", "q", "order"])
 def test_bad_lengths_skip_their_sequence(sage, q_len, what):
     p = Problem([q_len, q_len], [200, 200], 4, 2, 64, 16, seed=13)
-    good = check(sage, p)
+    ref, _, mean, spread = p.reference()
     if what == "kv":
         p.lens[1] = 201                                # beyond max_kv
     elif what == "q":
@@ -184,7 +184,9 @@ def test_bad_lengths_skip_their_sequence(sage, q_len, what):
     out = torch.full_like(p.q, 7.0)
     sage.attn_paged(*p.sage(sage), p.q, out=out, ws=ws)
     assert sage.device_status(ws) == sage.ERR_INVALID_ARG
-    assert torch.equal(out[:q_len], good[:q_len])
+    # the other sequence is right (its split into parts goes by the whole batch, so not to the bit)
+    tol = p.tolerance(ref, mean, spread)
+    assert ((out.double() - ref).abs() <= tol)[:q_len].all()
     assert (out[q_len:] == 7.0).all()
 
 
