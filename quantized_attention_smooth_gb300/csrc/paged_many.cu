@@ -38,6 +38,7 @@
 // of the pair sees are zeroed in shared memory (0 times NaN would be NaN).
 
 #include <atomic>
+#include <type_traits>
 
 #include "sage_kernels.h"
 #include "sage_paged_device.cuh"
@@ -111,6 +112,31 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, i
          "r"(smem_u32(bar))
       : "memory");
 }
+
+// One lane of a converged warp, the same one each time.  A branch on it, and
+// operands that come out of a shuffle, tell the compiler that the values are
+// the warp's: the MMAs then take them from uniform registers.  (From a branch on
+// the lane number each MMA cost about 90 cycles to issue, for 64 to run.)
+__device__ __forceinline__ bool elect_one() {
+  uint32_t yes;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n}"
+               : "=r"(yes));
+  return yes != 0;
+}
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(kAll, x, 0); }
+
+// A position in a ring of kN barriers and the parity of its present round.
+template <int kN>
+struct Ring {
+  int at = 0;
+  uint32_t parity = 0;
+  __device__ __forceinline__ void next() {
+    if (++at == kN) {
+      at = 0;
+      parity ^= 1u;
+    }
+  }
+};
 
 // The part of a (sequence, kv head, pair) that a CTA works on.
 struct Item {
@@ -338,7 +364,8 @@ paged_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     if (warp == 9 && !kQ8) {
       // ================================================== copies of K and V
       const int rows_box = min(c.page_size, kKeys), boxes = kKeys / rows_box;
-      int64_t seq = 0;                          // copies issued: K and V tiles alternate
+      Ring<kStages> ring;                       // K and V tiles alternate
+      int issued = 0;
       bool ok = true;
       while (ok && walk.next(p, &it)) {
         const int sinks = p.window > 0 ? p.sinks : 0;
@@ -355,27 +382,30 @@ paged_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             }
           }
 #pragma unroll
-          for (int kv = 0; kv < 2; ++kv, ++seq) {
-            const int st = static_cast<int>(seq % kStages);
-            if (seq >= kStages)
-              ok = __all_sync(kAll, mbar_wait(&empty[st], (seq / kStages - 1) & 1, abort_flag,
-                                              c.status, p.timeout_ns));
+          for (int kv = 0; kv < 2; ++kv) {
+            ok = __all_sync(kAll, mbar_wait(&empty[ring.at], ring.parity ^ 1u, abort_flag,
+                                            c.status, p.timeout_ns));
             if (!ok) break;
-            if (lane == 0) mbar_expect_tx(&full[st], L::kTileBytes);
+            if (lane == 0) mbar_expect_tx(&full[ring.at], L::kTileBytes);
             __syncwarp();
             if (lane < boxes) {
-              uint8_t* dst = smem + L::kRingOff + st * L::kTileBytes + lane * rows_box * 128;
+              uint8_t* dst = smem + L::kRingOff + ring.at * L::kTileBytes + lane * rows_box * 128;
 #pragma unroll
               for (int a = 0; a < kDp / 64; ++a)
                 tma_load_4d(dst + a * L::kPanel, kv == 0 ? &tm_k : &tm_v, 64 * a, slot, it.head,
-                            page, &full[st]);
+                            page, &full[ring.at]);
             }
+            ring.next();
+            issued = min(issued + 1, kStages);
           }
         }
       }
       // no copy may still be in flight when the CTA exits
-      for (int64_t i = seq > kStages ? seq - kStages : 0; i < seq; ++i)
-        mbar_wait(&full[i % kStages], (i / kStages) & 1, nullptr, c.status, p.timeout_ns);
+      for (int i = 1; i <= issued; ++i) {
+        const int st = ring.at - i;             // below 0: in the round before
+        mbar_wait(&full[st < 0 ? st + kStages : st], st < 0 ? ring.parity ^ 1u : ring.parity,
+                  nullptr, c.status, p.timeout_ns);
+      }
     } else if (warp == 8) {
       // ================================================== MMAs
       constexpr uint32_t kFmt = kMmaBF16 ? 1u : 0u;
@@ -387,53 +417,60 @@ paged_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
       // further (leading offset), the next 8 keys 1024 bytes further (stride offset)
       const uint32_t v_lo = ((smem_u32(smem + L::kRingOff) & 0x3FFFFu) >> 4) |
                             (static_cast<uint32_t>(L::kPanel >> 4) << 16);
-      auto qk = [&](int t, int st) {
+      const uint32_t tb = uniform(tbase);
+      // S_t = Q_t K^T and O_t (+)= P_t V, for one elected lane
+      auto qk = [&](auto tc, uint32_t k_lo) {
+        constexpr int t = decltype(tc)::value;
 #pragma unroll
         for (int k = 0; k < kDp / 16; ++k) {
           const uint32_t off = ((k / 4) * L::kPanel + (k % 4) * 32) >> 4;
-          mma_f16_ss_lo(tbase + t * 128, q_lo + ((t * L::kTileBytes) >> 4) + off,
-                        ring_lo + ((st * L::kTileBytes) >> 4) + off, kIdQk, k > 0 ? 1u : 0u);
+          mma_f16_ss_lo(tb + t * 128, q_lo + ((t * L::kTileBytes) >> 4) + off, k_lo + off, kIdQk,
+                        k > 0 ? 1u : 0u);
         }
       };
-      auto pv = [&](int t, int st, bool add) {
+      auto pv = [&](auto tc, uint32_t val_lo, uint32_t add) {
+        constexpr int t = decltype(tc)::value;
 #pragma unroll
         for (int k = 0; k < kKeys / 16; ++k)
-          mma_ts(tbase + 256 + t * kDp, tbase + t * 128 + 8 * k,
-                 v_lo + ((st * L::kTileBytes + k * 2048) >> 4), kSdescSw128Hi, kIdPv,
-                 add || k > 0 ? 1u : 0u);
+          mma_ts(tb + 256 + t * kDp, tb + t * 128 + 8 * k, val_lo + ((k * 2048) >> 4),
+                 kSdescSw128Hi, kIdPv, k > 0 ? 1u : add);
       };
-      int64_t seq = 0;                          // tiles taken from the ring
+      constexpr std::integral_constant<int, 0> T0{};
+      constexpr std::integral_constant<int, 1> T1{};
+      Ring<kStages> ring;
       uint32_t items[2] = {0, 0}, steps[2] = {0, 0};
       bool ok = true, issued = false;
       auto wait = [&](uint64_t* bar, uint32_t parity) {
         return __all_sync(kAll, mbar_wait(bar, parity & 1, abort_flag, c.status, p.timeout_ns));
       };
+      auto ring_lo_at = [&](uint32_t lo0) {
+        return uniform(lo0 + ring.at * (L::kTileBytes >> 4));
+      };
       while (ok && walk.next(p, &it)) {
         const bool two = it.pair * kPairRows + kTileRows < it.rows;
         const int sinks = p.window > 0 ? p.sinks : 0;
-        for (int t = 0; ok && t < (two ? 2 : 1); ++t) ok = wait(&q_ready[t], items[t]++);
-        const int k0 = static_cast<int>(seq % kStages);
-        ok = ok && wait(&full[k0], static_cast<uint32_t>(seq / kStages));
+        ok = wait(&q_ready[0], items[0]++);
+        if (ok && two) ok = wait(&q_ready[1], items[1]++);
+        ok = ok && wait(&full[ring.at], ring.parity);
         if (!ok) break;
-        ++seq;
         tc_fence_after();
-        if (lane == 0) {
-          qk(0, k0);
+        issued = true;
+        uint32_t k_lo = ring_lo_at(ring_lo);
+        if (elect_one()) {
+          qk(T0, k_lo);
           tc_commit(&s_full[0]);
           if (two) {
-            qk(1, k0);
+            qk(T1, k_lo);
             tc_commit(&s_full[1]);
           }
-          tc_commit(&empty[k0]);
+          tc_commit(&empty[ring.at]);
         }
         __syncwarp();
-        issued = true;
+        ring.next();
         for (int i = 0; ok && i < it.count; ++i) {
           const bool more = i + 1 < it.count;
-          const int sv = static_cast<int>(seq % kStages);
-          ok = wait(&full[sv], static_cast<uint32_t>(seq / kStages));
+          ok = wait(&full[ring.at], ring.parity);
           if (!ok) break;
-          ++seq;
           if constexpr (!kQ8) {
             const int key0 = it.key0(i);
             if (!(key0 + kKeys - 1 <= it.p_hi && (key0 >= it.lo || key0 + kKeys - 1 < sinks))) {
@@ -441,8 +478,8 @@ paged_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
               for (int r = lane; r < kKeys; r += 32) {
                 const int key = key0 + r;
                 if (key <= it.p_hi && (key >= it.lo || key < sinks)) continue;
-                uint4* row = reinterpret_cast<uint4*>(smem + L::kRingOff + sv * L::kTileBytes +
-                                                      r * 128);
+                uint4* row = reinterpret_cast<uint4*>(smem + L::kRingOff +
+                                                      ring.at * L::kTileBytes + r * 128);
 #pragma unroll
                 for (int a = 0; a < kDp / 64; ++a)
 #pragma unroll
@@ -452,37 +489,50 @@ paged_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
               __syncwarp();
             }
           }
-          int sk = 0;
-          for (int t = 0; ok && t < (two ? 2 : 1); ++t) {
-            ok = wait(&p_ready[t], steps[t]++);
+          const uint32_t val_lo = ring_lo_at(v_lo);
+          uint64_t* const v_empty = &empty[ring.at];
+          ring.next();
+          // ---- tile 0: PV, then the next QK^T
+          ok = wait(&p_ready[0], steps[0]++);
+          if (ok && more) ok = wait(&full[ring.at], ring.parity);
+          if (!ok) break;
+          tc_fence_after();
+          if (more) k_lo = ring_lo_at(ring_lo);
+          if (elect_one()) {
+            pv(T0, val_lo, i > 0 ? 1u : 0u);
+            if (!two) tc_commit(v_empty);
+            if (more) {
+              qk(T0, k_lo);
+              tc_commit(&s_full[0]);
+              if (!two) tc_commit(&empty[ring.at]);
+            } else {
+              tc_commit(&o_full[0]);
+            }
+          }
+          __syncwarp();
+          if (two) {
+            // ---- tile 1
+            ok = wait(&p_ready[1], steps[1]++);
             if (!ok) break;
             tc_fence_after();
-            if (lane == 0) pv(t, sv, i > 0);
-            const bool last_tile = t == (two ? 1 : 0);
-            if (lane == 0 && last_tile) tc_commit(&empty[sv]);
-            __syncwarp();
-            if (more) {
-              if (t == 0) {
-                sk = static_cast<int>(seq % kStages);
-                ok = wait(&full[sk], static_cast<uint32_t>(seq / kStages));
-                if (!ok) break;
-                ++seq;
-                tc_fence_after();
+            if (elect_one()) {
+              pv(T1, val_lo, i > 0 ? 1u : 0u);
+              tc_commit(v_empty);
+              if (more) {
+                qk(T1, k_lo);
+                tc_commit(&s_full[1]);
+                tc_commit(&empty[ring.at]);
+              } else {
+                tc_commit(&o_full[1]);
               }
-              if (lane == 0) {
-                qk(t, sk);
-                tc_commit(&s_full[t]);
-                if (last_tile) tc_commit(&empty[sk]);
-              }
-            } else if (lane == 0) {
-              tc_commit(&o_full[t]);
             }
             __syncwarp();
           }
+          if (more) ring.next();
         }
       }
       if (issued) {                             // every MMA ends before TMEM is released
-        if (lane == 0) tc_commit(drain);
+        if (elect_one()) tc_commit(drain);
         __syncwarp();
         mbar_wait(drain, 0, nullptr, c.status, p.timeout_ns);
       }
@@ -520,7 +570,7 @@ paged_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
           }
         }
       };
-      int64_t seq = 0;
+      Ring<kStages> ring;
       bool ok = true;
       bool have = walk.next(p, &it);
       if (have) load(it, 0, 0);
@@ -529,14 +579,11 @@ paged_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         bool have_next = true;
         for (int i = 0; ok && i < it.count; ++i) {
 #pragma unroll
-          for (int kv = 0; kv < 2; ++kv, ++seq) {
-            const int st = static_cast<int>(seq % kStages);
-            if (seq >= kStages)
-              ok = mbar_wait(&empty[st], (seq / kStages - 1) & 1, abort_flag, c.status,
-                             p.timeout_ns);
-            ok = __all_sync(kAll, ok);
+          for (int kv = 0; kv < 2; ++kv) {
+            ok = __all_sync(kAll, mbar_wait(&empty[ring.at], ring.parity ^ 1u, abort_flag,
+                                            c.status, p.timeout_ns));
             if (!ok) break;
-            uint8_t* tile = smem + L::kRingOff + st * L::kTileBytes + (ch / 64) * L::kPanel;
+            uint8_t* tile = smem + L::kRingOff + ring.at * L::kTileBytes + (ch / 64) * L::kPanel;
 #pragma unroll
             for (int j = 0; j < kIter; ++j) {
               const int r = r0 + j * (128 / kRowLanes);
@@ -554,10 +601,11 @@ paged_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
               uint4* row = reinterpret_cast<uint4*>(tile + r * 128);
               row[q0 ^ (r & 7)] = make_uint4(h[0], h[1], h[2], h[3]);
               row[(q0 + 1) ^ (r & 7)] = make_uint4(h[4], h[5], h[6], h[7]);
-              if (kv == 0 && ch == 0) scales[(seq / 2) % L::kScaleRing * kKeys + r] = ks[j];
+              if (kv == 0 && ch == 0) scales[(it.before + i) % L::kScaleRing * kKeys + r] = ks[j];
             }
             fence_proxy_async_smem();
-            mbar_arrive(&full[st]);
+            mbar_arrive(&full[ring.at]);
+            ring.next();
             // the next tile's loads run while the barriers turn
             if (kv == 0) load(it, i, 1);
             else if (i + 1 < it.count) load(it, i + 1, 0);
@@ -658,53 +706,84 @@ paged_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                                         p.timeout_ns));
         if (!ok) break;
         tc_fence_after();
-        uint32_t sr[4][32];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) tmem_ld32(ts + 32 * q, sr[q]);
-        tmem_ld_wait();
-#pragma unroll
-        for (int q = 0; q < 4; ++q) reg_fence(sr[q]);
-        if constexpr (kQ8) {
-          const float4* ks = reinterpret_cast<const float4*>(
-              smem + L::kScaleOff + ((it.before + i) % L::kScaleRing) * kKeys * 4);
-#pragma unroll
-          for (int q = 0; q < 32; ++q) {
-            const float4 k4 = ks[q];
-            uint32_t* x = &sr[q / 8][(q % 8) * 4];
-            const float2 a = __fmul2_rn(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])),
-                                        make_float2(k4.x, k4.y));
-            const float2 b = __fmul2_rn(make_float2(__uint_as_float(x[2]), __uint_as_float(x[3])),
-                                        make_float2(k4.z, k4.w));
-            x[0] = __float_as_uint(a.x);
-            x[1] = __float_as_uint(a.y);
-            x[2] = __float_as_uint(b.x);
-            x[3] = __float_as_uint(b.y);
-          }
-        }
         const int key0 = it.key0(i);
-        if (!(key0 + kKeys - 1 <= t_lo &&
-              (p.window <= 0 || key0 >= t_hi - p.window + 1 || key0 + kKeys - 1 < sinks))) {
-          const int hi = pos + 1 - key0;                            // keys below: not later
-          const int lo = p.window > 0 ? pos - p.window + 1 - key0 : 0;   // keys below: too early
+        const bool masked =
+            !(key0 + kKeys - 1 <= t_lo &&
+              (p.window <= 0 || key0 >= t_hi - p.window + 1 || key0 + kKeys - 1 < sinks));
+        // One pass over S in pieces of 32 keys, the next piece's load in flight
+        // behind the present one's arithmetic: exponentials against the reference
+        // at hand, and the maximum beside them.  Only if a row's maximum turns
+        // out to have outgrown its reference (always on an item's first tile),
+        // the reference moves and the pass is taken again; S is still there, as
+        // P is stored last.
+        uint32_t w[64];
+        float2 a01, a23;
+        while (true) {
+          const float safe = ref == -INFINITY ? 0.0f : ref;
+          const float2 sc2 = make_float2(sc, sc), nm2 = make_float2(-safe, -safe);
+          a01 = make_float2(0.0f, 0.0f);
+          a23 = make_float2(0.0f, 0.0f);
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          uint32_t x[2][32];
+          tmem_ld32(ts, x[0]);
+          tmem_ld_wait();
+          reg_fence(x[0]);
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            const uint32_t early = below(lo - 32 * q) & ~below(sinks - key0 - 32 * q);
-            const uint32_t see = below(hi - 32 * q) & ~early;
+            uint32_t (&y)[32] = x[q & 1];
+            if (q < 3) tmem_ld32(ts + 32 * (q + 1), x[(q + 1) & 1]);
+            if constexpr (kQ8) {
+              const float4* ks = reinterpret_cast<const float4*>(
+                  smem + L::kScaleOff +
+                  (((it.before + i) % L::kScaleRing) * kKeys + 32 * q) * 4);
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (!((see >> e) & 1u)) sr[q][e] = 0xFF800000u;       // -inf
+              for (int e = 0; e < 8; ++e) {
+                const float4 k4 = ks[e];
+                const float2 u = __fmul2_rn(
+                    make_float2(__uint_as_float(y[4 * e]), __uint_as_float(y[4 * e + 1])),
+                    make_float2(k4.x, k4.y));
+                const float2 v = __fmul2_rn(
+                    make_float2(__uint_as_float(y[4 * e + 2]), __uint_as_float(y[4 * e + 3])),
+                    make_float2(k4.z, k4.w));
+                y[4 * e] = __float_as_uint(u.x);
+                y[4 * e + 1] = __float_as_uint(u.y);
+                y[4 * e + 2] = __float_as_uint(v.x);
+                y[4 * e + 3] = __float_as_uint(v.y);
+              }
+            }
+            if (masked) {
+              const int hi = pos + 1 - key0 - 32 * q;                // keys below: not later
+              const int lo = p.window > 0 ? pos - p.window + 1 - key0 - 32 * q : 0;
+              const uint32_t early = below(lo) & ~below(sinks - key0 - 32 * q);
+              const uint32_t see = below(hi) & ~early;
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (!((see >> e) & 1u)) y[e] = 0xFF800000u;          // -inf
+            }
+#pragma unroll
+            for (int e = 0; e < 32; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(y[e]));
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float2 d01 = __ffma2_rn(
+                  make_float2(__uint_as_float(y[4 * e]), __uint_as_float(y[4 * e + 1])), sc2, nm2);
+              const float2 d23 = __ffma2_rn(
+                  make_float2(__uint_as_float(y[4 * e + 2]), __uint_as_float(y[4 * e + 3])), sc2,
+                  nm2);
+              const float2 p01 = make_float2(fast_exp2(d01.x), fast_exp2(d01.y));
+              const float2 p23 = make_float2(fast_exp2(d23.x), fast_exp2(d23.y));
+              w[16 * q + 2 * e] = pack2<kMmaBF16>(p01.x, p01.y);
+              w[16 * q + 2 * e + 1] = pack2<kMmaBF16>(p23.x, p23.y);
+              a01 = __fadd2_rn(a01, p01);
+              a23 = __fadd2_rn(a23, p23);
+            }
+            if (q < 3) {
+              tmem_ld_wait();
+              reg_fence(x[(q + 1) & 1]);
+            }
           }
-        }
-        float mx[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          mx[q] = __uint_as_float(sr[q][0]);
-#pragma unroll
-          for (int e = 1; e < 32; ++e) mx[q] = fmaxf(mx[q], __uint_as_float(sr[q][e]));
-        }
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
-        const bool grew = top > ref + kLazy || (ref == -INFINITY && top > -INFINITY);
-        if (__any_sync(kAll, grew)) {
+          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
+          const bool grew = top > ref + kLazy || (ref == -INFINITY && top > -INFINITY);
+          if (!__any_sync(kAll, grew)) break;
           const float next = grew ? top : ref;
           const float alpha = grew ? fast_exp2(ref - next) : 1.0f;  // 0 from -inf
           if (i > 0) {
@@ -722,28 +801,8 @@ paged_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
           l *= alpha;
           ref = next;
         }
-        const float safe = ref == -INFINITY ? 0.0f : ref;
-        const float2 sc2 = make_float2(sc, sc), nm2 = make_float2(-safe, -safe);
-        float2 a01 = make_float2(0.0f, 0.0f), a23 = make_float2(0.0f, 0.0f);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t w[32];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const uint32_t* x = &sr[2 * h + e / 8][(e % 8) * 4];
-            const float2 d01 = __ffma2_rn(
-                make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])), sc2, nm2);
-            const float2 d23 = __ffma2_rn(
-                make_float2(__uint_as_float(x[2]), __uint_as_float(x[3])), sc2, nm2);
-            const float2 p01 = make_float2(fast_exp2(d01.x), fast_exp2(d01.y));
-            const float2 p23 = make_float2(fast_exp2(d23.x), fast_exp2(d23.y));
-            w[2 * e] = pack2<kMmaBF16>(p01.x, p01.y);
-            w[2 * e + 1] = pack2<kMmaBF16>(p23.x, p23.y);
-            a01 = __fadd2_rn(a01, p01);
-            a23 = __fadd2_rn(a23, p23);
-          }
-          tmem_st32(ts + 32 * h, w);
-        }
+        tmem_st32(ts, reinterpret_cast<const uint32_t (&)[32]>(w[0]));
+        tmem_st32(ts + 32, reinterpret_cast<const uint32_t (&)[32]>(w[32]));
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive(&p_ready[t]);
