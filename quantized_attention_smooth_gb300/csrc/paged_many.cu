@@ -710,78 +710,77 @@ paged_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         const bool masked =
             !(key0 + kKeys - 1 <= t_lo &&
               (p.window <= 0 || key0 >= t_hi - p.window + 1 || key0 + kKeys - 1 < sinks));
-        // One pass over S in pieces of 32 keys, the next piece's load in flight
-        // behind the present one's arithmetic: exponentials against the reference
-        // at hand, and the maximum beside them.  Only if a row's maximum turns
-        // out to have outgrown its reference (always on an item's first tile),
-        // the reference moves and the pass is taken again; S is still there, as
-        // P is stored last.
+        // Exponentials against the reference at hand, and the maximum beside them,
+        // in one straight run of independent instructions.  Only if a row's
+        // maximum turns out to have outgrown its reference (always on an item's
+        // first tile), the reference moves and the run is taken again; S is still
+        // there, as P is stored last.
         uint32_t w[64];
         float2 a01, a23;
-        while (true) {
+        auto logits = [&](uint32_t (&x)[4][32], auto masked_c) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) tmem_ld32(ts + 32 * q, x[q]);
+          tmem_ld_wait();
+#pragma unroll
+          for (int q = 0; q < 4; ++q) reg_fence(x[q]);
+          if constexpr (kQ8) {
+            const float4* ks = reinterpret_cast<const float4*>(
+                smem + L::kScaleOff + ((it.before + i) % L::kScaleRing) * kKeys * 4);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const float4 k4 = ks[e];
+              uint32_t* y = &x[e / 8][(e % 8) * 4];
+              const float2 u = __fmul2_rn(make_float2(__uint_as_float(y[0]), __uint_as_float(y[1])),
+                                          make_float2(k4.x, k4.y));
+              const float2 v = __fmul2_rn(make_float2(__uint_as_float(y[2]), __uint_as_float(y[3])),
+                                          make_float2(k4.z, k4.w));
+              y[0] = __float_as_uint(u.x);
+              y[1] = __float_as_uint(u.y);
+              y[2] = __float_as_uint(v.x);
+              y[3] = __float_as_uint(v.y);
+            }
+          }
+          if constexpr (decltype(masked_c)::value) {
+            const int hi = pos + 1 - key0;                           // keys below: not later
+            const int lo = p.window > 0 ? pos - p.window + 1 - key0 : 0;   // below: too early
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const uint32_t early = below(lo - 32 * q) & ~below(sinks - key0 - 32 * q);
+              const uint32_t see = below(hi - 32 * q) & ~early;
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (!((see >> e) & 1u)) x[q][e] = 0xFF800000u;       // -inf
+            }
+          }
+        };
+        auto weigh = [&](auto masked_c) {
+          uint32_t x[4][32];
+          logits(x, masked_c);
           const float safe = ref == -INFINITY ? 0.0f : ref;
           const float2 sc2 = make_float2(sc, sc), nm2 = make_float2(-safe, -safe);
           a01 = make_float2(0.0f, 0.0f);
           a23 = make_float2(0.0f, 0.0f);
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-          uint32_t x[2][32];
-          tmem_ld32(ts, x[0]);
-          tmem_ld_wait();
-          reg_fence(x[0]);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            uint32_t (&y)[32] = x[q & 1];
-            if (q < 3) tmem_ld32(ts + 32 * (q + 1), x[(q + 1) & 1]);
-            if constexpr (kQ8) {
-              const float4* ks = reinterpret_cast<const float4*>(
-                  smem + L::kScaleOff +
-                  (((it.before + i) % L::kScaleRing) * kKeys + 32 * q) * 4);
+          for (int e = 0; e < 32; ++e) {
+            const uint32_t* y = &x[e / 8][(e % 8) * 4];
 #pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const float4 k4 = ks[e];
-                const float2 u = __fmul2_rn(
-                    make_float2(__uint_as_float(y[4 * e]), __uint_as_float(y[4 * e + 1])),
-                    make_float2(k4.x, k4.y));
-                const float2 v = __fmul2_rn(
-                    make_float2(__uint_as_float(y[4 * e + 2]), __uint_as_float(y[4 * e + 3])),
-                    make_float2(k4.z, k4.w));
-                y[4 * e] = __float_as_uint(u.x);
-                y[4 * e + 1] = __float_as_uint(u.y);
-                y[4 * e + 2] = __float_as_uint(v.x);
-                y[4 * e + 3] = __float_as_uint(v.y);
-              }
-            }
-            if (masked) {
-              const int hi = pos + 1 - key0 - 32 * q;                // keys below: not later
-              const int lo = p.window > 0 ? pos - p.window + 1 - key0 - 32 * q : 0;
-              const uint32_t early = below(lo) & ~below(sinks - key0 - 32 * q);
-              const uint32_t see = below(hi) & ~early;
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (!((see >> e) & 1u)) y[e] = 0xFF800000u;          // -inf
-            }
-#pragma unroll
-            for (int e = 0; e < 32; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(y[e]));
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float2 d01 = __ffma2_rn(
-                  make_float2(__uint_as_float(y[4 * e]), __uint_as_float(y[4 * e + 1])), sc2, nm2);
-              const float2 d23 = __ffma2_rn(
-                  make_float2(__uint_as_float(y[4 * e + 2]), __uint_as_float(y[4 * e + 3])), sc2,
-                  nm2);
-              const float2 p01 = make_float2(fast_exp2(d01.x), fast_exp2(d01.y));
-              const float2 p23 = make_float2(fast_exp2(d23.x), fast_exp2(d23.y));
-              w[16 * q + 2 * e] = pack2<kMmaBF16>(p01.x, p01.y);
-              w[16 * q + 2 * e + 1] = pack2<kMmaBF16>(p23.x, p23.y);
-              a01 = __fadd2_rn(a01, p01);
-              a23 = __fadd2_rn(a23, p23);
-            }
-            if (q < 3) {
-              tmem_ld_wait();
-              reg_fence(x[(q + 1) & 1]);
-            }
+            for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], __uint_as_float(y[k]));
+            const float2 d01 = __ffma2_rn(
+                make_float2(__uint_as_float(y[0]), __uint_as_float(y[1])), sc2, nm2);
+            const float2 d23 = __ffma2_rn(
+                make_float2(__uint_as_float(y[2]), __uint_as_float(y[3])), sc2, nm2);
+            const float2 p01 = make_float2(fast_exp2(d01.x), fast_exp2(d01.y));
+            const float2 p23 = make_float2(fast_exp2(d23.x), fast_exp2(d23.y));
+            w[2 * e] = pack2<kMmaBF16>(p01.x, p01.y);
+            w[2 * e + 1] = pack2<kMmaBF16>(p23.x, p23.y);
+            a01 = __fadd2_rn(a01, p01);
+            a23 = __fadd2_rn(a23, p23);
           }
-          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
+          return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
+        };
+        while (true) {
+          const float top = masked ? weigh(std::true_type{}) : weigh(std::false_type{});
           const bool grew = top > ref + kLazy || (ref == -INFINITY && top > -INFINITY);
           if (!__any_sync(kAll, grew)) break;
           const float next = grew ? top : ref;
