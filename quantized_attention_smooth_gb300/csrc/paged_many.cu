@@ -175,23 +175,27 @@ __device__ __forceinline__ Span pair_span(const PagedAttnParams& p, int base, in
 struct Walk {
   int s, pair, head, unit;
   int64_t left, tiles;
-  __device__ __forceinline__ bool next(const PagedAttnParams& p, Item* it) {
+  // *it holds the item before, if there was one (fresh: there was none)
+  __device__ __forceinline__ bool next(const PagedAttnParams& p, Item* it, bool fresh = false) {
     while (left > 0 && s < p.c.nseq) {
-      if (!served(p, s, &it->start, &it->n, &it->len, &it->rows) ||
-          pair * kPairRows >= it->rows) {
-        ++s;
-        pair = head = unit = 0;
-        continue;
+      if (fresh || head == 0) {                 // a new pair
+        if (((fresh || pair == 0) && !served(p, s, &it->start, &it->n, &it->len, &it->rows)) ||
+            pair * kPairRows >= it->rows) {
+          ++s;
+          pair = head = unit = 0;
+          continue;
+        }
+        it->span = pair_span(p, it->len - it->n, it->rows, pair, &it->p_lo, &it->p_hi);
+        it->s = s;
+        it->pair = pair;
+        it->per = it->span.count;
+        it->lo = p.window > 0 ? max(0, it->p_lo - p.window + 1) : 0;
+        fresh = false;
       }
-      it->span = pair_span(p, it->len - it->n, it->rows, pair, &it->p_lo, &it->p_hi);
-      it->s = s;
       it->head = head;
-      it->pair = pair;
-      it->per = it->span.count;
       it->first = max(0, unit - kItemUnits);
       const int64_t upto = unit + left - kItemUnits;      // tiles before the range's end
       it->count = static_cast<int>(min(static_cast<int64_t>(it->per), upto)) - it->first;
-      it->lo = p.window > 0 ? max(0, it->p_lo - p.window + 1) : 0;
       it->before = tiles;
       left -= it->per + kItemUnits - unit;
       unit = 0;
@@ -367,7 +371,7 @@ paged_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
       Ring<kStages> ring;                       // K and V tiles alternate
       int issued = 0;
       bool ok = true;
-      while (ok && walk.next(p, &it)) {
+      for (bool fresh = true; ok && walk.next(p, &it, fresh); fresh = false) {
         const int sinks = p.window > 0 ? p.sinks : 0;
         for (int i = 0; ok && i < it.count; ++i) {
           const int key0 = it.key0(i);
@@ -446,7 +450,7 @@ paged_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
       auto ring_lo_at = [&](uint32_t lo0) {
         return uniform(lo0 + ring.at * (L::kTileBytes >> 4));
       };
-      while (ok && walk.next(p, &it)) {
+      for (bool fresh = true; ok && walk.next(p, &it, fresh); fresh = false) {
         const bool two = it.pair * kPairRows + kTileRows < it.rows;
         const int sinks = p.window > 0 ? p.sinks : 0;
         ok = wait(&q_ready[0], items[0]++);
@@ -572,7 +576,7 @@ paged_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
       };
       Ring<kStages> ring;
       bool ok = true;
-      bool have = walk.next(p, &it);
+      bool have = walk.next(p, &it, true);
       if (have) load(it, 0, 0);
       while (ok && have) {
         Item nx = it;
@@ -626,69 +630,81 @@ paged_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     uint32_t items = 0, steps = 0;
     bool ok = true;
     // the next item that has rows in this tile
-    auto advance = [&](Item* x) {
-      while (walk.next(p, x))
+    auto advance = [&](Item* x, bool fresh) {
+      for (; walk.next(p, x, fresh); fresh = false)
         if (x->pair * kPairRows + t * kTileRows < x->rows) return true;
       return false;
     };
-    // This row's query into shared memory, swizzled as a copy would; returns the
-    // factor from S to base-2 logits.
+    // The queries of this warp's 32 rows into shared memory, swizzled as a copy
+    // would; returns this lane's row's factor from S to base-2 logits.  The lanes
+    // of a row load neighbouring vectors (a row per lane would touch 32 lines a
+    // load: 5000 cycles an item against 900).
     auto load_q = [&](const Item& x) {
-        const int rr = x.pair * kPairRows + t * kTileRows + r;
-        const bool has = rr < x.rows;
-        const int tok = rr / p.group, hq = x.head * p.group + rr % p.group;
-        float sc = p.scale_log2;
-        const uint16_t* q = p.q + (static_cast<int64_t>(x.start) + tok) * p.q_tok +
-                            static_cast<int64_t>(hq) * p.q_head;
-        uint8_t* dst = smem + t * L::kTileBytes + r * 128;
-        auto vec = [&](int i) {
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (has && 8 * i < c.D) {
+      constexpr int kVecs = kDp / 8, kRowsAtOnce = 32 / kVecs;
+      const int i = lane % kVecs, sub = lane / kVecs;
+      uint8_t* const dst = smem + t * L::kTileBytes + (i / 8) * L::kPanel;
+      float sc = p.scale_log2;
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half) {
+        uint4 v[kVecs / 2];
+#pragma unroll
+        for (int j = 0; j < kVecs / 2; ++j) {
+          const int row = (warp & 3) * 32 + (half * (kVecs / 2) + j) * kRowsAtOnce + sub;
+          const int rr = x.pair * kPairRows + t * kTileRows + row;
+          v[j] = make_uint4(0, 0, 0, 0);
+          if (rr < x.rows && 8 * i < c.D) {
+            const int tok = rr / p.group;
+            const uint16_t* q = p.q + (static_cast<int64_t>(x.start) + tok) * p.q_tok +
+                                static_cast<int64_t>(x.head * p.group + rr - tok * p.group) *
+                                    p.q_head + 8 * i;
             if (p.q_vec) {
-              v = *reinterpret_cast<const uint4*>(q + 8 * i);
+              v[j] = *reinterpret_cast<const uint4*>(q);
             } else {
               uint32_t u[4] = {0, 0, 0, 0};
 #pragma unroll
               for (int e = 0; e < 8; ++e)
-                u[e / 2] |= static_cast<uint32_t>(q[8 * i + e]) << (16 * (e & 1));
-              v = make_uint4(u[0], u[1], u[2], u[3]);
+                u[e / 2] |= static_cast<uint32_t>(q[e]) << (16 * (e & 1));
+              v[j] = make_uint4(u[0], u[1], u[2], u[3]);
             }
           }
-          return v;
-        };
-        uint4 v[kDp / 8];
+        }
 #pragma unroll
-        for (int i = 0; i < kDp / 8; ++i) v[i] = vec(i);
-        if constexpr (kQ8 && kQBF16) {
-          // bf16 queries into fp16's range: times 2^-e, e the exponent of the largest
-          float top = 0.0f;
-#pragma unroll
-          for (int i = 0; i < kDp / 8; ++i) {
-            const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+        for (int j = 0; j < kVecs / 2; ++j) {
+          const int in_warp = (half * (kVecs / 2) + j) * kRowsAtOnce + sub;
+          if constexpr (kQ8 && kQBF16) {
+            // bf16 queries into fp16's range: times 2^-e, e the exponent of the row's largest
+            const uint32_t u[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+            float top = 0.0f;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               top = fmaxf(top, fabsf(__uint_as_float(u[e] << 16)));
               top = fmaxf(top, fabsf(__uint_as_float(u[e] & 0xFFFF0000u)));
             }
+#pragma unroll
+            for (int d = kVecs / 2; d > 0; d /= 2)
+              top = fmaxf(top, __shfl_xor_sync(kAll, top, d));
+            const int ex = top > 0.0f ? ilogbf(top) : 0;
+            auto half2 = [&](uint32_t w2) {
+              return pack2<false>(ldexpf(__uint_as_float(w2 << 16), -ex),
+                                  ldexpf(__uint_as_float(w2 & 0xFFFF0000u), -ex));
+            };
+            v[j] = make_uint4(half2(u[0]), half2(u[1]), half2(u[2]), half2(u[3]));
+#pragma unroll
+            for (int g = 0; g < kRowsAtOnce; ++g) {
+              const int e = __shfl_sync(kAll, ex, g * kVecs);
+              if (lane == in_warp - sub + g) sc = ldexpf(p.scale_log2, e);
+            }
           }
-          const int ex = top > 0.0f ? ilogbf(top) : 0;
-          auto half = [&](uint32_t u) {
-            return pack2<false>(ldexpf(__uint_as_float(u << 16), -ex),
-                                ldexpf(__uint_as_float(u & 0xFFFF0000u), -ex));
-          };
-#pragma unroll
-          for (int i = 0; i < kDp / 8; ++i)
-            v[i] = make_uint4(half(v[i].x), half(v[i].y), half(v[i].z), half(v[i].w));
-          sc = ldexpf(sc, ex);
+          const int row = (warp & 3) * 32 + in_warp;
+          *reinterpret_cast<uint4*>(dst + row * 128 + (((i % 8) ^ (row & 7)) << 4)) = v[j];
         }
-#pragma unroll
-        for (int i = 0; i < kDp / 8; ++i)
-          *reinterpret_cast<uint4*>(dst + (i / 8) * L::kPanel + (((i % 8) ^ (r & 7)) << 4)) = v[i];
-        fence_proxy_async_smem();
-        mbar_arrive(&q_ready[t]);
-        return sc;
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      mbar_arrive(&q_ready[t]);
+      return sc;
     };
-    bool have = advance(&it);
+    bool have = advance(&it, true);
     float sc = have ? load_q(it) : 0.0f;
     while (ok && have) {
       const int row0 = it.pair * kPairRows + t * kTileRows;
@@ -813,7 +829,7 @@ paged_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
       // overwrites S_t behind the last PV that reads P_t; O_t is only
       // overwritten once this thread has delivered the next P.)
       Item nx = it;
-      const bool have_next = advance(&nx);
+      const bool have_next = advance(&nx, false);
       const float next_sc = have_next ? load_q(nx) : 0.0f;
       // ---- out = O / l, or a part
       ok = __all_sync(kAll, mbar_wait(&o_full[t], items++ & 1, abort_flag, c.status,
@@ -825,31 +841,51 @@ paged_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         const float inv = l > 0.0f ? 1.0f / l : 0.0f;
         const int64_t orow = (static_cast<int64_t>(it.start) + tok) * p.Hq + hq;
         const float* sv = c.v_scale + it.head * kDp;
+        // Four lanes trade their rows' 16-byte vectors, so that each store writes
+        // 64 bytes of a row (a row per lane would write 32 half sectors).
+        const int j = lane & 3;
+        int64_t rows4[4];
 #pragma unroll
+        for (int m = 0; m < 4; ++m) rows4[m] = __shfl_sync(kAll, orow, (lane & ~3) + m);
+#pragma unroll 1
         for (int q = 0; q < kDp / 32; ++q) {
           uint32_t o[32];
           tmem_ld32(to + 32 * q, o);
           tmem_ld_wait();
           reg_fence(o);
+          uint32_t u[4][4];
 #pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            const int ch = 32 * q + 8 * v;
-            if (has && ch < c.D) {
-              uint32_t w[4];
+          for (int v = 0; v < 4; ++v)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                float a = __uint_as_float(o[8 * v + 2 * e]) * inv;
-                float b = __uint_as_float(o[8 * v + 2 * e + 1]) * inv;
-                if constexpr (kQ8) {
-                  a *= sv[ch + 2 * e];
-                  b *= sv[ch + 2 * e + 1];
-                }
-                w[e] = pack2<kQBF16>(a, b);
+            for (int e = 0; e < 4; ++e) {
+              float a = __uint_as_float(o[8 * v + 2 * e]) * inv;
+              float b = __uint_as_float(o[8 * v + 2 * e + 1]) * inv;
+              if constexpr (kQ8) {
+                a *= sv[32 * q + 8 * v + 2 * e];
+                b *= sv[32 * q + 8 * v + 2 * e + 1];
               }
-              *reinterpret_cast<uint4*>(p.out + orow * c.D + ch) =
-                  make_uint4(w[0], w[1], w[2], w[3]);
+              u[v][e] = pack2<kQBF16>(a, b);
             }
-          }
+          // a 4 x 4 transpose of vectors: by pairs of lanes, then by pairs of pairs
+#pragma unroll
+          for (int d = 1; d <= 2; d *= 2)
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+              if (!(v & d)) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const uint32_t give = (j & d) ? u[v][e] : u[v + d][e];
+                  const uint32_t got = __shfl_xor_sync(kAll, give, d);
+                  if (j & d) u[v][e] = got;
+                  else u[v + d][e] = got;
+                }
+              }
+          const int ch = 32 * q + 8 * j;
+#pragma unroll
+          for (int m = 0; m < 4; ++m)
+            if (row0 + (r & ~3) + m < it.rows && ch < c.D)
+              *reinterpret_cast<uint4*>(p.out + rows4[m] * c.D + ch) =
+                  make_uint4(u[m][0], u[m][1], u[m][2], u[m][3]);
         }
         if (has && p.lse != nullptr)
           p.lse[orow] = l > 0.0f ? (ref + log2f(l)) * 0.69314718055994530942f : -INFINITY;
