@@ -307,6 +307,7 @@ sage_status sage_attn_paged(const sage_paged_cache* cache, const sage_paged_batc
   p.lse = lse;
   p.Hq = static_cast<int32_t>(Hq);
   p.group = static_cast<int32_t>(Hq / cache->Hkv);
+  p.magic = static_cast<uint32_t>((uint64_t(1) << 32) / static_cast<uint64_t>(p.group) + 1);
   // a window as long as the longest sequence hides nothing
   p.window = window >= batch->max_kv ? 0 : static_cast<int32_t>(window);
   p.sinks = p.window == 0 ? 0 : static_cast<int32_t>(sinks < batch->max_kv ? sinks : batch->max_kv);
@@ -318,7 +319,7 @@ sage_status sage_attn_paged(const sage_paged_cache* cache, const sage_paged_batc
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const bool bf16 = dtype == SAGE_BF16;
   const int64_t most = static_cast<int64_t>(batch->max_q) * p.group;
-  const bool many = most > kFewRows && paged_many_serves(p.c);
+  const bool many = most > kFewRows && paged_many_serves(p.c, p.group);
   cudaError_t e = cudaSuccess;
   p.min_rows = 0;
   p.max_rows = many ? kFewRows : INT_MAX;

@@ -9,6 +9,7 @@
 // A CTA works on a pair of 128-row tiles that share every K and V tile:
 //   warps 0-3, 4-7  softmax of tile 0 and 1: thread = row = TMEM lane
 //   warp 8          issues the MMAs (one thread)
+//   warp 10         cuts the CTA's range of work into items for the others
 //   warp 9          copies K and V tiles from the pages (16-bit cache): one
 //                   tensor copy per page and 64 channels, each by its own lane
 //   warps 12-15     8-bit cache only: read K and V codes, widen them to fp16
@@ -76,11 +77,15 @@ struct Many {
   static constexpr int kRingOff = 2 * kTileBytes;
   static constexpr int kScaleOff = kRingOff + kStages * kTileBytes;
   static constexpr int kBarOff = kScaleOff + (kQ8 ? kScaleRing * kKeys * 4 : 0);
-  // full[stages], empty[stages], q_ready[2], s_full[2], p_ready[2], o_full[2], drain
-  static constexpr int kNumBars = 2 * kStages + 9;
+  // full[stages], empty[stages], q_ready[2], s_full[2], p_ready[2], o_full[2], drain,
+  // item_full[items], item_empty[items]
+  static constexpr int kItems = 4;
+  static constexpr int kNumBars = 2 * kStages + 9 + 2 * kItems;
   static constexpr int kMiscOff = (kBarOff + kNumBars * 8 + 15) / 16 * 16;
-  static constexpr int kBytes = kMiscOff + 256;
-  static constexpr int kAlloc = kBytes + 1024;
+  static constexpr int kItemOff = kMiscOff + 256;
+  static constexpr int kAlloc = kItemOff + kItems * 128;
+  // warps that take items: softmax, MMA, and what fills the ring
+  static constexpr int kTakers = 8 + 1 + (kQ8 ? 4 : 1);
   static_assert(kAlloc <= 227 * 1024, "shared memory of one CTA");
 };
 
@@ -138,20 +143,28 @@ struct Ring {
   }
 };
 
-// The part of a (sequence, kv head, pair) that a CTA works on.
+// The part of a (sequence, kv head, pair) that a CTA works on, as the scheduling
+// warp leaves it in shared memory for the other roles (registers that they
+// would keep for it across an item cost spills in their loops).
 struct Item {
-  int s, head, pair;
-  int start, n, len, rows;
-  int p_lo, p_hi;            // positions of the pair's first and last row
+  int s, head, pair, start, rows;
+  int base;                  // position of the sequence's row 0
+  int p_hi;                  // position of the pair's last row
   int lo;                    // first key of the window of the first row
-  int first, count, per;     // key tiles: from, how many, of how many
-  int64_t before;            // key tiles of the CTA's earlier items
-  Span span;
+  int first, count, per;     // key tiles: from, how many (0: no more items), of how many
+  int sink, from;            // Span
+  int before;                // key tiles of the CTA's earlier items
+  struct {
+    int lo, hi;              // positions of the tile's first and last row
+    int tok, off;            // its first row's token, and query head within the group
+  } tile[2];
   __device__ __forceinline__ int key0(int i) const {     // first key of the i-th tile
     const int v = first + i;
-    return kKeys * (v < span.sink ? v : v - span.sink + span.from);
+    return kKeys * (v < sink ? v : v - sink + from);
   }
+  __device__ __forceinline__ bool two() const { return pair * kPairRows + kTileRows < rows; }
 };
+static_assert(sizeof(Item) <= 128, "items lie 128 bytes apart");
 
 __device__ __forceinline__ bool served(const PagedAttnParams& p, int s, int* start, int* n,
                                        int* len, int* rows) {
@@ -169,48 +182,19 @@ __device__ __forceinline__ Span pair_span(const PagedAttnParams& p, int base, in
   return r;
 }
 
-// Walks a CTA's range of units, item by item; every role walks on its own.  An
-// item takes kItemUnits + tiles units, the first ones without a tile; a CTA
-// whose range ends among those leaves the item to the next one.
+// A CTA's place in the units.  An item takes kItemUnits + tiles units, the first
+// ones without a tile; a CTA whose range ends among those leaves the item to the
+// next one.
 struct Walk {
   int s, pair, head, unit;
-  int64_t left, tiles;
-  // *it holds the item before, if there was one (fresh: there was none)
-  __device__ __forceinline__ bool next(const PagedAttnParams& p, Item* it, bool fresh = false) {
-    while (left > 0 && s < p.c.nseq) {
-      if (fresh || head == 0) {                 // a new pair
-        if (((fresh || pair == 0) && !served(p, s, &it->start, &it->n, &it->len, &it->rows)) ||
-            pair * kPairRows >= it->rows) {
-          ++s;
-          pair = head = unit = 0;
-          continue;
-        }
-        it->span = pair_span(p, it->len - it->n, it->rows, pair, &it->p_lo, &it->p_hi);
-        it->s = s;
-        it->pair = pair;
-        it->per = it->span.count;
-        it->lo = p.window > 0 ? max(0, it->p_lo - p.window + 1) : 0;
-        fresh = false;
-      }
-      it->head = head;
-      it->first = max(0, unit - kItemUnits);
-      const int64_t upto = unit + left - kItemUnits;      // tiles before the range's end
-      it->count = static_cast<int>(min(static_cast<int64_t>(it->per), upto)) - it->first;
-      it->before = tiles;
-      left -= it->per + kItemUnits - unit;
-      unit = 0;
-      if (++head == p.c.Hkv) {
-        head = 0;
-        ++pair;
-      }
-      if (it->count > 0) {
-        tiles += it->count;
-        return true;
-      }
-    }
-    return false;
-  }
+  int64_t left;
 };
+
+// x / group for a row's x < group + 256, by a multiplication: exact while
+// x * group < 2^32 (groups up to 16384).
+__device__ __forceinline__ int by_group(const PagedAttnParams& p, int x) {
+  return p.group == 1 ? x : static_cast<int>(__umulhi(static_cast<uint32_t>(x), p.magic));
+}
 
 // Inclusive sum over the block's threads; ends with a barrier.
 template <int kThreads>
@@ -247,9 +231,14 @@ paged_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
   constexpr bool kQ8 = L::kQ8;
   constexpr bool kMmaBF16 = kKind == kKindBF16;
   constexpr int kStages = L::kStages;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = align1024(smem_raw);
+  // The driver places dynamic shared memory behind its 1 KB reservation of a
+  // block; a base off the swizzle's grid is reported and the CTA does nothing.
+  extern __shared__ __align__(1024) uint8_t smem[];
   const PagedGeo& c = p.c;
+  if ((smem_u32(smem) & 1023u) != 0) {
+    if (threadIdx.x == 0) atomicOr(c.status, kStatusBadItem);
+    return;
+  }
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cta = blockIdx.x, ctas = gridDim.x;
   asm volatile("griddepcontrol.launch_dependents;");
@@ -261,6 +250,8 @@ paged_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
   uint64_t* p_ready = s_full + 2;
   uint64_t* o_full = p_ready + 2;
   uint64_t* drain = o_full + 2;
+  uint64_t* item_full = drain + 1;
+  uint64_t* item_empty = item_full + L::kItems;
   int* scan_s = reinterpret_cast<int*>(smem);     // the plan's; the queries come there later
   int64_t* sums_s = reinterpret_cast<int64_t*>(smem + L::kMiscOff);        // 16
   Walk* walk_s = reinterpret_cast<Walk*>(smem + L::kMiscOff + 128);
@@ -280,13 +271,16 @@ paged_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
       mbar_init(&o_full[t], 1);
     }
     mbar_init(drain, 1);
+    for (int i = 0; i < L::kItems; ++i) {
+      mbar_init(&item_full[i], 1);
+      mbar_init(&item_empty[i], L::kTakers);
+    }
     mbar_fence_init();
   }
   if (warp == 8) tmem_alloc(tmem_slot, kTmemCols);
 
   // ---- this CTA's range of units: pairs per sequence, then tiles per pair
-  Walk walk{0, 0, 0, 0, 0, 0};
-  bool used[2] = {false, false};
+  Walk walk{0, 0, 0, 0, 0};
   {
     constexpr int T = L::kThreads;
     const int spt = (c.nseq + T - 1) / T;
@@ -349,7 +343,7 @@ paged_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
           return false;
         }
         *walk_s = Walk{s, pair, static_cast<int>(off / per), static_cast<int>(off % per),
-                       u1 - u0, 0};
+                       u1 - u0};
         return true;
       });
     }
@@ -360,20 +354,105 @@ paged_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
   }
   const uint32_t tbase = *tmem_slot;
   const int wg = warp >> 2;
-  Item it;
+  auto item_at = [&](int i) -> const Item& {
+    return *reinterpret_cast<const Item*>(smem + L::kItemOff + 128 * i);
+  };
+  // waits for the next item; false at the end, or if a wait ran out
+  auto take = [&](const Ring<L::kItems>& at) {
+    return __all_sync(kAll, mbar_wait(&item_full[at.at], at.parity, abort_flag, c.status,
+                                      p.timeout_ns)) &&
+           item_at(at.at).count > 0;
+  };
+  auto give_back = [&](const Ring<L::kItems>& at) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&item_empty[at.at]);
+  };
 
   if (wg == 2) {
     if constexpr (kQ8) regs_decrease<72>();
     else regs_decrease<80>();
-    if (warp == 9 && !kQ8) {
+    if (warp == 10) {
+      // ================================================== items
+      Ring<L::kItems> at;
+      bool ok = true, more = true;
+      int start = 0, n = 0, len = 0, rows = 0, p_lo = 0, p_hi = 0, tiles = 0;
+      Span span{0, 0, 0};
+      bool fresh = true;
+      while (ok && more) {
+        int first = 0, count = 0;
+        while (count <= 0 && walk.left > 0 && walk.s < c.nseq) {
+          if (fresh || walk.head == 0) {        // a new pair
+            if (((fresh || walk.pair == 0) && !served(p, walk.s, &start, &n, &len, &rows)) ||
+                walk.pair * kPairRows >= rows) {
+              ++walk.s;
+              walk.pair = walk.head = walk.unit = 0;
+              continue;
+            }
+            span = pair_span(p, len - n, rows, walk.pair, &p_lo, &p_hi);
+            fresh = false;
+          }
+          first = max(0, walk.unit - kItemUnits);
+          const int64_t upto = walk.unit + walk.left - kItemUnits;   // tiles before the end
+          count = static_cast<int>(min(static_cast<int64_t>(span.count), upto)) - first;
+          walk.left -= span.count + kItemUnits - walk.unit;
+          walk.unit = 0;
+          if (count <= 0 && ++walk.head == c.Hkv) {
+            walk.head = 0;
+            ++walk.pair;
+          }
+        }
+        more = count > 0;
+        ok = __all_sync(kAll, mbar_wait(&item_empty[at.at], at.parity ^ 1u, abort_flag, c.status,
+                                        p.timeout_ns));
+        if (!ok) break;
+        if (lane == 0) {
+          Item& x = *reinterpret_cast<Item*>(smem + L::kItemOff + 128 * at.at);
+          x.count = max(count, 0);
+          if (more) {
+            x.s = walk.s;
+            x.head = walk.head;
+            x.pair = walk.pair;
+            x.start = start;
+            x.rows = rows;
+            x.base = len - n;
+            x.p_hi = p_hi;
+            x.lo = p.window > 0 ? max(0, p_lo - p.window + 1) : 0;
+            x.first = first;
+            x.per = span.count;
+            x.sink = span.sink;
+            x.from = span.from;
+            x.before = tiles;
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              const int row0 = walk.pair * kPairRows + t * kTileRows;
+              const int tok = row0 / p.group;
+              x.tile[t].tok = tok;
+              x.tile[t].off = row0 - tok * p.group;
+              x.tile[t].lo = x.base + tok;
+              x.tile[t].hi = x.base + (min(row0 + kTileRows, rows) - 1) / p.group;
+            }
+          }
+          mbar_arrive(&item_full[at.at]);
+        }
+        __syncwarp();
+        tiles += count;
+        if (++walk.head == c.Hkv) {
+          walk.head = 0;
+          ++walk.pair;
+        }
+        at.next();
+      }
+    } else if (warp == 9 && !kQ8) {
       // ================================================== copies of K and V
       const int rows_box = min(c.page_size, kKeys), boxes = kKeys / rows_box;
       Ring<kStages> ring;                       // K and V tiles alternate
       int issued = 0;
       bool ok = true;
-      for (bool fresh = true; ok && walk.next(p, &it, fresh); fresh = false) {
+      for (Ring<L::kItems> at; ok && take(at); give_back(at), at.next()) {
+        const Item& it = item_at(at.at);
         const int sinks = p.window > 0 ? p.sinks : 0;
-        for (int i = 0; ok && i < it.count; ++i) {
+        const int count = it.count, head = it.head;
+        for (int i = 0; ok && i < count; ++i) {
           const int key0 = it.key0(i);
           // lane b finds the page of box b
           int page = static_cast<int>(c.num_pages), slot = 0;
@@ -396,8 +475,8 @@ paged_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
               uint8_t* dst = smem + L::kRingOff + ring.at * L::kTileBytes + lane * rows_box * 128;
 #pragma unroll
               for (int a = 0; a < kDp / 64; ++a)
-                tma_load_4d(dst + a * L::kPanel, kv == 0 ? &tm_k : &tm_v, 64 * a, slot, it.head,
-                            page, &full[ring.at]);
+                tma_load_4d(dst + a * L::kPanel, kv == 0 ? &tm_k : &tm_v, 64 * a, slot, head, page,
+                            &full[ring.at]);
             }
             ring.next();
             issued = min(issued + 1, kStages);
@@ -450,9 +529,10 @@ paged_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
       auto ring_lo_at = [&](uint32_t lo0) {
         return uniform(lo0 + ring.at * (L::kTileBytes >> 4));
       };
-      for (bool fresh = true; ok && walk.next(p, &it, fresh); fresh = false) {
-        const bool two = it.pair * kPairRows + kTileRows < it.rows;
-        const int sinks = p.window > 0 ? p.sinks : 0;
+      for (Ring<L::kItems> item; ok && take(item); give_back(item), item.next()) {
+        const Item& it = item_at(item.at);
+        const bool two = it.two();
+        const int count = it.count, sinks = p.window > 0 ? p.sinks : 0;
         ok = wait(&q_ready[0], items[0]++);
         if (ok && two) ok = wait(&q_ready[1], items[1]++);
         ok = ok && wait(&full[ring.at], ring.parity);
@@ -471,8 +551,8 @@ paged_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         }
         __syncwarp();
         ring.next();
-        for (int i = 0; ok && i < it.count; ++i) {
-          const bool more = i + 1 < it.count;
+        for (int i = 0; ok && i < count; ++i) {
+          const bool more = i + 1 < count;
           ok = wait(&full[ring.at], ring.parity);
           if (!ok) break;
           if constexpr (!kQ8) {
@@ -575,13 +655,15 @@ paged_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         }
       };
       Ring<kStages> ring;
-      bool ok = true;
-      bool have = walk.next(p, &it, true);
-      if (have) load(it, 0, 0);
+      Ring<L::kItems> at;
+      bool ok = true, have = take(at);
+      if (have) load(item_at(at.at), 0, 0);
       while (ok && have) {
-        Item nx = it;
-        bool have_next = true;
-        for (int i = 0; ok && i < it.count; ++i) {
+        const Item& it = item_at(at.at);
+        const int count = it.count, before = it.before;
+        Ring<L::kItems> nx = at;
+        nx.next();
+        for (int i = 0; ok && i < count; ++i) {
 #pragma unroll
           for (int kv = 0; kv < 2; ++kv) {
             ok = __all_sync(kAll, mbar_wait(&empty[ring.at], ring.parity ^ 1u, abort_flag,
@@ -605,19 +687,19 @@ paged_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
               uint4* row = reinterpret_cast<uint4*>(tile + r * 128);
               row[q0 ^ (r & 7)] = make_uint4(h[0], h[1], h[2], h[3]);
               row[(q0 + 1) ^ (r & 7)] = make_uint4(h[4], h[5], h[6], h[7]);
-              if (kv == 0 && ch == 0) scales[(it.before + i) % L::kScaleRing * kKeys + r] = ks[j];
+              if (kv == 0 && ch == 0) scales[(before + i) % L::kScaleRing * kKeys + r] = ks[j];
             }
             fence_proxy_async_smem();
             mbar_arrive(&full[ring.at]);
             ring.next();
             // the next tile's loads run while the barriers turn
             if (kv == 0) load(it, i, 1);
-            else if (i + 1 < it.count) load(it, i + 1, 0);
-            else if ((have_next = walk.next(p, &nx))) load(nx, 0, 0);
+            else if (i + 1 < count) load(it, i + 1, 0);
+            else if ((have = take(nx))) load(item_at(nx.at), 0, 0);
           }
         }
-        it = nx;
-        have = have_next;
+        give_back(at);
+        at = nx;
       }
     }
   } else {
@@ -629,10 +711,11 @@ paged_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     const uint32_t ts = tbase + lane_off + t * 128, to = tbase + lane_off + 256 + t * kDp;
     uint32_t items = 0, steps = 0;
     bool ok = true;
+    bool used[2] = {false, false};
     // the next item that has rows in this tile
-    auto advance = [&](Item* x, bool fresh) {
-      for (; walk.next(p, x, fresh); fresh = false)
-        if (x->pair * kPairRows + t * kTileRows < x->rows) return true;
+    auto advance = [&](Ring<L::kItems>& at) {
+      for (; take(at); give_back(at), at.next())
+        if (t == 0 || item_at(at.at).two()) return true;
       return false;
     };
     // The queries of this warp's 32 rows into shared memory, swizzled as a copy
@@ -644,19 +727,20 @@ paged_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
       const int i = lane % kVecs, sub = lane / kVecs;
       uint8_t* const dst = smem + t * L::kTileBytes + (i / 8) * L::kPanel;
       float sc = p.scale_log2;
+      const int row_end = x.rows - x.pair * kPairRows - t * kTileRows;
+      const int off = x.tile[t].off;
+      const uint16_t* const q0 = p.q + (static_cast<int64_t>(x.start) + x.tile[t].tok) * p.q_tok +
+                                 static_cast<int64_t>(x.head) * p.group * p.q_head + 8 * i;
 #pragma unroll 1
       for (int half = 0; half < 2; ++half) {
         uint4 v[kVecs / 2];
 #pragma unroll
         for (int j = 0; j < kVecs / 2; ++j) {
           const int row = (warp & 3) * 32 + (half * (kVecs / 2) + j) * kRowsAtOnce + sub;
-          const int rr = x.pair * kPairRows + t * kTileRows + row;
           v[j] = make_uint4(0, 0, 0, 0);
-          if (rr < x.rows && 8 * i < c.D) {
-            const int tok = rr / p.group;
-            const uint16_t* q = p.q + (static_cast<int64_t>(x.start) + tok) * p.q_tok +
-                                static_cast<int64_t>(x.head * p.group + rr - tok * p.group) *
-                                    p.q_head + 8 * i;
+          if (row < row_end && 8 * i < c.D) {
+            const int dt = by_group(p, off + row);
+            const uint16_t* q = q0 + dt * p.q_tok + (off + row - dt * p.group) * p.q_head;
             if (p.q_vec) {
               v[j] = *reinterpret_cast<const uint4*>(q);
             } else {
@@ -704,20 +788,20 @@ paged_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
       mbar_arrive(&q_ready[t]);
       return sc;
     };
-    bool have = advance(&it, true);
-    float sc = have ? load_q(it) : 0.0f;
+    Ring<L::kItems> at;
+    bool have = advance(at);
+    float sc = have ? load_q(item_at(at.at)) : 0.0f;
     while (ok && have) {
-      const int row0 = it.pair * kPairRows + t * kTileRows;
-      const int base = it.len - it.n;
-      const int rr = row0 + r;
-      const bool has = rr < it.rows;
-      const int tok = rr / p.group, hq = it.head * p.group + rr % p.group;
-      const int pos = has ? base + tok : -1;
-      const int t_lo = base + row0 / p.group;
-      const int t_hi = base + (min(row0 + kTileRows, it.rows) - 1) / p.group;
+      const Item& it = item_at(at.at);
+      const int row_end = it.rows - it.pair * kPairRows - t * kTileRows;   // rows of this tile
+      const bool has = r < row_end;
+      const int dt = by_group(p, it.tile[t].off + r);         // this row's token, from the tile's
+      const int pos = has ? it.tile[t].lo + dt : -1;
+      const int t_lo = it.tile[t].lo, t_hi = it.tile[t].hi;
+      const int count = it.count, before = it.before;
       const int sinks = p.window > 0 ? p.sinks : 0;
       float ref = -INFINITY, l = 0.0f;
-      for (int i = 0; i < it.count; ++i) {
+      for (int i = 0; i < count; ++i) {
         ok = __all_sync(kAll, mbar_wait(&s_full[t], steps++ & 1, abort_flag, c.status,
                                         p.timeout_ns));
         if (!ok) break;
@@ -741,7 +825,7 @@ paged_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
           for (int q = 0; q < 4; ++q) reg_fence(x[q]);
           if constexpr (kQ8) {
             const float4* ks = reinterpret_cast<const float4*>(
-                smem + L::kScaleOff + ((it.before + i) % L::kScaleRing) * kKeys * 4);
+                smem + L::kScaleOff + ((before + i) % L::kScaleRing) * kKeys * 4);
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
               const float4 k4 = ks[e];
@@ -828,9 +912,10 @@ paged_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
       // this tile has been read, so its first one can run meanwhile.  (It
       // overwrites S_t behind the last PV that reads P_t; O_t is only
       // overwritten once this thread has delivered the next P.)
-      Item nx = it;
-      const bool have_next = advance(&nx, false);
-      const float next_sc = have_next ? load_q(nx) : 0.0f;
+      Ring<L::kItems> nx = at;
+      nx.next();
+      have = advance(nx);
+      const float next_sc = have ? load_q(item_at(nx.at)) : 0.0f;
       // ---- out = O / l, or a part
       ok = __all_sync(kAll, mbar_wait(&o_full[t], items++ & 1, abort_flag, c.status,
                                       p.timeout_ns));
@@ -839,7 +924,8 @@ paged_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
       const bool whole = it.first == 0 && it.count == it.per;
       if (whole) {
         const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-        const int64_t orow = (static_cast<int64_t>(it.start) + tok) * p.Hq + hq;
+        const int64_t orow = (static_cast<int64_t>(it.start) + it.tile[t].tok + dt) * p.Hq +
+                             it.head * p.group + it.tile[t].off + r - dt * p.group;
         const float* sv = c.v_scale + it.head * kDp;
         // Four lanes trade their rows' 16-byte vectors, so that each store writes
         // 64 bytes of a row (a row per lane would write 32 half sectors).
@@ -883,7 +969,7 @@ paged_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
           const int ch = 32 * q + 8 * j;
 #pragma unroll
           for (int m = 0; m < 4; ++m)
-            if (row0 + (r & ~3) + m < it.rows && ch < c.D)
+            if ((r & ~3) + m < row_end && ch < c.D)
               *reinterpret_cast<uint4*>(p.out + rows4[m] * c.D + ch) =
                   make_uint4(u[m][0], u[m][1], u[m][2], u[m][3]);
         }
@@ -920,8 +1006,8 @@ paged_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         }
       }
       tc_fence_before();                        // O_t has been read
-      it = nx;
-      have = have_next;
+      give_back(at);
+      at = nx;
       sc = next_sc;
     }
     if (tid == 0) {
@@ -1071,7 +1157,8 @@ size_t paged_many_bytes() { return 2 * static_cast<size_t>(kMaxManyCtas) * kMany
 
 // 16-bit pages are copied as boxes of whole pages or 128 slots, by tensor maps
 // whose strides are below 2^40 bytes; the 8-bit cache is read element-wise.
-bool paged_many_serves(const PagedGeo& c) {
+bool paged_many_serves(const PagedGeo& c, int group) {
+  if (group > 16384) return false;
   if (c.kind == kKindQ8) return true;
   if (c.page_size < kKeys ? kKeys % c.page_size != 0 : c.page_size % kKeys != 0) return false;
   return c.page_stride < (int64_t(1) << 39) && c.token_stride < (int64_t(1) << 39) &&

@@ -58,6 +58,7 @@ struct PagedAttnParams {
   float* lse;
   int64_t q_tok, q_head;     // elements
   int32_t Hq, group;         // group = Hq / Hkv
+  uint32_t magic;            // floor(2^32 / group) + 1: divides small numbers by the group
   int32_t window, sinks;     // window 0: every earlier key
   float scale_log2;          // sm_scale * log2(e)
   int32_t q_vec;             // q rows in whole 16-byte vectors
@@ -70,7 +71,7 @@ cudaError_t launch_paged_few(const PagedAttnParams& p, bool bf16, int sms, cudaS
 size_t paged_few_bytes();
 cudaError_t launch_paged_many(const PagedAttnParams& p, bool bf16, int sms, cudaStream_t st);
 size_t paged_many_bytes();
-bool paged_many_serves(const PagedGeo& c);
+bool paged_many_serves(const PagedGeo& c, int group);
 
 #ifdef __CUDACC__
 // A sequence's first row, new tokens and cached length; false (and the status
