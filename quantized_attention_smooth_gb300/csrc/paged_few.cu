@@ -219,12 +219,13 @@ paged_few_kernel(const PagedAttnParams p) {
           }
           top = fmaxf(top, __shfl_xor_sync(kAll, top, 1));
           top = fmaxf(top, __shfl_xor_sync(kAll, top, 2));
-          const int e = top > 0.0f ? ilogbf(top) : 0;
+          const int e = exponent_of(top);
+          const float down = power_of_2(-e);
 #pragma unroll
           for (int i = 0; i < kDp / 8; ++i)
-            qw[nr][i] = pack2<false>(ldexpf(__uint_as_float(qw[nr][i] << 16), -e),
-                                     ldexpf(__uint_as_float(qw[nr][i] & 0xFFFF0000u), -e));
-          row_scale = ldexpf(row_scale, e);
+            qw[nr][i] = pack2<false>(__uint_as_float(qw[nr][i] << 16) * down,
+                                     __uint_as_float(qw[nr][i] & 0xFFFF0000u) * down);
+          row_scale *= power_of_2(e);
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {

@@ -72,20 +72,26 @@ struct Many {
   static constexpr int kThreads = kQ8 ? 512 : 384;
   static constexpr int kPanel = kTileRows * 128;               // 128 rows x 64 channels
   static constexpr int kTileBytes = kDp / 64 * kPanel;         // Q, K or V tile of 16 bits
-  static constexpr int kStages = kQ8 ? (kDp == 128 ? 4 : 8) : (kDp == 128 ? 5 : 10);
-  static constexpr int kScaleRing = 8;                         // key scales of 8 tiles
+  static constexpr int kStages = kQ8 ? (kDp == 128 ? 3 : 6) : (kDp == 128 ? 5 : 10);
+  // 8-bit cache: codes as they lie in the pages, a tile and its key scales a stage
+  static constexpr int kRawStages = kDp == 128 ? 3 : 6;
+  // (the scales of each copied page on 128 bytes, as a tensor copy needs them)
+  static constexpr int kRawBytes = kKeys * kDp + 1024;
+  static constexpr int kScaleRing = 4;                         // key scales of 4 tiles
   static constexpr int kRingOff = 2 * kTileBytes;
-  static constexpr int kScaleOff = kRingOff + kStages * kTileBytes;
+  static constexpr int kRawOff = kRingOff + kStages * kTileBytes;
+  static constexpr int kScaleOff = kRawOff + (kQ8 ? kRawStages * kRawBytes : 0);
   static constexpr int kBarOff = kScaleOff + (kQ8 ? kScaleRing * kKeys * 4 : 0);
   // full[stages], empty[stages], q_ready[2], s_full[2], p_ready[2], o_full[2], drain,
-  // item_full[items], item_empty[items]
+  // item_full[items], item_empty[items], raw_full[raw], raw_empty[raw]
   static constexpr int kItems = 4;
-  static constexpr int kNumBars = 2 * kStages + 9 + 2 * kItems;
+  static constexpr int kC = kQ8 ? 2 : 4;         // a softmax run's keys, in 32s (registers)
+  static constexpr int kNumBars = 2 * kStages + 9 + 2 * kItems + 2 * kRawStages;
   static constexpr int kMiscOff = (kBarOff + kNumBars * 8 + 15) / 16 * 16;
   static constexpr int kItemOff = kMiscOff + 256;
   static constexpr int kAlloc = kItemOff + kItems * 128;
-  // warps that take items: softmax, MMA, and what fills the ring
-  static constexpr int kTakers = 8 + 1 + (kQ8 ? 4 : 1);
+  // warps that take items: softmax, MMA, copies, and the 8-bit cache's widening
+  static constexpr int kTakers = 8 + 1 + 1 + (kQ8 ? 4 : 0);
   static_assert(kAlloc <= 227 * 1024, "shared memory of one CTA");
 };
 
@@ -142,6 +148,16 @@ struct Ring {
     }
   }
 };
+
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z,
+                                            uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];"
+      :: "r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z),
+         "r"(smem_u32(bar))
+      : "memory");
+}
 
 // The part of a (sequence, kv head, pair) that a CTA works on, as the scheduling
 // warp leaves it in shared memory for the other roles (registers that they
@@ -226,11 +242,12 @@ __device__ __forceinline__ uint32_t below(int x) {       // the x lowest bits
 template <int kKind, bool kQBF16, int kDp>
 __global__ void __launch_bounds__(kKind == kKindQ8 ? 512 : 384, 1)
 paged_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                  const PagedAttnParams p) {
+                  const __grid_constant__ CUtensorMap tm_s, const PagedAttnParams p) {
   using L = Many<kKind, kDp>;
   constexpr bool kQ8 = L::kQ8;
   constexpr bool kMmaBF16 = kKind == kKindBF16;
   constexpr int kStages = L::kStages;
+  constexpr int kC = L::kC;
   // The driver places dynamic shared memory behind its 1 KB reservation of a
   // block; a base off the swizzle's grid is reported and the CTA does nothing.
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -252,6 +269,8 @@ paged_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
   uint64_t* drain = o_full + 2;
   uint64_t* item_full = drain + 1;
   uint64_t* item_empty = item_full + L::kItems;
+  uint64_t* raw_full = item_empty + L::kItems;
+  uint64_t* raw_empty = raw_full + L::kRawStages;
   int* scan_s = reinterpret_cast<int*>(smem);     // the plan's; the queries come there later
   int64_t* sums_s = reinterpret_cast<int64_t*>(smem + L::kMiscOff);        // 16
   Walk* walk_s = reinterpret_cast<Walk*>(smem + L::kMiscOff + 128);
@@ -274,6 +293,10 @@ paged_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     for (int i = 0; i < L::kItems; ++i) {
       mbar_init(&item_full[i], 1);
       mbar_init(&item_empty[i], L::kTakers);
+    }
+    for (int i = 0; i < L::kRawStages; ++i) {
+      mbar_init(&raw_full[i], p.tensor_copies ? 1 : 32);
+      mbar_init(&raw_empty[i], 128);
     }
     mbar_fence_init();
   }
@@ -442,6 +465,126 @@ paged_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         }
         at.next();
       }
+    } else if (warp == 9 && kQ8 && p.tensor_copies) {
+      // ================================================== copies of codes, by the page
+      const int rows_box = min(c.page_size, kKeys), boxes = kKeys / rows_box;
+      Ring<L::kRawStages> ring;                 // K and V tiles alternate
+      int issued = 0;
+      bool ok = true;
+      for (Ring<L::kItems> at; ok && take(at); give_back(at), at.next()) {
+        const Item& it = item_at(at.at);
+        const int sinks = p.window > 0 ? p.sinks : 0;
+        const int count = it.count, head = it.head;
+        for (int i = 0; ok && i < count; ++i) {
+          const int key0 = it.key0(i);
+          int page = static_cast<int>(c.num_pages), slot = 0;
+          if (lane < boxes) {
+            const int k = key0 + lane * rows_box;
+            if (k <= it.p_hi && (k + rows_box - 1 >= it.lo || k < sinks)) {
+              const int pn = k / c.page_size;
+              const int pg = paged_page(c, it.s, pn);
+              if (pg >= 0) page = pg;           // else the copy lies outside and reads zeros
+              slot = k - pn * c.page_size;
+            }
+          }
+#pragma unroll
+          for (int kv = 0; kv < 2; ++kv) {
+            ok = __all_sync(kAll, mbar_wait(&raw_empty[ring.at], ring.parity ^ 1u, abort_flag,
+                                            c.status, p.timeout_ns));
+            if (!ok) break;
+            if (lane == 0)
+              mbar_expect_tx(&raw_full[ring.at], kKeys * kDp + (kv == 0 ? kKeys * 4 : 0));
+            __syncwarp();
+            if (lane < boxes) {
+              uint8_t* dst = smem + L::kRawOff + ring.at * L::kRawBytes;
+              tma_load_4d(dst + lane * rows_box * kDp, kv == 0 ? &tm_k : &tm_v, 0, slot, head,
+                          page, &raw_full[ring.at]);
+              if (kv == 0)
+                tma_load_3d(dst + kKeys * kDp + lane * max(rows_box * 4, 128), &tm_s, slot, head, page,
+                            &raw_full[ring.at]);
+            }
+            ring.next();
+            issued = min(issued + 1, L::kRawStages);
+          }
+        }
+      }
+      // no copy may still be in flight when the CTA exits
+      for (int i = 1; i <= issued; ++i) {
+        const int st = ring.at - i;             // below 0: in the round before
+        mbar_wait(&raw_full[st < 0 ? st + L::kRawStages : st],
+                  st < 0 ? ring.parity ^ 1u : ring.parity, nullptr, c.status, p.timeout_ns);
+      }
+    } else if (warp == 9 && kQ8) {
+      // ================================================== copies of codes, for rows
+      // and pages that tensor copies cannot take (D % 16 == 8, page sizes that
+      // neither divide nor are multiples of 128); five times slower
+      Ring<L::kRawStages> ring;                 // K and V tiles alternate
+      bool ok = true;
+      const bool wide = c.D % 16 == 0;          // rows start on 16 bytes, else on 8
+      const int shift = (kDp == 128 ? 3 : 2) + (wide ? 0 : 1);   // log2 of a row's lanes
+      const int width = wide ? 16 : 8, col = (lane & ((1 << shift) - 1)) * width;
+      const int step = 32 >> shift;
+      for (Ring<L::kItems> at; ok && take(at); give_back(at), at.next()) {
+        const Item& it = item_at(at.at);
+        const int sinks = p.window > 0 ? p.sinks : 0;
+        const int count = it.count, head = it.head, lo = it.lo, p_hi = it.p_hi;
+        for (int i = 0; ok && i < count; ++i) {
+          const int key0 = it.key0(i);
+          // lane b < 8 finds the page of keys 16 b .. 16 b + 15
+          int page = -1, slot = 0;
+          const int kb = key0 + 16 * (lane & 7);
+          if (lane < 8 && kb <= p_hi && (kb + 15 >= lo || kb < sinks)) {
+            const int pn = kb / c.page_size;
+            page = paged_page(c, it.s, pn);
+            slot = kb - pn * c.page_size;
+          }
+#pragma unroll
+          for (int kv = 0; kv < 2; ++kv) {
+            ok = __all_sync(kAll, mbar_wait(&raw_empty[ring.at], ring.parity ^ 1u, abort_flag,
+                                            c.status, p.timeout_ns));
+            if (!ok) break;
+            const uint32_t dst = smem_u32(smem + L::kRawOff + ring.at * L::kRawBytes);
+            const uint8_t* const codes = kv == 0 ? c.k : c.v;
+#pragma unroll 4
+            for (int r = lane >> shift; r < kKeys; r += step) {
+              const int pg = __shfl_sync(kAll, page, r / 16), sl = __shfl_sync(kAll, slot, r / 16);
+              const int key = key0 + r;
+              const bool see = pg >= 0 && col < c.D && key <= p_hi && (key >= lo || key < sinks);
+              const uint8_t* src = codes;       // not read unless seen
+              if (see)
+                src += pg * c.page_stride + (sl + (r & 15)) * c.token_stride +
+                       head * c.head_stride + col;
+              if (wide)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+                             :: "r"(dst + r * kDp + col), "l"(src), "r"(see ? 16 : 0) : "memory");
+              else
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;"
+                             :: "r"(dst + r * kDp + col), "l"(src), "r"(see ? 8 : 0) : "memory");
+            }
+            if (kv == 0) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const int r = lane + 32 * j;
+                const int pg = __shfl_sync(kAll, page, r / 16),
+                          sl = __shfl_sync(kAll, slot, r / 16);
+                const int key = key0 + r;
+                const bool see = pg >= 0 && key <= p_hi && (key >= lo || key < sinks);
+                const float* src = c.k_scale;
+                if (see)
+                  src += (static_cast<int64_t>(pg) * c.Hkv + head) * c.page_size + sl + (r & 15);
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;"
+                             :: "r"(dst + kKeys * kDp + 4 * r), "l"(src), "r"(see ? 4 : 0)
+                             : "memory");
+              }
+            }
+            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];"
+                         :: "r"(smem_u32(&raw_full[ring.at])) : "memory");
+            ring.next();
+          }
+        }
+      }
+      // no copy may still be in flight when the CTA exits
+      asm volatile("cp.async.wait_all;" ::: "memory");
     } else if (warp == 9 && !kQ8) {
       // ================================================== copies of K and V
       const int rows_box = min(c.page_size, kKeys), boxes = kKeys / rows_box;
@@ -627,79 +770,72 @@ paged_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
       regs_decrease<88>();
       constexpr int kRowLanes = kDp / 16;       // 16-byte vectors of a row
       constexpr int kIter = kKeys * kRowLanes / 128;
-      const int r0 = (tid - 384) / kRowLanes, ch = (tid - 384) % kRowLanes * 16;
-      const bool wide = c.D % 16 == 0;
-      float* scales = reinterpret_cast<float*>(smem + L::kScaleOff);
-      uint32_t w[kIter][4];
-      float ks[kIter];
-      const int sinks = p.window > 0 ? p.sinks : 0;
-      // loads K (kv = 0) or V of the item's i-th tile
-      auto load = [&](const Item& x, int i, int kv) {
-        const int key0 = x.key0(i);
-#pragma unroll
-        for (int j = 0; j < kIter; ++j) {
-          const int key = key0 + r0 + j * (128 / kRowLanes);
-          w[j][0] = w[j][1] = w[j][2] = w[j][3] = 0;
-          ks[j] = 0.0f;
-          if (key <= x.p_hi && (key >= x.lo || key < sinks)) {
-            const int page = paged_page(c, x.s, key / c.page_size);
-            if (page >= 0) {
-              const int slot = key % c.page_size;
-              ld16_q8(w[j], (kv == 0 ? c.k : c.v) + page * c.page_stride + slot * c.token_stride +
-                                x.head * c.head_stride, ch, c.D, wide);
-              if (kv == 0 && ch == 0)
-                ks[j] = c.k_scale[(static_cast<int64_t>(page) * c.Hkv + x.head) * c.page_size +
-                                  slot];
-            }
-          }
-        }
-      };
+      const int id = tid - 384, r0 = id / kRowLanes, ch = id % kRowLanes * 16;
+      float* const scales = reinterpret_cast<float*>(smem + L::kScaleOff);
+      const int box = p.tensor_copies ? min(c.page_size, kKeys) : kKeys;
+      const int scale_at = kKeys * kDp + id / box * max(4 * box, 128) + id % box * 4;
       Ring<kStages> ring;
-      Ring<L::kItems> at;
-      bool ok = true, have = take(at);
-      if (have) load(item_at(at.at), 0, 0);
-      while (ok && have) {
+      Ring<L::kRawStages> raw;
+      bool ok = true;
+      for (Ring<L::kItems> at; ok && take(at); give_back(at), at.next()) {
         const Item& it = item_at(at.at);
-        const int count = it.count, before = it.before;
-        Ring<L::kItems> nx = at;
-        nx.next();
+        const int count = it.count, before = it.before, lo = it.lo, p_hi = it.p_hi;
+        const int sinks = p.window > 0 ? p.sinks : 0;
         for (int i = 0; ok && i < count; ++i) {
+          const int key0 = it.key0(i);
+          const bool part =
+              !(key0 + kKeys - 1 <= p_hi && (key0 >= lo || key0 + kKeys - 1 < sinks));
 #pragma unroll
           for (int kv = 0; kv < 2; ++kv) {
-            ok = __all_sync(kAll, mbar_wait(&empty[ring.at], ring.parity ^ 1u, abort_flag,
-                                            c.status, p.timeout_ns));
+            ok = __all_sync(kAll, mbar_wait(&raw_full[raw.at], raw.parity, abort_flag, c.status,
+                                            p.timeout_ns) &&
+                                      mbar_wait(&empty[ring.at], ring.parity ^ 1u, abort_flag,
+                                                c.status, p.timeout_ns));
             if (!ok) break;
-            uint8_t* tile = smem + L::kRingOff + ring.at * L::kTileBytes + (ch / 64) * L::kPanel;
+            const uint8_t* const codes = smem + L::kRawOff + raw.at * L::kRawBytes;
+            uint8_t* const tile = smem + L::kRingOff + ring.at * L::kTileBytes +
+                                  (ch / 64) * L::kPanel;
+            uint4 w[kIter];
+#pragma unroll
+            for (int j = 0; j < kIter; ++j)
+              w[j] = *reinterpret_cast<const uint4*>(codes + (r0 + j * (128 / kRowLanes)) * kDp +
+                                                     ch);
+            if (kv == 1 && part) {              // values of keys that no row of the pair sees
+#pragma unroll
+              for (int j = 0; j < kIter; ++j) {
+                const int key = key0 + r0 + j * (128 / kRowLanes);
+                if (!(key <= p_hi && (key >= lo || key < sinks))) w[j] = make_uint4(0, 0, 0, 0);
+              }
+            }
+            if (kv == 0)
+              scales[(before + i) % L::kScaleRing * kKeys + id] =
+                  *reinterpret_cast<const float*>(codes + scale_at);
 #pragma unroll
             for (int j = 0; j < kIter; ++j) {
               const int r = r0 + j * (128 / kRowLanes);
+              const uint32_t u[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
               uint32_t h[8];
 #pragma unroll
               for (int q = 0; q < 4; ++q) {
                 if (kv == 0) {
-                  int8_to_half(w[j][q], h[2 * q], h[2 * q + 1]);
+                  int8_to_half(u[q], h[2 * q], h[2 * q + 1]);
                 } else {
-                  h[2 * q] = e4m3x2_to_half2(w[j][q]);
-                  h[2 * q + 1] = e4m3x2_to_half2(w[j][q] >> 16);
+                  h[2 * q] = e4m3x2_to_half2(u[q]);
+                  h[2 * q + 1] = e4m3x2_to_half2(u[q] >> 16);
                 }
               }
               const int q0 = (ch % 64) / 8;
               uint4* row = reinterpret_cast<uint4*>(tile + r * 128);
               row[q0 ^ (r & 7)] = make_uint4(h[0], h[1], h[2], h[3]);
               row[(q0 + 1) ^ (r & 7)] = make_uint4(h[4], h[5], h[6], h[7]);
-              if (kv == 0 && ch == 0) scales[(before + i) % L::kScaleRing * kKeys + r] = ks[j];
             }
             fence_proxy_async_smem();
             mbar_arrive(&full[ring.at]);
+            mbar_arrive(&raw_empty[raw.at]);
             ring.next();
-            // the next tile's loads run while the barriers turn
-            if (kv == 0) load(it, i, 1);
-            else if (i + 1 < count) load(it, i + 1, 0);
-            else if ((have = take(nx))) load(item_at(nx.at), 0, 0);
+            raw.next();
           }
         }
-        give_back(at);
-        at = nx;
       }
     }
   } else {
@@ -767,16 +903,17 @@ paged_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
 #pragma unroll
             for (int d = kVecs / 2; d > 0; d /= 2)
               top = fmaxf(top, __shfl_xor_sync(kAll, top, d));
-            const int ex = top > 0.0f ? ilogbf(top) : 0;
+            const int ex = exponent_of(top);
+            const float down = power_of_2(-ex);
             auto half2 = [&](uint32_t w2) {
-              return pack2<false>(ldexpf(__uint_as_float(w2 << 16), -ex),
-                                  ldexpf(__uint_as_float(w2 & 0xFFFF0000u), -ex));
+              return pack2<false>(__uint_as_float(w2 << 16) * down,
+                                  __uint_as_float(w2 & 0xFFFF0000u) * down);
             };
             v[j] = make_uint4(half2(u[0]), half2(u[1]), half2(u[2]), half2(u[3]));
 #pragma unroll
             for (int g = 0; g < kRowsAtOnce; ++g) {
               const int e = __shfl_sync(kAll, ex, g * kVecs);
-              if (lane == in_warp - sub + g) sc = ldexpf(p.scale_log2, e);
+              if (lane == in_warp - sub + g) sc = p.scale_log2 * power_of_2(e);
             }
           }
           const int row = (warp & 3) * 32 + in_warp;
@@ -817,17 +954,18 @@ paged_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         // there, as P is stored last.
         uint32_t w[64];
         float2 a01, a23;
-        auto logits = [&](uint32_t (&x)[4][32], auto masked_c) {
+        // logits of 32 kC keys from the key0-th on, without the factor sc
+        auto logits = [&](auto& x, int c0, auto masked_c) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q) tmem_ld32(ts + 32 * q, x[q]);
+          for (int q = 0; q < kC; ++q) tmem_ld32(ts + 32 * (c0 + q), x[q]);
           tmem_ld_wait();
 #pragma unroll
-          for (int q = 0; q < 4; ++q) reg_fence(x[q]);
+          for (int q = 0; q < kC; ++q) reg_fence(x[q]);
           if constexpr (kQ8) {
             const float4* ks = reinterpret_cast<const float4*>(
-                smem + L::kScaleOff + ((before + i) % L::kScaleRing) * kKeys * 4);
+                smem + L::kScaleOff + (((before + i) % L::kScaleRing) * kKeys + 32 * c0) * 4);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
+            for (int e = 0; e < 8 * kC; ++e) {
               const float4 k4 = ks[e];
               uint32_t* y = &x[e / 8][(e % 8) * 4];
               const float2 u = __fmul2_rn(make_float2(__uint_as_float(y[0]), __uint_as_float(y[1])),
@@ -841,12 +979,13 @@ paged_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             }
           }
           if constexpr (decltype(masked_c)::value) {
-            const int hi = pos + 1 - key0;                           // keys below: not later
-            const int lo = p.window > 0 ? pos - p.window + 1 - key0 : 0;   // below: too early
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const uint32_t early = below(lo - 32 * q) & ~below(sinks - key0 - 32 * q);
-              const uint32_t see = below(hi - 32 * q) & ~early;
+            for (int q = 0; q < kC; ++q) {
+              const int k = key0 + 32 * (c0 + q);
+              const int hi = pos + 1 - k;                            // keys below: not later
+              const int lo = p.window > 0 ? pos - p.window + 1 - k : 0;   // below: too early
+              const uint32_t early = below(lo) & ~below(sinks - k);
+              const uint32_t see = below(hi) & ~early;
 #pragma unroll
               for (int e = 0; e < 32; ++e)
                 if (!((see >> e) & 1u)) x[q][e] = 0xFF800000u;       // -inf
@@ -854,28 +993,31 @@ paged_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
           }
         };
         auto weigh = [&](auto masked_c) {
-          uint32_t x[4][32];
-          logits(x, masked_c);
           const float safe = ref == -INFINITY ? 0.0f : ref;
           const float2 sc2 = make_float2(sc, sc), nm2 = make_float2(-safe, -safe);
           a01 = make_float2(0.0f, 0.0f);
           a23 = make_float2(0.0f, 0.0f);
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const uint32_t* y = &x[e / 8][(e % 8) * 4];
+          for (int c0 = 0; c0 < 4; c0 += kC) {
+            uint32_t x[kC][32];
+            logits(x, c0, masked_c);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], __uint_as_float(y[k]));
-            const float2 d01 = __ffma2_rn(
-                make_float2(__uint_as_float(y[0]), __uint_as_float(y[1])), sc2, nm2);
-            const float2 d23 = __ffma2_rn(
-                make_float2(__uint_as_float(y[2]), __uint_as_float(y[3])), sc2, nm2);
-            const float2 p01 = make_float2(fast_exp2(d01.x), fast_exp2(d01.y));
-            const float2 p23 = make_float2(fast_exp2(d23.x), fast_exp2(d23.y));
-            w[2 * e] = pack2<kMmaBF16>(p01.x, p01.y);
-            w[2 * e + 1] = pack2<kMmaBF16>(p23.x, p23.y);
-            a01 = __fadd2_rn(a01, p01);
-            a23 = __fadd2_rn(a23, p23);
+            for (int e = 0; e < 8 * kC; ++e) {
+              const uint32_t* y = &x[e / 8][(e % 8) * 4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], __uint_as_float(y[k]));
+              const float2 d01 = __ffma2_rn(
+                  make_float2(__uint_as_float(y[0]), __uint_as_float(y[1])), sc2, nm2);
+              const float2 d23 = __ffma2_rn(
+                  make_float2(__uint_as_float(y[2]), __uint_as_float(y[3])), sc2, nm2);
+              const float2 p01 = make_float2(fast_exp2(d01.x), fast_exp2(d01.y));
+              const float2 p23 = make_float2(fast_exp2(d23.x), fast_exp2(d23.y));
+              w[16 * c0 + 2 * e] = pack2<kMmaBF16>(p01.x, p01.y);
+              w[16 * c0 + 2 * e + 1] = pack2<kMmaBF16>(p23.x, p23.y);
+              a01 = __fadd2_rn(a01, p01);
+              a23 = __fadd2_rn(a23, p23);
+            }
           }
           return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
         };
@@ -1091,6 +1233,14 @@ paged_many_join_kernel(const PagedAttnParams p, int ctas) {
                                         : -INFINITY;
 }
 
+// Whether pages are whole boxes of a 128-key tile, or hold whole tiles, with
+// strides that a tensor map takes (below 2^40 bytes).
+bool page_boxes(const PagedGeo& c) {
+  if (c.page_size < kKeys ? kKeys % c.page_size != 0 : c.page_size % kKeys != 0) return false;
+  return c.page_stride < (int64_t(1) << 39) && c.token_stride < (int64_t(1) << 39) &&
+         c.head_stride < (int64_t(1) << 39);
+}
+
 template <int kKind, bool kQBF16, int kDp>
 cudaError_t launch_many(const PagedAttnParams& p, int sms, cudaStream_t st) {
   using L = Many<kKind, kDp>;
@@ -1105,21 +1255,35 @@ cudaError_t launch_many(const PagedAttnParams& p, int sms, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     configured[dev].store(true, std::memory_order_relaxed);
   }
-  CUtensorMap mk{}, mv{};
-  if constexpr (kKind != kKindQ8) {
-    const PagedGeo& c = p.c;
+  CUtensorMap mk{}, mv{}, ms{};
+  PagedAttnParams prm = p;
+  const PagedGeo& c = p.c;
+  const uint64_t el = kKind == kKindQ8 ? 1 : 2;                // bytes of an element
+  prm.tensor_copies = kKind != kKindQ8 || (page_boxes(c) && c.D % 16 == 0 &&
+                                           c.page_stride % 16 == 0 && c.token_stride % 16 == 0 &&
+                                           c.head_stride % 16 == 0);
+  if (prm.tensor_copies) {
     const uint64_t dims[4] = {static_cast<uint64_t>(c.D), static_cast<uint64_t>(c.page_size),
                               static_cast<uint64_t>(c.Hkv), static_cast<uint64_t>(c.num_pages)};
-    const uint64_t strides[3] = {static_cast<uint64_t>(c.token_stride) * 2,
-                                 static_cast<uint64_t>(c.head_stride) * 2,
-                                 static_cast<uint64_t>(c.page_stride) * 2};
-    const uint32_t box[4] = {64, static_cast<uint32_t>(c.page_size < kKeys ? c.page_size : kKeys),
-                             1, 1};
-    if (!encode_tiled(&mk, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, c.k, dims, strides, box,
-                      CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !encode_tiled(&mv, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, c.v, dims, strides, box,
-                      CU_TENSOR_MAP_SWIZZLE_128B))
-      return cudaErrorInvalidValue;
+    const uint64_t strides[3] = {static_cast<uint64_t>(c.token_stride) * el,
+                                 static_cast<uint64_t>(c.head_stride) * el,
+                                 static_cast<uint64_t>(c.page_stride) * el};
+    const uint32_t rows = static_cast<uint32_t>(c.page_size < kKeys ? c.page_size : kKeys);
+    const uint32_t box[4] = {kKind == kKindQ8 ? static_cast<uint32_t>(kDp) : 64u, rows, 1, 1};
+    const CUtensorMapDataType type =
+        kKind == kKindQ8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    const CUtensorMapSwizzle swizzle =
+        kKind == kKindQ8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B;
+    bool made = encode_tiled(&mk, type, 4, c.k, dims, strides, box, swizzle) &&
+                encode_tiled(&mv, type, 4, c.v, dims, strides, box, swizzle);
+    if (made && kKind == kKindQ8) {
+      const uint64_t sdims[3] = {dims[1], dims[2], dims[3]};
+      const uint64_t sstrides[2] = {dims[1] * 4, dims[1] * dims[2] * 4};
+      const uint32_t sbox[3] = {rows, 1, 1};
+      made = encode_tiled(&ms, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, c.k_scale, sdims, sstrides,
+                          sbox, CU_TENSOR_MAP_SWIZZLE_NONE);
+    }
+    if (!made) return cudaErrorInvalidValue;
   }
   // one CTA per SM, and no more than the units of the lengths the call declares
   const int64_t pairs = (static_cast<int64_t>(p.c.max_q) * p.group + kPairRows - 1) / kPairRows;
@@ -1127,7 +1291,7 @@ cudaError_t launch_many(const PagedAttnParams& p, int sms, cudaStream_t st) {
                        ((static_cast<int64_t>(p.c.max_kv) + kKeys - 1) / kKeys + 1);
   int ctas = sms < kMaxManyCtas ? sms : kMaxManyCtas;
   if (most < ctas) ctas = static_cast<int>(most);
-  kern<<<ctas, L::kThreads, L::kAlloc, st>>>(mk, mv, p);
+  kern<<<ctas, L::kThreads, L::kAlloc, st>>>(mk, mv, ms, prm);
   note_launch();
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
@@ -1155,14 +1319,11 @@ cudaError_t launch_many_dim(const PagedAttnParams& p, int sms, cudaStream_t st) 
 
 size_t paged_many_bytes() { return 2 * static_cast<size_t>(kMaxManyCtas) * kManyPartBytes; }
 
-// 16-bit pages are copied as boxes of whole pages or 128 slots, by tensor maps
-// whose strides are below 2^40 bytes; the 8-bit cache is read element-wise.
+// 16-bit pages are copied as boxes of whole pages or 128 slots, by tensor maps;
+// codes of 8 bits need not be.
 bool paged_many_serves(const PagedGeo& c, int group) {
   if (group > 16384) return false;
-  if (c.kind == kKindQ8) return true;
-  if (c.page_size < kKeys ? kKeys % c.page_size != 0 : c.page_size % kKeys != 0) return false;
-  return c.page_stride < (int64_t(1) << 39) && c.token_stride < (int64_t(1) << 39) &&
-         c.head_stride < (int64_t(1) << 39);
+  return c.kind == kKindQ8 || page_boxes(c);
 }
 
 cudaError_t launch_paged_many(const PagedAttnParams& p, bool bf16, int sms, cudaStream_t st) {

@@ -62,6 +62,7 @@ struct PagedAttnParams {
   int32_t window, sinks;     // window 0: every earlier key
   float scale_log2;          // sm_scale * log2(e)
   int32_t q_vec;             // q rows in whole 16-byte vectors
+  int32_t tensor_copies;     // the 8-bit cache's pages go by tensor copies (set by the launcher)
   int32_t min_rows, max_rows;  // rows (tokens x group) of the sequences a launch serves
   uint8_t* parts;            // split results (workspace)
   uint64_t timeout_ns;

@@ -40,6 +40,16 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   }
 }
 
+// The exponent of |x|, within -126..126 (zero and subnormal numbers: -126), so
+// that 2^e and 2^-e are both normal; and 2^e.
+__device__ __forceinline__ int exponent_of(float x) {
+  const int e = static_cast<int>((__float_as_uint(x) >> 23) & 255u) - 127;
+  return e < -126 ? -126 : e > 126 ? 126 : e;
+}
+__device__ __forceinline__ float power_of_2(int e) {
+  return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+}
+
 // Four int8 codes of a word as two fp16 pairs, exactly: the byte n + 128 under
 // 0x64 is the fp16 number 1024 + n + 128.
 __device__ __forceinline__ void int8_to_half(uint32_t w, uint32_t& lo, uint32_t& hi) {
