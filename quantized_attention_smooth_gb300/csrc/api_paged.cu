@@ -134,6 +134,7 @@ sage_status paged_geo(const sage_paged_cache* cache, const sage_paged_batch* b, 
   g->Dp = cache->D <= 64 ? 64 : 128;
   g->page_size = static_cast<int32_t>(cache->page_size);
   g->kind = kind;
+  g->page_shift = (g->page_size & (g->page_size - 1)) == 0 ? __builtin_ctz(g->page_size) : -1;
   g->cu_q = b->cu_q;
   g->kv_lens = b->kv_lens;
   g->table = b->block_table;

@@ -41,7 +41,7 @@ constexpr unsigned kAll = 0xFFFFFFFFu;
 
 // One part of a split item (in the workspace).
 struct PartHead {
-  int32_t used, seq, head, tile, last, pad[3];
+  int32_t parts, seq, head, tile;   // parts of the item from this one on; 0: none here
 };
 constexpr int kMaxRows = 16;
 constexpr size_t kPartBytes = sizeof(PartHead) + kMaxRows * 8 + kMaxRows * 128 * 4;
@@ -89,8 +89,9 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
   return d;
 }
 
-template <int kKind, bool kQBF16, int kDp, int kNr>
-__global__ void __launch_bounds__(kThreads)
+// kWide: rows of the 8-bit cache start on 16 bytes (D % 16 == 0), else on 8.
+template <int kKind, bool kQBF16, int kDp, int kNr, bool kWide>
+__global__ void __launch_bounds__(kThreads, kNr == 1 ? (kDp == 128 ? 3 : 4) : (kDp == 128 ? 2 : 3))
 paged_few_kernel(const PagedAttnParams p) {
   constexpr bool kQ8 = kKind == kKindQ8;
   constexpr bool kMmaBF16 = kKind == kKindBF16;
@@ -159,8 +160,6 @@ paged_few_kernel(const PagedAttnParams p) {
     __syncthreads();
     int s = seq_s;
     int64_t off = off_s;
-    const bool wide = !kQ8 || c.D % 16 == 0;
-
     for (int64_t cur = u0; cur < u1 && s < c.nseq;) {
       int start, n, len;
       const Units un = units_of<kRows, kUnitBlocks>(p, s, &start, &n, &len);
@@ -181,6 +180,10 @@ paged_few_kernel(const PagedAttnParams p) {
       const int sinks = p.window > 0 ? p.sinks : 0;
       const int lo = p.window > 0 ? max(0, p_lo - p.window + 1) : 0;        // first key of row0
       const int lo_hi = p.window > 0 ? max(0, p_hi - p.window + 1) : 0;     // of the last row
+
+      const int32_t* const table = c.table + s * c.table_stride;
+      const int64_t head_off = kvh * c.head_stride;
+      const int64_t k_off = g * c.token_stride, v_off = 2 * t * c.token_stride;
 
       // ---- the rows' queries, as the B operand of S^T
       uint32_t qw[kNr][kDp / 8];
@@ -248,52 +251,69 @@ paged_few_kernel(const PagedAttnParams p) {
 
       uint32_t kw[kKb][2][kKw], vw[kKb][4][kVw];
       float ks[kKb][2];
-      int key0[kKb], page[kKb];
-      // a step's blocks and their pages; key0 = -1: past the last block
-      auto locate = [&](int unit, int (&k0)[kKb], int (&pg)[kKb]) {
+      // a step's blocks: first key (-1: none), the table's entry, and where the
+      // block's keys lie in the cache (elements; -1: nothing to read)
+      int key0[kKb], next_key0[kKb], next_page[kKb];
+      auto locate = [&](int unit) {
 #pragma unroll
         for (int b = 0; b < kKb; ++b) {
           const int vb = (unit * kWarps + warp) * kKb + b;
-          const int blk = vb < sp.sink ? vb : vb - sp.sink + sp.from;
-          k0[b] = vb < sp.count ? 16 * blk : -1;
-          pg[b] = -1;
-          if (k0[b] >= 0 && k0[b] <= p_hi && (k0[b] + 15 >= lo || k0[b] < sinks))
-            pg[b] = paged_page(c, s, k0[b] / c.page_size);
-          else
-            k0[b] = -1;
+          const int k0 = 16 * (vb < sp.sink ? vb : vb - sp.sink + sp.from);
+          next_key0[b] = -1;
+          next_page[b] = -1;
+          if (vb < sp.count && k0 <= p_hi && (k0 + 15 >= lo || k0 < sinks)) {
+            next_key0[b] = k0;
+            next_page[b] = table[page_of(c, k0)];          // used a step later
+          }
+        }
+      };
+      int64_t at[kKb], scale_at[kKb];
+      bool whole[kKb];
+      auto resolve = [&]() {
+#pragma unroll
+        for (int b = 0; b < kKb; ++b) {
+          const int k0 = next_key0[b], pg = next_page[b];
+          key0[b] = k0;
+          at[b] = -1;
+          whole[b] = k0 + 15 <= p_hi && (k0 >= lo || k0 + 15 < sinks);
+          if (k0 >= 0) {
+            if (static_cast<uint32_t>(pg) < static_cast<uint32_t>(c.num_pages)) {
+              const int slot = k0 - page_of(c, k0) * c.page_size;
+              at[b] = pg * c.page_stride + slot * c.token_stride + head_off;
+              if (kQ8) scale_at[b] = (static_cast<int64_t>(pg) * c.Hkv + kvh) * c.page_size + slot;
+            } else if (lane == 0) {
+              atomicOr(c.status, kStatusBadPage);
+            }
+          }
         }
       };
       auto seen = [&](int j) { return j <= p_hi && (j >= lo || j < sinks); };
-      auto load_k = [&](const int (&k0)[kKb], const int (&pg)[kKb]) {
+      auto load_k = [&]() {
 #pragma unroll
         for (int b = 0; b < kKb; ++b) {
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
-            const int j = k0[b] + g + 8 * y;
 #pragma unroll
             for (int i = 0; i < kKw; ++i) kw[b][y][i] = 0;
             if (kQ8) ks[b][y] = 0.0f;
-            if (pg[b] >= 0 && seen(j)) {
-              const int slot = k0[b] % c.page_size + g + 8 * y;
-              const int64_t at = pg[b] * c.page_stride + slot * c.token_stride +
-                                 kvh * c.head_stride;
+            if (at[b] >= 0 && (whole[b] || seen(key0[b] + g + 8 * y))) {
+              const int64_t row = at[b] + k_off + 8 * y * c.token_stride;
               if constexpr (kQ8) {
 #pragma unroll
                 for (int i = 0; i < kDp / 64; ++i)
-                  ld16_q8(&kw[b][y][4 * i], c.k + at, 64 * i + 16 * t, c.D, wide);
-                ks[b][y] = c.k_scale[(static_cast<int64_t>(pg[b]) * c.Hkv + kvh) * c.page_size +
-                                     slot];
+                  ld16_q8<kWide>(&kw[b][y][4 * i], c.k + row, 64 * i + 16 * t, c.D);
+                ks[b][y] = c.k_scale[scale_at[b] + g + 8 * y];
               } else {
 #pragma unroll
                 for (int i = 0; i < kDp / 32; ++i)
                   if (32 * i + 8 * t < c.D)
-                    ld16(&kw[b][y][4 * i], c.k + 2 * (at + 32 * i + 8 * t));
+                    ld16(&kw[b][y][4 * i], c.k + 2 * (row + 32 * i + 8 * t));
               }
             }
           }
         }
       };
-      auto load_v = [&](const int (&k0)[kKb], const int (&pg)[kKb]) {
+      auto load_v = [&]() {
 #pragma unroll
         for (int b = 0; b < kKb; ++b) {
 #pragma unroll
@@ -301,38 +321,39 @@ paged_few_kernel(const PagedAttnParams p) {
             const int in = 2 * t + (y & 1) + 8 * (y >> 1);
 #pragma unroll
             for (int i = 0; i < kVw; ++i) vw[b][y][i] = 0;
-            if (pg[b] >= 0 && seen(k0[b] + in)) {
-              const int64_t at = pg[b] * c.page_stride +
-                                 (k0[b] % c.page_size + in) * c.token_stride +
-                                 kvh * c.head_stride;
+            if (at[b] >= 0 && (whole[b] || seen(key0[b] + in))) {
+              const int64_t row = at[b] + v_off + ((y & 1) + 8 * (y >> 1)) * c.token_stride;
               if constexpr (kQ8 && kDp == 128) {
-                ld16_q8(vw[b][y], c.v + at, 16 * g, c.D, wide);
+                ld16_q8<kWide>(vw[b][y], c.v + row, 16 * g, c.D);
               } else if constexpr (kQ8) {
-                if (8 * g < c.D) ld8(vw[b][y], c.v + at + 8 * g);
+                if (8 * g < c.D) ld8(vw[b][y], c.v + row + 8 * g);
               } else {
 #pragma unroll
                 for (int i = 0; i < kDp / 64; ++i)
                   if (64 * i + 8 * g < c.D)
-                    ld16(&vw[b][y][4 * i], c.v + 2 * (at + 64 * i + 8 * g));
+                    ld16(&vw[b][y][4 * i], c.v + 2 * (row + 64 * i + 8 * g));
               }
             }
           }
         }
       };
 
-      locate(first_unit, key0, page);
-      load_k(key0, page);
-      load_v(key0, page);
+      locate(first_unit);
+      resolve();
+      load_k();
+      load_v();
+      if (count > 1) locate(first_unit + 1);
       for (int u = first_unit; u < first_unit + count; ++u) {
-        int nkey0[kKb], npage[kKb];
         const bool more = u + 1 < first_unit + count;
-        if (more) locate(u + 1, nkey0, npage);
         // ---- S^T
+        int cur0[kKb];
+#pragma unroll
+        for (int b = 0; b < kKb; ++b) cur0[b] = key0[b];
         float x[kKb][kNr][4];
         bool any = false;
 #pragma unroll
         for (int b = 0; b < kKb; ++b) {
-          any |= key0[b] >= 0;
+          any |= cur0[b] >= 0;
 #pragma unroll
           for (int nr = 0; nr < kNr; ++nr) x[b][nr][0] = x[b][nr][1] = x[b][nr][2] = x[b][nr][3] = 0.0f;
 #pragma unroll
@@ -358,7 +379,11 @@ paged_few_kernel(const PagedAttnParams p) {
             sc[b][1] = ks[b][1];
           }
         }
-        if (more) load_k(nkey0, npage);
+        if (more) {
+          resolve();
+          load_k();
+          if (u + 2 < first_unit + count) locate(u + 2);
+        }
         if (any) {
           // ---- logits, masks, running maximum and sum
           float mx[kNr][2];
@@ -366,8 +391,8 @@ paged_few_kernel(const PagedAttnParams p) {
           for (int nr = 0; nr < kNr; ++nr) mx[nr][0] = mx[nr][1] = -INFINITY;
 #pragma unroll
           for (int b = 0; b < kKb; ++b) {
-            const bool full = key0[b] >= 0 && key0[b] + 15 <= p_lo &&
-                              (key0[b] >= lo_hi || key0[b] + 15 < sinks);
+            const bool full = cur0[b] >= 0 && cur0[b] + 15 <= p_lo &&
+                              (cur0[b] >= lo_hi || cur0[b] + 15 < sinks);
 #pragma unroll
             for (int nr = 0; nr < kNr; ++nr)
 #pragma unroll
@@ -375,9 +400,9 @@ paged_few_kernel(const PagedAttnParams p) {
                 float v = x[b][nr][e] * rs[nr][e & 1];
                 if constexpr (kQ8) v *= sc[b][e >> 1];
                 if (!full) {
-                  const int j = key0[b] + g + 8 * (e >> 1);
+                  const int j = cur0[b] + g + 8 * (e >> 1);
                   const int pos = rpos[nr][e & 1];
-                  const bool see = key0[b] >= 0 && j <= pos &&
+                  const bool see = cur0[b] >= 0 && j <= pos &&
                                    (p.window <= 0 || j > pos - p.window || j < sinks);
                   v = see ? v : -INFINITY;
                 }
@@ -450,14 +475,7 @@ paged_few_kernel(const PagedAttnParams p) {
             }
           }
         }
-        if (more) {
-          load_v(nkey0, npage);
-#pragma unroll
-          for (int b = 0; b < kKb; ++b) {
-            key0[b] = nkey0[b];
-            page[b] = npage[b];
-          }
-        }
+        if (more) load_v();
       }
 
       // ---- join the warps
@@ -486,22 +504,19 @@ paged_few_kernel(const PagedAttnParams p) {
             acc_s[warp][(8 * nr + 2 * t + (e & 1)) * kPitch + ch] = o[j][nr][e];
           }
       __syncthreads();
-      const bool whole = first_unit == 0 && count == un.per;
+      const bool alone = first_unit == 0 && count == un.per;
       const int which = first_unit == 0 ? 1 : 0;
       uint8_t* part = part_at(p.parts, cta, which);
       float* part_m = reinterpret_cast<float*>(part + sizeof(PartHead));
       float* part_l = part_m + kMaxRows;
       float* part_o = part_l + kMaxRows;
-      if (!whole) {
+      if (!alone) {
         used[which] = true;
         if (tid == 0) {
-          PartHead h{};
-          h.used = 1;
-          h.seq = s;
-          h.head = kvh;
-          h.tile = tile;
-          h.last = first_unit + count == un.per;
-          *reinterpret_cast<PartHead*>(part) = h;
+          // the CTA that holds the item's last unit: CTA i's range begins at total i / busy
+          const int64_t last = cur - first_unit + un.per - 1;
+          const int end_cta = static_cast<int>(((last + 1) * busy - 1) / total);
+          *reinterpret_cast<PartHead*>(part) = PartHead{end_cta - cta + 1, s, kvh, tile};
         }
       }
       for (int i = tid; i < kRows * (kDp / 4); i += kThreads) {
@@ -519,7 +534,7 @@ paged_few_kernel(const PagedAttnParams p) {
           const float4 v = *reinterpret_cast<const float4*>(&acc_s[w][r * kPitch + ch]);
           a.x += f * v.x; a.y += f * v.y; a.z += f * v.z; a.w += f * v.w;
         }
-        if (!whole) {
+        if (!alone) {
           *reinterpret_cast<float4*>(part_o + r * kDp + ch) = a;
           if (ch == 0) {
             part_m[r] = top;
@@ -549,7 +564,7 @@ paged_few_kernel(const PagedAttnParams p) {
     }
   }
   if (tid < 2 && !used[tid])
-    reinterpret_cast<PartHead*>(part_at(p.parts, cta, tid))->used = 0;
+    reinterpret_cast<PartHead*>(part_at(p.parts, cta, tid))->parts = 0;
 }
 
 // Joins the parts of one row of the item that begins in CTA blockIdx.x and
@@ -562,19 +577,12 @@ paged_join_kernel(const PagedAttnParams p, int ctas) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int c0 = blockIdx.x, r = blockIdx.y, tid = threadIdx.x;
   const PartHead h = *reinterpret_cast<const PartHead*>(part_at(p.parts, c0, 1));
-  if (!h.used) return;
+  const int parts = min(h.parts, ctas - c0);
+  if (parts <= 0) return;
   int start, n, len;
   if (!paged_seq(p.c, h.seq, &start, &n, &len)) return;
   const int rr = h.tile * kRows + r;
   if (rr >= n * p.group) return;
-  // the parts: CTA c0's second, then the first ones of the CTAs behind it up to the last
-  int parts = 1;
-  while (c0 + parts < ctas) {
-    const PartHead* q = reinterpret_cast<const PartHead*>(part_at(p.parts, c0 + parts, 0));
-    if (!q->used) break;
-    ++parts;
-    if (q->last) break;
-  }
   float top = -INFINITY;
   for (int i = tid; i < parts; i += 128) {
     const float v = reinterpret_cast<const float*>(part_at(p.parts, c0 + i, i == 0) +
@@ -618,9 +626,11 @@ paged_join_kernel(const PagedAttnParams p, int ctas) {
                                         : -INFINITY;
 }
 
-template <int kKind, bool kQBF16, int kDp, int kNr>
+template <int kKind, bool kQBF16, int kDp, int kNr, bool kWide = true>
 cudaError_t launch_few(const PagedAttnParams& p, int sms, cudaStream_t st) {
-  auto* kern = paged_few_kernel<kKind, kQBF16, kDp, kNr>;
+  if (kWide && kKind == kKindQ8 && p.c.D % 16 != 0)
+    return launch_few<kKind, kQBF16, kDp, kNr, kKind != kKindQ8>(p, sms, st);
+  auto* kern = paged_few_kernel<kKind, kQBF16, kDp, kNr, kWide>;
   static std::atomic<int> resident{0};       // CTAs of one SM (every GB300 is alike)
   int per = resident.load(std::memory_order_relaxed);
   if (per == 0) {

@@ -57,7 +57,8 @@ constexpr int kItemUnits = 2;
 constexpr float kLazy = 8.0f;             // log2 of the growth that rescales O
 
 struct ManyHead {
-  int32_t used, seq, head, pair, last, pad[59];
+  int32_t parts, seq, head, pair;   // parts of the item from this one on; 0: none here
+  int32_t pad[60];
 };
 constexpr size_t kManyPartBytes = sizeof(ManyHead) + 2 * kPairRows * 4 + kPairRows * 128 * 4;
 static_assert(sizeof(ManyHead) == 256, "parts stay 256-byte aligned");
@@ -170,6 +171,7 @@ struct Item {
   int first, count, per;     // key tiles: from, how many (0: no more items), of how many
   int sink, from;            // Span
   int before;                // key tiles of the CTA's earlier items
+  int parts;                 // CTAs from this one on that work on the pair
   struct {
     int lo, hi;              // positions of the tile's first and last row
     int tok, off;            // its first row's token, and query head within the group
@@ -203,7 +205,8 @@ __device__ __forceinline__ Span pair_span(const PagedAttnParams& p, int base, in
 // next one.
 struct Walk {
   int s, pair, head, unit;
-  int64_t left;
+  int64_t left, at, all;     // units left; where it stands in all units
+  int busy;                  // CTAs that share them
 };
 
 // x / group for a row's x < group + 256, by a multiplication: exact while
@@ -303,7 +306,7 @@ paged_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
   if (warp == 8) tmem_alloc(tmem_slot, kTmemCols);
 
   // ---- this CTA's range of units: pairs per sequence, then tiles per pair
-  Walk walk{0, 0, 0, 0, 0};
+  Walk walk{0, 0, 0, 0, 0, 0, 0, 0};
   {
     constexpr int T = L::kThreads;
     const int spt = (c.nseq + T - 1) / T;
@@ -366,7 +369,7 @@ paged_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
           return false;
         }
         *walk_s = Walk{s, pair, static_cast<int>(off / per), static_cast<int>(off % per),
-                       u1 - u0};
+                       u1 - u0, u0, all, static_cast<int>(busy)};
         return true;
       });
     }
@@ -402,7 +405,7 @@ paged_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
       Span span{0, 0, 0};
       bool fresh = true;
       while (ok && more) {
-        int first = 0, count = 0;
+        int first = 0, count = 0, parts = 0;
         while (count <= 0 && walk.left > 0 && walk.s < c.nseq) {
           if (fresh || walk.head == 0) {        // a new pair
             if (((fresh || walk.pair == 0) && !served(p, walk.s, &start, &n, &len, &rows)) ||
@@ -417,7 +420,11 @@ paged_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
           first = max(0, walk.unit - kItemUnits);
           const int64_t upto = walk.unit + walk.left - kItemUnits;   // tiles before the end
           count = static_cast<int>(min(static_cast<int64_t>(span.count), upto)) - first;
-          walk.left -= span.count + kItemUnits - walk.unit;
+          const int rest = span.count + kItemUnits - walk.unit;
+          // the CTA with the item's last unit: CTA i's range begins at all * i / busy
+          parts = static_cast<int>(((walk.at + rest) * walk.busy - 1) / walk.all) - cta + 1;
+          walk.at += rest;
+          walk.left -= rest;
           walk.unit = 0;
           if (count <= 0 && ++walk.head == c.Hkv) {
             walk.head = 0;
@@ -445,6 +452,7 @@ paged_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             x.sink = span.sink;
             x.from = span.from;
             x.before = tiles;
+            x.parts = parts;
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
               const int row0 = walk.pair * kPairRows + t * kTileRows;
@@ -481,7 +489,7 @@ paged_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
           if (lane < boxes) {
             const int k = key0 + lane * rows_box;
             if (k <= it.p_hi && (k + rows_box - 1 >= it.lo || k < sinks)) {
-              const int pn = k / c.page_size;
+              const int pn = page_of(c, k);
               const int pg = paged_page(c, it.s, pn);
               if (pg >= 0) page = pg;           // else the copy lies outside and reads zeros
               slot = k - pn * c.page_size;
@@ -534,7 +542,7 @@ paged_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
           int page = -1, slot = 0;
           const int kb = key0 + 16 * (lane & 7);
           if (lane < 8 && kb <= p_hi && (kb + 15 >= lo || kb < sinks)) {
-            const int pn = kb / c.page_size;
+            const int pn = page_of(c, kb);
             page = paged_page(c, it.s, pn);
             slot = kb - pn * c.page_size;
           }
@@ -602,9 +610,9 @@ paged_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
           if (lane < boxes) {
             const int k = key0 + lane * rows_box;
             if (k <= it.p_hi && (k + rows_box - 1 >= it.lo || k < sinks)) {
-              const int pg = paged_page(c, it.s, k / c.page_size);
+              const int pg = paged_page(c, it.s, page_of(c, k));
               if (pg >= 0) page = pg;           // else the copy lies outside and reads zeros
-              slot = k % c.page_size;
+              slot = k - page_of(c, k) * c.page_size;
             }
           }
 #pragma unroll
@@ -1123,11 +1131,10 @@ paged_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         used[which] = true;
         if (t == 0 && r == 0) {
           ManyHead* h = reinterpret_cast<ManyHead*>(part);
-          h->used = 1;
+          h->parts = it.parts;
           h->seq = it.s;
           h->head = it.head;
           h->pair = it.pair;
-          h->last = it.first + it.count == it.per;
         }
         const int row = t * kTileRows + r;
         float* ml = reinterpret_cast<float*>(part + sizeof(ManyHead));
@@ -1155,7 +1162,7 @@ paged_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     if (tid == 0) {
 #pragma unroll
       for (int w = 0; w < 2; ++w)
-        if (!used[w]) reinterpret_cast<ManyHead*>(many_part(p.parts, cta, w))->used = 0;
+        if (!used[w]) reinterpret_cast<ManyHead*>(many_part(p.parts, cta, w))->parts = 0;
     }
   }
 
@@ -1178,18 +1185,12 @@ paged_many_join_kernel(const PagedAttnParams p, int ctas) {
   const int c0 = blockIdx.x;
   const int row = blockIdx.y * 32 + (threadIdx.x & 31), grp = threadIdx.x >> 5;
   const ManyHead* h = reinterpret_cast<const ManyHead*>(many_part(p.parts, c0, 1));
-  if (!h->used) return;
+  const int parts = min(h->parts, ctas - c0);
+  if (parts <= 0) return;
   int start, n, len;
   if (!paged_seq(p.c, h->seq, &start, &n, &len)) return;
   const int rows = n * p.group, rr = h->pair * kPairRows + row;
   if (rr >= rows) return;
-  int parts = 1;
-  while (c0 + parts < ctas) {
-    const ManyHead* q = reinterpret_cast<const ManyHead*>(many_part(p.parts, c0 + parts, 0));
-    if (!q->used) break;
-    ++parts;
-    if (q->last) break;
-  }
   auto ml = [&](int i) {
     return reinterpret_cast<const float*>(many_part(p.parts, c0 + i, i == 0) + sizeof(ManyHead));
   };

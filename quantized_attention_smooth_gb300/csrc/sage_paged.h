@@ -20,6 +20,7 @@ struct PagedGeo {
   int64_t num_pages;
   int64_t page_stride, token_stride, head_stride;   // elements
   int32_t Hkv, D, Dp, page_size, kind;
+  int32_t page_shift;        // log2(page_size), or -1
   const int32_t* cu_q;
   const int32_t* kv_lens;
   const int32_t* table;

@@ -78,14 +78,20 @@ __device__ __forceinline__ void ld8(uint32_t* w, const uint8_t* p) {
                : "=r"(w[0]), "=r"(w[1]) : "l"(p));
 }
 // 16 channels of 8 bits at channel ch of a D-channel row: rows of the cache
-// start on 8 bytes at least, on 16 when D % 16 == 0 (wide).
-__device__ __forceinline__ void ld16_q8(uint32_t* w, const uint8_t* row, int ch, int D, bool wide) {
-  if (wide) {
+// start on 8 bytes at least, on 16 when D % 16 == 0 (kWide).
+template <bool kWide>
+__device__ __forceinline__ void ld16_q8(uint32_t* w, const uint8_t* row, int ch, int D) {
+  if constexpr (kWide) {
     if (ch < D) ld16(w, row + ch);
   } else {
     if (ch < D) ld8(w, row + ch);
     if (ch + 8 < D) ld8(w + 2, row + ch + 8);
   }
+}
+
+// The page slot of a key: a shift where the page size is a power of two.
+__device__ __forceinline__ int page_of(const PagedGeo& c, int key) {
+  return c.page_shift >= 0 ? key >> c.page_shift : key / c.page_size;
 }
 
 }  // namespace sage
