@@ -16,8 +16,7 @@
 // block's loads are in flight during the present block's arithmetic.  S^T's
 // accumulators become P^T's operands by an 8x8 register transpose.
 //
-// Work is cut into units of 4 warps x 16 keys (32 of the 8-bit cache) and
-// dealt evenly to a fixed grid: every CTA derives its own contiguous range
+// Work is cut into units of 4 warps x 16 keys and dealt evenly to a fixed grid: every CTA derives its own contiguous range
 // from the lengths (a scan over the sequences), so ragged batches balance and
 // no length comes to the host.  A (sequence, head) that spans CTAs leaves fp32
 // parts (max, sum, O) in the workspace, two per CTA at most; a second kernel
@@ -91,13 +90,13 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
 
 // kWide: rows of the 8-bit cache start on 16 bytes (D % 16 == 0), else on 8.
 template <int kKind, bool kQBF16, int kDp, int kNr, bool kWide>
-__global__ void __launch_bounds__(kThreads, kNr == 1 ? (kDp == 128 ? 3 : 4) : (kDp == 128 ? 2 : 3))
+__global__ void __launch_bounds__(kThreads, kNr == 1 ? (kKind == kKindQ8 || kDp == 64 ? 4 : 3) : (kDp == 128 ? 2 : 3))
 paged_few_kernel(const PagedAttnParams p) {
   constexpr bool kQ8 = kKind == kKindQ8;
   constexpr bool kMmaBF16 = kKind == kKindBF16;
   constexpr int kRows = 8 * kNr;
-  constexpr int kKb = kQ8 ? 2 : 1;                        // 16-key blocks of a warp's step
-  constexpr int kUnitBlocks = kWarps * kKb;
+  constexpr int kUnitBlocks = kWarps;                     // a unit: a block of each warp
+  constexpr int kEl = kQ8 ? 1 : 2;                        // bytes of an element
   constexpr int kKw = kQ8 ? kDp / 16 : kDp / 8;           // words of a key per lane
   constexpr int kVw = kQ8 ? kDp / 32 : kDp / 16;          // words of a value per lane
   constexpr int kSteps = kDp / 16;                        // k-steps of S^T
@@ -113,6 +112,7 @@ paged_few_kernel(const PagedAttnParams p) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t = lane & 3;
   const int cta = blockIdx.x, ctas = gridDim.x;
+  const int64_t ts = c.token_stride * kEl;
   asm volatile("griddepcontrol.launch_dependents;");
 
   // ---- this CTA's range of units
@@ -182,8 +182,10 @@ paged_few_kernel(const PagedAttnParams p) {
       const int lo_hi = p.window > 0 ? max(0, p_hi - p.window + 1) : 0;     // of the last row
 
       const int32_t* const table = c.table + s * c.table_stride;
-      const int64_t head_off = kvh * c.head_stride;
-      const int64_t k_off = g * c.token_stride, v_off = 2 * t * c.token_stride;
+      // this lane's place in a block's keys and values (bytes)
+      const uint8_t* const k_lane = c.k + (kvh * c.head_stride + g * c.token_stride) * kEl + 16 * t;
+      const uint8_t* const v_lane = c.v + (kvh * c.head_stride + 2 * t * c.token_stride) * kEl +
+                                    (kVw == 2 ? 8 : 16) * g;
 
       // ---- the rows' queries, as the B operand of S^T
       uint32_t qw[kNr][kDp / 8];
@@ -249,90 +251,92 @@ paged_few_kernel(const PagedAttnParams p) {
           for (int e = 0; e < 4; ++e) o[j][nr][e] = 0.0f;
       }
 
-      uint32_t kw[kKb][2][kKw], vw[kKb][4][kVw];
-      float ks[kKb][2];
-      // a step's blocks: first key (-1: none), the table's entry, and where the
-      // block's keys lie in the cache (elements; -1: nothing to read)
-      int key0[kKb], next_key0[kKb], next_page[kKb];
+      uint32_t kw[2][kKw], vw[4][kVw];
+      float ks[2] = {0.0f, 0.0f};
+      // A step is a block of 16 keys: its first key (-1: none), the table's entry,
+      // and where the block's keys begin in the head (bytes; -1: nothing to read).
+      int key0 = -1, next_key0 = -1, next_page = -1;
+      int64_t at = -1, scale_at = 0;
+      bool whole = false;                       // some row sees every key of the block
       auto locate = [&](int unit) {
-#pragma unroll
-        for (int b = 0; b < kKb; ++b) {
-          const int vb = (unit * kWarps + warp) * kKb + b;
-          const int k0 = 16 * (vb < sp.sink ? vb : vb - sp.sink + sp.from);
-          next_key0[b] = -1;
-          next_page[b] = -1;
-          if (vb < sp.count && k0 <= p_hi && (k0 + 15 >= lo || k0 < sinks)) {
-            next_key0[b] = k0;
-            next_page[b] = table[page_of(c, k0)];          // used a step later
-          }
+        const int vb = unit * kWarps + warp;
+        const int k0 = 16 * (vb < sp.sink ? vb : vb - sp.sink + sp.from);
+        next_key0 = next_page = -1;
+        if (vb < sp.count && k0 <= p_hi && (k0 + 15 >= lo || k0 < sinks)) {
+          next_key0 = k0;
+          next_page = table[page_of(c, k0)];    // used a step later
         }
       };
-      int64_t at[kKb], scale_at[kKb];
-      bool whole[kKb];
       auto resolve = [&]() {
-#pragma unroll
-        for (int b = 0; b < kKb; ++b) {
-          const int k0 = next_key0[b], pg = next_page[b];
-          key0[b] = k0;
-          at[b] = -1;
-          whole[b] = k0 + 15 <= p_hi && (k0 >= lo || k0 + 15 < sinks);
-          if (k0 >= 0) {
-            if (static_cast<uint32_t>(pg) < static_cast<uint32_t>(c.num_pages)) {
-              const int slot = k0 - page_of(c, k0) * c.page_size;
-              at[b] = pg * c.page_stride + slot * c.token_stride + head_off;
-              if (kQ8) scale_at[b] = (static_cast<int64_t>(pg) * c.Hkv + kvh) * c.page_size + slot;
-            } else if (lane == 0) {
-              atomicOr(c.status, kStatusBadPage);
-            }
+        key0 = next_key0;
+        at = -1;
+        whole = false;
+        if (key0 >= 0) {
+          if (static_cast<uint32_t>(next_page) < static_cast<uint32_t>(c.num_pages)) {
+            const int slot = key0 - page_of(c, key0) * c.page_size;
+            at = (next_page * c.page_stride + static_cast<int64_t>(slot) * c.token_stride) * kEl;
+            if (kQ8)
+              scale_at = (static_cast<int64_t>(next_page) * c.Hkv + kvh) * c.page_size + slot + g;
+            whole = c.D == kDp && key0 + 15 <= p_hi && (key0 >= lo || key0 + 15 < sinks);
+          } else if (lane == 0) {
+            atomicOr(c.status, kStatusBadPage);
           }
         }
       };
       auto seen = [&](int j) { return j <= p_hi && (j >= lo || j < sinks); };
       auto load_k = [&]() {
+        const uint8_t* const row = k_lane + at;
+        if (whole) {
 #pragma unroll
-        for (int b = 0; b < kKb; ++b) {
+          for (int y = 0; y < 2; ++y)
 #pragma unroll
-          for (int y = 0; y < 2; ++y) {
+            for (int i = 0; i < kKw / 4; ++i)
+              ld16_row<kQ8 && !kWide>(&kw[y][4 * i], row + y * 8 * ts + 64 * i);
+          if constexpr (kQ8) {
+            ks[0] = c.k_scale[scale_at];
+            ks[1] = c.k_scale[scale_at + 8];
+          }
+          return;
+        }
 #pragma unroll
-            for (int i = 0; i < kKw; ++i) kw[b][y][i] = 0;
-            if (kQ8) ks[b][y] = 0.0f;
-            if (at[b] >= 0 && (whole[b] || seen(key0[b] + g + 8 * y))) {
-              const int64_t row = at[b] + k_off + 8 * y * c.token_stride;
-              if constexpr (kQ8) {
+        for (int y = 0; y < 2; ++y) {
 #pragma unroll
-                for (int i = 0; i < kDp / 64; ++i)
-                  ld16_q8<kWide>(&kw[b][y][4 * i], c.k + row, 64 * i + 16 * t, c.D);
-                ks[b][y] = c.k_scale[scale_at[b] + g + 8 * y];
-              } else {
+          for (int i = 0; i < kKw; ++i) kw[y][i] = 0;
+          ks[y] = 0.0f;
+          if (at >= 0 && seen(key0 + g + 8 * y)) {
 #pragma unroll
-                for (int i = 0; i < kDp / 32; ++i)
-                  if (32 * i + 8 * t < c.D)
-                    ld16(&kw[b][y][4 * i], c.k + 2 * (row + 32 * i + 8 * t));
-              }
-            }
+            for (int i = 0; i < kKw / 4; ++i)
+              ld16_part<kEl, kQ8 && !kWide>(&kw[y][4 * i], row + y * 8 * ts + 64 * i,
+                                            c.D - (64 * i + 16 * t) / kEl);
+            if constexpr (kQ8) ks[y] = c.k_scale[scale_at + 8 * y];
           }
         }
       };
       auto load_v = [&]() {
+        const uint8_t* const row = v_lane + at;
 #pragma unroll
-        for (int b = 0; b < kKb; ++b) {
+        for (int y = 0; y < 4; ++y) {
+          const uint8_t* const r = row + ((y & 1) + 8 * (y >> 1)) * ts;
+          if (whole) {
+            if constexpr (kVw == 2) {
+              ld8(vw[y], r);
+            } else {
 #pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            const int in = 2 * t + (y & 1) + 8 * (y >> 1);
+              for (int i = 0; i < kVw / 4; ++i)
+                ld16_row<kQ8 && !kWide>(&vw[y][4 * i], r + 128 * i);
+            }
+            continue;
+          }
 #pragma unroll
-            for (int i = 0; i < kVw; ++i) vw[b][y][i] = 0;
-            if (at[b] >= 0 && (whole[b] || seen(key0[b] + in))) {
-              const int64_t row = at[b] + v_off + ((y & 1) + 8 * (y >> 1)) * c.token_stride;
-              if constexpr (kQ8 && kDp == 128) {
-                ld16_q8<kWide>(vw[b][y], c.v + row, 16 * g, c.D);
-              } else if constexpr (kQ8) {
-                if (8 * g < c.D) ld8(vw[b][y], c.v + row + 8 * g);
-              } else {
+          for (int i = 0; i < kVw; ++i) vw[y][i] = 0;
+          if (at >= 0 && seen(key0 + 2 * t + (y & 1) + 8 * (y >> 1))) {
+            if constexpr (kVw == 2) {
+              if (8 * g < c.D) ld8(vw[y], r);
+            } else {
 #pragma unroll
-                for (int i = 0; i < kDp / 64; ++i)
-                  if (64 * i + 8 * g < c.D)
-                    ld16(&vw[b][y][4 * i], c.v + 2 * (row + 64 * i + 8 * g));
-              }
+              for (int i = 0; i < kVw / 4; ++i)
+                ld16_part<kEl, kQ8 && !kWide>(&vw[y][4 * i], r + 128 * i,
+                                              c.D - (128 * i + 16 * g) / kEl);
             }
           }
         }
@@ -345,78 +349,58 @@ paged_few_kernel(const PagedAttnParams p) {
       if (count > 1) locate(first_unit + 1);
       for (int u = first_unit; u < first_unit + count; ++u) {
         const bool more = u + 1 < first_unit + count;
-        // ---- S^T
-        int cur0[kKb];
+        // ---- S^T, in two chains of products
+        const int cur0 = key0;
+        float x[kNr][4], x2[kNr][4];
 #pragma unroll
-        for (int b = 0; b < kKb; ++b) cur0[b] = key0[b];
-        float x[kKb][kNr][4];
-        bool any = false;
+        for (int nr = 0; nr < kNr; ++nr)
 #pragma unroll
-        for (int b = 0; b < kKb; ++b) {
-          any |= cur0[b] >= 0;
+          for (int e = 0; e < 4; ++e) x[nr][e] = x2[nr][e] = 0.0f;
 #pragma unroll
-          for (int nr = 0; nr < kNr; ++nr) x[b][nr][0] = x[b][nr][1] = x[b][nr][2] = x[b][nr][3] = 0.0f;
-#pragma unroll
-          for (int i = 0; i < kSteps; ++i) {
-            uint32_t a0, a1, a2, a3;
-            if constexpr (kQ8) {
-              int8_to_half(kw[b][0][i], a0, a2);
-              int8_to_half(kw[b][1][i], a1, a3);
-            } else {
-              a0 = kw[b][0][2 * i]; a2 = kw[b][0][2 * i + 1];
-              a1 = kw[b][1][2 * i]; a3 = kw[b][1][2 * i + 1];
-            }
-#pragma unroll
-            for (int nr = 0; nr < kNr; ++nr)
-              mma<kMmaBF16>(x[b][nr], a0, a1, a2, a3, qw[nr][2 * i], qw[nr][2 * i + 1]);
+        for (int i = 0; i < kSteps; ++i) {
+          uint32_t a0, a1, a2, a3;
+          if constexpr (kQ8) {
+            int8_to_half(kw[0][i], a0, a2);
+            int8_to_half(kw[1][i], a1, a3);
+          } else {
+            a0 = kw[0][2 * i]; a2 = kw[0][2 * i + 1];
+            a1 = kw[1][2 * i]; a3 = kw[1][2 * i + 1];
           }
-        }
-        float sc[kKb][2];
-        if constexpr (kQ8) {
 #pragma unroll
-          for (int b = 0; b < kKb; ++b) {
-            sc[b][0] = ks[b][0];
-            sc[b][1] = ks[b][1];
-          }
+          for (int nr = 0; nr < kNr; ++nr)
+            mma<kMmaBF16>((i & 1) ? x2[nr] : x[nr], a0, a1, a2, a3, qw[nr][2 * i],
+                          qw[nr][2 * i + 1]);
         }
+        const float s0 = kQ8 ? ks[0] : 1.0f, s1 = kQ8 ? ks[1] : 1.0f;
         if (more) {
           resolve();
           load_k();
           if (u + 2 < first_unit + count) locate(u + 2);
         }
-        if (any) {
+        if (cur0 >= 0) {
           // ---- logits, masks, running maximum and sum
-          float mx[kNr][2];
-#pragma unroll
-          for (int nr = 0; nr < kNr; ++nr) mx[nr][0] = mx[nr][1] = -INFINITY;
-#pragma unroll
-          for (int b = 0; b < kKb; ++b) {
-            const bool full = cur0[b] >= 0 && cur0[b] + 15 <= p_lo &&
-                              (cur0[b] >= lo_hi || cur0[b] + 15 < sinks);
-#pragma unroll
-            for (int nr = 0; nr < kNr; ++nr)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                float v = x[b][nr][e] * rs[nr][e & 1];
-                if constexpr (kQ8) v *= sc[b][e >> 1];
-                if (!full) {
-                  const int j = cur0[b] + g + 8 * (e >> 1);
-                  const int pos = rpos[nr][e & 1];
-                  const bool see = cur0[b] >= 0 && j <= pos &&
-                                   (p.window <= 0 || j > pos - p.window || j < sinks);
-                  v = see ? v : -INFINITY;
-                }
-                x[b][nr][e] = v;
-                mx[nr][e & 1] = fmaxf(mx[nr][e & 1], v);
-              }
-          }
-          float alpha[kNr][2];
+          const bool full =
+              cur0 + 15 <= p_lo && (cur0 >= lo_hi || cur0 + 15 < sinks);
+          float mx[kNr][2], alpha[kNr][2];
           bool grew = false;
 #pragma unroll
-          for (int nr = 0; nr < kNr; ++nr)
+          for (int nr = 0; nr < kNr; ++nr) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              float v = (x[nr][e] + x2[nr][e]) * rs[nr][e & 1];
+              if constexpr (kQ8) v *= (e >> 1) ? s1 : s0;
+              if (!full) {
+                const int j = cur0 + g + 8 * (e >> 1);
+                const int pos = rpos[nr][e & 1];
+                const bool see =
+                    j <= pos && (p.window <= 0 || j > pos - p.window || j < sinks);
+                v = see ? v : -INFINITY;
+              }
+              x[nr][e] = v;
+            }
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              float v = mx[nr][i];
+              float v = fmaxf(x[nr][i], x[nr][i + 2]);
               v = fmaxf(v, __shfl_xor_sync(kAll, v, 4));
               v = fmaxf(v, __shfl_xor_sync(kAll, v, 8));
               v = fmaxf(v, __shfl_xor_sync(kAll, v, 16));
@@ -428,6 +412,7 @@ paged_few_kernel(const PagedAttnParams p) {
               mx[nr][i] = safe;
               l[nr][i] *= alpha[nr][i];
             }
+          }
           if (__any_sync(kAll, grew)) {
 #pragma unroll
             for (int j = 0; j < kMt; ++j)
@@ -437,41 +422,50 @@ paged_few_kernel(const PagedAttnParams p) {
                 for (int e = 0; e < 4; ++e) o[j][nr][e] *= alpha[nr][e & 1];
           }
           // ---- P^T and O^T
+          uint32_t pb[kNr][2];
 #pragma unroll
-          for (int b = 0; b < kKb; ++b) {
-            uint32_t pb[kNr][2];
+          for (int nr = 0; nr < kNr; ++nr) {
+            float e4[4];
 #pragma unroll
-            for (int nr = 0; nr < kNr; ++nr) {
-              float e4[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                e4[e] = fast_exp2(x[b][nr][e] - mx[nr][e & 1]);
-                l[nr][e & 1] += e4[e];
-              }
-              pb[nr][0] = transpose8x8(pack2<kMmaBF16>(e4[0], e4[1]));
-              pb[nr][1] = transpose8x8(pack2<kMmaBF16>(e4[2], e4[3]));
+            for (int e = 0; e < 4; ++e) {
+              e4[e] = fast_exp2(x[nr][e] - mx[nr][e & 1]);
+              l[nr][e & 1] += e4[e];
             }
+            pb[nr][0] = transpose8x8(pack2<kMmaBF16>(e4[0], e4[1]));
+            pb[nr][1] = transpose8x8(pack2<kMmaBF16>(e4[2], e4[3]));
+          }
+          // operands of O^T's j-th tile: a0, a1 of keys 2t, 2t + 1 and the tile's two
+          // halves of channels, a2, a3 of the keys 8 further
+          auto product = [&](int j, const uint32_t (&a)[4]) {
+#pragma unroll
+            for (int nr = 0; nr < kNr; ++nr)
+              mma<kMmaBF16>(o[j][nr], a[0], a[1], a[2], a[3], pb[nr][0], pb[nr][1]);
+          };
+          if constexpr (kQ8) {
+#pragma unroll
+            for (int j = 0; j < kMt; j += 2) {          // two bytes of a word at a time
+              uint32_t a[2][4];
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                const int y = 2 * (q >> 1), word = (kDp == 128 ? 2 : 1) * (q & 1) + j / 4;
+                const uint32_t two = __byte_perm(vw[y][word], vw[y + 1][word],
+                                                 (j & 2) ? 0x7362 : 0x5140);
+                a[0][q] = e4m3x2_to_half2(two);
+                a[1][q] = e4m3x2_to_half2(two >> 16);
+              }
+              product(j, a[0]);
+              product(j + 1, a[1]);
+            }
+          } else {
 #pragma unroll
             for (int j = 0; j < kMt; ++j) {
               uint32_t a[4];
 #pragma unroll
-              for (int q = 0; q < 4; ++q) {               // a0, a1: keys 2t, 2t+1; a2, a3: +8
-                const int y = 2 * (q >> 1), hi = q & 1;
-                if constexpr (kQ8) {
-                  const int word = (kDp == 128 ? 2 : 1) * hi + j / 4;
-                  const uint32_t two = __byte_perm(vw[b][y][word], vw[b][y + 1][word],
-                                                   (j & 3) == 0 ? 0x40 : (j & 3) == 1 ? 0x51
-                                                   : (j & 3) == 2 ? 0x62 : 0x73);
-                  a[q] = e4m3x2_to_half2(two);
-                } else {
-                  const int word = (kDp == 128 ? 4 : 2) * hi + j / 2;
-                  a[q] = __byte_perm(vw[b][y][word], vw[b][y + 1][word],
-                                     (j & 1) ? 0x7632 : 0x5410);
-                }
+              for (int q = 0; q < 4; ++q) {
+                const int y = 2 * (q >> 1), word = (kDp == 128 ? 4 : 2) * (q & 1) + j / 2;
+                a[q] = __byte_perm(vw[y][word], vw[y + 1][word], (j & 1) ? 0x7632 : 0x5410);
               }
-#pragma unroll
-              for (int nr = 0; nr < kNr; ++nr)
-                mma<kMmaBF16>(o[j][nr], a[0], a[1], a[2], a[3], pb[nr][0], pb[nr][1]);
+              product(j, a);
             }
           }
         }
@@ -640,7 +634,7 @@ cudaError_t launch_few(const PagedAttnParams& p, int sms, cudaStream_t st) {
     resident.store(per, std::memory_order_relaxed);
   }
   // at most one CTA per unit of the longest lengths the call declares
-  constexpr int kUnitKeys = 16 * kWarps * (kKind == kKindQ8 ? 2 : 1);
+  constexpr int kUnitKeys = 16 * kWarps;
   const int64_t max_units = (static_cast<int64_t>(p.c.max_kv) + kUnitKeys - 1) / kUnitKeys + 1;
   const int64_t tiles = (static_cast<int64_t>(p.c.max_q) * p.group + 8 * kNr - 1) / (8 * kNr);
   const int64_t items = tiles * p.c.Hkv * p.c.nseq;

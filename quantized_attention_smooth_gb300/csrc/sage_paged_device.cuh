@@ -77,15 +77,25 @@ __device__ __forceinline__ void ld8(uint32_t* w, const uint8_t* p) {
   asm volatile("ld.global.L1::no_allocate.L2::128B.v2.u32 {%0,%1}, [%2];"
                : "=r"(w[0]), "=r"(w[1]) : "l"(p));
 }
-// 16 channels of 8 bits at channel ch of a D-channel row: rows of the cache
-// start on 8 bytes at least, on 16 when D % 16 == 0 (kWide).
-template <bool kWide>
-__device__ __forceinline__ void ld16_q8(uint32_t* w, const uint8_t* row, int ch, int D) {
-  if constexpr (kWide) {
-    if (ch < D) ld16(w, row + ch);
+// 16 bytes of a row of the cache: in halves where rows of 8 bits start on 8 bytes
+// only (kHalves: D % 16 == 8).
+template <bool kHalves>
+__device__ __forceinline__ void ld16_row(uint32_t* w, const uint8_t* p) {
+  if constexpr (kHalves) {
+    ld8(w, p);
+    ld8(w + 2, p + 8);
   } else {
-    if (ch < D) ld8(w, row + ch);
-    if (ch + 8 < D) ld8(w + 2, row + ch + 8);
+    ld16(w, p);
+  }
+}
+// The same of a row that ends after `left` more elements of kEl bytes.
+template <int kEl, bool kHalves>
+__device__ __forceinline__ void ld16_part(uint32_t* w, const uint8_t* p, int left) {
+  if constexpr (kHalves) {
+    if (left > 0) ld8(w, p);
+    if (left > 8) ld8(w + 2, p + 8);
+  } else {
+    if (left > 0) ld16(w, p);
   }
 }
 
