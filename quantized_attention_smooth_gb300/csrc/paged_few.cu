@@ -88,6 +88,16 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
   return d;
 }
 
+// The part of a (sequence, kv head, row tile) that a CTA is at, and where it
+// stands in its range of units: in shared memory, since registers that kept it
+// through the loop over the keys would cost the loop spills.
+struct FewItem {
+  int64_t cur, off, last, total;   // unit; unit within the sequence; past the range; all
+  int busy;                        // CTAs that share them
+  int s, start, rows, base, head, tile, first, count, per;
+  Span span;
+};
+
 // kWide: rows of the 8-bit cache start on 16 bytes (D % 16 == 0), else on 8.
 template <int kKind, bool kQBF16, int kDp, int kNr, bool kWide>
 __global__ void __launch_bounds__(kThreads, kNr == 1 ? (kKind == kKindQ8 || kDp == 64 ? 4 : 3) : (kDp == 128 ? 2 : 3))
@@ -103,8 +113,7 @@ paged_few_kernel(const PagedAttnParams p) {
   constexpr int kMt = kDp / 16;                           // 16-channel tiles of O^T
   constexpr int kPitch = kDp + 4;
   __shared__ int64_t scan_s[kWarps];
-  __shared__ int64_t off_s;
-  __shared__ int seq_s;
+  __shared__ FewItem it;
   __shared__ float m_s[kWarps][kRows], l_s[kWarps][kRows];
   __shared__ __align__(16) float acc_s[kWarps][kRows * kPitch];
 
@@ -154,29 +163,47 @@ paged_few_kernel(const PagedAttnParams p) {
         if (off < w) break;
         off -= w;
       }
-      seq_s = s;
-      off_s = off;
+      it.s = s;
+      it.off = off;
+      it.cur = u0;
+      it.last = u1;
+      it.total = total;
+      it.busy = static_cast<int>(busy);
     }
     __syncthreads();
-    int s = seq_s;
-    int64_t off = off_s;
-    for (int64_t cur = u0; cur < u1 && s < c.nseq;) {
-      int start, n, len;
-      const Units un = units_of<kRows, kUnitBlocks>(p, s, &start, &n, &len);
-      if (off >= un.total) {                              // an empty sequence
-        off = 0;
-        ++s;
-        continue;
+    while (true) {
+      if (tid == 0) {
+        it.count = 0;
+        while (it.cur < it.last && it.s < c.nseq) {
+          int start, n, len;
+          const Units un = units_of<kRows, kUnitBlocks>(p, it.s, &start, &n, &len);
+          if (it.off >= un.total) {                       // an empty sequence
+            it.off = 0;
+            ++it.s;
+            continue;
+          }
+          const int64_t item = it.off / un.per;
+          it.first = static_cast<int>(it.off - item * un.per);
+          it.count = static_cast<int>(
+              min(static_cast<int64_t>(un.per - it.first), it.last - it.cur));
+          it.per = un.per;
+          it.head = static_cast<int>(item / un.tiles);
+          it.tile = static_cast<int>(item - static_cast<int64_t>(it.head) * un.tiles);
+          it.start = start;
+          it.rows = n * p.group;
+          it.base = len - n;
+          it.span = span_of<16>(len - n, len - 1, p.window, p.sinks);
+          break;
+        }
       }
-      const int64_t item = off / un.per;
-      const int first_unit = static_cast<int>(off - item * un.per);
-      const int count = static_cast<int>(min(static_cast<int64_t>(un.per - first_unit), u1 - cur));
-      const int kvh = static_cast<int>(item / un.tiles), tile = static_cast<int>(item % un.tiles);
-      const int rows = n * p.group;
-      const int row0 = tile * kRows;
-      const int p_lo = len - n + row0 / p.group;
-      const int p_hi = len - n + (min(row0 + kRows, rows) - 1) / p.group;
-      const Span sp = span_of<16>(len - n, len - 1, p.window, p.sinks);
+      __syncthreads();
+      const int count = it.count, first_unit = it.first;
+      if (count == 0) break;
+      const int row0 = it.tile * kRows;
+      const int kvh = it.head, s = it.s;
+      const Span sp = it.span;
+      const int p_lo = it.base + row0 / p.group;
+      const int p_hi = it.base + (min(row0 + kRows, it.rows) - 1) / p.group;
       const int sinks = p.window > 0 ? p.sinks : 0;
       const int lo = p.window > 0 ? max(0, p_lo - p.window + 1) : 0;        // first key of row0
       const int lo_hi = p.window > 0 ? max(0, p_hi - p.window + 1) : 0;     // of the last row
@@ -194,8 +221,8 @@ paged_few_kernel(const PagedAttnParams p) {
 #pragma unroll
       for (int nr = 0; nr < kNr; ++nr) {
         const int r = row0 + 8 * nr + g;
-        const bool has = r < rows;
-        const uint16_t* qrow = p.q + (static_cast<int64_t>(start) + r / p.group) * p.q_tok +
+        const bool has = r < it.rows;
+        const uint16_t* qrow = p.q + (static_cast<int64_t>(it.start) + r / p.group) * p.q_tok +
                                (static_cast<int64_t>(kvh) * p.group + r % p.group) * p.q_head;
 #pragma unroll
         for (int i = 0; i < kDp / 32; ++i) {
@@ -236,7 +263,7 @@ paged_few_kernel(const PagedAttnParams p) {
         for (int i = 0; i < 2; ++i) {
           rs[nr][i] = __shfl_sync(kAll, row_scale, (2 * t + i) * 4);
           const int rr = row0 + 8 * nr + 2 * t + i;
-          rpos[nr][i] = rr < rows ? len - n + rr / p.group : -1;
+          rpos[nr][i] = rr < it.rows ? it.base + rr / p.group : -1;
         }
       }
 
@@ -498,8 +525,8 @@ paged_few_kernel(const PagedAttnParams p) {
             acc_s[warp][(8 * nr + 2 * t + (e & 1)) * kPitch + ch] = o[j][nr][e];
           }
       __syncthreads();
-      const bool alone = first_unit == 0 && count == un.per;
-      const int which = first_unit == 0 ? 1 : 0;
+      const bool alone = it.first == 0 && it.count == it.per;
+      const int which = it.first == 0 ? 1 : 0;
       uint8_t* part = part_at(p.parts, cta, which);
       float* part_m = reinterpret_cast<float*>(part + sizeof(PartHead));
       float* part_l = part_m + kMaxRows;
@@ -508,9 +535,10 @@ paged_few_kernel(const PagedAttnParams p) {
         used[which] = true;
         if (tid == 0) {
           // the CTA that holds the item's last unit: CTA i's range begins at total i / busy
-          const int64_t last = cur - first_unit + un.per - 1;
-          const int end_cta = static_cast<int>(((last + 1) * busy - 1) / total);
-          *reinterpret_cast<PartHead*>(part) = PartHead{end_cta - cta + 1, s, kvh, tile};
+          const int64_t beyond = it.cur - it.first + it.per;
+          const int end_cta = static_cast<int>((beyond * it.busy - 1) / it.total);
+          *reinterpret_cast<PartHead*>(part) =
+              PartHead{end_cta - cta + 1, it.s, it.head, it.tile};
         }
       }
       for (int i = tid; i < kRows * (kDp / 4); i += kThreads) {
@@ -536,14 +564,14 @@ paged_few_kernel(const PagedAttnParams p) {
           }
           continue;
         }
-        const int rr = row0 + r;
-        if (rr >= rows || ch >= c.D) continue;
-        const int64_t tok = static_cast<int64_t>(start) + rr / p.group;
-        const int h = kvh * p.group + rr % p.group;
+        const int rr = it.tile * kRows + r;
+        if (rr >= it.rows || ch >= c.D) continue;
+        const int64_t tok = static_cast<int64_t>(it.start) + rr / p.group;
+        const int h = it.head * p.group + rr % p.group;
         const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
         a.x *= inv; a.y *= inv; a.z *= inv; a.w *= inv;
         if constexpr (kQ8) {
-          const float4 sv = *reinterpret_cast<const float4*>(c.v_scale + kvh * kDp + ch);
+          const float4 sv = *reinterpret_cast<const float4*>(c.v_scale + it.head * kDp + ch);
           a.x *= sv.x; a.y *= sv.y; a.z *= sv.z; a.w *= sv.w;
         }
         *reinterpret_cast<uint2*>(p.out + (tok * p.Hq + h) * c.D + ch) =
@@ -553,8 +581,10 @@ paged_few_kernel(const PagedAttnParams p) {
                                              : -INFINITY;
       }
       __syncthreads();
-      cur += count;
-      off += count;
+      if (tid == 0) {
+        it.cur += it.count;
+        it.off += it.count;
+      }
     }
   }
   if (tid < 2 && !used[tid])
