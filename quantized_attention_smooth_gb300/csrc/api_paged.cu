@@ -16,10 +16,8 @@ bool on(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 
 
 constexpr int64_t kMaxStride = int64_t(1) << 39;
 constexpr size_t kStatusBytes = 256;
-// Rows (new tokens times the group) up to which a sequence is served by the
-// kernel for few rows.
-constexpr int kFewRows = 16;
-
+// Mean rows of a sequence from which on the tensor-core kernel takes them all.
+constexpr int64_t kAllMany = 512;
 size_t few_bytes() { return (paged_few_bytes() + 255) / 256 * 256; }
 
 // {token, head} strides of a (T, H, D) tensor; NULL: dense.  A dimension of
@@ -319,15 +317,22 @@ sage_status sage_attn_paged(const sage_paged_cache* cache, const sage_paged_batc
   uint8_t* parts = static_cast<uint8_t*>(ws) + kStatusBytes;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const bool bf16 = dtype == SAGE_BF16;
+  // Sequences whose rows (new tokens times the group) fit one tile of the kernel
+  // for few rows go there, longer ones to the tensor-core kernel, each launch
+  // skipping the other's; batches of long sequences run as the latter alone.
+  const int few = paged_few_rows(p.c.Dp);
   const int64_t most = static_cast<int64_t>(batch->max_q) * p.group;
-  const bool many = most > kFewRows && paged_many_serves(p.c, p.group);
+  const bool many = most > few && paged_many_serves(p.c, p.group);
+  const bool all = many && T * p.group >= kAllMany * batch->nseq;
   cudaError_t e = cudaSuccess;
-  p.min_rows = 0;
-  p.max_rows = many ? kFewRows : INT_MAX;
-  p.parts = parts;
-  e = launch_paged_few(p, bf16, sms, st);
+  if (!all) {
+    p.min_rows = 0;
+    p.max_rows = many ? few : INT_MAX;
+    p.parts = parts;
+    e = launch_paged_few(p, bf16, sms, st);
+  }
   if (e == cudaSuccess && many) {
-    p.min_rows = kFewRows + 1;
+    p.min_rows = all ? 0 : few + 1;
     p.max_rows = INT_MAX;
     p.parts = parts + few_bytes();
     e = launch_paged_many(p, bf16, sms, st);

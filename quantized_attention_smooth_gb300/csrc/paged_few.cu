@@ -42,7 +42,7 @@ constexpr unsigned kAll = 0xFFFFFFFFu;
 struct PartHead {
   int32_t parts, seq, head, tile;   // parts of the item from this one on; 0: none here
 };
-constexpr int kMaxRows = 16;
+constexpr int kMaxRows = 32;
 constexpr size_t kPartBytes = sizeof(PartHead) + kMaxRows * 8 + kMaxRows * 128 * 4;
 
 __device__ __forceinline__ uint8_t* part_at(uint8_t* parts, int cta, int which) {
@@ -100,7 +100,7 @@ struct FewItem {
 
 // kWide: rows of the 8-bit cache start on 16 bytes (D % 16 == 0), else on 8.
 template <int kKind, bool kQBF16, int kDp, int kNr, bool kWide>
-__global__ void __launch_bounds__(kThreads, kNr == 1 ? (kKind == kKindQ8 || kDp == 64 ? 4 : 3) : (kDp == 128 ? 2 : 3))
+__global__ void __launch_bounds__(kThreads, kDp == 64 ? 5 - kNr : kNr > 1 ? 2 : kKind == kKindQ8 ? 4 : 3)
 paged_few_kernel(const PagedAttnParams p) {
   constexpr bool kQ8 = kKind == kKindQ8;
   constexpr bool kMmaBF16 = kKind == kKindBF16;
@@ -122,6 +122,8 @@ paged_few_kernel(const PagedAttnParams p) {
   const int g = lane >> 2, t = lane & 3;
   const int cta = blockIdx.x, ctas = gridDim.x;
   const int64_t ts = c.token_stride * kEl;
+  // channels from this lane's first one on, of a key and of a value
+  const int k_left = c.D - 16 / kEl * t, v_left = c.D - (kVw == 2 ? 8 : 16 / kEl) * g;
   asm volatile("griddepcontrol.launch_dependents;");
 
   // ---- this CTA's range of units
@@ -278,7 +280,12 @@ paged_few_kernel(const PagedAttnParams p) {
           for (int e = 0; e < 4; ++e) o[j][nr][e] = 0.0f;
       }
 
+      // (vectors of channels from D on are never loaded and stay zero)
       uint32_t kw[2][kKw], vw[4][kVw];
+#pragma unroll
+      for (int i = 0; i < kKw; ++i) kw[0][i] = kw[1][i] = 0;
+#pragma unroll
+      for (int i = 0; i < kVw; ++i) vw[0][i] = vw[1][i] = vw[2][i] = vw[3][i] = 0;
       float ks[2] = {0.0f, 0.0f};
       // A step is a block of 16 keys: its first key (-1: none), the table's entry,
       // and where the block's keys begin in the head (bytes; -1: nothing to read).
@@ -304,7 +311,7 @@ paged_few_kernel(const PagedAttnParams p) {
             at = (next_page * c.page_stride + static_cast<int64_t>(slot) * c.token_stride) * kEl;
             if (kQ8)
               scale_at = (static_cast<int64_t>(next_page) * c.Hkv + kvh) * c.page_size + slot + g;
-            whole = c.D == kDp && key0 + 15 <= p_hi && (key0 >= lo || key0 + 15 < sinks);
+            whole = key0 + 15 <= p_hi && (key0 >= lo || key0 + 15 < sinks);
           } else if (lane == 0) {
             atomicOr(c.status, kStatusBadPage);
           }
@@ -318,7 +325,8 @@ paged_few_kernel(const PagedAttnParams p) {
           for (int y = 0; y < 2; ++y)
 #pragma unroll
             for (int i = 0; i < kKw / 4; ++i)
-              ld16_row<kQ8 && !kWide>(&kw[y][4 * i], row + y * 8 * ts + 64 * i);
+              ld16_part<kEl, kQ8 && !kWide>(&kw[y][4 * i], row + y * 8 * ts + 64 * i,
+                                            k_left - 64 / kEl * i);
           if constexpr (kQ8) {
             ks[0] = c.k_scale[scale_at];
             ks[1] = c.k_scale[scale_at + 8];
@@ -334,7 +342,7 @@ paged_few_kernel(const PagedAttnParams p) {
 #pragma unroll
             for (int i = 0; i < kKw / 4; ++i)
               ld16_part<kEl, kQ8 && !kWide>(&kw[y][4 * i], row + y * 8 * ts + 64 * i,
-                                            c.D - (64 * i + 16 * t) / kEl);
+                                            k_left - 64 / kEl * i);
             if constexpr (kQ8) ks[y] = c.k_scale[scale_at + 8 * y];
           }
         }
@@ -346,11 +354,11 @@ paged_few_kernel(const PagedAttnParams p) {
           const uint8_t* const r = row + ((y & 1) + 8 * (y >> 1)) * ts;
           if (whole) {
             if constexpr (kVw == 2) {
-              ld8(vw[y], r);
+              if (v_left > 0) ld8(vw[y], r);
             } else {
 #pragma unroll
               for (int i = 0; i < kVw / 4; ++i)
-                ld16_row<kQ8 && !kWide>(&vw[y][4 * i], r + 128 * i);
+                ld16_part<kEl, kQ8 && !kWide>(&vw[y][4 * i], r + 128 * i, v_left - 128 / kEl * i);
             }
             continue;
           }
@@ -358,12 +366,12 @@ paged_few_kernel(const PagedAttnParams p) {
           for (int i = 0; i < kVw; ++i) vw[y][i] = 0;
           if (at >= 0 && seen(key0 + 2 * t + (y & 1) + 8 * (y >> 1))) {
             if constexpr (kVw == 2) {
-              if (8 * g < c.D) ld8(vw[y], r);
+              if (v_left > 0) ld8(vw[y], r);
             } else {
 #pragma unroll
               for (int i = 0; i < kVw / 4; ++i)
                 ld16_part<kEl, kQ8 && !kWide>(&vw[y][4 * i], r + 128 * i,
-                                              c.D - (128 * i + 16 * g) / kEl);
+                                              v_left - 128 / kEl * i);
             }
           }
         }
@@ -688,19 +696,25 @@ cudaError_t launch_few(const PagedAttnParams& p, int sms, cudaStream_t st) {
   return e;
 }
 
+// Row tiles of 8, 16, 24 or 32 rows: the fewest that hold a sequence's rows, as a
+// wider tile costs registers and with them loads in flight.  Where the other
+// kernel takes the longer sequences, the ones left here are mostly single tokens.
 template <int kKind, bool kQBF16>
 cudaError_t launch_kind(const PagedAttnParams& p, int sms, cudaStream_t st) {
-  // 8 rows at a time when a token's group fits and few tokens come: fewer
-  // registers, more loads in flight
-  const bool one = static_cast<int64_t>(p.c.max_q) * p.group <= 8;
-  if (p.c.Dp == 64)
-    return one ? launch_few<kKind, kQBF16, 64, 1>(p, sms, st)
-               : launch_few<kKind, kQBF16, 64, 2>(p, sms, st);
-  return one ? launch_few<kKind, kQBF16, 128, 1>(p, sms, st)
-             : launch_few<kKind, kQBF16, 128, 2>(p, sms, st);
+  int64_t rows = static_cast<int64_t>(p.c.max_q) * p.group;
+  if (p.max_rows < rows) rows = p.group;
+  if (p.c.Dp == 128)
+    return rows <= 8 ? launch_few<kKind, kQBF16, 128, 1>(p, sms, st)
+                     : launch_few<kKind, kQBF16, 128, 2>(p, sms, st);
+  if (rows <= 8) return launch_few<kKind, kQBF16, 64, 1>(p, sms, st);
+  if (rows <= 16) return launch_few<kKind, kQBF16, 64, 2>(p, sms, st);
+  if (rows <= 24) return launch_few<kKind, kQBF16, 64, 3>(p, sms, st);
+  return launch_few<kKind, kQBF16, 64, 4>(p, sms, st);
 }
 
 }  // namespace
+
+int paged_few_rows(int Dp) { return Dp == 64 ? 32 : 16; }
 
 size_t paged_few_bytes() { return 2 * static_cast<size_t>(kMaxCtas) * kPartBytes; }
 

@@ -1062,10 +1062,14 @@ paged_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
       // this tile has been read, so its first one can run meanwhile.  (It
       // overwrites S_t behind the last PV that reads P_t; O_t is only
       // overwritten once this thread has delivered the next P.)
+      // Only the very next item is waited for here: one further on may need the
+      // slot of this one, which is given back below.
       Ring<L::kItems> nx = at;
       nx.next();
-      have = advance(nx);
-      const float next_sc = have ? load_q(item_at(nx.at)) : 0.0f;
+      have = take(nx);
+      const bool ready = have && (t == 0 || item_at(nx.at).two());
+      float next_sc = 0.0f;
+      if (ready) next_sc = load_q(item_at(nx.at));
       // ---- out = O / l, or a part
       ok = __all_sync(kAll, mbar_wait(&o_full[t], items++ & 1, abort_flag, c.status,
                                       p.timeout_ns));
@@ -1156,6 +1160,12 @@ paged_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
       }
       tc_fence_before();                        // O_t has been read
       give_back(at);
+      if (have && !ready) {                     // an item without rows in this tile
+        give_back(nx);
+        nx.next();
+        have = advance(nx);
+        if (have) next_sc = load_q(item_at(nx.at));
+      }
       at = nx;
       sc = next_sc;
     }

@@ -71,6 +71,7 @@ struct PagedAttnParams {
 
 cudaError_t launch_paged_few(const PagedAttnParams& p, bool bf16, int sms, cudaStream_t st);
 size_t paged_few_bytes();
+int paged_few_rows(int Dp);   // rows (new tokens x group) that one of its tiles holds
 cudaError_t launch_paged_many(const PagedAttnParams& p, bool bf16, int sms, cudaStream_t st);
 size_t paged_many_bytes();
 bool paged_many_serves(const PagedGeo& c, int group);

@@ -77,18 +77,9 @@ __device__ __forceinline__ void ld8(uint32_t* w, const uint8_t* p) {
   asm volatile("ld.global.L1::no_allocate.L2::128B.v2.u32 {%0,%1}, [%2];"
                : "=r"(w[0]), "=r"(w[1]) : "l"(p));
 }
-// 16 bytes of a row of the cache: in halves where rows of 8 bits start on 8 bytes
-// only (kHalves: D % 16 == 8).
-template <bool kHalves>
-__device__ __forceinline__ void ld16_row(uint32_t* w, const uint8_t* p) {
-  if constexpr (kHalves) {
-    ld8(w, p);
-    ld8(w + 2, p + 8);
-  } else {
-    ld16(w, p);
-  }
-}
-// The same of a row that ends after `left` more elements of kEl bytes.
+// 16 bytes of a row of the cache that ends after `left` more elements of kEl
+// bytes (untouched where none are left): in halves where rows of 8 bits start on
+// 8 bytes only (kHalves: D % 16 == 8).
 template <int kEl, bool kHalves>
 __device__ __forceinline__ void ld16_part(uint32_t* w, const uint8_t* p, int left) {
   if constexpr (kHalves) {

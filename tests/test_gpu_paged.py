@@ -110,6 +110,15 @@ def test_many_sequences(sage):
     check(sage, Problem(q_lens, kv_lens, 4, 1, 64, 16, "NHD", "bf16", torch.bfloat16, seed=8))
 
 
+@pytest.mark.parametrize("kind,dt", KINDS)
+def test_many_short_chunks_among_longer_ones(sage, kind, dt):
+    """Several hundred chunks of one row tile after chunks of two: the roles of a
+    CTA run ahead of each other by several items."""
+    q_lens = [200 if i % 10 == 0 else 33 + i % 60 for i in range(1500)]
+    kv_lens = [n + i % 70 for i, n in enumerate(q_lens)]
+    check(sage, Problem(q_lens, kv_lens, 1, 1, 64, 16, "NHD", kind, dt, seed=17))
+
+
 def test_declared_lengths_may_be_larger(sage):
     p = Problem([1, 40], [100, 70], 4, 2, 64, 16, "NHD", seed=9, max_kv=112)
     p.max_q = 1000
