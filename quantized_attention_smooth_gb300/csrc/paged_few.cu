@@ -98,8 +98,9 @@ struct FewItem {
   Span span;
 };
 
-// kWide: rows of the 8-bit cache start on 16 bytes (D % 16 == 0), else on 8.
-template <int kKind, bool kQBF16, int kDp, int kNr, bool kWide>
+// kForm: 0 D = Dp, every vector of a row is loaded; 1 vectors from D on are not; 2
+// so too, and rows of the 8-bit cache start on 8 bytes only (D % 16 == 8).
+template <int kKind, bool kQBF16, int kDp, int kNr, int kForm>
 __global__ void __launch_bounds__(kThreads, kDp == 64 ? 5 - kNr : kNr > 1 ? 2 : kKind == kKindQ8 ? 4 : 3)
 paged_few_kernel(const PagedAttnParams p) {
   constexpr bool kQ8 = kKind == kKindQ8;
@@ -325,7 +326,7 @@ paged_few_kernel(const PagedAttnParams p) {
           for (int y = 0; y < 2; ++y)
 #pragma unroll
             for (int i = 0; i < kKw / 4; ++i)
-              ld16_part<kEl, kQ8 && !kWide>(&kw[y][4 * i], row + y * 8 * ts + 64 * i,
+              ld16_part<kEl, kForm>(&kw[y][4 * i], row + y * 8 * ts + 64 * i,
                                             k_left - 64 / kEl * i);
           if constexpr (kQ8) {
             ks[0] = c.k_scale[scale_at];
@@ -341,7 +342,7 @@ paged_few_kernel(const PagedAttnParams p) {
           if (at >= 0 && seen(key0 + g + 8 * y)) {
 #pragma unroll
             for (int i = 0; i < kKw / 4; ++i)
-              ld16_part<kEl, kQ8 && !kWide>(&kw[y][4 * i], row + y * 8 * ts + 64 * i,
+              ld16_part<kEl, kForm>(&kw[y][4 * i], row + y * 8 * ts + 64 * i,
                                             k_left - 64 / kEl * i);
             if constexpr (kQ8) ks[y] = c.k_scale[scale_at + 8 * y];
           }
@@ -354,11 +355,11 @@ paged_few_kernel(const PagedAttnParams p) {
           const uint8_t* const r = row + ((y & 1) + 8 * (y >> 1)) * ts;
           if (whole) {
             if constexpr (kVw == 2) {
-              if (v_left > 0) ld8(vw[y], r);
+              if (kForm == 0 || v_left > 0) ld8(vw[y], r);
             } else {
 #pragma unroll
               for (int i = 0; i < kVw / 4; ++i)
-                ld16_part<kEl, kQ8 && !kWide>(&vw[y][4 * i], r + 128 * i, v_left - 128 / kEl * i);
+                ld16_part<kEl, kForm>(&vw[y][4 * i], r + 128 * i, v_left - 128 / kEl * i);
             }
             continue;
           }
@@ -366,11 +367,11 @@ paged_few_kernel(const PagedAttnParams p) {
           for (int i = 0; i < kVw; ++i) vw[y][i] = 0;
           if (at >= 0 && seen(key0 + 2 * t + (y & 1) + 8 * (y >> 1))) {
             if constexpr (kVw == 2) {
-              if (v_left > 0) ld8(vw[y], r);
+              if (kForm == 0 || v_left > 0) ld8(vw[y], r);
             } else {
 #pragma unroll
               for (int i = 0; i < kVw / 4; ++i)
-                ld16_part<kEl, kQ8 && !kWide>(&vw[y][4 * i], r + 128 * i,
+                ld16_part<kEl, kForm>(&vw[y][4 * i], r + 128 * i,
                                               v_left - 128 / kEl * i);
             }
           }
@@ -658,11 +659,14 @@ paged_join_kernel(const PagedAttnParams p, int ctas) {
                                         : -INFINITY;
 }
 
-template <int kKind, bool kQBF16, int kDp, int kNr, bool kWide = true>
+template <int kKind, bool kQBF16, int kDp, int kNr, int kForm = 0>
 cudaError_t launch_few(const PagedAttnParams& p, int sms, cudaStream_t st) {
-  if (kWide && kKind == kKindQ8 && p.c.D % 16 != 0)
-    return launch_few<kKind, kQBF16, kDp, kNr, kKind != kKindQ8>(p, sms, st);
-  auto* kern = paged_few_kernel<kKind, kQBF16, kDp, kNr, kWide>;
+  if constexpr (kForm == 0) {
+    if (kKind == kKindQ8 && p.c.D % 16 != 0)
+      return launch_few<kKind, kQBF16, kDp, kNr, kKind == kKindQ8 ? 2 : 1>(p, sms, st);
+    if (p.c.D != kDp) return launch_few<kKind, kQBF16, kDp, kNr, 1>(p, sms, st);
+  }
+  auto* kern = paged_few_kernel<kKind, kQBF16, kDp, kNr, kForm>;
   static std::atomic<int> resident{0};       // CTAs of one SM (every GB300 is alike)
   int per = resident.load(std::memory_order_relaxed);
   if (per == 0) {

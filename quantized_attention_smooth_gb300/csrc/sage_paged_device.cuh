@@ -78,15 +78,15 @@ __device__ __forceinline__ void ld8(uint32_t* w, const uint8_t* p) {
                : "=r"(w[0]), "=r"(w[1]) : "l"(p));
 }
 // 16 bytes of a row of the cache that ends after `left` more elements of kEl
-// bytes (untouched where none are left): in halves where rows of 8 bits start on
-// 8 bytes only (kHalves: D % 16 == 8).
-template <int kEl, bool kHalves>
+// bytes (untouched where none are left).  kForm 0: all are there; 2: rows start
+// on 8 bytes only.
+template <int kEl, int kForm>
 __device__ __forceinline__ void ld16_part(uint32_t* w, const uint8_t* p, int left) {
-  if constexpr (kHalves) {
+  if constexpr (kForm == 2) {
     if (left > 0) ld8(w, p);
     if (left > 8) ld8(w + 2, p + 8);
   } else {
-    if (left > 0) ld16(w, p);
+    if (kForm == 0 || left > 0) ld16(w, p);
   }
 }
 
