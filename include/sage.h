@@ -476,10 +476,12 @@ typedef struct {
 } sage_paged_batch;
 
 /* Workspace of the two paged calls: a fixed size for every problem, 256-byte
- * aligned.  Its contents need no preparation, except that the status word at
- * its start is cleared by the caller (16 zero bytes, once); the kernels only
- * set bits of it and sage_device_status reads it.  Calls that may overlap on
- * the GPU need workspaces of their own. */
+ * aligned.  The caller clears its first SAGE_PAGED_CLEAR_BYTES once, before the
+ * first call: they hold the status word, of which the kernels only set bits and
+ * which sage_device_status reads, and counters, which every call leaves at
+ * zero; the rest needs no preparation.  Calls that may overlap on the GPU need
+ * workspaces of their own. */
+#define SAGE_PAGED_CLEAR_BYTES 8192
 SAGE_API size_t sage_workspace_bytes_paged(void);
 
 /* Writes the new tokens' K and V (T rows of (T,Hkv,D), T = total_q) into the

@@ -15,7 +15,9 @@ namespace {
 bool on(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
 constexpr int64_t kMaxStride = int64_t(1) << 39;
-constexpr size_t kStatusBytes = 256;
+constexpr size_t kStatusBytes = 256;   // then the arrival counters
+constexpr size_t kClearBytes = kStatusBytes + kArrivalBytes;
+static_assert(kClearBytes == SAGE_PAGED_CLEAR_BYTES, "the header says what the caller clears");
 // Mean rows of a sequence from which on the tensor-core kernel takes them all.
 constexpr int64_t kAllMany = 512;
 size_t few_bytes() { return (paged_few_bytes() + 255) / 256 * 256; }
@@ -150,7 +152,7 @@ sage_status paged_geo(const sage_paged_cache* cache, const sage_paged_batch* b, 
 extern "C" {
 
 size_t sage_workspace_bytes_paged(void) {
-  return kStatusBytes + few_bytes() + paged_many_bytes();
+  return kClearBytes + few_bytes() + paged_many_bytes();
 }
 
 sage_status sage_rope(const void* q, const void* k, void* q_out, void* k_out, int dtype, int64_t T,
@@ -314,7 +316,8 @@ sage_status sage_attn_paged(const sage_paged_cache* cache, const sage_paged_batc
                  1.44269504088896340736f;
   p.q_vec = vec_rows(q, p.q_tok, p.q_head);
   p.timeout_ns = device_wait_ns();
-  uint8_t* parts = static_cast<uint8_t*>(ws) + kStatusBytes;
+  uint8_t* parts = static_cast<uint8_t*>(ws) + kClearBytes;
+  p.arrivals = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(ws) + kStatusBytes);
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const bool bf16 = dtype == SAGE_BF16;
   // Sequences whose rows (new tokens times the group) fit one tile of the kernel

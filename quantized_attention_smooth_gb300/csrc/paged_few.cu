@@ -19,8 +19,9 @@
 // Work is cut into units of 4 warps x 16 keys and dealt evenly to a fixed grid: every CTA derives its own contiguous range
 // from the lengths (a scan over the sequences), so ragged batches balance and
 // no length comes to the host.  A (sequence, head) that spans CTAs leaves fp32
-// parts (max, sum, O) in the workspace, two per CTA at most; a second kernel
-// joins them in the order of their ranges, so results do not depend on timing.
+// parts (max, sum, O) in the workspace, two per CTA at most; whoever finishes
+// last (or a second kernel) joins them in the order of their ranges, so results
+// do not depend on timing.
 //
 // P is rounded to the 16-bit type of the tensor instruction (relative 2^-9 in
 // bf16, 2^-12 in fp16, the size of the output's own rounding); the sum l takes
@@ -37,6 +38,8 @@ namespace {
 constexpr int kThreads = 128, kWarps = 4;
 constexpr int kMaxCtas = 152 * 8;
 constexpr unsigned kAll = 0xFFFFFFFFu;
+constexpr int kJoinInside = 40;   // most parts of an item, on average, that one CTA joins
+static_assert(kMaxCtas * 4 <= kArrivalBytes, "a counter for every CTA");
 
 // One part of a split item (in the workspace).
 struct PartHead {
@@ -45,8 +48,18 @@ struct PartHead {
 constexpr int kMaxRows = 32;
 constexpr size_t kPartBytes = sizeof(PartHead) + kMaxRows * 8 + kMaxRows * 128 * 4;
 
+// The CTA whose range holds unit x, where CTA i's begins at total i / busy.
+__device__ __forceinline__ int cta_of(int64_t x, int64_t total, int busy) {
+  return static_cast<int>(((x + 1) * busy - 1) / total);
+}
+
 __device__ __forceinline__ uint8_t* part_at(uint8_t* parts, int cta, int which) {
   return parts + (static_cast<size_t>(cta) * 2 + which) * kPartBytes;
+}
+
+// A part's maxima, sums and O.
+__device__ __forceinline__ const float* part_floats(uint8_t* parts, int cta, int which) {
+  return reinterpret_cast<const float*>(part_at(parts, cta, which) + sizeof(PartHead));
 }
 
 struct Units {
@@ -95,13 +108,15 @@ struct FewItem {
   int64_t cur, off, last, total;   // unit; unit within the sequence; past the range; all
   int busy;                        // CTAs that share them
   int s, start, rows, base, head, tile, first, count, per;
+  int first_cta, parts, joins;     // of a split item; whether this CTA joins it
   Span span;
 };
 
 // kForm: 0 D = Dp, every vector of a row is loaded; 1 vectors from D on are not; 2
 // so too, and rows of the 8-bit cache start on 8 bytes only (D % 16 == 8).
 template <int kKind, bool kQBF16, int kDp, int kNr, int kForm>
-__global__ void __launch_bounds__(kThreads, kDp == 64 ? 5 - kNr : kNr > 1 ? 2 : kKind == kKindQ8 ? 4 : 3)
+__global__ void __launch_bounds__(kThreads, kDp == 64 ? (kNr == 1 ? 4 : kNr < 4 ? 3 : 2)
+                                                 : kNr > 1 ? 2 : kKind == kKindQ8 ? 4 : 3)
 paged_few_kernel(const PagedAttnParams p) {
   constexpr bool kQ8 = kKind == kKindQ8;
   constexpr bool kMmaBF16 = kKind == kKindBF16;
@@ -125,7 +140,7 @@ paged_few_kernel(const PagedAttnParams p) {
   const int64_t ts = c.token_stride * kEl;
   // channels from this lane's first one on, of a key and of a value
   const int k_left = c.D - 16 / kEl * t, v_left = c.D - (kVw == 2 ? 8 : 16 / kEl) * g;
-  asm volatile("griddepcontrol.launch_dependents;");
+  if (!p.join_inside) asm volatile("griddepcontrol.launch_dependents;");
 
   // ---- this CTA's range of units
   const int per_thread = (c.nseq + kThreads - 1) / kThreads;
@@ -529,9 +544,8 @@ paged_few_kernel(const PagedAttnParams p) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int hi = e >> 1;
-            const int ch = kQ8 && kDp == 128 ? 16 * g + 8 * hi + j
-                           : kDp == 128 ? 64 * hi + 8 * g + j : 8 * g + 4 * hi + j;
-            acc_s[warp][(8 * nr + 2 * t + (e & 1)) * kPitch + ch] = o[j][nr][e];
+            // lanes g side by side: the 32 lanes of a store hit 32 banks
+            acc_s[warp][(8 * nr + 2 * t + (e & 1)) * kPitch + (kMt * hi + j) * 8 + g] = o[j][nr][e];
           }
       __syncthreads();
       const bool alone = it.first == 0 && it.count == it.per;
@@ -543,38 +557,18 @@ paged_few_kernel(const PagedAttnParams p) {
       if (!alone) {
         used[which] = true;
         if (tid == 0) {
-          // the CTA that holds the item's last unit: CTA i's range begins at total i / busy
-          const int64_t beyond = it.cur - it.first + it.per;
-          const int end_cta = static_cast<int>((beyond * it.busy - 1) / it.total);
+          const int64_t from = it.cur - it.first;
+          const int end_cta = cta_of(from + it.per - 1, it.total, it.busy);
+          it.first_cta = cta_of(from, it.total, it.busy);
+          it.parts = end_cta - it.first_cta + 1;
           *reinterpret_cast<PartHead*>(part) =
               PartHead{end_cta - cta + 1, it.s, it.head, it.tile};
         }
       }
-      for (int i = tid; i < kRows * (kDp / 4); i += kThreads) {
-        const int r = i / (kDp / 4), ch = 4 * (i % (kDp / 4));
-        float top = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, m_s[w][r]);
-        const float safe = top == -INFINITY ? 0.0f : top;
-        float sum = 0.0f;
-        float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          const float f = fast_exp2(m_s[w][r] - safe);
-          sum += f * l_s[w][r];
-          const float4 v = *reinterpret_cast<const float4*>(&acc_s[w][r * kPitch + ch]);
-          a.x += f * v.x; a.y += f * v.y; a.z += f * v.z; a.w += f * v.w;
-        }
-        if (!alone) {
-          *reinterpret_cast<float4*>(part_o + r * kDp + ch) = a;
-          if (ch == 0) {
-            part_m[r] = top;
-            part_l[r] = sum;
-          }
-          continue;
-        }
+      // out = O / l of four channels of a row
+      auto deliver = [&](int r, int ch, float top, float sum, float4 a) {
         const int rr = it.tile * kRows + r;
-        if (rr >= it.rows || ch >= c.D) continue;
+        if (rr >= it.rows || ch >= c.D) return;
         const int64_t tok = static_cast<int64_t>(it.start) + rr / p.group;
         const int h = it.head * p.group + rr % p.group;
         const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
@@ -588,6 +582,93 @@ paged_few_kernel(const PagedAttnParams p) {
         if (p.lse != nullptr && ch == 0)
           p.lse[tok * p.Hq + h] = sum > 0.0f ? (top + log2f(sum)) * 0.69314718055994530942f
                                              : -INFINITY;
+      };
+      for (int i = tid; i < kRows * (kDp / 4); i += kThreads) {
+        const int r = i / (kDp / 4), ch = 4 * (i % (kDp / 4));
+        // where channel ch stands: tile j, half hi and lane g of the products
+        const int cj = kQ8 && kDp == 128 ? ch % 8 : kDp == 128 ? ch % 8 : ch % 4;
+        const int chi = kQ8 && kDp == 128 ? (ch / 8) & 1 : kDp == 128 ? ch / 64 : (ch / 4) & 1;
+        const int cg = kQ8 && kDp == 128 ? ch / 16 : kDp == 128 ? (ch % 64) / 8 : ch / 8;
+        const int at4 = (kMt * chi + cj) * 8 + cg;
+        float top = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, m_s[w][r]);
+        const float safe = top == -INFINITY ? 0.0f : top;
+        float sum = 0.0f;
+        float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float f = fast_exp2(m_s[w][r] - safe);
+          sum += f * l_s[w][r];
+          const float* v = &acc_s[w][r * kPitch + at4];
+          a.x += f * v[0]; a.y += f * v[8]; a.z += f * v[16]; a.w += f * v[24];
+        }
+        if (!alone) {
+          *reinterpret_cast<float4*>(part_o + r * kDp + ch) = a;
+          if (ch == 0) {
+            part_m[r] = top;
+            part_l[r] = sum;
+          }
+          continue;
+        }
+        deliver(r, ch, top, sum, a);
+      }
+      if (!alone && p.join_inside) {
+        // The CTA that finishes an item's last part joins them all, in their order.
+        __threadfence();
+        __syncthreads();
+        if (tid == 0) {
+          const uint32_t arrived = atomicAdd(&p.arrivals[it.first_cta], 1u) + 1u;
+          it.joins = arrived == static_cast<uint32_t>(it.parts);
+          if (it.joins) p.arrivals[it.first_cta] = 0;     // for the next call
+          __threadfence();
+        }
+        __syncthreads();
+        if (it.joins) {
+          // the parts' maxima and sums through shared memory (as many as fit)
+          constexpr int kFit = kWarps * kRows * kPitch / (2 * kRows);
+          float* const ml = &acc_s[0][0];
+          const int parts = it.parts, fit = min(parts, kFit);
+          for (int i = tid; i < fit * kRows; i += kThreads) {
+            const float* f = part_floats(p.parts, it.first_cta + i / kRows, i < kRows) + i % kRows;
+            ml[i] = __ldcg(f);
+            ml[kFit * kRows + i] = __ldcg(f + kMaxRows);
+          }
+          __syncthreads();
+          for (int i = tid; i < kRows * (kDp / 4); i += kThreads) {
+            const int r = i / (kDp / 4), ch = 4 * (i % (kDp / 4));
+            if (it.tile * kRows + r >= it.rows) break;    // later ones are later rows
+            auto max_of = [&](int j) {
+              return j < kFit ? ml[j * kRows + r]
+                              : __ldcg(part_floats(p.parts, it.first_cta + j, 0) + r);
+            };
+            auto sum_of = [&](int j) {
+              return j < kFit ? ml[(kFit + j) * kRows + r]
+                              : __ldcg(part_floats(p.parts, it.first_cta + j, 0) + kMaxRows + r);
+            };
+            float top = -INFINITY;
+            for (int j = 0; j < parts; ++j) top = fmaxf(top, max_of(j));
+            const float safe = top == -INFINITY ? 0.0f : top;
+            float sum = 0.0f;
+            float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            for (int j0 = 0; j0 < parts; j0 += 8) {
+              float4 v[8];
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                v[j] = __ldcg(reinterpret_cast<const float4*>(
+                    part_floats(p.parts, it.first_cta + min(j0 + j, parts - 1),
+                                j0 + j == 0 || parts == 1) + 2 * kMaxRows + r * kDp + ch));
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                if (j0 + j < parts) {
+                  const float w = fast_exp2(max_of(j0 + j) - safe);
+                  sum += w * sum_of(j0 + j);
+                  a.x += w * v[j].x; a.y += w * v[j].y; a.z += w * v[j].z; a.w += w * v[j].w;
+                }
+            }
+            deliver(r, ch, top, sum, a);
+          }
+        }
       }
       __syncthreads();
       if (tid == 0) {
@@ -682,10 +763,15 @@ cudaError_t launch_few(const PagedAttnParams& p, int sms, cudaStream_t st) {
   const int64_t items = tiles * p.c.Hkv * p.c.nseq;
   int ctas = sms * per < kMaxCtas ? sms * per : kMaxCtas;
   if (items * max_units < ctas) ctas = static_cast<int>(items * max_units);
-  kern<<<ctas, kThreads, 0, st>>>(p);
+  // Parts are joined by the CTA that finishes an item last, which saves a launch,
+  // unless few items spread over many CTAs: one CTA would then read a hundred
+  // parts or more, and a second kernel does it by the row.
+  PagedAttnParams prm = p;
+  prm.join_inside = items * kJoinInside >= ctas;
+  kern<<<ctas, kThreads, 0, st>>>(prm);
   note_launch();
   cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || prm.join_inside) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(ctas), 8 * kNr);
   cfg.blockDim = dim3(128);

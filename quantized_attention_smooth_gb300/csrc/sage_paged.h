@@ -52,6 +52,8 @@ struct RowsParams {
 // mode 0: sage_rope; 1: append to a 16-bit cache; 2: append to a Q8 cache.
 cudaError_t launch_rows(const RowsParams& p, int mode, bool bf16, int sms, cudaStream_t st);
 
+constexpr int kArrivalBytes = 8192 - 256;
+
 struct PagedAttnParams {
   PagedGeo c;
   const uint16_t* q;
@@ -66,6 +68,8 @@ struct PagedAttnParams {
   int32_t tensor_copies;     // the 8-bit cache's pages go by tensor copies (set by the launcher)
   int32_t min_rows, max_rows;  // rows (tokens x group) of the sequences a launch serves
   uint8_t* parts;            // split results (workspace)
+  uint32_t* arrivals;        // kArrivalBytes of the workspace, zero between calls
+  int32_t join_inside;       // parts joined by the kernel itself (set by the launcher)
   uint64_t timeout_ns;
 };
 

@@ -651,16 +651,19 @@ class PagedBatch:
         return ctypes.byref(c)
 
 
+PAGED_CLEAR_BYTES = 8192      # SAGE_PAGED_CLEAR_BYTES
+
+
 def workspace_bytes_paged() -> int:
     return int(_lib.sage_workspace_bytes_paged())
 
 
 def alloc_workspace_paged(device="cuda", stream=None):
-    """A workspace of kv_append and attn_paged, its status word cleared.  One
+    """A workspace of kv_append and attn_paged, cleared where they need it.  One
     serves any number of calls in stream order."""
     def make():
         ws = alloc_workspace(workspace_bytes_paged(), device)
-        ws[:256].zero_()
+        ws[:PAGED_CLEAR_BYTES].zero_()
         return ws
     return _empty_on(stream, make)
 
