@@ -38,6 +38,7 @@ namespace {
 constexpr int kThreads = 128, kWarps = 4;
 constexpr int kMaxCtas = 152 * 8;
 constexpr unsigned kAll = 0xFFFFFFFFu;
+constexpr float kLazy = 8.0f;     // log2 of the growth of a row's maximum that rescales O
 constexpr int kJoinInside = 40;   // most parts of an item, on average, that one CTA joins
 static_assert(kMaxCtas * 4 <= kArrivalBytes, "a counter for every CTA");
 
@@ -432,8 +433,7 @@ paged_few_kernel(const PagedAttnParams p) {
           // ---- logits, masks, running maximum and sum
           const bool full =
               cur0 + 15 <= p_lo && (cur0 >= lo_hi || cur0 + 15 < sinks);
-          float mx[kNr][2], alpha[kNr][2];
-          bool grew = false;
+          bool over = false;                    // a logit has outgrown its row's reference
 #pragma unroll
           for (int nr = 0; nr < kNr; ++nr) {
 #pragma unroll
@@ -448,23 +448,26 @@ paged_few_kernel(const PagedAttnParams p) {
                 v = see ? v : -INFINITY;
               }
               x[nr][e] = v;
-            }
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              float v = fmaxf(x[nr][i], x[nr][i + 2]);
-              v = fmaxf(v, __shfl_xor_sync(kAll, v, 4));
-              v = fmaxf(v, __shfl_xor_sync(kAll, v, 8));
-              v = fmaxf(v, __shfl_xor_sync(kAll, v, 16));
-              v = fmaxf(v, m[nr][i]);
-              const float safe = v == -INFINITY ? 0.0f : v;
-              alpha[nr][i] = fast_exp2(m[nr][i] - safe);
-              grew |= v > m[nr][i];
-              m[nr][i] = v;
-              mx[nr][i] = safe;
-              l[nr][i] *= alpha[nr][i];
+              over |= v > m[nr][e & 1] + kLazy;  // with m = -inf: any logit but -inf
             }
           }
-          if (__any_sync(kAll, grew)) {
+          if (__any_sync(kAll, over)) {
+            // Rare after the first block: references move to the maximum, O and l
+            // follow.  (Any reference gives the same result; P stays below 2^kLazy.)
+            float alpha[kNr][2];
+#pragma unroll
+            for (int nr = 0; nr < kNr; ++nr)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                float v = fmaxf(x[nr][i], x[nr][i + 2]);
+                v = fmaxf(v, __shfl_xor_sync(kAll, v, 4));
+                v = fmaxf(v, __shfl_xor_sync(kAll, v, 8));
+                v = fmaxf(v, __shfl_xor_sync(kAll, v, 16));
+                const float next = v > m[nr][i] + kLazy ? v : m[nr][i];
+                alpha[nr][i] = next == m[nr][i] ? 1.0f : fast_exp2(m[nr][i] - next);
+                m[nr][i] = next;
+                l[nr][i] *= alpha[nr][i];
+              }
 #pragma unroll
             for (int j = 0; j < kMt; ++j)
 #pragma unroll
@@ -477,9 +480,11 @@ paged_few_kernel(const PagedAttnParams p) {
 #pragma unroll
           for (int nr = 0; nr < kNr; ++nr) {
             float e4[4];
+            const float safe[2] = {m[nr][0] == -INFINITY ? 0.0f : m[nr][0],
+                                   m[nr][1] == -INFINITY ? 0.0f : m[nr][1]};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              e4[e] = fast_exp2(x[nr][e] - mx[nr][e & 1]);
+              e4[e] = fast_exp2(x[nr][e] - safe[e & 1]);
               l[nr][e & 1] += e4[e];
             }
             pb[nr][0] = transpose8x8(pack2<kMmaBF16>(e4[0], e4[1]));
