@@ -476,31 +476,67 @@ def rope_freqs(rotary_dim, base=10000.0, scaling=None, factor=1.0, original_len=
     return f.to(device), mscale
 
 
-def _rows3(where, name, t, like=None):
-    """A (T, H, D) view the serving calls read or write: fp16/bf16 on the
-    current CUDA device, channel stride 1."""
-    if t.dim() != 3 or t.stride(2) != 1 and t.shape[2] > 1:
-        raise ValueError(f"{where}: {name} must be (T, H, D) with contiguous channels, got shape "
-                         f"{tuple(t.shape)}, strides {t.stride()}")
-    _on_device(where, name, t)
-    if like is not None and t.dtype != like.dtype:
-        raise TypeError(f"{where}: {name} is {t.dtype}, not {like.dtype}")
+# The serving calls run in a few microseconds on the GPU, so their wrappers do:
+# plain integers for pointers, one look at the current device, and no torch call
+# that a tensor's own methods can answer.
+_torch = None
 
 
-def _on_device(where, name, t):
-    import torch
+def _device(where, name, t):
+    """(index of the current device, its current stream's handle); t, the
+    call's first tensor, is on a CUDA device."""
+    global _torch
+    if not t.is_cuda:
+        _off_device(where, name, t, None)
+    if _torch is None:
+        import torch
+        _torch = torch
+        _CODES.update({torch.float16: F16, torch.bfloat16: BF16})
+    d = _torch._C._cuda_getDevice()
+    return d, _torch._C._cuda_getCurrentRawStream(d)
+
+
+def _off_device(where, name, t, dev):
     if not t.is_cuda:
         raise ValueError(f"{where}: {name} is not on a CUDA device")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{where}: {name} is on {t.device}, the current device is "
-                         f"cuda:{torch.cuda.current_device()}")
+    raise ValueError(f"{where}: {name} is on {t.device}, the current device is cuda:{dev}")
 
 
-def _row_strides(t):
-    """None for a dense (T, H, D) tensor, else its {token, head} strides."""
-    if t is None or t.is_contiguous():
-        return None
-    return (ctypes.c_int64 * 2)(t.stride(0), t.stride(1))
+def _rows3(where, name, t, dev):
+    """A (T, H, D) view the serving calls read or write: on the current CUDA
+    device, channel stride 1.  Returns its shape and the {token, head} strides
+    to pass (None: dense)."""
+    shape = t.shape
+    if len(shape) != 3 or t.stride(2) != 1 and shape[2] > 1:
+        raise ValueError(f"{where}: {name} must be (T, H, D) with contiguous channels, got shape "
+                         f"{tuple(shape)}, strides {t.stride()}")
+    if t.get_device() != dev:
+        _off_device(where, name, t, dev)
+    return shape, None if t.is_contiguous() else _Strides(t.stride(0), t.stride(1))
+
+
+def _on_device(where, name, t, dev=None):
+    dev = _device(where, name, t)[0] if dev is None else dev
+    if t.get_device() != dev:
+        _off_device(where, name, t, dev)
+
+
+def _code16(where, name, t):
+    """SAGE_F16 or SAGE_BF16."""
+    code = _CODES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{where}: {name} must be float16 or bfloat16, got {t.dtype}")
+    return code
+
+
+_CODES: dict = {}
+_Strides = ctypes.c_int64 * 2
+
+
+def _handle(stream, current):
+    if stream is None:
+        return current
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def _empty_on(stream, make):
@@ -515,17 +551,26 @@ def _empty_on(stream, make):
         return make()
 
 
-def _freqs(where, inv_freq):
-    import torch
-    if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+def _freqs(where, inv_freq, dev):
+    if inv_freq.dtype != _torch.float64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
         raise ValueError(f"{where}: inv_freq must be a contiguous 1-D float64 tensor")
-    _on_device(where, "inv_freq", inv_freq)
+    if inv_freq.get_device() != dev:
+        _off_device(where, "inv_freq", inv_freq, dev)
 
 
-def _out_like(where, name, out, t):
-    if tuple(out.shape) != tuple(t.shape):
-        raise ValueError(f"{where}: {name} has shape {tuple(out.shape)}, not {tuple(t.shape)}")
-    _rows3(where, name, out, t)
+def _result(where, name, out, t, stream, dev, dense):
+    """`out`, checked, or a new dense tensor of t's shape; with its strides.
+    dense: t is dense itself."""
+    if out is None:
+        if stream is not None:
+            return _empty_on(stream, lambda: t.new_empty(t.shape)), None
+        return _torch.empty_like(t) if dense else t.new_empty(t.shape), None
+    shape, st = _rows3(where, name, out, dev)
+    if shape != t.shape:
+        raise ValueError(f"{where}: {name} has shape {tuple(shape)}, not {tuple(t.shape)}")
+    if out.dtype != t.dtype:
+        raise TypeError(f"{where}: {name} is {out.dtype}, not {t.dtype}")
+    return out, st
 
 
 def rope(q, k, positions, inv_freq, interleaved=False, mscale=1.0, inverse=False, q_out=None,
@@ -536,36 +581,34 @@ def rope(q, k, positions, inv_freq, interleaved=False, mscale=1.0, inverse=False
     or (2i, 2i + 1) with `interleaved`.  q_out=q (k_out=k) turns in place.
     `inverse` turns back; applied to the outputs' gradients with the same
     mscale it gives the inputs' gradients.  Returns (q_out, k_out)."""
-    import torch
-    _rows3("rope", "q", q)
-    T, Hq, D = q.shape
-    Hkv = 0
-    if k is not None:
-        _rows3("rope", "k", k, q)
-        Hkv = k.shape[1]
-        if k.shape[0] != T or k.shape[2] != D:
-            raise ValueError(f"rope: k has shape {tuple(k.shape)}, q {tuple(q.shape)}")
-    if positions.dtype not in (torch.int64, torch.int32) or tuple(positions.shape) != (T,) or \
+    dev, current = _device("rope", "q", q)
+    (T, Hq, D), qs = _rows3("rope", "q", q, dev)
+    dtype = _code16("rope", "q", q)
+    bits = 64 if positions.dtype == _torch.int64 else 32
+    if bits == 32 and positions.dtype != _torch.int32 or positions.shape != (T,) or \
             not positions.is_contiguous():
         raise ValueError("rope: positions must be a contiguous int64 or int32 tensor of T entries")
-    _on_device("rope", "positions", positions)
-    _freqs("rope", inv_freq)
-    if q_out is None:
-        q_out = _empty_on(stream, lambda: torch.empty((T, Hq, D), dtype=q.dtype, device=q.device))
-    else:
-        _out_like("rope", "q_out", q_out, q)
+    if positions.get_device() != dev:
+        _off_device("rope", "positions", positions, dev)
+    _freqs("rope", inv_freq, dev)
+    q_out, qos = _result("rope", "q_out", q_out, q, stream, dev, qs is None)
+    Hkv, ks, kos, kp, kop = 0, None, None, 0, 0
     if k is None:
         k_out = None
-    elif k_out is None:
-        k_out = _empty_on(stream, lambda: torch.empty((T, Hkv, D), dtype=q.dtype, device=q.device))
     else:
-        _out_like("rope", "k_out", k_out, k)
-    rc = _lib.sage_rope(_ptr(q), _ptr(k), _ptr(q_out), _ptr(k_out), _dtype_code(q), T, Hq, Hkv, D,
-                        _row_strides(q), _row_strides(k), _row_strides(q_out), _row_strides(k_out),
-                        _ptr(positions), 64 if positions.dtype == torch.int64 else 32,
-                        _ptr(inv_freq), 2 * inv_freq.numel(), int(bool(interleaved)),
-                        float(mscale), int(bool(inverse)), _stream(stream))
-    _check(rc, "sage_rope")
+        (Tk, Hkv, Dk), ks = _rows3("rope", "k", k, dev)
+        if Tk != T or Dk != D:
+            raise ValueError(f"rope: k has shape {tuple(k.shape)}, q {tuple(q.shape)}")
+        if k.dtype != q.dtype:
+            raise TypeError(f"rope: k is {k.dtype}, not {q.dtype}")
+        k_out, kos = _result("rope", "k_out", k_out, k, stream, dev, ks is None)
+        kp, kop = k.data_ptr(), k_out.data_ptr()
+    rc = _lib.sage_rope(q.data_ptr(), kp, q_out.data_ptr(), kop, dtype, T, Hq, Hkv, D, qs, ks, qos,
+                        kos, positions.data_ptr(), bits, inv_freq.data_ptr(),
+                        2 * inv_freq.shape[0], 1 if interleaved else 0, mscale,
+                        1 if inverse else 0, _handle(stream, current))
+    if rc:
+        _check(rc, "sage_rope")
     return q_out, k_out
 
 
@@ -589,7 +632,7 @@ class PagedCache:
                 k.dtype not in (torch.float16, torch.bfloat16) or v.dtype != k.dtype):
             raise TypeError(f"PagedCache: k {k.dtype} and v {v.dtype} must be both float16, both "
                             "bfloat16, or int8 and float8_e4m3fn")
-        self.kind = Q8 if q8 else _dtype_code(k)
+        self.kind = Q8 if q8 else F16 if k.dtype == torch.float16 else BF16
         pages, self.D = k.shape[0], k.shape[3]
         slots, self.Hkv = (k.shape[2], k.shape[1]) if lay == HND else (k.shape[1], k.shape[2])
         st, page_dims = k.stride(), (2, 1) if lay == HND else (1, 2)
@@ -617,6 +660,7 @@ class PagedCache:
         ptr = lambda t: 0 if t is None else t.data_ptr()
         self._c = _CacheC(ptr(k), ptr(v), ptr(k_scale), ptr(k_mean), ptr(v_scale), pages, slots,
                           self.Hkv, self.D, st[0], st[page_dims[0]], st[page_dims[1]], self.kind)
+        self._ref = ctypes.byref(self._c)
 
 
 class PagedBatch:
@@ -642,12 +686,17 @@ class PagedBatch:
                              f"got {tuple(block_table.shape)}")
         self.cu_q, self.kv_lens, self.block_table = cu_q, kv_lens, block_table
         self.nseq, self.max_q, self.max_kv = n, int(max_q), int(max_kv)
+        self._calls = {}
         self._c = _BatchC(cu_q.data_ptr(), kv_lens.data_ptr(), block_table.data_ptr(), n, 0,
                           block_table.stride(0), block_table.shape[1], self.max_q, self.max_kv)
 
     def _rows(self, total_q):
-        c = _BatchC.from_buffer_copy(self._c)       # calls of several threads share the batch
-        c.total_q = total_q
+        c = self._calls.get(total_q)                # one struct per number of rows: calls of
+        if c is None:                               # several threads share the batch
+            c = _BatchC.from_buffer_copy(self._c)
+            c.total_q = total_q
+            if len(self._calls) < 64:
+                self._calls[total_q] = c
         return ctypes.byref(c)
 
 
@@ -673,36 +722,44 @@ def kv_append(cache, batch, k, v, q=None, q_out=None, inv_freq=None, interleaved
     """Writes the batch's new k and v (T, Hkv, D) into the cache.  With
     inv_freq, k is turned at each token's position first, and q (T, Hq, D), if
     given, into q_out (returned)."""
-    import torch
-    _rows3("kv_append", "k", k)
-    _rows3("kv_append", "v", v, k)
-    T = k.shape[0]
-    if k.shape[1] != cache.Hkv or k.shape[2] != cache.D or v.shape != k.shape:
-        raise ValueError(f"kv_append: k {tuple(k.shape)} and v {tuple(v.shape)} do not fit a cache "
+    dev, current = _device("kv_append", "k", k)
+    shape, ks = _rows3("kv_append", "k", k, dev)
+    vshape, vs = _rows3("kv_append", "v", v, dev)
+    dtype = _code16("kv_append", "k", k)
+    T = shape[0]
+    if shape[1] != cache.Hkv or shape[2] != cache.D or vshape != shape:
+        raise ValueError(f"kv_append: k {tuple(shape)} and v {tuple(vshape)} do not fit a cache "
                          f"of {cache.Hkv} heads of {cache.D} channels")
-    Hq = 0
+    if v.dtype != k.dtype:
+        raise TypeError(f"kv_append: v is {v.dtype}, not {k.dtype}")
+    Hq, qs, qos, qp, qop = 0, None, None, 0, 0
     if q is not None:
-        _rows3("kv_append", "q", q, k)
-        Hq = q.shape[1]
-        if q.shape[0] != T or q.shape[2] != cache.D:
-            raise ValueError(f"kv_append: q has shape {tuple(q.shape)}, k {tuple(k.shape)}")
-        if q_out is None:
-            q_out = _empty_on(stream, lambda: torch.empty((T, Hq, cache.D), dtype=q.dtype,
-                                                          device=q.device))
-        else:
-            _out_like("kv_append", "q_out", q_out, q)
+        (Tq, Hq, Dq), qs = _rows3("kv_append", "q", q, dev)
+        if Tq != T or Dq != cache.D:
+            raise ValueError(f"kv_append: q has shape {tuple(q.shape)}, k {tuple(shape)}")
+        if q.dtype != k.dtype:
+            raise TypeError(f"kv_append: q is {q.dtype}, not {k.dtype}")
+        q_out, qos = _result("kv_append", "q_out", q_out, q, stream, dev, qs is None)
+        qp, qop = q.data_ptr(), q_out.data_ptr()
+    fp, R = 0, 0
     if inv_freq is not None:
-        _freqs("kv_append", inv_freq)
-    if ws is None:
-        ws = alloc_workspace_paged(k.device, stream)
-    rc = _lib.sage_kv_append(
-        ctypes.byref(cache._c), batch._rows(T), _ptr(k), _ptr(v), _ptr(q),
-        _ptr(q_out if q is not None else None), _dtype_code(k), Hq, _row_strides(k),
-        _row_strides(v), _row_strides(q), _row_strides(q_out if q is not None else None),
-        _ptr(inv_freq), 0 if inv_freq is None else 2 * inv_freq.numel(), int(bool(interleaved)),
-        float(mscale), _ptr(ws), ws.numel(), _stream(stream))
-    _check(rc, "sage_kv_append")
+        _freqs("kv_append", inv_freq, dev)
+        fp, R = inv_freq.data_ptr(), 2 * inv_freq.shape[0]
+    ws = _workspace("kv_append", ws, stream, dev)
+    rc = _lib.sage_kv_append(cache._ref, batch._rows(T), k.data_ptr(), v.data_ptr(), qp, qop, dtype,
+                             Hq, ks, vs, qs, qos, fp, R, 1 if interleaved else 0, mscale,
+                             ws.data_ptr(), ws.numel(), _handle(stream, current))
+    if rc:
+        _check(rc, "sage_kv_append")
     return q_out if q is not None else None
+
+
+def _workspace(where, ws, stream, dev):
+    if ws is None:
+        return alloc_workspace_paged("cuda", stream)
+    if ws.get_device() != dev:
+        _off_device(where, "ws", ws, dev)
+    return ws
 
 
 def attn_paged(cache, batch, q, out=None, window=0, sinks=0, sm_scale=None, lse=None, ws=None,
@@ -711,28 +768,26 @@ def attn_paged(cache, batch, q, out=None, window=0, sinks=0, sm_scale=None, lse=
     causal, with window > 0 only the last `window` keys and the first `sinks`
     ones.  Returns out (T, Hq, D) of q's type; lse, if given, is a float32
     (T, Hq) tensor that receives the log-sum-exp of every row."""
-    import torch
-    _rows3("attn_paged", "q", q)
-    T, Hq, D = q.shape
+    dev, current = _device("attn_paged", "q", q)
+    (T, Hq, D), qs = _rows3("attn_paged", "q", q, dev)
+    dtype = _code16("attn_paged", "q", q)
     if D != cache.D:
         raise ValueError(f"attn_paged: q has {D} channels, the cache {cache.D}")
-    if out is None:
-        out = _empty_on(stream, lambda: torch.empty((T, Hq, D), dtype=q.dtype, device=q.device))
-    else:
-        _out_like("attn_paged", "out", out, q)
-        if not out.is_contiguous():
-            raise ValueError("attn_paged: out must be contiguous")
+    out, os_ = _result("attn_paged", "out", out, q, stream, dev, qs is None)
+    if os_ is not None:
+        raise ValueError("attn_paged: out must be contiguous")
+    lp = 0
     if lse is not None:
-        if lse.dtype != torch.float32 or tuple(lse.shape) != (T, Hq) or not lse.is_contiguous():
+        if lse.dtype != _torch.float32 or lse.shape != (T, Hq) or not lse.is_contiguous():
             raise ValueError("attn_paged: lse must be a contiguous float32 (T, Hq) tensor")
-        _on_device("attn_paged", "lse", lse)
-    if ws is None:
-        ws = alloc_workspace_paged(q.device, stream)
-    rc = _lib.sage_attn_paged(ctypes.byref(cache._c), batch._rows(T), _ptr(q), _ptr(out),
-                              _ptr(lse), _dtype_code(q), Hq, _row_strides(q), int(window),
-                              int(sinks), float(sm_scale or 0.0), _ptr(ws), ws.numel(),
-                              _stream(stream))
-    _check(rc, "sage_attn_paged")
+        _on_device("attn_paged", "lse", lse, dev)
+        lp = lse.data_ptr()
+    ws = _workspace("attn_paged", ws, stream, dev)
+    rc = _lib.sage_attn_paged(cache._ref, batch._rows(T), q.data_ptr(), out.data_ptr(), lp, dtype,
+                              Hq, qs, window, sinks, sm_scale or 0.0, ws.data_ptr(), ws.numel(),
+                              _handle(stream, current))
+    if rc:
+        _check(rc, "sage_attn_paged")
     return out
 
 

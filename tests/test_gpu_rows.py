@@ -119,6 +119,46 @@ def test_rope_inverse_is_the_gradient(sage):
             assert abs(slope - float(grad[4, 1, ch])) <= 2.0 ** -11 * 4 * 3 * gain
 
 
+def test_the_binding_refuses_what_it_would_misread(sage):
+    q, pos = randn(8, 3, 2, 64), torch.arange(3, device="cuda")
+    f, _ = sage.rope_freqs(64)
+    for bad, match in [((q[0], None, pos, f), r"\(T, H, D\)"), ((q.float(), None, pos, f), "float16"),
+                       ((q, q.half(), pos, f), "not torch.bfloat16"), ((q, q[:2], pos, f), "shape"),
+                       ((q, None, pos[:2], f), "positions"), ((q, None, pos.float(), f), "positions"),
+                       ((q, None, pos.cpu(), f), "positions is not on"), ((q, None, pos, f.float()), "inv_freq"),
+                       ((q.transpose(1, 2), None, pos, f), "contiguous channels")]:
+        with pytest.raises((ValueError, TypeError), match=match):
+            sage.rope(*bad)
+    with pytest.raises(ValueError, match="q_out has shape"):
+        sage.rope(q, None, pos, f, q_out=q[:2])
+    with pytest.raises(sage.SageError, match="even"):
+        sage.rope(q, None, pos, torch.ones(33, dtype=torch.float64, device="cuda"))
+    p = torch.zeros(4, 16, 2, 64, dtype=torch.bfloat16, device="cuda")
+    cache = sage.PagedCache(p, p.clone())
+    batch = sage.PagedBatch(torch.tensor([0, 3], dtype=torch.int32, device="cuda"),
+                            torch.tensor([3], dtype=torch.int32, device="cuda"),
+                            torch.zeros(1, 1, dtype=torch.int32, device="cuda"), 3, 16)
+    with pytest.raises(ValueError, match="do not fit"):
+        sage.kv_append(cache, batch, q[:, :1], q[:, :1])
+    with pytest.raises(sage.SageError, match="kind"):
+        sage.kv_append(cache, batch, q.half(), q.half())
+    with pytest.raises(ValueError, match="channels"):
+        sage.attn_paged(cache, batch, q[..., :32])
+    with pytest.raises(ValueError, match="contiguous"):
+        sage.attn_paged(cache, batch, q, out=randn(9, 3, 4, 64)[:, ::2])
+    with pytest.raises(ValueError, match="lse"):
+        sage.attn_paged(cache, batch, q, lse=torch.zeros(3, 2, device="cuda").double())
+    for bad, match in [((p, p.half()), "bfloat16"), ((p, p[:2]), "one shape"),
+                       ((p.to(torch.int8), p.to(torch.float8_e4m3fn)), "k_scale"),
+                       ((p, p.transpose(1, 2).contiguous().transpose(1, 2)), "strides")]:
+        with pytest.raises((ValueError, TypeError), match=match):
+            sage.PagedCache(*bad)
+    with pytest.raises(TypeError, match="int32"):
+        sage.PagedBatch(batch.cu_q.long(), batch.kv_lens, batch.block_table, 3, 16)
+    with pytest.raises(ValueError, match="entries"):
+        sage.PagedBatch(batch.cu_q[:1], batch.kv_lens, batch.block_table, 3, 16)
+
+
 def test_rope_frequencies(sage):
     f, g = sage.rope_freqs(64, base=500.0)
     assert g == 1.0 and torch.allclose(f, 500.0 ** (-torch.arange(32, device="cuda").double() / 32),

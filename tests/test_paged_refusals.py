@@ -142,8 +142,6 @@ def test_binding_refuses_host_tensors():
     f = torch.ones(32, dtype=torch.float64)
     with pytest.raises(ValueError, match="CUDA"):
         sage.rope(x, None, torch.arange(3), f)
-    with pytest.raises(ValueError, match=r"\(T, H, D\)"):
-        sage.rope(x[0], None, torch.arange(3), f)
     p = torch.zeros(4, 16, 2, 64, dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="CUDA"):
         sage.PagedCache(p, p)
