@@ -123,7 +123,8 @@ __global__ void __launch_bounds__(kRowThreads)
 rows_kernel(const RowsParams p) {
   __shared__ float2 cs[kMaxToks * 64];
   __shared__ int64_t pos_s[kMaxToks];
-  __shared__ int page_s[kMaxToks];          // -1: nothing is written for this token
+  __shared__ int page_s[kMaxToks];          // -1: no such page; -2: no such token
+  __shared__ int64_t slot_s[kMaxToks], scale_s[kMaxToks];   // the slot of head 0, and its scale
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * p.toks;
   const int nt = static_cast<int>(min(static_cast<int64_t>(p.toks), p.T - t0));
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -148,7 +149,12 @@ rows_kernel(const RowsParams p) {
           if (pos >= 0) page = paged_page(c, s, static_cast<int>(pos / c.page_size));
         }
         pos_s[i] = pos;
-        page_s[i] = pos < 0 ? -2 : page;    // -2: no such token; -1: no such page
+        page_s[i] = pos < 0 ? -2 : page;
+        if (page >= 0) {
+          const int slot = static_cast<int>(pos % c.page_size);
+          slot_s[i] = page * c.page_stride + slot * c.token_stride;
+          scale_s[i] = static_cast<int64_t>(page) * c.Hkv * c.page_size + slot;
+        }
       }
     }
   }
@@ -262,8 +268,7 @@ rows_kernel(const RowsParams p) {
                      pack8<kBF16>(x));
           }
           const int page = page_s[t];
-          const int slot = static_cast<int>(pos_s[t] % c.page_size);
-          const int64_t at = page * c.page_stride + slot * c.token_stride + h * c.head_stride + c0;
+          const int64_t at = slot_s[t] + h * c.head_stride + c0;
           const bool put = has && what != 0 && page >= 0;
           if constexpr (kMode == 1) {
             if (put) {
@@ -292,7 +297,7 @@ rows_kernel(const RowsParams p) {
                             << (8 * (e & 3));
               *reinterpret_cast<uint2*>(c.k + at) = make_uint2(w[0], w[1]);
               if (sub == 0)
-                c.k_scale[(static_cast<int64_t>(page) * c.Hkv + h) * c.page_size + slot] =
+                c.k_scale[scale_s[t] + static_cast<int64_t>(h) * c.page_size] =
                     __fdiv_rn(top, 127.0f);
             } else if (put) {
               uint32_t w[2];
