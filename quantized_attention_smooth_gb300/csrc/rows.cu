@@ -33,6 +33,8 @@ namespace {
 
 constexpr int kRowThreads = 256;
 constexpr int kMaxToks = 8;          // tokens of one CTA
+constexpr int kMaxQ8Toks = 16;
+constexpr int kMaxQ8Table = 4096;    // kv heads x padded channels
 constexpr unsigned kAll = 0xFFFFFFFFu;
 
 template <bool kBF16>
@@ -116,6 +118,48 @@ __device__ __forceinline__ int find_seq(const PagedGeo& c, int64_t tok, int lane
   return lo;
 }
 
+// Each token's position and slot (append), by a warp per token.
+__device__ __forceinline__ void place_tokens(const RowsParams& p, int64_t t0, int nt, int64_t* pos_s,
+                                             int* page_s, int64_t* slot_s, int64_t* scale_s) {
+  const PagedGeo& c = p.c;
+  const int lane = threadIdx.x & 31;
+  for (int i = threadIdx.x >> 5; i < nt; i += kRowThreads / 32) {
+    const int64_t tok = t0 + i;
+    const int s = find_seq(c, tok, lane);
+    if (lane == 0) {
+      int start = 0, n = 0, len = 0, page = -1;
+      int64_t pos = -1;
+      if (paged_seq(c, s, &start, &n, &len) && tok >= start && tok < start + n) {
+        pos = static_cast<int64_t>(len) - n + (tok - start);
+        if (pos >= 0) page = paged_page(c, s, static_cast<int>(pos / c.page_size));
+      }
+      pos_s[i] = pos;
+      page_s[i] = pos < 0 ? -2 : page;
+      if (page >= 0) {
+        const int slot = static_cast<int>(pos % c.page_size);
+        slot_s[i] = page * c.page_stride + slot * c.token_stride;
+        scale_s[i] = static_cast<int64_t>(page) * c.Hkv * c.page_size + slot;
+      }
+    }
+  }
+}
+
+// cos and sin of the CTA's tokens, times the gain, 64 apart per token.
+__device__ __forceinline__ void turn_table(const RowsParams& p, int nt, const int64_t* pos_s,
+                                           float2* cs) {
+  const int half = p.R / 2;
+  for (int i = threadIdx.x; i < nt * half; i += kRowThreads) {
+    const int t = i / half, f = i - t * half;
+    const double turns = p.inv_freq[f] * 0.15915494309189533577;     // 1 / (2 pi)
+    const uint64_t frac = __double2ull_rn((turns - floor(turns)) * 18446744073709551616.0);
+    const uint64_t a = frac * static_cast<uint64_t>(pos_s[t]) + (1ull << 31);
+    float sn, cn;
+    sincospif(static_cast<float>(static_cast<int32_t>(a >> 32)) * 4.656612873077392578125e-10f,
+              &sn, &cn);                                             // 2^-31
+    cs[t * 64 + f] = make_float2(cn * p.mscale, sn * p.mscale * p.sign);
+  }
+}
+
 // kMode: 0 rope, 1 append 16-bit, 2 append Q8.  kLanes: lanes of a row.
 // kShfl: the half layout's partner vector is another lane's whole vector.
 template <int kMode, bool kBF16, int kLanes, bool kShfl>
@@ -127,7 +171,6 @@ rows_kernel(const RowsParams p) {
   __shared__ int64_t slot_s[kMaxToks], scale_s[kMaxToks];   // the slot of head 0, and its scale
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * p.toks;
   const int nt = static_cast<int>(min(static_cast<int64_t>(p.toks), p.T - t0));
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int half = p.R / 2;
   const PagedGeo& c = p.c;
 
@@ -138,39 +181,10 @@ rows_kernel(const RowsParams p) {
       page_s[threadIdx.x] = 0;
     }
   } else {
-    for (int i = warp; i < nt; i += kRowThreads / 32) {
-      const int64_t tok = t0 + i;
-      const int s = find_seq(c, tok, lane);
-      if (lane == 0) {
-        int start = 0, n = 0, len = 0, page = -1;
-        int64_t pos = -1;
-        if (paged_seq(c, s, &start, &n, &len) && tok >= start && tok < start + n) {
-          pos = static_cast<int64_t>(len) - n + (tok - start);
-          if (pos >= 0) page = paged_page(c, s, static_cast<int>(pos / c.page_size));
-        }
-        pos_s[i] = pos;
-        page_s[i] = pos < 0 ? -2 : page;
-        if (page >= 0) {
-          const int slot = static_cast<int>(pos % c.page_size);
-          slot_s[i] = page * c.page_stride + slot * c.token_stride;
-          scale_s[i] = static_cast<int64_t>(page) * c.Hkv * c.page_size + slot;
-        }
-      }
-    }
+    place_tokens(p, t0, nt, pos_s, page_s, slot_s, scale_s);
   }
   __syncthreads();
-  if (p.inv_freq != nullptr) {
-    for (int i = threadIdx.x; i < nt * half; i += kRowThreads) {
-      const int t = i / half, f = i - t * half;
-      const double turns = p.inv_freq[f] * 0.15915494309189533577;   // 1 / (2 pi)
-      const uint64_t frac = __double2ull_rn((turns - floor(turns)) * 18446744073709551616.0);
-      const uint64_t a = frac * static_cast<uint64_t>(pos_s[t]) + (1ull << 31);
-      float sn, cn;
-      sincospif(static_cast<float>(static_cast<int32_t>(a >> 32)) * 4.656612873077392578125e-10f,
-                &sn, &cn);                                           // 2^-31
-      cs[t * 64 + f] = make_float2(cn * p.mscale, sn * p.mscale * p.sign);
-    }
-  }
+  if (p.inv_freq != nullptr) turn_table(p, nt, pos_s, cs);
   __syncthreads();
 
   const int nq = p.Hq;
@@ -317,6 +331,203 @@ rows_kernel(const RowsParams p) {
   }
 }
 
+// ---- Q8 cache, many rows: arithmetic, not memory, bounds the kernel above there
+// (164 instructions for two rows of 80 channels).  Here a lane holds 16 channels
+// and a row ceil(D / 16) lanes, so that 80 channels fill 30 of 32 lanes with six
+// rows; the means and the values' multipliers come from a table of the CTA.
+
+__device__ __forceinline__ int wrap(int x, int n) { return x >= n ? x - n : x; }
+
+template <bool kBF16>
+__global__ void __launch_bounds__(kRowThreads)
+q8_rows_kernel(const RowsParams p) {
+  extern __shared__ __align__(16) float table[];        // means, multipliers, cos and sin
+  __shared__ int64_t pos_s[kMaxQ8Toks], slot_s[kMaxQ8Toks], scale_s[kMaxQ8Toks];
+  __shared__ int page_s[kMaxQ8Toks];
+  const PagedGeo& c = p.c;
+  const int entries = c.Hkv * c.Dp;
+  float* const mean = table;
+  float* const mult = table + entries;
+  float2* const cs = reinterpret_cast<float2*>(table + 2 * entries);
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * p.toks;
+  const int nt = static_cast<int>(min(static_cast<int64_t>(p.toks), p.T - t0));
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  place_tokens(p, t0, nt, pos_s, page_s, slot_s, scale_s);
+  for (int i = threadIdx.x; i < entries; i += kRowThreads) {
+    mean[i] = c.k_mean[i];
+    const float s = c.v_scale[i];
+    mult[i] = s > 0.0f ? __fdiv_rn(1.0f, s) : 0.0f;
+  }
+  __syncthreads();
+  if (p.inv_freq != nullptr) turn_table(p, nt, pos_s, cs);
+  __syncthreads();
+
+  const int per = (p.D + 15) / 16;                      // lanes of a row
+  const int fit = 32 / per;                             // rows of a warp
+  const int sub = lane % per, slot = lane / per;
+  const int base = slot * per, c0 = 16 * sub;
+  const bool two = c0 + 8 < p.D;                        // D % 16 == 8: the last lane has half
+  const int half = p.R / 2;
+  const int rows = p.Hq + 2 * p.Hkv;
+  const int groups = kRowThreads / 32 * fit;
+  const int stride = groups * gridDim.y;
+  int row = blockIdx.y * groups + warp * fit + slot, t = 0;
+  while (row >= rows) {
+    row -= rows;
+    ++t;
+  }
+  const int mate = base + (c0 < half ? wrap(sub + p.R / 32, per) : max(0, sub - p.R / 32));
+  // whole warps stay in the loop as long as one of their rows has a token left
+  while (__any_sync(kAll, slot < fit && t < nt)) {
+    const bool has = slot < fit && t < nt;
+    const int what = row < p.Hq ? 0 : row < p.Hq + p.Hkv ? 1 : 2;       // q, k, v
+    const int h = what == 0 ? row : what == 1 ? row - p.Hq : row - p.Hq - p.Hkv;
+    uint4 raw[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+    if (has) {
+      const uint16_t* src = (what == 0   ? p.q + (t0 + t) * p.q_tok + h * p.q_head
+                             : what == 1 ? p.k + (t0 + t) * p.k_tok + h * p.k_head
+                                         : p.v + (t0 + t) * p.v_tok + h * p.v_head) + c0;
+      raw[0] = *reinterpret_cast<const uint4*>(src);
+      if (two) raw[1] = *reinterpret_cast<const uint4*>(src + 8);
+    }
+    __syncwarp();                                       // in place: rows are read
+    float x[2][8];
+    unpack8<kBF16>(raw[0], x[0]);
+    unpack8<kBF16>(raw[1], x[1]);
+    if (p.inv_freq != nullptr) {
+      const float2* const a = cs + (has ? t : 0) * 64;
+      if (p.interleaved) {
+        if (what != 2) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (c0 + 2 * i < p.R) {
+              const float2 w = a[c0 / 2 + i];
+              float &x1 = x[i / 4][2 * (i % 4)], &x2 = x[i / 4][2 * (i % 4) + 1];
+              const float y1 = x1 * w.x - x2 * w.y;
+              x2 = x2 * w.x + x1 * w.y;
+              x1 = y1;
+            }
+        }
+      } else {                                          // R % 32 == 0: a lane's mate is one lane
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+          uint4 other;
+          other.x = __shfl_sync(kAll, raw[v].x, mate);
+          other.y = __shfl_sync(kAll, raw[v].y, mate);
+          other.z = __shfl_sync(kAll, raw[v].z, mate);
+          other.w = __shfl_sync(kAll, raw[v].w, mate);
+          float y[8];
+          unpack8<kBF16>(other, y);
+          if (what != 2 && c0 < p.R) {
+            const bool low = c0 < half;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float2 w = a[(low ? c0 : c0 - half) + 8 * v + e];
+              x[v][e] = low ? x[v][e] * w.x - y[e] * w.y : x[v][e] * w.x + y[e] * w.y;
+            }
+          }
+        }
+      }
+    }
+    float top = 0.0f;
+    if (what == 1) {
+      const float4* m4 = reinterpret_cast<const float4*>(mean + h * c.Dp + c0);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (i >= 2 && !two) break;
+        const float4 m = m4[i];
+        float* y = &x[i / 2][4 * (i % 2)];
+        y[0] = __fsub_rn(y[0], m.x);
+        y[1] = __fsub_rn(y[1], m.y);
+        y[2] = __fsub_rn(y[2], m.z);
+        y[3] = __fsub_rn(y[3], m.w);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) top = fmaxf(top, fabsf(y[e]));
+      }
+    }
+    // the row's largest, in every lane of the row
+    if ((per & (per - 1)) == 0) {
+      for (int d = 1; d < per; d *= 2) top = fmaxf(top, __shfl_xor_sync(kAll, top, d));
+    } else {
+      const float mine = top;
+      for (int k = 1; k < per; ++k)
+        top = fmaxf(top, __shfl_sync(kAll, mine, base + wrap(sub + k, per)));
+    }
+    const int page = has ? page_s[t] : -1;
+    if (has && what == 0 && page != -2) {
+      uint16_t* dst = p.q_out + (t0 + t) * p.qo_tok + h * p.qo_head + c0;
+      *reinterpret_cast<uint4*>(dst) = pack8<kBF16>(x[0]);
+      if (two) *reinterpret_cast<uint4*>(dst + 8) = pack8<kBF16>(x[1]);
+    }
+    if (has && what != 0 && page >= 0) {
+      uint32_t w[4];
+      if (what == 1) {
+        const float inv = top > 0.0f ? __fdiv_rn(127.0f, top) : 0.0f;
+        // rint by adding 1.5 * 2^23: the low byte is the code
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t b[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            b[e] = __float_as_uint(
+                __fadd_rn(__fmul_rn(x[i / 2][4 * (i % 2) + e], inv), 12582912.0f));
+          w[i] = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040),
+                             0x5410);
+        }
+        if (sub == 0)
+          c.k_scale[scale_s[t] + static_cast<int64_t>(h) * c.page_size] = __fdiv_rn(top, 127.0f);
+      } else {
+        const float4* m4 = reinterpret_cast<const float4*>(mult + h * c.Dp + c0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (i >= 2 && !two) {
+            w[i] = 0;
+            continue;
+          }
+          const float4 m = m4[i];
+          const float* y = &x[i / 2][4 * (i % 2)];
+          w[i] = pack_e4m3x2(__fmul_rn(y[0], m.x), __fmul_rn(y[1], m.y)) |
+                 pack_e4m3x2(__fmul_rn(y[2], m.z), __fmul_rn(y[3], m.w)) << 16;
+        }
+      }
+      uint8_t* dst = (what == 1 ? c.k : c.v) + slot_s[t] + h * c.head_stride + c0;
+      if (p.D % 16 == 0 && p.wide_slots) {
+        *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+      } else {                                          // slots on 8 bytes
+        *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+        if (two) *reinterpret_cast<uint2*>(dst + 8) = make_uint2(w[2], w[3]);
+      }
+    }
+    row += stride;
+    while (row >= rows) {
+      row -= rows;
+      ++t;
+    }
+    __syncwarp();
+  }
+}
+
+template <bool kBF16>
+cudaError_t launch_q8(const RowsParams& p0, int sms, cudaStream_t st) {
+  RowsParams p = p0;
+  p.toks = 1;
+  while (p.toks < kMaxQ8Toks && p.T / (2 * p.toks) >= 4 * sms) p.toks *= 2;
+  p.wide_slots = p.c.page_stride % 16 == 0 && p.c.token_stride % 16 == 0 &&
+                 p.c.head_stride % 16 == 0;
+  const int groups = kRowThreads / 32 * (32 / ((p.D + 15) / 16));
+  const int rows = p.Hq + 2 * p.Hkv;
+  const int64_t ctas = (p.T + p.toks - 1) / p.toks;
+  int64_t y = (static_cast<int64_t>(rows) * p.toks + groups - 1) / groups;
+  if (ctas * y > 2 * sms) y = 2 * sms / ctas > 1 ? 2 * sms / ctas : 1;
+  if (ctas > 0x7FFFFFFF) return cudaErrorInvalidValue;
+  const size_t smem = sizeof(float) * 2 * p.c.Hkv * p.c.Dp +
+                      (p.inv_freq != nullptr ? sizeof(float2) * 64 * p.toks : 0);
+  q8_rows_kernel<kBF16><<<dim3(static_cast<unsigned>(ctas), static_cast<unsigned>(y)), kRowThreads,
+                          smem, st>>>(p);
+  note_launch();
+  return cudaGetLastError();
+}
+
 template <int kMode, bool kBF16, int kLanes>
 cudaError_t launch_lanes(const RowsParams& p, bool shfl, dim3 grid, cudaStream_t st) {
   if (shfl) rows_kernel<kMode, kBF16, kLanes, true><<<grid, kRowThreads, 0, st>>>(p);
@@ -353,6 +564,11 @@ cudaError_t launch_mode(const RowsParams& p0, bool bf16, int sms, cudaStream_t s
 cudaError_t launch_rows(const RowsParams& p, int mode, bool bf16, int sms, cudaStream_t st) {
   if (mode == 0) return launch_mode<0>(p, bf16, sms, st);
   if (mode == 1) return launch_mode<1>(p, bf16, sms, st);
+  // the table of means and multipliers fits beside cos and sin; rotations whose
+  // partners lie in one lane of 16 channels
+  const bool table = p.c.Hkv * p.c.Dp <= kMaxQ8Table &&
+                     p.vec && (p.inv_freq == nullptr || p.interleaved || p.R % 32 == 0);
+  if (table) return bf16 ? launch_q8<true>(p, sms, st) : launch_q8<false>(p, sms, st);
   return launch_mode<2>(p, bf16, sms, st);
 }
 

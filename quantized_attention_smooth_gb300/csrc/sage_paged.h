@@ -46,6 +46,7 @@ struct RowsParams {
   float mscale, sign;        // sign -1: the inverse rotation
   int32_t vec;               // 16-byte rows: base, strides and D in whole vectors
   int32_t toks;              // tokens per CTA (set by the launcher)
+  int32_t wide_slots;        // 8-bit cache: slots start on 16 bytes (set by the launcher)
   PagedGeo c;                // sage_kv_append only
 };
 
