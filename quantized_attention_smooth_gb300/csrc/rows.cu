@@ -377,19 +377,35 @@ q8_rows_kernel(const RowsParams p) {
     ++t;
   }
   const int mate = base + (c0 < half ? wrap(sub + p.R / 32, per) : max(0, sub - p.R / 32));
+  auto kind_of = [&](int r) { return r < p.Hq ? 0 : r < p.Hq + p.Hkv ? 1 : 2; };   // q, k, v
+  auto head_of = [&](int r, int what) {
+    return what == 0 ? r : what == 1 ? r - p.Hq : r - p.Hq - p.Hkv;
+  };
+  // the next row's loads run during the present one's arithmetic
+  uint4 next[2];
+  auto load = [&](int r, int tok) {
+    next[0] = next[1] = make_uint4(0, 0, 0, 0);
+    if (slot < fit && tok < nt) {
+      const int what = kind_of(r), h = head_of(r, what);
+      const uint16_t* src = (what == 0   ? p.q + (t0 + tok) * p.q_tok + h * p.q_head
+                             : what == 1 ? p.k + (t0 + tok) * p.k_tok + h * p.k_head
+                                         : p.v + (t0 + tok) * p.v_tok + h * p.v_head) + c0;
+      next[0] = *reinterpret_cast<const uint4*>(src);
+      if (two) next[1] = *reinterpret_cast<const uint4*>(src + 8);
+    }
+  };
+  load(row, t);
   // whole warps stay in the loop as long as one of their rows has a token left
   while (__any_sync(kAll, slot < fit && t < nt)) {
     const bool has = slot < fit && t < nt;
-    const int what = row < p.Hq ? 0 : row < p.Hq + p.Hkv ? 1 : 2;       // q, k, v
-    const int h = what == 0 ? row : what == 1 ? row - p.Hq : row - p.Hq - p.Hkv;
-    uint4 raw[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-    if (has) {
-      const uint16_t* src = (what == 0   ? p.q + (t0 + t) * p.q_tok + h * p.q_head
-                             : what == 1 ? p.k + (t0 + t) * p.k_tok + h * p.k_head
-                                         : p.v + (t0 + t) * p.v_tok + h * p.v_head) + c0;
-      raw[0] = *reinterpret_cast<const uint4*>(src);
-      if (two) raw[1] = *reinterpret_cast<const uint4*>(src + 8);
+    const int what = kind_of(row), h = head_of(row, what);
+    const uint4 raw[2] = {next[0], next[1]};
+    int row2 = row + stride, t2 = t;
+    while (row2 >= rows) {
+      row2 -= rows;
+      ++t2;
     }
+    load(row2, t2);
     __syncwarp();                                       // in place: rows are read
     float x[2][8];
     unpack8<kBF16>(raw[0], x[0]);
@@ -498,11 +514,8 @@ q8_rows_kernel(const RowsParams p) {
         if (two) *reinterpret_cast<uint2*>(dst + 8) = make_uint2(w[2], w[3]);
       }
     }
-    row += stride;
-    while (row >= rows) {
-      row -= rows;
-      ++t;
-    }
+    row = row2;
+    t = t2;
     __syncwarp();
   }
 }
