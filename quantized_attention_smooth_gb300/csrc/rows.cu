@@ -33,8 +33,7 @@ namespace {
 
 constexpr int kRowThreads = 256;
 constexpr int kMaxToks = 8;          // tokens of one CTA
-constexpr int kMaxQ8Toks = 16;
-constexpr int kMaxQ8Table = 4096;    // kv heads x padded channels
+constexpr int kMaxQ8Toks = 64;
 constexpr unsigned kAll = 0xFFFFFFFFu;
 
 template <bool kBF16>
@@ -331,89 +330,77 @@ rows_kernel(const RowsParams p) {
   }
 }
 
-// ---- Q8 cache, many rows: arithmetic, not memory, bounds the kernel above there
-// (164 instructions for two rows of 80 channels).  Here a lane holds 16 channels
-// and a row ceil(D / 16) lanes, so that 80 channels fill 30 of 32 lanes with six
-// rows; the means and the values' multipliers come from a table of the CTA.
+// ---- Q8 cache: arithmetic, not memory, bounds the kernel above there (164
+// instructions for two rows of 80 channels).  Here a lane holds 16 channels and a
+// row ceil(D / 16) lanes, so that 80 channels fill 30 of 32 lanes with six rows;
+// K rows, V rows and q rows go in passes of their own (no warp does two kinds),
+// and a lane keeps its head through the CTA's tokens, with the head's means or
+// multipliers in registers.
 
 __device__ __forceinline__ int wrap(int x, int n) { return x >= n ? x - n : x; }
 
-template <bool kBF16>
-__global__ void __launch_bounds__(kRowThreads)
-q8_rows_kernel(const RowsParams p) {
-  extern __shared__ __align__(16) float table[];        // means, multipliers, cos and sin
-  __shared__ int64_t pos_s[kMaxQ8Toks], slot_s[kMaxQ8Toks], scale_s[kMaxQ8Toks];
-  __shared__ int page_s[kMaxQ8Toks];
-  const PagedGeo& c = p.c;
-  const int entries = c.Hkv * c.Dp;
-  float* const mean = table;
-  float* const mult = table + entries;
-  float2* const cs = reinterpret_cast<float2*>(table + 2 * entries);
-  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * p.toks;
-  const int nt = static_cast<int>(min(static_cast<int64_t>(p.toks), p.T - t0));
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  place_tokens(p, t0, nt, pos_s, page_s, slot_s, scale_s);
-  for (int i = threadIdx.x; i < entries; i += kRowThreads) {
-    mean[i] = c.k_mean[i];
-    const float s = c.v_scale[i];
-    mult[i] = s > 0.0f ? __fdiv_rn(1.0f, s) : 0.0f;
-  }
-  __syncthreads();
-  if (p.inv_freq != nullptr) turn_table(p, nt, pos_s, cs);
-  __syncthreads();
+struct Q8Tokens {
+  int64_t pos[kMaxQ8Toks], slot[kMaxQ8Toks], scale[kMaxQ8Toks];
+  int page[kMaxQ8Toks];
+};
 
-  const int per = (p.D + 15) / 16;                      // lanes of a row
-  const int fit = 32 / per;                             // rows of a warp
-  const int sub = lane % per, slot = lane / per;
+// kWhat: 0 q, 1 k, 2 v.
+template <int kWhat, bool kBF16>
+__device__ __forceinline__ void q8_pass(const RowsParams& p, const Q8Tokens& tk, const float2* cs,
+                                        int64_t t0, int nt) {
+  const PagedGeo& c = p.c;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int per = (p.D + 15) / 16, fit = 32 / per;      // lanes of a row; rows of a warp
+  const int slot = lane / per, sub = lane - slot * per;
   const int base = slot * per, c0 = 16 * sub;
   const bool two = c0 + 8 < p.D;                        // D % 16 == 8: the last lane has half
   const int half = p.R / 2;
-  const int rows = p.Hq + 2 * p.Hkv;
-  const int groups = kRowThreads / 32 * fit;
-  const int stride = groups * gridDim.y;
-  int row = blockIdx.y * groups + warp * fit + slot, t = 0;
-  while (row >= rows) {
-    row -= rows;
-    ++t;
-  }
+  const bool turn = kWhat != 2 && p.inv_freq != nullptr;
+  const int heads = kWhat == 0 ? p.Hq : p.Hkv;
+  const int groups = kRowThreads / 32 * fit, group = warp * fit + slot;
+  const int at_once = min(heads, groups);               // heads side by side
+  const int step = groups / at_once;                    // tokens side by side
+  const int tok0 = group / at_once, head0 = group - tok0 * at_once;
   const int mate = base + (c0 < half ? wrap(sub + p.R / 32, per) : max(0, sub - p.R / 32));
-  auto kind_of = [&](int r) { return r < p.Hq ? 0 : r < p.Hq + p.Hkv ? 1 : 2; };   // q, k, v
-  auto head_of = [&](int r, int what) {
-    return what == 0 ? r : what == 1 ? r - p.Hq : r - p.Hq - p.Hkv;
-  };
-  // the next row's loads run during the present one's arithmetic
-  uint4 next[2];
-  auto load = [&](int r, int tok) {
-    next[0] = next[1] = make_uint4(0, 0, 0, 0);
-    if (slot < fit && tok < nt) {
-      const int what = kind_of(r), h = head_of(r, what);
-      const uint16_t* src = (what == 0   ? p.q + (t0 + tok) * p.q_tok + h * p.q_head
-                             : what == 1 ? p.k + (t0 + tok) * p.k_tok + h * p.k_head
-                                         : p.v + (t0 + tok) * p.v_tok + h * p.v_head) + c0;
-      next[0] = *reinterpret_cast<const uint4*>(src);
-      if (two) next[1] = *reinterpret_cast<const uint4*>(src + 8);
+  const uint16_t* const rows = kWhat == 0 ? p.q : kWhat == 1 ? p.k : p.v;
+  const int64_t tok_stride = kWhat == 0 ? p.q_tok : kWhat == 1 ? p.k_tok : p.v_tok;
+  const int64_t head_stride = kWhat == 0 ? p.q_head : kWhat == 1 ? p.k_head : p.v_head;
+
+  for (int hb = 0; hb < heads; hb += at_once) {
+    const int h = hb + head0;
+    const bool mine = slot < fit && tok0 < step && h < heads;
+    float chan[16];                                     // k: means; v: 1 / scale
+    if (kWhat != 0) {
+      const float* src = (kWhat == 1 ? c.k_mean : c.v_scale) + h * c.Dp + c0;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        chan[e] = mine && c0 + e < p.D ? src[e] : 0.0f;
+        if (kWhat == 2) chan[e] = chan[e] > 0.0f ? __fdiv_rn(1.0f, chan[e]) : 0.0f;
+      }
     }
-  };
-  load(row, t);
-  // whole warps stay in the loop as long as one of their rows has a token left
-  while (__any_sync(kAll, slot < fit && t < nt)) {
-    const bool has = slot < fit && t < nt;
-    const int what = kind_of(row), h = head_of(row, what);
-    const uint4 raw[2] = {next[0], next[1]};
-    int row2 = row + stride, t2 = t;
-    while (row2 >= rows) {
-      row2 -= rows;
-      ++t2;
-    }
-    load(row2, t2);
-    __syncwarp();                                       // in place: rows are read
-    float x[2][8];
-    unpack8<kBF16>(raw[0], x[0]);
-    unpack8<kBF16>(raw[1], x[1]);
-    if (p.inv_freq != nullptr) {
-      const float2* const a = cs + (has ? t : 0) * 64;
-      if (p.interleaved) {
-        if (what != 2) {
+    const uint16_t* src = rows + (t0 + tok0) * tok_stride + h * head_stride + c0;
+    uint4 next[2];
+    auto load = [&](int t) {                            // runs a token ahead
+      next[0] = next[1] = make_uint4(0, 0, 0, 0);
+      if (mine && t < nt) {
+        next[0] = *reinterpret_cast<const uint4*>(src);
+        if (two) next[1] = *reinterpret_cast<const uint4*>(src + 8);
+      }
+      src += step * tok_stride;
+    };
+    load(tok0);
+    for (int tb = 0; tb < nt; tb += step) {
+      const int t = tb + tok0;
+      const bool has = mine && t < nt;
+      const uint4 raw[2] = {next[0], next[1]};
+      load(t + step);
+      __syncwarp();                                     // in place: rows are read
+      float x[2][8];
+      unpack8<kBF16>(raw[0], x[0]);
+      unpack8<kBF16>(raw[1], x[1]);
+      if (turn) {
+        const float2* const a = cs + (has ? t : 0) * 64;
+        if (p.interleaved) {
 #pragma unroll
           for (int i = 0; i < 8; ++i)
             if (c0 + 2 * i < p.R) {
@@ -423,61 +410,55 @@ q8_rows_kernel(const RowsParams p) {
               x2 = x2 * w.x + x1 * w.y;
               x1 = y1;
             }
-        }
-      } else {                                          // R % 32 == 0: a lane's mate is one lane
+        } else {                                        // R % 32 == 0: a lane's mate is one lane
+          const bool low = c0 < half;
 #pragma unroll
-        for (int v = 0; v < 2; ++v) {
-          uint4 other;
-          other.x = __shfl_sync(kAll, raw[v].x, mate);
-          other.y = __shfl_sync(kAll, raw[v].y, mate);
-          other.z = __shfl_sync(kAll, raw[v].z, mate);
-          other.w = __shfl_sync(kAll, raw[v].w, mate);
-          float y[8];
-          unpack8<kBF16>(other, y);
-          if (what != 2 && c0 < p.R) {
-            const bool low = c0 < half;
+          for (int v = 0; v < 2; ++v) {
+            uint4 other;
+            other.x = __shfl_sync(kAll, raw[v].x, mate);
+            other.y = __shfl_sync(kAll, raw[v].y, mate);
+            other.z = __shfl_sync(kAll, raw[v].z, mate);
+            other.w = __shfl_sync(kAll, raw[v].w, mate);
+            float y[8];
+            unpack8<kBF16>(other, y);
+            if (c0 < p.R) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float2 w = a[(low ? c0 : c0 - half) + 8 * v + e];
-              x[v][e] = low ? x[v][e] * w.x - y[e] * w.y : x[v][e] * w.x + y[e] * w.y;
+              for (int e = 0; e < 8; ++e) {
+                const float2 w = a[(low ? c0 : c0 - half) + 8 * v + e];
+                x[v][e] = low ? x[v][e] * w.x - y[e] * w.y : x[v][e] * w.x + y[e] * w.y;
+              }
             }
           }
         }
       }
-    }
-    float top = 0.0f;
-    if (what == 1) {
-      const float4* m4 = reinterpret_cast<const float4*>(mean + h * c.Dp + c0);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (i >= 2 && !two) break;
-        const float4 m = m4[i];
-        float* y = &x[i / 2][4 * (i % 2)];
-        y[0] = __fsub_rn(y[0], m.x);
-        y[1] = __fsub_rn(y[1], m.y);
-        y[2] = __fsub_rn(y[2], m.z);
-        y[3] = __fsub_rn(y[3], m.w);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) top = fmaxf(top, fabsf(y[e]));
+      const int page = has ? tk.page[t] : -1;
+      if constexpr (kWhat == 0) {
+        if (has && page != -2) {
+          uint16_t* dst = p.q_out + (t0 + t) * p.qo_tok + h * p.qo_head + c0;
+          *reinterpret_cast<uint4*>(dst) = pack8<kBF16>(x[0]);
+          if (two) *reinterpret_cast<uint4*>(dst + 8) = pack8<kBF16>(x[1]);
+        }
+        continue;
       }
-    }
-    // the row's largest, in every lane of the row
-    if ((per & (per - 1)) == 0) {
-      for (int d = 1; d < per; d *= 2) top = fmaxf(top, __shfl_xor_sync(kAll, top, d));
-    } else {
-      const float mine = top;
-      for (int k = 1; k < per; ++k)
-        top = fmaxf(top, __shfl_sync(kAll, mine, base + wrap(sub + k, per)));
-    }
-    const int page = has ? page_s[t] : -1;
-    if (has && what == 0 && page != -2) {
-      uint16_t* dst = p.q_out + (t0 + t) * p.qo_tok + h * p.qo_head + c0;
-      *reinterpret_cast<uint4*>(dst) = pack8<kBF16>(x[0]);
-      if (two) *reinterpret_cast<uint4*>(dst + 8) = pack8<kBF16>(x[1]);
-    }
-    if (has && what != 0 && page >= 0) {
       uint32_t w[4];
-      if (what == 1) {
+      if constexpr (kWhat == 1) {
+        float top = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          x[e / 8][e % 8] = __fsub_rn(x[e / 8][e % 8], chan[e]);
+          top = fmaxf(top, fabsf(x[e / 8][e % 8]));
+        }
+        // the row's largest, in every lane of the row
+        if ((per & (per - 1)) == 0) {
+          for (int d = 1; d < per; d *= 2) top = fmaxf(top, __shfl_xor_sync(kAll, top, d));
+        } else {
+          const float part = top;
+          int from = sub;
+          for (int k = 1; k < per; ++k) {
+            from = wrap(from + 1, per);
+            top = fmaxf(top, __shfl_sync(kAll, part, base + from));
+          }
+        }
         const float inv = top > 0.0f ? __fdiv_rn(127.0f, top) : 0.0f;
         // rint by adding 1.5 * 2^23: the low byte is the code
 #pragma unroll
@@ -490,33 +471,47 @@ q8_rows_kernel(const RowsParams p) {
           w[i] = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040),
                              0x5410);
         }
-        if (sub == 0)
-          c.k_scale[scale_s[t] + static_cast<int64_t>(h) * c.page_size] = __fdiv_rn(top, 127.0f);
+        if (sub == 0 && page >= 0)
+          c.k_scale[tk.scale[t] + static_cast<int64_t>(h) * c.page_size] = __fdiv_rn(top, 127.0f);
       } else {
-        const float4* m4 = reinterpret_cast<const float4*>(mult + h * c.Dp + c0);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          if (i >= 2 && !two) {
-            w[i] = 0;
-            continue;
-          }
-          const float4 m = m4[i];
           const float* y = &x[i / 2][4 * (i % 2)];
-          w[i] = pack_e4m3x2(__fmul_rn(y[0], m.x), __fmul_rn(y[1], m.y)) |
-                 pack_e4m3x2(__fmul_rn(y[2], m.z), __fmul_rn(y[3], m.w)) << 16;
+          w[i] = pack_e4m3x2(__fmul_rn(y[0], chan[4 * i]), __fmul_rn(y[1], chan[4 * i + 1])) |
+                 pack_e4m3x2(__fmul_rn(y[2], chan[4 * i + 2]), __fmul_rn(y[3], chan[4 * i + 3]))
+                     << 16;
         }
       }
-      uint8_t* dst = (what == 1 ? c.k : c.v) + slot_s[t] + h * c.head_stride + c0;
-      if (p.D % 16 == 0 && p.wide_slots) {
-        *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
-      } else {                                          // slots on 8 bytes
-        *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
-        if (two) *reinterpret_cast<uint2*>(dst + 8) = make_uint2(w[2], w[3]);
+      if (page >= 0) {
+        uint8_t* dst = (kWhat == 1 ? c.k : c.v) + tk.slot[t] + h * c.head_stride + c0;
+        if (p.wide_slots) {
+          *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+        } else {                                        // slots on 8 bytes
+          *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+          if (two) *reinterpret_cast<uint2*>(dst + 8) = make_uint2(w[2], w[3]);
+        }
       }
     }
-    row = row2;
-    t = t2;
-    __syncwarp();
+  }
+}
+
+template <bool kBF16>
+__global__ void __launch_bounds__(kRowThreads, 4)
+q8_rows_kernel(const RowsParams p) {
+  __shared__ float2 cs[kMaxQ8Toks * 64];
+  __shared__ Q8Tokens tk;
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * p.toks;
+  const int nt = static_cast<int>(min(static_cast<int64_t>(p.toks), p.T - t0));
+  place_tokens(p, t0, nt, tk.pos, tk.page, tk.slot, tk.scale);
+  __syncthreads();
+  if (p.inv_freq != nullptr) {
+    turn_table(p, nt, tk.pos, cs);
+    __syncthreads();
+  }
+  for (int what = blockIdx.y; what < 3; what += gridDim.y) {
+    if (what == 0) q8_pass<1, kBF16>(p, tk, cs, t0, nt);
+    else if (what == 1) q8_pass<2, kBF16>(p, tk, cs, t0, nt);
+    else if (p.Hq > 0) q8_pass<0, kBF16>(p, tk, cs, t0, nt);
   }
 }
 
@@ -525,18 +520,12 @@ cudaError_t launch_q8(const RowsParams& p0, int sms, cudaStream_t st) {
   RowsParams p = p0;
   p.toks = 1;
   while (p.toks < kMaxQ8Toks && p.T / (2 * p.toks) >= 4 * sms) p.toks *= 2;
-  p.wide_slots = p.c.page_stride % 16 == 0 && p.c.token_stride % 16 == 0 &&
+  p.wide_slots = p.D % 16 == 0 && p.c.page_stride % 16 == 0 && p.c.token_stride % 16 == 0 &&
                  p.c.head_stride % 16 == 0;
-  const int groups = kRowThreads / 32 * (32 / ((p.D + 15) / 16));
-  const int rows = p.Hq + 2 * p.Hkv;
   const int64_t ctas = (p.T + p.toks - 1) / p.toks;
-  int64_t y = (static_cast<int64_t>(rows) * p.toks + groups - 1) / groups;
-  if (ctas * y > 2 * sms) y = 2 * sms / ctas > 1 ? 2 * sms / ctas : 1;
   if (ctas > 0x7FFFFFFF) return cudaErrorInvalidValue;
-  const size_t smem = sizeof(float) * 2 * p.c.Hkv * p.c.Dp +
-                      (p.inv_freq != nullptr ? sizeof(float2) * 64 * p.toks : 0);
-  q8_rows_kernel<kBF16><<<dim3(static_cast<unsigned>(ctas), static_cast<unsigned>(y)), kRowThreads,
-                          smem, st>>>(p);
+  const unsigned y = ctas > 2 * sms ? 1 : p.Hq > 0 ? 3 : 2;    // few tokens: a CTA per pass
+  q8_rows_kernel<kBF16><<<dim3(static_cast<unsigned>(ctas), y), kRowThreads, 0, st>>>(p);
   note_launch();
   return cudaGetLastError();
 }
@@ -577,11 +566,9 @@ cudaError_t launch_mode(const RowsParams& p0, bool bf16, int sms, cudaStream_t s
 cudaError_t launch_rows(const RowsParams& p, int mode, bool bf16, int sms, cudaStream_t st) {
   if (mode == 0) return launch_mode<0>(p, bf16, sms, st);
   if (mode == 1) return launch_mode<1>(p, bf16, sms, st);
-  // the table of means and multipliers fits beside cos and sin; rotations whose
-  // partners lie in one lane of 16 channels
-  const bool table = p.c.Hkv * p.c.Dp <= kMaxQ8Table &&
-                     p.vec && (p.inv_freq == nullptr || p.interleaved || p.R % 32 == 0);
-  if (table) return bf16 ? launch_q8<true>(p, sms, st) : launch_q8<false>(p, sms, st);
+  // 16-byte rows, and rotations whose partners lie in one lane of 16 channels
+  if (p.vec && (p.inv_freq == nullptr || p.interleaved || p.R % 32 == 0))
+    return bf16 ? launch_q8<true>(p, sms, st) : launch_q8<false>(p, sms, st);
   return launch_mode<2>(p, bf16, sms, st);
 }
 
