@@ -11,14 +11,14 @@
 // few tokens of 2 or 4.  A contraction's order is free, so each lane takes the
 // operands as whole 16-byte vectors of the cache: 4 lanes cover 64 bytes of a
 // key for S^T, 8 lanes 128 bytes of a value row for O^T, and the fragments are
-// put together by byte permutes.  K and V therefore go from memory straight to
-// registers, with no shared memory and no barrier in the loop; the next
-// block's loads are in flight during the present block's arithmetic.  S^T's
-// accumulators become P^T's operands by an 8x8 register transpose.
+// put together by byte permutes.  Every warp streams blocks of 16 keys through a
+// ring of its own in shared memory, by asynchronous copies two or three blocks
+// ahead, with no barrier in the loop.  S^T's accumulators become P^T's operands
+// by an 8x8 register transpose.
 //
-// Work is cut into units of 4 warps x 16 keys and dealt evenly to a fixed grid: every CTA derives its own contiguous range
-// from the lengths (a scan over the sequences), so ragged batches balance and
-// no length comes to the host.  A (sequence, head) that spans CTAs leaves fp32
+// Work is cut into units of 4 warps x 16 keys and dealt evenly to a fixed grid:
+// every CTA derives its own contiguous range from the lengths (a scan over the
+// sequences), so ragged batches balance and no length comes to the host.  A (sequence, head) that spans CTAs leaves fp32
 // parts (max, sum, O) in the workspace, two per CTA at most; whoever finishes
 // last (or a second kernel) joins them in the order of their ranges, so results
 // do not depend on timing.
@@ -115,9 +115,22 @@ struct FewItem {
 
 // kForm: 0 D = Dp, every vector of a row is loaded; 1 vectors from D on are not; 2
 // so too, and rows of the 8-bit cache start on 8 bytes only (D % 16 == 8).
+// A warp's ring of blocks in shared memory, and the merge buffer that takes its
+// place at an item's end.
+template <int kKind, int kDp, int kNr>
+struct Few {
+  static constexpr int kRowB = kDp * (kKind == kKindQ8 ? 1 : 2);      // bytes of a row
+  static constexpr int kBlockB = 32 * kRowB + (kKind == kKindQ8 ? 64 : 0);   // K, V, scales
+  static constexpr int kStages = kRowB == 64 ? 4 : 3;
+  static constexpr int kPitch = kDp + 4;
+  static constexpr int kRing = kWarps * kStages * kBlockB;
+  static constexpr int kMerge = kWarps * 8 * kNr * kPitch * 4;
+  static constexpr int kSmem = kRing > kMerge ? kRing : kMerge;
+  static constexpr int kCtas = kRowB == 256 || kNr > 2 ? 2 : kNr == 2 ? (kDp == 128 ? 2 : 3) : 4;
+};
+
 template <int kKind, bool kQBF16, int kDp, int kNr, int kForm>
-__global__ void __launch_bounds__(kThreads, kDp == 64 ? (kNr == 1 ? 4 : kNr < 4 ? 3 : 2)
-                                                 : kNr > 1 ? 2 : kKind == kKindQ8 ? 4 : 3)
+__global__ void __launch_bounds__(kThreads, Few<kKind, kDp, kNr>::kCtas)
 paged_few_kernel(const PagedAttnParams p) {
   constexpr bool kQ8 = kKind == kKindQ8;
   constexpr bool kMmaBF16 = kKind == kKindBF16;
@@ -128,19 +141,33 @@ paged_few_kernel(const PagedAttnParams p) {
   constexpr int kVw = kQ8 ? kDp / 32 : kDp / 16;          // words of a value per lane
   constexpr int kSteps = kDp / 16;                        // k-steps of S^T
   constexpr int kMt = kDp / 16;                           // 16-channel tiles of O^T
-  constexpr int kPitch = kDp + 4;
+  using L = Few<kKind, kDp, kNr>;
+  constexpr int kPitch = L::kPitch, kRowB = L::kRowB, kStages = L::kStages;
+  constexpr int kChunks = kRowB / 16;                     // 16-byte vectors of a row
+  extern __shared__ __align__(16) uint8_t ring_s[];
+  float (*const acc_s)[kRows * kPitch] = reinterpret_cast<float (*)[kRows * kPitch]>(ring_s);
   __shared__ int64_t scan_s[kWarps];
   __shared__ FewItem it;
   __shared__ float m_s[kWarps][kRows], l_s[kWarps][kRows];
-  __shared__ __align__(16) float acc_s[kWarps][kRows * kPitch];
 
   const PagedGeo& c = p.c;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t = lane & 3;
   const int cta = blockIdx.x, ctas = gridDim.x;
   const int64_t ts = c.token_stride * kEl;
-  // channels from this lane's first one on, of a key and of a value
-  const int k_left = c.D - 16 / kEl * t, v_left = c.D - (kVw == 2 ? 8 : 16 / kEl) * g;
+  uint8_t* const ring = ring_s + warp * kStages * L::kBlockB;
+  // Copies: lane -> vector lc of every kRows32-th row.  A vector's place in its row
+  // is turned by the row, so that the reads below hit every bank once.
+  constexpr int kRows32 = 32 / kChunks;
+  const int lc = lane % kChunks, lr = lane / kChunks;
+  const int lc_left = c.D - lc * (16 / kEl);              // channels from the vector's first on
+  auto k_at = [](int row, int vec) {
+    return row * kRowB + ((kChunks >= 8 ? vec ^ ((row & 1) << 2) : vec) << 4);
+  };
+  auto v_at = [](int row, int vec) {
+    return (16 + row) * kRowB +
+           ((kChunks >= 8 ? vec ^ (row & 6) : vec ^ ((row >> 1) & 3)) << 4);
+  };
   if (!p.join_inside) asm volatile("griddepcontrol.launch_dependents;");
 
   // ---- this CTA's range of units
@@ -228,10 +255,8 @@ paged_few_kernel(const PagedAttnParams p) {
       const int lo_hi = p.window > 0 ? max(0, p_hi - p.window + 1) : 0;     // of the last row
 
       const int32_t* const table = c.table + s * c.table_stride;
-      // this lane's place in a block's keys and values (bytes)
-      const uint8_t* const k_lane = c.k + (kvh * c.head_stride + g * c.token_stride) * kEl + 16 * t;
-      const uint8_t* const v_lane = c.v + (kvh * c.head_stride + 2 * t * c.token_stride) * kEl +
-                                    (kVw == 2 ? 8 : 16) * g;
+      // this lane's vector in a block's keys and values (bytes)
+      const int64_t lane_off = (kvh * c.head_stride + lr * c.token_stride) * kEl + 16 * lc;
 
       // ---- the rows' queries, as the B operand of S^T
       uint32_t qw[kNr][kDp / 8];
@@ -297,139 +322,117 @@ paged_few_kernel(const PagedAttnParams p) {
           for (int e = 0; e < 4; ++e) o[j][nr][e] = 0.0f;
       }
 
-      // (vectors of channels from D on are never loaded and stay zero)
-      uint32_t kw[2][kKw], vw[4][kVw];
-#pragma unroll
-      for (int i = 0; i < kKw; ++i) kw[0][i] = kw[1][i] = 0;
-#pragma unroll
-      for (int i = 0; i < kVw; ++i) vw[0][i] = vw[1][i] = vw[2][i] = vw[3][i] = 0;
-      float ks[2] = {0.0f, 0.0f};
-      // A step is a block of 16 keys: its first key (-1: none), the table's entry,
-      // and where the block's keys begin in the head (bytes; -1: nothing to read).
-      int key0 = -1, next_key0 = -1, next_page = -1;
-      int64_t at = -1, scale_at = 0;
-      bool whole = false;                       // some row sees every key of the block
-      auto locate = [&](int unit) {
+      // Vectors of channels from D on are never loaded: zero once.
+      if (kForm != 0) {
+        for (int i = lane; i < kStages * L::kBlockB / 16; i += 32)
+          reinterpret_cast<uint4*>(ring)[i] = make_uint4(0, 0, 0, 0);
+        __syncwarp();
+      }
+      // A step is a block of 16 keys.  Its first key (-1: none that a row sees):
+      auto key_of = [&](int unit) {
         const int vb = unit * kWarps + warp;
         const int k0 = 16 * (vb < sp.sink ? vb : vb - sp.sink + sp.from);
-        next_key0 = next_page = -1;
-        if (vb < sp.count && k0 <= p_hi && (k0 + 15 >= lo || k0 < sinks)) {
-          next_key0 = k0;
-          next_page = table[page_of(c, k0)];    // used a step later
-        }
+        return vb < sp.count && k0 <= p_hi && (k0 + 15 >= lo || k0 < sinks) ? k0 : -1;
       };
-      auto resolve = [&]() {
-        key0 = next_key0;
-        at = -1;
-        whole = false;
-        if (key0 >= 0) {
-          if (static_cast<uint32_t>(next_page) < static_cast<uint32_t>(c.num_pages)) {
-            const int slot = key0 - page_of(c, key0) * c.page_size;
+      auto seen = [&](int j) { return j <= p_hi && (j >= lo || j < sinks); };
+      int next_key0 = -1, next_page = -1;
+      auto locate = [&](int unit) {             // the table's entry, used a step later
+        next_key0 = key_of(unit);
+        if (next_key0 >= 0) next_page = table[page_of(c, next_key0)];
+      };
+      // Starts the copies of the located block into a stage; rows that no row of
+      // the tile sees become zero (0 times what lies there could be NaN).
+      auto issue = [&](int stage) {
+        const int k0 = next_key0;
+        if (k0 >= 0) {
+          int64_t at = 0;
+          const bool there =
+              static_cast<uint32_t>(next_page) < static_cast<uint32_t>(c.num_pages);
+          const uint32_t dst = smem_u32(ring + stage * L::kBlockB);
+          const float* scales = c.k_scale;
+          if (there) {
+            const int slot = k0 - page_of(c, k0) * c.page_size;
             at = (next_page * c.page_stride + static_cast<int64_t>(slot) * c.token_stride) * kEl;
             if (kQ8)
-              scale_at = (static_cast<int64_t>(next_page) * c.Hkv + kvh) * c.page_size + slot + g;
-            whole = key0 + 15 <= p_hi && (key0 >= lo || key0 + 15 < sinks);
+              scales += (static_cast<int64_t>(next_page) * c.Hkv + kvh) * c.page_size + slot +
+                        4 * (lane & 3);
           } else if (lane == 0) {
             atomicOr(c.status, kStatusBadPage);
           }
-        }
-      };
-      auto seen = [&](int j) { return j <= p_hi && (j >= lo || j < sinks); };
-      auto load_k = [&]() {
-        const uint8_t* const row = k_lane + at;
-        if (whole) {
+          if (kQ8 && lane < 4)
+            copy16(dst + 32 * kRowB + 16 * lane, reinterpret_cast<const uint8_t*>(scales),
+                   there ? 16 : 0);
+          const bool whole = there && k0 + 15 <= p_hi && (k0 >= lo || k0 + 15 < sinks);
+          const uint8_t* src_k = c.k + at + lane_off;
+          const uint8_t* src_v = c.v + at + lane_off;
+          const int64_t down = kRows32 * ts;
 #pragma unroll
-          for (int y = 0; y < 2; ++y)
-#pragma unroll
-            for (int i = 0; i < kKw / 4; ++i)
-              ld16_part<kEl, kForm>(&kw[y][4 * i], row + y * 8 * ts + 64 * i,
-                                            k_left - 64 / kEl * i);
-          if constexpr (kQ8) {
-            ks[0] = c.k_scale[scale_at];
-            ks[1] = c.k_scale[scale_at + 8];
-          }
-          return;
-        }
-#pragma unroll
-        for (int y = 0; y < 2; ++y) {
-#pragma unroll
-          for (int i = 0; i < kKw; ++i) kw[y][i] = 0;
-          ks[y] = 0.0f;
-          if (at >= 0 && seen(key0 + g + 8 * y)) {
-#pragma unroll
-            for (int i = 0; i < kKw / 4; ++i)
-              ld16_part<kEl, kForm>(&kw[y][4 * i], row + y * 8 * ts + 64 * i,
-                                            k_left - 64 / kEl * i);
-            if constexpr (kQ8) ks[y] = c.k_scale[scale_at + 8 * y];
+          for (int i = 0; i < 16 / kRows32; ++i) {
+            const int row = lr + i * kRows32;
+            const bool see = whole || (there && seen(k0 + row));
+            copy_part<kForm>(dst + k_at(row, lc), see ? src_k : c.k, see, lc_left);
+            copy_part<kForm>(dst + v_at(row, lc), see ? src_v : c.v, see, lc_left);
+            src_k += down;
+            src_v += down;
           }
         }
-      };
-      auto load_v = [&]() {
-        const uint8_t* const row = v_lane + at;
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          const uint8_t* const r = row + ((y & 1) + 8 * (y >> 1)) * ts;
-          if (whole) {
-            if constexpr (kVw == 2) {
-              if (kForm == 0 || v_left > 0) ld8(vw[y], r);
-            } else {
-#pragma unroll
-              for (int i = 0; i < kVw / 4; ++i)
-                ld16_part<kEl, kForm>(&vw[y][4 * i], r + 128 * i, v_left - 128 / kEl * i);
-            }
-            continue;
-          }
-#pragma unroll
-          for (int i = 0; i < kVw; ++i) vw[y][i] = 0;
-          if (at >= 0 && seen(key0 + 2 * t + (y & 1) + 8 * (y >> 1))) {
-            if constexpr (kVw == 2) {
-              if (kForm == 0 || v_left > 0) ld8(vw[y], r);
-            } else {
-#pragma unroll
-              for (int i = 0; i < kVw / 4; ++i)
-                ld16_part<kEl, kForm>(&vw[y][4 * i], r + 128 * i,
-                                              v_left - 128 / kEl * i);
-            }
-          }
-        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
       };
 
+      const int end_unit = first_unit + count;
       locate(first_unit);
-      resolve();
-      load_k();
-      load_v();
-      if (count > 1) locate(first_unit + 1);
-      for (int u = first_unit; u < first_unit + count; ++u) {
-        const bool more = u + 1 < first_unit + count;
+#pragma unroll
+      for (int i = 0; i < kStages - 1; ++i) {
+        issue(i);
+        next_key0 = -1;
+        if (first_unit + i + 1 < end_unit) locate(first_unit + i + 1);
+      }
+      int stage = 0;
+      for (int u = first_unit; u < end_unit; ++u) {
+        asm volatile("cp.async.wait_group %0;" :: "n"(kStages - 2) : "memory");
+        __syncwarp();                           // every lane's copies; and the last stage is read
+        issue(stage == 0 ? kStages - 1 : stage - 1);
+        next_key0 = -1;
+        if (u + kStages < end_unit) locate(u + kStages);
+        const uint8_t* const block = ring + stage * L::kBlockB;
+        stage = stage + 1 == kStages ? 0 : stage + 1;
         // ---- S^T, in two chains of products
-        const int cur0 = key0;
+        const int cur0 = key_of(u);
+        if (cur0 < 0) continue;
         float x[kNr][4], x2[kNr][4];
 #pragma unroll
         for (int nr = 0; nr < kNr; ++nr)
 #pragma unroll
           for (int e = 0; e < 4; ++e) x[nr][e] = x2[nr][e] = 0.0f;
 #pragma unroll
-        for (int i = 0; i < kSteps; ++i) {
-          uint32_t a0, a1, a2, a3;
-          if constexpr (kQ8) {
-            int8_to_half(kw[0][i], a0, a2);
-            int8_to_half(kw[1][i], a1, a3);
-          } else {
-            a0 = kw[0][2 * i]; a2 = kw[0][2 * i + 1];
-            a1 = kw[1][2 * i]; a3 = kw[1][2 * i + 1];
-          }
+        for (int v = 0; v < kKw / 4; ++v) {
+          const uint4 ka = *reinterpret_cast<const uint4*>(block + k_at(g, 4 * v + t));
+          const uint4 kb = *reinterpret_cast<const uint4*>(block + k_at(g + 8, 4 * v + t));
+          const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
+          constexpr int kPer = kQ8 ? 4 : 2;     // k-steps of a vector
 #pragma unroll
-          for (int nr = 0; nr < kNr; ++nr)
-            mma<kMmaBF16>((i & 1) ? x2[nr] : x[nr], a0, a1, a2, a3, qw[nr][2 * i],
-                          qw[nr][2 * i + 1]);
+          for (int i = 0; i < kPer; ++i) {
+            uint32_t a0, a1, a2, a3;
+            if constexpr (kQ8) {
+              int8_to_half(wa[i], a0, a2);
+              int8_to_half(wb[i], a1, a3);
+            } else {
+              a0 = wa[2 * i]; a2 = wa[2 * i + 1];
+              a1 = wb[2 * i]; a3 = wb[2 * i + 1];
+            }
+            const int step = kPer * v + i;
+#pragma unroll
+            for (int nr = 0; nr < kNr; ++nr)
+              mma<kMmaBF16>((step & 1) ? x2[nr] : x[nr], a0, a1, a2, a3, qw[nr][2 * step],
+                            qw[nr][2 * step + 1]);
+          }
         }
-        const float s0 = kQ8 ? ks[0] : 1.0f, s1 = kQ8 ? ks[1] : 1.0f;
-        if (more) {
-          resolve();
-          load_k();
-          if (u + 2 < first_unit + count) locate(u + 2);
+        float ks[2] = {1.0f, 1.0f};
+        if constexpr (kQ8) {
+          ks[0] = reinterpret_cast<const float*>(block + 32 * kRowB)[g];
+          ks[1] = reinterpret_cast<const float*>(block + 32 * kRowB)[g + 8];
         }
-        if (cur0 >= 0) {
+        {
           // ---- logits, masks, running maximum and sum
           const bool full =
               cur0 + 15 <= p_lo && (cur0 >= lo_hi || cur0 + 15 < sinks);
@@ -439,7 +442,7 @@ paged_few_kernel(const PagedAttnParams p) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               float v = (x[nr][e] + x2[nr][e]) * rs[nr][e & 1];
-              if constexpr (kQ8) v *= (e >> 1) ? s1 : s0;
+              if constexpr (kQ8) v *= ks[e >> 1];
               if (!full) {
                 const int j = cur0 + g + 8 * (e >> 1);
                 const int pos = rpos[nr][e & 1];
@@ -490,6 +493,26 @@ paged_few_kernel(const PagedAttnParams p) {
             pb[nr][0] = transpose8x8(pack2<kMmaBF16>(e4[0], e4[1]));
             pb[nr][1] = transpose8x8(pack2<kMmaBF16>(e4[2], e4[3]));
           }
+          uint32_t vw[4][kVw];
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const int row = 2 * t + (y & 1) + 8 * (y >> 1);
+            if constexpr (kVw == 2) {
+              const uint2 v = *reinterpret_cast<const uint2*>(block + v_at(row, g / 2) +
+                                                              8 * (g & 1));
+              vw[y][0] = v.x;
+              vw[y][1] = v.y;
+            } else {
+#pragma unroll
+              for (int i = 0; i < kVw / 4; ++i) {
+                const uint4 v = *reinterpret_cast<const uint4*>(block + v_at(row, g + 8 * i));
+                vw[y][4 * i] = v.x;
+                vw[y][4 * i + 1] = v.y;
+                vw[y][4 * i + 2] = v.z;
+                vw[y][4 * i + 3] = v.w;
+              }
+            }
+          }
           // operands of O^T's j-th tile: a0, a1 of keys 2t, 2t + 1 and the tile's two
           // halves of channels, a2, a3 of the keys 8 further
           auto product = [&](int j, const uint32_t (&a)[4]) {
@@ -525,8 +548,9 @@ paged_few_kernel(const PagedAttnParams p) {
             }
           }
         }
-        if (more) load_v();
       }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      __syncthreads();                          // the rings become the merge buffer
 
       // ---- join the warps
 #pragma unroll
@@ -752,14 +776,21 @@ cudaError_t launch_few(const PagedAttnParams& p, int sms, cudaStream_t st) {
       return launch_few<kKind, kQBF16, kDp, kNr, kKind == kKindQ8 ? 2 : 1>(p, sms, st);
     if (p.c.D != kDp) return launch_few<kKind, kQBF16, kDp, kNr, 1>(p, sms, st);
   }
+  using L = Few<kKind, kDp, kNr>;
   auto* kern = paged_few_kernel<kKind, kQBF16, kDp, kNr, kForm>;
-  static std::atomic<int> resident{0};       // CTAs of one SM (every GB300 is alike)
-  int per = resident.load(std::memory_order_relaxed);
+  static std::atomic<int> resident[64] = {};   // CTAs of one SM, per device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  int per = resident[dev].load(std::memory_order_relaxed);
   if (per == 0) {
-    const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kern, kThreads, 0);
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
+    if (e == cudaSuccess)
+      e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kern, kThreads, L::kSmem);
     if (e != cudaSuccess) return e;
     per = per < 1 ? 1 : per > 8 ? 8 : per;
-    resident.store(per, std::memory_order_relaxed);
+    resident[dev].store(per, std::memory_order_relaxed);
   }
   // at most one CTA per unit of the longest lengths the call declares
   constexpr int kUnitKeys = 16 * kWarps;
@@ -773,9 +804,9 @@ cudaError_t launch_few(const PagedAttnParams& p, int sms, cudaStream_t st) {
   // parts or more, and a second kernel does it by the row.
   PagedAttnParams prm = p;
   prm.join_inside = items * kJoinInside >= ctas;
-  kern<<<ctas, kThreads, 0, st>>>(prm);
+  kern<<<ctas, kThreads, L::kSmem, st>>>(prm);
   note_launch();
-  cudaError_t e = cudaGetLastError();
+  e = cudaGetLastError();
   if (e != cudaSuccess || prm.join_inside) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(ctas), 8 * kNr);

@@ -69,24 +69,26 @@ __device__ __forceinline__ uint32_t e4m3x2_to_half2(uint32_t two) {
   return r;
 }
 
-__device__ __forceinline__ void ld16(uint32_t* w, const uint8_t* p) {
-  asm volatile("ld.global.L1::no_allocate.L2::128B.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "l"(p));
+// Asynchronous copies to shared memory of 16 or 8 bytes; `bytes` of them are read,
+// the rest is zero.
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;"
+               :: "r"(dst), "l"(src), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ void ld8(uint32_t* w, const uint8_t* p) {
-  asm volatile("ld.global.L1::no_allocate.L2::128B.v2.u32 {%0,%1}, [%2];"
-               : "=r"(w[0]), "=r"(w[1]) : "l"(p));
+__device__ __forceinline__ void copy8(uint32_t dst, const uint8_t* src, int bytes) {
+  asm volatile("cp.async.ca.shared.global.L2::128B [%0], [%1], 8, %2;"
+               :: "r"(dst), "l"(src), "r"(bytes) : "memory");
 }
-// 16 bytes of a row of the cache that ends after `left` more elements of kEl
-// bytes (untouched where none are left).  kForm 0: all are there; 2: rows start
-// on 8 bytes only.
-template <int kEl, int kForm>
-__device__ __forceinline__ void ld16_part(uint32_t* w, const uint8_t* p, int left) {
+// A vector of a row that ends after `left` more elements (untouched where none
+// are left), zero unless `see`.  kForm 0: all are there; 2: rows of 8 bits that
+// start on 8 bytes only.
+template <int kForm>
+__device__ __forceinline__ void copy_part(uint32_t dst, const uint8_t* src, bool see, int left) {
   if constexpr (kForm == 2) {
-    if (left > 0) ld8(w, p);
-    if (left > 8) ld8(w + 2, p + 8);
+    if (left > 0) copy8(dst, src, see ? 8 : 0);
+    if (left > 8) copy8(dst + 8, see ? src + 8 : src, see ? 8 : 0);
   } else {
-    if (kForm == 0 || left > 0) ld16(w, p);
+    if (kForm == 0 || left > 0) copy16(dst, src, see ? 16 : 0);
   }
 }
 
