@@ -139,7 +139,6 @@ paged_few_kernel(const PagedAttnParams p) {
   constexpr int kEl = kQ8 ? 1 : 2;                        // bytes of an element
   constexpr int kKw = kQ8 ? kDp / 16 : kDp / 8;           // words of a key per lane
   constexpr int kVw = kQ8 ? kDp / 32 : kDp / 16;          // words of a value per lane
-  constexpr int kSteps = kDp / 16;                        // k-steps of S^T
   constexpr int kMt = kDp / 16;                           // 16-channel tiles of O^T
   using L = Few<kKind, kDp, kNr>;
   constexpr int kPitch = L::kPitch, kRowB = L::kRowB, kStages = L::kStages;

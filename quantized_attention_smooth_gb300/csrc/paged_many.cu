@@ -53,7 +53,7 @@ constexpr uint32_t kTmemCols = 512;
 constexpr unsigned kAll = 0xFFFFFFFFu;
 // Units that an item costs besides its key tiles: filling and draining the
 // pipeline takes about as long as this many tiles.
-constexpr int kItemUnits = 2;
+constexpr int kItemUnits = 4;
 constexpr float kLazy = 8.0f;             // log2 of the growth that rescales O
 
 struct ManyHead {
@@ -644,7 +644,10 @@ paged_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
       // ================================================== MMAs
       constexpr uint32_t kFmt = kMmaBF16 ? 1u : 0u;
       constexpr uint32_t kIdQk = make_idesc(kFmt, kFmt, kTileRows, kKeys);
-      constexpr uint32_t kIdPv = make_idesc(kFmt, kFmt, kTileRows, kDp) | (1u << 16);
+      // only the caller's channels, in 16s: k-steps of S, columns of O
+      const int d16 = (c.D + 15) / 16;
+      const uint32_t id_pv = uniform(make_idesc(kFmt, kFmt, kTileRows, 16) & ~(0x3Fu << 17) |
+                                     (static_cast<uint32_t>(2 * d16) << 17) | (1u << 16));
       const uint32_t q_lo = sdesc_sw128_lo(smem_u32(smem));
       const uint32_t ring_lo = sdesc_sw128_lo(smem_u32(smem + L::kRingOff));
       // V: rows of 64 channels contiguous (MN-major), the next 64 channels a panel
@@ -655,11 +658,21 @@ paged_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
       // S_t = Q_t K^T and O_t (+)= P_t V, for one elected lane
       auto qk = [&](auto tc, uint32_t k_lo) {
         constexpr int t = decltype(tc)::value;
+        if (d16 == kDp / 16) {
+#pragma unroll
+          for (int k = 0; k < kDp / 16; ++k) {
+            const uint32_t off = ((k / 4) * L::kPanel + (k % 4) * 32) >> 4;
+            mma_f16_ss_lo(tb + t * 128, q_lo + ((t * L::kTileBytes) >> 4) + off, k_lo + off, kIdQk,
+                          k > 0 ? 1u : 0u);
+          }
+          return;
+        }
 #pragma unroll
         for (int k = 0; k < kDp / 16; ++k) {
           const uint32_t off = ((k / 4) * L::kPanel + (k % 4) * 32) >> 4;
-          mma_f16_ss_lo(tb + t * 128, q_lo + ((t * L::kTileBytes) >> 4) + off, k_lo + off, kIdQk,
-                        k > 0 ? 1u : 0u);
+          if (k < d16)
+            mma_f16_ss_lo(tb + t * 128, q_lo + ((t * L::kTileBytes) >> 4) + off, k_lo + off, kIdQk,
+                          k > 0 ? 1u : 0u);
         }
       };
       auto pv = [&](auto tc, uint32_t val_lo, uint32_t add) {
@@ -667,7 +680,7 @@ paged_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
 #pragma unroll
         for (int k = 0; k < kKeys / 16; ++k)
           mma_ts(tb + 256 + t * kDp, tb + t * 128 + 8 * k, val_lo + ((k * 2048) >> 4),
-                 kSdescSw128Hi, kIdPv, k > 0 ? 1u : add);
+                 kSdescSw128Hi, id_pv, k > 0 ? 1u : add);
       };
       constexpr std::integral_constant<int, 0> T0{};
       constexpr std::integral_constant<int, 1> T1{};
