@@ -65,6 +65,23 @@ def test_chunks(sage, kind, dt, page, layout, both, q_lens, kv_lens):
 
 
 @pytest.mark.parametrize("kind,dt", KINDS)
+@pytest.mark.parametrize("d", [8, 40, 56, 72, 104, 112, 120])
+@pytest.mark.parametrize("page,layout,both", [(16, "HND", False), (80, "NHD", True),
+                                              (64, "NHD", False), (384, "HND", True)])
+def test_chunks_of_odd_head_sizes(sage, kind, dt, d, page, layout, both):
+    check(sage, Problem([140, 30, 1], [140, 400, 300], 6, 2, d, page, layout, kind, dt, seed=d,
+                        both=both))
+
+
+@pytest.mark.parametrize("kind,dt", KINDS)
+@pytest.mark.parametrize("group", [1, 3, 7, 16, 40, 129])
+@pytest.mark.parametrize("q_lens,kv_lens", [([1, 1], [90, 700]), ([4, 37], [60, 300])])
+def test_groups(sage, kind, dt, group, q_lens, kv_lens):
+    """Any number of query heads on a kv head, also more than a row tile holds."""
+    check(sage, Problem(q_lens, kv_lens, group, 1, 64, 32, "NHD", kind, dt, seed=group))
+
+
+@pytest.mark.parametrize("kind,dt", KINDS)
 @pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (7, 3), (16, 16), (100, 0), (100, 40),
                                           (129, 5), (600, 2), (5000, 4), (30, 2000)])
 @pytest.mark.parametrize("q_lens,kv_lens,d", [([1, 5, 1, 33], [700, 700, 20, 64], 64),
@@ -227,6 +244,27 @@ def test_graphs_share_a_workspace(sage, kind):
             p.kv_lens = lens
             check(sage, p)
     assert sage.device_status(ws) == sage.OK
+
+
+@pytest.mark.parametrize("kind", ["bf16", "q8"])
+def test_two_calls_at_once(sage, kind):
+    """Calls on two streams, each with its own workspace, do not disturb each other."""
+    ps = [Problem([1, 1, 90], [4000, 300, 900], 8, 2, 128, 16, "NHD", kind, seed=s)
+          for s in (18, 19)]
+    want = [check(sage, p) for p in ps]
+    args = [p.sage(sage) + (p.q,) for p in ps]
+    ws = [sage.alloc_workspace_paged() for _ in ps]
+    streams = [torch.cuda.Stream() for _ in ps]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(sage.attn_paged(*args[i], ws=ws[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert sage.device_status(ws[i]) == sage.OK
+        assert all(torch.equal(x, want[i]) for x in got[i])
 
 
 def test_another_stream(sage):
