@@ -479,21 +479,26 @@ def rope_freqs(rotary_dim, base=10000.0, scaling=None, factor=1.0, original_len=
 # The serving calls run in a few microseconds on the GPU, so their wrappers do:
 # plain integers for pointers, one look at the current device, and no torch call
 # that a tensor's own methods can answer.
-_torch = None
+_torch = _get_device = _get_stream = _empty_like = None
+
+
+def _bind_torch():
+    global _torch, _get_device, _get_stream, _empty_like
+    import torch
+    _torch, _empty_like = torch, torch.empty_like
+    _get_device, _get_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+    _CODES.update({torch.float16: F16, torch.bfloat16: BF16})
 
 
 def _device(where, name, t):
     """(index of the current device, its current stream's handle); t, the
     call's first tensor, is on a CUDA device."""
-    global _torch
     if not t.is_cuda:
         _off_device(where, name, t, None)
     if _torch is None:
-        import torch
-        _torch = torch
-        _CODES.update({torch.float16: F16, torch.bfloat16: BF16})
-    d = _torch._C._cuda_getDevice()
-    return d, _torch._C._cuda_getCurrentRawStream(d)
+        _bind_torch()
+    d = _get_device()
+    return d, _get_stream(d)
 
 
 def _off_device(where, name, t, dev):
@@ -507,12 +512,14 @@ def _rows3(where, name, t, dev):
     device, channel stride 1.  Returns its shape and the {token, head} strides
     to pass (None: dense)."""
     shape = t.shape
+    if t.get_device() != dev:
+        _off_device(where, name, t, dev)
+    if t.is_contiguous() and len(shape) == 3:
+        return shape, None
     if len(shape) != 3 or t.stride(2) != 1 and shape[2] > 1:
         raise ValueError(f"{where}: {name} must be (T, H, D) with contiguous channels, got shape "
                          f"{tuple(shape)}, strides {t.stride()}")
-    if t.get_device() != dev:
-        _off_device(where, name, t, dev)
-    return shape, None if t.is_contiguous() else _Strides(t.stride(0), t.stride(1))
+    return shape, _Strides(t.stride(0), t.stride(1))
 
 
 def _on_device(where, name, t, dev=None):
@@ -564,7 +571,7 @@ def _result(where, name, out, t, stream, dev, dense):
     if out is None:
         if stream is not None:
             return _empty_on(stream, lambda: t.new_empty(t.shape)), None
-        return _torch.empty_like(t) if dense else t.new_empty(t.shape), None
+        return _empty_like(t) if dense else t.new_empty(t.shape), None
     shape, st = _rows3(where, name, out, dev)
     if shape != t.shape:
         raise ValueError(f"{where}: {name} has shape {tuple(shape)}, not {tuple(t.shape)}")
@@ -591,7 +598,11 @@ def rope(q, k, positions, inv_freq, interleaved=False, mscale=1.0, inverse=False
     if positions.get_device() != dev:
         _off_device("rope", "positions", positions, dev)
     _freqs("rope", inv_freq, dev)
-    q_out, qos = _result("rope", "q_out", q_out, q, stream, dev, qs is None)
+    qos = None
+    if q_out is None and stream is None and qs is None:
+        q_out = _empty_like(q)
+    else:
+        q_out, qos = _result("rope", "q_out", q_out, q, stream, dev, qs is None)
     Hkv, ks, kos, kp, kop = 0, None, None, 0, 0
     if k is None:
         k_out = None
@@ -601,7 +612,10 @@ def rope(q, k, positions, inv_freq, interleaved=False, mscale=1.0, inverse=False
             raise ValueError(f"rope: k has shape {tuple(k.shape)}, q {tuple(q.shape)}")
         if k.dtype != q.dtype:
             raise TypeError(f"rope: k is {k.dtype}, not {q.dtype}")
-        k_out, kos = _result("rope", "k_out", k_out, k, stream, dev, ks is None)
+        if k_out is None and stream is None and ks is None:
+            k_out = _empty_like(k)
+        else:
+            k_out, kos = _result("rope", "k_out", k_out, k, stream, dev, ks is None)
         kp, kop = k.data_ptr(), k_out.data_ptr()
     rc = _lib.sage_rope(q.data_ptr(), kp, q_out.data_ptr(), kop, dtype, T, Hq, Hkv, D, qs, ks, qos,
                         kos, positions.data_ptr(), bits, inv_freq.data_ptr(),
@@ -773,9 +787,12 @@ def attn_paged(cache, batch, q, out=None, window=0, sinks=0, sm_scale=None, lse=
     dtype = _code16("attn_paged", "q", q)
     if D != cache.D:
         raise ValueError(f"attn_paged: q has {D} channels, the cache {cache.D}")
-    out, os_ = _result("attn_paged", "out", out, q, stream, dev, qs is None)
-    if os_ is not None:
-        raise ValueError("attn_paged: out must be contiguous")
+    if out is None and stream is None and qs is None:
+        out = _empty_like(q)
+    else:
+        out, os_ = _result("attn_paged", "out", out, q, stream, dev, qs is None)
+        if os_ is not None:
+            raise ValueError("attn_paged: out must be contiguous")
     lp = 0
     if lse is not None:
         if lse.dtype != _torch.float32 or lse.shape != (T, Hq) or not lse.is_contiguous():
