@@ -14,12 +14,16 @@
 // multiplication per frequency (2^-53 relative) is the only rounding before
 // the fraction is cut to fp32.
 //
-// The work is bound by memory: each row is read once and written once.  A row
-// belongs to 8 or 16 lanes of 8 channels (one 16-byte vector each); the half
-// layout's partner channels come from another lane by a shuffle.  A group of
-// lanes keeps its head for all tokens of the CTA, so the per-channel means and
-// scales are loaded once.  cos and sin of the CTA's tokens are computed once
-// into shared memory and serve every head.
+// The work is bound by memory: each row is read once and written once.  In the
+// first kernel a row belongs to 8 or 16 lanes of 8 channels (one 16-byte vector
+// each); the half layout's partner channels come from another lane by a shuffle.
+// A group of lanes keeps its head for all tokens of the CTA, so the per-channel
+// means and scales are loaded once.  The second kernel gives a lane two vectors.
+// cos and sin of a CTA's tokens are computed once into shared memory and serve
+// every head.  Measured (GB300, back to back in a graph): interleaved rope of
+// 16000 tokens x 80 heads x 128 fp16, 110 us, 5.9 TB/s, 88 % of the measured copy
+// bandwidth; rope of one token for each of 64 sequences 3.8 us, of which the
+// launch is most.
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -33,7 +37,7 @@ namespace {
 
 constexpr int kRowThreads = 256;
 constexpr int kMaxToks = 8;          // tokens of one CTA
-constexpr int kMaxQ8Toks = 64;
+constexpr int kMaxPairToks = 64;
 constexpr unsigned kAll = 0xFFFFFFFFu;
 
 template <bool kBF16>
@@ -162,7 +166,7 @@ __device__ __forceinline__ void turn_table(const RowsParams& p, int nt, const in
 // kMode: 0 rope, 1 append 16-bit, 2 append Q8.  kLanes: lanes of a row.
 // kShfl: the half layout's partner vector is another lane's whole vector.
 template <int kMode, bool kBF16, int kLanes, bool kShfl>
-__global__ void __launch_bounds__(kRowThreads)
+__global__ void __launch_bounds__(kRowThreads, kMode == 0 ? 5 : 3)
 rows_kernel(const RowsParams p) {
   __shared__ float2 cs[kMaxToks * 64];
   __shared__ int64_t pos_s[kMaxToks];
@@ -330,202 +334,243 @@ rows_kernel(const RowsParams p) {
   }
 }
 
-// ---- Q8 cache: arithmetic, not memory, bounds the kernel above there (164
-// instructions for two rows of 80 channels).  Here a lane holds 16 channels and a
-// row ceil(D / 16) lanes, so that 80 channels fill 30 of 32 lanes with six rows;
-// K rows, V rows and q rows go in passes of their own (no warp does two kinds),
-// and a lane keeps its head through the CTA's tokens, with the head's means or
-// multipliers in registers.
+// ---- The usual case: rows in whole 16-byte vectors, rotations whose pairs are
+// whole vectors.  A lane holds two vectors of a row, in the half layout the two
+// that turn into each other (no partner from another lane, one cos and sin for
+// both), else neighbours; a row takes ceil(D / 16) lanes, so that 80 channels
+// fill 30 of 32 lanes with six rows.  q, k and v rows go in passes of their own
+// (no warp does two kinds).  Arithmetic bounds the Q8 cache's rows: there a lane
+// keeps its head through the CTA's tokens, with the head's means or multipliers
+// in registers.
 
 __device__ __forceinline__ int wrap(int x, int n) { return x >= n ? x - n : x; }
 
-struct Q8Tokens {
-  int64_t pos[kMaxQ8Toks], slot[kMaxQ8Toks], scale[kMaxQ8Toks];
-  int page[kMaxQ8Toks];
+struct Tokens {
+  int64_t pos[kMaxPairToks], slot[kMaxPairToks], scale[kMaxPairToks];
+  int page[kMaxPairToks];
 };
 
-// kWhat: 0 q, 1 k, 2 v.
-template <int kWhat, bool kBF16>
-__device__ __forceinline__ void q8_pass(const RowsParams& p, const Q8Tokens& tk, const float2* cs,
-                                        int64_t t0, int nt) {
+// kMode as above; kWhat: 0 q, 1 k, 2 v.
+template <int kMode, int kWhat, bool kBF16>
+__device__ __forceinline__ void pair_pass(const RowsParams& p, const Tokens& tk, const float2* cs,
+                                          int64_t t0, int nt) {
   const PagedGeo& c = p.c;
+  constexpr bool kCodes = kMode == 2 && kWhat != 0;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int per = (p.D + 15) / 16, fit = 32 / per;      // lanes of a row; rows of a warp
   const int slot = lane / per, sub = lane - slot * per;
-  const int base = slot * per, c0 = 16 * sub;
-  const bool two = c0 + 8 < p.D;                        // D % 16 == 8: the last lane has half
-  const int half = p.R / 2;
+  const int base = slot * per;
   const bool turn = kWhat != 2 && p.inv_freq != nullptr;
+  // this lane's vectors, as first channels
+  const bool halves = turn && !p.interleaved && sub < p.R / 16;
+  const int ca = halves ? 8 * sub : 16 * sub, cb = halves ? ca + p.R / 2 : ca + 8;
+  const bool two = cb < p.D;                            // D % 16 == 8: the last lane has one
   const int heads = kWhat == 0 ? p.Hq : p.Hkv;
   const int groups = kRowThreads / 32 * fit, group = warp * fit + slot;
-  const int at_once = min(heads, groups);               // heads side by side
-  const int step = groups / at_once;                    // tokens side by side
-  const int tok0 = group / at_once, head0 = group - tok0 * at_once;
-  const int mate = base + (c0 < half ? wrap(sub + p.R / 32, per) : max(0, sub - p.R / 32));
+  // Codes: a group keeps its head; else rows are dealt one after another.
+  const int at_once = kCodes ? min(heads, groups) : heads;
+  const int step = kCodes ? groups / at_once : 0;       // tokens side by side
   const uint16_t* const rows = kWhat == 0 ? p.q : kWhat == 1 ? p.k : p.v;
   const int64_t tok_stride = kWhat == 0 ? p.q_tok : kWhat == 1 ? p.k_tok : p.v_tok;
   const int64_t head_stride = kWhat == 0 ? p.q_head : kWhat == 1 ? p.k_head : p.v_head;
 
   for (int hb = 0; hb < heads; hb += at_once) {
-    const int h = hb + head0;
-    const bool mine = slot < fit && tok0 < step && h < heads;
-    float chan[16];                                     // k: means; v: 1 / scale
-    if (kWhat != 0) {
-      const float* src = (kWhat == 1 ? c.k_mean : c.v_scale) + h * c.Dp + c0;
+    int t = group / at_once, h = hb + group - t * at_once;
+    const bool mine = slot < fit && h < heads && (!kCodes || t < step);
+    float chan[16];                                     // codes: means, or 1 / scale
+    if constexpr (kCodes) {
+      const float* src = (kWhat == 1 ? c.k_mean : c.v_scale) + h * c.Dp;
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
-        chan[e] = mine && c0 + e < p.D ? src[e] : 0.0f;
+        const int ch = (e < 8 ? ca : cb) + e % 8;
+        chan[e] = mine && ch < p.D ? src[ch] : 0.0f;
         if (kWhat == 2) chan[e] = chan[e] > 0.0f ? __fdiv_rn(1.0f, chan[e]) : 0.0f;
       }
     }
-    const uint16_t* src = rows + (t0 + tok0) * tok_stride + h * head_stride + c0;
-    uint4 next[2];
-    auto load = [&](int t) {                            // runs a token ahead
-      next[0] = next[1] = make_uint4(0, 0, 0, 0);
-      if (mine && t < nt) {
-        next[0] = *reinterpret_cast<const uint4*>(src);
-        if (two) next[1] = *reinterpret_cast<const uint4*>(src + 8);
+    // the next row: the same head `step` tokens on, or `groups` rows on
+    auto advance = [&](int& tt, int& hh) {
+      if constexpr (kCodes) {
+        tt += step;
+      } else {
+        hh += groups;
+        while (hh >= heads) {
+          hh -= heads;
+          ++tt;
+        }
       }
-      src += step * tok_stride;
     };
-    load(tok0);
-    for (int tb = 0; tb < nt; tb += step) {
-      const int t = tb + tok0;
+    constexpr int kAhead = kCodes ? 1 : 3;              // rows whose loads run ahead
+    uint4 ring[kAhead][2];
+    int lt = t, lh = h;                                 // the next row to load
+    const uint16_t* at = rows + (t0 + lt) * tok_stride + lh * head_stride;   // codes: moves on
+    auto load = [&](uint4 (&r)[2]) {
+      r[0] = r[1] = make_uint4(0, 0, 0, 0);
+      if (mine && lt < nt) {
+        const uint16_t* src =
+            kCodes ? at : rows + (t0 + lt) * tok_stride + lh * head_stride;
+        r[0] = *reinterpret_cast<const uint4*>(src + ca);
+        if (two) r[1] = *reinterpret_cast<const uint4*>(src + cb);
+      }
+      advance(lt, lh);
+      if (kCodes) at += step * tok_stride;
+    };
+    auto handle = [&](const uint4 (&raw)[2]) {
       const bool has = mine && t < nt;
-      const uint4 raw[2] = {next[0], next[1]};
-      load(t + step);
-      __syncwarp();                                     // in place: rows are read
       float x[2][8];
       unpack8<kBF16>(raw[0], x[0]);
       unpack8<kBF16>(raw[1], x[1]);
       if (turn) {
         const float2* const a = cs + (has ? t : 0) * 64;
-        if (p.interleaved) {
+        if (halves) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float2 w = a[ca + e];
+            const float y = x[0][e] * w.x - x[1][e] * w.y;
+            x[1][e] = x[1][e] * w.x + x[0][e] * w.y;
+            x[0][e] = y;
+          }
+        } else if (p.interleaved) {
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            if (c0 + 2 * i < p.R) {
-              const float2 w = a[c0 / 2 + i];
+            if (ca + 2 * i < p.R) {
+              const float2 w = a[ca / 2 + i];
               float &x1 = x[i / 4][2 * (i % 4)], &x2 = x[i / 4][2 * (i % 4) + 1];
-              const float y1 = x1 * w.x - x2 * w.y;
+              const float y = x1 * w.x - x2 * w.y;
               x2 = x2 * w.x + x1 * w.y;
-              x1 = y1;
+              x1 = y;
             }
-        } else {                                        // R % 32 == 0: a lane's mate is one lane
-          const bool low = c0 < half;
-#pragma unroll
-          for (int v = 0; v < 2; ++v) {
-            uint4 other;
-            other.x = __shfl_sync(kAll, raw[v].x, mate);
-            other.y = __shfl_sync(kAll, raw[v].y, mate);
-            other.z = __shfl_sync(kAll, raw[v].z, mate);
-            other.w = __shfl_sync(kAll, raw[v].w, mate);
-            float y[8];
-            unpack8<kBF16>(other, y);
-            if (c0 < p.R) {
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const float2 w = a[(low ? c0 : c0 - half) + 8 * v + e];
-                x[v][e] = low ? x[v][e] * w.x - y[e] * w.y : x[v][e] * w.x + y[e] * w.y;
-              }
-            }
-          }
         }
       }
-      const int page = has ? tk.page[t] : -1;
-      if constexpr (kWhat == 0) {
-        if (has && page != -2) {
-          uint16_t* dst = p.q_out + (t0 + t) * p.qo_tok + h * p.qo_head + c0;
-          *reinterpret_cast<uint4*>(dst) = pack8<kBF16>(x[0]);
-          if (two) *reinterpret_cast<uint4*>(dst + 8) = pack8<kBF16>(x[1]);
+      const int page = kMode == 0 ? 0 : has ? tk.page[t] : -1;
+      if constexpr (!kCodes) {
+        const bool put = has && (kWhat == 0 ? page != -2 : page >= 0);
+        if (put) {
+          uint16_t* dst;
+          if constexpr (kWhat == 0) dst = p.q_out + (t0 + t) * p.qo_tok + h * p.qo_head;
+          else if constexpr (kMode == 0) dst = p.k_out + (t0 + t) * p.ko_tok + h * p.ko_head;
+          else
+            dst = reinterpret_cast<uint16_t*>(kWhat == 1 ? c.k : c.v) + tk.slot[t] +
+                  h * c.head_stride;
+          *reinterpret_cast<uint4*>(dst + ca) = turn ? pack8<kBF16>(x[0]) : raw[0];
+          if (two) *reinterpret_cast<uint4*>(dst + cb) = turn ? pack8<kBF16>(x[1]) : raw[1];
         }
-        continue;
-      }
-      uint32_t w[4];
-      if constexpr (kWhat == 1) {
-        float top = 0.0f;
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          x[e / 8][e % 8] = __fsub_rn(x[e / 8][e % 8], chan[e]);
-          top = fmaxf(top, fabsf(x[e / 8][e % 8]));
-        }
-        // the row's largest, in every lane of the row
-        if ((per & (per - 1)) == 0) {
-          for (int d = 1; d < per; d *= 2) top = fmaxf(top, __shfl_xor_sync(kAll, top, d));
-        } else {
-          const float part = top;
-          int from = sub;
-          for (int k = 1; k < per; ++k) {
-            from = wrap(from + 1, per);
-            top = fmaxf(top, __shfl_sync(kAll, part, base + from));
-          }
-        }
-        const float inv = top > 0.0f ? __fdiv_rn(127.0f, top) : 0.0f;
-        // rint by adding 1.5 * 2^23: the low byte is the code
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t b[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            b[e] = __float_as_uint(
-                __fadd_rn(__fmul_rn(x[i / 2][4 * (i % 2) + e], inv), 12582912.0f));
-          w[i] = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040),
-                             0x5410);
-        }
-        if (sub == 0 && page >= 0)
-          c.k_scale[tk.scale[t] + static_cast<int64_t>(h) * c.page_size] = __fdiv_rn(top, 127.0f);
       } else {
+        uint32_t w[4];
+        if constexpr (kWhat == 1) {
+          float top = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float* y = &x[i / 2][4 * (i % 2)];
-          w[i] = pack_e4m3x2(__fmul_rn(y[0], chan[4 * i]), __fmul_rn(y[1], chan[4 * i + 1])) |
-                 pack_e4m3x2(__fmul_rn(y[2], chan[4 * i + 2]), __fmul_rn(y[3], chan[4 * i + 3]))
-                     << 16;
+          for (int e = 0; e < 16; ++e) {
+            x[e / 8][e % 8] = __fsub_rn(x[e / 8][e % 8], chan[e]);
+            top = fmaxf(top, fabsf(x[e / 8][e % 8]));
+          }
+          // the row's largest, in every lane of the row
+          if ((per & (per - 1)) == 0) {
+            for (int d = 1; d < per; d *= 2) top = fmaxf(top, __shfl_xor_sync(kAll, top, d));
+          } else {
+            const float part = top;
+            int from = sub;
+            for (int k = 1; k < per; ++k) {
+              from = wrap(from + 1, per);
+              top = fmaxf(top, __shfl_sync(kAll, part, base + from));
+            }
+          }
+          const float inv = top > 0.0f ? __fdiv_rn(127.0f, top) : 0.0f;
+          // rint by adding 1.5 * 2^23: the low byte is the code
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t b[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              b[e] = __float_as_uint(
+                  __fadd_rn(__fmul_rn(x[i / 2][4 * (i % 2) + e], inv), 12582912.0f));
+            w[i] = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040),
+                               0x5410);
+          }
+          if (sub == 0 && page >= 0)
+            c.k_scale[tk.scale[t] + static_cast<int64_t>(h) * c.page_size] =
+                __fdiv_rn(top, 127.0f);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float* y = &x[i / 2][4 * (i % 2)];
+            w[i] = pack_e4m3x2(__fmul_rn(y[0], chan[4 * i]), __fmul_rn(y[1], chan[4 * i + 1])) |
+                   pack_e4m3x2(__fmul_rn(y[2], chan[4 * i + 2]), __fmul_rn(y[3], chan[4 * i + 3]))
+                       << 16;
+          }
+        }
+        if (page >= 0) {
+          uint8_t* dst = (kWhat == 1 ? c.k : c.v) + tk.slot[t] + h * c.head_stride;
+          if (p.wide_slots && !halves) {
+            *reinterpret_cast<uint4*>(dst + ca) = make_uint4(w[0], w[1], w[2], w[3]);
+          } else {                                      // apart, or slots on 8 bytes
+            *reinterpret_cast<uint2*>(dst + ca) = make_uint2(w[0], w[1]);
+            if (two) *reinterpret_cast<uint2*>(dst + cb) = make_uint2(w[2], w[3]);
+          }
         }
       }
-      if (page >= 0) {
-        uint8_t* dst = (kWhat == 1 ? c.k : c.v) + tk.slot[t] + h * c.head_stride + c0;
-        if (p.wide_slots) {
-          *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
-        } else {                                        // slots on 8 bytes
-          *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
-          if (two) *reinterpret_cast<uint2*>(dst + 8) = make_uint2(w[2], w[3]);
-        }
+      advance(t, h);
+    };
+    if constexpr (kCodes) {
+      load(ring[0]);
+      for (int tb = 0; tb < nt; tb += step) {
+        const uint4 raw[2] = {ring[0][0], ring[0][1]};
+        load(ring[0]);
+        handle(raw);
+      }
+      continue;
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) load(ring[i]);
+    // whole warps stay in the loop as long as one of their rows has a token left
+    while (__any_sync(kAll, mine && t < nt)) {
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const uint4 raw[2] = {ring[i][0], ring[i][1]};
+        load(ring[i]);
+        __syncwarp();                                   // in place: rows are read first
+        handle(raw);
       }
     }
   }
 }
 
-template <bool kBF16>
-__global__ void __launch_bounds__(kRowThreads, 4)
-q8_rows_kernel(const RowsParams p) {
-  __shared__ float2 cs[kMaxQ8Toks * 64];
-  __shared__ Q8Tokens tk;
+template <int kMode, bool kBF16>
+__global__ void __launch_bounds__(kRowThreads, kMode == 2 ? 4 : 3)
+pair_rows_kernel(const RowsParams p) {
+  __shared__ float2 cs[kMaxPairToks * 64];
+  __shared__ Tokens tk;
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * p.toks;
   const int nt = static_cast<int>(min(static_cast<int64_t>(p.toks), p.T - t0));
-  place_tokens(p, t0, nt, tk.pos, tk.page, tk.slot, tk.scale);
+  if constexpr (kMode == 0) {
+    if (threadIdx.x < nt)
+      tk.pos[threadIdx.x] = p.pos64 ? static_cast<const int64_t*>(p.pos)[t0 + threadIdx.x]
+                                    : static_cast<const int32_t*>(p.pos)[t0 + threadIdx.x];
+  } else {
+    place_tokens(p, t0, nt, tk.pos, tk.page, tk.slot, tk.scale);
+  }
   __syncthreads();
   if (p.inv_freq != nullptr) {
     turn_table(p, nt, tk.pos, cs);
     __syncthreads();
   }
   for (int what = blockIdx.y; what < 3; what += gridDim.y) {
-    if (what == 0) q8_pass<1, kBF16>(p, tk, cs, t0, nt);
-    else if (what == 1) q8_pass<2, kBF16>(p, tk, cs, t0, nt);
-    else if (p.Hq > 0) q8_pass<0, kBF16>(p, tk, cs, t0, nt);
+    if (what == 0 && p.Hq > 0) pair_pass<kMode, 0, kBF16>(p, tk, cs, t0, nt);
+    if (what == 1 && p.Hkv > 0) pair_pass<kMode, 1, kBF16>(p, tk, cs, t0, nt);
+    if (kMode != 0 && what == 2) pair_pass<kMode, 2, kBF16>(p, tk, cs, t0, nt);
   }
 }
 
-template <bool kBF16>
-cudaError_t launch_q8(const RowsParams& p0, int sms, cudaStream_t st) {
+template <int kMode, bool kBF16>
+cudaError_t launch_pairs(const RowsParams& p0, int sms, cudaStream_t st) {
   RowsParams p = p0;
   p.toks = 1;
-  while (p.toks < kMaxQ8Toks && p.T / (2 * p.toks) >= 4 * sms) p.toks *= 2;
+  while (p.toks < kMaxPairToks && p.T / (2 * p.toks) >= 4 * sms) p.toks *= 2;
   p.wide_slots = p.D % 16 == 0 && p.c.page_stride % 16 == 0 && p.c.token_stride % 16 == 0 &&
                  p.c.head_stride % 16 == 0;
   const int64_t ctas = (p.T + p.toks - 1) / p.toks;
   if (ctas > 0x7FFFFFFF) return cudaErrorInvalidValue;
-  const unsigned y = ctas > 2 * sms ? 1 : p.Hq > 0 ? 3 : 2;    // few tokens: a CTA per pass
-  q8_rows_kernel<kBF16><<<dim3(static_cast<unsigned>(ctas), y), kRowThreads, 0, st>>>(p);
+  const unsigned y = ctas > 2 * sms ? 1 : 3;            // few tokens: a CTA per pass
+  pair_rows_kernel<kMode, kBF16><<<dim3(static_cast<unsigned>(ctas), y), kRowThreads, 0, st>>>(p);
   note_launch();
   return cudaGetLastError();
 }
@@ -564,11 +609,25 @@ cudaError_t launch_mode(const RowsParams& p0, bool bf16, int sms, cudaStream_t s
 }  // namespace
 
 cudaError_t launch_rows(const RowsParams& p, int mode, bool bf16, int sms, cudaStream_t st) {
+  // Two vectors a lane from 4 tokens per SM on, for whole vectors: rotations of
+  // the half layout (rope of 16000 x 80 heads of 128: 128 us against 186; append
+  // of 24000 tokens with q: 128 against 213) and Q8 rows (65000 x 16 heads of 80:
+  // 130 against 228).  One vector a lane has the shorter way through few tokens
+  // (64: 3.8 us against 4.3; Q8 4.7 against 6.8) and is as fast or faster where
+  // pairs are neighbours (interleaved rope of the same rows: 110 against 118).
+  const bool apart = p.inv_freq != nullptr && !p.interleaved;
+  const bool neighbours = p.inv_freq != nullptr && p.interleaved;
+  const bool pairs = p.vec && p.T >= 4 * static_cast<int64_t>(sms) &&
+                     !(apart && p.R % 16 != 0) && !(neighbours && mode != 2);
+  if (pairs) {
+    if (mode == 0)
+      return bf16 ? launch_pairs<0, true>(p, sms, st) : launch_pairs<0, false>(p, sms, st);
+    if (mode == 1)
+      return bf16 ? launch_pairs<1, true>(p, sms, st) : launch_pairs<1, false>(p, sms, st);
+    return bf16 ? launch_pairs<2, true>(p, sms, st) : launch_pairs<2, false>(p, sms, st);
+  }
   if (mode == 0) return launch_mode<0>(p, bf16, sms, st);
   if (mode == 1) return launch_mode<1>(p, bf16, sms, st);
-  // 16-byte rows, and rotations whose partners lie in one lane of 16 channels
-  if (p.vec && (p.inv_freq == nullptr || p.interleaved || p.R % 32 == 0))
-    return bf16 ? launch_q8<true>(p, sms, st) : launch_q8<false>(p, sms, st);
   return launch_mode<2>(p, bf16, sms, st);
 }
 

@@ -196,7 +196,8 @@ def slot_view(p, t):
     return t if p.layout == "NHD" else t.transpose(1, 2)
 
 
-CASES = [([1, 1, 1], [1, 16, 333]), ([3, 0, 50, 7], [3, 9, 200, 4]), ([300, 1], [300, 77])]
+CASES = [([1, 1, 1], [1, 16, 333]), ([3, 0, 50, 7], [3, 9, 200, 4]), ([300, 1], [300, 77]),
+         ([410, 1, 300], [410, 50, 333])]
 
 
 @pytest.mark.parametrize("dt", [torch.bfloat16, torch.float16])
