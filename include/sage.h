@@ -508,7 +508,13 @@ SAGE_API sage_status sage_kv_append(const sage_paged_cache* cache, const sage_pa
  * exponentials (of the smoothed logits with SAGE_Q8: all of a row's logits
  * lack sm_scale * q . k_mean).  A row without visible keys gives zeros and
  * -inf.  Keys and values that no row sees may hold anything; visible ones
- * are finite.
+ * are finite.  How the work is split into parts goes by the whole batch, so a
+ * sequence's rows may differ in their last bits between batches, never between
+ * runs of one.  out overlaps no input.
+ * Sequences of up to 16 rows (32 with D <= 64; new tokens times Hq/Hkv) take a
+ * kernel that reads the cache at memory speed, longer ones the tensor cores.
+ * The latter needs, for a 16-bit cache, pages that divide 128 slots or are
+ * multiples of it; with other page sizes long chunks run an order slower.
  *   q_strides: host int64[2], {token, head} in elements, or NULL: dense. */
 SAGE_API sage_status sage_attn_paged(const sage_paged_cache* cache, const sage_paged_batch* batch,
                                      const void* q, void* out, float* lse, int dtype, int64_t Hq,

@@ -18,7 +18,10 @@ constexpr int64_t kMaxStride = int64_t(1) << 39;
 constexpr size_t kStatusBytes = 256;   // then the arrival counters
 constexpr size_t kClearBytes = kStatusBytes + kArrivalBytes;
 static_assert(kClearBytes == SAGE_PAGED_CLEAR_BYTES, "the header says what the caller clears");
-// Mean rows of a sequence from which on the tensor-core kernel takes them all.
+// Mean rows of a sequence from which on the tensor-core kernel takes them all:
+// with 16 decoding sequences and 4 chunks of 200-1500 tokens (mean 170 rows) the
+// two kernels take 277 us and the one 300; without short sequences the launch
+// that finds nothing costs 8.
 constexpr int64_t kAllMany = 512;
 size_t few_bytes() { return (paged_few_bytes() + 255) / 256 * 256; }
 

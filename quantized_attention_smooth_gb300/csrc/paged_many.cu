@@ -37,6 +37,18 @@
 // second kernel, which joins them in order.  Key tiles that no row sees (before
 // the window, behind the sinks) are never visited.  Values of keys that no row
 // of the pair sees are zeroed in shared memory (0 times NaN would be NaN).
+//
+// Measured on GB300 (32 query heads on 8 kv heads of 128 channels): 2048 new
+// tokens over 30720 cached ones, bf16, 752 us, 1417 TFLOP/s, 74 % of the measured
+// bf16 peak; two causal prompts of 8192 tokens 836 us, 1316 TFLOP/s; chunks over
+// the 8-bit cache 462 us, 948 TFLOP/s.  A key step of both tiles takes about 2950
+// cycles against 2048 of the tensor pipe: the softmax of a tile (1490 cycles, two
+// and a half per instruction with one warp of it per scheduler) and its products
+// (1024 and the signals' latency) follow one another, and the two tiles overlap
+// only that far.  Tried and slower: the logits in four pieces with a load ahead
+// (1830 cycles), two threads a row (registers spill), P in shared memory.  The
+// 8-bit cache adds the key scales (64 products and 32 loads a row) and shares the
+// issue slots with the widening warps: 2500 cycles a tile.
 
 #include <atomic>
 #include <type_traits>
@@ -52,7 +64,8 @@ constexpr int kMaxManyCtas = 152;
 constexpr uint32_t kTmemCols = 512;
 constexpr unsigned kAll = 0xFFFFFFFFu;
 // Units that an item costs besides its key tiles: filling and draining the
-// pipeline takes about as long as this many tiles.
+// pipeline takes about as long as this many tiles.  (Two prompts of 8192 tokens:
+// 930 us with 2, 830 with 3 or 4, 849 with 6: the first rows' items are short.)
 constexpr int kItemUnits = 4;
 constexpr float kLazy = 8.0f;             // log2 of the growth that rescales O
 
