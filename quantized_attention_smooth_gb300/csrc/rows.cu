@@ -121,29 +121,47 @@ __device__ __forceinline__ int find_seq(const PagedGeo& c, int64_t tok, int lane
   return lo;
 }
 
-// Each token's position and slot (append), by a warp per token.
+// A token's position and slot, given its sequence.
+__device__ __forceinline__ void place(const PagedGeo& c, int64_t tok, int s, int64_t* pos_out,
+                                      int* page_out, int64_t* slot_out, int64_t* scale_out) {
+  int start = 0, n = 0, len = 0, page = -1;
+  int64_t pos = -1;
+  if (paged_seq(c, s, &start, &n, &len) && tok >= start && tok < start + n) {
+    pos = static_cast<int64_t>(len) - n + (tok - start);
+    if (pos >= 0) {
+      const int pn = static_cast<int>(pos) / c.page_size;
+      page = paged_page(c, s, pn);
+      const int slot = static_cast<int>(pos) - pn * c.page_size;
+      *slot_out = page * c.page_stride + slot * c.token_stride;
+      *scale_out = static_cast<int64_t>(page) * c.Hkv * c.page_size + slot;
+    }
+  }
+  *pos_out = pos;
+  *page_out = pos < 0 ? -2 : page;
+}
+
+// Each token's position and slot (append): a warp per token where a CTA has one
+// for each (fewest round trips), else a thread per token (all at once).
 __device__ __forceinline__ void place_tokens(const RowsParams& p, int64_t t0, int nt, int64_t* pos_s,
                                              int* page_s, int64_t* slot_s, int64_t* scale_s) {
   const PagedGeo& c = p.c;
-  const int lane = threadIdx.x & 31;
-  for (int i = threadIdx.x >> 5; i < nt; i += kRowThreads / 32) {
-    const int64_t tok = t0 + i;
-    const int s = find_seq(c, tok, lane);
-    if (lane == 0) {
-      int start = 0, n = 0, len = 0, page = -1;
-      int64_t pos = -1;
-      if (paged_seq(c, s, &start, &n, &len) && tok >= start && tok < start + n) {
-        pos = static_cast<int64_t>(len) - n + (tok - start);
-        if (pos >= 0) page = paged_page(c, s, static_cast<int>(pos / c.page_size));
-      }
-      pos_s[i] = pos;
-      page_s[i] = pos < 0 ? -2 : page;
-      if (page >= 0) {
-        const int slot = static_cast<int>(pos % c.page_size);
-        slot_s[i] = page * c.page_stride + slot * c.token_stride;
-        scale_s[i] = static_cast<int64_t>(page) * c.Hkv * c.page_size + slot;
-      }
+  if (nt <= kRowThreads / 32) {
+    const int i = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (i < nt) {
+      const int s = find_seq(c, t0 + i, lane);
+      if (lane == 0) place(c, t0 + i, s, &pos_s[i], &page_s[i], &slot_s[i], &scale_s[i]);
     }
+    return;
+  }
+  const int i = threadIdx.x;
+  if (i < nt) {
+    int lo = 0, hi = c.nseq;                            // the last s with cu_q[s] <= token
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (c.cu_q[mid] <= t0 + i) lo = mid;
+      else hi = mid;
+    }
+    place(c, t0 + i, lo, &pos_s[i], &page_s[i], &slot_s[i], &scale_s[i]);
   }
 }
 
