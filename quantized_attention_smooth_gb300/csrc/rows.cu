@@ -629,8 +629,8 @@ cudaError_t launch_mode(const RowsParams& p0, bool bf16, int sms, cudaStream_t s
 cudaError_t launch_rows(const RowsParams& p, int mode, bool bf16, int sms, cudaStream_t st) {
   // Two vectors a lane from 4 tokens per SM on, for whole vectors: rotations of
   // the half layout (rope of 16000 x 80 heads of 128: 128 us against 186; append
-  // of 24000 tokens with q: 128 against 213) and Q8 rows (65000 x 16 heads of 80:
-  // 130 against 228).  One vector a lane has the shorter way through few tokens
+  // of 24000 tokens with q: 124 against 213) and Q8 rows (65000 x 16 heads of 80:
+  // 122 against 228).  One vector a lane has the shorter way through few tokens
   // (64: 3.8 us against 4.3; Q8 4.7 against 6.8) and is as fast or faster where
   // pairs are neighbours (interleaved rope of the same rows: 110 against 118).
   const bool apart = p.inv_freq != nullptr && !p.interleaved;

@@ -150,13 +150,15 @@ class Problem:
         the output's rounding, u |out|; P's rounding to the type of the tensor
         instruction, up p_j each, up sum w_j |v_j|; fp16's P below 2^-14 has
         steps of 2^-24, half of one each: 2^-25 sum |v_j| / l (l the sum of
-        exponentials, P <= 1).  The logits: |x| <= 40 here, with D <= 128 fp32
+        exponentials, P <= 1); an fp16 output below 2^-14 has the same steps, so its
+        rounding is off by up to 2^-25 there.  The logits: |x| <= 40 here, with D <= 128 fp32
         products whose errors add up to less than 2^-16, which moves a weight
         by 2 * 2^-16 relative; the fp32 sums and exp2 stay below 2^-16 more."""
         u = HALF[self.q.dtype]
         up = 2.0 ** -8 if self.kind == "bf16" else 2.0 ** -11
         sub = 0.0 if self.kind == "bf16" else 2.0 ** -25
-        return u * out.abs() + (up + 3 * 2.0 ** -16) * mean * (1 + u) + sub * spread + 1e-30
+        step = 2.0 ** -25 if self.q.dtype == torch.float16 else 1e-30
+        return u * out.abs() + (up + 3 * 2.0 ** -16) * mean * (1 + u) + sub * spread + step
 
     def sage(self, sage):
         return (sage.PagedCache(self.k, self.v, self.layout, self.k_scale, self.k_mean,

@@ -197,7 +197,7 @@ def slot_view(p, t):
 
 
 CASES = [([1, 1, 1], [1, 16, 333]), ([3, 0, 50, 7], [3, 9, 200, 4]), ([300, 1], [300, 77]),
-         ([410, 1, 300], [410, 50, 333])]
+         ([410, 1, 300], [410, 50, 333]), ([3000, 0, 1, 2500], [3100, 0, 5, 2400])]
 
 
 @pytest.mark.parametrize("dt", [torch.bfloat16, torch.float16])
