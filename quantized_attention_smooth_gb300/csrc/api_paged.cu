@@ -138,6 +138,9 @@ sage_status paged_geo(const sage_paged_cache* cache, const sage_paged_batch* b, 
   g->page_size = static_cast<int32_t>(cache->page_size);
   g->kind = kind;
   g->page_shift = (g->page_size & (g->page_size - 1)) == 0 ? __builtin_ctz(g->page_size) : -1;
+  // strides are multiples of 8 elements: 16 bytes, or 8 of an 8-bit cache
+  const int64_t vec = kind == SAGE_Q8 ? 16 : 8;
+  g->wide = cache->D % vec == 0 && ps % vec == 0 && ts % vec == 0 && hs % vec == 0;
   g->cu_q = b->cu_q;
   g->kv_lens = b->kv_lens;
   g->table = b->block_table;

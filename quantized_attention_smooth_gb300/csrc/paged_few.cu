@@ -124,7 +124,8 @@ struct FewItem {
 };
 
 // kForm: 0 D = Dp, every vector of a row is loaded; 1 vectors from D on are not; 2
-// so too, and rows of the 8-bit cache start on 8 bytes only (D % 16 == 8).
+// so too, and rows of the 8-bit cache go in 8 bytes at a time (D or a stride is an
+// odd multiple of 8, so that they end or start on 8 bytes only).
 // A warp's ring of blocks in shared memory, and the merge buffer that takes its
 // place at an item's end.
 template <int kKind, int kDp, int kNr>
@@ -781,7 +782,7 @@ paged_join_kernel(const PagedAttnParams p, int ctas) {
 template <int kKind, bool kQBF16, int kDp, int kNr, int kForm = 0>
 cudaError_t launch_few(const PagedAttnParams& p, int sms, cudaStream_t st) {
   if constexpr (kForm == 0) {
-    if (kKind == kKindQ8 && p.c.D % 16 != 0)
+    if (!p.c.wide)                              // 8-bit only: 16-bit rows always are
       return launch_few<kKind, kQBF16, kDp, kNr, kKind == kKindQ8 ? 2 : 1>(p, sms, st);
     if (p.c.D != kDp) return launch_few<kKind, kQBF16, kDp, kNr, 1>(p, sms, st);
   }

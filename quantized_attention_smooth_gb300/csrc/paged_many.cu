@@ -537,11 +537,12 @@ paged_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
       }
     } else if (warp == 9 && kQ8) {
       // ================================================== copies of codes, for rows
-      // and pages that tensor copies cannot take (D % 16 == 8, page sizes that
-      // neither divide nor are multiples of 128); five times slower
+      // and pages that tensor copies cannot take (D or a stride an odd multiple of
+      // 8, page sizes that neither divide nor are multiples of 128); five times
+      // slower
       Ring<L::kRawStages> ring;                 // K and V tiles alternate
       bool ok = true;
-      const bool wide = c.D % 16 == 0;          // rows start on 16 bytes, else on 8
+      const bool wide = c.wide;                 // rows in vectors of 16 bytes, else of 8
       const int shift = (kDp == 128 ? 3 : 2) + (wide ? 0 : 1);   // log2 of a row's lanes
       const int width = wide ? 16 : 8, col = (lane & ((1 << shift) - 1)) * width;
       const int step = 32 >> shift;
@@ -1296,9 +1297,7 @@ cudaError_t launch_many(const PagedAttnParams& p, int sms, cudaStream_t st) {
   PagedAttnParams prm = p;
   const PagedGeo& c = p.c;
   const uint64_t el = kKind == kKindQ8 ? 1 : 2;                // bytes of an element
-  prm.tensor_copies = kKind != kKindQ8 || (page_boxes(c) && c.D % 16 == 0 &&
-                                           c.page_stride % 16 == 0 && c.token_stride % 16 == 0 &&
-                                           c.head_stride % 16 == 0);
+  prm.tensor_copies = kKind != kKindQ8 || (page_boxes(c) && c.wide);
   if (prm.tensor_copies) {
     const uint64_t dims[4] = {static_cast<uint64_t>(c.D), static_cast<uint64_t>(c.page_size),
                               static_cast<uint64_t>(c.Hkv), static_cast<uint64_t>(c.num_pages)};

@@ -518,7 +518,7 @@ __device__ __forceinline__ void pair_pass(const RowsParams& p, const Tokens& tk,
         }
         if (page >= 0) {
           uint8_t* dst = (kWhat == 1 ? c.k : c.v) + tk.slot[t] + h * c.head_stride;
-          if (p.wide_slots && !halves) {
+          if (c.wide && !halves) {
             *reinterpret_cast<uint4*>(dst + ca) = make_uint4(w[0], w[1], w[2], w[3]);
           } else {                                      // apart, or slots on 8 bytes
             *reinterpret_cast<uint2*>(dst + ca) = make_uint2(w[0], w[1]);
@@ -583,8 +583,6 @@ cudaError_t launch_pairs(const RowsParams& p0, int sms, cudaStream_t st) {
   RowsParams p = p0;
   p.toks = 1;
   while (p.toks < kMaxPairToks && p.T / (2 * p.toks) >= 4 * sms) p.toks *= 2;
-  p.wide_slots = p.D % 16 == 0 && p.c.page_stride % 16 == 0 && p.c.token_stride % 16 == 0 &&
-                 p.c.head_stride % 16 == 0;
   const int64_t ctas = (p.T + p.toks - 1) / p.toks;
   if (ctas > 0x7FFFFFFF) return cudaErrorInvalidValue;
   const unsigned y = ctas > 2 * sms ? 1 : 3;            // few tokens: a CTA per pass

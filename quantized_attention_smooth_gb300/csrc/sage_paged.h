@@ -21,6 +21,7 @@ struct PagedGeo {
   int64_t page_stride, token_stride, head_stride;   // elements
   int32_t Hkv, D, Dp, page_size, kind;
   int32_t page_shift;        // log2(page_size), or -1
+  int32_t wide;              // every row is whole 16-byte vectors that start on 16 bytes
   const int32_t* cu_q;
   const int32_t* kv_lens;
   const int32_t* table;
@@ -46,7 +47,6 @@ struct RowsParams {
   float mscale, sign;        // sign -1: the inverse rotation
   int32_t vec;               // 16-byte rows: base, strides and D in whole vectors
   int32_t toks;              // tokens per CTA (set by the launcher)
-  int32_t wide_slots;        // 8-bit cache: slots start on 16 bytes (set by the launcher)
   PagedGeo c;                // sage_kv_append only
 };
 

@@ -80,8 +80,8 @@ __device__ __forceinline__ void copy8(uint32_t dst, const uint8_t* src, int byte
                :: "r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 // A vector of a row that ends after `left` more elements (untouched where none
-// are left), zero unless `see`.  kForm 0: all are there; 2: rows of 8 bits that
-// start on 8 bytes only.
+// are left), zero unless `see`.  kForm 0: all are there; 2: rows of 8-bit codes
+// that start or end on 8 bytes only.
 template <int kForm>
 __device__ __forceinline__ void copy_part(uint32_t dst, const uint8_t* src, bool see, int left) {
   if constexpr (kForm == 2) {
