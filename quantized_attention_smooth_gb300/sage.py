@@ -646,7 +646,7 @@ class PagedCache:
                 k.dtype not in (torch.float16, torch.bfloat16) or v.dtype != k.dtype):
             raise TypeError(f"PagedCache: k {k.dtype} and v {v.dtype} must be both float16, both "
                             "bfloat16, or int8 and float8_e4m3fn")
-        self.kind = Q8 if q8 else F16 if k.dtype == torch.float16 else BF16
+        self.kind, self._dev = Q8 if q8 else F16 if k.dtype == torch.float16 else BF16, k.get_device()
         pages, self.D = k.shape[0], k.shape[3]
         slots, self.Hkv = (k.shape[2], k.shape[1]) if lay == HND else (k.shape[1], k.shape[2])
         st, page_dims = k.stride(), (2, 1) if lay == HND else (1, 2)
@@ -700,7 +700,7 @@ class PagedBatch:
                              f"got {tuple(block_table.shape)}")
         self.cu_q, self.kv_lens, self.block_table = cu_q, kv_lens, block_table
         self.nseq, self.max_q, self.max_kv = n, int(max_q), int(max_kv)
-        self._calls = {}
+        self._calls, self._dev = {}, kv_lens.get_device()
         self._c = _BatchC(cu_q.data_ptr(), kv_lens.data_ptr(), block_table.data_ptr(), n, 0,
                           block_table.stride(0), block_table.shape[1], self.max_q, self.max_kv)
 
@@ -737,6 +737,8 @@ def kv_append(cache, batch, k, v, q=None, q_out=None, inv_freq=None, interleaved
     inv_freq, k is turned at each token's position first, and q (T, Hq, D), if
     given, into q_out (returned)."""
     dev, current = _device("kv_append", "k", k)
+    if cache._dev != dev or batch._dev != dev:
+        _off_cache("kv_append", cache, batch, dev)
     shape, ks = _rows3("kv_append", "k", k, dev)
     vshape, vs = _rows3("kv_append", "v", v, dev)
     dtype = _code16("kv_append", "k", k)
@@ -768,6 +770,14 @@ def kv_append(cache, batch, k, v, q=None, q_out=None, inv_freq=None, interleaved
     return q_out if q is not None else None
 
 
+def _off_cache(where, cache, batch, dev):
+    """The cache and the batch hold pointers of the device they were built on."""
+    for name, index in (("cache", cache._dev), ("batch", batch._dev)):
+        if index != dev:
+            raise ValueError(f"{where}: the {name} is on cuda:{index}, the current device is "
+                             f"cuda:{dev}")
+
+
 def _workspace(where, ws, stream, dev):
     if ws is None:
         return alloc_workspace_paged("cuda", stream)
@@ -783,6 +793,8 @@ def attn_paged(cache, batch, q, out=None, window=0, sinks=0, sm_scale=None, lse=
     ones.  Returns out (T, Hq, D) of q's type; lse, if given, is a float32
     (T, Hq) tensor that receives the log-sum-exp of every row."""
     dev, current = _device("attn_paged", "q", q)
+    if cache._dev != dev or batch._dev != dev:
+        _off_cache("attn_paged", cache, batch, dev)
     (T, Hq, D), qs = _rows3("attn_paged", "q", q, dev)
     dtype = _code16("attn_paged", "q", q)
     if D != cache.D:

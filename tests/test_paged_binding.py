@@ -1,0 +1,47 @@
+"""The serving calls' binding, on the host: what it checks before it launches."""
+import sys
+
+import pytest
+
+torch = pytest.importorskip("torch")
+from quantized_attention_smooth_gb300 import sage  # noqa: E402
+
+
+class Rows:
+    """Stands for a dense (3, 2, 64) tensor on a CUDA device."""
+    is_cuda, dtype, shape = True, torch.bfloat16, (3, 2, 64)
+
+    def __init__(self, index):
+        self.index, self.device = index, f"cuda:{index}"
+
+    def get_device(self):
+        return self.index
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return 0x100000
+
+
+def held(index):
+    """A cache and a batch built on device `index`."""
+    cache, batch = object.__new__(sage.PagedCache), object.__new__(sage.PagedBatch)
+    cache.Hkv, cache.D, cache._dev, batch._dev = 2, 64, index, index
+    return cache, batch
+
+
+@pytest.mark.parametrize("cache_on,batch_on,name", [(0, 1, "cache"), (1, 0, "batch"), (0, 0, "cache")])
+def test_cache_and_batch_of_another_device(monkeypatch, cache_on, batch_on, name):
+    """The call's tensors are on the current device, the cache or the batch is not."""
+    monkeypatch.setattr(sage, "_torch", torch)
+    monkeypatch.setattr(sage, "_get_device", lambda: 1)
+    monkeypatch.setattr(sage, "_get_stream", lambda d: 0)
+    monkeypatch.setattr(sage, "_CODES", {torch.bfloat16: sage.BF16})
+    monkeypatch.setattr(sage, "_empty_like", lambda t: t)
+    cache, batch = held(cache_on)[0], held(batch_on)[1]
+    x = Rows(1)
+    with pytest.raises(ValueError, match=f"kv_append: the {name} is on cuda:0, the current device"):
+        sage.kv_append(cache, batch, x, x)
+    with pytest.raises(ValueError, match=f"attn_paged: the {name} is on cuda:0, the current device"):
+        sage.attn_paged(cache, batch, x)
