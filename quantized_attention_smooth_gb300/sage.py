@@ -485,9 +485,10 @@ _torch = _get_device = _get_stream = _empty_like = None
 def _bind_torch():
     global _torch, _get_device, _get_stream, _empty_like
     import torch
-    _torch, _empty_like = torch, torch.empty_like
+    _empty_like = torch.empty_like
     _get_device, _get_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
     _CODES.update({torch.float16: F16, torch.bfloat16: BF16})
+    _torch = torch                # last: other threads take it for a sign that all are set
 
 
 def _device(where, name, t):

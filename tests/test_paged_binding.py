@@ -45,3 +45,28 @@ def test_cache_and_batch_of_another_device(monkeypatch, cache_on, batch_on, name
         sage.kv_append(cache, batch, x, x)
     with pytest.raises(ValueError, match=f"attn_paged: the {name} is on cuda:0, the current device"):
         sage.attn_paged(cache, batch, x)
+
+
+def test_first_calls_of_two_threads(monkeypatch):
+    """A thread that sees _torch set finds everything set that goes with it: no
+    line of the binding runs with _torch set and the rest not."""
+    names = ("_torch", "_get_device", "_get_stream", "_empty_like")
+    for n in names:
+        monkeypatch.setattr(sage, n, None)
+    monkeypatch.setattr(sage, "_CODES", {})
+    early = []
+
+    def trace(frame, event, arg):
+        if frame.f_code is sage._bind_torch.__code__:
+            if sage._torch is not None and not (sage._CODES and all(getattr(sage, n) for n in names)):
+                early.append(frame.f_lineno)
+            return trace
+        return None
+
+    before = sys.gettrace()
+    sys.settrace(trace)
+    try:
+        sage._bind_torch()
+    finally:
+        sys.settrace(before)
+    assert sage._torch is torch and not early
