@@ -699,6 +699,9 @@ class PagedBatch:
                 block_table.shape[1] > 1 and block_table.stride(1) != 1:
             raise ValueError(f"PagedBatch: block_table must be (n, width) with contiguous rows, "
                              f"got {tuple(block_table.shape)}")
+        for name, x in (("max_q", max_q), ("max_kv", max_kv)):
+            if not 0 <= int(x) <= 2 ** 31 - 1:
+                raise ValueError(f"PagedBatch: {name} must be in 0..2147483647, got {x}")
         self.cu_q, self.kv_lens, self.block_table = cu_q, kv_lens, block_table
         self.nseq, self.max_q, self.max_kv = n, int(max_q), int(max_kv)
         self._calls, self._dev = {}, kv_lens.get_device()

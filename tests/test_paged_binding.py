@@ -70,3 +70,15 @@ def test_first_calls_of_two_threads(monkeypatch):
     finally:
         sys.settrace(before)
     assert sage._torch is torch and not early
+
+
+@pytest.mark.parametrize("name", ["max_q", "max_kv"])
+@pytest.mark.parametrize("value", [2 ** 31, 2 ** 32 + 5, -1, -2 ** 32])
+def test_bounds_that_pass_32_bits(monkeypatch, name, value):
+    """The batch's bounds are 32-bit: a larger one is refused, not cut."""
+    monkeypatch.setattr(sage, "_on_device", lambda *a, **k: None)
+    args = dict(max_q=3, max_kv=40)
+    args[name] = value
+    i32 = dict(dtype=torch.int32)
+    with pytest.raises(ValueError, match=f"PagedBatch: {name} must be in 0..2147483647"):
+        sage.PagedBatch(torch.zeros(2, **i32), torch.zeros(1, **i32), torch.zeros(1, 3, **i32), **args)
