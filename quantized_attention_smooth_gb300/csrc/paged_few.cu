@@ -806,14 +806,14 @@ cudaError_t launch_few(const PagedAttnParams& p, int sms, cudaStream_t st) {
   constexpr int kUnitKeys = 16 * kWarps;
   const int64_t max_units = (static_cast<int64_t>(p.c.max_kv) + kUnitKeys - 1) / kUnitKeys + 1;
   const int64_t tiles = (static_cast<int64_t>(p.c.max_q) * p.group + 8 * kNr - 1) / (8 * kNr);
-  const int64_t items = tiles * p.c.Hkv * p.c.nseq;
+  const int64_t items = tiles * p.c.Hkv * p.c.nseq;    // below 2^63; times max_units perhaps not
   int ctas = sms * per < kMaxCtas ? sms * per : kMaxCtas;
-  if (items * max_units < ctas) ctas = static_cast<int>(items * max_units);
+  if (items < ctas && items * max_units < ctas) ctas = static_cast<int>(items * max_units);
   // Parts are joined by the CTA that finishes an item last, which saves a launch,
   // unless few items spread over many CTAs: one CTA would then read a hundred
   // parts or more, and a second kernel does it by the row.
   PagedAttnParams prm = p;
-  prm.join_inside = items * kJoinInside >= ctas;
+  prm.join_inside = items >= (ctas + kJoinInside - 1) / kJoinInside;
   kern<<<ctas, kThreads, L::kSmem, st>>>(prm);
   note_launch();
   e = cudaGetLastError();

@@ -1323,10 +1323,10 @@ cudaError_t launch_many(const PagedAttnParams& p, int sms, cudaStream_t st) {
   }
   // one CTA per SM, and no more than the units of the lengths the call declares
   const int64_t pairs = (static_cast<int64_t>(p.c.max_q) * p.group + kPairRows - 1) / kPairRows;
-  const int64_t most = pairs * p.c.nseq * p.c.Hkv *
-                       ((static_cast<int64_t>(p.c.max_kv) + kKeys - 1) / kKeys + 1);
+  const int64_t items = pairs * p.c.nseq * p.c.Hkv;   // below 2^58; times the tiles perhaps not
+  const int64_t tiles = (static_cast<int64_t>(p.c.max_kv) + kKeys - 1) / kKeys + 1;
   int ctas = sms < kMaxManyCtas ? sms : kMaxManyCtas;
-  if (most < ctas) ctas = static_cast<int>(most);
+  if (items < ctas && items * tiles < ctas) ctas = static_cast<int>(items * tiles);
   kern<<<ctas, L::kThreads, L::kAlloc, st>>>(mk, mv, ms, prm);
   note_launch();
   e = cudaGetLastError();
