@@ -51,6 +51,7 @@
 // issue slots with the widening warps: 2500 cycles a tile.
 
 #include <atomic>
+#include <cfloat>
 #include <type_traits>
 
 #include "sage_kernels.h"
@@ -948,7 +949,8 @@ paged_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
 #pragma unroll
             for (int g = 0; g < kRowsAtOnce; ++g) {
               const int e = __shfl_sync(kAll, ex, g * kVecs);
-              if (lane == in_warp - sub + g) sc = p.scale_log2 * power_of_2(e);
+              // not 0, however small the row and the scale: hidden logits are -inf
+              if (lane == in_warp - sub + g) sc = fmaxf(p.scale_log2 * power_of_2(e), FLT_MIN);
             }
           }
           const int row = (warp & 3) * 32 + in_warp;

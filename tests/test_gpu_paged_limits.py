@@ -8,6 +8,18 @@ from tests.test_gpu_paged import check, sage  # noqa: E402,F401
 pytestmark = pytest.mark.gpu
 
 
+@pytest.mark.parametrize("kind,dt", [("bf16", torch.bfloat16), ("f16", torch.float16),
+                                     ("q8", torch.bfloat16), ("q8", torch.float16)])
+@pytest.mark.parametrize("n", [1, 5, 200])
+@pytest.mark.parametrize("scale", [1e-8, 1e-30])
+def test_scale_near_zero_and_rows_of_zeros(sage, kind, dt, n, scale):  # noqa: F811
+    """All logits are next to zero, among them those of rows without a number in them."""
+    p = Problem([n, 40], [300, 40], 4, 2, 64, 16, "NHD", kind, dt, seed=71)
+    p.q[::2] = 0.0
+    p.q[1::4] = (p.q[1::4].float() * 1e-7).to(dt)
+    check(sage, p, scale)
+
+
 def test_declared_bounds_near_2_31(sage):  # noqa: F811
     """Bounds say what may come; 1024 sequences of a few keys each."""
     n = 1024
