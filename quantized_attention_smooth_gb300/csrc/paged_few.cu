@@ -1,7 +1,7 @@
 // Attention of few new tokens per sequence over the paged cache (decoding,
 // checking drafted tokens): bound by reading the cache once.
 //
-//   x_jr = c q_r . K_j  (base 2, fp32),  m_r = max_j x_jr,
+//   x_jr = c q_r . K_j  (base 2, fp32),  m_r a reference near max_j x_jr,
 //   O_r  = sum_j 2^(x_jr - m_r) V_j,  l_r = sum_j 2^(x_jr - m_r),  out = O / l
 //
 // The rows of one (sequence, kv head) are its new tokens times the query heads
@@ -48,7 +48,6 @@ namespace {
 constexpr int kThreads = 128, kWarps = 4;
 constexpr int kMaxCtas = 152 * 8;
 constexpr unsigned kAll = 0xFFFFFFFFu;
-constexpr float kLazy = 8.0f;     // log2 of the growth of a row's maximum that rescales O
 constexpr int kJoinInside = 40;   // most parts of an item, on average, that one CTA joins
 static_assert(kMaxCtas * 4 <= kArrivalBytes, "a counter for every CTA");
 
@@ -145,6 +144,7 @@ __global__ void __launch_bounds__(kThreads, Few<kKind, kDp, kNr>::kCtas)
 paged_few_kernel(const PagedAttnParams p) {
   constexpr bool kQ8 = kKind == kKindQ8;
   constexpr bool kMmaBF16 = kKind == kKindBF16;
+  constexpr float kDown = kBelow<kMmaBF16>, kOver = kLazy + kDown;
   constexpr int kRows = 8 * kNr;
   constexpr int kUnitBlocks = kWarps;                     // a unit: a block of each warp
   constexpr int kEl = kQ8 ? 1 : 2;                        // bytes of an element
@@ -461,12 +461,12 @@ paged_few_kernel(const PagedAttnParams p) {
                 v = see ? v : -INFINITY;
               }
               x[nr][e] = v;
-              over |= v > m[nr][e & 1] + kLazy;  // with m = -inf: any logit but -inf
+              over |= v > m[nr][e & 1] + kOver;  // with m = -inf: any logit but -inf
             }
           }
           if (__any_sync(kAll, over)) {
-            // Rare after the first block: references move to the maximum, O and l
-            // follow.  (Any reference gives the same result; P stays below 2^kLazy.)
+            // Rare after the first block: references move with the maximum, O and l
+            // follow.
             float alpha[kNr][2];
 #pragma unroll
             for (int nr = 0; nr < kNr; ++nr)
@@ -476,7 +476,7 @@ paged_few_kernel(const PagedAttnParams p) {
                 v = fmaxf(v, __shfl_xor_sync(kAll, v, 4));
                 v = fmaxf(v, __shfl_xor_sync(kAll, v, 8));
                 v = fmaxf(v, __shfl_xor_sync(kAll, v, 16));
-                const float next = v > m[nr][i] + kLazy ? v : m[nr][i];
+                const float next = v > m[nr][i] + kOver ? v - kDown : m[nr][i];
                 alpha[nr][i] = next == m[nr][i] ? 1.0f : fast_exp2(m[nr][i] - next);
                 m[nr][i] = next;
                 l[nr][i] *= alpha[nr][i];

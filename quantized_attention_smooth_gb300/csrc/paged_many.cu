@@ -28,8 +28,8 @@
 // before it, so S_t(j+1) ready also means that PV_t(j) is done, and a softmax
 // warp may rescale O_t itself, with nobody else at it.  It does so only when
 // the row's maximum has grown by more than 2^8 since m_ref was taken (any m_ref
-// gives the same result; P then stays below 2^8 and keeps its relative
-// precision), which after the first tiles is hardly ever.
+// gives the same result; P then stays below 2^8, or 2^15 in fp16, and keeps its
+// relative precision), which after the first tiles is hardly ever.
 //
 // Work is cut into units of (pair of tiles, kv head, 128 keys), dealt evenly to
 // one CTA per SM as one contiguous range each, derived from the lengths on the
@@ -68,7 +68,6 @@ constexpr unsigned kAll = 0xFFFFFFFFu;
 // pipeline takes about as long as this many tiles.  (Two prompts of 8192 tokens:
 // 930 us with 2, 830 with 3 or 4, 849 with 6: the first rows' items are short.)
 constexpr int kItemUnits = 4;
-constexpr float kLazy = 8.0f;             // log2 of the growth that rescales O
 
 struct ManyHead {
   int32_t parts, seq, head, pair;   // parts of the item from this one on; 0: none here
@@ -263,6 +262,7 @@ paged_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
   using L = Many<kKind, kDp>;
   constexpr bool kQ8 = L::kQ8;
   constexpr bool kMmaBF16 = kKind == kKindBF16;
+  constexpr float kDown = kBelow<kMmaBF16>, kOver = kLazy + kDown;
   constexpr int kStages = L::kStages;
   constexpr int kC = L::kC;
   // The driver places dynamic shared memory behind its 1 KB reservation of a
@@ -1060,9 +1060,9 @@ paged_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         };
         while (true) {
           const float top = masked ? weigh(std::true_type{}) : weigh(std::false_type{});
-          const bool grew = top > ref + kLazy || (ref == -INFINITY && top > -INFINITY);
+          const bool grew = top > ref + kOver || (ref == -INFINITY && top > -INFINITY);
           if (!__any_sync(kAll, grew)) break;
-          const float next = grew ? top : ref;
+          const float next = grew ? top - kDown : ref;
           const float alpha = grew ? fast_exp2(ref - next) : 1.0f;  // 0 from -inf
           if (i > 0) {
 #pragma unroll

@@ -40,6 +40,15 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   }
 }
 
+// A row's reference, from which P = 2^(x - reference) is taken, moves only when a
+// logit has outgrown it by 2^kLazy; any reference gives the same result.  In fp16
+// the reference is 2^7 below the maximum at which it is taken: P reaches 2^15, within
+// fp16's 65504, and a weight of 2^-31 of the largest is still a step of fp16.  (With
+// P up to 2^8 weights of 2^-25 and less went missing in O, but not in l.)
+constexpr float kLazy = 8.0f;
+template <bool kBF16>
+constexpr float kBelow = kBF16 ? 0.0f : 7.0f;
+
 // The exponent of |x|, within -126..126 (zero and subnormal numbers: -126), so
 // that 2^e and 2^-e are both normal; and 2^e.
 __device__ __forceinline__ int exponent_of(float x) {
