@@ -449,8 +449,10 @@ def rope_freqs(rotary_dim, base=10000.0, scaling=None, factor=1.0, original_len=
                   stretched by `factor`, the shortest kept
       "by_parts"  frequencies that turn fewer than `low` times in original_len
                   divided by `factor`, those above `high` kept, a linear ramp
-                  between
-      "yarn"      by_parts, and mscale = 0.1 ln(factor) + 1 on cos and sin"""
+                  in the number of turns between
+      "yarn"      between the same two ends, rounded outwards to whole pairs, a
+                  ramp linear in the pair's index i instead, as models trained
+                  with YaRN have it; and mscale = 0.1 ln(factor) + 1"""
     import math
     import torch
     r = int(rotary_dim)
@@ -466,11 +468,21 @@ def rope_freqs(rotary_dim, base=10000.0, scaling=None, factor=1.0, original_len=
     mscale = 1.0
     if scaling == "linear":
         f = f / factor
-    elif scaling in ("by_parts", "yarn"):
+    elif scaling == "by_parts":
         keep = ((original_len * f / (2 * math.pi) - low) / (high - low)).clamp(0, 1)
         f = f * (keep + (1 - keep) / factor)
-        if scaling == "yarn":
-            mscale = 0.1 * math.log(factor) + 1.0
+    elif scaling == "yarn":
+        if not (0 < low <= high and base > 1 and original_len > 0):
+            raise ValueError("rope_freqs: yarn scaling needs 0 < low <= high, base > 1 and a "
+                             "positive original_len")
+        # base ** (-2 i / r) * original_len / (2 pi) = n turns, solved for i
+        def pair(n):
+            return r / 2 * math.log(original_len / (2 * math.pi * n)) / math.log(base)
+        first, last = max(math.floor(pair(high)), 0), min(math.ceil(pair(low)), r - 1)
+        away = ((torch.arange(r // 2, dtype=torch.float64) - first) /
+                max(last - first, 1e-3)).clamp(0, 1)
+        f = f * (1 - away + away / factor)
+        mscale = 0.1 * math.log(factor) + 1.0
     elif scaling not in (None, "ntk"):
         raise ValueError(f"rope_freqs: unknown scaling {scaling!r}")
     return f.to(device), mscale
