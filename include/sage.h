@@ -417,8 +417,9 @@ SAGE_API sage_status sage_kv_stats_noalloc_status(sage_stream_t stream);
  *   q_out may be q itself with the same strides (in place), and likewise
  *       k_out; any other overlap of inputs and outputs is not supported.
  *   k may be NULL (Hkv = 0): q alone is turned.
- *   pos: device int64 (pos_bits 64) or int32 (32), any value; the angle is
- *       reduced exactly in 64-bit fixed point, so far positions lose nothing.
+ *   pos: device int64 (pos_bits 64) or int32 (32), any value.  The angle is
+ *       reduced in 64-bit fixed point: for frequencies from 0 on its error is
+ *       |pos| (inv_freq 2^-52 + 2^-62) rad, below fp32's own while |pos inv_freq| < 2^28 and |pos| < 2^38.
  *   inv_freq: device double[R/2]; R even, 2..D; D 1..128.
  *   inverse: turns by the negative angle (the transpose up to mscale^2): the
  *       gradient of the forward call, with the same mscale. */

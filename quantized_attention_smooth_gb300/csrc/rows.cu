@@ -10,9 +10,11 @@
 //
 // The angle of a far position needs more bits than fp32 has: pos * inv_freq is
 // formed in turns as a 64-bit fixed-point fraction, F = frac(inv_freq / 2 pi)
-// * 2^64, whose product with the position modulo 2^64 is exact, so one double
-// multiplication per frequency (2^-53 relative) is the only rounding before
-// the fraction is cut to fp32.
+// * 2^64, whose product with the position modulo 2^64 is exact.  F itself is off by
+// the roundings of 1 / (2 pi) and of one double multiplication (2^-53 of the turns
+// each) and by its own last bit, which the position multiplies: the phase is off by
+// |pos| (inv_freq 2^-52 + 2^-62) rad, less than the 2^-24 of the cut to fp32 while
+// |pos inv_freq| < 2^28 and |pos| < 2^38.
 //
 // The work is bound by memory: each row is read once and written once.  In the
 // first kernel a row belongs to 8 or 16 lanes of 8 channels (one 16-byte vector
