@@ -573,11 +573,9 @@ pair_rows_kernel(const RowsParams p) {
     turn_table(p, nt, tk.pos, cs);
     __syncthreads();
   }
-  for (int what = blockIdx.y; what < 3; what += gridDim.y) {
-    if (what == 0 && p.Hq > 0) pair_pass<kMode, 0, kBF16>(p, tk, cs, t0, nt);
-    if (what == 1 && p.Hkv > 0) pair_pass<kMode, 1, kBF16>(p, tk, cs, t0, nt);
-    if (kMode != 0 && what == 2) pair_pass<kMode, 2, kBF16>(p, tk, cs, t0, nt);
-  }
+  if (p.Hq > 0) pair_pass<kMode, 0, kBF16>(p, tk, cs, t0, nt);
+  if (p.Hkv > 0) pair_pass<kMode, 1, kBF16>(p, tk, cs, t0, nt);
+  if (kMode != 0) pair_pass<kMode, 2, kBF16>(p, tk, cs, t0, nt);
 }
 
 template <int kMode, bool kBF16>
@@ -587,8 +585,7 @@ cudaError_t launch_pairs(const RowsParams& p0, int sms, cudaStream_t st) {
   while (p.toks < kMaxPairToks && p.T / (2 * p.toks) >= 4 * sms) p.toks *= 2;
   const int64_t ctas = (p.T + p.toks - 1) / p.toks;
   if (ctas > 0x7FFFFFFF) return cudaErrorInvalidValue;
-  const unsigned y = ctas > 2 * sms ? 1 : 3;            // few tokens: a CTA per pass
-  pair_rows_kernel<kMode, kBF16><<<dim3(static_cast<unsigned>(ctas), y), kRowThreads, 0, st>>>(p);
+  pair_rows_kernel<kMode, kBF16><<<static_cast<unsigned>(ctas), kRowThreads, 0, st>>>(p);
   note_launch();
   return cudaGetLastError();
 }
