@@ -419,7 +419,8 @@ SAGE_API sage_status sage_kv_stats_noalloc_status(sage_stream_t stream);
  *   k may be NULL (Hkv = 0): q alone is turned.
  *   pos: device int64 (pos_bits 64) or int32 (32), any value.  The angle is
  *       reduced in 64-bit fixed point: for frequencies from 0 on its error is
- *       |pos| (inv_freq 2^-52 + 2^-62) rad, below fp32's own while |pos inv_freq| < 2^28 and |pos| < 2^38.
+ *       |pos| (inv_freq 2^-52 + 2^-62) rad, below fp32's own while
+ *       |pos inv_freq| < 2^28 and |pos| < 2^38.
  *   inv_freq: device double[R/2]; R even, 2..D; D 1..128.
  *   inverse: turns by the negative angle (the transpose up to mscale^2): the
  *       gradient of the forward call, with the same mscale. */
@@ -444,7 +445,9 @@ SAGE_API sage_status sage_rope(const void* q, const void* k, void* q_out, void* 
  *     [Hkv][Dp] (Dp = 64 if D <= 64 else 128), as sage_kv_stats_noalloc
  *     writes them for one sequence; they stay fixed while the cache is used.
  * page_size: a multiple of 16, up to 65536; D: a multiple of 8, 8..128; k and
- * v 16-byte aligned, strides multiples of 8 elements. */
+ * v 16-byte aligned, strides multiples of 8 elements.  An 8-bit cache is read
+ * fastest with D and strides of multiples of 16; otherwise 8 bytes at a time, which
+ * takes long chunks five times as long. */
 enum { SAGE_Q8 = 2 };
 typedef struct {
   void* k;

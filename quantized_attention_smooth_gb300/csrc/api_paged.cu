@@ -18,10 +18,21 @@ constexpr int64_t kMaxStride = int64_t(1) << 39;
 constexpr size_t kStatusBytes = 256;   // then the arrival counters
 constexpr size_t kClearBytes = kStatusBytes + kArrivalBytes;
 static_assert(kClearBytes == SAGE_PAGED_CLEAR_BYTES, "the header says what the caller clears");
-// Mean rows of a sequence from which on the tensor-core kernel takes them all:
-// with 16 decoding sequences and 4 chunks of 200-1500 tokens (mean 170 rows) the
-// two kernels take 277 us and the one 300; without short sequences the launch
-// that finds nothing costs 8.
+// Mean rows of a sequence from which on the tensor-core kernel takes them all.
+// Both sides measured (us, single tokens over 4000 keys beside chunks over as many):
+//   heads, channels   chunks     single tokens   mean rows   two kernels   one
+//   32 on 8, 128      1 x 1500   0               6000        132           123
+//   32 on 8, 128      4 x 1500   16              1203        458           440
+//   32 on 8, 128      4 x 400    16              323         200           179
+//   32 on 8, 128      4 x 400    64              98          319           329
+//   16 on 16, 80      16 x 1500  16              750         847           855
+//   16 on 16, 80      4 x 1500   64              89          566           642
+//   8 on 2, 64        4 x 400    4               802         74            49
+//   8 on 2, 64        1 x 100    4               83          65            32
+// The one kernel wins with few single tokens (about 4, or 16 with a group of 4) and
+// the two with many, by a quarter at most.  The mean, which is all that the host
+// knows, tells them apart only roughly: batches of many single tokens are on their
+// faster side, small ones with few of them pay up to twice (the last row).
 constexpr int64_t kAllMany = 512;
 size_t few_bytes() { return (paged_few_bytes() + 255) / 256 * 256; }
 

@@ -38,10 +38,11 @@
 // the window, behind the sinks) are never visited.  Values of keys that no row
 // of the pair sees are zeroed in shared memory (0 times NaN would be NaN).
 //
-// Measured on GB300 (32 query heads on 8 kv heads of 128 channels): 2048 new
-// tokens over 30720 cached ones, bf16, 752 us, 1417 TFLOP/s, 74 % of the measured
-// bf16 peak; two causal prompts of 8192 tokens 836 us, 1316 TFLOP/s; chunks over
-// the 8-bit cache 462 us, 948 TFLOP/s.  A key step of both tiles takes about 2950
+// Measured on GB300 (32 query heads on 8 kv heads of 128 channels; four calls in a
+// graph): 2048 new tokens over 30720 cached ones, bf16, 752 us, 1417 TFLOP/s, 74 %
+// of the measured bf16 peak; two causal prompts of 8192 tokens 836 us, 1316 TFLOP/s;
+// chunks over the 8-bit cache 462 us, 948 TFLOP/s.  Call after call, at the power
+// cap, they take 819 us (1302 TFLOP/s, 77 % of the sustained peak), 869 and 454.  A key step of both tiles takes about 2950
 // cycles against 2048 of the tensor pipe: the softmax of a tile (1490 cycles, two
 // and a half per instruction with one warp of it per scheduler) and its products
 // (1024 and the signals' latency) follow one another, and the two tiles overlap
@@ -66,7 +67,9 @@ constexpr uint32_t kTmemCols = 512;
 constexpr unsigned kAll = 0xFFFFFFFFu;
 // Units that an item costs besides its key tiles: filling and draining the
 // pipeline takes about as long as this many tiles.  (Two prompts of 8192 tokens:
-// 930 us with 2, 830 with 3 or 4, 849 with 6: the first rows' items are short.)
+// 945 us with 2, 847 with 3, 843 with 4, 865 with 6: the first rows' items are
+// short.  32 of 512: 190, 186, 183, 192; five ragged chunks: 362, 321, 314, 327; eight of
+// 2048 over the 8-bit cache: 621, 558, 524, 552.  Long chunks do not care.)
 constexpr int kItemUnits = 4;
 
 struct ManyHead {
@@ -540,7 +543,7 @@ paged_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
       // ================================================== copies of codes, for rows
       // and pages that tensor copies cannot take (D or a stride an odd multiple of
       // 8, page sizes that neither divide nor are multiples of 128); five times
-      // slower
+      // slower (three chunks of 1000 tokens over 9000: 2738 us against 484)
       Ring<L::kRawStages> ring;                 // K and V tiles alternate
       bool ok = true;
       const bool wide = c.wide;                 // rows in vectors of 16 bytes, else of 8

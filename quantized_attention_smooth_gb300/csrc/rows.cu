@@ -624,12 +624,19 @@ cudaError_t launch_mode(const RowsParams& p0, bool bf16, int sms, cudaStream_t s
 }  // namespace
 
 cudaError_t launch_rows(const RowsParams& p, int mode, bool bf16, int sms, cudaStream_t st) {
-  // Two vectors a lane from 4 tokens per SM on, for whole vectors: rotations of
-  // the half layout (rope of 16000 x 80 heads of 128: 128 us against 186; append
-  // of 24000 tokens with q: 124 against 213) and Q8 rows (65000 x 16 heads of 80:
-  // 122 against 228).  One vector a lane has the shorter way through few tokens
-  // (64: 3.8 us against 4.3; Q8 4.7 against 6.8) and is as fast or faster where
-  // pairs are neighbours (interleaved rope of the same rows: 110 against 118).
+  // Two vectors a lane from 4 tokens per SM on, for whole vectors.  Measured, two
+  // vectors against one (us; one call in a graph, L2 flushed):
+  //   rope, half layout, 16000 tokens x (40 + 40) heads of 128      132   192
+  //   16-bit append, half layout, q beside it: 24000 tokens, 32 q
+  //     heads on 8 kv heads of 128                                 130   192
+  //     65000 tokens, 16 on 16 heads of 80                         231   370
+  //   16-bit append as it is, 65000 x 16 of 80 | 16000 x 40 of 128  128   161 | 122   120
+  //   Q8 append as it is, the same two                             128   237 | 149   156
+  //   Q8 append, half layout, the rows of the 16-bit one           210   220 | 280   471
+  //   Q8 append, interleaved, 24000 tokens, 32 on 8 of 128          261   161
+  // The last one is on the slower side.  One vector a lane has the shorter way
+  // through few tokens (64: 3.8 us against 4.3; Q8 4.7 against 6.8), and rope and
+  // 16-bit appends whose pairs are neighbours stay with it (110 against 118).
   const bool apart = p.inv_freq != nullptr && !p.interleaved;
   const bool neighbours = p.inv_freq != nullptr && p.interleaved;
   const bool pairs = p.vec && p.T >= 4 * static_cast<int64_t>(sms) &&
