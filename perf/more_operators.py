@@ -306,7 +306,7 @@ def prepare(case, seed):
         s["table"][req.long()[row], slot] = order[:sum(have)]
         s["free"] = torch.full((total,), -1, dtype=torch.int32, device=dev)
         s["free"][:c["spare"]] = order[sum(have):]
-        s["counts"] = torch.tensor([c["spare"], 0], dtype=torch.int32, device=dev)
+        s["left"] = torch.tensor([c["spare"]], dtype=torch.int32, device=dev)
         s["rows"], s["max_q"] = sum(new), max(new)
         return s
 
@@ -424,7 +424,7 @@ def _plain_step(s):
     have, after = (old + page - 1) // page, (old + new + page - 1) // page
     need = after - have
     upto = need.cumsum(0)
-    free = s["counts"][0].long()
+    free = s["left"][0].long()
     fits = ((need == 0) | (upto <= free)) & (old + new <= c["max_len"])
     got = torch.where(fits, need, 0)
     end = torch.where(fits, have + need, have)
@@ -442,23 +442,23 @@ def _plain_step(s):
     kv_lens = torch.where(fits, old + new, 0)
     s["table"][req] = torch.where(j < end[:, None], table.int(), s["table"][req])
     s["lens"][req] = torch.where(fits, old + new, old).int()
-    s["counts"][0] -= got.sum()
+    s["left"] -= got.sum().int()
     # back to the lengths from before: the pages go onto the stack in the order that
     # undoes the step
     now, keep = s["lens"][req].long(), s["keep"].long()
     back = (now + page - 1) // page - (keep + page - 1) // page
     first = (back.cumsum(0) - back)[:, None] - ((keep + page - 1) // page)[:, None]
-    total = s["counts"][0].long() + back.sum()
+    total = s["left"][0].long() + back.sum()
     gone = (j >= ((keep + page - 1) // page)[:, None]) & (j < ((now + page - 1) // page)[:, None])
     to = torch.where(gone, total - 1 - first - j, s["free"].numel())
     room = torch.cat((s["free"], s["free"][:1]))
     room[to] = s["table"][req]
     s["free"].copy_(room[:-1])
     s["lens"][req] = torch.minimum(now, keep).int()
-    s["counts"][0] += back.sum()
+    s["left"] += back.sum().int()
     return {"cu_q": cu.int(), "kv_lens": kv_lens.int(), "block_table": table.int(),
             "positions": pos, "slots": slots, "denied": (~fits).sum().int(), "lens": s["lens"],
-            "free": s["free"], "left": s["counts"][0]}
+            "free": s["free"], "left": s["left"]}
 
 
 def _values(s, name, packed, groups):
@@ -558,7 +558,7 @@ def _own_step(s):
     from quantized_attention_smooth_gb300 import sage
     c = s["case"]
     if "pool" not in s:
-        s["pool"] = sage.PagePool(s["free"], s["counts"], s["table"], s["lens"], c["page"])
+        s["pool"] = sage.PagePool(s["free"], s["left"], s["table"], s["lens"], c["page"])
         s["plan"] = sage.PagedPlan(s["pool"], c["n"], s["rows"], s["max_q"], c["max_len"])
         s["ws"] = sage.alloc_workspace_paged()
     pool, plan = s["pool"], s["plan"]
@@ -566,7 +566,7 @@ def _own_step(s):
     sage.paged_trim(pool, s["req"], s["keep"], ws=s["ws"])
     return {"cu_q": plan.cu_q, "kv_lens": plan.kv_lens, "block_table": plan.block_table,
             "positions": plan.positions, "slots": plan.slots, "denied": plan.denied,
-            "lens": s["lens"], "free": s["free"], "left": s["counts"][0]}
+            "lens": s["lens"], "free": s["free"], "left": s["left"]}
 
 
 def _own_append(s):
