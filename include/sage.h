@@ -432,6 +432,20 @@ SAGE_API sage_status sage_rope(const void* q, const void* k, void* q_out, void* 
                                int interleaved, float mscale, int inverse,
                                sage_stream_t stream);
 
+/* sage_rope with positions of several axes (time, height and width of a video's
+ * or an image's tokens): pair i turns by pos[axis_of[i]][t] * inv_freq[i].  Any
+ * pair may follow any axis, with any frequency, so sections of the pairs, axes in
+ * turn along them and axes with frequencies of their own are all served.
+ *   pos: device, naxes rows of T positions, axis_stride elements apart; naxes 1..8.
+ *   axis_of: device uint8_t[R/2], entries below naxes (a larger one takes the last
+ *       axis); NULL: axis 0 for every pair. */
+SAGE_API sage_status sage_rope_axes(
+    const void* q, const void* k, void* q_out, void* k_out, int dtype, int64_t T, int64_t Hq,
+    int64_t Hkv, int64_t D, const int64_t* q_strides, const int64_t* k_strides,
+    const int64_t* qo_strides, const int64_t* ko_strides, const void* pos, int pos_bits,
+    int64_t naxes, int64_t axis_stride, const uint8_t* axis_of, const double* inv_freq, int64_t R,
+    int interleaved, float mscale, int inverse, sage_stream_t stream);
+
 /* A paged key/value cache.  Page p, slot t, kv head h holds D channels of K
  * and V at p*page_stride + t*token_stride + h*head_stride elements of k and
  * of v (both tensors share the strides, which cover (pages, slots, heads, D)
@@ -444,20 +458,29 @@ SAGE_API sage_status sage_rope(const void* q, const void* k, void* q_out, void* 
  *     codes of v / v_scale, saturating.  k_mean and v_scale are fp32
  *     [Hkv][Dp] (Dp = 64 if D <= 64 else 128), as sage_kv_stats_noalloc
  *     writes them for one sequence; they stay fixed while the cache is used.
+ *   kind SAGE_Q4: codes n = -7..7 of four bits, each run of 32 channels of a
+ *     token and head with an fp16 scale s: K = n s + k_mean, V = n s 64 v_scale
+ *     (k_mean and v_scale as for SAGE_Q8).  A row is 16 ceil(D/32) bytes,
+ *     n + 8 of channel c in the low (c even) or high half of byte c/2, and the
+ *     strides count bytes, multiples of 16.  Scales: k_groups and v_groups
+ *     [num_pages][Hkv][page_size][Dp/32] fp16.  K less its mean saturates at
+ *     7 * 9352, V at 448 v_scale as in SAGE_Q8.
  * page_size: a multiple of 16, up to 65536; D: a multiple of 8, 8..128; k and
  * v 16-byte aligned, strides multiples of 8 elements.  An 8-bit cache is read
  * fastest with D and strides of multiples of 16; otherwise 8 bytes at a time, which
  * takes long chunks five times as long. */
-enum { SAGE_Q8 = 2 };
+enum { SAGE_Q8 = 2, SAGE_Q4 = 3 };
 typedef struct {
   void* k;
   void* v;
   float* k_scale;        /* SAGE_Q8 only, else NULL */
-  const float* k_mean;   /* SAGE_Q8 only, else NULL */
-  const float* v_scale;  /* SAGE_Q8 only, else NULL */
+  const float* k_mean;   /* SAGE_Q8 and SAGE_Q4 only, else NULL */
+  const float* v_scale;  /* SAGE_Q8 and SAGE_Q4 only, else NULL */
   int64_t num_pages, page_size, Hkv, D;
   int64_t page_stride, token_stride, head_stride;
   int32_t kind;
+  void* k_groups;        /* SAGE_Q4 only, not read otherwise */
+  void* v_groups;        /* SAGE_Q4 only, not read otherwise */
 } sage_paged_cache;
 
 /* A batch of new tokens.  Sequence s holds the packed rows cu_q[s] ..
@@ -504,13 +527,96 @@ SAGE_API sage_status sage_kv_append(const sage_paged_cache* cache, const sage_pa
                                     int interleaved, float mscale, void* ws, size_t ws_bytes,
                                     sage_stream_t stream);
 
+/* sage_kv_append whose rotation takes the positions given (as sage_rope_axes
+ * does; T = total_q of them on each axis) in place of the tokens' places in their
+ * sequences, which say where they are stored.  inv_freq is needed. */
+SAGE_API sage_status sage_kv_append_axes(
+    const sage_paged_cache* cache, const sage_paged_batch* batch, const void* k, const void* v,
+    const void* q, void* q_out, int dtype, int64_t Hq, const int64_t* k_strides,
+    const int64_t* v_strides, const int64_t* q_strides, const int64_t* qo_strides, const void* pos,
+    int pos_bits, int64_t naxes, int64_t axis_stride, const uint8_t* axis_of,
+    const double* inv_freq, int64_t R, int interleaved, float mscale, void* ws, size_t ws_bytes,
+    sage_stream_t stream);
+
+/* Reads the batch's tokens (T rows) back from the cache as 16-bit rows, k and v
+ * (T,Hkv,D) of `dtype` (a 16-bit cache: its own): what sage_kv_append stored of
+ * them, rotation included, K with its mean.  A batch whose new tokens are all
+ * the cached ones gives whole sequences, for a dense call over a cached prefix
+ * or for another cache.  Tokens at negative positions and on pages outside the
+ * cache give zeros; rows behind cu_q[nseq] are left as they are.
+ *   k_strides, v_strides: host int64[2], {token, head}; NULL: dense. */
+SAGE_API sage_status sage_kv_gather(const sage_paged_cache* cache, const sage_paged_batch* batch,
+                                    void* k, void* v, int dtype, const int64_t* k_strides,
+                                    const int64_t* v_strides, void* ws, size_t ws_bytes,
+                                    sage_stream_t stream);
+
+/* The pages of a cache and who holds them, in device memory of the caller's:
+ *   free_pages [num_pages]: a stack of page indices, the next one to go at its end;
+ *   left [1]: pages on it;
+ *   table [max_requests][table_stride]: each request's pages, table_width at most;
+ *   lens [max_requests]: its cached length;
+ *   marks [max_requests]: the library's, zero before the first call.
+ * Aligned to their elements; calls on one pool run in stream order. */
+typedef struct {
+  int32_t* free_pages;
+  int32_t* left;
+  int32_t* table;
+  int32_t* lens;
+  uint32_t* marks;
+  int64_t num_pages, page_size, max_requests, table_stride, table_width;
+} sage_page_pool;
+
+/* What a step of n sequences gets: cu_q [n+1], kv_lens [n] and block_table
+ * [n][table_stride] make a sage_paged_batch; of each of `rows` packed rows, its
+ * position in its sequence and its slot, page * page_size + place in the page
+ * (either may be NULL); denied [1]: sequences that got no pages. */
+typedef struct {
+  int32_t* cu_q;
+  int32_t* kv_lens;
+  int32_t* block_table;
+  int64_t* positions;
+  int64_t* slots;
+  int32_t* denied;
+  int64_t n, rows, table_stride, table_width;
+  int32_t max_q, max_kv;
+} sage_paged_plan;
+
+/* Makes room for new_lens[i] more tokens of request requests[i] (rows of the
+ * pool's tables; both device int32 [n]), takes the pages that they need from the
+ * pool, advances the pool's lengths, and writes the plan's tables: sequence i has
+ * rows cu_q[i] .. cu_q[i+1]-1 and kv_lens[i] cached tokens with the new ones.
+ * Entries of the block table behind a sequence's pages are -1.
+ * Requests are served in order while the pages last: once one's pages do not
+ * fit, it and every later one that needs pages are denied.  A denied sequence keeps
+ * its rows (position and slot -1) and its length in the pool, and its kv_lens[i] is
+ * 0, which sage_kv_append and sage_attn_paged take for rows without a place.
+ * Denied as well, and recorded in the workspace's status word: a request outside the
+ * pool or given before in the same call, a length below zero, more than max_q new
+ * tokens or max_kv in all, more pages than either table has columns, rows that pass
+ * `rows` (nothing is written behind it).  Page indices are handed out as they lie on
+ * the stack.  n up to 65536, page_size as in sage_paged_cache; the workspace is the
+ * paged calls'. */
+SAGE_API sage_status sage_paged_step(const sage_page_pool* pool, const sage_paged_plan* plan,
+                                     const int32_t* requests, const int32_t* new_lens, void* ws,
+                                     size_t ws_bytes, sage_stream_t stream);
+
+/* Cuts requests (device int32 [n]) to keep_lens[i] tokens (NULL: none, the
+ * request ends) and puts the pages behind them back on the stack: drafted tokens
+ * that were rejected, finished requests.  A length that is not longer stays.  The
+ * pages go back in the order that undoes a step: cutting a step's requests to
+ * their lengths before it leaves the stack as it was.  A request outside the pool
+ * or given before in the same call is skipped and recorded in the status word. */
+SAGE_API sage_status sage_paged_trim(const sage_page_pool* pool, const int32_t* requests,
+                                     const int32_t* keep_lens, int64_t n, void* ws,
+                                     size_t ws_bytes, sage_stream_t stream);
+
 /* Attention of the new tokens (q (T,Hq,D)) over the cache, causal: the row
  * at position p sees the keys j <= p of its sequence, and with window > 0 of
  * those only j > p - window and j < sinks.  Logits, softmax and sums in fp32,
  * P rounded to 16 bits for the tensor cores.  out: dense (T,Hq,D) of q's
  * type; lse: NULL or fp32 (T,Hq), the natural logarithm of the row's sum of
- * exponentials (of the smoothed logits with SAGE_Q8: all of a row's logits
- * lack sm_scale * q . k_mean).  A row without visible keys gives zeros and
+ * exponentials (of the smoothed logits with SAGE_Q8 and SAGE_Q4: all of a row's
+ * logits lack sm_scale * q . k_mean).  A row without visible keys gives zeros and
  * -inf.  Keys and values that no row sees may hold anything; visible ones
  * are finite.  How the work is split into parts goes by the whole batch, so a
  * sequence's rows may differ in their last bits between batches, never between

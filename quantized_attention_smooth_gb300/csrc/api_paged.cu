@@ -77,9 +77,9 @@ sage_status paged_geo(const sage_paged_cache* cache, const sage_paged_batch* b, 
   if (cache == nullptr || b == nullptr)
     return refuse(SAGE_ERR_INVALID_ARG, "cache and batch must not be null");
   const int kind = cache->kind;
-  if (kind != SAGE_F16 && kind != SAGE_BF16 && kind != SAGE_Q8)
-    return refuse(SAGE_ERR_INVALID_ARG, "cache kind %d is none of SAGE_F16, SAGE_BF16, SAGE_Q8",
-                  kind);
+  if (kind != SAGE_F16 && kind != SAGE_BF16 && kind != SAGE_Q8 && kind != SAGE_Q4)
+    return refuse(SAGE_ERR_INVALID_ARG,
+                  "cache kind %d is none of SAGE_F16, SAGE_BF16, SAGE_Q8, SAGE_Q4", kind);
   if (cache->D < 8 || cache->D > 128 || cache->D % 8 != 0)
     return refuse(SAGE_ERR_UNSUPPORTED, "a paged cache needs head_dim D=%lld in 8..128, a "
                   "multiple of 8", (long long)cache->D);
@@ -91,14 +91,17 @@ sage_status paged_geo(const sage_paged_cache* cache, const sage_paged_batch* b, 
                   (long long)cache->Hkv, (long long)cache->num_pages);
   if (cache->k == nullptr || cache->v == nullptr || !on(cache->k, 16) || !on(cache->v, 16))
     return refuse(SAGE_ERR_INVALID_ARG, "cache k and v must be 16-byte aligned device pointers");
-  const int64_t ps = cache->num_pages > 1 ? cache->page_stride : cache->D;
+  // a row: D elements, or the bytes of its groups
+  const int64_t row = kind == SAGE_Q4 ? 16 * ((cache->D + 31) / 32) : cache->D;
+  const int64_t unit = kind == SAGE_Q4 ? 16 : 8;
+  const int64_t ps = cache->num_pages > 1 ? cache->page_stride : row;
   const int64_t ts = cache->token_stride;
-  const int64_t hs = cache->Hkv > 1 ? cache->head_stride : cache->D;
-  if (ps < cache->D || ts < cache->D || hs < cache->D || ps >= kMaxStride || ts >= kMaxStride ||
-      hs >= kMaxStride || ps % 8 != 0 || ts % 8 != 0 || hs % 8 != 0)
+  const int64_t hs = cache->Hkv > 1 ? cache->head_stride : row;
+  if (ps < row || ts < row || hs < row || ps >= kMaxStride || ts >= kMaxStride ||
+      hs >= kMaxStride || ps % unit != 0 || ts % unit != 0 || hs % unit != 0)
     return refuse(SAGE_ERR_UNSUPPORTED, "cache strides {page %lld, token %lld, head %lld} must be "
-                  "multiples of 8 elements, at least D and below 2^39",
-                  (long long)ps, (long long)ts, (long long)hs);
+                  "multiples of %lld elements, at least %lld (a row) and below 2^39",
+                  (long long)ps, (long long)ts, (long long)hs, (long long)unit, (long long)row);
   if (static_cast<__int128>(cache->num_pages) * ps +
           static_cast<__int128>(cache->page_size) * ts + static_cast<__int128>(cache->Hkv) * hs >
       (static_cast<__int128>(1) << 60))
@@ -108,6 +111,13 @@ sage_status paged_geo(const sage_paged_cache* cache, const sage_paged_batch* b, 
         !on(cache->k_scale, 16) || !on(cache->k_mean, 16) || !on(cache->v_scale, 16))
       return refuse(SAGE_ERR_INVALID_ARG, "a SAGE_Q8 cache needs k_scale, k_mean and v_scale, "
                     "16-byte aligned device pointers");
+  }
+  if (kind == SAGE_Q4) {
+    if (cache->k_groups == nullptr || cache->v_groups == nullptr || cache->k_mean == nullptr ||
+        cache->v_scale == nullptr || !on(cache->k_groups, 16) || !on(cache->v_groups, 16) ||
+        !on(cache->k_mean, 16) || !on(cache->v_scale, 16))
+      return refuse(SAGE_ERR_INVALID_ARG, "a SAGE_Q4 cache needs k_groups, v_groups, k_mean and "
+                    "v_scale, 16-byte aligned device pointers");
   }
   if (b->nseq < 0 || b->total_q < 0 || b->max_q < 0 || b->max_kv < 0 || b->table_width < 0)
     return refuse(SAGE_ERR_INVALID_ARG, "negative batch size (nseq=%lld total_q=%lld max_q=%d "
@@ -137,6 +147,10 @@ sage_status paged_geo(const sage_paged_cache* cache, const sage_paged_batch* b, 
   g->k = static_cast<uint8_t*>(cache->k);
   g->v = static_cast<uint8_t*>(cache->v);
   g->k_scale = cache->k_scale;
+  if (kind == SAGE_Q4) {
+    g->k_groups = static_cast<uint16_t*>(cache->k_groups);
+    g->v_groups = static_cast<uint16_t*>(cache->v_groups);
+  }
   g->k_mean = cache->k_mean;
   g->v_scale = cache->v_scale;
   g->num_pages = cache->num_pages;
@@ -149,9 +163,11 @@ sage_status paged_geo(const sage_paged_cache* cache, const sage_paged_batch* b, 
   g->page_size = static_cast<int32_t>(cache->page_size);
   g->kind = kind;
   g->page_shift = (g->page_size & (g->page_size - 1)) == 0 ? __builtin_ctz(g->page_size) : -1;
-  // strides are multiples of 8 elements: 16 bytes, or 8 of an 8-bit cache
+  // strides are multiples of 8 elements: 16 bytes, or 8 of an 8-bit cache (of 16 bytes
+  // with 4 bits)
   const int64_t vec = kind == SAGE_Q8 ? 16 : 8;
-  g->wide = cache->D % vec == 0 && ps % vec == 0 && ts % vec == 0 && hs % vec == 0;
+  g->wide = kind == SAGE_Q4 || cache->D % vec == 0 && ps % vec == 0 && ts % vec == 0 &&
+            hs % vec == 0;
   g->cu_q = b->cu_q;
   g->kv_lens = b->kv_lens;
   g->table = b->block_table;
@@ -164,19 +180,100 @@ sage_status paged_geo(const sage_paged_cache* cache, const sage_paged_batch* b, 
   return SAGE_OK;
 }
 
-}  // namespace
+// Where a rotation takes its positions from.
+struct Axes {
+  const void* pos;
+  int pos_bits;
+  int32_t naxes;             // 0: sage_rope's one axis, or the cache's places
+  int64_t stride;
+  const uint8_t* axis_of;
+  void give(RowsParams* p) const {
+    p->pos = pos;
+    p->pos64 = pos_bits == 64;
+    p->naxes = naxes;
+    p->axis_stride = stride;
+    p->axis_of = axis_of;
+  }
+};
 
-extern "C" {
-
-size_t sage_workspace_bytes_paged(void) {
-  return kClearBytes + few_bytes() + paged_many_bytes();
+sage_status check_axes(int64_t naxes, int64_t stride, int64_t T) {
+  if (naxes < 1 || naxes > 8)
+    return refuse(SAGE_ERR_UNSUPPORTED, "naxes=%lld is outside 1..8", (long long)naxes);
+  if (naxes > 1 && (stride < T || stride >= kMaxStride))
+    return refuse(SAGE_ERR_INVALID_ARG, "axis_stride=%lld is below T=%lld or beyond 2^39",
+                  (long long)stride, (long long)T);
+  return SAGE_OK;
 }
 
-sage_status sage_rope(const void* q, const void* k, void* q_out, void* k_out, int dtype, int64_t T,
+sage_status check_positions(const void* pos, int pos_bits) {
+  if (pos_bits != 32 && pos_bits != 64)
+    return refuse(SAGE_ERR_INVALID_ARG, "pos_bits=%d is neither 32 nor 64", pos_bits);
+  if (pos == nullptr || !on(pos, pos_bits / 8))
+    return refuse(SAGE_ERR_INVALID_ARG, "pos must be an aligned device pointer");
+  return SAGE_OK;
+}
+
+sage_status check_kind(const sage_paged_cache* cache, int dtype) {
+  if (cache->kind != SAGE_Q8 && cache->kind != SAGE_Q4 && cache->kind != dtype)
+    return refuse(SAGE_ERR_INVALID_ARG, "dtype %d differs from the cache's kind %d", dtype,
+                  cache->kind);
+  return SAGE_OK;
+}
+
+sage_status pool_params(const sage_page_pool* pool, const int32_t* requests, int64_t n, void* ws,
+                        size_t ws_bytes, PoolParams* p) {
+  if (pool == nullptr) return refuse(SAGE_ERR_INVALID_ARG, "pool and plan must not be null");
+  if (n < 0 || n > kMaxStepSeqs)
+    return refuse(SAGE_ERR_UNSUPPORTED, "n=%lld sequences are not within 0..%d", (long long)n,
+                  kMaxStepSeqs);
+  if (pool->page_size < 16 || pool->page_size > 65536 || pool->page_size % 16 != 0)
+    return refuse(SAGE_ERR_UNSUPPORTED, "page_size=%lld must be a multiple of 16, up to 65536",
+                  (long long)pool->page_size);
+  if (pool->num_pages < 1 || pool->num_pages > INT_MAX || pool->max_requests < 1 ||
+      pool->max_requests > INT_MAX || pool->table_width < 1 || pool->table_width > INT_MAX)
+    return refuse(SAGE_ERR_INVALID_ARG, "num_pages=%lld, max_requests=%lld or table_width=%lld "
+                  "out of range", (long long)pool->num_pages, (long long)pool->max_requests,
+                  (long long)pool->table_width);
+  if (pool->max_requests > 1 &&
+      (pool->table_stride < pool->table_width || pool->table_stride >= kMaxStride / 2))
+    return refuse(SAGE_ERR_INVALID_ARG, "the pool's table_stride=%lld is below its table_width="
+                  "%lld or beyond 2^38", (long long)pool->table_stride,
+                  (long long)pool->table_width);
+  if (pool->free_pages == nullptr || pool->left == nullptr || pool->table == nullptr ||
+      pool->lens == nullptr || pool->marks == nullptr || !on(pool->free_pages, 4) ||
+      !on(pool->left, 4) || !on(pool->table, 4) || !on(pool->lens, 4) || !on(pool->marks, 4))
+    return refuse(SAGE_ERR_INVALID_ARG, "the pool's free_pages, left, table, lens and marks must "
+                  "be 4-byte aligned device pointers");
+  if (n > 0 && (requests == nullptr || !on(requests, 4)))
+    return refuse(SAGE_ERR_INVALID_ARG, "requests must be a 4-byte aligned device pointer");
+  if (ws == nullptr || !on(ws, 256))
+    return refuse(SAGE_ERR_WORKSPACE, "workspace must be a 256-byte aligned device pointer");
+  if (ws_bytes < sage_workspace_bytes_paged())
+    return refuse(SAGE_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes,
+                  sage_workspace_bytes_paged());
+  p->free_pages = pool->free_pages;
+  p->left = pool->left;
+  p->table = pool->table;
+  p->lens = pool->lens;
+  p->marks = pool->marks;
+  p->table_stride = pool->max_requests > 1 ? pool->table_stride : 0;
+  p->width = pool->table_width;
+  p->num_pages = static_cast<int32_t>(pool->num_pages);
+  p->page_size = static_cast<int32_t>(pool->page_size);
+  p->page_shift = (p->page_size & (p->page_size - 1)) == 0 ? __builtin_ctz(p->page_size) : -1;
+  p->max_requests = static_cast<int32_t>(pool->max_requests);
+  p->n = static_cast<int32_t>(n);
+  p->requests = requests;
+  // the parts of split results lie idle between calls
+  p->seqs = reinterpret_cast<int4*>(static_cast<uint8_t*>(ws) + kClearBytes);
+  p->status = static_cast<uint32_t*>(ws);
+  return SAGE_OK;
+}
+
+sage_status rope(const void* q, const void* k, void* q_out, void* k_out, int dtype, int64_t T,
                       int64_t Hq, int64_t Hkv, int64_t D, const int64_t* q_strides,
                       const int64_t* k_strides, const int64_t* qo_strides,
-                      const int64_t* ko_strides, const void* pos, int pos_bits,
-                      const double* inv_freq, int64_t R, int interleaved, float mscale,
+                      const int64_t* ko_strides, const Axes& axes, const double* inv_freq, int64_t R, int interleaved, float mscale,
                       int inverse, sage_stream_t stream) {
   sage_status s = check_dtype(dtype);
   if (s != SAGE_OK) return s;
@@ -192,10 +289,7 @@ sage_status sage_rope(const void* q, const void* k, void* q_out, void* k_out, in
       !on(k, 2) || !on(q_out, 2) || !on(k_out, 2))
     return refuse(SAGE_ERR_INVALID_ARG, "q, k and their outputs must be 2-byte aligned device "
                   "pointers");
-  if (pos_bits != 32 && pos_bits != 64)
-    return refuse(SAGE_ERR_INVALID_ARG, "pos_bits=%d is neither 32 nor 64", pos_bits);
-  if (pos == nullptr || !on(pos, pos_bits / 8))
-    return refuse(SAGE_ERR_INVALID_ARG, "pos must be an aligned device pointer");
+  if ((s = check_positions(axes.pos, axes.pos_bits)) != SAGE_OK) return s;
   if ((s = check_rotation(inv_freq, R, D)) != SAGE_OK) return s;
   RowsParams p{};
   if ((s = row_strides("q", q_strides, T, Hq, D, &p.q_tok, &p.q_head)) != SAGE_OK) return s;
@@ -218,8 +312,7 @@ sage_status sage_rope(const void* q, const void* k, void* q_out, void* k_out, in
   p.Hq = static_cast<int32_t>(Hq);
   p.Hkv = static_cast<int32_t>(Hkv);
   p.D = static_cast<int32_t>(D);
-  p.pos = pos;
-  p.pos64 = pos_bits == 64;
+  axes.give(&p);
   p.inv_freq = inv_freq;
   p.R = static_cast<int32_t>(R);
   p.interleaved = interleaved ? 1 : 0;
@@ -232,19 +325,17 @@ sage_status sage_rope(const void* q, const void* k, void* q_out, void* k_out, in
   return e == cudaSuccess ? succeeded() : cuda_refused(e, "rotary launch");
 }
 
-sage_status sage_kv_append(const sage_paged_cache* cache, const sage_paged_batch* batch,
+sage_status append(const sage_paged_cache* cache, const sage_paged_batch* batch,
                            const void* k, const void* v, const void* q, void* q_out, int dtype,
                            int64_t Hq, const int64_t* k_strides, const int64_t* v_strides,
                            const int64_t* q_strides, const int64_t* qo_strides,
-                           const double* inv_freq, int64_t R, int interleaved, float mscale,
+                           const Axes& axes, const double* inv_freq, int64_t R, int interleaved, float mscale,
                            void* ws, size_t ws_bytes, sage_stream_t stream) {
   sage_status s = check_dtype(dtype);
   if (s != SAGE_OK) return s;
   RowsParams p{};
   if ((s = paged_geo(cache, batch, ws, ws_bytes, &p.c)) != SAGE_OK) return s;
-  if (cache->kind != SAGE_Q8 && cache->kind != dtype)
-    return refuse(SAGE_ERR_INVALID_ARG, "dtype %d differs from the cache's kind %d", dtype,
-                  cache->kind);
+  if ((s = check_kind(cache, dtype)) != SAGE_OK) return s;
   const int64_t T = batch->total_q, Hkv = cache->Hkv, D = cache->D;
   if (q != nullptr && inv_freq == nullptr)
     return refuse(SAGE_ERR_INVALID_ARG, "q is given without inv_freq: there is nothing to do");
@@ -275,6 +366,7 @@ sage_status sage_kv_append(const sage_paged_cache* cache, const sage_paged_batch
   p.Hq = q != nullptr ? static_cast<int32_t>(Hq) : 0;
   p.Hkv = static_cast<int32_t>(Hkv);
   p.D = static_cast<int32_t>(D);
+  axes.give(&p);
   p.inv_freq = inv_freq;
   p.R = inv_freq != nullptr ? static_cast<int32_t>(R) : 0;
   p.interleaved = interleaved ? 1 : 0;
@@ -283,9 +375,158 @@ sage_status sage_kv_append(const sage_paged_cache* cache, const sage_paged_batch
   p.vec = vec_rows(k, p.k_tok, p.k_head) && vec_rows(v, p.v_tok, p.v_head) &&
           (q == nullptr ||
            (vec_rows(q, p.q_tok, p.q_head) && vec_rows(q_out, p.qo_tok, p.qo_head)));
-  const cudaError_t e = launch_rows(p, cache->kind == SAGE_Q8 ? 2 : 1, dtype == SAGE_BF16, sms,
+  const cudaError_t e = launch_rows(p, cache->kind == SAGE_Q4 ? 3 : cache->kind == SAGE_Q8 ? 2 : 1, dtype == SAGE_BF16, sms,
                                     reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? succeeded() : cuda_refused(e, "cache append launch");
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t sage_workspace_bytes_paged(void) {
+  return kClearBytes + few_bytes() + paged_many_bytes();
+}
+
+sage_status sage_rope(const void* q, const void* k, void* q_out, void* k_out, int dtype, int64_t T,
+                      int64_t Hq, int64_t Hkv, int64_t D, const int64_t* q_strides,
+                      const int64_t* k_strides, const int64_t* qo_strides,
+                      const int64_t* ko_strides, const void* pos, int pos_bits,
+                      const double* inv_freq, int64_t R, int interleaved, float mscale,
+                      int inverse, sage_stream_t stream) {
+  const Axes one{pos, pos_bits, 0, 0, nullptr};
+  return rope(q, k, q_out, k_out, dtype, T, Hq, Hkv, D, q_strides, k_strides, qo_strides,
+              ko_strides, one, inv_freq, R, interleaved, mscale, inverse, stream);
+}
+
+sage_status sage_rope_axes(const void* q, const void* k, void* q_out, void* k_out, int dtype,
+                           int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
+                           const int64_t* q_strides, const int64_t* k_strides,
+                           const int64_t* qo_strides, const int64_t* ko_strides, const void* pos,
+                           int pos_bits, int64_t naxes, int64_t axis_stride,
+                           const uint8_t* axis_of, const double* inv_freq, int64_t R,
+                           int interleaved, float mscale, int inverse, sage_stream_t stream) {
+  const sage_status s = check_axes(naxes, axis_stride, T);
+  if (s != SAGE_OK) return s;
+  const Axes axes{pos, pos_bits, static_cast<int32_t>(naxes), axis_stride, axis_of};
+  return rope(q, k, q_out, k_out, dtype, T, Hq, Hkv, D, q_strides, k_strides, qo_strides,
+              ko_strides, axes, inv_freq, R, interleaved, mscale, inverse, stream);
+}
+
+sage_status sage_kv_append(const sage_paged_cache* cache, const sage_paged_batch* batch,
+                           const void* k, const void* v, const void* q, void* q_out, int dtype,
+                           int64_t Hq, const int64_t* k_strides, const int64_t* v_strides,
+                           const int64_t* q_strides, const int64_t* qo_strides,
+                           const double* inv_freq, int64_t R, int interleaved, float mscale,
+                           void* ws, size_t ws_bytes, sage_stream_t stream) {
+  return append(cache, batch, k, v, q, q_out, dtype, Hq, k_strides, v_strides, q_strides,
+                qo_strides, Axes{}, inv_freq, R, interleaved, mscale, ws, ws_bytes, stream);
+}
+
+sage_status sage_kv_append_axes(const sage_paged_cache* cache, const sage_paged_batch* batch,
+                                const void* k, const void* v, const void* q, void* q_out,
+                                int dtype, int64_t Hq, const int64_t* k_strides,
+                                const int64_t* v_strides, const int64_t* q_strides,
+                                const int64_t* qo_strides, const void* pos, int pos_bits,
+                                int64_t naxes, int64_t axis_stride, const uint8_t* axis_of,
+                                const double* inv_freq, int64_t R, int interleaved, float mscale,
+                                void* ws, size_t ws_bytes, sage_stream_t stream) {
+  if (batch == nullptr) return refuse(SAGE_ERR_INVALID_ARG, "cache and batch must not be null");
+  sage_status s = check_axes(naxes, axis_stride, batch->total_q);
+  if (s == SAGE_OK) s = check_positions(pos, pos_bits);
+  if (s != SAGE_OK) return s;
+  if (inv_freq == nullptr)
+    return refuse(SAGE_ERR_INVALID_ARG, "positions are given without inv_freq");
+  const Axes axes{pos, pos_bits, static_cast<int32_t>(naxes), axis_stride, axis_of};
+  return append(cache, batch, k, v, q, q_out, dtype, Hq, k_strides, v_strides, q_strides,
+                qo_strides, axes, inv_freq, R, interleaved, mscale, ws, ws_bytes, stream);
+}
+
+sage_status sage_kv_gather(const sage_paged_cache* cache, const sage_paged_batch* batch, void* k,
+                           void* v, int dtype, const int64_t* k_strides, const int64_t* v_strides,
+                           void* ws, size_t ws_bytes, sage_stream_t stream) {
+  sage_status s = check_dtype(dtype);
+  if (s != SAGE_OK) return s;
+  RowsParams p{};
+  if ((s = paged_geo(cache, batch, ws, ws_bytes, &p.c)) != SAGE_OK) return s;
+  if ((s = check_kind(cache, dtype)) != SAGE_OK) return s;
+  const int64_t T = batch->total_q, Hkv = cache->Hkv, D = cache->D;
+  if (T == 0 || batch->nseq == 0) return succeeded();
+  if (k == nullptr || v == nullptr || !on(k, 2) || !on(v, 2))
+    return refuse(SAGE_ERR_INVALID_ARG, "k and v must be 2-byte aligned device pointers");
+  if ((s = row_strides("k", k_strides, T, Hkv, D, &p.ko_tok, &p.ko_head)) != SAGE_OK) return s;
+  if ((s = row_strides("v", v_strides, T, Hkv, D, &p.qo_tok, &p.qo_head)) != SAGE_OK) return s;
+  int sms = 0;
+  if ((s = require_device(&sms)) != SAGE_OK) return s;
+  p.k_out = static_cast<uint16_t*>(k);
+  p.q_out = static_cast<uint16_t*>(v);
+  p.T = T;
+  p.Hkv = static_cast<int32_t>(Hkv);
+  p.D = static_cast<int32_t>(D);
+  p.vec = vec_rows(k, p.ko_tok, p.ko_head) && vec_rows(v, p.qo_tok, p.qo_head);
+  const cudaError_t e =
+      launch_gather(p, dtype == SAGE_BF16, sms, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? succeeded() : cuda_refused(e, "cache gather launch");
+}
+
+sage_status sage_paged_step(const sage_page_pool* pool, const sage_paged_plan* plan,
+                            const int32_t* requests, const int32_t* new_lens, void* ws,
+                            size_t ws_bytes, sage_stream_t stream) {
+  PoolParams p{};
+  if (plan == nullptr) return refuse(SAGE_ERR_INVALID_ARG, "pool and plan must not be null");
+  sage_status s = pool_params(pool, requests, plan->n, ws, ws_bytes, &p);
+  if (s != SAGE_OK) return s;
+  if (plan->rows < 0 || plan->rows > INT_MAX || plan->max_q < 0 || plan->max_kv < 0 ||
+      plan->table_width < 0 || plan->table_width > INT_MAX)
+    return refuse(SAGE_ERR_INVALID_ARG, "plan sizes (rows=%lld max_q=%d max_kv=%d table_width="
+                  "%lld) out of range", (long long)plan->rows, plan->max_q, plan->max_kv,
+                  (long long)plan->table_width);
+  if (plan->n > 1 && (plan->table_stride < plan->table_width || plan->table_stride >= kMaxStride))
+    return refuse(SAGE_ERR_INVALID_ARG, "the plan's table_stride=%lld is below its table_width="
+                  "%lld or beyond 2^39", (long long)plan->table_stride,
+                  (long long)plan->table_width);
+  if (plan->cu_q == nullptr || !on(plan->cu_q, 4) || plan->denied == nullptr ||
+      !on(plan->denied, 4) ||
+      (plan->n > 0 && (plan->kv_lens == nullptr || !on(plan->kv_lens, 4) || new_lens == nullptr ||
+                       !on(new_lens, 4))) ||
+      (plan->n > 0 && plan->table_width > 0 &&
+       (plan->block_table == nullptr || !on(plan->block_table, 4))))
+    return refuse(SAGE_ERR_INVALID_ARG, "new_lens, cu_q, kv_lens, block_table and denied must be "
+                  "4-byte aligned device pointers");
+  if (!on(plan->positions, 8) || !on(plan->slots, 8))
+    return refuse(SAGE_ERR_INVALID_ARG, "positions and slots must be 8-byte aligned");
+  int sms = 0;
+  if ((s = require_device(&sms)) != SAGE_OK) return s;
+  p.new_lens = new_lens;
+  p.cu_q = plan->cu_q;
+  p.kv_lens = plan->kv_lens;
+  p.block_table = plan->block_table;
+  p.positions = plan->positions;
+  p.slots = plan->slots;
+  p.denied = plan->denied;
+  p.rows = plan->rows;
+  p.plan_stride = plan->n > 1 ? plan->table_stride : 0;
+  p.plan_width = static_cast<int32_t>(plan->table_width);
+  p.max_q = plan->max_q;
+  p.max_kv = plan->max_kv;
+  const cudaError_t e = launch_paged_step(p, sms, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? succeeded() : cuda_refused(e, "page tables launch");
+}
+
+sage_status sage_paged_trim(const sage_page_pool* pool, const int32_t* requests,
+                            const int32_t* keep_lens, int64_t n, void* ws, size_t ws_bytes,
+                            sage_stream_t stream) {
+  PoolParams p{};
+  sage_status s = pool_params(pool, requests, n, ws, ws_bytes, &p);
+  if (s != SAGE_OK) return s;
+  if (!on(keep_lens, 4))
+    return refuse(SAGE_ERR_INVALID_ARG, "keep_lens must be a 4-byte aligned device pointer");
+  if (n == 0) return succeeded();
+  int sms = 0;
+  if ((s = require_device(&sms)) != SAGE_OK) return s;
+  p.new_lens = keep_lens;
+  const cudaError_t e = launch_paged_trim(p, sms, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? succeeded() : cuda_refused(e, "page release launch");
 }
 
 sage_status sage_attn_paged(const sage_paged_cache* cache, const sage_paged_batch* batch,
@@ -296,9 +537,7 @@ sage_status sage_attn_paged(const sage_paged_cache* cache, const sage_paged_batc
   if (s != SAGE_OK) return s;
   PagedAttnParams p{};
   if ((s = paged_geo(cache, batch, ws, ws_bytes, &p.c)) != SAGE_OK) return s;
-  if (cache->kind != SAGE_Q8 && cache->kind != dtype)
-    return refuse(SAGE_ERR_INVALID_ARG, "dtype %d differs from the cache's kind %d", dtype,
-                  cache->kind);
+  if ((s = check_kind(cache, dtype)) != SAGE_OK) return s;
   if (Hq < 1 || Hq > 65535 || Hq % cache->Hkv != 0)
     return refuse(SAGE_ERR_INVALID_ARG, "Hq=%lld must be a positive multiple of Hkv=%lld",
                   (long long)Hq, (long long)cache->Hkv);

@@ -1363,7 +1363,7 @@ size_t paged_many_bytes() { return 2 * static_cast<size_t>(kMaxManyCtas) * kMany
 // 16-bit pages are copied as boxes of whole pages or 128 slots, by tensor maps;
 // codes of 8 bits need not be.
 bool paged_many_serves(const PagedGeo& c, int group) {
-  if (group > 16384) return false;
+  if (group > 16384 || c.kind == kKindQ4) return false;
   return c.kind == kKindQ8 || page_boxes(c);
 }
 

@@ -7,6 +7,9 @@
 //   Q8         x = k - mean;  s = max|x| / 127;  code = rint(x * (127 / max|x|))
 //              V code = e4m3(v * (1 / v_scale)), saturating
 //              (each one IEEE fp32 operation, as in the quantisation prologue)
+//   Q4         x = k - mean, or v * (1 / (64 v_scale)), in groups of 32 channels:
+//              s = fp16(min(max|x| * fl(1/7), most)),  code = rint(x * (1 / s)), within
+//              -7..7; most = 9352 (K: 7 of it fit 16 bits) or 1 (V: 7 * 64 v_scale)
 //
 // The angle of a far position needs more bits than fp32 has: pos * inv_freq is
 // formed in turns as a 64-bit fixed-point fraction, F = frac(inv_freq / 2 pi)
@@ -41,6 +44,8 @@ constexpr int kRowThreads = 256;
 constexpr int kMaxToks = 8;          // tokens of one CTA
 constexpr int kMaxPairToks = 64;
 constexpr unsigned kAll = 0xFFFFFFFFu;
+constexpr float kSeventh = 1.0f / 7.0f;
+constexpr float kMostK = 9352.0f, kMostV = 1.0f;   // largest scales of a Q4 group
 
 template <bool kBF16>
 __device__ __forceinline__ void unpack8(const uint4& r, float (&x)[8]) {
@@ -72,6 +77,13 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
     }
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// The number that an e4m3 code stands for.
+__device__ __forceinline__ float e4m3_value(uint32_t code) {
+  uint32_t two;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(two) : "h"(static_cast<uint16_t>(code)));
+  return __half2float(__ushort_as_half(static_cast<uint16_t>(two)));
 }
 
 // Channels c0..c0+7 of a row (zeros from D on), element by element.
@@ -167,15 +179,24 @@ __device__ __forceinline__ void place_tokens(const RowsParams& p, int64_t t0, in
   }
 }
 
-// cos and sin of the CTA's tokens, times the gain, 64 apart per token.
-__device__ __forceinline__ void turn_table(const RowsParams& p, int nt, const int64_t* pos_s,
-                                           float2* cs) {
+// cos and sin of the CTA's tokens, times the gain, 64 apart per token.  Rotations of
+// several axes take a pair's position from the axis that it follows.
+__device__ __forceinline__ void turn_table(const RowsParams& p, int64_t t0, int nt,
+                                           const int64_t* pos_s, float2* cs) {
   const int half = p.R / 2;
   for (int i = threadIdx.x; i < nt * half; i += kRowThreads) {
     const int t = i / half, f = i - t * half;
+    int64_t pos;
+    if (p.naxes > 0) {
+      const int axis = p.axis_of != nullptr ? min(static_cast<int>(p.axis_of[f]), p.naxes - 1) : 0;
+      const int64_t at = axis * p.axis_stride + t0 + t;
+      pos = p.pos64 ? static_cast<const int64_t*>(p.pos)[at] : static_cast<const int32_t*>(p.pos)[at];
+    } else {
+      pos = pos_s[t];
+    }
     const double turns = p.inv_freq[f] * 0.15915494309189533577;     // 1 / (2 pi)
     const uint64_t frac = __double2ull_rn((turns - floor(turns)) * 18446744073709551616.0);
-    const uint64_t a = frac * static_cast<uint64_t>(pos_s[t]) + (1ull << 31);
+    const uint64_t a = frac * static_cast<uint64_t>(pos) + (1ull << 31);
     float sn, cn;
     sincospif(static_cast<float>(static_cast<int32_t>(a >> 32)) * 4.656612873077392578125e-10f,
               &sn, &cn);                                             // 2^-31
@@ -183,7 +204,22 @@ __device__ __forceinline__ void turn_table(const RowsParams& p, int nt, const in
   }
 }
 
-// kMode: 0 rope, 1 append 16-bit, 2 append Q8.  kLanes: lanes of a row.
+// Q4: the group's scale from its largest, and the codes of eight channels plus 8, in
+// nibbles.
+__device__ __forceinline__ __half group_scale(float top, float most) {
+  return __float2half_rn(fminf(__fmul_rn(top, kSeventh), most));
+}
+__device__ __forceinline__ uint32_t pack_nibbles(const float (&x)[8], float inv) {
+  uint32_t w = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float n = fminf(fmaxf(rintf(__fmul_rn(x[e], inv)), -7.0f), 7.0f);
+    w |= static_cast<uint32_t>(static_cast<int>(n) + 8) << (4 * e);
+  }
+  return w;
+}
+
+// kMode: 0 rope, 1 append 16-bit, 2 append Q8, 3 append Q4.  kLanes: lanes of a row.
 // kShfl: the half layout's partner vector is another lane's whole vector.
 template <int kMode, bool kBF16, int kLanes, bool kShfl>
 __global__ void __launch_bounds__(kRowThreads, kMode == 0 ? 5 : 3)
@@ -198,16 +234,15 @@ rows_kernel(const RowsParams p) {
   const PagedGeo& c = p.c;
 
   if constexpr (kMode == 0) {
-    if (threadIdx.x < nt) {
+    if (threadIdx.x < nt && p.naxes == 0) {
       pos_s[threadIdx.x] = p.pos64 ? static_cast<const int64_t*>(p.pos)[t0 + threadIdx.x]
                                    : static_cast<const int32_t*>(p.pos)[t0 + threadIdx.x];
-      page_s[threadIdx.x] = 0;
     }
   } else {
     place_tokens(p, t0, nt, pos_s, page_s, slot_s, scale_s);
   }
   __syncthreads();
-  if (p.inv_freq != nullptr) turn_table(p, nt, pos_s, cs);
+  if (p.inv_freq != nullptr) turn_table(p, t0, nt, pos_s, cs);
   __syncthreads();
 
   const int nq = p.Hq;
@@ -229,8 +264,8 @@ rows_kernel(const RowsParams p) {
                           : what == 1 ? p.k + h * p.k_head : p.v + h * p.v_head;
     const int64_t tok_stride = what == 0 ? p.q_tok : what == 1 ? p.k_tok : p.v_tok;
     const bool turn = p.inv_freq != nullptr && what != 2;
-    float chan[8];                          // Q8: k mean, or 1 / v scale
-    if constexpr (kMode == 2) {
+    float chan[8];                          // codes: k mean, or the values' factor
+    if constexpr (kMode >= 2) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) chan[e] = 0.0f;
       if (has && what != 0) {
@@ -238,7 +273,9 @@ rows_kernel(const RowsParams p) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           chan[e] = src4[e];
-          if (what == 2) chan[e] = chan[e] > 0.0f ? __fdiv_rn(1.0f, chan[e]) : 0.0f;
+          if (what == 2)
+            chan[e] = chan[e] > 0.0f ? __fdiv_rn(1.0f, kMode == 3 ? 64.0f * chan[e] : chan[e])
+                                     : 0.0f;
         }
       }
     }
@@ -307,7 +344,29 @@ rows_kernel(const RowsParams p) {
           const int page = page_s[t];
           const int64_t at = slot_s[t] + h * c.head_stride + c0;
           const bool put = has && what != 0 && page >= 0;
-          if constexpr (kMode == 1) {
+          if constexpr (kMode == 3) {
+            float top = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              x[e] = what == 1 ? __fsub_rn(x[e], chan[e]) : __fmul_rn(x[e], chan[e]);
+              top = fmaxf(top, fabsf(x[e]));
+            }
+            // four lanes are a group
+            top = fmaxf(top, __shfl_xor_sync(kAll, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(kAll, top, 2));
+            if (r < rows && what != 0 && page >= 0) {
+              const __half scale = group_scale(top, what == 1 ? kMostK : kMostV);
+              const float s = __half2float(scale);
+              const float inv = s > 0.0f ? __fdiv_rn(1.0f, s) : 0.0f;
+              if (c0 < 32 * ((p.D + 31) / 32))
+                *reinterpret_cast<uint32_t*>((what == 1 ? c.k : c.v) + slot_s[t] +
+                                             h * c.head_stride + c0 / 2) = pack_nibbles(x, inv);
+              if (sub % 4 == 0)
+                reinterpret_cast<__half*>(what == 1 ? c.k_groups : c.v_groups)
+                    [(scale_s[t] + static_cast<int64_t>(h) * c.page_size) * (c.Dp / 32) + sub / 4] =
+                        scale;
+            }
+          } else if constexpr (kMode == 1) {
             if (put) {
               uint16_t* base = reinterpret_cast<uint16_t*>(what == 1 ? c.k : c.v);
               *reinterpret_cast<uint4*>(base + at) = turn ? pack8<kBF16>(x) : raw[u];
@@ -562,7 +621,7 @@ pair_rows_kernel(const RowsParams p) {
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * p.toks;
   const int nt = static_cast<int>(min(static_cast<int64_t>(p.toks), p.T - t0));
   if constexpr (kMode == 0) {
-    if (threadIdx.x < nt)
+    if (threadIdx.x < nt && p.naxes == 0)
       tk.pos[threadIdx.x] = p.pos64 ? static_cast<const int64_t*>(p.pos)[t0 + threadIdx.x]
                                     : static_cast<const int32_t*>(p.pos)[t0 + threadIdx.x];
   } else {
@@ -570,7 +629,7 @@ pair_rows_kernel(const RowsParams p) {
   }
   __syncthreads();
   if (p.inv_freq != nullptr) {
-    turn_table(p, nt, tk.pos, cs);
+    turn_table(p, t0, nt, tk.pos, cs);
     __syncthreads();
   }
   if (p.Hq > 0) pair_pass<kMode, 0, kBF16>(p, tk, cs, t0, nt);
@@ -621,9 +680,126 @@ cudaError_t launch_mode(const RowsParams& p0, bool bf16, int sms, cudaStream_t s
               : launch_lanes<kMode, false, 16>(p, shfl, grid, st);
 }
 
+// ---- Reading back: thread = 8 channels of a head's keys or values, for several of
+// the CTA's tokens, so that a quantised cache's means and scales stay in registers.
+constexpr int kGatherToks = 32;
+
+template <int kKind, bool kBF16>
+__global__ void __launch_bounds__(kRowThreads)
+gather_kernel(const RowsParams p) {
+  __shared__ int64_t pos_s[kGatherToks], slot_s[kGatherToks], scale_s[kGatherToks];
+  __shared__ int page_s[kGatherToks];
+  const PagedGeo& c = p.c;
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * p.toks;
+  const int nt = static_cast<int>(min(static_cast<int64_t>(p.toks), p.T - t0));
+  const int64_t tokens = c.cu_q[c.nseq];                // rows behind stay as they are
+  place_tokens(p, t0, nt, pos_s, page_s, slot_s, scale_s);
+  __syncthreads();
+  const int vecs = p.D / 8, units = 2 * p.Hkv * vecs;
+  const int at_once = min(units, kRowThreads), step = kRowThreads / at_once;
+  const int t_first = threadIdx.x / at_once;
+  if (t_first >= step) return;
+  for (int u = blockIdx.y * at_once + threadIdx.x % at_once; u < units;
+       u += at_once * gridDim.y) {
+    const int h2 = u / vecs, c0 = 8 * (u - h2 * vecs);
+    const bool val = h2 >= p.Hkv;
+    const int h = val ? h2 - p.Hkv : h2;
+    float chan[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) chan[e] = 0.0f;
+    if constexpr (kKind == kKindQ8 || kKind == kKindQ4) {
+      const float4* src = reinterpret_cast<const float4*>((val ? c.v_scale : c.k_mean) + h * c.Dp + c0);
+      const float4 a = src[0], b = src[1];
+      const float unit = kKind == kKindQ4 && val ? 64.0f : 1.0f;
+      chan[0] = a.x * unit; chan[1] = a.y * unit; chan[2] = a.z * unit; chan[3] = a.w * unit;
+      chan[4] = b.x * unit; chan[5] = b.y * unit; chan[6] = b.z * unit; chan[7] = b.w * unit;
+    }
+    const uint8_t* const codes = val ? c.v : c.k;
+    uint16_t* const out = (val ? p.q_out : p.k_out) + h * (val ? p.qo_head : p.ko_head);
+    const int64_t out_tok = val ? p.qo_tok : p.ko_tok;
+    constexpr int kUnroll = 4;
+    for (int tb = t_first; tb < nt; tb += kUnroll * step) {
+      uint4 raw[kUnroll];
+      float scale[kUnroll];
+#pragma unroll
+      for (int k = 0; k < kUnroll; ++k) {
+        const int t = tb + k * step;
+        raw[k] = make_uint4(0, 0, 0, 0);
+        scale[k] = 0.0f;
+        if (t >= nt || page_s[t] < 0) continue;
+        const int64_t at = slot_s[t] + h * c.head_stride;
+        const int64_t sc = scale_s[t] + static_cast<int64_t>(h) * c.page_size;
+        if constexpr (kKind == kKindQ4) {
+          raw[k].x = *reinterpret_cast<const uint32_t*>(codes + at + c0 / 2);
+          scale[k] = __half2float(reinterpret_cast<const __half*>(
+              val ? c.v_groups : c.k_groups)[sc * (c.Dp / 32) + c0 / 32]);
+        } else if constexpr (kKind == kKindQ8) {
+          const uint2 w = *reinterpret_cast<const uint2*>(codes + at + c0);
+          raw[k].x = w.x;
+          raw[k].y = w.y;
+          scale[k] = val ? 1.0f : c.k_scale[sc];
+        } else {
+          raw[k] = *reinterpret_cast<const uint4*>(codes + 2 * (at + c0));
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kUnroll; ++k) {
+        const int t = tb + k * step;
+        if (t >= nt || t0 + t >= tokens) continue;
+        uint4 put = raw[k];
+        if constexpr (kKind == kKindQ8 || kKind == kKindQ4) {
+          float x[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            float n;
+            if constexpr (kKind == kKindQ4) {
+              n = static_cast<float>(static_cast<int>((raw[k].x >> (4 * e)) & 15u) - 8);
+            } else {
+              const uint32_t b = ((e < 4 ? raw[k].x : raw[k].y) >> (8 * (e & 3))) & 0xFFu;
+              n = val ? e4m3_value(b) : static_cast<float>(static_cast<int8_t>(b));
+            }
+            // one rounding each
+            const float y = __fmul_rn(n, scale[k]);
+            x[e] = val ? __fmul_rn(y, chan[e]) : __fadd_rn(y, chan[e]);
+          }
+          put = page_s[t] < 0 ? make_uint4(0, 0, 0, 0) : pack8<kBF16>(x);
+        }
+        store8(out + (t0 + t) * out_tok, c0, p.D, p.vec, put);
+      }
+    }
+  }
+}
+
+template <int kKind, bool kBF16>
+cudaError_t launch_gather_kind(const RowsParams& p0, int sms, cudaStream_t st) {
+  RowsParams p = p0;
+  const int units = 2 * p.Hkv * (p.D / 8);
+  p.toks = 1;
+  while (p.toks < kGatherToks && p.T / (2 * p.toks) >= 4 * sms) p.toks *= 2;
+  const int64_t ctas = (p.T + p.toks - 1) / p.toks;
+  if (ctas > 0x7FFFFFFF) return cudaErrorInvalidValue;
+  int64_t y = (units + kRowThreads - 1) / kRowThreads;
+  if (ctas * y > 4 * sms) y = 4 * sms / ctas > 1 ? 4 * sms / ctas : 1;
+  gather_kernel<kKind, kBF16><<<dim3(static_cast<unsigned>(ctas), static_cast<unsigned>(y)),
+                                kRowThreads, 0, st>>>(p);
+  note_launch();
+  return cudaGetLastError();
+}
+
 }  // namespace
 
+cudaError_t launch_gather(const RowsParams& p, bool bf16, int sms, cudaStream_t st) {
+  if (p.c.kind == kKindQ4)
+    return bf16 ? launch_gather_kind<kKindQ4, true>(p, sms, st)
+                : launch_gather_kind<kKindQ4, false>(p, sms, st);
+  if (p.c.kind == kKindQ8)
+    return bf16 ? launch_gather_kind<kKindQ8, true>(p, sms, st)
+                : launch_gather_kind<kKindQ8, false>(p, sms, st);
+  return launch_gather_kind<kKindF16, false>(p, sms, st);   // bits as they are, either type
+}
+
 cudaError_t launch_rows(const RowsParams& p, int mode, bool bf16, int sms, cudaStream_t st) {
+  if (mode == 3) return launch_mode<3>(p, bf16, sms, st);
   // Two vectors a lane from 4 tokens per SM on, for whole vectors.  Measured, two
   // vectors against one (us; one call in a graph, L2 flushed):
   //   rope, half layout, 16000 tokens x (40 + 40) heads of 128      132   192

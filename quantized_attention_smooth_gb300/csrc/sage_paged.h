@@ -9,12 +9,15 @@
 
 namespace sage {
 
-constexpr int kKindF16 = 0, kKindBF16 = 1, kKindQ8 = 2;   // as in sage.h
+constexpr int kKindF16 = 0, kKindBF16 = 1, kKindQ8 = 2,   // as in sage.h
+              kKindQ4 = 3;
 
 struct PagedGeo {
-  uint8_t* k;                // pages; elements of 2 bytes, or 1 (kKindQ8)
+  uint8_t* k;                // pages; elements of 2 bytes, or 1 (kKindQ8; kKindQ4: two codes)
   uint8_t* v;
-  float* k_scale;            // [num_pages][Hkv][page_size]
+  float* k_scale;            // [num_pages][Hkv][page_size], kKindQ8
+  uint16_t* k_groups;        // [num_pages][Hkv][page_size][Dp/32] fp16, kKindQ4
+  uint16_t* v_groups;
   const float* k_mean;       // [Hkv][Dp]
   const float* v_scale;      // [Hkv][Dp]
   int64_t num_pages;
@@ -40,8 +43,11 @@ struct RowsParams {
   int64_t q_tok, q_head, k_tok, k_head, v_tok, v_head, qo_tok, qo_head, ko_tok, ko_head;
   int64_t T;
   int32_t Hq, Hkv, D;        // Hq = 0: no q rows
-  const void* pos;           // sage_rope only
+  const void* pos;           // sage_rope, and rotations at given positions
   int32_t pos64;
+  int32_t naxes;             // 0: one position a token, of pos (sage_rope) or the cache's place
+  int64_t axis_stride;       // elements between the axes' positions
+  const uint8_t* axis_of;    // each pair's axis; NULL: the first
   const double* inv_freq;    // NULL: no rotation
   int32_t R, interleaved;
   float mscale, sign;        // sign -1: the inverse rotation
@@ -50,8 +56,38 @@ struct RowsParams {
   PagedGeo c;                // sage_kv_append only
 };
 
-// mode 0: sage_rope; 1: append to a 16-bit cache; 2: append to a Q8 cache.
+// mode 0: sage_rope; 1: append to a 16-bit cache; 2, 3: append to a Q8 or Q4 cache.
 cudaError_t launch_rows(const RowsParams& p, int mode, bool bf16, int sms, cudaStream_t st);
+
+// sage_kv_gather: k_out and v_out with their strides in k and v's fields of RowsParams.
+cudaError_t launch_gather(const RowsParams& p, bool bf16, int sms, cudaStream_t st);
+
+// A pool's tables and a step's (sage_paged_step, sage_paged_trim).
+struct PoolParams {
+  int32_t* free_pages;
+  int32_t* left;
+  int32_t* table;
+  int32_t* lens;
+  uint32_t* marks;
+  int64_t table_stride, width;         // of the pool's table
+  int32_t num_pages, page_size, max_requests, n;
+  int32_t page_shift;                  // log2(page_size), or -1
+  const int32_t* requests;
+  const int32_t* new_lens;             // trim: lengths to keep, or NULL
+  int32_t* cu_q;                       // step only, down to max_kv
+  int32_t* kv_lens;
+  int32_t* block_table;
+  int64_t* positions;
+  int64_t* slots;
+  int32_t* denied;
+  int64_t rows, plan_stride;
+  int32_t plan_width, max_q, max_kv;
+  int4* seqs;                          // workspace: one per sequence
+  uint32_t* status;
+};
+constexpr int kMaxStepSeqs = 65536;
+cudaError_t launch_paged_step(const PoolParams& p, int sms, cudaStream_t st);
+cudaError_t launch_paged_trim(const PoolParams& p, int sms, cudaStream_t st);
 
 constexpr int kArrivalBytes = 8192 - 256;
 
@@ -75,6 +111,7 @@ struct PagedAttnParams {
 };
 
 cudaError_t launch_paged_few(const PagedAttnParams& p, bool bf16, int sms, cudaStream_t st);
+cudaError_t launch_paged_few_q4(const PagedAttnParams& p, bool bf16, int sms, cudaStream_t st);
 size_t paged_few_bytes();
 int paged_few_rows(int Dp);   // rows (new tokens x group) that one of its tiles holds
 cudaError_t launch_paged_many(const PagedAttnParams& p, bool bf16, int sms, cudaStream_t st);

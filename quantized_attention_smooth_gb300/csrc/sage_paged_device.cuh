@@ -72,6 +72,22 @@ __device__ __forceinline__ void int8_to_half(uint32_t w, uint32_t& lo, uint32_t&
   hi = *reinterpret_cast<uint32_t*>(&b);
 }
 
+// Eight codes u of four bits as numbers u - 8, exactly: pairs of nibbles j and j + 4.
+// Under 0x64 a nibble is the fp16 number 1024 + u, four bits higher 1024 + 16 u.
+__device__ __forceinline__ void nibbles_to_half(uint32_t w, uint32_t (&h)[4]) {
+  const __half2 bias = __floats2half2_rn(-1032.0f, -1032.0f);
+  const __half2 part = __floats2half2_rn(0.0625f, 0.0625f), bias16 = __floats2half2_rn(-72.0f, -72.0f);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t v = i == 0 ? w : w >> 8;
+    const uint32_t lo = (v & 0x000F000Fu) | 0x64006400u, hi = (v & 0x00F000F0u) | 0x64006400u;
+    const __half2 a = __hadd2(*reinterpret_cast<const __half2*>(&lo), bias);
+    const __half2 b = __hfma2(*reinterpret_cast<const __half2*>(&hi), part, bias16);
+    h[2 * i] = *reinterpret_cast<const uint32_t*>(&a);
+    h[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&b);
+  }
+}
+
 __device__ __forceinline__ uint32_t e4m3x2_to_half2(uint32_t two) {
   uint32_t r;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(two)));
@@ -87,6 +103,16 @@ __device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src, int byt
 __device__ __forceinline__ void copy8(uint32_t dst, const uint8_t* src, int bytes) {
   asm volatile("cp.async.ca.shared.global.L2::128B [%0], [%1], 8, %2;"
                :: "r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+template <int kBytes>
+__device__ __forceinline__ void copy_small(uint32_t dst, const uint8_t* src, int bytes) {
+  static_assert(kBytes == 4 || kBytes == 8, "");
+  if constexpr (kBytes == 8)
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;"
+                 :: "r"(dst), "l"(src), "r"(bytes) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;"
+                 :: "r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 // A vector of a row that ends after `left` more elements (untouched where none
 // are left), zero unless `see`.  kForm 0: all are there; 2: rows of 8-bit codes

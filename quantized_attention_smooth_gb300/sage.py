@@ -12,7 +12,7 @@ import os
 
 from . import _build
 
-F16, BF16, Q8 = 0, 1, 2
+F16, BF16, Q8, Q4 = 0, 1, 2, 3
 HND, NHD = 0, 1
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_WORKSPACE, ERR_CUDA, ERR_DEVICE_TIMEOUT = range(6)
 STATUS_NAMES = ["OK", "INVALID_ARG", "UNSUPPORTED", "WORKSPACE", "CUDA", "DEVICE_TIMEOUT"]
@@ -31,6 +31,8 @@ EXPORTS = (
     "sage_debug_tc_rate", "sage_workspace_bytes_varlen_host", "sage_attn_fwd_varlen_host",
     "sage_debug_set_host_fail_chunk",
     "sage_rope", "sage_workspace_bytes_paged", "sage_kv_append", "sage_attn_paged",
+    "sage_rope_axes", "sage_kv_append_axes", "sage_kv_gather", "sage_paged_step",
+    "sage_paged_trim",
 )
 
 
@@ -68,6 +70,7 @@ class _CacheC(ctypes.Structure):
         ("num_pages", ctypes.c_int64), ("page_size", ctypes.c_int64), ("Hkv", ctypes.c_int64),
         ("D", ctypes.c_int64), ("page_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
         ("head_stride", ctypes.c_int64), ("kind", ctypes.c_int32),
+        ("k_groups", ctypes.c_void_p), ("v_groups", ctypes.c_void_p),
     ]
 
 
@@ -76,6 +79,26 @@ class _BatchC(ctypes.Structure):
     _fields_ = [
         ("cu_q", ctypes.c_void_p), ("kv_lens", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
         ("nseq", ctypes.c_int64), ("total_q", ctypes.c_int64), ("table_stride", ctypes.c_int64),
+        ("table_width", ctypes.c_int64), ("max_q", ctypes.c_int32), ("max_kv", ctypes.c_int32),
+    ]
+
+
+class _PoolC(ctypes.Structure):
+    """Mirror of sage_page_pool."""
+    _fields_ = [
+        ("free_pages", ctypes.c_void_p), ("left", ctypes.c_void_p), ("table", ctypes.c_void_p),
+        ("lens", ctypes.c_void_p), ("marks", ctypes.c_void_p), ("num_pages", ctypes.c_int64),
+        ("page_size", ctypes.c_int64), ("max_requests", ctypes.c_int64),
+        ("table_stride", ctypes.c_int64), ("table_width", ctypes.c_int64),
+    ]
+
+
+class _PlanC(ctypes.Structure):
+    """Mirror of sage_paged_plan."""
+    _fields_ = [
+        ("cu_q", ctypes.c_void_p), ("kv_lens", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
+        ("positions", ctypes.c_void_p), ("slots", ctypes.c_void_p), ("denied", ctypes.c_void_p),
+        ("n", ctypes.c_int64), ("rows", ctypes.c_int64), ("table_stride", ctypes.c_int64),
         ("table_width", ctypes.c_int64), ("max_q", ctypes.c_int32), ("max_kv", ctypes.c_int32),
     ]
 
@@ -131,6 +154,13 @@ def _load():
         "sage_workspace_bytes_paged": ([], SZ),
         "sage_kv_append": ([P, P, P, P, P, P, I, I64, P, P, P, P, P, I64, I, F, P, SZ, P], I),
         "sage_attn_paged": ([P, P, P, P, P, I, I64, P, I64, I64, F, P, SZ, P], I),
+        "sage_rope_axes": ([P, P, P, P, I, I64, I64, I64, I64, P, P, P, P, P, I, I64, I64, P, P,
+                            I64, I, F, I, P], I),
+        "sage_kv_append_axes": ([P, P, P, P, P, P, I, I64, P, P, P, P, P, I, I64, I64, P, P, I64,
+                                 I, F, P, SZ, P], I),
+        "sage_kv_gather": ([P, P, P, P, I, P, P, P, SZ, P], I),
+        "sage_paged_step": ([P, P, P, P, P, SZ, P], I),
+        "sage_paged_trim": ([P, P, P, I64, P, SZ, P], I),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -593,19 +623,65 @@ def _result(where, name, out, t, stream, dev, dense):
     return out, st
 
 
+def rope_axes(sections, in_turn=False, device="cuda"):
+    """The axis that each channel pair follows, for `rope` and `kv_append`: uint8
+    [sum(sections)] on `device`, sections[a] pairs of axis a: one section after
+    the other, or with `in_turn` axis 0, 1, 2, 0, 1, 2, ... while an axis has pairs
+    left.  Frequencies go by the pair (`rope_freqs`), or by the axis if the
+    caller puts those of each axis where its pairs are."""
+    import torch
+    sections = [int(x) for x in sections]
+    if not 1 <= len(sections) <= 8 or min(sections) < 0 or not 1 <= sum(sections) <= 64:
+        raise ValueError(f"rope_axes: 1 to 8 sections of 1 to 64 pairs in all, got {sections}")
+    order = [a for a, x in enumerate(sections) for _ in range(x)]
+    if in_turn:
+        nth = [i for x in sections for i in range(x)]
+        order = [a for _, a in sorted(zip(nth, order))]
+    return torch.tensor(order, dtype=torch.uint8, device=device)
+
+
+def _axes(where, positions, axes, T, R, dev):
+    """Checks positions (A, T) and axes; the arguments that the library takes."""
+    shape = positions.shape
+    bits = 64 if positions.dtype == _torch.int64 else 32
+    if bits == 32 and positions.dtype != _torch.int32 or not 1 <= len(shape) <= 2 or \
+            shape[-1] != T or len(shape) == 2 and not 1 <= shape[0] <= 8 or \
+            T > 1 and positions.stride(-1) != 1:
+        raise ValueError(f"{where}: positions must be int64 or int32, (axes, {T}) with contiguous "
+                         f"rows and 1 to 8 axes, got {positions.dtype} {tuple(shape)}")
+    if positions.get_device() != dev:
+        _off_device(where, "positions", positions, dev)
+    ap = 0
+    if axes is not None:
+        if axes.dtype != _torch.uint8 or axes.shape != (R // 2,) or not axes.is_contiguous():
+            raise ValueError(f"{where}: axes must be a contiguous uint8 tensor of {R // 2} entries")
+        if axes.get_device() != dev:
+            _off_device(where, "axes", axes, dev)
+        ap = axes.data_ptr()
+    if len(shape) == 1:
+        return positions.data_ptr(), bits, 1, T, ap
+    return positions.data_ptr(), bits, shape[0], positions.stride(0) if shape[0] > 1 else T, ap
+
+
 def rope(q, k, positions, inv_freq, interleaved=False, mscale=1.0, inverse=False, q_out=None,
-         k_out=None, stream=None):
+         k_out=None, stream=None, axes=None):
     """Rotary positions of q (T, Hq, D) and k (T, Hkv, D), fp16/bf16 views with
     contiguous channels; k may be None.  positions: int64 or int32 (T,);
     inv_freq: float64 (R/2,), R <= D (see rope_freqs).  Pairs are (i, i + R/2),
     or (2i, 2i + 1) with `interleaved`.  q_out=q (k_out=k) turns in place.
     `inverse` turns back; applied to the outputs' gradients with the same
-    mscale it gives the inputs' gradients.  Returns (q_out, k_out)."""
+    mscale it gives the inputs' gradients.  With `axes` (uint8 (R/2,), see
+    rope_axes) positions are (A, T), a row for each of up to 8 axes, and pair i
+    turns by its axis' position.  Returns (q_out, k_out)."""
     dev, current = _device("rope", "q", q)
     (T, Hq, D), qs = _rows3("rope", "q", q, dev)
     dtype = _code16("rope", "q", q)
+    many = None
     bits = 64 if positions.dtype == _torch.int64 else 32
-    if bits == 32 and positions.dtype != _torch.int32 or positions.shape != (T,) or \
+    if axes is not None:
+        _freqs("rope", inv_freq, dev)
+        many = _axes("rope", positions, axes, T, 2 * inv_freq.shape[0], dev)
+    elif bits == 32 and positions.dtype != _torch.int32 or positions.shape != (T,) or \
             not positions.is_contiguous():
         raise ValueError("rope: positions must be a contiguous int64 or int32 tensor of T entries")
     if positions.get_device() != dev:
@@ -630,6 +706,15 @@ def rope(q, k, positions, inv_freq, interleaved=False, mscale=1.0, inverse=False
         else:
             k_out, kos = _result("rope", "k_out", k_out, k, stream, dev, ks is None)
         kp, kop = k.data_ptr(), k_out.data_ptr()
+    if many is not None:
+        pp, bits, naxes, step, ap = many
+        rc = _lib.sage_rope_axes(q.data_ptr(), kp, q_out.data_ptr(), kop, dtype, T, Hq, Hkv, D, qs,
+                                 ks, qos, kos, pp, bits, naxes, step, ap, inv_freq.data_ptr(),
+                                 2 * inv_freq.shape[0], 1 if interleaved else 0, mscale,
+                                 1 if inverse else 0, _handle(stream, current))
+        if rc:
+            _check(rc, "sage_rope_axes")
+        return q_out, k_out
     rc = _lib.sage_rope(q.data_ptr(), kp, q_out.data_ptr(), kop, dtype, T, Hq, Hkv, D, qs, ks, qos,
                         kos, positions.data_ptr(), bits, inv_freq.data_ptr(),
                         2 * inv_freq.shape[0], 1 if interleaved else 0, mscale,
@@ -646,21 +731,33 @@ class PagedCache:
     as they are; an int8 k with a float8_e4m3fn v holds them quantised, with
     k_scale float32 (pages, Hkv, slots) and the fixed k_mean and v_scale
     float32 (Hkv, Dp), Dp = 64 if D <= 64 else 128 (kv_stats_noalloc writes
-    them from a sample of keys and values)."""
+    them from a sample of keys and values).  uint8 tensors with head_dim = D hold
+    four bits a channel: rows of 16 * ceil(D / 32) bytes in the place of D, the
+    same k_mean and v_scale, and k_groups and v_groups float16 (pages, Hkv, slots,
+    Dp / 32), a scale for each token, head and 32 channels (SAGE_Q4 in sage.h)."""
 
-    def __init__(self, k, v, layout="NHD", k_scale=None, k_mean=None, v_scale=None):
+    def __init__(self, k, v, layout="NHD", k_scale=None, k_mean=None, v_scale=None, k_groups=None,
+                 v_groups=None, head_dim=None):
         import torch
         lay = _layout_code(layout)
         if k.dim() != 4 or tuple(v.shape) != tuple(k.shape):
             raise ValueError(f"PagedCache: k {tuple(k.shape)} and v {tuple(v.shape)} must be 4-D "
                              "tensors of one shape")
-        q8 = k.dtype == torch.int8
-        if q8 and v.dtype != torch.float8_e4m3fn or not q8 and (
-                k.dtype not in (torch.float16, torch.bfloat16) or v.dtype != k.dtype):
+        q8, q4 = k.dtype == torch.int8, k.dtype == torch.uint8
+        if q8 and v.dtype != torch.float8_e4m3fn or q4 and v.dtype != torch.uint8 or \
+                not (q8 or q4) and (k.dtype not in (torch.float16, torch.bfloat16) or
+                                    v.dtype != k.dtype):
             raise TypeError(f"PagedCache: k {k.dtype} and v {v.dtype} must be both float16, both "
-                            "bfloat16, or int8 and float8_e4m3fn")
-        self.kind, self._dev = Q8 if q8 else F16 if k.dtype == torch.float16 else BF16, k.get_device()
-        pages, self.D = k.shape[0], k.shape[3]
+                            "bfloat16, int8 and float8_e4m3fn, or both uint8 (two codes a byte)")
+        self.kind = Q4 if q4 else Q8 if q8 else F16 if k.dtype == torch.float16 else BF16
+        self._dev = k.get_device()
+        pages, width = k.shape[0], k.shape[3]
+        self.D = width if head_dim is None else int(head_dim)
+        if q4 and (head_dim is None or width != 16 * -(-self.D // 32)):
+            raise ValueError("PagedCache: a 4-bit cache needs head_dim, and rows of "
+                             f"16 * ceil(head_dim / 32) bytes, got {width} for {head_dim}")
+        if not q4 and self.D != width:
+            raise ValueError(f"PagedCache: head_dim is {head_dim}, the rows have {width} channels")
         slots, self.Hkv = (k.shape[2], k.shape[1]) if lay == HND else (k.shape[1], k.shape[2])
         st, page_dims = k.stride(), (2, 1) if lay == HND else (1, 2)
         for name, t in (("k", k), ("v", v)):
@@ -668,25 +765,31 @@ class PagedCache:
             if any(n > 1 and a != b for n, a, b in zip(k.shape, t.stride(), st)):
                 raise ValueError(f"PagedCache: k and v must share their strides ({k.stride()} and "
                                  f"{v.stride()})")
-        if st[3] != 1 and self.D > 1:
+        if st[3] != 1 and width > 1:
             raise ValueError("PagedCache: the channels must be contiguous")
-        scales = (("k_scale", k_scale, (pages, self.Hkv, slots)),
-                  ("k_mean", k_mean, (self.Hkv, 64 if self.D <= 64 else 128)),
-                  ("v_scale", v_scale, (self.Hkv, 64 if self.D <= 64 else 128)))
-        for name, t, shape in scales:
-            if not q8:
+        dp = 64 if self.D <= 64 else 128
+        scales = (("k_scale", k_scale, q8, torch.float32, (pages, self.Hkv, slots)),
+                  ("k_mean", k_mean, q8 or q4, torch.float32, (self.Hkv, dp)),
+                  ("v_scale", v_scale, q8 or q4, torch.float32, (self.Hkv, dp)),
+                  ("k_groups", k_groups, q4, torch.float16, (pages, self.Hkv, slots, dp // 32)),
+                  ("v_groups", v_groups, q4, torch.float16, (pages, self.Hkv, slots, dp // 32)))
+        for name, t, wanted, dtype, shape in scales:
+            if not wanted:
                 if t is not None:
-                    raise ValueError(f"PagedCache: {name} belongs to a quantised cache only")
+                    raise ValueError(f"PagedCache: {name} belongs to a quantised cache only"
+                                     if not (q8 or q4) else
+                                     f"PagedCache: {name} does not belong to this kind of cache")
                 continue
-            if t is None or t.dtype != torch.float32 or tuple(t.shape) != shape or \
-                    not t.is_contiguous():
-                raise ValueError(f"PagedCache: {name} must be a contiguous float32 tensor of shape "
-                                 f"{shape}")
+            if t is None or t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
+                raise ValueError(f"PagedCache: {name} must be a contiguous "
+                                 f"{str(dtype).replace('torch.', '')} tensor of shape {shape}")
             _on_device("PagedCache", name, t)
         self.k, self.v, self.k_scale, self.k_mean, self.v_scale = k, v, k_scale, k_mean, v_scale
+        self.k_groups, self.v_groups = k_groups, v_groups
         ptr = lambda t: 0 if t is None else t.data_ptr()
         self._c = _CacheC(ptr(k), ptr(v), ptr(k_scale), ptr(k_mean), ptr(v_scale), pages, slots,
-                          self.Hkv, self.D, st[0], st[page_dims[0]], st[page_dims[1]], self.kind)
+                          self.Hkv, self.D, st[0], st[page_dims[0]], st[page_dims[1]], self.kind,
+                          ptr(k_groups), ptr(v_groups))
         self._ref = ctypes.byref(self._c)
 
 
@@ -748,10 +851,11 @@ def alloc_workspace_paged(device="cuda", stream=None):
 
 
 def kv_append(cache, batch, k, v, q=None, q_out=None, inv_freq=None, interleaved=False, mscale=1.0,
-              ws=None, stream=None):
+              ws=None, stream=None, positions=None, axes=None):
     """Writes the batch's new k and v (T, Hkv, D) into the cache.  With
     inv_freq, k is turned at each token's position first, and q (T, Hq, D), if
-    given, into q_out (returned)."""
+    given, into q_out (returned).  The rotation's positions are the tokens' places
+    in their sequences, or `positions` (T,) or (A, T) with `axes`, as in rope."""
     dev, current = _device("kv_append", "k", k)
     if cache._dev != dev or batch._dev != dev:
         _off_cache("kv_append", cache, batch, dev)
@@ -778,12 +882,180 @@ def kv_append(cache, batch, k, v, q=None, q_out=None, inv_freq=None, interleaved
         _freqs("kv_append", inv_freq, dev)
         fp, R = inv_freq.data_ptr(), 2 * inv_freq.shape[0]
     ws = _workspace("kv_append", ws, stream, dev)
+    if positions is not None:
+        if inv_freq is None:
+            raise ValueError("kv_append: positions are given without inv_freq")
+        if axes is None and positions.dim() != 1:
+            raise ValueError("kv_append: positions of several axes need `axes`")
+        pp, bits, naxes, step, ap = _axes("kv_append", positions, axes, T, R, dev)
+        rc = _lib.sage_kv_append_axes(cache._ref, batch._rows(T), k.data_ptr(), v.data_ptr(), qp,
+                                      qop, dtype, Hq, ks, vs, qs, qos, pp, bits, naxes, step, ap,
+                                      fp, R, 1 if interleaved else 0, mscale, ws.data_ptr(),
+                                      ws.numel(), _handle(stream, current))
+        if rc:
+            _check(rc, "sage_kv_append_axes")
+        return q_out if q is not None else None
+    if axes is not None:
+        raise ValueError("kv_append: axes are given without positions")
     rc = _lib.sage_kv_append(cache._ref, batch._rows(T), k.data_ptr(), v.data_ptr(), qp, qop, dtype,
                              Hq, ks, vs, qs, qos, fp, R, 1 if interleaved else 0, mscale,
                              ws.data_ptr(), ws.numel(), _handle(stream, current))
     if rc:
         _check(rc, "sage_kv_append")
     return q_out if q is not None else None
+
+
+def kv_gather(cache, batch, rows, dtype=None, k_out=None, v_out=None, ws=None, stream=None):
+    """The batch's `rows` tokens read back from the cache: k and v (rows, Hkv, D) of
+    `dtype` (a 16-bit cache: its own), as kv_append stored them, k with its mean.
+    A batch whose new tokens are all the cached ones gives whole sequences.
+    Tokens without a place give zeros; rows behind the batch's are left as they are
+    in k_out and v_out."""
+    if _torch is None:
+        _bind_torch()
+    dev, T = _get_device(), int(rows)
+    if cache._dev != dev or batch._dev != dev:
+        _off_cache("kv_gather", cache, batch, dev)
+    own = cache.k.dtype if cache.kind in (F16, BF16) else None
+    dtype = dtype or (k_out.dtype if k_out is not None else own)
+    if dtype not in _CODES or own is not None and dtype != own:
+        raise TypeError(f"kv_gather: a cache of {cache.k.dtype} does not give {dtype}")
+    if T < 0:
+        raise ValueError(f"kv_gather: rows must not be negative, got {rows}")
+    outs, shape = [], (T, cache.Hkv, cache.D)
+    for name, t in (("k_out", k_out), ("v_out", v_out)):
+        st = None
+        if t is None:
+            t = _empty_on(stream, lambda: _torch.empty(shape, dtype=dtype, device=cache.k.device))
+        else:
+            got, st = _rows3("kv_gather", name, t, dev)
+            if got != shape or t.dtype != dtype:
+                raise ValueError(f"kv_gather: {name} must be {dtype} of shape {shape}, got {t.dtype} "
+                                 f"{tuple(got)}")
+        outs.append((t, st))
+    ws = _workspace("kv_gather", ws, stream, dev)
+    (k, ks), (v, vs) = outs
+    rc = _lib.sage_kv_gather(cache._ref, batch._rows(T), k.data_ptr(), v.data_ptr(), _CODES[dtype],
+                             ks, vs, ws.data_ptr(), ws.numel(), _handle(stream, _get_stream(dev)))
+    if rc:
+        _check(rc, "sage_kv_gather")
+    return k, v
+
+
+def _int32s(where, name, t, shape, dev=None):
+    """A contiguous int32 tensor of this shape on the (current) device."""
+    if t.dtype != _torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{where}: {name} must be a contiguous int32 tensor of shape {shape}, got "
+                         f"{t.dtype} {tuple(t.shape)}")
+    _on_device(where, name, t, dev)
+
+
+class PagePool:
+    """The pages of a cache and who holds them, in the caller's int32 CUDA tensors:
+    free (pages,), a stack of page indices whose next one is its last of left (1,)
+    pages; table (requests, width), each request's pages; lens (requests,), its
+    cached length.  `PagePool.new` makes an empty pool."""
+
+    def __init__(self, free, left, table, lens, page_size):
+        if _torch is None:
+            _bind_torch()
+        if table.dim() != 2 or table.dtype != _torch.int32 or \
+                table.shape[1] > 1 and table.stride(1) != 1:
+            raise ValueError("PagePool: table must be an int32 (requests, width) tensor with "
+                             f"contiguous rows, got {table.dtype} {tuple(table.shape)}")
+        requests, width = table.shape
+        _on_device("PagePool", "table", table)
+        self._dev = table.get_device()
+        for name, t, shape in (("free", free, (free.numel(),)), ("left", left, (1,)),
+                               ("lens", lens, (requests,))):
+            _int32s("PagePool", name, t, shape, self._dev)
+        self.free, self.left, self.table, self.lens = free, left, table, lens
+        self.page_size = int(page_size)
+        self.marks = _torch.zeros(requests, dtype=_torch.int32, device=table.device)
+        self._c = _PoolC(free.data_ptr(), left.data_ptr(), table.data_ptr(), lens.data_ptr(),
+                         self.marks.data_ptr(), free.numel(), self.page_size, requests,
+                         table.stride(0) if requests > 1 else width, width)
+        self._ref = ctypes.byref(self._c)
+
+    @classmethod
+    def new(cls, pages, page_size, requests, max_len, device="cuda"):
+        """All `pages` free (0 goes first), `requests` of up to `max_len` tokens."""
+        import torch
+        i32 = dict(dtype=torch.int32, device=device)
+        return cls(torch.arange(pages - 1, -1, -1, **i32), torch.full((1,), pages, **i32),
+                   torch.full((requests, max(1, -(-int(max_len) // int(page_size)))), -1, **i32),
+                   torch.zeros(requests, **i32), page_size)
+
+
+class PagedPlan:
+    """The buffers of a step of n sequences with `rows` packed rows in all, at most
+    max_q of one and max_kv cached tokens: cu_q, kv_lens and block_table, as the
+    PagedBatch `batch`; positions and slots (int64, rows), slots as page * page_size
+    + place in the page; denied (int32, 1), sequences that got no pages."""
+
+    def __init__(self, pool, n, rows, max_q, max_kv):
+        import torch
+        n, rows, max_kv = int(n), int(rows), int(max_kv)
+        if n < 0 or rows < 0 or max_kv < 0:
+            raise ValueError(f"PagedPlan: sizes must not be negative (n={n}, rows={rows}, "
+                             f"max_kv={max_kv})")
+        width = max(1, -(-max_kv // pool.page_size))
+        new = lambda *shape, dtype=torch.int32, fill=0: torch.full(
+            shape, fill, dtype=dtype, device=pool.table.device)
+        self.cu_q, self.kv_lens, self.denied = new(n + 1), new(n), new(1)
+        self.block_table = new(n, width, fill=-1)
+        self.positions, self.slots = (new(rows, dtype=torch.int64, fill=-1) for _ in range(2))
+        self.batch = PagedBatch(self.cu_q, self.kv_lens, self.block_table, max_q, max_kv)
+        self.n, self.rows = n, rows
+        self._c = _PlanC(self.cu_q.data_ptr(), self.kv_lens.data_ptr(), self.block_table.data_ptr(),
+                         self.positions.data_ptr(), self.slots.data_ptr(), self.denied.data_ptr(),
+                         n, rows, width, width, self.batch.max_q, self.batch.max_kv)
+        self._ref = ctypes.byref(self._c)
+
+
+def _pool_call(where, pool, requests, ws, stream):
+    """(device, requests, workspace, stream's handle) of a call on a pool."""
+    dev = _get_device()
+    if pool._dev != dev:
+        raise ValueError(f"{where}: the pool is on cuda:{pool._dev}, the current device is "
+                         f"cuda:{dev}")
+    if requests.dim() != 1:
+        raise ValueError(f"{where}: requests must be 1-D, got {tuple(requests.shape)}")
+    _int32s(where, "requests", requests, tuple(requests.shape), dev)
+    return dev, _workspace(where, ws, stream, dev), _handle(stream, _get_stream(dev))
+
+
+def paged_step(pool, plan, requests, new_lens, ws=None, stream=None):
+    """Makes room for new_lens (n,) more tokens of the pool's requests (n,), both
+    int32: takes the pages that they need, advances the lengths and fills the plan.
+    Sequences whose pages do not fit (and every later one that needs pages) are
+    denied: their rows have position and slot -1, kv_lens 0, and the pool's length
+    stays.  Bad requests and lengths are denied and recorded in the workspace's
+    status word.  Returns plan.batch."""
+    dev, ws, handle = _pool_call("paged_step", pool, requests, ws, stream)
+    if requests.shape[0] != plan.n or plan.batch._dev != dev:
+        raise ValueError(f"paged_step: {requests.shape[0]} requests on cuda:{dev} for a plan of "
+                         f"{plan.n} on cuda:{plan.batch._dev}")
+    _int32s("paged_step", "new_lens", new_lens, (plan.n,), dev)
+    rc = _lib.sage_paged_step(pool._ref, plan._ref, requests.data_ptr(), new_lens.data_ptr(),
+                              ws.data_ptr(), ws.numel(), handle)
+    if rc:
+        _check(rc, "sage_paged_step")
+    return plan.batch
+
+
+def paged_trim(pool, requests, keep_lens=None, ws=None, stream=None):
+    """Cuts the pool's requests (n,) to keep_lens (n,) tokens (None: they end) and
+    gives the pages behind them back: drafted tokens that were rejected, finished
+    requests.  A request that is not longer stays as it is."""
+    dev, ws, handle = _pool_call("paged_trim", pool, requests, ws, stream)
+    if keep_lens is not None:
+        _int32s("paged_trim", "keep_lens", keep_lens, tuple(requests.shape), dev)
+    rc = _lib.sage_paged_trim(pool._ref, requests.data_ptr(),
+                              0 if keep_lens is None else keep_lens.data_ptr(), requests.shape[0],
+                              ws.data_ptr(), ws.numel(), handle)
+    if rc:
+        _check(rc, "sage_paged_trim")
 
 
 def _off_cache(where, cache, batch, dev):
