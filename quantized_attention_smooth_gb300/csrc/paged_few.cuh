@@ -40,6 +40,7 @@
 #pragma once
 
 #include <atomic>
+#include <type_traits>
 
 #include "sage_kernels.h"
 #include "sage_paged_device.cuh"
@@ -78,17 +79,17 @@ struct Units {
   int per, tiles;            // units of one item; row tiles of one kv head
   int64_t total;
 };
-template <int kRows, int kUnitBlocks>
+template <int kRows, int kUnitBlocks, int kKeys>
 __device__ __forceinline__ Units units_of(const PagedAttnParams& p, int s, int* start, int* n,
-                                          int* len) {
+                                          int* len, int team) {
   Units u{0, 0, 0};
   if (!paged_seq(p.c, s, start, n, len)) return u;
   const int64_t rows = static_cast<int64_t>(*n) * p.group;
   if (rows < p.min_rows || rows > p.max_rows || rows == 0) return u;
-  const Span sp = span_of<16>(*len - *n, *len - 1, p.window, p.sinks);
+  const Span sp = span_of<kKeys>(*len - *n, *len - 1, p.window, p.sinks);
   u.per = max(1, (sp.count + kUnitBlocks - 1) / kUnitBlocks);
   u.tiles = static_cast<int>((rows + kRows - 1) / kRows);
-  u.total = static_cast<int64_t>(u.per) * u.tiles * p.c.Hkv;
+  u.total = static_cast<int64_t>(u.per) * u.tiles * (p.c.Hkv / team);
   return u;
 }
 
@@ -113,6 +114,11 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
   return d;
 }
 
+template <int kN>
+__device__ __forceinline__ int wrapped(int x) {
+  return x >= kN ? x - kN : x;
+}
+
 // Four 8x8 matrices of 16 bits from shared memory, a row of 16 bytes from each lane's
 // address: lane 4 g + t gets word t of row g, or transposed halfword g of rows 2t, 2t + 1.
 template <bool kTrans>
@@ -123,6 +129,62 @@ __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t at) {
   else
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
+}
+
+// fp16 products on top of sums that stay as they are.
+__device__ __forceinline__ void mma_from(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1, float c0, float c1,
+                                         float c2, float c3) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, "
+               "{%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+               : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2),
+                 "f"(c3));
+}
+
+// 16 rows of codes by the group: of rows 0-7 and 8-15 (kG 4 or 2 groups).
+template <bool kTrans, int kG>
+__device__ __forceinline__ void load_codes(uint32_t (&lo)[kG], uint32_t (&hi)[kG], uint32_t at) {
+  if constexpr (kG == 4) {
+    ldmatrix4<kTrans>(lo, at);
+    ldmatrix4<kTrans>(hi, at + 8 * 64);
+  } else {
+    uint32_t w[4];
+    ldmatrix4<kTrans>(w, at);
+    lo[0] = w[0]; lo[1] = w[1]; hi[0] = w[2]; hi[1] = w[3];
+  }
+}
+
+// A row's scales (kG halves), and those of two rows side by side.
+template <int kG>
+__device__ __forceinline__ void row_scales(uint32_t at, float (&s)[kG]) {
+  uint32_t w[2] = {0, 0};
+  if constexpr (kG == 4)
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(at) : "memory");
+  else
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(at) : "memory");
+#pragma unroll
+  for (int i = 0; i < kG / 2; ++i) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+    s[2 * i] = f.x;
+    s[2 * i + 1] = f.y;
+  }
+}
+template <int kG>
+__device__ __forceinline__ void pair_scales(uint32_t at, uint32_t (&s)[kG]) {
+  uint32_t w[4];
+  if constexpr (kG == 4) {
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at) : "memory");
+  } else {
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[2]) : "r"(at) : "memory");
+    w[1] = w[3] = 0;
+  }
+#pragma unroll
+  for (int i = 0; i < kG / 2; ++i) {
+    s[2 * i] = __byte_perm(w[i], w[2 + i], 0x5410);
+    s[2 * i + 1] = __byte_perm(w[i], w[2 + i], 0x7632);
+  }
 }
 
 __device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
@@ -159,22 +221,39 @@ struct Few {
   static constexpr int kRowB =                                        // bytes of a row
       kKind == kKindQ4 ? kDp / 2 : kDp * (kKind == kKindQ8 ? 1 : 2);
   static constexpr int kScaleB = kDp / 16;                            // a 4-bit row's scales
+  static constexpr int kKeys = kKind == kKindQ4 ? 32 : 16;            // of a block
   static constexpr int kBlockB =                                      // K, V, scales
-      32 * kRowB + (kKind == kKindQ8 ? 64 : kKind == kKindQ4 ? 32 * kScaleB : 0);
-  static constexpr int kStages = kRowB <= 64 ? 4 : 3;
+      2 * kKeys * kRowB + (kKind == kKindQ8 ? 64 : kKind == kKindQ4 ? 512 : 0);
+  static constexpr int kStages = kKind == kKindQ4 ? (kDp == 128 ? 3 : 4) : kRowB == 64 ? 4 : 3;
+  // where a 4-bit block's scales lie, of keys and 256 bytes on of values: 16 rows on 128
+  // bytes, as a tensor copy wants them
+  static constexpr int kScales = 2 * kKeys * kRowB;
   static constexpr int kPitch = kDp + 4;
   static constexpr int kRing = kWarps * kStages * kBlockB;
   static constexpr int kMerge = kWarps * 8 * kNr * kPitch * 4;
   static constexpr int kSmem = kRing > kMerge ? kRing : kMerge;
-  static constexpr int kCtas = kRowB == 256 || kNr > 2 ? 2 : kNr == 2 ? (kDp == 128 ? 2 : 3) : 4;
+  static constexpr int kCtas = kRowB == 256 || kNr > 2 ? 2
+                               : kNr == 2 ? (kDp == 128 ? 2 : 3)
+                               : kKind == kKindQ4 && kDp == 128 ? 3 : 4;
 };
+
+// Tensor maps of a 4-bit cache: codes of K and V, their scales.
+struct Maps4 {
+  CUtensorMap t[4];
+};
+struct NoMaps {};
+template <int kKind>
+using Maps = std::conditional_t<kKind == kKindQ4, Maps4, NoMaps>;
 
 template <int kKind, bool kQBF16, int kDp, int kNr, int kForm>
 __global__ void __launch_bounds__(kThreads, Few<kKind, kDp, kNr>::kCtas)
-paged_few_kernel(const PagedAttnParams p) {
+paged_few_kernel(const PagedAttnParams p, const __grid_constant__ Maps<kKind> maps) {
   constexpr bool kQ8 = kKind == kKindQ8, kQ4 = kKind == kKindQ4;
   constexpr bool kMmaBF16 = kKind == kKindBF16;
   constexpr float kDown = kBelow<kMmaBF16>, kOver = kLazy + kDown;
+  // 4 bits: where the results are fp16, P times a value's scale is rounded once, from 32
+  // bits; for bf16, whose own rounding is eight times as large, P and the product are.
+  constexpr bool kOnce = !kQBF16;
   constexpr int kRows = 8 * kNr;
   constexpr int kUnitBlocks = kWarps;                     // a unit: a block of each warp
   constexpr int kEl = kQ8 || kQ4 ? 1 : 2;                 // bytes of an element
@@ -182,18 +261,23 @@ paged_few_kernel(const PagedAttnParams p) {
   constexpr int kVw = kQ8 ? kDp / 32 : kDp / 16;          // words of a value per lane
   constexpr int kMt = kDp / 16;                           // 16-channel tiles of O^T
   using L = Few<kKind, kDp, kNr>;
-  constexpr int kPitch = L::kPitch, kRowB = L::kRowB, kStages = L::kStages;
+  constexpr int kPitch = L::kPitch, kRowB = L::kRowB, kStages = L::kStages, kKeys = L::kKeys;
+  constexpr int kSubs = kKeys / 16;                       // 16 keys to a product
   constexpr int kChunks = kRowB / 16;                     // 16-byte vectors of a row
-  extern __shared__ __align__(16) uint8_t ring_s[];
+  extern __shared__ __align__(1024) uint8_t ring_s[];
   float (*const acc_s)[kRows * kPitch] = reinterpret_cast<float (*)[kRows * kPitch]>(ring_s);
   __shared__ int64_t scan_s[kWarps];
   __shared__ FewItem it;
+  __shared__ uint64_t full_s[kQ4 ? kWarps * kStages : 1];
   __shared__ float m_s[kWarps][kRows], l_s[kWarps][kRows];
 
   const PagedGeo& c = p.c;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t = lane & 3;
-  const int cta = blockIdx.x, ctas = gridDim.x;
+  const int cta = blockIdx.x;
+  // Teams of CTAs work on as many heads side by side (4 bits only, see launch_few).
+  const int team = kQ4 ? p.team : 1, member = kQ4 ? cta % team : 0;
+  const int seat = kQ4 ? cta / team : cta, seats = kQ4 ? gridDim.x / team : gridDim.x;
   const int64_t ts = c.token_stride * kEl;
   uint8_t* const ring = ring_s + warp * kStages * L::kBlockB;
   // Copies: lane -> vector lc of every kRows32-th row.  A vector's place in its row
@@ -207,19 +291,40 @@ paged_few_kernel(const PagedAttnParams p) {
     return row * kRowB + ((kChunks >= 8 ? vec ^ ((row & 1) << 2) : vec) << 4);
   };
   auto v_at = [&](int row, int vec) {
-    if constexpr (kQ4) return 16 * kRowB + k_at(row, vec);
+    if constexpr (kQ4) return kKeys * kRowB + k_at(row, vec);
     return (16 + row) * kRowB +
            ((kChunks >= 8 ? vec ^ (row & 6) : vec ^ ((row >> 1) & 3)) << 4);
   };
   if (!p.join_inside) asm volatile("griddepcontrol.launch_dependents;");
 
+  if constexpr (kQ4) {
+    if ((smem_u32(ring_s) & 511u) != 0) {       // the copies' swizzle goes by the address
+      if (tid == 0) atomicOr(c.status, kStatusBadItem);
+      if (tid < 2) reinterpret_cast<PartHead*>(part_at(p.parts, cta, tid))->parts = 0;
+      return;
+    }
+    if (tid == 0) {
+      for (int i = 0; i < kWarps * kStages; ++i) mbar_init(&full_s[i], 1);
+      mbar_fence_init();
+    }
+  }
+  // 4 bits: 32-bit shared addresses, and this lane's part of those that the loop reads:
+  // rows 8 and 16 further and the values lie at fixed distances
+  const uint32_t ring_u = smem_u32(ring);
+  const uint32_t mat_off = kDp == 128 ? k_at(lane & 7, lane >> 3)
+                                      : k_at((lane & 7) + 8 * (lane >> 4), (lane >> 3) & 1);
+  const uint32_t key_scales = 2 * kKeys * kRowB + g * L::kScaleB;
+  const uint32_t val_scales = 2 * kKeys * kRowB + 256 + (kOnce ? g : 2 * t) * L::kScaleB;
+  uint64_t* const full = full_s + (kQ4 ? warp * kStages : 0);
+  uint32_t parities = 0;                        // of the stages' next rounds
+  int stage4 = 0;                               // the next one to be read
   // ---- this CTA's range of units
   const int per_thread = (c.nseq + kThreads - 1) / kThreads;
   const int s_begin = min(c.nseq, tid * per_thread), s_end = min(c.nseq, s_begin + per_thread);
   int64_t mine = 0;
   for (int s = s_begin; s < s_end; ++s) {
     int a, n, len;
-    mine += units_of<kRows, kUnitBlocks>(p, s, &a, &n, &len).total;
+    mine += units_of<kRows, kUnitBlocks, L::kKeys>(p, s, &a, &n, &len, team).total;
   }
   int64_t incl = mine;
 #pragma unroll
@@ -238,9 +343,9 @@ paged_few_kernel(const PagedAttnParams p) {
   const int64_t end = before + incl, begin = end - mine;
   // no CTA between two parts of an item is left without a unit: the join walks
   // from CTA to CTA
-  const int64_t busy = min(total, static_cast<int64_t>(ctas));
-  const int64_t u0 = cta < busy ? total * cta / busy : 0;
-  const int64_t u1 = cta < busy ? total * (cta + 1) / busy : 0;
+  const int64_t busy = min(total, static_cast<int64_t>(seats));
+  const int64_t u0 = seat < busy ? total * seat / busy : 0;
+  const int64_t u1 = seat < busy ? total * (seat + 1) / busy : 0;
   bool used[2] = {false, false};
   if (u0 < u1) {
     if (begin <= u0 && u0 < end) {                        // one thread
@@ -248,7 +353,7 @@ paged_few_kernel(const PagedAttnParams p) {
       int s = s_begin;
       for (; s < s_end; ++s) {
         int a, n, len;
-        const int64_t w = units_of<kRows, kUnitBlocks>(p, s, &a, &n, &len).total;
+        const int64_t w = units_of<kRows, kUnitBlocks, L::kKeys>(p, s, &a, &n, &len, team).total;
         if (off < w) break;
         off -= w;
       }
@@ -265,7 +370,8 @@ paged_few_kernel(const PagedAttnParams p) {
         it.count = 0;
         while (it.cur < it.last && it.s < c.nseq) {
           int start, n, len;
-          const Units un = units_of<kRows, kUnitBlocks>(p, it.s, &start, &n, &len);
+          const Units un =
+              units_of<kRows, kUnitBlocks, L::kKeys>(p, it.s, &start, &n, &len, team);
           if (it.off >= un.total) {                       // an empty sequence
             it.off = 0;
             ++it.s;
@@ -276,12 +382,13 @@ paged_few_kernel(const PagedAttnParams p) {
           it.count = static_cast<int>(
               min(static_cast<int64_t>(un.per - it.first), it.last - it.cur));
           it.per = un.per;
-          it.head = static_cast<int>(item / un.tiles);
-          it.tile = static_cast<int>(item - static_cast<int64_t>(it.head) * un.tiles);
+          const int heads = static_cast<int>(item / un.tiles);
+          it.head = heads * team + member;
+          it.tile = static_cast<int>(item - static_cast<int64_t>(heads) * un.tiles);
           it.start = start;
           it.rows = n * p.group;
           it.base = len - n;
-          it.span = span_of<16>(len - n, len - 1, p.window, p.sinks);
+          it.span = span_of<L::kKeys>(len - n, len - 1, p.window, p.sinks);
           break;
         }
       }
@@ -404,22 +511,55 @@ paged_few_kernel(const PagedAttnParams p) {
       }
 
       // Vectors of channels from D on are never loaded: zero once.
-      if (kForm != 0) {
+      if (kForm != 0 && !kQ4) {
         for (int i = lane; i < kStages * L::kBlockB / 16; i += 32)
           reinterpret_cast<uint4*>(ring)[i] = make_uint4(0, 0, 0, 0);
         __syncwarp();
       }
-      // A step is a block of 16 keys.  Its first key (-1: none that a row sees):
+      // A step is a block of kKeys keys.  Its first key (-1: none that a row sees):
       auto key_of = [&](int unit) {
         const int vb = unit * kWarps + warp;
-        const int k0 = 16 * (vb < sp.sink ? vb : vb - sp.sink + sp.from);
-        return vb < sp.count && k0 <= p_hi && (k0 + 15 >= lo || k0 < sinks) ? k0 : -1;
+        const int k0 = kKeys * (vb < sp.sink ? vb : vb - sp.sink + sp.from);
+        return vb < sp.count && k0 <= p_hi && (k0 + kKeys - 1 >= lo || k0 < sinks) ? k0 : -1;
       };
       auto seen = [&](int j) { return j <= p_hi && (j >= lo || j < sinks); };
       int next_key0 = -1, next_page = -1;
+      int next_slot = 0;
       auto locate = [&](int unit) {             // the table's entry, used a step later
         next_key0 = key_of(unit);
-        if (next_key0 >= 0) next_page = table[page_of(c, next_key0)];
+        if constexpr (kQ4) {
+          // lanes 0-3 and 4-7 copy K, V, their scales of 16 keys each, which share a page
+          const int k0 = next_key0 + 16 * (lane >> 2);
+          if (lane < 8 && next_key0 >= 0) {
+            next_page = -2;                     // one that no row sees
+            if (k0 <= p_hi && (k0 + 15 >= lo || k0 < sinks)) {
+              next_page = table[page_of(c, k0)];
+              next_slot = k0 - page_of(c, k0) * c.page_size;
+            }
+          }
+        } else {
+          if (next_key0 >= 0) next_page = table[page_of(c, next_key0)];
+        }
+      };
+      // Four bits: tensor copies; pages that are not there lie outside and read zeros.
+      auto issue_q4 = [&](int stage) {
+        if constexpr (kQ4) {
+        if (next_key0 < 0) return;
+        if (lane == 0) mbar_expect_tx(&full[stage], 2 * kKeys * (kRowB + L::kScaleB));
+        __syncwarp();
+        if (lane < 8) {
+          if (static_cast<uint32_t>(next_page) >= static_cast<uint32_t>(c.num_pages)) {
+            if (next_page != -2) atomicOr(c.status, kStatusBadPage);
+            next_page = static_cast<int>(c.num_pages);
+          }
+          const int what = lane & 3, half = lane >> 2;    // K, V, scales of K, of V
+          const uint32_t at = what < 2 ? (what * kKeys + 16 * half) * kRowB
+                                       : L::kScales + (what - 2) * 256 + half * 128;
+          tma_load_4d(ring + stage * L::kBlockB + at, &maps.t[what],
+                      what < 2 ? 0 : next_slot * (kDp / 64), what < 2 ? next_slot : 0, kvh,
+                      next_page, &full[stage]);
+        }
+        }
       };
       // Starts the copies of the located block into a stage; rows that no row of
       // the tile sees become zero (0 times what lies there could be NaN).
@@ -443,21 +583,6 @@ paged_few_kernel(const PagedAttnParams p) {
           if (kQ8 && lane < 4)
             copy16(dst + 32 * kRowB + 16 * lane, reinterpret_cast<const uint8_t*>(scales),
                    there ? 16 : 0);
-          if constexpr (kQ4) {
-            // A lane per row of scales; those of rows that nobody sees and of groups
-            // behind D become zero (a scale there could be NaN).
-            const int row = lane & 15;
-            const bool see = there && seen(k0 + row);
-            const uint16_t* from = lane < 16 ? c.k_groups : c.v_groups;
-            if (see) {
-              const int slot = k0 - page_of(c, k0) * c.page_size;
-              from += ((static_cast<int64_t>(next_page) * c.Hkv + kvh) * c.page_size + slot + row) *
-                      (kDp / 32);
-            }
-            copy_small<L::kScaleB>(dst + 32 * kRowB + lane * L::kScaleB,
-                                   reinterpret_cast<const uint8_t*>(from),
-                                   see ? 2 * ((c.D + 31) / 32) : 0);
-          }
           const bool whole = there && k0 + 15 <= p_hi && (k0 >= lo || k0 + 15 < sinks);
           const uint8_t* src_k = c.k + at + lane_off;
           const uint8_t* src_v = c.v + at + lane_off;
@@ -477,25 +602,40 @@ paged_few_kernel(const PagedAttnParams p) {
 
       const int end_unit = first_unit + count;
       locate(first_unit);
+      int key_queue[kStages - 1];               // 4 bits: first keys of the blocks under way
 #pragma unroll
       for (int i = 0; i < kStages - 1; ++i) {
-        issue(i);
+        key_queue[i] = next_key0;
+        if constexpr (kQ4) issue_q4(wrapped<kStages>(stage4 + i));
+        else issue(i);
         next_key0 = -1;
         if (first_unit + i + 1 < end_unit) locate(first_unit + i + 1);
       }
       int stage = 0;
       for (int u = first_unit; u < end_unit; ++u) {
-        asm volatile("cp.async.wait_group %0;" :: "n"(kStages - 2) : "memory");
+        if constexpr (!kQ4) asm volatile("cp.async.wait_group %0;" :: "n"(kStages - 2) : "memory");
         __syncwarp();                           // every lane's copies; and the last stage is read
-        issue(stage == 0 ? kStages - 1 : stage - 1);
+        const int cur0 = kQ4 ? key_queue[0] : key_of(u);
+#pragma unroll
+        for (int i = 0; i < kStages - 1; ++i)
+          key_queue[i] = i + 2 < kStages ? key_queue[i + 1] : next_key0;
+        if constexpr (kQ4) issue_q4(stage4 == 0 ? kStages - 1 : stage4 - 1);
+        else issue(stage == 0 ? kStages - 1 : stage - 1);
         next_key0 = -1;
         if (u + kStages < end_unit) locate(u + kStages);
         const uint8_t* const block = ring + stage * L::kBlockB;
+        const uint32_t base = ring_u + stage4 * L::kBlockB;
+        if constexpr (kQ4) {
+          if (cur0 >= 0) {                      // a block that was asked for
+            mbar_wait(&full[stage4], (parities >> stage4) & 1, nullptr, c.status, p.timeout_ns);
+            parities ^= 1u << stage4;
+          }
+          stage4 = wrapped<kStages>(stage4 + 1);
+        }
         stage = stage + 1 == kStages ? 0 : stage + 1;
         // ---- S^T, in two chains of products
-        const int cur0 = key_of(u);
         if (cur0 < 0) continue;
-        float x[kNr][4], x2[kNr][4];
+        float x[kSubs * kNr][4], x2[kNr][4];    // of the first 16 keys, then the next
 #pragma unroll
         for (int nr = 0; nr < kNr; ++nr)
 #pragma unroll
@@ -503,31 +643,34 @@ paged_few_kernel(const PagedAttnParams p) {
         if constexpr (kQ4) {
           // lane: word t of a group of keys g and g + 8
           constexpr int kG = kDp / 32;
-          uint32_t wa[kG], wb[kG];
-          if constexpr (kG == 4) {
-            ldmatrix4<false>(wa, smem_u32(block + k_at(lane & 7, lane >> 3)));
-            ldmatrix4<false>(wb, smem_u32(block + k_at(8 + (lane & 7), lane >> 3)));
-          } else {
-            uint32_t w[4];
-            ldmatrix4<false>(w, smem_u32(block + k_at((lane & 7) + 8 * (lane >> 4), (lane >> 3) & 1)));
-            wa[0] = w[0]; wa[1] = w[1]; wb[0] = w[2]; wb[1] = w[3];
-          }
-          const __half* const sa = reinterpret_cast<const __half*>(block + 32 * kRowB) + g * kG;
 #pragma unroll
-          for (int i = 0; i < kG; ++i) {
-            const uint32_t ua = wa[i] >> 8, ub = wb[i] >> 8;
+          for (int sub = 0; sub < kSubs; ++sub) {
+            uint32_t wa[kG], wb[kG];
+            load_codes<false, kG>(wa, wb, base + mat_off + 16 * sub * kRowB);
+            float sa[kG], sb[kG];
+            row_scales<kG>(base + key_scales + 128 * sub, sa);
+            row_scales<kG>(base + key_scales + 128 * sub + 8 * L::kScaleB, sb);
+            if constexpr (kForm != 0)           // groups behind D: anything
 #pragma unroll
-            for (int nr = 0; nr < kNr; ++nr) {
-              float y[4] = {qoff[nr][i][0], qoff[nr][i][1], qoff[nr][i][0], qoff[nr][i][1]};
-              mma<false>(y, wa[i] & kLow, wb[i] & kLow, wa[i] & kHigh, wb[i] & kHigh,
-                         qw[nr][4 * i], qw[nr][4 * i + 1]);
-              mma<false>(y, ua & kLow, ub & kLow, ua & kHigh, ub & kHigh, qw[nr][4 * i + 2],
-                         qw[nr][4 * i + 3]);
-              const float s0 = __half2float(sa[i]), s1 = __half2float(sa[8 * kG + i]);
-              x[nr][0] += s0 * y[0];
-              x[nr][1] += s0 * y[1];
-              x[nr][2] += s1 * y[2];
-              x[nr][3] += s1 * y[3];
+              for (int i = 0; i < kG; ++i)
+                if (32 * i >= c.D) sa[i] = sb[i] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < kG; ++i) {
+              const uint32_t ua = wa[i] >> 8, ub = wb[i] >> 8;
+#pragma unroll
+              for (int nr = 0; nr < kNr; ++nr) {
+                float y[4], z[4];
+                float (&w)[4] = x[sub * kNr + nr];
+                mma_from(y, wa[i] & kLow, wb[i] & kLow, wa[i] & kHigh, wb[i] & kHigh,
+                         qw[nr][4 * i], qw[nr][4 * i + 1], qoff[nr][i][0], qoff[nr][i][1],
+                         qoff[nr][i][0], qoff[nr][i][1]);
+                mma_from(z, ua & kLow, ub & kLow, ua & kHigh, ub & kHigh, qw[nr][4 * i + 2],
+                         qw[nr][4 * i + 3], y[0], y[1], y[2], y[3]);
+                w[0] = i == 0 ? sa[i] * z[0] : w[0] + sa[i] * z[0];
+                w[1] = i == 0 ? sa[i] * z[1] : w[1] + sa[i] * z[1];
+                w[2] = i == 0 ? sb[i] * z[2] : w[2] + sb[i] * z[2];
+                w[3] = i == 0 ? sb[i] * z[3] : w[3] + sb[i] * z[3];
+              }
             }
           }
         }
@@ -561,23 +704,24 @@ paged_few_kernel(const PagedAttnParams p) {
         }
         {
           // ---- logits, masks, running maximum and sum
-          const bool full =
-              cur0 + 15 <= p_lo && (cur0 >= lo_hi || cur0 + 15 < sinks);
+          const bool full_block =
+              cur0 + kKeys - 1 <= p_lo && (cur0 >= lo_hi || cur0 + kKeys - 1 < sinks);
           bool over = false;                    // a logit has outgrown its row's reference
 #pragma unroll
-          for (int nr = 0; nr < kNr; ++nr) {
+          for (int sn = 0; sn < kSubs * kNr; ++sn) {
+            const int nr = sn % kNr;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              float v = (x[nr][e] + x2[nr][e]) * rs[nr][e & 1];
+              float v = (kQ4 ? x[sn][e] : x[sn][e] + x2[nr][e]) * rs[nr][e & 1];
               if constexpr (kQ8) v *= ks[e >> 1];
-              if (!full) {
-                const int j = cur0 + g + 8 * (e >> 1);
+              if (!full_block) {
+                const int j = cur0 + 16 * (sn / kNr) + g + 8 * (e >> 1);
                 const int pos = rpos[nr][e & 1];
                 const bool see =
                     j <= pos && (p.window <= 0 || j > pos - p.window || j < sinks);
                 v = see ? v : -INFINITY;
               }
-              x[nr][e] = v;
+              x[sn][e] = v;
               over |= v > m[nr][e & 1] + kOver;  // with m = -inf: any logit but -inf
             }
           }
@@ -590,6 +734,8 @@ paged_few_kernel(const PagedAttnParams p) {
 #pragma unroll
               for (int i = 0; i < 2; ++i) {
                 float v = fmaxf(x[nr][i], x[nr][i + 2]);
+                if constexpr (kSubs == 2)
+                  v = fmaxf(v, fmaxf(x[kNr + nr][i], x[kNr + nr][i + 2]));
                 v = fmaxf(v, __shfl_xor_sync(kAll, v, 4));
                 v = fmaxf(v, __shfl_xor_sync(kAll, v, 8));
                 v = fmaxf(v, __shfl_xor_sync(kAll, v, 16));
@@ -606,6 +752,83 @@ paged_few_kernel(const PagedAttnParams p) {
                 for (int e = 0; e < 4; ++e) o[j][nr][e] *= alpha[nr][e & 1];
           }
           // ---- P^T and O^T
+          if constexpr (kQ4) {
+            // lane: channels 4 g .. 4 g + 3 of each group, of keys 2t and 2t + 1 (lo), and
+            // of those 8 further (hi); a value's scale goes into P, by the group
+            constexpr int kG = kDp / 32;
+            float safe[kNr][2];
+#pragma unroll
+            for (int nr = 0; nr < kNr; ++nr)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) safe[nr][i] = m[nr][i] == -INFINITY ? 0.0f : m[nr][i];
+#pragma unroll
+            for (int sub = 0; sub < kSubs; ++sub) {
+              float e4[kNr][4];
+#pragma unroll
+              for (int nr = 0; nr < kNr; ++nr)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  e4[nr][e] = fast_exp2(x[sub * kNr + nr][e] - safe[nr][e & 1]);
+                  l[nr][e & 1] += e4[nr][e];
+                }
+              uint32_t vl[kG], vh[kG];
+              load_codes<true, kG>(vl, vh, base + mat_off + (kKeys + 16 * sub) * kRowB);
+              // P times the scales: of keys g and g + 8 before P is turned round, or of
+              // 2t, 2t + 1 and those 8 further behind it
+              float sa[kG], sb[kG];
+              uint32_t s2[2][kG], pt[kNr][2];
+              if constexpr (kOnce) {
+                row_scales<kG>(base + val_scales + 128 * sub, sa);
+                row_scales<kG>(base + val_scales + 128 * sub + 8 * L::kScaleB, sb);
+              } else {
+                pair_scales<kG>(base + val_scales + 128 * sub, s2[0]);
+                pair_scales<kG>(base + val_scales + 128 * sub + 8 * L::kScaleB, s2[1]);
+#pragma unroll
+                for (int nr = 0; nr < kNr; ++nr) {
+                  pt[nr][0] = transpose8x8(pack2<false>(e4[nr][0], e4[nr][1]));
+                  pt[nr][1] = transpose8x8(pack2<false>(e4[nr][2], e4[nr][3]));
+                }
+              }
+              if (!full_block) {                // scales that no row sees may be NaN
+                const int j = cur0 + 16 * sub;
+                if constexpr (kOnce) {
+#pragma unroll
+                  for (int i = 0; i < kG; ++i) {
+                    if (!seen(j + g)) sa[i] = 0.0f;
+                    if (!seen(j + g + 8)) sb[i] = 0.0f;
+                  }
+                } else {
+#pragma unroll
+                  for (int h = 0; h < 2; ++h) {
+                    const uint32_t mask = (seen(j + 8 * h + 2 * t) ? 0xFFFFu : 0u) |
+                                          (seen(j + 8 * h + 2 * t + 1) ? 0xFFFF0000u : 0u);
+#pragma unroll
+                    for (int i = 0; i < kG; ++i) s2[h][i] &= mask;
+                  }
+                }
+              }
+#pragma unroll
+              for (int i = 0; i < kG; ++i) {
+                uint32_t n[2][4];               // the four channels, as numbers -8..7
+                nibbles_to_half(vl[i], n[0]);
+                nibbles_to_half(vh[i], n[1]);
+#pragma unroll
+                for (int nr = 0; nr < kNr; ++nr) {
+                  uint32_t b0, b1;
+                  if constexpr (kOnce) {
+                    b0 = transpose8x8(pack2<false>(e4[nr][0] * sa[i], e4[nr][1] * sa[i]));
+                    b1 = transpose8x8(pack2<false>(e4[nr][2] * sb[i], e4[nr][3] * sb[i]));
+                  } else {
+                    b0 = mul_half2(pt[nr][0], s2[0][i]);
+                    b1 = mul_half2(pt[nr][1], s2[1][i]);
+                  }
+                  mma<false>(o[2 * i][nr], n[0][0], n[0][1], n[1][0], n[1][1], b0, b1);
+                  mma<false>(o[2 * i + 1][nr], n[0][2], n[0][3], n[1][2], n[1][3], b0, b1);
+                }
+              }
+            }
+            continue;
+          }
           uint32_t pb[kNr][2];
 #pragma unroll
           for (int nr = 0; nr < kNr; ++nr) {
@@ -619,44 +842,6 @@ paged_few_kernel(const PagedAttnParams p) {
             }
             pb[nr][0] = transpose8x8(pack2<kMmaBF16>(e4[0], e4[1]));
             pb[nr][1] = transpose8x8(pack2<kMmaBF16>(e4[2], e4[3]));
-          }
-          if constexpr (kQ4) {
-            // lane: channels 4 g .. 4 g + 3 of each group, of keys 2t and 2t + 1 (lo), and
-            // of those 8 further (hi); a value's scale goes into P, by the group
-            constexpr int kG = kDp / 32;
-            uint32_t vl[kG], vh[kG];
-            if constexpr (kG == 4) {
-              ldmatrix4<true>(vl, smem_u32(block + v_at(lane & 7, lane >> 3)));
-              ldmatrix4<true>(vh, smem_u32(block + v_at(8 + (lane & 7), lane >> 3)));
-            } else {
-              uint32_t w[4];
-              ldmatrix4<true>(w, smem_u32(block + v_at((lane & 7) + 8 * (lane >> 4), (lane >> 3) & 1)));
-              vl[0] = w[0]; vl[1] = w[1]; vh[0] = w[2]; vh[1] = w[3];
-            }
-            const uint32_t* const sv = reinterpret_cast<const uint32_t*>(
-                block + 32 * kRowB + 16 * L::kScaleB) + t * kG;      // rows 2t, 2t + 1
-            uint32_t s2[kG][2];
-#pragma unroll
-            for (int i = 0; i < kG / 2; ++i)
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const uint32_t a = sv[h * 4 * kG + i], b = sv[h * 4 * kG + kG / 2 + i];
-                s2[2 * i][h] = __byte_perm(a, b, 0x5410);
-                s2[2 * i + 1][h] = __byte_perm(a, b, 0x7632);
-              }
-#pragma unroll
-            for (int i = 0; i < kG; ++i) {
-              uint32_t n[2][4];                 // the four channels, as numbers -8..7
-              nibbles_to_half(vl[i], n[0]);
-              nibbles_to_half(vh[i], n[1]);
-#pragma unroll
-              for (int nr = 0; nr < kNr; ++nr) {
-                const uint32_t b0 = mul_half2(pb[nr][0], s2[i][0]), b1 = mul_half2(pb[nr][1], s2[i][1]);
-                mma<false>(o[2 * i][nr], n[0][0], n[0][1], n[1][0], n[1][1], b0, b1);
-                mma<false>(o[2 * i + 1][nr], n[0][2], n[0][3], n[1][2], n[1][3], b0, b1);
-              }
-            }
-            continue;
           }
           uint32_t vw[4][kVw];
 #pragma unroll
@@ -714,7 +899,7 @@ paged_few_kernel(const PagedAttnParams p) {
           }
         }
       }
-      asm volatile("cp.async.wait_all;" ::: "memory");
+      if constexpr (!kQ4) asm volatile("cp.async.wait_all;" ::: "memory");
       __syncthreads();                          // the rings become the merge buffer
 
       // ---- join the warps
@@ -754,11 +939,12 @@ paged_few_kernel(const PagedAttnParams p) {
         used[which] = true;
         if (tid == 0) {
           const int64_t from = it.cur - it.first;
-          const int end_cta = cta_of(from + it.per - 1, it.total, it.busy);
-          it.first_cta = cta_of(from, it.total, it.busy);
-          it.parts = end_cta - it.first_cta + 1;
+          const int end_seat = cta_of(from + it.per - 1, it.total, it.busy);
+          const int first_seat = cta_of(from, it.total, it.busy);
+          it.first_cta = first_seat * team + member;
+          it.parts = end_seat - first_seat + 1;
           *reinterpret_cast<PartHead*>(part) =
-              PartHead{end_cta - cta + 1, it.s, it.head, it.tile};
+              PartHead{end_seat - seat + 1, it.s, it.head, it.tile};
         }
       }
       // out = O / l of four channels of a row
@@ -827,7 +1013,7 @@ paged_few_kernel(const PagedAttnParams p) {
           float* const ml = &acc_s[0][0];
           const int parts = it.parts, fit = min(parts, kFit);
           for (int i = tid; i < fit * kRows; i += kThreads) {
-            const float* f = part_floats(p.parts, it.first_cta + i / kRows, i < kRows) + i % kRows;
+            const float* f = part_floats(p.parts, it.first_cta + i / kRows * team, i < kRows) + i % kRows;
             ml[i] = __ldcg(f);
             ml[kFit * kRows + i] = __ldcg(f + kMaxRows);
           }
@@ -837,11 +1023,11 @@ paged_few_kernel(const PagedAttnParams p) {
             if (it.tile * kRows + r >= it.rows) break;    // later ones are later rows
             auto max_of = [&](int j) {
               return j < kFit ? ml[j * kRows + r]
-                              : __ldcg(part_floats(p.parts, it.first_cta + j, 0) + r);
+                              : __ldcg(part_floats(p.parts, it.first_cta + j * team, 0) + r);
             };
             auto sum_of = [&](int j) {
               return j < kFit ? ml[(kFit + j) * kRows + r]
-                              : __ldcg(part_floats(p.parts, it.first_cta + j, 0) + kMaxRows + r);
+                              : __ldcg(part_floats(p.parts, it.first_cta + j * team, 0) + kMaxRows + r);
             };
             float top = -INFINITY;
             for (int j = 0; j < parts; ++j) top = fmaxf(top, max_of(j));
@@ -853,7 +1039,7 @@ paged_few_kernel(const PagedAttnParams p) {
 #pragma unroll
               for (int j = 0; j < 8; ++j)
                 v[j] = __ldcg(reinterpret_cast<const float4*>(
-                    part_floats(p.parts, it.first_cta + min(j0 + j, parts - 1),
+                    part_floats(p.parts, it.first_cta + min(j0 + j, parts - 1) * team,
                                 j0 + j == 0 || parts == 1) + 2 * kMaxRows + r * kDp + ch));
 #pragma unroll
               for (int j = 0; j < 8; ++j)
@@ -867,6 +1053,7 @@ paged_few_kernel(const PagedAttnParams p) {
           }
         }
       }
+      if constexpr (kQ4) fence_proxy_async_smem();      // the ring again
       __syncthreads();
       if (tid == 0) {
         it.cur += it.count;
@@ -888,7 +1075,7 @@ paged_join_kernel(const PagedAttnParams p, int ctas) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int c0 = blockIdx.x, r = blockIdx.y, tid = threadIdx.x;
   const PartHead h = *reinterpret_cast<const PartHead*>(part_at(p.parts, c0, 1));
-  const int parts = min(h.parts, ctas - c0);
+  const int parts = min(h.parts, (ctas - c0 + p.team - 1) / p.team);
   if (parts <= 0) return;
   int start, n, len;
   if (!paged_seq(p.c, h.seq, &start, &n, &len)) return;
@@ -896,7 +1083,7 @@ paged_join_kernel(const PagedAttnParams p, int ctas) {
   if (rr >= n * p.group) return;
   float top = -INFINITY;
   for (int i = tid; i < parts; i += 128) {
-    const float v = reinterpret_cast<const float*>(part_at(p.parts, c0 + i, i == 0) +
+    const float v = reinterpret_cast<const float*>(part_at(p.parts, c0 + i * p.team, i == 0) +
                                                    sizeof(PartHead))[r];
     w_s[i] = v;
     top = fmaxf(top, v);
@@ -911,7 +1098,7 @@ paged_join_kernel(const PagedAttnParams p, int ctas) {
   const int ch = tid;
 #pragma unroll 4
   for (int i = 0; i < parts; ++i) {
-    const float* f = reinterpret_cast<const float*>(part_at(p.parts, c0 + i, i == 0) +
+    const float* f = reinterpret_cast<const float*>(part_at(p.parts, c0 + i * p.team, i == 0) +
                                                     sizeof(PartHead));
     const float w = fast_exp2(w_s[i] - safe);
     sum += w * f[kMaxRows + r];
@@ -963,21 +1150,33 @@ cudaError_t launch_few(const PagedAttnParams& p, int sms, cudaStream_t st) {
     resident[dev].store(per, std::memory_order_relaxed);
   }
   // at most one CTA per unit of the longest lengths the call declares
-  constexpr int kUnitKeys = 16 * kWarps;
+  constexpr int kUnitKeys = L::kKeys * kWarps;
   const int64_t max_units = (static_cast<int64_t>(p.c.max_kv) + kUnitKeys - 1) / kUnitKeys + 1;
   const int64_t tiles = (static_cast<int64_t>(p.c.max_q) * p.group + 8 * kNr - 1) / (8 * kNr);
   const int64_t items = tiles * p.c.Hkv * p.c.nseq;    // below 2^63; times max_units perhaps not
   int ctas = sms * per < kMaxCtas ? sms * per : kMaxCtas;
   if (items < ctas && items * max_units < ctas) ctas = static_cast<int>(items * max_units);
+  PagedAttnParams prm = p;
+  prm.team = 1;
+  Maps<kKind> maps{};
+  if constexpr (kKind == kKindQ4) {
+    if (!paged_maps4(p.c, 16, maps.t)) return cudaErrorInvalidValue;
+    // Heads whose rows lie side by side are read at the same time, by a team of CTAs in
+    // step: a row of 64 bytes alone is half a line of the L2, and its other half came
+    // from memory again.  (Rows that lie apart have neighbours of their own.)
+    if (p.c.head_stride == 16 * ((p.c.D + 31) / 32))
+      while (prm.team < 8 && p.c.Hkv % (2 * prm.team) == 0) prm.team *= 2;
+    ctas = ctas / prm.team * prm.team;
+    if (ctas == 0) ctas = prm.team;
+  }
   // Parts are joined by the CTA that finishes an item last, which saves the host a
   // launch, unless few items spread over many CTAs: one CTA would then read a
   // hundred parts or more, and a second kernel does it by the row.  (Sequence and
   // head pairs over 32768 keys, inside against second kernel: 1: 91 and 63 us, 2: 54
   // and 45, 4: 44 and 40, 8: 50 and 48, 128: 351 and 353; over 2000 keys the second
   // kernel is 1 to 2 us ahead up to 64 of them, at the price of its launch.)
-  PagedAttnParams prm = p;
   prm.join_inside = items >= (ctas + kJoinInside - 1) / kJoinInside;
-  kern<<<ctas, kThreads, L::kSmem, st>>>(prm);
+  kern<<<ctas, kThreads, L::kSmem, st>>>(prm, maps);
   note_launch();
   e = cudaGetLastError();
   if (e != cudaSuccess || prm.join_inside) return e;
@@ -990,7 +1189,7 @@ cudaError_t launch_few(const PagedAttnParams& p, int sms, cudaStream_t st) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, paged_join_kernel<kQBF16, kDp, 8 * kNr>, p, ctas);
+  e = cudaLaunchKernelEx(&cfg, paged_join_kernel<kQBF16, kDp, 8 * kNr>, prm, ctas);
   note_launch();
   return e;
 }

@@ -209,14 +209,20 @@ __device__ __forceinline__ void turn_table(const RowsParams& p, int64_t t0, int 
 __device__ __forceinline__ __half group_scale(float top, float most) {
   return __float2half_rn(fminf(__fmul_rn(top, kSeventh), most));
 }
-__device__ __forceinline__ uint32_t pack_nibbles(const float (&x)[8], float inv) {
+__device__ __forceinline__ uint32_t pack_nibbles(const float (&x)[8], float top, float inv) {
+  float n[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) n[e] = __fmul_rn(x[e], inv);
+  if (!(__fmul_rn(top, inv) < 7.25f)) {         // a scale at its bounds
+#pragma unroll
+    for (int e = 0; e < 8; ++e) n[e] = fminf(fmaxf(n[e], -7.0f), 7.0f);
+  }
+  // 1.5 * 2^23 + 8 rounds to whole numbers and leaves n + 8 in the lowest bits; above
+  // them stands 0x4B400000, which comes off the sum of all eight
   uint32_t w = 0;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const float n = fminf(fmaxf(rintf(__fmul_rn(x[e], inv)), -7.0f), 7.0f);
-    w |= static_cast<uint32_t>(static_cast<int>(n) + 8) << (4 * e);
-  }
-  return w;
+  for (int e = 7; e >= 0; --e) w = w * 16u + __float_as_uint(__fadd_rn(n[e], 12582920.0f));
+  return w - 0x4B400000u * 0x11111111u;
 }
 
 // kMode: 0 rope, 1 append 16-bit, 2 append Q8, 3 append Q4.  kLanes: lanes of a row.
@@ -360,7 +366,7 @@ rows_kernel(const RowsParams p) {
               const float inv = s > 0.0f ? __fdiv_rn(1.0f, s) : 0.0f;
               if (c0 < 32 * ((p.D + 31) / 32))
                 *reinterpret_cast<uint32_t*>((what == 1 ? c.k : c.v) + slot_s[t] +
-                                             h * c.head_stride + c0 / 2) = pack_nibbles(x, inv);
+                                             h * c.head_stride + c0 / 2) = pack_nibbles(x, top, inv);
               if (sub % 4 == 0)
                 reinterpret_cast<__half*>(what == 1 ? c.k_groups : c.v_groups)
                     [(scale_s[t] + static_cast<int64_t>(h) * c.page_size) * (c.Dp / 32) + sub / 4] =
@@ -613,6 +619,119 @@ __device__ __forceinline__ void pair_pass(const RowsParams& p, const Tokens& tk,
   }
 }
 
+// ---- Q4, many tokens: four lanes are a group of 32 channels of one head's keys or
+// values and keep it for the CTA's tokens, with the means or factors in registers;
+// heads of any size fill the lanes (80 channels: 10 of 12).  In the half layout a
+// lane reads its partner channels as well (they come out of the L1) and turns its own.
+template <bool kBF16>
+__device__ __forceinline__ void quad_pass(const RowsParams& p, const Tokens& tk, const float2* cs,
+                                          int64_t t0, int nt) {
+  const PagedGeo& c = p.c;
+  constexpr int kQuads = kRowThreads / 4, kAhead = 4;
+  const int quad = threadIdx.x >> 2, ql = threadIdx.x & 3;
+  const int groups = (p.D + 31) / 32, padded = c.Dp / 32, units = 2 * p.Hkv * groups;
+  const int at_once = min(units, kQuads), step = kQuads / at_once;
+  const int first = quad / at_once, rounds = (nt + step - 1) / step;
+  const int half = p.R / 2;
+  for (int ub = 0; ub < units; ub += at_once) {
+    const int u = ub + quad - first * at_once;
+    const bool mine = u < units && first < step;
+    const int row = u / groups, grp = u - row * groups;
+    const bool val = row >= p.Hkv;
+    const int h = val ? row - p.Hkv : row, c0 = 32 * grp + 8 * ql;
+    const bool live = mine && c0 < p.D;
+    const bool turn = p.inv_freq != nullptr && !val && c0 < p.R;
+    const bool apart = turn && !p.interleaved;
+    const int mate = c0 < half ? half : -half;          // from a channel to its partner
+    float chan[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      chan[e] = live ? (val ? c.v_scale : c.k_mean)[h * c.Dp + c0 + e] : 0.0f;
+      if (val) chan[e] = chan[e] > 0.0f ? __fdiv_rn(1.0f, 64.0f * chan[e]) : 0.0f;
+    }
+    const int64_t stride = val ? p.v_tok : p.k_tok;
+    const uint16_t* const src = (val ? p.v + h * p.v_head : p.k + h * p.k_head) + t0 * stride + c0;
+    uint8_t* const codes = (val ? c.v : c.k) + h * c.head_stride + c0 / 2;
+    __half* const scales = reinterpret_cast<__half*>(val ? c.v_groups : c.k_groups) + grp;
+    for (int rb = 0; rb < rounds; rb += kAhead) {
+      uint4 raw[kAhead], other[kAhead];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int t = first + (rb + k) * step;
+        raw[k] = other[k] = make_uint4(0, 0, 0, 0);
+        if (live && t < nt) {
+          raw[k] = *reinterpret_cast<const uint4*>(src + t * stride);
+          if (apart) other[k] = *reinterpret_cast<const uint4*>(src + t * stride + mate);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        if (rb + k >= rounds) break;                    // the same for every lane
+        const int t = first + (rb + k) * step;
+        const int at = t < nt ? t : 0;
+        float x[8];
+        unpack8<kBF16>(raw[k], x);
+        if (apart) {
+          float y[8];
+          unpack8<kBF16>(other[k], y);
+          const float2* const a = cs + at * 64 + (c0 < half ? c0 : c0 - half);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float2 w = a[e];
+            x[e] = c0 < half ? x[e] * w.x - y[e] * w.y : x[e] * w.x + y[e] * w.y;
+          }
+        } else if (turn) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (c0 + 2 * i < p.R) {
+              const float2 w = cs[at * 64 + c0 / 2 + i];
+              const float x1 = x[2 * i], x2 = x[2 * i + 1];
+              x[2 * i] = x1 * w.x - x2 * w.y;
+              x[2 * i + 1] = x2 * w.x + x1 * w.y;
+            }
+        }
+        float top = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          x[e] = val ? __fmul_rn(x[e], chan[e]) : __fsub_rn(x[e], chan[e]);
+          top = fmaxf(top, fabsf(x[e]));
+        }
+        top = fmaxf(top, __shfl_xor_sync(kAll, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(kAll, top, 2));
+        const __half scale = group_scale(top, val ? kMostV : kMostK);
+        const float s = __half2float(scale);
+        const float inv = s > 0.0f ? __fdiv_rn(1.0f, s) : 0.0f;
+        if (mine && t < nt && tk.page[at] >= 0) {
+          *reinterpret_cast<uint32_t*>(codes + tk.slot[at]) = pack_nibbles(x, top, inv);
+          if (ql == 0) {
+            __half* const to = scales + (tk.scale[at] + static_cast<int64_t>(h) * c.page_size) * padded;
+            *to = scale;
+            if (grp == groups - 1)                      // groups behind D
+              for (int e = groups; e < padded; ++e) to[e - grp] = __ushort_as_half(0);
+          }
+        }
+      }
+    }
+  }
+}
+
+template <bool kBF16>
+__global__ void __launch_bounds__(kRowThreads, 3)
+quad_rows_kernel(const RowsParams p) {
+  __shared__ float2 cs[kMaxPairToks * 64];
+  __shared__ Tokens tk;
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * p.toks;
+  const int nt = static_cast<int>(min(static_cast<int64_t>(p.toks), p.T - t0));
+  place_tokens(p, t0, nt, tk.pos, tk.page, tk.slot, tk.scale);
+  __syncthreads();
+  if (p.inv_freq != nullptr) {
+    turn_table(p, t0, nt, tk.pos, cs);
+    __syncthreads();
+  }
+  if (p.Hq > 0) pair_pass<3, 0, kBF16>(p, tk, cs, t0, nt);
+  quad_pass<kBF16>(p, tk, cs, t0, nt);
+}
+
 template <int kMode, bool kBF16>
 __global__ void __launch_bounds__(kRowThreads, kMode == 2 ? 4 : 3)
 pair_rows_kernel(const RowsParams p) {
@@ -644,7 +763,10 @@ cudaError_t launch_pairs(const RowsParams& p0, int sms, cudaStream_t st) {
   while (p.toks < kMaxPairToks && p.T / (2 * p.toks) >= 4 * sms) p.toks *= 2;
   const int64_t ctas = (p.T + p.toks - 1) / p.toks;
   if (ctas > 0x7FFFFFFF) return cudaErrorInvalidValue;
-  pair_rows_kernel<kMode, kBF16><<<static_cast<unsigned>(ctas), kRowThreads, 0, st>>>(p);
+  if constexpr (kMode == 3)
+    quad_rows_kernel<kBF16><<<static_cast<unsigned>(ctas), kRowThreads, 0, st>>>(p);
+  else
+    pair_rows_kernel<kMode, kBF16><<<static_cast<unsigned>(ctas), kRowThreads, 0, st>>>(p);
   note_launch();
   return cudaGetLastError();
 }
@@ -799,7 +921,6 @@ cudaError_t launch_gather(const RowsParams& p, bool bf16, int sms, cudaStream_t 
 }
 
 cudaError_t launch_rows(const RowsParams& p, int mode, bool bf16, int sms, cudaStream_t st) {
-  if (mode == 3) return launch_mode<3>(p, bf16, sms, st);
   // Two vectors a lane from 4 tokens per SM on, for whole vectors.  Measured, two
   // vectors against one (us; one call in a graph, L2 flushed):
   //   rope, half layout, 16000 tokens x (40 + 40) heads of 128      132   192
@@ -816,8 +937,10 @@ cudaError_t launch_rows(const RowsParams& p, int mode, bool bf16, int sms, cudaS
   const bool apart = p.inv_freq != nullptr && !p.interleaved;
   const bool neighbours = p.inv_freq != nullptr && p.interleaved;
   const bool pairs = p.vec && p.T >= 4 * static_cast<int64_t>(sms) &&
-                     !(apart && p.R % 16 != 0) && !(neighbours && mode != 2);
+                     !(apart && p.R % 16 != 0) && !(neighbours && mode < 2);
   if (pairs) {
+    if (mode == 3)
+      return bf16 ? launch_pairs<3, true>(p, sms, st) : launch_pairs<3, false>(p, sms, st);
     if (mode == 0)
       return bf16 ? launch_pairs<0, true>(p, sms, st) : launch_pairs<0, false>(p, sms, st);
     if (mode == 1)
@@ -826,7 +949,8 @@ cudaError_t launch_rows(const RowsParams& p, int mode, bool bf16, int sms, cudaS
   }
   if (mode == 0) return launch_mode<0>(p, bf16, sms, st);
   if (mode == 1) return launch_mode<1>(p, bf16, sms, st);
-  return launch_mode<2>(p, bf16, sms, st);
+  if (mode == 2) return launch_mode<2>(p, bf16, sms, st);
+  return launch_mode<3>(p, bf16, sms, st);
 }
 
 }  // namespace sage

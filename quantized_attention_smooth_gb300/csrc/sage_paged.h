@@ -2,6 +2,7 @@
 // host launchers and the kernels that write and read the cache.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -107,14 +108,18 @@ struct PagedAttnParams {
   uint8_t* parts;            // split results (workspace)
   uint32_t* arrivals;        // kArrivalBytes of the workspace, zero between calls
   int32_t join_inside;       // parts joined by the kernel itself (set by the launcher)
+  int32_t team;              // CTAs that read neighbouring heads side by side (likewise)
   uint64_t timeout_ns;
 };
 
 cudaError_t launch_paged_few(const PagedAttnParams& p, bool bf16, int sms, cudaStream_t st);
+// Tensor maps of a 4-bit cache in boxes of `rows` slots: codes of K and V, scales of K and V.
+bool paged_maps4(const PagedGeo& c, int rows, CUtensorMap* maps);
 cudaError_t launch_paged_few_q4(const PagedAttnParams& p, bool bf16, int sms, cudaStream_t st);
 size_t paged_few_bytes();
 int paged_few_rows(int Dp);   // rows (new tokens x group) that one of its tiles holds
 cudaError_t launch_paged_many(const PagedAttnParams& p, bool bf16, int sms, cudaStream_t st);
+cudaError_t launch_paged_many_q4(const PagedAttnParams& p, bool bf16, int sms, cudaStream_t st);
 size_t paged_many_bytes();
 bool paged_many_serves(const PagedGeo& c, int group);
 

@@ -104,16 +104,16 @@ __device__ __forceinline__ void copy8(uint32_t dst, const uint8_t* src, int byte
   asm volatile("cp.async.ca.shared.global.L2::128B [%0], [%1], 8, %2;"
                :: "r"(dst), "l"(src), "r"(bytes) : "memory");
 }
-template <int kBytes>
-__device__ __forceinline__ void copy_small(uint32_t dst, const uint8_t* src, int bytes) {
-  static_assert(kBytes == 4 || kBytes == 8, "");
-  if constexpr (kBytes == 8)
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;"
-                 :: "r"(dst), "l"(src), "r"(bytes) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;"
-                 :: "r"(dst), "l"(src), "r"(bytes) : "memory");
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, int x, int y, int z,
+                                            int w, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];"
+      :: "r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w),
+         "r"(smem_u32(bar))
+      : "memory");
 }
+
 // A vector of a row that ends after `left` more elements (untouched where none
 // are left), zero unless `see`.  kForm 0: all are there; 2: rows of 8-bit codes
 // that start or end on 8 bytes only.

@@ -991,7 +991,7 @@ class PagedPlan:
     """The buffers of a step of n sequences with `rows` packed rows in all, at most
     max_q of one and max_kv cached tokens: cu_q, kv_lens and block_table, as the
     PagedBatch `batch`; positions and slots (int64, rows), slots as page * page_size
-    + place in the page; denied (int32, 1), sequences that got no pages."""
+    + place in the page; denied, an int32 scalar, sequences that got no pages."""
 
     def __init__(self, pool, n, rows, max_q, max_kv):
         import torch
@@ -1002,7 +1002,7 @@ class PagedPlan:
         width = max(1, -(-max_kv // pool.page_size))
         new = lambda *shape, dtype=torch.int32, fill=0: torch.full(
             shape, fill, dtype=dtype, device=pool.table.device)
-        self.cu_q, self.kv_lens, self.denied = new(n + 1), new(n), new(1)
+        self.cu_q, self.kv_lens, self.denied = new(n + 1), new(n), new()
         self.block_table = new(n, width, fill=-1)
         self.positions, self.slots = (new(rows, dtype=torch.int64, fill=-1) for _ in range(2))
         self.batch = PagedBatch(self.cu_q, self.kv_lens, self.block_table, max_q, max_kv)
