@@ -48,7 +48,7 @@
 namespace sage {
 namespace {
 
-constexpr int kThreads = 128, kWarps = 4;
+constexpr int kWarps = 4;                 // that take the keys
 constexpr int kMaxCtas = 152 * 8;
 constexpr unsigned kAll = 0xFFFFFFFFu;
 constexpr int kJoinInside = 40;   // most parts of an item, on average, that one CTA joins
@@ -114,9 +114,11 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
   return d;
 }
 
-template <int kN>
-__device__ __forceinline__ int wrapped(int x) {
-  return x >= kN ? x - kN : x;
+// A barrier of the whole block that two places of the code may reach.
+template <bool kTwoPlaces>
+__device__ __forceinline__ void block_barrier(int threads) {
+  if constexpr (kTwoPlaces) asm volatile("barrier.sync 1, %0;" :: "r"(threads) : "memory");
+  else __syncthreads();
 }
 
 // Four 8x8 matrices of 16 bits from shared memory, a row of 16 bytes from each lane's
@@ -135,7 +137,7 @@ __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t at) {
 __device__ __forceinline__ void mma_from(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1, float c0, float c1,
                                          float c2, float c3) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, "
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, "
                "{%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
                : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
                : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2),
@@ -155,7 +157,7 @@ __device__ __forceinline__ void load_codes(uint32_t (&lo)[kG], uint32_t (&hi)[kG
   }
 }
 
-// A row's scales (kG halves), and those of two rows side by side.
+// A row's scales (kG halves).
 template <int kG>
 __device__ __forceinline__ void row_scales(uint32_t at, float (&s)[kG]) {
   uint32_t w[2] = {0, 0};
@@ -170,29 +172,6 @@ __device__ __forceinline__ void row_scales(uint32_t at, float (&s)[kG]) {
     s[2 * i + 1] = f.y;
   }
 }
-template <int kG>
-__device__ __forceinline__ void pair_scales(uint32_t at, uint32_t (&s)[kG]) {
-  uint32_t w[4];
-  if constexpr (kG == 4) {
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at) : "memory");
-  } else {
-    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[2]) : "r"(at) : "memory");
-    w[1] = w[3] = 0;
-  }
-#pragma unroll
-  for (int i = 0; i < kG / 2; ++i) {
-    s[2 * i] = __byte_perm(w[i], w[2 + i], 0x5410);
-    s[2 * i + 1] = __byte_perm(w[i], w[2 + i], 0x7632);
-  }
-}
-
-__device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
-  const __half2 c = __hmul2(*reinterpret_cast<const __half2*>(&a),
-                            *reinterpret_cast<const __half2*>(&b));
-  return *reinterpret_cast<const uint32_t*>(&c);
-}
-
 // A nibble u in the lowest bits of an fp16 is the number u 2^-24, four bits higher
 // u 2^-20, exactly: a mask makes two operands of eight codes, and -8 of each comes off
 // the sums (K).  Values become numbers n = u - 8 first, since their sums may be far
@@ -221,10 +200,11 @@ struct Few {
   static constexpr int kRowB =                                        // bytes of a row
       kKind == kKindQ4 ? kDp / 2 : kDp * (kKind == kKindQ8 ? 1 : 2);
   static constexpr int kScaleB = kDp / 16;                            // a 4-bit row's scales
-  static constexpr int kKeys = kKind == kKindQ4 ? 32 : 16;            // of a block
+  // keys of a block: 32 of 4 bits as far as registers go
+  static constexpr int kKeys = kKind == kKindQ4 && kNr * kDp <= 128 ? 32 : 16;
   static constexpr int kBlockB =                                      // K, V, scales
       2 * kKeys * kRowB + (kKind == kKindQ8 ? 64 : kKind == kKindQ4 ? 512 : 0);
-  static constexpr int kStages = kKind == kKindQ4 ? (kDp == 128 ? 3 : 4) : kRowB == 64 ? 4 : 3;
+  static constexpr int kStages = kKind == kKindQ4 ? 4 : kRowB == 64 ? 4 : 3;
   // where a 4-bit block's scales lie, of keys and 256 bytes on of values: 16 rows on 128
   // bytes, as a tensor copy wants them
   static constexpr int kScales = 2 * kKeys * kRowB;
@@ -234,26 +214,25 @@ struct Few {
   static constexpr int kSmem = kRing > kMerge ? kRing : kMerge;
   static constexpr int kCtas = kRowB == 256 || kNr > 2 ? 2
                                : kNr == 2 ? (kDp == 128 ? 2 : 3)
-                               : kKind == kKindQ4 && kDp == 128 ? 3 : 4;
+                               : kKind == kKindQ4 ? 3 : 4;
+  // 4 bits: a fifth warp makes the copies of the other four
+  static constexpr int kThreads = kKind == kKindQ4 ? 160 : 128;
 };
 
-// Tensor maps of a 4-bit cache: codes of K and V, their scales.
+// Tensor maps of a 4-bit cache's codes, K and V.
 struct Maps4 {
-  CUtensorMap t[4];
+  CUtensorMap t[2];
 };
 struct NoMaps {};
 template <int kKind>
 using Maps = std::conditional_t<kKind == kKindQ4, Maps4, NoMaps>;
 
 template <int kKind, bool kQBF16, int kDp, int kNr, int kForm>
-__global__ void __launch_bounds__(kThreads, Few<kKind, kDp, kNr>::kCtas)
+__global__ void __launch_bounds__(Few<kKind, kDp, kNr>::kThreads, Few<kKind, kDp, kNr>::kCtas)
 paged_few_kernel(const PagedAttnParams p, const __grid_constant__ Maps<kKind> maps) {
   constexpr bool kQ8 = kKind == kKindQ8, kQ4 = kKind == kKindQ4;
   constexpr bool kMmaBF16 = kKind == kKindBF16;
   constexpr float kDown = kBelow<kMmaBF16>, kOver = kLazy + kDown;
-  // 4 bits: where the results are fp16, P times a value's scale is rounded once, from 32
-  // bits; for bf16, whose own rounding is eight times as large, P and the product are.
-  constexpr bool kOnce = !kQBF16;
   constexpr int kRows = 8 * kNr;
   constexpr int kUnitBlocks = kWarps;                     // a unit: a block of each warp
   constexpr int kEl = kQ8 || kQ4 ? 1 : 2;                 // bytes of an element
@@ -263,12 +242,17 @@ paged_few_kernel(const PagedAttnParams p, const __grid_constant__ Maps<kKind> ma
   using L = Few<kKind, kDp, kNr>;
   constexpr int kPitch = L::kPitch, kRowB = L::kRowB, kStages = L::kStages, kKeys = L::kKeys;
   constexpr int kSubs = kKeys / 16;                       // 16 keys to a product
+  constexpr int kThreads = L::kThreads;
   constexpr int kChunks = kRowB / 16;                     // 16-byte vectors of a row
   extern __shared__ __align__(1024) uint8_t ring_s[];
   float (*const acc_s)[kRows * kPitch] = reinterpret_cast<float (*)[kRows * kPitch]>(ring_s);
-  __shared__ int64_t scan_s[kWarps];
+  __shared__ int64_t scan_s[kThreads / 32];
   __shared__ FewItem it;
-  __shared__ uint64_t full_s[kQ4 ? kWarps * kStages : 1];
+  // 4 bits: each warp's stages, filled and read; the first key of a stage's block
+  constexpr int kRings = kQ4 ? kWarps * kStages : 1;
+  __shared__ uint64_t full_s[kRings], empty_s[kRings];
+  __shared__ int key_s[kRings];
+  __shared__ volatile int abort_s;
   __shared__ float m_s[kWarps][kRows], l_s[kWarps][kRows];
 
   const PagedGeo& c = p.c;
@@ -304,7 +288,11 @@ paged_few_kernel(const PagedAttnParams p, const __grid_constant__ Maps<kKind> ma
       return;
     }
     if (tid == 0) {
-      for (int i = 0; i < kWarps * kStages; ++i) mbar_init(&full_s[i], 1);
+      abort_s = 0;
+      for (int i = 0; i < kRings; ++i) {
+        mbar_init(&full_s[i], 1 + 8);           // codes; the lanes that copy scales
+        mbar_init(&empty_s[i], 1);
+      }
       mbar_fence_init();
     }
   }
@@ -314,10 +302,16 @@ paged_few_kernel(const PagedAttnParams p, const __grid_constant__ Maps<kKind> ma
   const uint32_t mat_off = kDp == 128 ? k_at(lane & 7, lane >> 3)
                                       : k_at((lane & 7) + 8 * (lane >> 4), (lane >> 3) & 1);
   const uint32_t key_scales = 2 * kKeys * kRowB + g * L::kScaleB;
-  const uint32_t val_scales = 2 * kKeys * kRowB + 256 + (kOnce ? g : 2 * t) * L::kScaleB;
-  uint64_t* const full = full_s + (kQ4 ? warp * kStages : 0);
-  uint32_t parities = 0;                        // of the stages' next rounds
-  int stage4 = 0;                               // the next one to be read
+  const uint32_t val_scales = 2 * kKeys * kRowB + 256 + g * L::kScaleB;
+  int stage4 = 0;                               // the stage at hand and its round's parity
+  uint32_t parity4 = 0;
+  bool ok = true;
+  auto next_stage = [&] {
+    if (++stage4 == kStages) {
+      stage4 = 0;
+      parity4 ^= 1u;
+    }
+  };
   // ---- this CTA's range of units
   const int per_thread = (c.nseq + kThreads - 1) / kThreads;
   const int s_begin = min(c.nseq, tid * per_thread), s_end = min(c.nseq, s_begin + per_thread);
@@ -336,7 +330,7 @@ paged_few_kernel(const PagedAttnParams p, const __grid_constant__ Maps<kKind> ma
   __syncthreads();
   int64_t total = 0, before = 0;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
+  for (int w = 0; w < kThreads / 32; ++w) {
     if (w < warp) before += scan_s[w];
     total += scan_s[w];
   }
@@ -408,6 +402,79 @@ paged_few_kernel(const PagedAttnParams p, const __grid_constant__ Maps<kKind> ma
       // this lane's vector in a block's keys and values (bytes)
       const int64_t lane_off = (kvh * c.head_stride + lr * c.token_stride) * kEl + 16 * lc;
 
+      const int end_unit = first_unit + count;
+      if constexpr (kQ4) {
+        if (warp == kWarps) {
+          // ---- the copies of the other warps' blocks: lanes 8 w .. 8 w + 7 those of warp
+          // w, by 16 keys, which share a page: codes of K and V by a tensor copy each,
+          // their scales by 16 bytes a lane.  (By tensor copies as well they took longer
+          // than the codes: 128 us for the copies of 64 x 8520 keys alone, 103 without.)
+          // Pages that are not there, and 16 keys that no row sees, lie outside and read
+          // zeros.
+          const int w = lane >> 3, j8 = lane & 7, kv = j8 & 1, half = j8 >> 1;
+          uint8_t* const to = ring_s + w * kStages * L::kBlockB;
+          const uint32_t to_u = smem_u32(to) + L::kScales + 16 * j8;
+          const CUtensorMap* const map = &maps.t[kv];
+          const int64_t page_b = static_cast<int64_t>(c.Hkv) * c.page_size * L::kScaleB;
+          const int64_t head_b = static_cast<int64_t>(kvh) * c.page_size * L::kScaleB + 16 * j8;
+          int k0 = -1, page[kSubs], slot[kSubs];
+          auto locate4 = [&](int u) {           // a block's first key and its pages
+            const int vb = u * kWarps + w;
+            k0 = kKeys * (vb < sp.sink ? vb : vb - sp.sink + sp.from);
+            if (!(vb < sp.count && k0 <= p_hi && (k0 + kKeys - 1 >= lo || k0 < sinks))) k0 = -1;
+#pragma unroll
+            for (int h = 0; h < kSubs; ++h) {
+              const int kh = k0 + 16 * h;
+              page[h] = -2;
+              slot[h] = 0;
+              if (k0 >= 0 && kh <= p_hi && (kh + 15 >= lo || kh < sinks)) {
+                const int pn = page_of(c, kh);
+                page[h] = table[pn];
+                slot[h] = kh - pn * c.page_size;
+              }
+            }
+          };
+          locate4(first_unit);
+          for (int u = first_unit; u < end_unit; ++u) {
+            const int ring_at = w * kStages + stage4;
+            ok = __all_sync(kAll, mbar_wait(&empty_s[ring_at], parity4 ^ 1u, &abort_s, c.status,
+                                            p.timeout_ns));
+            if (!ok) break;
+            if (j8 == 0) {
+              key_s[ring_at] = k0;
+              if (k0 >= 0) mbar_expect_tx(&full_s[ring_at], 2 * kKeys * kRowB);
+              else mbar_arrive(&full_s[ring_at]);
+            }
+            __syncwarp();
+            if (k0 >= 0) {
+#pragma unroll
+              for (int h = 0; h < kSubs; ++h) {
+                const bool there =
+                    static_cast<uint32_t>(page[h]) < static_cast<uint32_t>(c.num_pages);
+                if (!there && page[h] != -2) atomicOr(c.status, kStatusBadPage);
+                if (half == h)
+                  tma_load_4d(to + stage4 * L::kBlockB + (kv * kKeys + 16 * h) * kRowB, map, 0,
+                              slot[h], kvh, there ? page[h] : static_cast<int>(c.num_pages),
+                              &full_s[ring_at]);
+                if (L::kScaleB == 8 || j8 < 4) {
+                  const int64_t at =
+                      there ? page[h] * page_b + head_b + slot[h] * L::kScaleB : 0;
+                  const uint32_t dst = to_u + stage4 * L::kBlockB + 128 * h;
+                  copy16(dst, reinterpret_cast<const uint8_t*>(c.k_groups) + at, there ? 16 : 0);
+                  copy16(dst + 256, reinterpret_cast<const uint8_t*>(c.v_groups) + at,
+                         there ? 16 : 0);
+                }
+              }
+            }
+            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];"
+                         :: "r"(smem_u32(&full_s[ring_at])) : "memory");
+            __syncwarp();
+            next_stage();
+            if (u + 1 < end_unit) locate4(u + 1);
+          }
+        }
+      }
+      if (!kQ4 || warp < kWarps) {
       // ---- the rows' queries, as the B operand of S^T
       uint32_t qw[kNr][kDp / 8];
       float qoff[kNr][kQ4 ? kDp / 32 : 1][2];             // 4 bits: -8 sum q of a group
@@ -524,42 +591,9 @@ paged_few_kernel(const PagedAttnParams p, const __grid_constant__ Maps<kKind> ma
       };
       auto seen = [&](int j) { return j <= p_hi && (j >= lo || j < sinks); };
       int next_key0 = -1, next_page = -1;
-      int next_slot = 0;
       auto locate = [&](int unit) {             // the table's entry, used a step later
         next_key0 = key_of(unit);
-        if constexpr (kQ4) {
-          // lanes 0-3 and 4-7 copy K, V, their scales of 16 keys each, which share a page
-          const int k0 = next_key0 + 16 * (lane >> 2);
-          if (lane < 8 && next_key0 >= 0) {
-            next_page = -2;                     // one that no row sees
-            if (k0 <= p_hi && (k0 + 15 >= lo || k0 < sinks)) {
-              next_page = table[page_of(c, k0)];
-              next_slot = k0 - page_of(c, k0) * c.page_size;
-            }
-          }
-        } else {
-          if (next_key0 >= 0) next_page = table[page_of(c, next_key0)];
-        }
-      };
-      // Four bits: tensor copies; pages that are not there lie outside and read zeros.
-      auto issue_q4 = [&](int stage) {
-        if constexpr (kQ4) {
-        if (next_key0 < 0) return;
-        if (lane == 0) mbar_expect_tx(&full[stage], 2 * kKeys * (kRowB + L::kScaleB));
-        __syncwarp();
-        if (lane < 8) {
-          if (static_cast<uint32_t>(next_page) >= static_cast<uint32_t>(c.num_pages)) {
-            if (next_page != -2) atomicOr(c.status, kStatusBadPage);
-            next_page = static_cast<int>(c.num_pages);
-          }
-          const int what = lane & 3, half = lane >> 2;    // K, V, scales of K, of V
-          const uint32_t at = what < 2 ? (what * kKeys + 16 * half) * kRowB
-                                       : L::kScales + (what - 2) * 256 + half * 128;
-          tma_load_4d(ring + stage * L::kBlockB + at, &maps.t[what],
-                      what < 2 ? 0 : next_slot * (kDp / 64), what < 2 ? next_slot : 0, kvh,
-                      next_page, &full[stage]);
-        }
-        }
+        if (next_key0 >= 0) next_page = table[page_of(c, next_key0)];
       };
       // Starts the copies of the located block into a stage; rows that no row of
       // the tile sees become zero (0 times what lies there could be NaN).
@@ -600,41 +634,45 @@ paged_few_kernel(const PagedAttnParams p, const __grid_constant__ Maps<kKind> ma
         asm volatile("cp.async.commit_group;" ::: "memory");
       };
 
-      const int end_unit = first_unit + count;
-      locate(first_unit);
-      int key_queue[kStages - 1];               // 4 bits: first keys of the blocks under way
+      if constexpr (!kQ4) {
+        locate(first_unit);
 #pragma unroll
-      for (int i = 0; i < kStages - 1; ++i) {
-        key_queue[i] = next_key0;
-        if constexpr (kQ4) issue_q4(wrapped<kStages>(stage4 + i));
-        else issue(i);
-        next_key0 = -1;
-        if (first_unit + i + 1 < end_unit) locate(first_unit + i + 1);
+        for (int i = 0; i < kStages - 1; ++i) {
+          issue(i);
+          next_key0 = -1;
+          if (first_unit + i + 1 < end_unit) locate(first_unit + i + 1);
+        }
       }
       int stage = 0;
       for (int u = first_unit; u < end_unit; ++u) {
-        if constexpr (!kQ4) asm volatile("cp.async.wait_group %0;" :: "n"(kStages - 2) : "memory");
-        __syncwarp();                           // every lane's copies; and the last stage is read
-        const int cur0 = kQ4 ? key_queue[0] : key_of(u);
-#pragma unroll
-        for (int i = 0; i < kStages - 1; ++i)
-          key_queue[i] = i + 2 < kStages ? key_queue[i + 1] : next_key0;
-        if constexpr (kQ4) issue_q4(stage4 == 0 ? kStages - 1 : stage4 - 1);
-        else issue(stage == 0 ? kStages - 1 : stage - 1);
-        next_key0 = -1;
-        if (u + kStages < end_unit) locate(u + kStages);
         const uint8_t* const block = ring + stage * L::kBlockB;
         const uint32_t base = ring_u + stage4 * L::kBlockB;
+        int cur0;
         if constexpr (kQ4) {
-          if (cur0 >= 0) {                      // a block that was asked for
-            mbar_wait(&full[stage4], (parities >> stage4) & 1, nullptr, c.status, p.timeout_ns);
-            parities ^= 1u << stage4;
-          }
-          stage4 = wrapped<kStages>(stage4 + 1);
+          const int at = warp * kStages + stage4;
+          ok = __all_sync(kAll, mbar_wait(&full_s[at], parity4, &abort_s, c.status, p.timeout_ns));
+          if (!ok) break;
+          cur0 = key_s[at];
+        } else {
+          asm volatile("cp.async.wait_group %0;" :: "n"(kStages - 2) : "memory");
+          __syncwarp();                         // every lane's copies; and the last stage is read
+          issue(stage == 0 ? kStages - 1 : stage - 1);
+          next_key0 = -1;
+          if (u + kStages < end_unit) locate(u + kStages);
+          stage = stage + 1 == kStages ? 0 : stage + 1;
+          cur0 = key_of(u);
         }
-        stage = stage + 1 == kStages ? 0 : stage + 1;
+        // a 4-bit block has been read
+        auto release = [&] {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&empty_s[warp * kStages + stage4]);
+          next_stage();
+        };
         // ---- S^T, in two chains of products
-        if (cur0 < 0) continue;
+        if (cur0 < 0) {
+          if constexpr (kQ4) release();
+          continue;
+        }
         float x[kSubs * kNr][4], x2[kNr][4];    // of the first 16 keys, then the next
 #pragma unroll
         for (int nr = 0; nr < kNr; ++nr)
@@ -707,21 +745,48 @@ paged_few_kernel(const PagedAttnParams p, const __grid_constant__ Maps<kKind> ma
           const bool full_block =
               cur0 + kKeys - 1 <= p_lo && (cur0 >= lo_hi || cur0 + kKeys - 1 < sinks);
           bool over = false;                    // a logit has outgrown its row's reference
+          if constexpr (kQ4) {
+            // (branches once for the block: a test per logit costs as much as the logits)
 #pragma unroll
-          for (int sn = 0; sn < kSubs * kNr; ++sn) {
-            const int nr = sn % kNr;
+            for (int sn = 0; sn < kSubs * kNr; ++sn)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) x[sn][e] *= rs[sn % kNr][e & 1];
+            if (!full_block) {
+#pragma unroll
+              for (int sn = 0; sn < kSubs * kNr; ++sn)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const int j = cur0 + 16 * (sn / kNr) + g + 8 * (e >> 1);
+                  const int pos = rpos[sn % kNr][e & 1];
+                  if (!(j <= pos && (p.window <= 0 || j > pos - p.window || j < sinks)))
+                    x[sn][e] = -INFINITY;
+                }
+            }
+#pragma unroll
+            for (int nr = 0; nr < kNr; ++nr)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                float v = fmaxf(x[nr][i], x[nr][i + 2]);
+                if constexpr (kSubs == 2)
+                  v = fmaxf(v, fmaxf(x[kNr + nr][i], x[kNr + nr][i + 2]));
+                over |= v > m[nr][i] + kOver;
+              }
+          }
+#pragma unroll
+          for (int sn = 0; sn < (kQ4 ? 0 : kNr); ++sn) {
+            const int nr = sn;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              float v = (kQ4 ? x[sn][e] : x[sn][e] + x2[nr][e]) * rs[nr][e & 1];
+              float v = (x[nr][e] + x2[nr][e]) * rs[nr][e & 1];
               if constexpr (kQ8) v *= ks[e >> 1];
               if (!full_block) {
-                const int j = cur0 + 16 * (sn / kNr) + g + 8 * (e >> 1);
+                const int j = cur0 + g + 8 * (e >> 1);
                 const int pos = rpos[nr][e & 1];
                 const bool see =
                     j <= pos && (p.window <= 0 || j > pos - p.window || j < sinks);
                 v = see ? v : -INFINITY;
               }
-              x[sn][e] = v;
+              x[nr][e] = v;
               over |= v > m[nr][e & 1] + kOver;  // with m = -inf: any logit but -inf
             }
           }
@@ -773,38 +838,16 @@ paged_few_kernel(const PagedAttnParams p, const __grid_constant__ Maps<kKind> ma
                 }
               uint32_t vl[kG], vh[kG];
               load_codes<true, kG>(vl, vh, base + mat_off + (kKeys + 16 * sub) * kRowB);
-              // P times the scales: of keys g and g + 8 before P is turned round, or of
-              // 2t, 2t + 1 and those 8 further behind it
+              // P times the scales of keys g and g + 8, rounded once, before P is turned round
               float sa[kG], sb[kG];
-              uint32_t s2[2][kG], pt[kNr][2];
-              if constexpr (kOnce) {
-                row_scales<kG>(base + val_scales + 128 * sub, sa);
-                row_scales<kG>(base + val_scales + 128 * sub + 8 * L::kScaleB, sb);
-              } else {
-                pair_scales<kG>(base + val_scales + 128 * sub, s2[0]);
-                pair_scales<kG>(base + val_scales + 128 * sub + 8 * L::kScaleB, s2[1]);
-#pragma unroll
-                for (int nr = 0; nr < kNr; ++nr) {
-                  pt[nr][0] = transpose8x8(pack2<false>(e4[nr][0], e4[nr][1]));
-                  pt[nr][1] = transpose8x8(pack2<false>(e4[nr][2], e4[nr][3]));
-                }
-              }
+              row_scales<kG>(base + val_scales + 128 * sub, sa);
+              row_scales<kG>(base + val_scales + 128 * sub + 8 * L::kScaleB, sb);
               if (!full_block) {                // scales that no row sees may be NaN
-                const int j = cur0 + 16 * sub;
-                if constexpr (kOnce) {
+                const int j = cur0 + 16 * sub + g;
 #pragma unroll
-                  for (int i = 0; i < kG; ++i) {
-                    if (!seen(j + g)) sa[i] = 0.0f;
-                    if (!seen(j + g + 8)) sb[i] = 0.0f;
-                  }
-                } else {
-#pragma unroll
-                  for (int h = 0; h < 2; ++h) {
-                    const uint32_t mask = (seen(j + 8 * h + 2 * t) ? 0xFFFFu : 0u) |
-                                          (seen(j + 8 * h + 2 * t + 1) ? 0xFFFF0000u : 0u);
-#pragma unroll
-                    for (int i = 0; i < kG; ++i) s2[h][i] &= mask;
-                  }
+                for (int i = 0; i < kG; ++i) {
+                  if (!seen(j)) sa[i] = 0.0f;
+                  if (!seen(j + 8)) sb[i] = 0.0f;
                 }
               }
 #pragma unroll
@@ -814,19 +857,16 @@ paged_few_kernel(const PagedAttnParams p, const __grid_constant__ Maps<kKind> ma
                 nibbles_to_half(vh[i], n[1]);
 #pragma unroll
                 for (int nr = 0; nr < kNr; ++nr) {
-                  uint32_t b0, b1;
-                  if constexpr (kOnce) {
-                    b0 = transpose8x8(pack2<false>(e4[nr][0] * sa[i], e4[nr][1] * sa[i]));
-                    b1 = transpose8x8(pack2<false>(e4[nr][2] * sb[i], e4[nr][3] * sb[i]));
-                  } else {
-                    b0 = mul_half2(pt[nr][0], s2[0][i]);
-                    b1 = mul_half2(pt[nr][1], s2[1][i]);
-                  }
+                  const uint32_t b0 =
+                      transpose8x8(pack2<false>(e4[nr][0] * sa[i], e4[nr][1] * sa[i]));
+                  const uint32_t b1 =
+                      transpose8x8(pack2<false>(e4[nr][2] * sb[i], e4[nr][3] * sb[i]));
                   mma<false>(o[2 * i][nr], n[0][0], n[0][1], n[1][0], n[1][1], b0, b1);
                   mma<false>(o[2 * i + 1][nr], n[0][2], n[0][3], n[1][2], n[1][3], b0, b1);
                 }
               }
             }
+            release();
             continue;
           }
           uint32_t pb[kNr][2];
@@ -900,7 +940,7 @@ paged_few_kernel(const PagedAttnParams p, const __grid_constant__ Maps<kKind> ma
         }
       }
       if constexpr (!kQ4) asm volatile("cp.async.wait_all;" ::: "memory");
-      __syncthreads();                          // the rings become the merge buffer
+      block_barrier<kQ4>(kThreads);             // the rings become the merge buffer
 
       // ---- join the warps
 #pragma unroll
@@ -928,6 +968,19 @@ paged_few_kernel(const PagedAttnParams p, const __grid_constant__ Maps<kKind> ma
             // 4 bits: tile j holds channels 4 g + 2 (j % 2) + hi of group j / 2
             row[(kQ4 ? 2 * j + hi : kMt * hi + j) * 8 + g] = o[j][nr][e];
           }
+      } else {
+        block_barrier<kQ4>(kThreads);
+        if constexpr (kQ4) {
+          if (abort_s) {                        // no copy may be in flight when the CTA exits
+            for (int i = 1; i <= kStages; ++i) {
+              const int st = stage4 - i;        // below 0: in the round before
+              mbar_wait(&full_s[(lane >> 3) * kStages + (st < 0 ? st + kStages : st)],
+                        st < 0 ? parity4 ^ 1u : parity4, nullptr, c.status, p.timeout_ns);
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
+          }
+        }
+      }
       __syncthreads();
       const bool alone = it.first == 0 && it.count == it.per;
       const int which = it.first == 0 ? 1 : 0;
@@ -1055,6 +1108,7 @@ paged_few_kernel(const PagedAttnParams p, const __grid_constant__ Maps<kKind> ma
       }
       if constexpr (kQ4) fence_proxy_async_smem();      // the ring again
       __syncthreads();
+      if (kQ4 && abort_s) break;                // a wait ran out: reported, and no more of it
       if (tid == 0) {
         it.cur += it.count;
         it.off += it.count;
@@ -1144,7 +1198,7 @@ cudaError_t launch_few(const PagedAttnParams& p, int sms, cudaStream_t st) {
   if (per == 0) {
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
     if (e == cudaSuccess)
-      e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kern, kThreads, L::kSmem);
+      e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kern, L::kThreads, L::kSmem);
     if (e != cudaSuccess) return e;
     per = per < 1 ? 1 : per > 8 ? 8 : per;
     resident[dev].store(per, std::memory_order_relaxed);
@@ -1160,12 +1214,12 @@ cudaError_t launch_few(const PagedAttnParams& p, int sms, cudaStream_t st) {
   prm.team = 1;
   Maps<kKind> maps{};
   if constexpr (kKind == kKindQ4) {
-    if (!paged_maps4(p.c, 16, maps.t)) return cudaErrorInvalidValue;
-    // Heads whose rows lie side by side are read at the same time, by a team of CTAs in
-    // step: a row of 64 bytes alone is half a line of the L2, and its other half came
-    // from memory again.  (Rows that lie apart have neighbours of their own.)
-    if (p.c.head_stride == 16 * ((p.c.D + 31) / 32))
-      while (prm.team < 8 && p.c.Hkv % (2 * prm.team) == 0) prm.team *= 2;
+    if (!paged_maps4(p.c, 16, maps.t, nullptr)) return cudaErrorInvalidValue;
+    // Neighbouring heads are read at the same time, by a team of CTAs in step: a row of
+    // 64 bytes alone is half a line of the L2, and its other half came from memory again
+    // (NHD, 64 x 8520 keys: 1090 MB read instead of 631, 196 us instead of 182); where
+    // heads lie apart their scales are neighbours all the same.
+    while (prm.team < 8 && p.c.Hkv % (2 * prm.team) == 0) prm.team *= 2;
     ctas = ctas / prm.team * prm.team;
     if (ctas == 0) ctas = prm.team;
   }
@@ -1176,7 +1230,7 @@ cudaError_t launch_few(const PagedAttnParams& p, int sms, cudaStream_t st) {
   // and 45, 4: 44 and 40, 8: 50 and 48, 128: 351 and 353; over 2000 keys the second
   // kernel is 1 to 2 us ahead up to 64 of them, at the price of its launch.)
   prm.join_inside = items >= (ctas + kJoinInside - 1) / kJoinInside;
-  kern<<<ctas, kThreads, L::kSmem, st>>>(prm, maps);
+  kern<<<ctas, L::kThreads, L::kSmem, st>>>(prm, maps);
   note_launch();
   e = cudaGetLastError();
   if (e != cudaSuccess || prm.join_inside) return e;

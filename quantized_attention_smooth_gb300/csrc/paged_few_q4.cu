@@ -5,7 +5,7 @@
 
 namespace sage {
 
-bool paged_maps4(const PagedGeo& c, int rows, CUtensorMap* maps) {
+bool paged_maps4(const PagedGeo& c, int rows, CUtensorMap* codes, CUtensorMap* scales) {
   const uint64_t row = 16 * ((static_cast<uint64_t>(c.D) + 31) / 32);     // bytes of a row
   const uint64_t words = static_cast<uint64_t>(c.Dp) / 64;                // of a row's scales
   const uint64_t slots = static_cast<uint64_t>(c.page_size), heads = static_cast<uint64_t>(c.Hkv),
@@ -22,12 +22,14 @@ bool paged_maps4(const PagedGeo& c, int rows, CUtensorMap* maps) {
   // rows of 64 or 32 bytes, turned so that eight of one vector hit every bank once
   const CUtensorMapSwizzle turn =
       c.Dp == 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B;
-  return encode_tiled(&maps[0], CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, c.k, dims, strides, box, turn) &&
-         encode_tiled(&maps[1], CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, c.v, dims, strides, box, turn) &&
-         encode_tiled(&maps[2], CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, c.k_groups, sdims, sstrides, sbox,
-                      CU_TENSOR_MAP_SWIZZLE_NONE) &&
-         encode_tiled(&maps[3], CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, c.v_groups, sdims, sstrides, sbox,
-                      CU_TENSOR_MAP_SWIZZLE_NONE);
+  if (!encode_tiled(&codes[0], CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, c.k, dims, strides, box, turn) ||
+      !encode_tiled(&codes[1], CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, c.v, dims, strides, box, turn))
+    return false;
+  return scales == nullptr ||
+         (encode_tiled(&scales[0], CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, c.k_groups, sdims, sstrides,
+                       sbox, CU_TENSOR_MAP_SWIZZLE_NONE) &&
+          encode_tiled(&scales[1], CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, c.v_groups, sdims, sstrides,
+                       sbox, CU_TENSOR_MAP_SWIZZLE_NONE));
 }
 
 cudaError_t launch_paged_few_q4(const PagedAttnParams& p, bool bf16, int sms, cudaStream_t st) {

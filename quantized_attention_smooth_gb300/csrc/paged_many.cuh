@@ -1459,7 +1459,7 @@ cudaError_t launch_many(const PagedAttnParams& p, int sms, cudaStream_t st) {
   prm.tensor_copies = (kKind != kKindQ8 && kKind != kKindQ4) || (page_boxes(c) && c.wide);
   if (kKind == kKindQ4 && prm.tensor_copies) {
     CUtensorMap maps[4];
-    if (!paged_maps4(c, c.page_size < kKeys ? c.page_size : kKeys, maps))
+    if (!paged_maps4(c, c.page_size < kKeys ? c.page_size : kKeys, maps, maps + 2))
       return cudaErrorInvalidValue;
     mk = maps[0];
     mv = maps[1];

@@ -36,6 +36,7 @@
 #include "sage_device.cuh"
 #include "sage_kernels.h"
 #include "sage_paged.h"
+#include "sage_paged_device.cuh"
 
 namespace sage {
 namespace {
@@ -183,19 +184,23 @@ __device__ __forceinline__ void place_tokens(const RowsParams& p, int64_t t0, in
 // several axes take a pair's position from the axis that it follows.
 __device__ __forceinline__ void turn_table(const RowsParams& p, int64_t t0, int nt,
                                            const int64_t* pos_s, float2* cs) {
-  const int half = p.R / 2;
-  for (int i = threadIdx.x; i < nt * half; i += kRowThreads) {
-    const int t = i / half, f = i - t * half;
+  // A thread keeps its pair, whose fraction of a turn takes doubles: a pair and a token
+  // each time, the FP64 pipe would be what a long CTA waits for.
+  const int half = p.R / 2, rows = kRowThreads / half;
+  const int f = threadIdx.x % half;
+  if (threadIdx.x >= rows * half) return;
+  const double turns = p.inv_freq[f] * 0.15915494309189533577;       // 1 / (2 pi)
+  const uint64_t frac = __double2ull_rn((turns - floor(turns)) * 18446744073709551616.0);
+  const int axis =
+      p.naxes > 0 && p.axis_of != nullptr ? min(static_cast<int>(p.axis_of[f]), p.naxes - 1) : 0;
+  for (int t = threadIdx.x / half; t < nt; t += rows) {
     int64_t pos;
     if (p.naxes > 0) {
-      const int axis = p.axis_of != nullptr ? min(static_cast<int>(p.axis_of[f]), p.naxes - 1) : 0;
       const int64_t at = axis * p.axis_stride + t0 + t;
       pos = p.pos64 ? static_cast<const int64_t*>(p.pos)[at] : static_cast<const int32_t*>(p.pos)[at];
     } else {
       pos = pos_s[t];
     }
-    const double turns = p.inv_freq[f] * 0.15915494309189533577;     // 1 / (2 pi)
-    const uint64_t frac = __double2ull_rn((turns - floor(turns)) * 18446744073709551616.0);
     const uint64_t a = frac * static_cast<uint64_t>(pos) + (1ull << 31);
     float sn, cn;
     sincospif(static_cast<float>(static_cast<int32_t>(a >> 32)) * 4.656612873077392578125e-10f,
@@ -623,11 +628,11 @@ __device__ __forceinline__ void pair_pass(const RowsParams& p, const Tokens& tk,
 // values and keep it for the CTA's tokens, with the means or factors in registers;
 // heads of any size fill the lanes (80 channels: 10 of 12).  In the half layout a
 // lane reads its partner channels as well (they come out of the L1) and turns its own.
-template <bool kBF16>
+template <bool kBF16, bool kTurn>
 __device__ __forceinline__ void quad_pass(const RowsParams& p, const Tokens& tk, const float2* cs,
                                           int64_t t0, int nt) {
   const PagedGeo& c = p.c;
-  constexpr int kQuads = kRowThreads / 4, kAhead = 4;
+  constexpr int kQuads = kRowThreads / 4, kAhead = kTurn ? 2 : 4;
   const int quad = threadIdx.x >> 2, ql = threadIdx.x & 3;
   const int groups = (p.D + 31) / 32, padded = c.Dp / 32, units = 2 * p.Hkv * groups;
   const int at_once = min(units, kQuads), step = kQuads / at_once;
@@ -640,71 +645,78 @@ __device__ __forceinline__ void quad_pass(const RowsParams& p, const Tokens& tk,
     const bool val = row >= p.Hkv;
     const int h = val ? row - p.Hkv : row, c0 = 32 * grp + 8 * ql;
     const bool live = mine && c0 < p.D;
-    const bool turn = p.inv_freq != nullptr && !val && c0 < p.R;
-    const bool apart = turn && !p.interleaved;
+    const bool turn = kTurn && !val && c0 < p.R, apart = turn && !p.interleaved;
     const int mate = c0 < half ? half : -half;          // from a channel to its partner
-    float chan[8];
+    // x times mul plus add, one of them 1 or 0: one rounding
+    float mul[8], add[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      chan[e] = live ? (val ? c.v_scale : c.k_mean)[h * c.Dp + c0 + e] : 0.0f;
-      if (val) chan[e] = chan[e] > 0.0f ? __fdiv_rn(1.0f, 64.0f * chan[e]) : 0.0f;
+      const float v = live ? (val ? c.v_scale : c.k_mean)[h * c.Dp + c0 + e] : 0.0f;
+      mul[e] = !val ? 1.0f : v > 0.0f ? __fdiv_rn(1.0f, 64.0f * v) : 0.0f;
+      add[e] = val ? 0.0f : -v;
     }
+    const float most = val ? kMostV : kMostK;
     const int64_t stride = val ? p.v_tok : p.k_tok;
-    const uint16_t* const src = (val ? p.v + h * p.v_head : p.k + h * p.k_head) + t0 * stride + c0;
+    const uint16_t* src = (val ? p.v + h * p.v_head : p.k + h * p.k_head) +
+                          (t0 + first) * stride + c0;
+    const int64_t ahead = step * stride;
     uint8_t* const codes = (val ? c.v : c.k) + h * c.head_stride + c0 / 2;
-    __half* const scales = reinterpret_cast<__half*>(val ? c.v_groups : c.k_groups) + grp;
+    __half* const scales = reinterpret_cast<__half*>(val ? c.v_groups : c.k_groups) + grp +
+                           static_cast<int64_t>(h) * c.page_size * padded;
     for (int rb = 0; rb < rounds; rb += kAhead) {
       uint4 raw[kAhead], other[kAhead];
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
-        const int t = first + (rb + k) * step;
-        raw[k] = other[k] = make_uint4(0, 0, 0, 0);
-        if (live && t < nt) {
-          raw[k] = *reinterpret_cast<const uint4*>(src + t * stride);
-          if (apart) other[k] = *reinterpret_cast<const uint4*>(src + t * stride + mate);
+        raw[k] = make_uint4(0, 0, 0, 0);
+        if (kTurn) other[k] = make_uint4(0, 0, 0, 0);
+        if (live && first + (rb + k) * step < nt) {
+          raw[k] = *reinterpret_cast<const uint4*>(src);
+          if (apart) other[k] = *reinterpret_cast<const uint4*>(src + mate);
         }
+        src += ahead;
       }
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
-        if (rb + k >= rounds) break;                    // the same for every lane
         const int t = first + (rb + k) * step;
         const int at = t < nt ? t : 0;
         float x[8];
         unpack8<kBF16>(raw[k], x);
-        if (apart) {
-          float y[8];
-          unpack8<kBF16>(other[k], y);
-          const float2* const a = cs + at * 64 + (c0 < half ? c0 : c0 - half);
+        if constexpr (kTurn) {
+          if (apart) {
+            float y[8];
+            unpack8<kBF16>(other[k], y);
+            const float2* const a = cs + at * 64 + (c0 < half ? c0 : c0 - half);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float2 w = a[e];
-            x[e] = c0 < half ? x[e] * w.x - y[e] * w.y : x[e] * w.x + y[e] * w.y;
-          }
-        } else if (turn) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (c0 + 2 * i < p.R) {
-              const float2 w = cs[at * 64 + c0 / 2 + i];
-              const float x1 = x[2 * i], x2 = x[2 * i + 1];
-              x[2 * i] = x1 * w.x - x2 * w.y;
-              x[2 * i + 1] = x2 * w.x + x1 * w.y;
+            for (int e = 0; e < 8; ++e) {
+              const float2 w = a[e];
+              x[e] = c0 < half ? x[e] * w.x - y[e] * w.y : x[e] * w.x + y[e] * w.y;
             }
+          } else if (turn) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (c0 + 2 * i < p.R) {
+                const float2 w = cs[at * 64 + c0 / 2 + i];
+                const float x1 = x[2 * i], x2 = x[2 * i + 1];
+                x[2 * i] = x1 * w.x - x2 * w.y;
+                x[2 * i + 1] = x2 * w.x + x1 * w.y;
+              }
+          }
         }
         float top = 0.0f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          x[e] = val ? __fmul_rn(x[e], chan[e]) : __fsub_rn(x[e], chan[e]);
+          x[e] = __fmaf_rn(x[e], mul[e], add[e]);
           top = fmaxf(top, fabsf(x[e]));
         }
         top = fmaxf(top, __shfl_xor_sync(kAll, top, 1));
         top = fmaxf(top, __shfl_xor_sync(kAll, top, 2));
-        const __half scale = group_scale(top, val ? kMostV : kMostK);
+        const __half scale = group_scale(top, most);
         const float s = __half2float(scale);
-        const float inv = s > 0.0f ? __fdiv_rn(1.0f, s) : 0.0f;
+        const float inv = s > 0.0f ? __frcp_rn(s) : 0.0f;
         if (mine && t < nt && tk.page[at] >= 0) {
           *reinterpret_cast<uint32_t*>(codes + tk.slot[at]) = pack_nibbles(x, top, inv);
           if (ql == 0) {
-            __half* const to = scales + (tk.scale[at] + static_cast<int64_t>(h) * c.page_size) * padded;
+            __half* const to = scales + tk.scale[at] * padded;
             *to = scale;
             if (grp == groups - 1)                      // groups behind D
               for (int e = groups; e < padded; ++e) to[e - grp] = __ushort_as_half(0);
@@ -715,21 +727,21 @@ __device__ __forceinline__ void quad_pass(const RowsParams& p, const Tokens& tk,
   }
 }
 
-template <bool kBF16>
-__global__ void __launch_bounds__(kRowThreads, 3)
+template <bool kBF16, bool kTurn>
+__global__ void __launch_bounds__(kRowThreads, kTurn ? 3 : 4)
 quad_rows_kernel(const RowsParams p) {
-  __shared__ float2 cs[kMaxPairToks * 64];
+  __shared__ float2 cs[kTurn ? kMaxPairToks * 64 : 1];
   __shared__ Tokens tk;
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * p.toks;
   const int nt = static_cast<int>(min(static_cast<int64_t>(p.toks), p.T - t0));
   place_tokens(p, t0, nt, tk.pos, tk.page, tk.slot, tk.scale);
   __syncthreads();
-  if (p.inv_freq != nullptr) {
+  if constexpr (kTurn) {
     turn_table(p, t0, nt, tk.pos, cs);
     __syncthreads();
+    if (p.Hq > 0) pair_pass<3, 0, kBF16>(p, tk, cs, t0, nt);
   }
-  if (p.Hq > 0) pair_pass<3, 0, kBF16>(p, tk, cs, t0, nt);
-  quad_pass<kBF16>(p, tk, cs, t0, nt);
+  quad_pass<kBF16, kTurn>(p, tk, cs, t0, nt);
 }
 
 template <int kMode, bool kBF16>
@@ -763,8 +775,10 @@ cudaError_t launch_pairs(const RowsParams& p0, int sms, cudaStream_t st) {
   while (p.toks < kMaxPairToks && p.T / (2 * p.toks) >= 4 * sms) p.toks *= 2;
   const int64_t ctas = (p.T + p.toks - 1) / p.toks;
   if (ctas > 0x7FFFFFFF) return cudaErrorInvalidValue;
-  if constexpr (kMode == 3)
-    quad_rows_kernel<kBF16><<<static_cast<unsigned>(ctas), kRowThreads, 0, st>>>(p);
+  if (kMode == 3 && p.inv_freq == nullptr)      // q comes with a rotation only
+    quad_rows_kernel<kBF16, false><<<static_cast<unsigned>(ctas), kRowThreads, 0, st>>>(p);
+  else if constexpr (kMode == 3)
+    quad_rows_kernel<kBF16, true><<<static_cast<unsigned>(ctas), kRowThreads, 0, st>>>(p);
   else
     pair_rows_kernel<kMode, kBF16><<<static_cast<unsigned>(ctas), kRowThreads, 0, st>>>(p);
   note_launch();
@@ -826,15 +840,15 @@ gather_kernel(const RowsParams p) {
     const int h2 = u / vecs, c0 = 8 * (u - h2 * vecs);
     const bool val = h2 >= p.Hkv;
     const int h = val ? h2 - p.Hkv : h2;
-    float chan[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) chan[e] = 0.0f;
+    // the number times mul plus add, one of them 1 or 0: one rounding
+    float mul[8], add[8];
     if constexpr (kKind == kKindQ8 || kKind == kKindQ4) {
-      const float4* src = reinterpret_cast<const float4*>((val ? c.v_scale : c.k_mean) + h * c.Dp + c0);
-      const float4 a = src[0], b = src[1];
-      const float unit = kKind == kKindQ4 && val ? 64.0f : 1.0f;
-      chan[0] = a.x * unit; chan[1] = a.y * unit; chan[2] = a.z * unit; chan[3] = a.w * unit;
-      chan[4] = b.x * unit; chan[5] = b.y * unit; chan[6] = b.z * unit; chan[7] = b.w * unit;
+      const float* src = (val ? c.v_scale : c.k_mean) + h * c.Dp + c0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        mul[e] = !val ? 1.0f : kKind == kKindQ4 ? 64.0f * src[e] : src[e];
+        add[e] = val ? 0.0f : src[e];
+      }
     }
     const uint8_t* const codes = val ? c.v : c.k;
     uint16_t* const out = (val ? p.q_out : p.k_out) + h * (val ? p.qo_head : p.ko_head);
@@ -871,19 +885,24 @@ gather_kernel(const RowsParams p) {
         uint4 put = raw[k];
         if constexpr (kKind == kKindQ8 || kKind == kKindQ4) {
           float x[8];
+          if constexpr (kKind == kKindQ4) {
+            uint32_t n[4];                      // channels 0 and 4, 1 and 5, ...
+            nibbles_to_half(raw[k].x, n);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            float n;
-            if constexpr (kKind == kKindQ4) {
-              n = static_cast<float>(static_cast<int>((raw[k].x >> (4 * e)) & 15u) - 8);
-            } else {
-              const uint32_t b = ((e < 4 ? raw[k].x : raw[k].y) >> (8 * (e & 3))) & 0xFFu;
-              n = val ? e4m3_value(b) : static_cast<float>(static_cast<int8_t>(b));
+            for (int e = 0; e < 4; ++e) {
+              const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&n[e]));
+              x[e] = f.x;
+              x[e + 4] = f.y;
             }
-            // one rounding each
-            const float y = __fmul_rn(n, scale[k]);
-            x[e] = val ? __fmul_rn(y, chan[e]) : __fadd_rn(y, chan[e]);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const uint32_t b = ((e < 4 ? raw[k].x : raw[k].y) >> (8 * (e & 3))) & 0xFFu;
+              x[e] = val ? e4m3_value(b) : static_cast<float>(static_cast<int8_t>(b));
+            }
           }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] = __fmaf_rn(__fmul_rn(x[e], scale[k]), mul[e], add[e]);
           put = page_s[t] < 0 ? make_uint4(0, 0, 0, 0) : pack8<kBF16>(x);
         }
         store8(out + (t0 + t) * out_tok, c0, p.D, p.vec, put);

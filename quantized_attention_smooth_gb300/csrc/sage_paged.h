@@ -113,8 +113,9 @@ struct PagedAttnParams {
 };
 
 cudaError_t launch_paged_few(const PagedAttnParams& p, bool bf16, int sms, cudaStream_t st);
-// Tensor maps of a 4-bit cache in boxes of `rows` slots: codes of K and V, scales of K and V.
-bool paged_maps4(const PagedGeo& c, int rows, CUtensorMap* maps);
+// Tensor maps of a 4-bit cache in boxes of `rows` slots: codes of K and V, and their scales
+// (NULL: none).
+bool paged_maps4(const PagedGeo& c, int rows, CUtensorMap* codes, CUtensorMap* scales);
 cudaError_t launch_paged_few_q4(const PagedAttnParams& p, bool bf16, int sms, cudaStream_t st);
 size_t paged_few_bytes();
 int paged_few_rows(int Dp);   // rows (new tokens x group) that one of its tiles holds
