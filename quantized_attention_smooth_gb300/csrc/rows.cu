@@ -624,103 +624,102 @@ __device__ __forceinline__ void pair_pass(const RowsParams& p, const Tokens& tk,
   }
 }
 
-// ---- Q4, many tokens: four lanes are a group of 32 channels of one head's keys or
-// values and keep it for the CTA's tokens, with the means or factors in registers;
-// heads of any size fill the lanes (80 channels: 10 of 12).  In the half layout a
-// lane reads its partner channels as well (they come out of the L1) and turns its own.
-template <bool kBF16, bool kTurn>
-__device__ __forceinline__ void quad_pass(const RowsParams& p, const Tokens& tk, const float2* cs,
-                                          int64_t t0, int nt) {
+// ---- Q4, many tokens: two lanes are a group of 32 channels of one head's keys or
+// values and keep it for the CTA's tokens, with the means or factors in registers.  In
+// the half layout a lane reads its partner channels as well (they come out of the L1) and
+// turns its own.  Arithmetic bounds this: what a group costs besides its channels (the
+// largest across lanes, the scale, places and stores) is shared by 16 channels a lane;
+// with 8, four lanes a group, the rows of 76000 tokens x 16 heads x 80 took 211 us.
+template <bool kBF16, bool kTurn, bool kVal>
+__device__ __forceinline__ void group_pass(const RowsParams& p, const Tokens& tk, const float2* cs,
+                                           int64_t t0, int nt) {
   const PagedGeo& c = p.c;
-  constexpr int kQuads = kRowThreads / 4, kAhead = kTurn ? 2 : 4;
-  const int quad = threadIdx.x >> 2, ql = threadIdx.x & 3;
-  const int groups = (p.D + 31) / 32, padded = c.Dp / 32, units = 2 * p.Hkv * groups;
-  const int at_once = min(units, kQuads), step = kQuads / at_once;
-  const int first = quad / at_once, rounds = (nt + step - 1) / step;
+  constexpr int kPairs = kRowThreads / 2;
+  constexpr bool kRot = kTurn && !kVal;
+  const int pair = threadIdx.x >> 1, side = threadIdx.x & 1;
+  const int groups = (p.D + 31) / 32, padded = c.Dp / 32, units = p.Hkv * groups;
+  const int at_once = min(units, kPairs), step = kPairs / at_once;
+  const int first = pair / at_once, rounds = (nt + step - 1) / step;
   const int half = p.R / 2;
+  const int64_t stride = kVal ? p.v_tok : p.k_tok, ahead = step * stride;
   for (int ub = 0; ub < units; ub += at_once) {
-    const int u = ub + quad - first * at_once;
+    const int u = ub + pair - first * at_once;
     const bool mine = u < units && first < step;
-    const int row = u / groups, grp = u - row * groups;
-    const bool val = row >= p.Hkv;
-    const int h = val ? row - p.Hkv : row, c0 = 32 * grp + 8 * ql;
-    const bool live = mine && c0 < p.D;
-    const bool turn = kTurn && !val && c0 < p.R, apart = turn && !p.interleaved;
-    const int mate = c0 < half ? half : -half;          // from a channel to its partner
-    // x times mul plus add, one of them 1 or 0: one rounding
-    float mul[8], add[8];
+    const int h = u / groups, grp = u - h * groups, c0 = 32 * grp + 16 * side;
+    const int left = mine ? p.D - c0 : 0;               // channels from c0 on
+    float chan[16];                                     // means, or 1 / (64 scale)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float v = live ? (val ? c.v_scale : c.k_mean)[h * c.Dp + c0 + e] : 0.0f;
-      mul[e] = !val ? 1.0f : v > 0.0f ? __fdiv_rn(1.0f, 64.0f * v) : 0.0f;
-      add[e] = val ? 0.0f : -v;
+    for (int e = 0; e < 16; ++e) {
+      chan[e] = e < left ? (kVal ? c.v_scale : c.k_mean)[h * c.Dp + c0 + e] : 0.0f;
+      if (kVal) chan[e] = chan[e] > 0.0f ? __fdiv_rn(1.0f, 64.0f * chan[e]) : 0.0f;
     }
-    const float most = val ? kMostV : kMostK;
-    const int64_t stride = val ? p.v_tok : p.k_tok;
-    const uint16_t* src = (val ? p.v + h * p.v_head : p.k + h * p.k_head) +
+    const uint16_t* src = (kVal ? p.v + h * p.v_head : p.k + h * p.k_head) +
                           (t0 + first) * stride + c0;
-    const int64_t ahead = step * stride;
-    uint8_t* const codes = (val ? c.v : c.k) + h * c.head_stride + c0 / 2;
-    __half* const scales = reinterpret_cast<__half*>(val ? c.v_groups : c.k_groups) + grp +
+    uint8_t* const codes = (kVal ? c.v : c.k) + h * c.head_stride + c0 / 2;
+    __half* const scales = reinterpret_cast<__half*>(kVal ? c.v_groups : c.k_groups) + grp +
                            static_cast<int64_t>(h) * c.page_size * padded;
-    for (int rb = 0; rb < rounds; rb += kAhead) {
-      uint4 raw[kAhead], other[kAhead];
-#pragma unroll
-      for (int k = 0; k < kAhead; ++k) {
-        raw[k] = make_uint4(0, 0, 0, 0);
-        if (kTurn) other[k] = make_uint4(0, 0, 0, 0);
-        if (live && first + (rb + k) * step < nt) {
-          raw[k] = *reinterpret_cast<const uint4*>(src);
-          if (apart) other[k] = *reinterpret_cast<const uint4*>(src + mate);
-        }
-        src += ahead;
+    uint4 next[2];
+    auto load = [&](int t) {
+      next[0] = next[1] = make_uint4(0, 0, 0, 0);
+      if (t < nt) {
+        if (left > 0) next[0] = *reinterpret_cast<const uint4*>(src);
+        if (left > 8) next[1] = *reinterpret_cast<const uint4*>(src + 8);
       }
+    };
+    load(first);
+    for (int r = 0; r < rounds; ++r) {
+      const int t = first + r * step, at = t < nt ? t : 0;
+      float x[2][8];
+      unpack8<kBF16>(next[0], x[0]);
+      unpack8<kBF16>(next[1], x[1]);
+      if constexpr (kRot) {
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k) {
-        const int t = first + (rb + k) * step;
-        const int at = t < nt ? t : 0;
-        float x[8];
-        unpack8<kBF16>(raw[k], x);
-        if constexpr (kTurn) {
-          if (apart) {
+        for (int v = 0; v < 2; ++v) {
+          const int ch = c0 + 8 * v;
+          if (ch >= p.R || 8 * v >= left || t >= nt) continue;
+          if (!p.interleaved) {
+            const bool low = ch < half;
             float y[8];
-            unpack8<kBF16>(other[k], y);
-            const float2* const a = cs + at * 64 + (c0 < half ? c0 : c0 - half);
+            unpack8<kBF16>(*reinterpret_cast<const uint4*>(src + 8 * v + (low ? half : -half)), y);
+            const float2* const a = cs + at * 64 + (low ? ch : ch - half);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
               const float2 w = a[e];
-              x[e] = c0 < half ? x[e] * w.x - y[e] * w.y : x[e] * w.x + y[e] * w.y;
+              x[v][e] = low ? x[v][e] * w.x - y[e] * w.y : x[v][e] * w.x + y[e] * w.y;
             }
-          } else if (turn) {
+          } else {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              if (c0 + 2 * i < p.R) {
-                const float2 w = cs[at * 64 + c0 / 2 + i];
-                const float x1 = x[2 * i], x2 = x[2 * i + 1];
-                x[2 * i] = x1 * w.x - x2 * w.y;
-                x[2 * i + 1] = x2 * w.x + x1 * w.y;
+              if (ch + 2 * i < p.R) {
+                const float2 w = cs[at * 64 + ch / 2 + i];
+                const float x1 = x[v][2 * i], x2 = x[v][2 * i + 1];
+                x[v][2 * i] = x1 * w.x - x2 * w.y;
+                x[v][2 * i + 1] = x2 * w.x + x1 * w.y;
               }
           }
         }
-        float top = 0.0f;
+      }
+      src += ahead;
+      load(t + step);                                   // the next row's loads run ahead
+      float top = 0.0f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          x[e] = __fmaf_rn(x[e], mul[e], add[e]);
-          top = fmaxf(top, fabsf(x[e]));
-        }
-        top = fmaxf(top, __shfl_xor_sync(kAll, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(kAll, top, 2));
-        const __half scale = group_scale(top, most);
-        const float s = __half2float(scale);
-        const float inv = s > 0.0f ? __frcp_rn(s) : 0.0f;
-        if (mine && t < nt && tk.page[at] >= 0) {
-          *reinterpret_cast<uint32_t*>(codes + tk.slot[at]) = pack_nibbles(x, top, inv);
-          if (ql == 0) {
-            __half* const to = scales + tk.scale[at] * padded;
-            *to = scale;
-            if (grp == groups - 1)                      // groups behind D
-              for (int e = groups; e < padded; ++e) to[e - grp] = __ushort_as_half(0);
-          }
+      for (int e = 0; e < 16; ++e) {
+        float& y = x[e / 8][e % 8];
+        y = kVal ? __fmul_rn(y, chan[e]) : __fsub_rn(y, chan[e]);
+        top = fmaxf(top, fabsf(y));
+      }
+      top = fmaxf(top, __shfl_xor_sync(kAll, top, 1));
+      const __half scale = group_scale(top, kVal ? kMostV : kMostK);
+      const float s = __half2float(scale);
+      const float inv = s > 0.0f ? __frcp_rn(s) : 0.0f;
+      if (mine && t < nt && tk.page[at] >= 0) {
+        *reinterpret_cast<uint2*>(codes + tk.slot[at]) =
+            make_uint2(pack_nibbles(x[0], top, inv), pack_nibbles(x[1], top, inv));
+        if (side == 0) {
+          __half* const to = scales + tk.scale[at] * padded;
+          *to = scale;
+          if (grp == groups - 1)                        // groups behind D
+            for (int e = groups; e < padded; ++e) to[e - grp] = __ushort_as_half(0);
         }
       }
     }
@@ -729,7 +728,7 @@ __device__ __forceinline__ void quad_pass(const RowsParams& p, const Tokens& tk,
 
 template <bool kBF16, bool kTurn>
 __global__ void __launch_bounds__(kRowThreads, kTurn ? 3 : 4)
-quad_rows_kernel(const RowsParams p) {
+group_rows_kernel(const RowsParams p) {
   __shared__ float2 cs[kTurn ? kMaxPairToks * 64 : 1];
   __shared__ Tokens tk;
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * p.toks;
@@ -741,7 +740,8 @@ quad_rows_kernel(const RowsParams p) {
     __syncthreads();
     if (p.Hq > 0) pair_pass<3, 0, kBF16>(p, tk, cs, t0, nt);
   }
-  quad_pass<kBF16, kTurn>(p, tk, cs, t0, nt);
+  group_pass<kBF16, kTurn, false>(p, tk, cs, t0, nt);
+  group_pass<kBF16, kTurn, true>(p, tk, cs, t0, nt);
 }
 
 template <int kMode, bool kBF16>
@@ -776,9 +776,9 @@ cudaError_t launch_pairs(const RowsParams& p0, int sms, cudaStream_t st) {
   const int64_t ctas = (p.T + p.toks - 1) / p.toks;
   if (ctas > 0x7FFFFFFF) return cudaErrorInvalidValue;
   if (kMode == 3 && p.inv_freq == nullptr)      // q comes with a rotation only
-    quad_rows_kernel<kBF16, false><<<static_cast<unsigned>(ctas), kRowThreads, 0, st>>>(p);
+    group_rows_kernel<kBF16, false><<<static_cast<unsigned>(ctas), kRowThreads, 0, st>>>(p);
   else if constexpr (kMode == 3)
-    quad_rows_kernel<kBF16, true><<<static_cast<unsigned>(ctas), kRowThreads, 0, st>>>(p);
+    group_rows_kernel<kBF16, true><<<static_cast<unsigned>(ctas), kRowThreads, 0, st>>>(p);
   else
     pair_rows_kernel<kMode, kBF16><<<static_cast<unsigned>(ctas), kRowThreads, 0, st>>>(p);
   note_launch();
@@ -821,7 +821,7 @@ cudaError_t launch_mode(const RowsParams& p0, bool bf16, int sms, cudaStream_t s
 constexpr int kGatherToks = 32;
 
 template <int kKind, bool kBF16>
-__global__ void __launch_bounds__(kRowThreads)
+__global__ void __launch_bounds__(kRowThreads, 4)
 gather_kernel(const RowsParams p) {
   __shared__ int64_t pos_s[kGatherToks], slot_s[kGatherToks], scale_s[kGatherToks];
   __shared__ int page_s[kGatherToks];
@@ -840,15 +840,11 @@ gather_kernel(const RowsParams p) {
     const int h2 = u / vecs, c0 = 8 * (u - h2 * vecs);
     const bool val = h2 >= p.Hkv;
     const int h = val ? h2 - p.Hkv : h2;
-    // the number times mul plus add, one of them 1 or 0: one rounding
-    float mul[8], add[8];
+    float chan[8];                              // K's means, V's factors
     if constexpr (kKind == kKindQ8 || kKind == kKindQ4) {
       const float* src = (val ? c.v_scale : c.k_mean) + h * c.Dp + c0;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        mul[e] = !val ? 1.0f : kKind == kKindQ4 ? 64.0f * src[e] : src[e];
-        add[e] = val ? 0.0f : src[e];
-      }
+      for (int e = 0; e < 8; ++e) chan[e] = kKind == kKindQ4 && val ? 64.0f * src[e] : src[e];
     }
     const uint8_t* const codes = val ? c.v : c.k;
     uint16_t* const out = (val ? p.q_out : p.k_out) + h * (val ? p.qo_head : p.ko_head);
@@ -901,8 +897,14 @@ gather_kernel(const RowsParams p) {
               x[e] = val ? e4m3_value(b) : static_cast<float>(static_cast<int8_t>(b));
             }
           }
+          // one rounding each (with 4 bits the first product is exact)
+          if (val) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] = __fmaf_rn(__fmul_rn(x[e], scale[k]), mul[e], add[e]);
+            for (int e = 0; e < 8; ++e) x[e] = __fmul_rn(__fmul_rn(x[e], scale[k]), chan[e]);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = __fadd_rn(__fmul_rn(x[e], scale[k]), chan[e]);
+          }
           put = page_s[t] < 0 ? make_uint4(0, 0, 0, 0) : pack8<kBF16>(x);
         }
         store8(out + (t0 + t) * out_tok, c0, p.D, p.vec, put);
