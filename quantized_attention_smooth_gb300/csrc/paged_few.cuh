@@ -114,10 +114,10 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
   return d;
 }
 
-// A barrier of the whole block that two places of the code may reach.
-template <bool kTwoPlaces>
-__device__ __forceinline__ void block_barrier(int threads) {
-  if constexpr (kTwoPlaces) asm volatile("barrier.sync 1, %0;" :: "r"(threads) : "memory");
+// A barrier of the warps that take the keys (4 bits: a fifth one is elsewhere).
+template <bool kSome>
+__device__ __forceinline__ void workers_barrier() {
+  if constexpr (kSome) asm volatile("bar.sync 1, %0;" :: "n"(32 * kWarps) : "memory");
   else __syncthreads();
 }
 
@@ -204,14 +204,17 @@ struct Few {
   static constexpr int kKeys = kKind == kKindQ4 && kNr * kDp <= 128 ? 32 : 16;
   static constexpr int kBlockB =                                      // K, V, scales
       2 * kKeys * kRowB + (kKind == kKindQ8 ? 64 : kKind == kKindQ4 ? 512 : 0);
-  static constexpr int kStages = kKind == kKindQ4 ? 4 : kRowB == 64 ? 4 : 3;
+  static constexpr int kStages = kKind == kKindQ4 ? (kDp * kKeys == 4096 ? 3 : 4)
+                                                     : kRowB == 64 ? 4 : 3;
   // where a 4-bit block's scales lie, of keys and 256 bytes on of values: 16 rows on 128
   // bytes, as a tensor copy wants them
   static constexpr int kScales = 2 * kKeys * kRowB;
   static constexpr int kPitch = kDp + 4;
   static constexpr int kRing = kWarps * kStages * kBlockB;
   static constexpr int kMerge = kWarps * 8 * kNr * kPitch * 4;
-  static constexpr int kSmem = kRing > kMerge ? kRing : kMerge;
+  // (4 bits: beside the rings, which already take the next item's blocks)
+  static constexpr int kMergeAt = kKind == kKindQ4 ? kRing : 0;
+  static constexpr int kSmem = kMergeAt + (kRing - kMergeAt > kMerge ? kRing - kMergeAt : kMerge);
   static constexpr int kCtas = kRowB == 256 || kNr > 2 ? 2
                                : kNr == 2 ? (kDp == 128 ? 2 : 3)
                                : kKind == kKindQ4 ? 3 : 4;
@@ -245,14 +248,14 @@ paged_few_kernel(const PagedAttnParams p, const __grid_constant__ Maps<kKind> ma
   constexpr int kThreads = L::kThreads;
   constexpr int kChunks = kRowB / 16;                     // 16-byte vectors of a row
   extern __shared__ __align__(1024) uint8_t ring_s[];
-  float (*const acc_s)[kRows * kPitch] = reinterpret_cast<float (*)[kRows * kPitch]>(ring_s);
+  float (*const acc_s)[kRows * kPitch] = reinterpret_cast<float (*)[kRows * kPitch]>(ring_s + L::kMergeAt);
   __shared__ int64_t scan_s[kThreads / 32];
-  __shared__ FewItem it;
+  __shared__ FewItem it_s[kQ4 ? 2 : 1];         // the item at hand (4 bits: and the next one)
   // 4 bits: each warp's stages, filled and read; the first key of a stage's block
   constexpr int kRings = kQ4 ? kWarps * kStages : 1;
   __shared__ uint64_t full_s[kRings], empty_s[kRings];
   __shared__ int key_s[kRings];
-  __shared__ volatile int abort_s;
+  __shared__ volatile int abort_s, stop_s[2];
   __shared__ float m_s[kWarps][kRows], l_s[kWarps][kRows];
 
   const PagedGeo& c = p.c;
@@ -351,6 +354,7 @@ paged_few_kernel(const PagedAttnParams p, const __grid_constant__ Maps<kKind> ma
         if (off < w) break;
         off -= w;
       }
+      FewItem& it = it_s[0];
       it.s = s;
       it.off = off;
       it.cur = u0;
@@ -359,8 +363,8 @@ paged_few_kernel(const PagedAttnParams p, const __grid_constant__ Maps<kKind> ma
       it.busy = static_cast<int>(busy);
     }
     __syncthreads();
-    while (true) {
-      if (tid == 0) {
+    // an item from where its CTA stands in its range (count 0: none left), by one thread
+    auto seek = [&](FewItem& it) {
         it.count = 0;
         while (it.cur < it.last && it.s < c.nseq) {
           int start, n, len;
@@ -385,10 +389,108 @@ paged_few_kernel(const PagedAttnParams p, const __grid_constant__ Maps<kKind> ma
           it.span = span_of<L::kKeys>(len - n, len - 1, p.window, p.sinks);
           break;
         }
+    };
+    // 4 bits: the fifth warp's copies of units from..to-1 of an item: lanes 8 w .. 8 w + 7
+    // serve warp w, by 16 keys, which share a page: codes of K and V by a tensor copy each,
+    // their scales by 16 bytes a lane.  (By tensor copies as well they took longer than
+    // the codes: 128 us for the copies of 64 x 8520 keys alone, 103 without.)  Pages that
+    // are not there, and 16 keys that no row sees, lie outside and read zeros.
+    auto send = [&](const FewItem& it, int from, int to) {
+      if constexpr (kQ4) {
+        const int w = lane >> 3, j8 = lane & 7, kv = j8 & 1, half = j8 >> 1;
+        const Span sp = it.span;
+        const int row0 = it.tile * kRows, kvh = it.head;
+        const int p_hi = it.base + (min(row0 + kRows, it.rows) - 1) / p.group;
+        const int sinks = p.window > 0 ? p.sinks : 0;
+        const int lo = p.window > 0 ? max(0, it.base + row0 / p.group - p.window + 1) : 0;
+        const int32_t* const table = c.table + it.s * c.table_stride;
+        uint8_t* const dst = ring_s + w * kStages * L::kBlockB;
+        const uint32_t dst_u = smem_u32(dst) + L::kScales + 16 * j8;
+        const CUtensorMap* const map = &maps.t[kv];
+        const int64_t page_b = static_cast<int64_t>(c.Hkv) * c.page_size * L::kScaleB;
+        const int64_t head_b = static_cast<int64_t>(kvh) * c.page_size * L::kScaleB + 16 * j8;
+        int k0 = -1, page[kSubs], slot[kSubs];
+        auto locate = [&](int u) {              // a block's first key and its pages
+          const int vb = u * kWarps + w;
+          k0 = kKeys * (vb < sp.sink ? vb : vb - sp.sink + sp.from);
+          if (!(vb < sp.count && k0 <= p_hi && (k0 + kKeys - 1 >= lo || k0 < sinks))) k0 = -1;
+#pragma unroll
+          for (int h = 0; h < kSubs; ++h) {
+            const int kh = k0 + 16 * h;
+            page[h] = -2;
+            slot[h] = 0;
+            if (k0 >= 0 && kh <= p_hi && (kh + 15 >= lo || kh < sinks)) {
+              const int pn = page_of(c, kh);
+              page[h] = table[pn];
+              slot[h] = kh - pn * c.page_size;
+            }
+          }
+        };
+        if (from < to) locate(from);
+        for (int u = from; ok && u < to; ++u) {
+          const int ring_at = w * kStages + stage4;
+          ok = __all_sync(kAll, mbar_wait(&empty_s[ring_at], parity4 ^ 1u, &abort_s, c.status,
+                                          p.timeout_ns));
+          if (!ok) break;
+          if (j8 == 0) {
+            key_s[ring_at] = k0;
+            if (k0 >= 0) mbar_expect_tx(&full_s[ring_at], 2 * kKeys * kRowB);
+            else mbar_arrive(&full_s[ring_at]);
+          }
+          __syncwarp();
+          if (k0 >= 0) {
+#pragma unroll
+            for (int h = 0; h < kSubs; ++h) {
+              const bool there =
+                  static_cast<uint32_t>(page[h]) < static_cast<uint32_t>(c.num_pages);
+              if (!there && page[h] != -2) atomicOr(c.status, kStatusBadPage);
+              if (half == h)
+                tma_load_4d(dst + stage4 * L::kBlockB + (kv * kKeys + 16 * h) * kRowB, map, 0,
+                            slot[h], kvh, there ? page[h] : static_cast<int>(c.num_pages),
+                            &full_s[ring_at]);
+              if (L::kScaleB == 8 || j8 < 4) {
+                const int64_t at = there ? page[h] * page_b + head_b + slot[h] * L::kScaleB : 0;
+                const uint32_t to_u = dst_u + stage4 * L::kBlockB + 128 * h;
+                copy16(to_u, reinterpret_cast<const uint8_t*>(c.k_groups) + at, there ? 16 : 0);
+                copy16(to_u + 256, reinterpret_cast<const uint8_t*>(c.v_groups) + at,
+                       there ? 16 : 0);
+              }
+            }
+          }
+          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];"
+                       :: "r"(smem_u32(&full_s[ring_at])) : "memory");
+          __syncwarp();
+          next_stage();
+          if (u + 1 < to) locate(u + 1);
+        }
       }
-      __syncthreads();
+    };
+    if (kQ4 && tid == 32 * kWarps) seek(it_s[0]);
+    int nth = 0, sent = 0;                      // items begun; blocks of the item sent ahead
+    while (true) {
+      FewItem& it = it_s[kQ4 ? nth & 1 : 0];
+      if (!kQ4 && tid == 0) seek(it);
+      if (kQ4 && tid == 0) stop_s[nth & 1] = abort_s;
+      __syncthreads();                          // 4 bits: the warps are through with the last item
       const int count = it.count, first_unit = it.first;
-      if (count == 0) break;
+      if (count == 0 || (kQ4 && stop_s[nth & 1])) break;
+      ++nth;
+      if (kQ4 && warp == kWarps) {
+        // the rest of this item's blocks, then the first ones of the next item, which
+        // are on their way while the other warps join their parts of this one
+        send(it, first_unit + sent, first_unit + count);
+        FewItem& next = it_s[nth & 1];
+        if (lane == 0) {
+          next = it;
+          next.cur += count;
+          next.off += count;
+          seek(next);
+        }
+        __syncwarp();
+        sent = min(next.count, kStages);
+        send(next, next.first, next.first + sent);
+        continue;
+      }
       const int row0 = it.tile * kRows;
       const int kvh = it.head, s = it.s;
       const Span sp = it.span;
@@ -403,78 +505,6 @@ paged_few_kernel(const PagedAttnParams p, const __grid_constant__ Maps<kKind> ma
       const int64_t lane_off = (kvh * c.head_stride + lr * c.token_stride) * kEl + 16 * lc;
 
       const int end_unit = first_unit + count;
-      if constexpr (kQ4) {
-        if (warp == kWarps) {
-          // ---- the copies of the other warps' blocks: lanes 8 w .. 8 w + 7 those of warp
-          // w, by 16 keys, which share a page: codes of K and V by a tensor copy each,
-          // their scales by 16 bytes a lane.  (By tensor copies as well they took longer
-          // than the codes: 128 us for the copies of 64 x 8520 keys alone, 103 without.)
-          // Pages that are not there, and 16 keys that no row sees, lie outside and read
-          // zeros.
-          const int w = lane >> 3, j8 = lane & 7, kv = j8 & 1, half = j8 >> 1;
-          uint8_t* const to = ring_s + w * kStages * L::kBlockB;
-          const uint32_t to_u = smem_u32(to) + L::kScales + 16 * j8;
-          const CUtensorMap* const map = &maps.t[kv];
-          const int64_t page_b = static_cast<int64_t>(c.Hkv) * c.page_size * L::kScaleB;
-          const int64_t head_b = static_cast<int64_t>(kvh) * c.page_size * L::kScaleB + 16 * j8;
-          int k0 = -1, page[kSubs], slot[kSubs];
-          auto locate4 = [&](int u) {           // a block's first key and its pages
-            const int vb = u * kWarps + w;
-            k0 = kKeys * (vb < sp.sink ? vb : vb - sp.sink + sp.from);
-            if (!(vb < sp.count && k0 <= p_hi && (k0 + kKeys - 1 >= lo || k0 < sinks))) k0 = -1;
-#pragma unroll
-            for (int h = 0; h < kSubs; ++h) {
-              const int kh = k0 + 16 * h;
-              page[h] = -2;
-              slot[h] = 0;
-              if (k0 >= 0 && kh <= p_hi && (kh + 15 >= lo || kh < sinks)) {
-                const int pn = page_of(c, kh);
-                page[h] = table[pn];
-                slot[h] = kh - pn * c.page_size;
-              }
-            }
-          };
-          locate4(first_unit);
-          for (int u = first_unit; u < end_unit; ++u) {
-            const int ring_at = w * kStages + stage4;
-            ok = __all_sync(kAll, mbar_wait(&empty_s[ring_at], parity4 ^ 1u, &abort_s, c.status,
-                                            p.timeout_ns));
-            if (!ok) break;
-            if (j8 == 0) {
-              key_s[ring_at] = k0;
-              if (k0 >= 0) mbar_expect_tx(&full_s[ring_at], 2 * kKeys * kRowB);
-              else mbar_arrive(&full_s[ring_at]);
-            }
-            __syncwarp();
-            if (k0 >= 0) {
-#pragma unroll
-              for (int h = 0; h < kSubs; ++h) {
-                const bool there =
-                    static_cast<uint32_t>(page[h]) < static_cast<uint32_t>(c.num_pages);
-                if (!there && page[h] != -2) atomicOr(c.status, kStatusBadPage);
-                if (half == h)
-                  tma_load_4d(to + stage4 * L::kBlockB + (kv * kKeys + 16 * h) * kRowB, map, 0,
-                              slot[h], kvh, there ? page[h] : static_cast<int>(c.num_pages),
-                              &full_s[ring_at]);
-                if (L::kScaleB == 8 || j8 < 4) {
-                  const int64_t at =
-                      there ? page[h] * page_b + head_b + slot[h] * L::kScaleB : 0;
-                  const uint32_t dst = to_u + stage4 * L::kBlockB + 128 * h;
-                  copy16(dst, reinterpret_cast<const uint8_t*>(c.k_groups) + at, there ? 16 : 0);
-                  copy16(dst + 256, reinterpret_cast<const uint8_t*>(c.v_groups) + at,
-                         there ? 16 : 0);
-                }
-              }
-            }
-            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];"
-                         :: "r"(smem_u32(&full_s[ring_at])) : "memory");
-            __syncwarp();
-            next_stage();
-            if (u + 1 < end_unit) locate4(u + 1);
-          }
-        }
-      }
-      if (!kQ4 || warp < kWarps) {
       // ---- the rows' queries, as the B operand of S^T
       uint32_t qw[kNr][kDp / 8];
       float qoff[kNr][kQ4 ? kDp / 32 : 1][2];             // 4 bits: -8 sum q of a group
@@ -940,7 +970,7 @@ paged_few_kernel(const PagedAttnParams p, const __grid_constant__ Maps<kKind> ma
         }
       }
       if constexpr (!kQ4) asm volatile("cp.async.wait_all;" ::: "memory");
-      block_barrier<kQ4>(kThreads);             // the rings become the merge buffer
+      workers_barrier<kQ4>();                   // the rings become the merge buffer
 
       // ---- join the warps
 #pragma unroll
@@ -968,20 +998,7 @@ paged_few_kernel(const PagedAttnParams p, const __grid_constant__ Maps<kKind> ma
             // 4 bits: tile j holds channels 4 g + 2 (j % 2) + hi of group j / 2
             row[(kQ4 ? 2 * j + hi : kMt * hi + j) * 8 + g] = o[j][nr][e];
           }
-      } else {
-        block_barrier<kQ4>(kThreads);
-        if constexpr (kQ4) {
-          if (abort_s) {                        // no copy may be in flight when the CTA exits
-            for (int i = 1; i <= kStages; ++i) {
-              const int st = stage4 - i;        // below 0: in the round before
-              mbar_wait(&full_s[(lane >> 3) * kStages + (st < 0 ? st + kStages : st)],
-                        st < 0 ? parity4 ^ 1u : parity4, nullptr, c.status, p.timeout_ns);
-            }
-            asm volatile("cp.async.wait_all;" ::: "memory");
-          }
-        }
-      }
-      __syncthreads();
+      workers_barrier<kQ4>();
       const bool alone = it.first == 0 && it.count == it.per;
       const int which = it.first == 0 ? 1 : 0;
       uint8_t* part = part_at(p.parts, cta, which);
@@ -1019,7 +1036,7 @@ paged_few_kernel(const PagedAttnParams p, const __grid_constant__ Maps<kKind> ma
           p.lse[tok * p.Hq + h] = sum > 0.0f ? (top + log2f(sum)) * 0.69314718055994530942f
                                              : -INFINITY;
       };
-      for (int i = tid; i < kRows * (kDp / 4); i += kThreads) {
+      for (int i = tid; i < kRows * (kDp / 4); i += 32 * kWarps) {
         const int r = i / (kDp / 4), ch = 4 * (i % (kDp / 4));
         // where channel ch stands: tile j, half hi and lane g of the products
         const int cj = kQ8 && kDp == 128 ? ch % 8 : kDp == 128 ? ch % 8 : ch % 4;
@@ -1052,26 +1069,26 @@ paged_few_kernel(const PagedAttnParams p, const __grid_constant__ Maps<kKind> ma
       if (!alone && p.join_inside) {
         // The CTA that finishes an item's last part joins them all, in their order.
         __threadfence();
-        __syncthreads();
+        workers_barrier<kQ4>();
         if (tid == 0) {
           const uint32_t arrived = atomicAdd(&p.arrivals[it.first_cta], 1u) + 1u;
           it.joins = arrived == static_cast<uint32_t>(it.parts);
           if (it.joins) p.arrivals[it.first_cta] = 0;     // for the next call
           __threadfence();
         }
-        __syncthreads();
+        workers_barrier<kQ4>();
         if (it.joins) {
           // the parts' maxima and sums through shared memory (as many as fit)
           constexpr int kFit = kWarps * kRows * kPitch / (2 * kRows);
           float* const ml = &acc_s[0][0];
           const int parts = it.parts, fit = min(parts, kFit);
-          for (int i = tid; i < fit * kRows; i += kThreads) {
+          for (int i = tid; i < fit * kRows; i += 32 * kWarps) {
             const float* f = part_floats(p.parts, it.first_cta + i / kRows * team, i < kRows) + i % kRows;
             ml[i] = __ldcg(f);
             ml[kFit * kRows + i] = __ldcg(f + kMaxRows);
           }
-          __syncthreads();
-          for (int i = tid; i < kRows * (kDp / 4); i += kThreads) {
+          workers_barrier<kQ4>();
+          for (int i = tid; i < kRows * (kDp / 4); i += 32 * kWarps) {
             const int r = i / (kDp / 4), ch = 4 * (i % (kDp / 4));
             if (it.tile * kRows + r >= it.rows) break;    // later ones are later rows
             auto max_of = [&](int j) {
@@ -1106,13 +1123,21 @@ paged_few_kernel(const PagedAttnParams p, const __grid_constant__ Maps<kKind> ma
           }
         }
       }
-      if constexpr (kQ4) fence_proxy_async_smem();      // the ring again
-      __syncthreads();
-      if (kQ4 && abort_s) break;                // a wait ran out: reported, and no more of it
-      if (tid == 0) {
-        it.cur += it.count;
-        it.off += it.count;
+      if constexpr (!kQ4) {
+        __syncthreads();
+        if (tid == 0) {
+          it.cur += it.count;
+          it.off += it.count;
+        }
       }
+    }
+    if (kQ4 && warp == kWarps && abort_s) {     // no copy may be in flight when the CTA exits
+      for (int i = 1; i <= kStages; ++i) {
+        const int st = stage4 - i;              // below 0: in the round before
+        mbar_wait(&full_s[(lane >> 3) * kStages + (st < 0 ? st + kStages : st)],
+                  st < 0 ? parity4 ^ 1u : parity4, nullptr, c.status, p.timeout_ns);
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
     }
   }
   if (tid < 2 && !used[tid])
