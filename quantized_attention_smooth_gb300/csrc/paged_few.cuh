@@ -673,44 +673,16 @@ paged_few_kernel(const PagedAttnParams p, const __grid_constant__ Maps<kKind> ma
           if (first_unit + i + 1 < end_unit) locate(first_unit + i + 1);
         }
       }
-      int stage = 0;
-      for (int u = first_unit; u < end_unit; ++u) {
-        const uint8_t* const block = ring + stage * L::kBlockB;
-        const uint32_t base = ring_u + stage4 * L::kBlockB;
-        int cur0;
-        if constexpr (kQ4) {
-          const int at = warp * kStages + stage4;
+      if constexpr (kQ4) {
+        constexpr int kG = kDp / 32, kX = kSubs * kNr;
+        // waits for the block in a stage; its first key (-1: nothing that a row sees)
+        auto take = [&](int at) {
           ok = __all_sync(kAll, mbar_wait(&full_s[at], parity4, &abort_s, c.status, p.timeout_ns));
-          if (!ok) break;
-          cur0 = key_s[at];
-        } else {
-          asm volatile("cp.async.wait_group %0;" :: "n"(kStages - 2) : "memory");
-          __syncwarp();                         // every lane's copies; and the last stage is read
-          issue(stage == 0 ? kStages - 1 : stage - 1);
-          next_key0 = -1;
-          if (u + kStages < end_unit) locate(u + kStages);
-          stage = stage + 1 == kStages ? 0 : stage + 1;
-          cur0 = key_of(u);
-        }
-        // a 4-bit block has been read
-        auto release = [&] {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&empty_s[warp * kStages + stage4]);
-          next_stage();
+          return ok ? key_s[at] : -1;
         };
-        // ---- S^T, in two chains of products
-        if (cur0 < 0) {
-          if constexpr (kQ4) release();
-          continue;
-        }
-        float x[kSubs * kNr][4], x2[kNr][4];    // of the first 16 keys, then the next
-#pragma unroll
-        for (int nr = 0; nr < kNr; ++nr)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) x[nr][e] = x2[nr][e] = 0.0f;
-        if constexpr (kQ4) {
+        // ---- S^T of a block, times its rows' factors
+        auto logits = [&](uint32_t base, float (&x)[kX][4]) {
           // lane: word t of a group of keys g and g + 8
-          constexpr int kG = kDp / 32;
 #pragma unroll
           for (int sub = 0; sub < kSubs; ++sub) {
             uint32_t wa[kG], wb[kG];
@@ -741,9 +713,143 @@ paged_few_kernel(const PagedAttnParams p, const __grid_constant__ Maps<kKind> ma
               }
             }
           }
-        }
 #pragma unroll
-        for (int v = 0; v < (kQ4 ? 0 : kKw / 4); ++v) {
+          for (int sn = 0; sn < kX; ++sn)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[sn][e] *= rs[sn % kNr][e & 1];
+        };
+        // ---- masks, running maximum and sum, O^T
+        auto weigh = [&](uint32_t base, float (&x)[kX][4], int cur0) {
+          // (branches once for the block: a test per logit costs as much as the logits)
+          const bool full_block =
+              cur0 + kKeys - 1 <= p_lo && (cur0 >= lo_hi || cur0 + kKeys - 1 < sinks);
+          if (!full_block) {
+#pragma unroll
+            for (int sn = 0; sn < kX; ++sn)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int j = cur0 + 16 * (sn / kNr) + g + 8 * (e >> 1);
+                const int pos = rpos[sn % kNr][e & 1];
+                if (!(j <= pos && (p.window <= 0 || j > pos - p.window || j < sinks)))
+                  x[sn][e] = -INFINITY;
+              }
+          }
+          bool over = false;                    // a logit has outgrown its row's reference
+          float top[kNr][2];
+#pragma unroll
+          for (int nr = 0; nr < kNr; ++nr)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              top[nr][i] = fmaxf(x[nr][i], x[nr][i + 2]);
+              if constexpr (kSubs == 2)
+                top[nr][i] = fmaxf(top[nr][i], fmaxf(x[kNr + nr][i], x[kNr + nr][i + 2]));
+              over |= top[nr][i] > m[nr][i] + kOver;    // with m = -inf: any logit but -inf
+            }
+          if (__any_sync(kAll, over)) {
+            // Rare after the first block: references move with the maximum, O and l
+            // follow.
+            float alpha[kNr][2];
+#pragma unroll
+            for (int nr = 0; nr < kNr; ++nr)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                float v = top[nr][i];
+                v = fmaxf(v, __shfl_xor_sync(kAll, v, 4));
+                v = fmaxf(v, __shfl_xor_sync(kAll, v, 8));
+                v = fmaxf(v, __shfl_xor_sync(kAll, v, 16));
+                const float next = v > m[nr][i] + kOver ? v - kDown : m[nr][i];
+                alpha[nr][i] = next == m[nr][i] ? 1.0f : fast_exp2(m[nr][i] - next);
+                m[nr][i] = next;
+                l[nr][i] *= alpha[nr][i];
+              }
+#pragma unroll
+            for (int j = 0; j < kMt; ++j)
+#pragma unroll
+              for (int nr = 0; nr < kNr; ++nr)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[j][nr][e] *= alpha[nr][e & 1];
+          }
+          // lane: channels 4 g .. 4 g + 3 of each group, of keys 2t and 2t + 1 (lo), and
+          // of those 8 further (hi); a value's scale goes into P, by the group
+          float safe[kNr][2];
+#pragma unroll
+          for (int nr = 0; nr < kNr; ++nr)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) safe[nr][i] = m[nr][i] == -INFINITY ? 0.0f : m[nr][i];
+#pragma unroll
+          for (int sub = 0; sub < kSubs; ++sub) {
+            float e4[kNr][4];
+#pragma unroll
+            for (int nr = 0; nr < kNr; ++nr)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                e4[nr][e] = fast_exp2(x[sub * kNr + nr][e] - safe[nr][e & 1]);
+                l[nr][e & 1] += e4[nr][e];
+              }
+            uint32_t vl[kG], vh[kG];
+            load_codes<true, kG>(vl, vh, base + mat_off + (kKeys + 16 * sub) * kRowB);
+            // P times the scales of keys g and g + 8, rounded once, before P is turned round
+            float sa[kG], sb[kG];
+            row_scales<kG>(base + val_scales + 128 * sub, sa);
+            row_scales<kG>(base + val_scales + 128 * sub + 8 * L::kScaleB, sb);
+            if (!full_block) {                // scales that no row sees may be NaN
+              const int j = cur0 + 16 * sub + g;
+#pragma unroll
+              for (int i = 0; i < kG; ++i) {
+                if (!seen(j)) sa[i] = 0.0f;
+                if (!seen(j + 8)) sb[i] = 0.0f;
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < kG; ++i) {
+              uint32_t n[2][4];               // the four channels, as numbers -8..7
+              nibbles_to_half(vl[i], n[0]);
+              nibbles_to_half(vh[i], n[1]);
+#pragma unroll
+              for (int nr = 0; nr < kNr; ++nr) {
+                const uint32_t b0 =
+                    transpose8x8(pack2<false>(e4[nr][0] * sa[i], e4[nr][1] * sa[i]));
+                const uint32_t b1 =
+                    transpose8x8(pack2<false>(e4[nr][2] * sb[i], e4[nr][3] * sb[i]));
+                mma<false>(o[2 * i][nr], n[0][0], n[0][1], n[1][0], n[1][1], b0, b1);
+                mma<false>(o[2 * i + 1][nr], n[0][2], n[0][3], n[1][2], n[1][3], b0, b1);
+              }
+            }
+          }
+        };
+        for (int u = first_unit; ok && u < end_unit; ++u) {
+          const uint32_t base = ring_u + stage4 * L::kBlockB;
+          const int at = warp * kStages + stage4;
+          const int cur0 = take(at);
+          if (cur0 >= 0) {
+            float x[kX][4];
+            logits(base, x);
+            weigh(base, x, cur0);
+          }
+          __syncwarp();                         // the block has been read
+          if (lane == 0) mbar_arrive(&empty_s[at]);
+          next_stage();
+        }
+      }
+      int stage = 0;
+      for (int u = kQ4 ? end_unit : first_unit; u < end_unit; ++u) {
+        asm volatile("cp.async.wait_group %0;" :: "n"(kStages - 2) : "memory");
+        __syncwarp();                           // every lane's copies; and the last stage is read
+        issue(stage == 0 ? kStages - 1 : stage - 1);
+        next_key0 = -1;
+        if (u + kStages < end_unit) locate(u + kStages);
+        const uint8_t* const block = ring + stage * L::kBlockB;
+        stage = stage + 1 == kStages ? 0 : stage + 1;
+        // ---- S^T, in two chains of products
+        const int cur0 = key_of(u);
+        if (cur0 < 0) continue;
+        float x[kNr][4], x2[kNr][4];
+#pragma unroll
+        for (int nr = 0; nr < kNr; ++nr)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[nr][e] = x2[nr][e] = 0.0f;
+#pragma unroll
+        for (int v = 0; v < kKw / 4; ++v) {
           const uint4 ka = *reinterpret_cast<const uint4*>(block + k_at(g, 4 * v + t));
           const uint4 kb = *reinterpret_cast<const uint4*>(block + k_at(g + 8, 4 * v + t));
           const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
@@ -772,44 +878,16 @@ paged_few_kernel(const PagedAttnParams p, const __grid_constant__ Maps<kKind> ma
         }
         {
           // ---- logits, masks, running maximum and sum
-          const bool full_block =
-              cur0 + kKeys - 1 <= p_lo && (cur0 >= lo_hi || cur0 + kKeys - 1 < sinks);
+          const bool full =
+              cur0 + 15 <= p_lo && (cur0 >= lo_hi || cur0 + 15 < sinks);
           bool over = false;                    // a logit has outgrown its row's reference
-          if constexpr (kQ4) {
-            // (branches once for the block: a test per logit costs as much as the logits)
 #pragma unroll
-            for (int sn = 0; sn < kSubs * kNr; ++sn)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) x[sn][e] *= rs[sn % kNr][e & 1];
-            if (!full_block) {
-#pragma unroll
-              for (int sn = 0; sn < kSubs * kNr; ++sn)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  const int j = cur0 + 16 * (sn / kNr) + g + 8 * (e >> 1);
-                  const int pos = rpos[sn % kNr][e & 1];
-                  if (!(j <= pos && (p.window <= 0 || j > pos - p.window || j < sinks)))
-                    x[sn][e] = -INFINITY;
-                }
-            }
-#pragma unroll
-            for (int nr = 0; nr < kNr; ++nr)
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                float v = fmaxf(x[nr][i], x[nr][i + 2]);
-                if constexpr (kSubs == 2)
-                  v = fmaxf(v, fmaxf(x[kNr + nr][i], x[kNr + nr][i + 2]));
-                over |= v > m[nr][i] + kOver;
-              }
-          }
-#pragma unroll
-          for (int sn = 0; sn < (kQ4 ? 0 : kNr); ++sn) {
-            const int nr = sn;
+          for (int nr = 0; nr < kNr; ++nr) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               float v = (x[nr][e] + x2[nr][e]) * rs[nr][e & 1];
               if constexpr (kQ8) v *= ks[e >> 1];
-              if (!full_block) {
+              if (!full) {
                 const int j = cur0 + g + 8 * (e >> 1);
                 const int pos = rpos[nr][e & 1];
                 const bool see =
@@ -829,8 +907,6 @@ paged_few_kernel(const PagedAttnParams p, const __grid_constant__ Maps<kKind> ma
 #pragma unroll
               for (int i = 0; i < 2; ++i) {
                 float v = fmaxf(x[nr][i], x[nr][i + 2]);
-                if constexpr (kSubs == 2)
-                  v = fmaxf(v, fmaxf(x[kNr + nr][i], x[kNr + nr][i + 2]));
                 v = fmaxf(v, __shfl_xor_sync(kAll, v, 4));
                 v = fmaxf(v, __shfl_xor_sync(kAll, v, 8));
                 v = fmaxf(v, __shfl_xor_sync(kAll, v, 16));
@@ -847,58 +923,6 @@ paged_few_kernel(const PagedAttnParams p, const __grid_constant__ Maps<kKind> ma
                 for (int e = 0; e < 4; ++e) o[j][nr][e] *= alpha[nr][e & 1];
           }
           // ---- P^T and O^T
-          if constexpr (kQ4) {
-            // lane: channels 4 g .. 4 g + 3 of each group, of keys 2t and 2t + 1 (lo), and
-            // of those 8 further (hi); a value's scale goes into P, by the group
-            constexpr int kG = kDp / 32;
-            float safe[kNr][2];
-#pragma unroll
-            for (int nr = 0; nr < kNr; ++nr)
-#pragma unroll
-              for (int i = 0; i < 2; ++i) safe[nr][i] = m[nr][i] == -INFINITY ? 0.0f : m[nr][i];
-#pragma unroll
-            for (int sub = 0; sub < kSubs; ++sub) {
-              float e4[kNr][4];
-#pragma unroll
-              for (int nr = 0; nr < kNr; ++nr)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  e4[nr][e] = fast_exp2(x[sub * kNr + nr][e] - safe[nr][e & 1]);
-                  l[nr][e & 1] += e4[nr][e];
-                }
-              uint32_t vl[kG], vh[kG];
-              load_codes<true, kG>(vl, vh, base + mat_off + (kKeys + 16 * sub) * kRowB);
-              // P times the scales of keys g and g + 8, rounded once, before P is turned round
-              float sa[kG], sb[kG];
-              row_scales<kG>(base + val_scales + 128 * sub, sa);
-              row_scales<kG>(base + val_scales + 128 * sub + 8 * L::kScaleB, sb);
-              if (!full_block) {                // scales that no row sees may be NaN
-                const int j = cur0 + 16 * sub + g;
-#pragma unroll
-                for (int i = 0; i < kG; ++i) {
-                  if (!seen(j)) sa[i] = 0.0f;
-                  if (!seen(j + 8)) sb[i] = 0.0f;
-                }
-              }
-#pragma unroll
-              for (int i = 0; i < kG; ++i) {
-                uint32_t n[2][4];               // the four channels, as numbers -8..7
-                nibbles_to_half(vl[i], n[0]);
-                nibbles_to_half(vh[i], n[1]);
-#pragma unroll
-                for (int nr = 0; nr < kNr; ++nr) {
-                  const uint32_t b0 =
-                      transpose8x8(pack2<false>(e4[nr][0] * sa[i], e4[nr][1] * sa[i]));
-                  const uint32_t b1 =
-                      transpose8x8(pack2<false>(e4[nr][2] * sb[i], e4[nr][3] * sb[i]));
-                  mma<false>(o[2 * i][nr], n[0][0], n[0][1], n[1][0], n[1][1], b0, b1);
-                  mma<false>(o[2 * i + 1][nr], n[0][2], n[0][3], n[1][2], n[1][3], b0, b1);
-                }
-              }
-            }
-            release();
-            continue;
-          }
           uint32_t pb[kNr][2];
 #pragma unroll
           for (int nr = 0; nr < kNr; ++nr) {
