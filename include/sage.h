@@ -463,8 +463,9 @@ SAGE_API sage_status sage_rope_axes(
  *     (k_mean and v_scale as for SAGE_Q8).  A row is 16 ceil(D/32) bytes,
  *     n + 8 of channel c in the low (c even) or high half of byte c/2, and the
  *     strides count bytes, multiples of 16.  Scales: k_groups and v_groups
- *     [num_pages][Hkv][page_size][Dp/32] fp16.  K less its mean saturates at
- *     7 * 9352, V at 448 v_scale as in SAGE_Q8.
+ *     [num_pages][Hkv][page_size][Dp/32] fp16, at most 9352 and 1: K less its
+ *     mean saturates at 7 * 9352, V at 448 v_scale as in SAGE_Q8.  Those of
+ *     groups behind D are not read (sage_kv_append writes zeros).
  * page_size: a multiple of 16, up to 65536; D: a multiple of 8, 8..128; k and
  * v 16-byte aligned, strides multiples of 8 elements.  An 8-bit cache is read
  * fastest with D and strides of multiples of 16; otherwise 8 bytes at a time, which
@@ -506,8 +507,8 @@ typedef struct {
  * aligned.  The caller clears its first SAGE_PAGED_CLEAR_BYTES once, before the
  * first call: they hold the status word, of which the kernels only set bits and
  * which sage_device_status reads, and counters, which every call leaves at
- * zero; the rest needs no preparation.  Calls that may overlap on the GPU need
- * workspaces of their own. */
+ * zero (after SAGE_ERR_DEVICE_TIMEOUT they are cleared again); the rest needs no
+ * preparation.  Calls that may overlap on the GPU need workspaces of their own. */
 #define SAGE_PAGED_CLEAR_BYTES 8192
 SAGE_API size_t sage_workspace_bytes_paged(void);
 

@@ -1170,6 +1170,9 @@ sage_status status_of_word(uint32_t word) {
     return fail(SAGE_ERR_INVALID_ARG, "cu_seqlens inconsistent with totals/maxima");
   if (word & kStatusBadPage)
     return fail(SAGE_ERR_INVALID_ARG, "a block table entry lies outside the cache's pages");
+  if (word & kStatusBadPool)
+    return fail(SAGE_ERR_INVALID_ARG, "a page pool's request, length or number of pages cannot "
+                "be (a request outside the pool or given twice, too long, pages returned twice)");
   if (word & kStatusBadItem)
     return fail(SAGE_ERR_UNSUPPORTED, "internal error: a prologue work item fell outside "
                 "the call's plan and was skipped");

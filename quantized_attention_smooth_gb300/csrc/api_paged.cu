@@ -343,6 +343,7 @@ sage_status append(const sage_paged_cache* cache, const sage_paged_batch* batch,
     return refuse(SAGE_ERR_INVALID_ARG, "Hq=%lld out of range", (long long)Hq);
   if (inv_freq != nullptr && (s = check_rotation(inv_freq, R, D)) != SAGE_OK) return s;
   if (T == 0 || batch->nseq == 0) return succeeded();
+  if (axes.naxes > 0 && (s = check_positions(axes.pos, axes.pos_bits)) != SAGE_OK) return s;
   if (k == nullptr || v == nullptr || !on(k, 2) || !on(v, 2) ||
       (q != nullptr && (!on(q, 2) || q_out == nullptr || !on(q_out, 2))))
     return refuse(SAGE_ERR_INVALID_ARG, "k, v (and q with q_out) must be 2-byte aligned device "
@@ -432,8 +433,7 @@ sage_status sage_kv_append_axes(const sage_paged_cache* cache, const sage_paged_
                                 const double* inv_freq, int64_t R, int interleaved, float mscale,
                                 void* ws, size_t ws_bytes, sage_stream_t stream) {
   if (batch == nullptr) return refuse(SAGE_ERR_INVALID_ARG, "cache and batch must not be null");
-  sage_status s = check_axes(naxes, axis_stride, batch->total_q);
-  if (s == SAGE_OK) s = check_positions(pos, pos_bits);
+  const sage_status s = check_axes(naxes, axis_stride, batch->total_q);
   if (s != SAGE_OK) return s;
   if (inv_freq == nullptr)
     return refuse(SAGE_ERR_INVALID_ARG, "positions are given without inv_freq");

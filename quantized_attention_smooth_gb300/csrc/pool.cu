@@ -100,7 +100,7 @@ __device__ __forceinline__ void clear_marks(const PoolParams& p) {
 __device__ __forceinline__ int height(const PoolParams& p) {
   const int left = p.left[0];
   if (left >= 0 && left <= p.num_pages) return left;
-  if (threadIdx.x == 0) atomicOr(p.status, kStatusBadItem);
+  if (threadIdx.x == 0) atomicOr(p.status, kStatusBadPool);
   return left < 0 ? 0 : p.num_pages;
 }
 
@@ -135,7 +135,7 @@ __device__ __forceinline__ void plan_step(const PoolParams& p) {
     int64_t none = 0, all_none;
     scan2(row, none, &all_rows, &all_none);
     if (rows + row > p.rows) fine = false;
-    if (i < p.n && !fine) atomicOr(p.status, kStatusBadSeqlens);
+    if (i < p.n && !fine) atomicOr(p.status, kStatusBadPool);
     if (fine) need = pages_of(p, static_cast<int64_t>(old) + fresh) - have;
     upto = need;
     int64_t refused = 0, all_refused;
@@ -246,7 +246,7 @@ __device__ __forceinline__ void plan_trim(const PoolParams& p) {
       const int keep = p.new_lens != nullptr ? p.new_lens[i] : 0;
       const bool fine = first_place(p, i, r) && keep >= 0;
       if (!fine) {
-        atomicOr(p.status, kStatusBadSeqlens);
+        atomicOr(p.status, kStatusBadPool);
       } else {
         const int len = p.lens[r];
         if (keep < len && pages_of(p, len) <= p.width) {
@@ -254,7 +254,7 @@ __device__ __forceinline__ void plan_trim(const PoolParams& p) {
           back = pages_of(p, len) - kept;
           p.lens[r] = keep;
         } else if (keep < len || len < 0) {
-          atomicOr(p.status, kStatusBadSeqlens);
+          atomicOr(p.status, kStatusBadPool);
         }
       }
     }
@@ -268,7 +268,7 @@ __device__ __forceinline__ void plan_trim(const PoolParams& p) {
   __syncthreads();
   if (threadIdx.x == 0) {
     // more pages than the stack has room for: some went back twice
-    if (left + gone > p.num_pages) atomicOr(p.status, kStatusBadItem);
+    if (left + gone > p.num_pages) atomicOr(p.status, kStatusBadPool);
     p.left[0] = static_cast<int>(min(left + gone, static_cast<int64_t>(p.num_pages)));
   }
 }
