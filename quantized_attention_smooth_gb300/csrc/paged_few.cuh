@@ -34,8 +34,21 @@
 // eight in a tile are empty and the arithmetic is the same.
 //
 // P is rounded to the 16-bit type of the tensor instruction (by up to 2^-8 of it in
-// bf16, 2^-11 in fp16, as the output's own rounding); the sum l takes it unrounded.  The 8-bit cache's codes are exact in fp16: K codes |n| <= 127,
-// e4m3 values <= 448; bf16 queries are scaled per row by a power of two first.
+// bf16, 2^-11 in fp16, as the output's own rounding); the sum l takes it unrounded.
+// The 8-bit cache's codes are exact in fp16: K codes |n| <= 127, e4m3 values <= 448;
+// bf16 queries are scaled per row by a power of two first.
+//
+// The 4-bit cache: x_j = sum over groups of s_jg (sum of q n over the group's channels),
+// O_c = sum_j (P_j s_jg) n_jc, both on fp16 products of exact codes.  Eight rows of
+// one group's 16 bytes are what ldmatrix moves: as they stand the A operands of S^T,
+// transposed those of O^T, whose tiles then have one group each, so that a group's
+// scale multiplies S^T's partial sums and P, in fp32.  Blocks are 32 keys (16 where
+// registers are short: 171 us with them below); a fifth warp fills the others' rings by
+// tensor copies and goes on to the next item while they join the last.  64 x 8520
+// keys of 32 heads on 8 x 128: 162 us, 3.88 TB/s, 58 % of the measured copy bandwidth:
+// the instructions bound it (660 a warp and step, half on the ALU pipe; three warps
+// share a scheduler), the copies alone take 128 us.  The first form, with 16 keys a step
+// and copies by the warps themselves, took 205.
 
 #pragma once
 

@@ -28,7 +28,9 @@
 // every head.  Measured (GB300, back to back in a graph): interleaved rope of
 // 16000 tokens x 80 heads x 128 fp16, 110 us, 5.9 TB/s, 88 % of the measured copy
 // bandwidth; rope of one token for each of 64 sequences 3.8 us, of which the
-// launch is most.
+// launch is most; three axes, 32768 tokens x 80 x 128 bf16, 215 us, 6.24 TB/s, 93 %.
+// Packed prompts into the 4-bit cache, 76000 tokens x 16 heads x 80 fp16: 140 us, 3.7
+// TB/s, issue slots 74 % full; read back 144 us, 3.3 TB/s, waiting for loads.
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -952,6 +954,7 @@ cudaError_t launch_rows(const RowsParams& p, int mode, bool bf16, int sms, cudaS
   //   Q8 append as it is, the same two                             128   237 | 149   156
   //   Q8 append, half layout, the rows of the 16-bit one           210   220 | 280   471
   //   Q8 append, interleaved, 24000 tokens, 32 on 8 of 128          261   161
+  //   Q4 append as it is (two lanes a group), 76000 x 16 of 80      140   340
   // The last one is on the slower side.  One vector a lane has the shorter way
   // through few tokens (64: 3.8 us against 4.3; Q8 4.7 against 6.8), and rope and
   // 16-bit appends whose pairs are neighbours stay with it (110 against 118).
