@@ -14,7 +14,7 @@
 // hands them to the others, which write tables, positions and slots.  A request that
 // is given twice is found by a mark per request, which the first CTA clears again.
 // Measured (GB300, in a graph): a step and a cut of 64 requests over 1028 columns 15 us,
-// of 256 prompts (51000 rows, 264 columns) 28 us; their bytes would take 0.2.
+// of 256 prompts (52000 rows, 264 columns) 28 us; their bytes would take 0.2.
 
 #include <climits>
 

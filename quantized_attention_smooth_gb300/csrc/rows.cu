@@ -954,13 +954,16 @@ cudaError_t launch_rows(const RowsParams& p, int mode, bool bf16, int sms, cudaS
   //   Q8 append as it is, the same two                             128   237 | 149   156
   //   Q8 append, half layout, the rows of the 16-bit one           210   220 | 280   471
   //   Q8 append, interleaved, 24000 tokens, 32 on 8 of 128          261   161
-  //   Q4 append as it is (two lanes a group), 76000 x 16 of 80      140   340
+  // and two lanes a group against eight channels a lane, Q4 append as it is:
+  //   76000 x 16 of 80 | 76000 x 8 of 128                           138   310 | 83   172
+  //   4096, 1280 and 576 tokens x 8 of 128                           25    16 | 21   9 | 13   9
+  // (they cross near 8000 tokens: one CTA's chain of loads is longer).
   // The last one is on the slower side.  One vector a lane has the shorter way
   // through few tokens (64: 3.8 us against 4.3; Q8 4.7 against 6.8), and rope and
   // 16-bit appends whose pairs are neighbours stay with it (110 against 118).
   const bool apart = p.inv_freq != nullptr && !p.interleaved;
   const bool neighbours = p.inv_freq != nullptr && p.interleaved;
-  const bool pairs = p.vec && p.T >= 4 * static_cast<int64_t>(sms) &&
+  const bool pairs = p.vec && p.T >= (mode == 3 ? 48 : 4) * static_cast<int64_t>(sms) &&
                      !(apart && p.R % 16 != 0) && !(neighbours && mode < 2);
   if (pairs) {
     if (mode == 3)

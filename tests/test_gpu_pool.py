@@ -36,7 +36,8 @@ class Model:
             start, at = at, at + max(n, 0)
             cu.append(at)
             fine = 0 <= r < len(self.lens) and r not in seen and 0 <= n <= max_q and at <= rows
-            if 0 <= r < len(self.lens):
+            own = 0 <= r < len(self.lens) and r not in seen
+            if own:
                 seen.add(r)
             end = 0
             if fine:
@@ -46,7 +47,6 @@ class Model:
             need = end - len(self.pages[r]) if fine else 0
             if fine and need > 0 and (dry or need > len(self.stack)):
                 dry, fine = True, False
-            own = 0 <= r < len(self.lens) and [x for x in reqs].index(r) == len(cu) - 2
             if not fine:
                 denied += 1
                 out.append((0, list(self.pages[r][:width]) if own else []))

@@ -17,6 +17,7 @@ def sage():
     return sage
 
 
+ALL = CASES + [([5000, 0, 1, 2999], [5100, 0, 5, 2900])]     # the last: the kernel for many tokens
 SHAPES = [(128, 8, 16, "NHD", False), (80, 3, 32, "HND", True), (64, 1, 64, "NHD", True),
           (40, 5, 48, "HND", False), (104, 2, 16, "NHD", False), (8, 2, 16, "HND", False),
           (32, 4, 256, "NHD", False)]
@@ -33,9 +34,9 @@ def wanted(p, k, v):
 
 @pytest.mark.parametrize("dt", [torch.bfloat16, torch.float16])
 @pytest.mark.parametrize("d,hkv,page,layout,both", SHAPES)
-@pytest.mark.parametrize("case", range(len(CASES)))
+@pytest.mark.parametrize("case", range(len(ALL)))
 def test_append(sage, dt, d, hkv, page, layout, both, case):
-    q_lens, kv_lens = CASES[case]
+    q_lens, kv_lens = ALL[case]
     p = Problem4(q_lens, kv_lens, hkv, hkv, d, page, layout, dt, seed=23, both=both, poison=False,
                  offset=3.0, spare_rows=2)
     k, v = randn(24, p.q.shape[0], hkv, d, dt=dt), randn(25, p.q.shape[0], hkv, d, dt=dt)
@@ -68,9 +69,9 @@ def test_append(sage, dt, d, hkv, page, layout, both, case):
 @pytest.mark.parametrize("dt", [torch.bfloat16, torch.float16])
 @pytest.mark.parametrize("d,hkv,page,layout,both", SHAPES[:5])
 @pytest.mark.parametrize("r,interleaved", [(8, False), (8, True), (-1, False), (-1, True)])
-@pytest.mark.parametrize("case", [1, 3])
+@pytest.mark.parametrize("case", [1, 3, len(ALL) - 1])
 def test_append_with_rotation(sage, dt, d, hkv, page, layout, both, r, interleaved, case):
-    q_lens, kv_lens = CASES[case]
+    q_lens, kv_lens = ALL[case]
     r = d if r < 0 else r
     p = Problem4(q_lens, kv_lens, 2 * hkv, hkv, d, page, layout, dt, seed=26, both=both, poison=False,
                  offset=2.0)

@@ -107,7 +107,8 @@ def test_an_axis_beyond_the_last_takes_the_last(sage):
 @pytest.mark.parametrize("kind", ["bf16", "q8", "q4"])
 @pytest.mark.parametrize("interleaved", [False, True])
 @pytest.mark.parametrize("q_lens,kv_lens", [([1, 1, 1], [1, 16, 333]), ([3, 0, 50, 7], [3, 9, 200, 4]),
-                                            ([700, 1, 300], [710, 50, 333])])
+                                            ([700, 1, 300], [710, 50, 333]),
+                                            ([7000, 1, 900], [7010, 50, 950])])
 def test_append(sage, kind, interleaved, q_lens, kv_lens):
     """The append at given positions stores what the rotation alone gives, and turns q alike."""
     dt, hkv, d = torch.bfloat16, 2, 128
