@@ -1291,7 +1291,11 @@ cudaError_t launch_few(const PagedAttnParams& p, int sms, cudaStream_t st) {
   // head pairs over 32768 keys, inside against second kernel: 1: 91 and 63 us, 2: 54
   // and 45, 4: 44 and 40, 8: 50 and 48, 128: 351 and 353; over 2000 keys the second
   // kernel is 1 to 2 us ahead up to 64 of them, at the price of its launch.)
-  prm.join_inside = items >= (ctas + kJoinInside - 1) / kJoinInside;
+  // Over four bits the second kernel is worth its launch sooner with more rows to join (tiles
+  // of 16 and 24 rows; inside against second: 9.5 parts an item 43 and 36, 25 and 21; 19
+  // parts 31 and 20; 2.4 and 1.6 parts 81 and 78, 29.8 and 30.8).
+  constexpr int kInside = kKind == kKindQ4 && kNr > 1 ? 6 : kJoinInside;
+  prm.join_inside = items >= (ctas + kInside - 1) / kInside;
   kern<<<ctas, L::kThreads, L::kSmem, st>>>(prm, maps);
   note_launch();
   e = cudaGetLastError();
