@@ -13,8 +13,8 @@
 // the requests, a thread each, and leaves 16 bytes a sequence; the cluster's barrier
 // hands them to the others, which write tables, positions and slots.  A request that
 // is given twice is found by a mark per request, which the first CTA clears again.
-// Measured (GB300, in a graph): a step and a cut of 64 requests over 1028 columns 15 us,
-// of 256 prompts (52000 rows, 264 columns) 28 us; their bytes would take 0.2.
+// Measured (GB300, in a graph): a step and a cut of 64 requests over 1028 columns 14 us,
+// of 256 prompts (52000 rows, 264 columns) 21 us; their bytes would take 0.2.
 
 #include <climits>
 
@@ -25,6 +25,7 @@ namespace sage {
 namespace {
 
 constexpr int kThreads = 1024, kCluster = 8;
+constexpr int kStaged = 1024;        // sequences whose entries fit in shared memory
 constexpr unsigned kAll = 0xFFFFFFFFu;
 
 __device__ __forceinline__ int pages_of(const PoolParams& p, int64_t tokens) {
@@ -186,51 +187,87 @@ __device__ __forceinline__ int page_at(const PoolParams& p, const int32_t* row, 
 
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
 step_kernel(const PoolParams p) {
+  // Up to kStaged sequences each CTA keeps the entries, rows and requests by itself: the
+  // search for a row's sequence is a chain of log2 n loads (256 prompts, from the L2 and
+  // a row at a time: 28 us, so 21).  More sequences are read where they lie.
+  __shared__ int4 seqs_s[kStaged];
+  __shared__ int cu_s[kStaged + 1], requests_s[kStaged];
   if (blockIdx.x == 0) plan_step(p);
   cluster_barrier();
+  const bool staged = p.n <= kStaged;
+  if (staged) {
+    for (int i = threadIdx.x; i <= p.n; i += kThreads) {
+      cu_s[i] = __ldcg(&p.cu_q[i]);
+      if (i < p.n) {
+        seqs_s[i] = __ldcg(&p.seqs[i]);
+        requests_s[i] = p.requests[i];
+      }
+    }
+    __syncthreads();
+  }
+  const int* const cu = staged ? cu_s : p.cu_q;
+  const int4* const seqs = staged ? seqs_s : p.seqs;
+  const int* const requests = staged ? requests_s : p.requests;
   const int id = blockIdx.x * kThreads + threadIdx.x, threads = kCluster * kThreads;
   // ---- the tables: a warp per 128 columns of a row
   const int lane = threadIdx.x & 31, warps = threads / 32;
   const int chunks = (p.plan_width + 127) / 128;
   for (int64_t u = id / 32; u < static_cast<int64_t>(p.n) * chunks; u += warps) {
-    const int i = static_cast<int>(u / chunks), j0 = static_cast<int>(u - static_cast<int64_t>(i) * chunks) * 128;
-    const int4 q = __ldcg(&p.seqs[i]);
-    const int r = p.requests[i];
-    int32_t* const own = p.table + (q.z + q.w > 0 ? r * p.table_stride : 0);
+    const int i = static_cast<int>(u / chunks);
+    const int j0 = static_cast<int>(u - static_cast<int64_t>(i) * chunks) * 128;
+    const int4 q = seqs[i];
+    int32_t* const own = p.table + (q.z + q.w > 0 ? requests[i] * p.table_stride : 0);
     int32_t* const out = p.block_table + i * p.plan_stride;
+    int page[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int j = j0 + 32 * k + lane;
+      page[k] = j < p.plan_width && j < q.z + q.w ? page_at(p, own, q, j) : -1;
+    }
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const int j = j0 + 32 * k + lane;
       if (j >= p.plan_width) continue;
-      int page = -1;
-      if (j < q.z + q.w) {
-        page = page_at(p, own, q, j);
-        if (j >= q.z) own[j] = page;
-      }
-      out[j] = page;
+      if (j >= q.z && j < q.z + q.w) own[j] = page[k];
+      out[j] = page[k];
     }
   }
-  // ---- the rows
+  // ---- the rows, four at a time
   if (p.positions == nullptr && p.slots == nullptr) return;
-  const int64_t total = min(static_cast<int64_t>(__ldcg(&p.cu_q[p.n])), p.rows);
-  for (int64_t t = id; t < total; t += threads) {
-    int lo = 0, hi = p.n;                       // the last i with cu_q[i] <= t
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) / 2;
-      if (__ldcg(&p.cu_q[mid]) <= t) lo = mid;
-      else hi = mid;
+  const int64_t total = min(static_cast<int64_t>(cu[p.n]), p.rows);
+  constexpr int kUnroll = 4;
+  for (int64_t tb = id; tb < total; tb += kUnroll * threads) {
+    int64_t pos[kUnroll];
+    int page[kUnroll], in[kUnroll];
+#pragma unroll
+    for (int k = 0; k < kUnroll; ++k) {
+      const int64_t t = tb + k * threads;
+      pos[k] = page[k] = -1;
+      in[k] = 0;
+      if (t >= total) continue;
+      int lo = 0, hi = p.n;                     // the last i with cu[i] <= t
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (cu[mid] <= t) lo = mid;
+        else hi = mid;
+      }
+      const int4 q = seqs[lo];
+      if (q.x >= 0) {
+        const int at = q.x + static_cast<int>(t - cu[lo]);
+        const int j = p.page_shift >= 0 ? at >> p.page_shift : at / p.page_size;
+        pos[k] = at;
+        in[k] = at - j * p.page_size;
+        page[k] = page_at(p, p.table + requests[lo] * p.table_stride, q, j);
+      }
     }
-    const int4 q = __ldcg(&p.seqs[lo]);
-    int64_t pos = -1, slot = -1;
-    if (q.x >= 0) {
-      const int at = q.x + static_cast<int>(t - __ldcg(&p.cu_q[lo]));
-      const int j = p.page_shift >= 0 ? at >> p.page_shift : at / p.page_size;
-      pos = at;
-      slot = static_cast<int64_t>(page_at(p, p.table + p.requests[lo] * p.table_stride, q, j)) *
-                 p.page_size + (at - j * p.page_size);
+#pragma unroll
+    for (int k = 0; k < kUnroll; ++k) {
+      const int64_t t = tb + k * threads;
+      if (t >= total) continue;
+      if (p.positions != nullptr) p.positions[t] = pos[k];
+      if (p.slots != nullptr)
+        p.slots[t] = pos[k] < 0 ? -1 : static_cast<int64_t>(page[k]) * p.page_size + in[k];
     }
-    if (p.positions != nullptr) p.positions[t] = pos;
-    if (p.slots != nullptr) p.slots[t] = slot;
   }
 }
 
