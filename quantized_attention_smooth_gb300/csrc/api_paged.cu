@@ -271,10 +271,10 @@ sage_status pool_params(const sage_page_pool* pool, const int32_t* requests, int
 }
 
 sage_status rope(const void* q, const void* k, void* q_out, void* k_out, int dtype, int64_t T,
-                      int64_t Hq, int64_t Hkv, int64_t D, const int64_t* q_strides,
-                      const int64_t* k_strides, const int64_t* qo_strides,
-                      const int64_t* ko_strides, const Axes& axes, const double* inv_freq, int64_t R, int interleaved, float mscale,
-                      int inverse, sage_stream_t stream) {
+                 int64_t Hq, int64_t Hkv, int64_t D, const int64_t* q_strides,
+                 const int64_t* k_strides, const int64_t* qo_strides, const int64_t* ko_strides,
+                 const Axes& axes, const double* inv_freq, int64_t R, int interleaved,
+                 float mscale, int inverse, sage_stream_t stream) {
   sage_status s = check_dtype(dtype);
   if (s != SAGE_OK) return s;
   if (D < 1 || D > 128)
@@ -325,12 +325,12 @@ sage_status rope(const void* q, const void* k, void* q_out, void* k_out, int dty
   return e == cudaSuccess ? succeeded() : cuda_refused(e, "rotary launch");
 }
 
-sage_status append(const sage_paged_cache* cache, const sage_paged_batch* batch,
-                           const void* k, const void* v, const void* q, void* q_out, int dtype,
-                           int64_t Hq, const int64_t* k_strides, const int64_t* v_strides,
-                           const int64_t* q_strides, const int64_t* qo_strides,
-                           const Axes& axes, const double* inv_freq, int64_t R, int interleaved, float mscale,
-                           void* ws, size_t ws_bytes, sage_stream_t stream) {
+sage_status append(const sage_paged_cache* cache, const sage_paged_batch* batch, const void* k,
+                   const void* v, const void* q, void* q_out, int dtype, int64_t Hq,
+                   const int64_t* k_strides, const int64_t* v_strides, const int64_t* q_strides,
+                   const int64_t* qo_strides, const Axes& axes, const double* inv_freq, int64_t R,
+                   int interleaved, float mscale, void* ws, size_t ws_bytes,
+                   sage_stream_t stream) {
   sage_status s = check_dtype(dtype);
   if (s != SAGE_OK) return s;
   RowsParams p{};
@@ -376,8 +376,9 @@ sage_status append(const sage_paged_cache* cache, const sage_paged_batch* batch,
   p.vec = vec_rows(k, p.k_tok, p.k_head) && vec_rows(v, p.v_tok, p.v_head) &&
           (q == nullptr ||
            (vec_rows(q, p.q_tok, p.q_head) && vec_rows(q_out, p.qo_tok, p.qo_head)));
-  const cudaError_t e = launch_rows(p, cache->kind == SAGE_Q4 ? 3 : cache->kind == SAGE_Q8 ? 2 : 1, dtype == SAGE_BF16, sms,
-                                    reinterpret_cast<cudaStream_t>(stream));
+  const int mode = cache->kind == SAGE_Q4 ? 3 : cache->kind == SAGE_Q8 ? 2 : 1;
+  const cudaError_t e =
+      launch_rows(p, mode, dtype == SAGE_BF16, sms, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? succeeded() : cuda_refused(e, "cache append launch");
 }
 

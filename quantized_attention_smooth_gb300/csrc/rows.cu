@@ -27,10 +27,12 @@
 // cos and sin of a CTA's tokens are computed once into shared memory and serve
 // every head.  Measured (GB300, back to back in a graph): interleaved rope of
 // 16000 tokens x 80 heads x 128 fp16, 110 us, 5.9 TB/s, 88 % of the measured copy
-// bandwidth; rope of one token for each of 64 sequences 3.8 us, of which the
+// bandwidth (half layout 108); rope of one token for each of 64 sequences 3.8 us, of which the
 // launch is most; three axes, 32768 tokens x 80 x 128 bf16, 215 us, 6.24 TB/s, 93 %.
 // Packed prompts into the 4-bit cache, 76000 tokens x 16 heads x 80 fp16: 140 us, 3.7
-// TB/s, issue slots 74 % full; read back 144 us, 3.3 TB/s, waiting for loads.
+// TB/s, issue slots 74 % full; read back 144 us, 3.3 TB/s, waiting for loads.  24000
+// tokens, 32 heads of q and 8 of k and v, 128 bf16, half layout: into 16 bits 99 us,
+// 5.8 TB/s; 8 bits 108; 4 bits 114.
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -47,6 +49,11 @@ constexpr int kRowThreads = 256;
 constexpr int kMaxToks = 8;          // tokens of one CTA
 constexpr int kMaxPairToks = 64;
 constexpr unsigned kAll = 0xFFFFFFFFu;
+// CTAs of an SM, as the kernels' registers allow.
+constexpr int row_ctas(int mode) { return mode == 0 ? 5 : 3; }
+constexpr int pair_ctas(int mode) { return mode == 2 ? 4 : 3; }
+constexpr int group_ctas(bool turn) { return turn ? 3 : 4; }
+constexpr int kGatherCtas = 4;
 constexpr float kSeventh = 1.0f / 7.0f;
 constexpr float kMostK = 9352.0f, kMostV = 1.0f;   // largest scales of a Q4 group
 
@@ -235,7 +242,7 @@ __device__ __forceinline__ uint32_t pack_nibbles(const float (&x)[8], float top,
 // kMode: 0 rope, 1 append 16-bit, 2 append Q8, 3 append Q4.  kLanes: lanes of a row.
 // kShfl: the half layout's partner vector is another lane's whole vector.
 template <int kMode, bool kBF16, int kLanes, bool kShfl>
-__global__ void __launch_bounds__(kRowThreads, kMode == 0 ? 5 : 3)
+__global__ void __launch_bounds__(kRowThreads, row_ctas(kMode))
 rows_kernel(const RowsParams p) {
   __shared__ float2 cs[kMaxToks * 64];
   __shared__ int64_t pos_s[kMaxToks];
@@ -729,7 +736,7 @@ __device__ __forceinline__ void group_pass(const RowsParams& p, const Tokens& tk
 }
 
 template <bool kBF16, bool kTurn>
-__global__ void __launch_bounds__(kRowThreads, kTurn ? 3 : 4)
+__global__ void __launch_bounds__(kRowThreads, group_ctas(kTurn))
 group_rows_kernel(const RowsParams p) {
   __shared__ float2 cs[kTurn ? kMaxPairToks * 64 : 1];
   __shared__ Tokens tk;
@@ -747,7 +754,7 @@ group_rows_kernel(const RowsParams p) {
 }
 
 template <int kMode, bool kBF16>
-__global__ void __launch_bounds__(kRowThreads, kMode == 2 ? 4 : 3)
+__global__ void __launch_bounds__(kRowThreads, pair_ctas(kMode))
 pair_rows_kernel(const RowsParams p) {
   __shared__ float2 cs[kMaxPairToks * 64];
   __shared__ Tokens tk;
@@ -770,11 +777,21 @@ pair_rows_kernel(const RowsParams p) {
   if (kMode != 0) pair_pass<kMode, 2, kBF16>(p, tk, cs, t0, nt);
 }
 
+// Tokens of a CTA, `most` at most, so that the CTAs fill whole waves of `slots`.  Each
+// begins with a chain of dependent loads (sequence, page, positions) and the angles, so
+// a wave and a bit take as long as two: 16-bit append of 9868 rotated tokens (617 CTAs of
+// 16 on 456 slots) 38.5 us, in one wave 28.6; Q8, 9872 tokens 71 and 56; rope 48 and 38;
+// read back 43.3 and 39.2.  Two smaller waves instead of one were slower (40, 66, 40).
+inline int tokens_of_cta(int64_t T, int most, int64_t slots) {
+  const int64_t waves = (T + most * slots - 1) / (most * slots);
+  return T > 0 ? static_cast<int>((T + waves * slots - 1) / (waves * slots)) : 1;
+}
+
 template <int kMode, bool kBF16>
 cudaError_t launch_pairs(const RowsParams& p0, int sms, cudaStream_t st) {
   RowsParams p = p0;
-  p.toks = 1;
-  while (p.toks < kMaxPairToks && p.T / (2 * p.toks) >= 4 * sms) p.toks *= 2;
+  const int per_sm = kMode == 3 ? group_ctas(p.inv_freq != nullptr) : pair_ctas(kMode);
+  p.toks = tokens_of_cta(p.T, kMaxPairToks, static_cast<int64_t>(per_sm) * sms);
   const int64_t ctas = (p.T + p.toks - 1) / p.toks;
   if (ctas > 0x7FFFFFFF) return cudaErrorInvalidValue;
   if (kMode == 3 && p.inv_freq == nullptr)      // q comes with a rotation only
@@ -802,9 +819,8 @@ cudaError_t launch_mode(const RowsParams& p0, bool bf16, int sms, cudaStream_t s
   const int rows = p.Hq + p.Hkv * (kMode == 0 ? 1 : 2);
   const int groups = kRowThreads / lanes;
   // Few tokens: one per CTA, and its heads over several CTAs, so that every SM
-  // has work; many: kMaxToks, which serve the means, scales and angles.
-  p.toks = 1;
-  while (p.toks < kMaxToks && p.T / (2 * p.toks) >= 4 * sms) p.toks *= 2;
+  // has work; many: up to kMaxToks, which share the means, scales and angles.
+  p.toks = tokens_of_cta(p.T, kMaxToks, static_cast<int64_t>(row_ctas(kMode)) * sms);
   const int64_t ctas = (p.T + p.toks - 1) / p.toks;
   int64_t y = (rows + groups - 1) / groups;
   if (ctas * y > 2 * sms) y = 2 * sms / ctas > 1 ? 2 * sms / ctas : 1;
@@ -823,7 +839,7 @@ cudaError_t launch_mode(const RowsParams& p0, bool bf16, int sms, cudaStream_t s
 constexpr int kGatherToks = 32;
 
 template <int kKind, bool kBF16>
-__global__ void __launch_bounds__(kRowThreads, 4)
+__global__ void __launch_bounds__(kRowThreads, kGatherCtas)
 gather_kernel(const RowsParams p) {
   __shared__ int64_t pos_s[kGatherToks], slot_s[kGatherToks], scale_s[kGatherToks];
   __shared__ int page_s[kGatherToks];
@@ -919,8 +935,7 @@ template <int kKind, bool kBF16>
 cudaError_t launch_gather_kind(const RowsParams& p0, int sms, cudaStream_t st) {
   RowsParams p = p0;
   const int units = 2 * p.Hkv * (p.D / 8);
-  p.toks = 1;
-  while (p.toks < kGatherToks && p.T / (2 * p.toks) >= 4 * sms) p.toks *= 2;
+  p.toks = tokens_of_cta(p.T, kGatherToks, static_cast<int64_t>(kGatherCtas) * sms);
   const int64_t ctas = (p.T + p.toks - 1) / p.toks;
   if (ctas > 0x7FFFFFFF) return cudaErrorInvalidValue;
   int64_t y = (units + kRowThreads - 1) / kRowThreads;
@@ -944,27 +959,31 @@ cudaError_t launch_gather(const RowsParams& p, bool bf16, int sms, cudaStream_t 
 }
 
 cudaError_t launch_rows(const RowsParams& p, int mode, bool bf16, int sms, cudaStream_t st) {
-  // Two vectors a lane from 4 tokens per SM on, for whole vectors.  Measured, two
-  // vectors against one (us; one call in a graph, L2 flushed):
-  //   rope, half layout, 16000 tokens x (40 + 40) heads of 128      132   192
-  //   16-bit append, half layout, q beside it: 24000 tokens, 32 q
-  //     heads on 8 kv heads of 128                                 130   192
-  //     65000 tokens, 16 on 16 heads of 80                         231   370
-  //   16-bit append as it is, 65000 x 16 of 80 | 16000 x 40 of 128  128   161 | 122   120
-  //   Q8 append as it is, the same two                             128   237 | 149   156
-  //   Q8 append, half layout, the rows of the 16-bit one           210   220 | 280   471
-  //   Q8 append, interleaved, 24000 tokens, 32 on 8 of 128          261   161
-  // and two lanes a group against eight channels a lane, Q4 append as it is:
-  //   76000 x 16 of 80 | 76000 x 8 of 128                           138   310 | 83   172
-  //   4096, 1280 and 576 tokens x 8 of 128                           25    16 | 21   9 | 13   9
-  // (they cross near 8000 tokens: one CTA's chain of loads is longer).
-  // The last one is on the slower side.  One vector a lane has the shorter way
-  // through few tokens (64: 3.8 us against 4.3; Q8 4.7 against 6.8), and rope and
-  // 16-bit appends whose pairs are neighbours stay with it (110 against 118).
+  // Two vectors a lane (over four bits, two lanes a group), for whole vectors: fewer
+  // instructions a row, but one CTA's chain of loads is longer, so one vector a lane has
+  // the shorter way through few tokens.  Measured, one vector against the other (us; 32
+  // heads of q and 8 of k and v, D = 128, 152 SMs):
+  //   tokens                        700         1500        2500        5000        9872
+  //   rope, half layout          10.8  9.7   14.7 13.9   22.2 14.5   36.7 22.0   68.1 38.2
+  //   16 bits as they are         4.6  6.3    5.1  7.0    6.2  7.5   10.1  9.4   15.9 16.2
+  //   16 bits, half layout       11.6 12.0   16.8 16.6   22.6 17.3   46.4 26.1   81.1 44.6
+  //   16 bits, interleaved        9.1 12.1   12.1 16.6   16.6 18.3   33.6 28.2   56.2 49.3
+  //   Q8 as it is                 6.0 11.1    7.4 13.8    8.7 15.2   14.5 16.9   23.7 20.7
+  //   Q8, half layout            13.5 15.5   19.8 19.5   27.0 25.5   53.4 36.4   94.4 56.2
+  //   Q8, interleaved            10.8 17.8   14.7 22.4   19.8 29.9   40.1 41.8   68.5 66.2
+  //   Q4 as it is                 6.3 10.8    7.5 13.8    9.4 15.2   15.9 16.9   25.5 20.3
+  //   Q4, half layout            13.5 16.4   19.8 21.2   27.2 23.4   52.6 34.7   93.7 57.2
+  //   Q4, interleaved            10.8 16.2   14.7 20.7   20.0 23.4   39.4 33.6   67.4 55.8
+  // Interleaved rope is as fast either way where rows fill the lanes of one vector each
+  // (16000 tokens x 80 heads x 128: 111 118; 76000 x 40: 265 276) and stays there; where
+  // they leave lanes idle it goes by the table (65000 x 32 x 80: 159 137).
   const bool apart = p.inv_freq != nullptr && !p.interleaved;
   const bool neighbours = p.inv_freq != nullptr && p.interleaved;
-  const bool pairs = p.vec && p.T >= (mode == 3 ? 48 : 4) * static_cast<int64_t>(sms) &&
-                     !(apart && p.R % 16 != 0) && !(neighbours && mode < 2);
+  // tokens per SM (rope has no row as it is)
+  constexpr int kAsIs[4] = {0, 28, 48, 48}, kApart[4] = {4, 4, 10, 13}, kNear[4] = {28, 28, 48, 28};
+  const int least = apart ? kApart[mode] : neighbours ? kNear[mode] : kAsIs[mode];
+  const bool pairs = p.vec && p.T >= static_cast<int64_t>(least) * sms &&
+                     !(apart && p.R % 16 != 0) && !(neighbours && mode == 0 && p.D % 64 == 0);
   if (pairs) {
     if (mode == 3)
       return bf16 ? launch_pairs<3, true>(p, sms, st) : launch_pairs<3, false>(p, sms, st);
