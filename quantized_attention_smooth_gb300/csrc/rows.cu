@@ -190,21 +190,26 @@ __device__ __forceinline__ void place_tokens(const RowsParams& p, int64_t t0, in
 }
 
 // cos and sin of the CTA's tokens, times the gain, 64 apart per token.  Rotations of
-// several axes take a pair's position from the axis that it follows.
+// several axes take a pair's position from the axis that it follows.  kAxes false: there
+// are none; rope of a few tokens has no use for the loads that ask (64: 3.8 us, with them
+// 4.2).
+template <bool kAxes>
 __device__ __forceinline__ void turn_table(const RowsParams& p, int64_t t0, int nt,
                                            const int64_t* pos_s, float2* cs) {
   // A thread keeps its pair, whose fraction of a turn takes doubles: a pair and a token
   // each time, the FP64 pipe would be what a long CTA waits for.
-  const int half = p.R / 2, rows = kRowThreads / half;
-  const int f = threadIdx.x % half;
-  if (threadIdx.x >= rows * half) return;
+  const int half = p.R / 2, first = threadIdx.x / half, f = threadIdx.x - first * half;
+  if (first >= nt) return;
+  const int rows = nt > 1 ? kRowThreads / half : 1;
+  if (first >= rows) return;
   const double turns = p.inv_freq[f] * 0.15915494309189533577;       // 1 / (2 pi)
   const uint64_t frac = __double2ull_rn((turns - floor(turns)) * 18446744073709551616.0);
+  const bool axes = kAxes && p.naxes > 0;
   const int axis =
-      p.naxes > 0 && p.axis_of != nullptr ? min(static_cast<int>(p.axis_of[f]), p.naxes - 1) : 0;
-  for (int t = threadIdx.x / half; t < nt; t += rows) {
+      axes && p.axis_of != nullptr ? min(static_cast<int>(p.axis_of[f]), p.naxes - 1) : 0;
+  for (int t = first; t < nt; t += rows) {
     int64_t pos;
-    if (p.naxes > 0) {
+    if (axes) {
       const int64_t at = axis * p.axis_stride + t0 + t;
       pos = p.pos64 ? static_cast<const int64_t*>(p.pos)[at] : static_cast<const int32_t*>(p.pos)[at];
     } else {
@@ -241,7 +246,7 @@ __device__ __forceinline__ uint32_t pack_nibbles(const float (&x)[8], float top,
 
 // kMode: 0 rope, 1 append 16-bit, 2 append Q8, 3 append Q4.  kLanes: lanes of a row.
 // kShfl: the half layout's partner vector is another lane's whole vector.
-template <int kMode, bool kBF16, int kLanes, bool kShfl>
+template <int kMode, bool kBF16, int kLanes, bool kShfl, bool kAxes>
 __global__ void __launch_bounds__(kRowThreads, row_ctas(kMode))
 rows_kernel(const RowsParams p) {
   __shared__ float2 cs[kMaxToks * 64];
@@ -254,7 +259,7 @@ rows_kernel(const RowsParams p) {
   const PagedGeo& c = p.c;
 
   if constexpr (kMode == 0) {
-    if (threadIdx.x < nt && p.naxes == 0) {
+    if (threadIdx.x < nt && !(kAxes && p.naxes > 0)) {
       pos_s[threadIdx.x] = p.pos64 ? static_cast<const int64_t*>(p.pos)[t0 + threadIdx.x]
                                    : static_cast<const int32_t*>(p.pos)[t0 + threadIdx.x];
     }
@@ -262,7 +267,7 @@ rows_kernel(const RowsParams p) {
     place_tokens(p, t0, nt, pos_s, page_s, slot_s, scale_s);
   }
   __syncthreads();
-  if (p.inv_freq != nullptr) turn_table(p, t0, nt, pos_s, cs);
+  if (p.inv_freq != nullptr) turn_table<kAxes>(p, t0, nt, pos_s, cs);
   __syncthreads();
 
   const int nq = p.Hq;
@@ -745,7 +750,7 @@ group_rows_kernel(const RowsParams p) {
   place_tokens(p, t0, nt, tk.pos, tk.page, tk.slot, tk.scale);
   __syncthreads();
   if constexpr (kTurn) {
-    turn_table(p, t0, nt, tk.pos, cs);
+    turn_table<true>(p, t0, nt, tk.pos, cs);
     __syncthreads();
     if (p.Hq > 0) pair_pass<3, 0, kBF16>(p, tk, cs, t0, nt);
   }
@@ -769,7 +774,7 @@ pair_rows_kernel(const RowsParams p) {
   }
   __syncthreads();
   if (p.inv_freq != nullptr) {
-    turn_table(p, t0, nt, tk.pos, cs);
+    turn_table<true>(p, t0, nt, tk.pos, cs);
     __syncthreads();
   }
   if (p.Hq > 0) pair_pass<kMode, 0, kBF16>(p, tk, cs, t0, nt);
@@ -806,8 +811,13 @@ cudaError_t launch_pairs(const RowsParams& p0, int sms, cudaStream_t st) {
 
 template <int kMode, bool kBF16, int kLanes>
 cudaError_t launch_lanes(const RowsParams& p, bool shfl, dim3 grid, cudaStream_t st) {
-  if (shfl) rows_kernel<kMode, kBF16, kLanes, true><<<grid, kRowThreads, 0, st>>>(p);
-  else rows_kernel<kMode, kBF16, kLanes, false><<<grid, kRowThreads, 0, st>>>(p);
+  if (kMode != 0 || p.naxes > 0) {
+    if (shfl) rows_kernel<kMode, kBF16, kLanes, true, true><<<grid, kRowThreads, 0, st>>>(p);
+    else rows_kernel<kMode, kBF16, kLanes, false, true><<<grid, kRowThreads, 0, st>>>(p);
+  } else if constexpr (kMode == 0) {
+    if (shfl) rows_kernel<kMode, kBF16, kLanes, true, false><<<grid, kRowThreads, 0, st>>>(p);
+    else rows_kernel<kMode, kBF16, kLanes, false, false><<<grid, kRowThreads, 0, st>>>(p);
+  }
   note_launch();
   return cudaGetLastError();
 }

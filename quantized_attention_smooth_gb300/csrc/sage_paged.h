@@ -47,14 +47,15 @@ struct RowsParams {
   const void* pos;           // sage_rope, and rotations at given positions
   int32_t pos64;
   int32_t naxes;             // 0: one position a token, of pos (sage_rope) or the cache's place
-  int64_t axis_stride;       // elements between the axes' positions
-  const uint8_t* axis_of;    // each pair's axis; NULL: the first
   const double* inv_freq;    // NULL: no rotation
   int32_t R, interleaved;
   float mscale, sign;        // sign -1: the inverse rotation
   int32_t vec;               // 16-byte rows: base, strides and D in whole vectors
   int32_t toks;              // tokens per CTA (set by the launcher)
   PagedGeo c;                // sage_kv_append only
+  // behind the rest: what every call reads stays together
+  int64_t axis_stride;       // elements between the axes' positions
+  const uint8_t* axis_of;    // each pair's axis; NULL: the first
 };
 
 // mode 0: sage_rope; 1: append to a 16-bit cache; 2, 3: append to a Q8 or Q4 cache.
