@@ -465,7 +465,9 @@ SAGE_API sage_status sage_rope_axes(
  *     strides count bytes, multiples of 16.  Scales: k_groups and v_groups
  *     [num_pages][Hkv][page_size][Dp/32] fp16, at most 9352 and 1: K less its
  *     mean saturates at 7 * 9352, V at 448 v_scale as in SAGE_Q8.  Those of
- *     groups behind D are not read (sage_kv_append writes zeros).
+ *     groups behind D are not read (sage_kv_append writes zeros).  A group that
+ *     holds a NaN gets a NaN scale and zero codes, so that it reads back as NaN,
+ *     and an infinity saturates; other groups keep theirs.
  * page_size: a multiple of 16, up to 65536; D: a multiple of 8, 8..128; k and
  * v 16-byte aligned, strides multiples of 8 elements.  An 8-bit cache is read
  * fastest with D and strides of multiples of 16; otherwise 8 bytes at a time, which

@@ -223,16 +223,27 @@ __device__ __forceinline__ void turn_table(const RowsParams& p, int64_t t0, int 
   }
 }
 
+// The larger of two numbers; NaN if one of them is (fmaxf would give the other).
+__device__ __forceinline__ float max_or_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 // Q4: the group's scale from its largest, and the codes of eight channels plus 8, in
-// nibbles.
+// nibbles.  A group that holds a NaN has a scale of NaN and codes of zero, so that it
+// reads back as NaN; infinities take the largest scale and code.
 __device__ __forceinline__ __half group_scale(float top, float most) {
-  return __float2half_rn(fminf(__fmul_rn(top, kSeventh), most));
+  float s;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(s) : "f"(__fmul_rn(top, kSeventh)), "f"(most));
+  return __float2half_rn(s);
 }
 __device__ __forceinline__ uint32_t pack_nibbles(const float (&x)[8], float top, float inv) {
   float n[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) n[e] = __fmul_rn(x[e], inv);
-  if (!(__fmul_rn(top, inv) < 7.25f)) {         // a scale at its bounds
+  if (!(__fmul_rn(top, inv) < 7.25f)) {         // a scale at its bounds, or NaN
+    if (isnan(top)) return 0x88888888u;         // (its bits would borrow from other codes)
 #pragma unroll
     for (int e = 0; e < 8; ++e) n[e] = fminf(fmaxf(n[e], -7.0f), 7.0f);
   }
@@ -374,11 +385,11 @@ rows_kernel(const RowsParams p) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
               x[e] = what == 1 ? __fsub_rn(x[e], chan[e]) : __fmul_rn(x[e], chan[e]);
-              top = fmaxf(top, fabsf(x[e]));
+              top = max_or_nan(top, fabsf(x[e]));
             }
             // four lanes are a group
-            top = fmaxf(top, __shfl_xor_sync(kAll, top, 1));
-            top = fmaxf(top, __shfl_xor_sync(kAll, top, 2));
+            top = max_or_nan(top, __shfl_xor_sync(kAll, top, 1));
+            top = max_or_nan(top, __shfl_xor_sync(kAll, top, 2));
             if (r < rows && what != 0 && page >= 0) {
               const __half scale = group_scale(top, what == 1 ? kMostK : kMostV);
               const float s = __half2float(scale);
@@ -720,9 +731,9 @@ __device__ __forceinline__ void group_pass(const RowsParams& p, const Tokens& tk
       for (int e = 0; e < 16; ++e) {
         float& y = x[e / 8][e % 8];
         y = kVal ? __fmul_rn(y, chan[e]) : __fsub_rn(y, chan[e]);
-        top = fmaxf(top, fabsf(y));
+        top = max_or_nan(top, fabsf(y));
       }
-      top = fmaxf(top, __shfl_xor_sync(kAll, top, 1));
+      top = max_or_nan(top, __shfl_xor_sync(kAll, top, 1));
       const __half scale = group_scale(top, kVal ? kMostV : kMostK);
       const float s = __half2float(scale);
       const float inv = s > 0.0f ? __frcp_rn(s) : 0.0f;
