@@ -434,7 +434,7 @@ paged_few_kernel(const PagedAttnParams p, const __grid_constant__ Maps<kKind> ma
             slot[h] = 0;
             if (k0 >= 0 && kh <= p_hi && (kh + 15 >= lo || kh < sinks)) {
               const int pn = page_of(c, kh);
-              page[h] = table[pn];
+              page[h] = max(table[pn], -1);     // -2 is for keys that are not needed
               slot[h] = kh - pn * c.page_size;
             }
           }
