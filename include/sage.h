@@ -436,7 +436,8 @@ SAGE_API sage_status sage_rope(const void* q, const void* k, void* q_out, void* 
  * or an image's tokens): pair i turns by pos[axis_of[i]][t] * inv_freq[i].  Any
  * pair may follow any axis, with any frequency, so sections of the pairs, axes in
  * turn along them and axes with frequencies of their own are all served.
- *   pos: device, naxes rows of T positions, axis_stride elements apart; naxes 1..8.
+ *   pos: device, naxes rows of T positions, axis_stride elements apart (at least T, or
+ *       0: every axis has the same positions); naxes 1..8.
  *   axis_of: device uint8_t[R/2], entries below naxes (a larger one takes the last
  *       axis); NULL: axis 0 for every pair. */
 SAGE_API sage_status sage_rope_axes(

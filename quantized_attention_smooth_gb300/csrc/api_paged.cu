@@ -199,9 +199,10 @@ struct Axes {
 sage_status check_axes(int64_t naxes, int64_t stride, int64_t T) {
   if (naxes < 1 || naxes > 8)
     return refuse(SAGE_ERR_UNSUPPORTED, "naxes=%lld is outside 1..8", (long long)naxes);
-  if (naxes > 1 && (stride < T || stride >= kMaxStride))
-    return refuse(SAGE_ERR_INVALID_ARG, "axis_stride=%lld is below T=%lld or beyond 2^39",
-                  (long long)stride, (long long)T);
+  // 0: every axis has the same positions, which are only read
+  if (naxes > 1 && stride != 0 && (stride < T || stride >= kMaxStride))
+    return refuse(SAGE_ERR_INVALID_ARG, "axis_stride=%lld is neither 0 nor at least T=%lld and "
+                  "below 2^39", (long long)stride, (long long)T);
   return SAGE_OK;
 }
 

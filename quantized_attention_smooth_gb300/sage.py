@@ -671,8 +671,9 @@ def rope(q, k, positions, inv_freq, interleaved=False, mscale=1.0, inverse=False
     or (2i, 2i + 1) with `interleaved`.  q_out=q (k_out=k) turns in place.
     `inverse` turns back; applied to the outputs' gradients with the same
     mscale it gives the inputs' gradients.  With `axes` (uint8 (R/2,), see
-    rope_axes) positions are (A, T), a row for each of up to 8 axes, and pair i
-    turns by its axis' position.  Returns (q_out, k_out)."""
+    rope_axes) positions are (A, T), a row for each of up to 8 axes (one row for
+    all: positions.expand(A, T)), and pair i turns by its axis' position.  Returns
+    (q_out, k_out)."""
     dev, current = _device("rope", "q", q)
     (T, Hq, D), qs = _rows3("rope", "q", q, dev)
     dtype = _code16("rope", "q", q)
