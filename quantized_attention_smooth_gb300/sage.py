@@ -955,9 +955,11 @@ class PagePool:
     """The pages of a cache and who holds them, in the caller's int32 CUDA tensors:
     free (pages,), a stack of page indices whose next one is its last of left (1,)
     pages; table (requests, width), each request's pages; lens (requests,), its
-    cached length.  `PagePool.new` makes an empty pool."""
+    cached length.  `PagePool.new` makes an empty pool.  What is made here is made
+    and filled on `stream` (None: the current one); calls on another stream wait for
+    it first."""
 
-    def __init__(self, free, left, table, lens, page_size):
+    def __init__(self, free, left, table, lens, page_size, stream=None):
         if _torch is None:
             _bind_torch()
         if table.dim() != 2 or table.dtype != _torch.int32 or \
@@ -972,29 +974,34 @@ class PagePool:
             _int32s("PagePool", name, t, shape, self._dev)
         self.free, self.left, self.table, self.lens = free, left, table, lens
         self.page_size = int(page_size)
-        self.marks = _torch.zeros(requests, dtype=_torch.int32, device=table.device)
+        self.marks = _empty_on(stream, lambda: _torch.zeros(requests, dtype=_torch.int32,
+                                                            device=table.device))
         self._c = _PoolC(free.data_ptr(), left.data_ptr(), table.data_ptr(), lens.data_ptr(),
                          self.marks.data_ptr(), free.numel(), self.page_size, requests,
                          table.stride(0) if requests > 1 else width, width)
         self._ref = ctypes.byref(self._c)
 
     @classmethod
-    def new(cls, pages, page_size, requests, max_len, device="cuda"):
+    def new(cls, pages, page_size, requests, max_len, device="cuda", stream=None):
         """All `pages` free (0 goes first), `requests` of up to `max_len` tokens."""
         import torch
         i32 = dict(dtype=torch.int32, device=device)
-        return cls(torch.arange(pages - 1, -1, -1, **i32), torch.full((1,), pages, **i32),
-                   torch.full((requests, max(1, -(-int(max_len) // int(page_size)))), -1, **i32),
-                   torch.zeros(requests, **i32), page_size)
+        width = max(1, -(-int(max_len) // int(page_size)))
+        return cls(*_empty_on(stream, lambda: (
+            torch.arange(pages - 1, -1, -1, **i32), torch.full((1,), pages, **i32),
+            torch.full((requests, width), -1, **i32), torch.zeros(requests, **i32))),
+            page_size, stream)
 
 
 class PagedPlan:
     """The buffers of a step of n sequences with `rows` packed rows in all, at most
     max_q of one and max_kv cached tokens: cu_q, kv_lens and block_table, as the
     PagedBatch `batch`; positions and slots (int64, rows), slots as page * page_size
-    + place in the page; denied, an int32 scalar, sequences that got no pages."""
+    + place in the page; denied, an int32 scalar, sequences that got no pages.  They
+    are made and filled on `stream` (None: the current one); a step on another stream
+    waits for it first."""
 
-    def __init__(self, pool, n, rows, max_q, max_kv):
+    def __init__(self, pool, n, rows, max_q, max_kv, stream=None):
         import torch
         n, rows, max_kv = int(n), int(rows), int(max_kv)
         if n < 0 or rows < 0 or max_kv < 0:
@@ -1003,9 +1010,10 @@ class PagedPlan:
         width = max(1, -(-max_kv // pool.page_size))
         new = lambda *shape, dtype=torch.int32, fill=0: torch.full(
             shape, fill, dtype=dtype, device=pool.table.device)
-        self.cu_q, self.kv_lens, self.denied = new(n + 1), new(n), new()
-        self.block_table = new(n, width, fill=-1)
-        self.positions, self.slots = (new(rows, dtype=torch.int64, fill=-1) for _ in range(2))
+        self.cu_q, self.kv_lens, self.denied, self.block_table, self.positions, self.slots = \
+            _empty_on(stream, lambda: (
+                new(n + 1), new(n), new(), new(n, width, fill=-1),
+                *(new(rows, dtype=torch.int64, fill=-1) for _ in range(2))))
         self.batch = PagedBatch(self.cu_q, self.kv_lens, self.block_table, max_q, max_kv)
         self.n, self.rows = n, rows
         self._c = _PlanC(self.cu_q.data_ptr(), self.kv_lens.data_ptr(), self.block_table.data_ptr(),
