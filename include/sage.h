@@ -621,8 +621,9 @@ SAGE_API sage_status sage_paged_trim(const sage_page_pool* pool, const int32_t* 
  * type; lse: NULL or fp32 (T,Hq), the natural logarithm of the row's sum of
  * exponentials (of the smoothed logits with SAGE_Q8 and SAGE_Q4: all of a row's
  * logits lack sm_scale * q . k_mean).  A row without visible keys gives zeros and
- * -inf.  Keys and values that no row sees may hold anything; visible ones
- * are finite.  How the work is split into parts goes by the whole batch, so a
+ * -inf.  Keys and values that no row sees may hold anything; visible ones are
+ * finite (a NaN among them shows in the rows that see it, and perhaps in others
+ * of the call that do not).  How the work is split into parts goes by the whole batch, so a
  * sequence's rows may differ in their last bits between batches, never between
  * runs of one.  out overlaps no input.
  * Sequences of up to 16 rows (32 with D <= 64; new tokens times Hq/Hkv) take a

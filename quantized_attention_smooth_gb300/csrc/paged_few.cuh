@@ -1070,8 +1070,8 @@ paged_few_kernel(const PagedAttnParams p, const __grid_constant__ Maps<kKind> ma
         *reinterpret_cast<uint2*>(p.out + (tok * p.Hq + h) * c.D + ch) =
             make_uint2(pack2<kQBF16>(a.x, a.y), pack2<kQBF16>(a.z, a.w));
         if (p.lse != nullptr && ch == 0)
-          p.lse[tok * p.Hq + h] = sum > 0.0f ? (top + log2f(sum)) * 0.69314718055994530942f
-                                             : -INFINITY;
+          p.lse[tok * p.Hq + h] = sum == 0.0f ? -INFINITY
+                                              : (top + log2f(sum)) * 0.69314718055994530942f;
       };
       for (int i = tid; i < kRows * (kDp / 4); i += 32 * kWarps) {
         const int r = i / (kDp / 4), ch = 4 * (i % (kDp / 4));
@@ -1227,7 +1227,7 @@ paged_join_kernel(const PagedAttnParams p, int ctas) {
   const int64_t tok = static_cast<int64_t>(start) + rr / p.group;
   const int hq = h.head * p.group + rr % p.group;
   if (ch < p.c.D) {
-    float v = sum > 0.0f ? acc / sum : 0.0f;
+    float v = sum == 0.0f ? 0.0f : acc / sum;           // (a NaN shows)
     if (p.c.kind == kKindQ8) v *= p.c.v_scale[h.head * kDp + ch];
     if (p.c.kind == kKindQ4) v *= 64.0f * p.c.v_scale[h.head * kDp + ch];
     uint16_t bits;
@@ -1241,8 +1241,8 @@ paged_join_kernel(const PagedAttnParams p, int ctas) {
     p.out[(tok * p.Hq + hq) * p.c.D + ch] = bits;
   }
   if (p.lse != nullptr && ch == 0)
-    p.lse[tok * p.Hq + hq] = sum > 0.0f ? (top + log2f(sum)) * 0.69314718055994530942f
-                                        : -INFINITY;
+    p.lse[tok * p.Hq + hq] = sum == 0.0f ? -INFINITY
+                                         : (top + log2f(sum)) * 0.69314718055994530942f;
 }
 
 template <int kKind, bool kQBF16, int kDp, int kNr, int kForm = 0>

@@ -1317,7 +1317,7 @@ paged_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                   make_uint4(u[m][0], u[m][1], u[m][2], u[m][3]);
         }
         if (has && p.lse != nullptr)
-          p.lse[orow] = l > 0.0f ? (ref + log2f(l)) * 0.69314718055994530942f : -INFINITY;
+          p.lse[orow] = l == 0.0f ? -INFINITY : (ref + log2f(l)) * 0.69314718055994530942f;
       } else {
         const int which = it.first == 0 ? 1 : 0;
         uint8_t* part = many_part(p.parts, cta, which);
@@ -1432,8 +1432,8 @@ paged_many_join_kernel(const PagedAttnParams p, int ctas) {
         make_uint2(pack2<kQBF16>(a.x, a.y), pack2<kQBF16>(a.z, a.w));
   }
   if (p.lse != nullptr && grp == 0)
-    p.lse[tok * p.Hq + hq] = sum > 0.0f ? (top + log2f(sum)) * 0.69314718055994530942f
-                                        : -INFINITY;
+    p.lse[tok * p.Hq + hq] = sum == 0.0f ? -INFINITY
+                                         : (top + log2f(sum)) * 0.69314718055994530942f;
 }
 
 // Whether pages are whole boxes of a 128-key tile, or hold whole tiles, with
