@@ -191,8 +191,8 @@ __device__ __forceinline__ void place_tokens(const RowsParams& p, int64_t t0, in
 
 // cos and sin of the CTA's tokens, times the gain, 64 apart per token.  Rotations of
 // several axes take a pair's position from the axis that it follows.  kAxes false: there
-// are none; rope of a few tokens has no use for the loads that ask (64: 3.8 us, with them
-// 4.2).
+// are none; few tokens have no use for the loads that ask (rope of 64: 3.8 us, with them
+// 4.2; appends of 64 to 300 3 to 4 % longer with them).
 template <bool kAxes>
 __device__ __forceinline__ void turn_table(const RowsParams& p, int64_t t0, int nt,
                                            const int64_t* pos_s, float2* cs) {
@@ -822,10 +822,10 @@ cudaError_t launch_pairs(const RowsParams& p0, int sms, cudaStream_t st) {
 
 template <int kMode, bool kBF16, int kLanes>
 cudaError_t launch_lanes(const RowsParams& p, bool shfl, dim3 grid, cudaStream_t st) {
-  if (kMode != 0 || p.naxes > 0) {
+  if (p.naxes > 0) {
     if (shfl) rows_kernel<kMode, kBF16, kLanes, true, true><<<grid, kRowThreads, 0, st>>>(p);
     else rows_kernel<kMode, kBF16, kLanes, false, true><<<grid, kRowThreads, 0, st>>>(p);
-  } else if constexpr (kMode == 0) {
+  } else {
     if (shfl) rows_kernel<kMode, kBF16, kLanes, true, false><<<grid, kRowThreads, 0, st>>>(p);
     else rows_kernel<kMode, kBF16, kLanes, false, false><<<grid, kRowThreads, 0, st>>>(p);
   }
