@@ -981,29 +981,40 @@ cudaError_t launch_gather(const RowsParams& p, bool bf16, int sms, cudaStream_t 
 
 cudaError_t launch_rows(const RowsParams& p, int mode, bool bf16, int sms, cudaStream_t st) {
   // Two vectors a lane (over four bits, two lanes a group), for whole vectors: fewer
-  // instructions a row, but one CTA's chain of loads is longer, so one vector a lane has
-  // the shorter way through few tokens.  Measured, one vector against the other (us; 32
-  // heads of q and 8 of k and v, D = 128, 152 SMs):
-  //   tokens                        700         1500        2500        5000        9872
-  //   rope, half layout          10.8  9.7   14.7 13.9   22.2 14.5   36.7 22.0   68.1 38.2
-  //   16 bits as they are         4.6  6.3    5.1  7.0    6.2  7.5   10.1  9.4   15.9 16.2
-  //   16 bits, half layout       11.6 12.0   16.8 16.6   22.6 17.3   46.4 26.1   81.1 44.6
-  //   16 bits, interleaved        9.1 12.1   12.1 16.6   16.6 18.3   33.6 28.2   56.2 49.3
-  //   Q8 as it is                 6.0 11.1    7.4 13.8    8.7 15.2   14.5 16.9   23.7 20.7
-  //   Q8, half layout            13.5 15.5   19.8 19.5   27.0 25.5   53.4 36.4   94.4 56.2
-  //   Q8, interleaved            10.8 17.8   14.7 22.4   19.8 29.9   40.1 41.8   68.5 66.2
-  //   Q4 as it is                 6.3 10.8    7.5 13.8    9.4 15.2   15.9 16.9   25.5 20.3
-  //   Q4, half layout            13.5 16.4   19.8 21.2   27.2 23.4   52.6 34.7   93.7 57.2
-  //   Q4, interleaved            10.8 16.2   14.7 20.7   20.0 23.4   39.4 33.6   67.4 55.8
+  // instructions a row, but q, k and v go in passes of their own, one after another, and a
+  // pass of few heads leaves lanes idle, so one vector a lane has the shorter way through
+  // few tokens, and through more of them where heads are few.  Measured, one vector against
+  // the other (us; bf16, 152 SMs; q heads on kv heads x channels, tokens):
+  //                      32 on 8 x 128                      8 on 1 x 64                       16 on 16 x 80
+  //                   600         3000       9000        3000       9000       27000       1000       4500
+  //   rope, half     8.4  7.4   22.3 17.0   60.9 35.2    7.8 17.1   17.1 18.6   41.6 26.9    8.9  9.0   22.2 14.9
+  //   16 bits as is  4.2  5.8    6.3  7.8   14.6 15.6    5.8 22.3   12.5 23.2   31.9 26.7    5.9  6.7   13.1 10.5
+  //   16 bits, half  9.5  9.9   25.3 20.2   75.2 41.8    9.9 27.2   24.2 29.1   64.8 39.1   11.4 11.9   31.1 19.1
+  //   16 bits, near  7.9 10.4   16.6 21.1   53.5 46.3    7.9 27.4   18.5 29.8   47.4 40.1    8.9 11.5   24.2 19.1
+  //   Q8 as is       5.3 13.0    8.9 15.4   21.7 19.5    8.8  9.3   21.7  9.8   57.5 10.0    8.4 14.4   20.6 18.7
+  //   Q8, half      11.4 17.0   29.8 25.2   87.3 51.2   12.9 14.5   33.0 16.6   90.3 22.7   14.5 18.1   38.3 26.0
+  //   Q8, near       9.4 19.1   21.3 29.5   64.8 60.1   10.9 16.0   27.4 18.6   73.5 26.3   12.4 20.2   30.9 28.2
+  //   Q4 as is       5.8 13.1    9.9 15.6   24.3 19.4    8.9  8.9   22.2  9.4   58.0  9.9    9.9 12.4   24.2 18.1
+  //   Q4, half      11.4 12.9   30.4 26.4   87.3 53.0   12.9 12.5   33.5 14.4   91.3 22.7   15.3 16.1   41.7 27.3
+  //   Q4, near       9.4 12.5   21.3 25.9   64.4 52.2   10.8 12.9   27.8 14.4   73.0 22.1   13.1 15.6   34.5 25.2
+  // Hence a least number of tokens per SM, fixed + by_pass * (the sum over the passes of 1 /
+  // (lanes of a row x heads)).  Over nine shapes from 1 to 64 heads at 300 to 60000 tokens the
+  // choice takes 0.7 % longer than the faster kernel on average and 27 % at most.
   // Interleaved rope is as fast either way where rows fill the lanes of one vector each
-  // (16000 tokens x 80 heads x 128: 111 118; 76000 x 40: 265 276) and stays there; where
-  // they leave lanes idle it goes by the table (65000 x 32 x 80: 159 137).
+  // (16000 tokens x 80 heads x 128: 111 118; 76000 x 40: 265 276) and stays there.
+  struct Least {
+    double fixed, by_pass;
+  };
+  constexpr Least kAsIs[4] = {{0, 0}, {14, 500}, {28, 0}, {28, 0}};   // (rope has no row as it is)
+  constexpr Least kApart[4] = {{1, 500}, {1, 300}, {10, 50}, {14, 0}};
+  constexpr Least kNear[4] = {{8, 1200}, {14, 500}, {24, 0}, {28, 0}};
   const bool apart = p.inv_freq != nullptr && !p.interleaved;
   const bool neighbours = p.inv_freq != nullptr && p.interleaved;
-  // tokens per SM (rope has no row as it is)
-  constexpr int kAsIs[4] = {0, 28, 48, 48}, kApart[4] = {4, 4, 10, 13}, kNear[4] = {28, 28, 48, 28};
-  const int least = apart ? kApart[mode] : neighbours ? kNear[mode] : kAsIs[mode];
-  const bool pairs = p.vec && p.T >= static_cast<int64_t>(least) * sms &&
+  const Least least = apart ? kApart[mode] : neighbours ? kNear[mode] : kAsIs[mode];
+  const double passes = ((p.Hq > 0 ? 1.0 / p.Hq : 0.0) +
+                         (p.Hkv > 0 ? (mode == 0 ? 1.0 : 2.0) / p.Hkv : 0.0)) /
+                        (p.D <= 64 ? 8 : 16);
+  const bool pairs = p.vec && p.T >= (least.fixed + least.by_pass * passes) * sms &&
                      !(apart && p.R % 16 != 0) && !(neighbours && mode == 0 && p.D % 64 == 0);
   if (pairs) {
     if (mode == 3)
