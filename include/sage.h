@@ -617,8 +617,12 @@ SAGE_API sage_status sage_paged_trim(const sage_page_pool* pool, const int32_t* 
 /* Attention of the new tokens (q (T,Hq,D)) over the cache, causal: the row
  * at position p sees the keys j <= p of its sequence, and with window > 0 of
  * those only j > p - window and j < sinks.  Logits, softmax and sums in fp32,
- * P rounded to 16 bits for the tensor cores.  out: dense (T,Hq,D) of q's
- * type; lse: NULL or fp32 (T,Hq), the natural logarithm of the row's sum of
+ * P rounded to 16 bits for the tensor cores.  Over SAGE_Q4 few rows (below) take K's
+ * codes exactly and round P times a value's scale to fp16, once; many rows round every
+ * element n s of K and V to fp16 first, by up to 2^-11 of it (2^-25 where it is below
+ * 2^-14), which moves a logit by up to 2^-11 sm_scale sum |q_c k_c|, the row's lse by as
+ * much and a weight by twice that of itself: the same token's results in the two differ
+ * by that.  out: dense (T,Hq,D) of q's type; lse: NULL or fp32 (T,Hq), the natural logarithm of the row's sum of
  * exponentials (of the smoothed logits with SAGE_Q8 and SAGE_Q4: all of a row's
  * logits lack sm_scale * q . k_mean).  A row without visible keys gives zeros and
  * -inf.  Keys and values that no row sees may hold anything; visible ones are

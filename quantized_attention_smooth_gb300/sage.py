@@ -1088,7 +1088,8 @@ def attn_paged(cache, batch, q, out=None, window=0, sinks=0, sm_scale=None, lse=
     """Attention of the batch's new tokens, q (T, Hq, D), over the cache:
     causal, with window > 0 only the last `window` keys and the first `sinks`
     ones.  Returns out (T, Hq, D) of q's type; lse, if given, is a float32
-    (T, Hq) tensor that receives the log-sum-exp of every row."""
+    (T, Hq) tensor that receives the log-sum-exp of every row.  Over four bits
+    batches of many rows round K and V to fp16 (sage_attn_paged in sage.h)."""
     dev, current = _device("attn_paged", "q", q)
     if cache._dev != dev or batch._dev != dev:
         _off_cache("attn_paged", cache, batch, dev)
