@@ -546,8 +546,9 @@ SAGE_API sage_status sage_kv_append_axes(
  * (T,Hkv,D) of `dtype` (a 16-bit cache: its own): what sage_kv_append stored of
  * them, rotation included, K with its mean.  A batch whose new tokens are all
  * the cached ones gives whole sequences, for a dense call over a cached prefix
- * or for another cache.  Tokens at negative positions and on pages outside the
- * cache give zeros; rows behind cu_q[nseq] are left as they are.
+ * or for another cache.  Tokens at negative positions, on pages outside the cache
+ * and of sequences whose entries break the batch's bounds give zeros; rows behind
+ * cu_q[nseq] are left as they are.
  *   k_strides, v_strides: host int64[2], {token, head}; NULL: dense. */
 SAGE_API sage_status sage_kv_gather(const sage_paged_cache* cache, const sage_paged_batch* batch,
                                     void* k, void* v, int dtype, const int64_t* k_strides,
@@ -571,9 +572,13 @@ typedef struct {
 } sage_page_pool;
 
 /* What a step of n sequences gets: cu_q [n+1], kv_lens [n] and block_table
- * [n][table_stride] make a sage_paged_batch; of each of `rows` packed rows, its
- * position in its sequence and its slot, page * page_size + place in the page
- * (either may be NULL); denied [1]: sequences that got no pages. */
+ * [n][table_stride] make a sage_paged_batch; of each packed row below cu_q[n] (and
+ * below `rows`, what the arrays hold), its position in its sequence and its slot,
+ * page * page_size + place in the page (either may be NULL); denied [1]: sequences
+ * that got no pages.  Rows from cu_q[n] on are left as they are, as everywhere: in
+ * buffers that serve several steps they hold an earlier step's places, whose pages
+ * may have gone to other requests since, so whoever writes by the slots stops at
+ * cu_q[n]. */
 typedef struct {
   int32_t* cu_q;
   int32_t* kv_lens;
@@ -593,11 +598,15 @@ typedef struct {
  * Requests are served in order while the pages last: once one's pages do not
  * fit, it and every later one that needs pages are denied.  A denied sequence keeps
  * its rows (position and slot -1) and its length in the pool, and its kv_lens[i] is
- * 0, which sage_kv_append and sage_attn_paged take for rows without a place.
+ * 0, which sage_kv_append and sage_attn_paged take for rows without a place (nothing
+ * is stored, out is zero).
  * Denied as well, and recorded in the workspace's status word: a request outside the
- * pool or given before in the same call, a length below zero, more than max_q new
- * tokens or max_kv in all, more pages than either table has columns, rows that pass
- * `rows` (nothing is written behind it).  Page indices are handed out as they lie on
+ * pool or given before in the same call, a length below zero (it has no rows), more
+ * than max_q new tokens or max_kv in all, more pages than either table has columns,
+ * rows that pass `rows` (nothing is written behind it).  With more than max_q new
+ * tokens, or rows that pass `rows`, the sequence breaks the batch's bounds as well, and
+ * every later one whose rows pass `rows` with it: the paged calls skip it, so that
+ * nothing is stored and its rows of out are left as they are.  Page indices are handed out as they lie on
  * the stack.  n up to 65536, page_size as in sage_paged_cache; the workspace is the
  * paged calls'. */
 SAGE_API sage_status sage_paged_step(const sage_page_pool* pool, const sage_paged_plan* plan,

@@ -910,8 +910,8 @@ def kv_gather(cache, batch, rows, dtype=None, k_out=None, v_out=None, ws=None, s
     """The batch's `rows` tokens read back from the cache: k and v (rows, Hkv, D) of
     `dtype` (a 16-bit cache: its own), as kv_append stored them, k with its mean.
     A batch whose new tokens are all the cached ones gives whole sequences.
-    Tokens without a place give zeros; rows behind the batch's are left as they are
-    in k_out and v_out."""
+    Tokens without a place and of sequences beyond the batch's bounds give zeros; rows
+    behind the batch's are left as they are in k_out and v_out."""
     if _torch is None:
         _bind_torch()
     dev, T = _get_device(), int(rows)
@@ -997,9 +997,11 @@ class PagedPlan:
     """The buffers of a step of n sequences with `rows` packed rows in all, at most
     max_q of one and max_kv cached tokens: cu_q, kv_lens and block_table, as the
     PagedBatch `batch`; positions and slots (int64, rows), slots as page * page_size
-    + place in the page; denied, an int32 scalar, sequences that got no pages.  They
-    are made and filled on `stream` (None: the current one); a step on another stream
-    waits for it first."""
+    + place in the page; denied, an int32 scalar, sequences that got no pages.
+    Positions and slots from cu_q[n] on keep what an earlier step wrote there, whose
+    pages may be another request's by now: go by cu_q.  The buffers are made and
+    filled on `stream` (None: the current one); a step on another stream waits for it
+    first."""
 
     def __init__(self, pool, n, rows, max_q, max_kv, stream=None):
         import torch
@@ -1040,7 +1042,8 @@ def paged_step(pool, plan, requests, new_lens, ws=None, stream=None):
     Sequences whose pages do not fit (and every later one that needs pages) are
     denied: their rows have position and slot -1, kv_lens 0, and the pool's length
     stays.  Bad requests and lengths are denied and recorded in the workspace's
-    status word.  Returns plan.batch."""
+    status word; of those with more than max_q new tokens, or rows behind the plan's,
+    attn_paged leaves the rows unwritten.  Returns plan.batch."""
     dev, ws, handle = _pool_call("paged_step", pool, requests, ws, stream)
     if requests.shape[0] != plan.n or plan.batch._dev != dev:
         raise ValueError(f"paged_step: {requests.shape[0]} requests on cuda:{dev} for a plan of "
