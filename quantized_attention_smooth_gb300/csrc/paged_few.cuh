@@ -423,18 +423,22 @@ paged_few_kernel(const PagedAttnParams p, const __grid_constant__ Maps<kKind> ma
         const int64_t page_b = static_cast<int64_t>(c.Hkv) * c.page_size * L::kScaleB;
         const int64_t head_b = static_cast<int64_t>(kvh) * c.page_size * L::kScaleB + 16 * j8;
         int k0 = -1, page[kSubs], slot[kSubs];
-        auto locate = [&](int u) {              // a block's first key and its pages
+        bool need[kSubs];
+        // a block's first key and its pages; the table's entries are used a step later, and
+        // nothing here waits for them (64 x 8520 keys: 162 us, with a bound on them 180)
+        auto locate = [&](int u) {
           const int vb = u * kWarps + w;
           k0 = kKeys * (vb < sp.sink ? vb : vb - sp.sink + sp.from);
           if (!(vb < sp.count && k0 <= p_hi && (k0 + kKeys - 1 >= lo || k0 < sinks))) k0 = -1;
 #pragma unroll
           for (int h = 0; h < kSubs; ++h) {
             const int kh = k0 + 16 * h;
-            page[h] = -2;
+            need[h] = k0 >= 0 && kh <= p_hi && (kh + 15 >= lo || kh < sinks);
+            page[h] = -1;
             slot[h] = 0;
-            if (k0 >= 0 && kh <= p_hi && (kh + 15 >= lo || kh < sinks)) {
+            if (need[h]) {
               const int pn = page_of(c, kh);
-              page[h] = max(table[pn], -1);     // -2 is for keys that are not needed
+              page[h] = table[pn];
               slot[h] = kh - pn * c.page_size;
             }
           }
@@ -456,7 +460,7 @@ paged_few_kernel(const PagedAttnParams p, const __grid_constant__ Maps<kKind> ma
             for (int h = 0; h < kSubs; ++h) {
               const bool there =
                   static_cast<uint32_t>(page[h]) < static_cast<uint32_t>(c.num_pages);
-              if (!there && page[h] != -2) atomicOr(c.status, kStatusBadPage);
+              if (!there && need[h]) atomicOr(c.status, kStatusBadPage);
               if (half == h)
                 tma_load_4d(dst + stage4 * L::kBlockB + (kv * kKeys + 16 * h) * kRowB, map, 0,
                             slot[h], kvh, there ? page[h] : static_cast<int>(c.num_pages),
