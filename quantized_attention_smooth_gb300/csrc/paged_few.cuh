@@ -497,10 +497,13 @@ paged_few_kernel(const PagedAttnParams p, const __grid_constant__ Maps<kKind> ma
         // are on their way while the other warps join their parts of this one
         send(it, first_unit + sent, first_unit + count);
         FewItem& next = it_s[nth & 1];
-        if (lane == 0) {
-          next = it;
-          next.cur += count;
-          next.off += count;
+        if (lane == 0) {                        // (the rest of `it` is the other warps')
+          next.cur = it.cur + count;
+          next.off = it.off + count;
+          next.last = it.last;
+          next.total = it.total;
+          next.busy = it.busy;
+          next.s = it.s;
           seek(next);
         }
         __syncwarp();
