@@ -511,7 +511,7 @@ sage_status sage_paged_step(const sage_page_pool* pool, const sage_paged_plan* p
   p.plan_width = static_cast<int32_t>(plan->table_width);
   p.max_q = plan->max_q;
   p.max_kv = plan->max_kv;
-  const cudaError_t e = launch_paged_step(p, sms, reinterpret_cast<cudaStream_t>(stream));
+  const cudaError_t e = launch_paged_step(p, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? succeeded() : cuda_refused(e, "page tables launch");
 }
 
@@ -527,7 +527,7 @@ sage_status sage_paged_trim(const sage_page_pool* pool, const int32_t* requests,
   int sms = 0;
   if ((s = require_device(&sms)) != SAGE_OK) return s;
   p.new_lens = keep_lens;
-  const cudaError_t e = launch_paged_trim(p, sms, reinterpret_cast<cudaStream_t>(stream));
+  const cudaError_t e = launch_paged_trim(p, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? succeeded() : cuda_refused(e, "page release launch");
 }
 

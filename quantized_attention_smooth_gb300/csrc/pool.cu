@@ -331,13 +331,13 @@ trim_kernel(const PoolParams p) {
 
 }  // namespace
 
-cudaError_t launch_paged_step(const PoolParams& p, int, cudaStream_t st) {
+cudaError_t launch_paged_step(const PoolParams& p, cudaStream_t st) {
   step_kernel<<<kCluster, kThreads, 0, st>>>(p);
   note_launch();
   return cudaGetLastError();
 }
 
-cudaError_t launch_paged_trim(const PoolParams& p, int, cudaStream_t st) {
+cudaError_t launch_paged_trim(const PoolParams& p, cudaStream_t st) {
   trim_kernel<<<kCluster, kThreads, 0, st>>>(p);
   note_launch();
   return cudaGetLastError();

@@ -88,8 +88,8 @@ struct PoolParams {
   uint32_t* status;
 };
 constexpr int kMaxStepSeqs = 65536;
-cudaError_t launch_paged_step(const PoolParams& p, int sms, cudaStream_t st);
-cudaError_t launch_paged_trim(const PoolParams& p, int sms, cudaStream_t st);
+cudaError_t launch_paged_step(const PoolParams& p, cudaStream_t st);
+cudaError_t launch_paged_trim(const PoolParams& p, cudaStream_t st);
 
 constexpr int kArrivalBytes = 8192 - 256;
 
