@@ -278,22 +278,12 @@ paged_few_kernel(const PagedAttnParams p, const __grid_constant__ Maps<kKind> ma
   // Teams of CTAs work on as many heads side by side (4 bits only, see launch_few).
   const int team = kQ4 ? p.team : 1, member = kQ4 ? cta % team : 0;
   const int seat = kQ4 ? cta / team : cta, seats = kQ4 ? gridDim.x / team : gridDim.x;
-  const int64_t ts = c.token_stride * kEl;
   uint8_t* const ring = ring_s + warp * kStages * L::kBlockB;
-  // Copies: lane -> vector lc of every kRows32-th row.  A vector's place in its row
-  // is turned by the row, so that the reads below hit every bank once.
-  constexpr int kRows32 = 32 / kChunks;
-  const int lc = lane % kChunks, lr = lane / kChunks;
-  const int lc_left = c.D - lc * (kQ4 ? 32 : 16 / kEl);   // channels from the vector's first on
-  // (4 bits: eight rows of one vector, as ldmatrix takes them)
+  // where a vector of a key lies in a block (4 bits: eight rows of one vector, as ldmatrix
+  // takes them)
   auto k_at = [](int row, int vec) {
     if constexpr (kQ4) return row * kRowB + ((vec ^ ((row >> (kChunks == 4 ? 1 : 2)) & (kChunks - 1))) << 4);
     return row * kRowB + ((kChunks >= 8 ? vec ^ ((row & 1) << 2) : vec) << 4);
-  };
-  auto v_at = [&](int row, int vec) {
-    if constexpr (kQ4) return kKeys * kRowB + k_at(row, vec);
-    return (16 + row) * kRowB +
-           ((kChunks >= 8 ? vec ^ (row & 6) : vec ^ ((row >> 1) & 3)) << 4);
   };
   if (!p.join_inside) asm volatile("griddepcontrol.launch_dependents;");
 
@@ -520,10 +510,6 @@ paged_few_kernel(const PagedAttnParams p, const __grid_constant__ Maps<kKind> ma
       const int lo = p.window > 0 ? max(0, p_lo - p.window + 1) : 0;        // first key of row0
       const int lo_hi = p.window > 0 ? max(0, p_hi - p.window + 1) : 0;     // of the last row
 
-      const int32_t* const table = c.table + s * c.table_stride;
-      // this lane's vector in a block's keys and values (bytes)
-      const int64_t lane_off = (kvh * c.head_stride + lr * c.token_stride) * kEl + 16 * lc;
-
       const int end_unit = first_unit + count;
       // ---- the rows' queries, as the B operand of S^T
       uint32_t qw[kNr][kDp / 8];
@@ -627,72 +613,7 @@ paged_few_kernel(const PagedAttnParams p, const __grid_constant__ Maps<kKind> ma
           for (int e = 0; e < 4; ++e) o[j][nr][e] = 0.0f;
       }
 
-      // Vectors of channels from D on are never loaded: zero once.
-      if (kForm != 0 && !kQ4) {
-        for (int i = lane; i < kStages * L::kBlockB / 16; i += 32)
-          reinterpret_cast<uint4*>(ring)[i] = make_uint4(0, 0, 0, 0);
-        __syncwarp();
-      }
-      // A step is a block of kKeys keys.  Its first key (-1: none that a row sees):
-      auto key_of = [&](int unit) {
-        const int vb = unit * kWarps + warp;
-        const int k0 = kKeys * (vb < sp.sink ? vb : vb - sp.sink + sp.from);
-        return vb < sp.count && k0 <= p_hi && (k0 + kKeys - 1 >= lo || k0 < sinks) ? k0 : -1;
-      };
       auto seen = [&](int j) { return j <= p_hi && (j >= lo || j < sinks); };
-      int next_key0 = -1, next_page = -1;
-      auto locate = [&](int unit) {             // the table's entry, used a step later
-        next_key0 = key_of(unit);
-        if (next_key0 >= 0) next_page = table[page_of(c, next_key0)];
-      };
-      // Starts the copies of the located block into a stage; rows that no row of
-      // the tile sees become zero (0 times what lies there could be NaN).
-      auto issue = [&](int stage) {
-        const int k0 = next_key0;
-        if (k0 >= 0) {
-          int64_t at = 0;
-          const bool there =
-              static_cast<uint32_t>(next_page) < static_cast<uint32_t>(c.num_pages);
-          const uint32_t dst = smem_u32(ring + stage * L::kBlockB);
-          const float* scales = c.k_scale;
-          if (there) {
-            const int slot = k0 - page_of(c, k0) * c.page_size;
-            at = (next_page * c.page_stride + static_cast<int64_t>(slot) * c.token_stride) * kEl;
-            if (kQ8)
-              scales += (static_cast<int64_t>(next_page) * c.Hkv + kvh) * c.page_size + slot +
-                        4 * (lane & 3);
-          } else if (lane == 0) {
-            atomicOr(c.status, kStatusBadPage);
-          }
-          if (kQ8 && lane < 4)
-            copy16(dst + 32 * kRowB + 16 * lane, reinterpret_cast<const uint8_t*>(scales),
-                   there ? 16 : 0);
-          const bool whole = there && k0 + 15 <= p_hi && (k0 >= lo || k0 + 15 < sinks);
-          const uint8_t* src_k = c.k + at + lane_off;
-          const uint8_t* src_v = c.v + at + lane_off;
-          const int64_t down = kRows32 * ts;
-#pragma unroll
-          for (int i = 0; i < 16 / kRows32; ++i) {
-            const int row = lr + i * kRows32;
-            const bool see = whole || (there && seen(k0 + row));
-            copy_part<kForm>(dst + k_at(row, lc), see ? src_k : c.k, see, lc_left);
-            copy_part<kForm>(dst + v_at(row, lc), see ? src_v : c.v, see, lc_left);
-            src_k += down;
-            src_v += down;
-          }
-        }
-        asm volatile("cp.async.commit_group;" ::: "memory");
-      };
-
-      if constexpr (!kQ4) {
-        locate(first_unit);
-#pragma unroll
-        for (int i = 0; i < kStages - 1; ++i) {
-          issue(i);
-          next_key0 = -1;
-          if (first_unit + i + 1 < end_unit) locate(first_unit + i + 1);
-        }
-      }
       if constexpr (kQ4) {
         constexpr int kG = kDp / 32, kX = kSubs * kNr;
         // waits for the block in a stage; its first key (-1: nothing that a row sees)
@@ -850,170 +771,246 @@ paged_few_kernel(const PagedAttnParams p, const __grid_constant__ Maps<kKind> ma
           if (lane == 0) mbar_arrive(&empty_s[at]);
           next_stage();
         }
-      }
-      int stage = 0;
-      for (int u = kQ4 ? end_unit : first_unit; u < end_unit; ++u) {
-        asm volatile("cp.async.wait_group %0;" :: "n"(kStages - 2) : "memory");
-        __syncwarp();                           // every lane's copies; and the last stage is read
-        issue(stage == 0 ? kStages - 1 : stage - 1);
-        next_key0 = -1;
-        if (u + kStages < end_unit) locate(u + kStages);
-        const uint8_t* const block = ring + stage * L::kBlockB;
-        stage = stage + 1 == kStages ? 0 : stage + 1;
-        // ---- S^T, in two chains of products
-        const int cur0 = key_of(u);
-        if (cur0 < 0) continue;
-        float x[kNr][4], x2[kNr][4];
-#pragma unroll
-        for (int nr = 0; nr < kNr; ++nr)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) x[nr][e] = x2[nr][e] = 0.0f;
-#pragma unroll
-        for (int v = 0; v < kKw / 4; ++v) {
-          const uint4 ka = *reinterpret_cast<const uint4*>(block + k_at(g, 4 * v + t));
-          const uint4 kb = *reinterpret_cast<const uint4*>(block + k_at(g + 8, 4 * v + t));
-          const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
-          constexpr int kPer = kQ8 ? 4 : 2;     // k-steps of a vector
-#pragma unroll
-          for (int i = 0; i < kPer; ++i) {
-            uint32_t a0, a1, a2, a3;
-            if constexpr (kQ8) {
-              int8_to_half(wa[i], a0, a2);
-              int8_to_half(wb[i], a1, a3);
-            } else {
-              a0 = wa[2 * i]; a2 = wa[2 * i + 1];
-              a1 = wb[2 * i]; a3 = wb[2 * i + 1];
-            }
-            const int step = kPer * v + i;
-#pragma unroll
-            for (int nr = 0; nr < kNr; ++nr)
-              mma<kMmaBF16>((step & 1) ? x2[nr] : x[nr], a0, a1, a2, a3, qw[nr][2 * step],
-                            qw[nr][2 * step + 1]);
-          }
+      } else {
+        const int32_t* const table = c.table + s * c.table_stride;
+        const int64_t ts = c.token_stride * kEl;
+        // Copies: lane -> vector lc of every kRows32-th row.  A vector's place in its row
+        // is turned by the row, so that the reads below hit every bank once.
+        constexpr int kRows32 = 32 / kChunks;
+        const int lc = lane % kChunks, lr = lane / kChunks;
+        const int lc_left = c.D - lc * (16 / kEl);          // channels from the vector's first on
+        auto v_at = [](int row, int vec) {
+          return (16 + row) * kRowB +
+                 ((kChunks >= 8 ? vec ^ (row & 6) : vec ^ ((row >> 1) & 3)) << 4);
+        };
+        // this lane's vector in a block's keys and values (bytes)
+        const int64_t lane_off = (kvh * c.head_stride + lr * c.token_stride) * kEl + 16 * lc;
+        // Vectors of channels from D on are never loaded: zero once.
+        if (kForm != 0) {
+          for (int i = lane; i < kStages * L::kBlockB / 16; i += 32)
+            reinterpret_cast<uint4*>(ring)[i] = make_uint4(0, 0, 0, 0);
+          __syncwarp();
         }
-        float ks[2] = {1.0f, 1.0f};
-        if constexpr (kQ8) {
-          ks[0] = reinterpret_cast<const float*>(block + 32 * kRowB)[g];
-          ks[1] = reinterpret_cast<const float*>(block + 32 * kRowB)[g + 8];
-        }
-        {
-          // ---- logits, masks, running maximum and sum
-          const bool full =
-              cur0 + 15 <= p_lo && (cur0 >= lo_hi || cur0 + 15 < sinks);
-          bool over = false;                    // a logit has outgrown its row's reference
+        // A step is a block of kKeys keys.  Its first key (-1: none that a row sees):
+        auto key_of = [&](int unit) {
+          const int vb = unit * kWarps + warp;
+          const int k0 = kKeys * (vb < sp.sink ? vb : vb - sp.sink + sp.from);
+          return vb < sp.count && k0 <= p_hi && (k0 + kKeys - 1 >= lo || k0 < sinks) ? k0 : -1;
+        };
+        int next_key0 = -1, next_page = -1;
+        auto locate = [&](int unit) {             // the table's entry, used a step later
+          next_key0 = key_of(unit);
+          if (next_key0 >= 0) next_page = table[page_of(c, next_key0)];
+        };
+        // Starts the copies of the located block into a stage; rows that no row of
+        // the tile sees become zero (0 times what lies there could be NaN).
+        auto issue = [&](int stage) {
+          const int k0 = next_key0;
+          if (k0 >= 0) {
+            int64_t at = 0;
+            const bool there =
+                static_cast<uint32_t>(next_page) < static_cast<uint32_t>(c.num_pages);
+            const uint32_t dst = smem_u32(ring + stage * L::kBlockB);
+            const float* scales = c.k_scale;
+            if (there) {
+              const int slot = k0 - page_of(c, k0) * c.page_size;
+              at = (next_page * c.page_stride + static_cast<int64_t>(slot) * c.token_stride) * kEl;
+              if (kQ8)
+                scales += (static_cast<int64_t>(next_page) * c.Hkv + kvh) * c.page_size + slot +
+                          4 * (lane & 3);
+            } else if (lane == 0) {
+              atomicOr(c.status, kStatusBadPage);
+            }
+            if (kQ8 && lane < 4)
+              copy16(dst + 32 * kRowB + 16 * lane, reinterpret_cast<const uint8_t*>(scales),
+                     there ? 16 : 0);
+            const bool whole = there && k0 + 15 <= p_hi && (k0 >= lo || k0 + 15 < sinks);
+            const uint8_t* src_k = c.k + at + lane_off;
+            const uint8_t* src_v = c.v + at + lane_off;
+            const int64_t down = kRows32 * ts;
 #pragma unroll
-          for (int nr = 0; nr < kNr; ++nr) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              float v = (x[nr][e] + x2[nr][e]) * rs[nr][e & 1];
-              if constexpr (kQ8) v *= ks[e >> 1];
-              if (!full) {
-                const int j = cur0 + g + 8 * (e >> 1);
-                const int pos = rpos[nr][e & 1];
-                const bool see =
-                    j <= pos && (p.window <= 0 || j > pos - p.window || j < sinks);
-                v = see ? v : -INFINITY;
-              }
-              x[nr][e] = v;
-              over |= v > m[nr][e & 1] + kOver;  // with m = -inf: any logit but -inf
+            for (int i = 0; i < 16 / kRows32; ++i) {
+              const int row = lr + i * kRows32;
+              const bool see = whole || (there && seen(k0 + row));
+              copy_part<kForm>(dst + k_at(row, lc), see ? src_k : c.k, see, lc_left);
+              copy_part<kForm>(dst + v_at(row, lc), see ? src_v : c.v, see, lc_left);
+              src_k += down;
+              src_v += down;
             }
           }
-          if (__any_sync(kAll, over)) {
-            // Rare after the first block: references move with the maximum, O and l
-            // follow.
-            float alpha[kNr][2];
+          asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        locate(first_unit);
 #pragma unroll
-            for (int nr = 0; nr < kNr; ++nr)
+        for (int i = 0; i < kStages - 1; ++i) {
+          issue(i);
+          next_key0 = -1;
+          if (first_unit + i + 1 < end_unit) locate(first_unit + i + 1);
+        }
+        int stage = 0;
+        for (int u = first_unit; u < end_unit; ++u) {
+          asm volatile("cp.async.wait_group %0;" :: "n"(kStages - 2) : "memory");
+          __syncwarp();                           // every lane's copies; and the last stage is read
+          issue(stage == 0 ? kStages - 1 : stage - 1);
+          next_key0 = -1;
+          if (u + kStages < end_unit) locate(u + kStages);
+          const uint8_t* const block = ring + stage * L::kBlockB;
+          stage = stage + 1 == kStages ? 0 : stage + 1;
+          // ---- S^T, in two chains of products
+          const int cur0 = key_of(u);
+          if (cur0 < 0) continue;
+          float x[kNr][4], x2[kNr][4];
 #pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                float v = fmaxf(x[nr][i], x[nr][i + 2]);
-                v = fmaxf(v, __shfl_xor_sync(kAll, v, 4));
-                v = fmaxf(v, __shfl_xor_sync(kAll, v, 8));
-                v = fmaxf(v, __shfl_xor_sync(kAll, v, 16));
-                const float next = v > m[nr][i] + kOver ? v - kDown : m[nr][i];
-                alpha[nr][i] = next == m[nr][i] ? 1.0f : fast_exp2(m[nr][i] - next);
-                m[nr][i] = next;
-                l[nr][i] *= alpha[nr][i];
+          for (int nr = 0; nr < kNr; ++nr)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[nr][e] = x2[nr][e] = 0.0f;
+#pragma unroll
+          for (int v = 0; v < kKw / 4; ++v) {
+            const uint4 ka = *reinterpret_cast<const uint4*>(block + k_at(g, 4 * v + t));
+            const uint4 kb = *reinterpret_cast<const uint4*>(block + k_at(g + 8, 4 * v + t));
+            const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
+            constexpr int kPer = kQ8 ? 4 : 2;     // k-steps of a vector
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+              uint32_t a0, a1, a2, a3;
+              if constexpr (kQ8) {
+                int8_to_half(wa[i], a0, a2);
+                int8_to_half(wb[i], a1, a3);
+              } else {
+                a0 = wa[2 * i]; a2 = wa[2 * i + 1];
+                a1 = wb[2 * i]; a3 = wb[2 * i + 1];
               }
+              const int step = kPer * v + i;
 #pragma unroll
-            for (int j = 0; j < kMt; ++j)
+              for (int nr = 0; nr < kNr; ++nr)
+                mma<kMmaBF16>((step & 1) ? x2[nr] : x[nr], a0, a1, a2, a3, qw[nr][2 * step],
+                              qw[nr][2 * step + 1]);
+            }
+          }
+          float ks[2] = {1.0f, 1.0f};
+          if constexpr (kQ8) {
+            ks[0] = reinterpret_cast<const float*>(block + 32 * kRowB)[g];
+            ks[1] = reinterpret_cast<const float*>(block + 32 * kRowB)[g + 8];
+          }
+          {
+            // ---- logits, masks, running maximum and sum
+            const bool full =
+                cur0 + 15 <= p_lo && (cur0 >= lo_hi || cur0 + 15 < sinks);
+            bool over = false;                    // a logit has outgrown its row's reference
+#pragma unroll
+            for (int nr = 0; nr < kNr; ++nr) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                float v = (x[nr][e] + x2[nr][e]) * rs[nr][e & 1];
+                if constexpr (kQ8) v *= ks[e >> 1];
+                if (!full) {
+                  const int j = cur0 + g + 8 * (e >> 1);
+                  const int pos = rpos[nr][e & 1];
+                  const bool see =
+                      j <= pos && (p.window <= 0 || j > pos - p.window || j < sinks);
+                  v = see ? v : -INFINITY;
+                }
+                x[nr][e] = v;
+                over |= v > m[nr][e & 1] + kOver;  // with m = -inf: any logit but -inf
+              }
+            }
+            if (__any_sync(kAll, over)) {
+              // Rare after the first block: references move with the maximum, O and l
+              // follow.
+              float alpha[kNr][2];
 #pragma unroll
               for (int nr = 0; nr < kNr; ++nr)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) o[j][nr][e] *= alpha[nr][e & 1];
-          }
-          // ---- P^T and O^T
-          uint32_t pb[kNr][2];
+                for (int i = 0; i < 2; ++i) {
+                  float v = fmaxf(x[nr][i], x[nr][i + 2]);
+                  v = fmaxf(v, __shfl_xor_sync(kAll, v, 4));
+                  v = fmaxf(v, __shfl_xor_sync(kAll, v, 8));
+                  v = fmaxf(v, __shfl_xor_sync(kAll, v, 16));
+                  const float next = v > m[nr][i] + kOver ? v - kDown : m[nr][i];
+                  alpha[nr][i] = next == m[nr][i] ? 1.0f : fast_exp2(m[nr][i] - next);
+                  m[nr][i] = next;
+                  l[nr][i] *= alpha[nr][i];
+                }
 #pragma unroll
-          for (int nr = 0; nr < kNr; ++nr) {
-            float e4[4];
-            const float safe[2] = {m[nr][0] == -INFINITY ? 0.0f : m[nr][0],
-                                   m[nr][1] == -INFINITY ? 0.0f : m[nr][1]};
+              for (int j = 0; j < kMt; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              e4[e] = fast_exp2(x[nr][e] - safe[e & 1]);
-              l[nr][e & 1] += e4[e];
+                for (int nr = 0; nr < kNr; ++nr)
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) o[j][nr][e] *= alpha[nr][e & 1];
             }
-            pb[nr][0] = transpose8x8(pack2<kMmaBF16>(e4[0], e4[1]));
-            pb[nr][1] = transpose8x8(pack2<kMmaBF16>(e4[2], e4[3]));
-          }
-          uint32_t vw[4][kVw];
+            // ---- P^T and O^T
+            uint32_t pb[kNr][2];
 #pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            const int row = 2 * t + (y & 1) + 8 * (y >> 1);
-            if constexpr (kVw == 2) {
-              const uint2 v = *reinterpret_cast<const uint2*>(block + v_at(row, g / 2) +
-                                                              8 * (g & 1));
-              vw[y][0] = v.x;
-              vw[y][1] = v.y;
+            for (int nr = 0; nr < kNr; ++nr) {
+              float e4[4];
+              const float safe[2] = {m[nr][0] == -INFINITY ? 0.0f : m[nr][0],
+                                     m[nr][1] == -INFINITY ? 0.0f : m[nr][1]};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                e4[e] = fast_exp2(x[nr][e] - safe[e & 1]);
+                l[nr][e & 1] += e4[e];
+              }
+              pb[nr][0] = transpose8x8(pack2<kMmaBF16>(e4[0], e4[1]));
+              pb[nr][1] = transpose8x8(pack2<kMmaBF16>(e4[2], e4[3]));
+            }
+            uint32_t vw[4][kVw];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              const int row = 2 * t + (y & 1) + 8 * (y >> 1);
+              if constexpr (kVw == 2) {
+                const uint2 v = *reinterpret_cast<const uint2*>(block + v_at(row, g / 2) +
+                                                                8 * (g & 1));
+                vw[y][0] = v.x;
+                vw[y][1] = v.y;
+              } else {
+#pragma unroll
+                for (int i = 0; i < kVw / 4; ++i) {
+                  const uint4 v = *reinterpret_cast<const uint4*>(block + v_at(row, g + 8 * i));
+                  vw[y][4 * i] = v.x;
+                  vw[y][4 * i + 1] = v.y;
+                  vw[y][4 * i + 2] = v.z;
+                  vw[y][4 * i + 3] = v.w;
+                }
+              }
+            }
+            // operands of O^T's j-th tile: a0, a1 of keys 2t, 2t + 1 and the tile's two
+            // halves of channels, a2, a3 of the keys 8 further
+            auto product = [&](int j, const uint32_t (&a)[4]) {
+#pragma unroll
+              for (int nr = 0; nr < kNr; ++nr)
+                mma<kMmaBF16>(o[j][nr], a[0], a[1], a[2], a[3], pb[nr][0], pb[nr][1]);
+            };
+            if constexpr (kQ8) {
+#pragma unroll
+              for (int j = 0; j < kMt; j += 2) {          // two bytes of a word at a time
+                uint32_t a[2][4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                  const int y = 2 * (q >> 1), word = (kDp == 128 ? 2 : 1) * (q & 1) + j / 4;
+                  const uint32_t two = __byte_perm(vw[y][word], vw[y + 1][word],
+                                                   (j & 2) ? 0x7362 : 0x5140);
+                  a[0][q] = e4m3x2_to_half2(two);
+                  a[1][q] = e4m3x2_to_half2(two >> 16);
+                }
+                product(j, a[0]);
+                product(j + 1, a[1]);
+              }
             } else {
 #pragma unroll
-              for (int i = 0; i < kVw / 4; ++i) {
-                const uint4 v = *reinterpret_cast<const uint4*>(block + v_at(row, g + 8 * i));
-                vw[y][4 * i] = v.x;
-                vw[y][4 * i + 1] = v.y;
-                vw[y][4 * i + 2] = v.z;
-                vw[y][4 * i + 3] = v.w;
+              for (int j = 0; j < kMt; ++j) {
+                uint32_t a[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                  const int y = 2 * (q >> 1), word = (kDp == 128 ? 4 : 2) * (q & 1) + j / 2;
+                  a[q] = __byte_perm(vw[y][word], vw[y + 1][word], (j & 1) ? 0x7632 : 0x5410);
+                }
+                product(j, a);
               }
-            }
-          }
-          // operands of O^T's j-th tile: a0, a1 of keys 2t, 2t + 1 and the tile's two
-          // halves of channels, a2, a3 of the keys 8 further
-          auto product = [&](int j, const uint32_t (&a)[4]) {
-#pragma unroll
-            for (int nr = 0; nr < kNr; ++nr)
-              mma<kMmaBF16>(o[j][nr], a[0], a[1], a[2], a[3], pb[nr][0], pb[nr][1]);
-          };
-          if constexpr (kQ8) {
-#pragma unroll
-            for (int j = 0; j < kMt; j += 2) {          // two bytes of a word at a time
-              uint32_t a[2][4];
-#pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                const int y = 2 * (q >> 1), word = (kDp == 128 ? 2 : 1) * (q & 1) + j / 4;
-                const uint32_t two = __byte_perm(vw[y][word], vw[y + 1][word],
-                                                 (j & 2) ? 0x7362 : 0x5140);
-                a[0][q] = e4m3x2_to_half2(two);
-                a[1][q] = e4m3x2_to_half2(two >> 16);
-              }
-              product(j, a[0]);
-              product(j + 1, a[1]);
-            }
-          } else {
-#pragma unroll
-            for (int j = 0; j < kMt; ++j) {
-              uint32_t a[4];
-#pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                const int y = 2 * (q >> 1), word = (kDp == 128 ? 4 : 2) * (q & 1) + j / 2;
-                a[q] = __byte_perm(vw[y][word], vw[y + 1][word], (j & 1) ? 0x7632 : 0x5410);
-              }
-              product(j, a);
             }
           }
         }
+        asm volatile("cp.async.wait_all;" ::: "memory");
       }
-      if constexpr (!kQ4) asm volatile("cp.async.wait_all;" ::: "memory");
       workers_barrier<kQ4>();                   // the rings become the merge buffer
 
       // ---- join the warps
