@@ -45,10 +45,11 @@
 // scale multiplies S^T's partial sums and P, in fp32.  Blocks are 32 keys (16 where
 // registers are short: 171 us with them below); a fifth warp fills the others' rings by
 // tensor copies and goes on to the next item while they join the last.  64 x 8520
-// keys of 32 heads on 8 x 128: 162 us, 3.88 TB/s, 58 % of the measured copy bandwidth:
-// the instructions bound it (660 a warp and step, half on the ALU pipe; three warps
-// share a scheduler), the copies alone take 128 us.  The first form, with 16 keys a step
-// and copies by the warps themselves, took 205.
+// keys of 32 heads on 8 x 128: 161 us, 3.90 TB/s, 58 % of the measured copy bandwidth.
+// No pipe is full (issue slots 50 %, ALU 42 %): the 12 warps an SM that 128 registers a
+// thread leave wait for their own results through 660 instructions a step, and the
+// copies alone take 128 us.  The first form, with 16 keys a step and copies by the
+// warps themselves, took 205.
 
 #pragma once
 

@@ -30,9 +30,9 @@
 // bandwidth (half layout 108); rope of one token for each of 64 sequences 3.8 us, of which the
 // launch is most; three axes, 32768 tokens x 80 x 128 bf16, 215 us, 6.24 TB/s, 93 %.
 // Packed prompts into the 4-bit cache, 76000 tokens x 16 heads x 80 fp16: 140 us, 3.7
-// TB/s, issue slots 74 % full; read back 144 us, 3.3 TB/s, waiting for loads.  24000
-// tokens, 32 heads of q and 8 of k and v, 128 bf16, half layout: into 16 bits 99 us,
-// 5.8 TB/s; 8 bits 108; 4 bits 114.
+// TB/s, issue slots 74 % full; read back 145 us, 3.6 TB/s, waiting for loads.  24000
+// tokens, 32 heads of q and 8 of k and v, 128 bf16, half layout: into 16 bits 100 us,
+// 5.9 TB/s; 8 bits 109; 4 bits 114.
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
