@@ -232,7 +232,7 @@ step_kernel(const PoolParams p) {
       out[j] = page[k];
     }
   }
-  // ---- the rows, four at a time
+  // ---- the rows, four at a time; those from cu[n] on stay as they are
   if (p.positions == nullptr && p.slots == nullptr) return;
   const int64_t total = min(static_cast<int64_t>(cu[p.n]), p.rows);
   constexpr int kUnroll = 4;
