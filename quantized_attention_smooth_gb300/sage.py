@@ -956,8 +956,8 @@ class PagePool:
     free (pages,), a stack of page indices whose next one is its last of left (1,)
     pages; table (requests, width), each request's pages; lens (requests,), its
     cached length.  `PagePool.new` makes an empty pool.  What is made here is made
-    and filled on `stream` (None: the current one); calls on another stream wait for
-    it first."""
+    and filled on `stream` (None: the current one); nothing makes a call on another
+    stream wait for that, so give the stream of the calls."""
 
     def __init__(self, free, left, table, lens, page_size, stream=None):
         if _torch is None:
@@ -1000,8 +1000,8 @@ class PagedPlan:
     + place in the page; denied, an int32 scalar, sequences that got no pages.
     Positions and slots from cu_q[n] on keep what an earlier step wrote there, whose
     pages may be another request's by now: go by cu_q.  The buffers are made and
-    filled on `stream` (None: the current one); a step on another stream waits for it
-    first."""
+    filled on `stream` (None: the current one); nothing makes a step on another stream
+    wait for that, so give the stream of the steps."""
 
     def __init__(self, pool, n, rows, max_q, max_kv, stream=None):
         import torch
